@@ -1,6 +1,7 @@
 """GB300 MoE token dispatch / combine: thin Python binding over libep.so.
 
-Each function has the name of the C entry point it wraps (include/ep.h) and
+Each function has the name of the C entry point it wraps (include/ep.h; the
+operators around the MoE layer, include/ep_layer.h, are bound in layer.py) and
 only marshals arguments: torch tensors become device pointers, the current
 torch CUDA stream becomes the stream argument, and a non-OK status raises
 EPError. All computation runs in the library's CUDA kernels; there is no CPU
@@ -16,7 +17,7 @@ import torch
 from .build import LIB as _LIB_PATH, build
 
 EP_OK, EP_ERR_INVALID_ARG, EP_ERR_INVALID_EXPERT, EP_ERR_CAPACITY, EP_ERR_CUDA, EP_ERR_ALLOC = range(6)
-EP_DTYPE_BF16, EP_DTYPE_FP8_E4M3, EP_DTYPE_FP8_E5M2 = 0, 1, 2
+EP_DTYPE_BF16, EP_DTYPE_FP8_E4M3, EP_DTYPE_FP8_E5M2, EP_DTYPE_FP16, EP_DTYPE_FP32 = range(5)
 EP_SCALE_FP32, EP_SCALE_POW2, EP_SCALE_UE8M0 = 0, 1, 2
 
 
@@ -25,7 +26,7 @@ class DispatchConfig(ctypes.Structure):
     _fields_ = [("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("scale_mode", ctypes.c_int),
                 ("scales_col_major", ctypes.c_int), ("scales_ld", ctypes.c_int64), ("overlap_layout", ctypes.c_int)]
 
-# Exported symbols declared in include/ep.h.
+# Symbols declared in include/ep.h; those of include/ep_layer.h (layer.py) join them below.
 EXPORTS = ("ep_layout", "ep_layout_aligned", "ep_layout_strided", "ep_layout_nonexpand",
            "ep_nonexpand_recv_topk", "ep_dispatch", "ep_dispatch_ex", "ep_combine", "ep_combine_backward",
            "ep_dispatch_backward", "ep_topk_to_routing_map", "ep_routing_map_to_topk", "ep_handle_query",
@@ -75,6 +76,7 @@ def lib() -> ctypes.CDLL:
         for name in EXPORTS:
             if name != "ep_status_string":
                 getattr(L, name).restype = i32
+        layer.declare(L)
         _lib = L
     return _lib
 
@@ -419,3 +421,11 @@ def ep_layout_cluster_ctas(T: int, K: int, E: int, R: int) -> int:
 
 def ep_handle_destroy(handle: Handle) -> None:
     handle.destroy()
+
+
+from . import layer  # noqa: E402  (needs the names above)
+from .layer import (EP_ACT_NONE, EP_ACT_SWIGLU, EP_SCORE_SIGMOID, EP_SCORE_SOFTMAX, ep_expert_w4,  # noqa: E402,F401
+                    ep_kv_append, ep_paged_attention, ep_paged_attention_workspace, ep_router_topk,
+                    ep_router_topk_backward)
+
+EXPORTS = EXPORTS + layer.EXPORTS

@@ -96,7 +96,9 @@ typedef enum {
 typedef enum {
     EP_DTYPE_BF16 = 0,         /* receive rows are the bf16 token rows        */
     EP_DTYPE_FP8_E4M3 = 1,     /* receive rows are e4m3 bytes + fp32 scales   */
-    EP_DTYPE_FP8_E5M2 = 2      /* receive rows are e5m2 bytes + fp32 scales   */
+    EP_DTYPE_FP8_E5M2 = 2,     /* receive rows are e5m2 bytes + fp32 scales   */
+    EP_DTYPE_FP16 = 3,         /* only the operators of ep_layer.h take these */
+    EP_DTYPE_FP32 = 4          /* two (dispatch refuses them)                 */
 } ep_dtype_t;
 
 /* How fp8 block scales are formed and stored (one per 128 channels). F is the

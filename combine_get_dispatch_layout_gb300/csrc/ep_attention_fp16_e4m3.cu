@@ -1,0 +1,10 @@
+// Paged attention kernels of one pair of types (ep_attention_kernel.cuh).
+#include "ep_attention_kernel.cuh"
+
+namespace ep {
+namespace attn {
+
+cudaError_t launch_fp16_e4m3(const AttentionArgs& a, int sms, cudaStream_t stream) { return launch_type<__half, true>(a, sms, stream); }
+
+}  // namespace attn
+}  // namespace ep

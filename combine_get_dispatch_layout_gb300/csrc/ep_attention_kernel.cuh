@@ -1,0 +1,830 @@
+// Paged attention of one new token: the kernels' template, instantiated per
+// element type by ep_attention_*.cu.
+//
+// Mathematics. For one cache head and the `heads` query heads that share it,
+// with scores s_i = c q.k_i (c = scale * log2 e): the running maximum m, the sum
+// l = sum 2^(s_i - m) and O = sum 2^(s_i - m) v_i, one pass over the keys; a
+// larger m rescales l and O by 2^(m_old - m). Parts of the key range join by
+// the same rule, so the range can be cut anywhere.
+//
+// What bounds it: each key and value is read once for all its query heads, so
+// DRAM (4 * heads / 2 operations per cache byte is far below the tensor rate).
+// The layout serves that: a persistent grid whose CTAs take equal shares of
+// all sequences' keys, laid end to end in chunks of 64 to 256, so no CTA waits for
+// another's longer sequence; a ring of chunks in shared memory, filled by
+// 16-byte asynchronous copies that run several chunks ahead and straight on
+// into the next sequence.
+//
+// The products run transposed, keys as the matrix instruction's 16 rows and
+// query heads as its 8 columns: S^T = K Q^T, O^T = V^T P^T. One cache head is
+// shared by few query heads (8 is common); as the 16-row operand they would
+// leave half the instruction empty. A warp takes a quarter of each chunk with
+// statistics of its own; the four warps join when a segment (a CTA's part of one
+// sequence and head) ends.
+#pragma once
+
+#include <math.h>
+
+#include <type_traits>
+
+#include "ep_layer.cuh"
+
+namespace ep {
+namespace attn {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kJoinThreads = 256;
+constexpr int kMaxGrid = 1024;  // CTAs of the main kernel, and so parts of one sequence
+
+struct Plan {
+    int grid;        // CTAs of the main kernel
+    int split;       // 1: CTAs take equal shares of chunks and the join kernel runs; 0: whole (sequence, head) units
+    int units;       // units of one sequence: cache heads * head blocks
+    int blocks;      // head blocks per cache head
+    unsigned page_mul, page_shift;  // i / page_size = (umulhi(i, page_mul) + ...) as page_of
+    int min_chunks;  // a CTA's share is at least this many chunks
+    float out_scale; // of O / l
+};
+
+// Quotient by the page size for 0 <= i < 2^31: with L = ceil(log2 d) and
+// mul = ceil(2^(31 + L) / d), floor(i * mul / 2^(31 + L)) is exact (the error
+// of mul, below 1, times i / 2^(31 + L) stays below 1 / d).
+__device__ __forceinline__ int page_of(const Plan& p, int i) {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<unsigned>(i)) * p.page_mul) >> p.page_shift);
+}
+
+// Keys [low, end) of sequence b count; returns their number of chunks.
+template <int CHUNK>
+__device__ __forceinline__ int sequence(const AttentionArgs& a, int b, int& low, int& end) {
+    const int most = a.max_pages * a.page_size;   // < 2^31, checked on the host
+    end = min(max(a.lens[b], 0), most);
+    low = a.window > 0 && end > a.window ? end - a.window : 0;
+    return (end - low) / CHUNK + ((end - low) % CHUNK != 0);
+}
+
+// Exclusive prefix of the sequences' chunks: total over all B, and for
+// `target` (a position in chunk space divided by `units`, see below) the
+// sequence that holds it and the chunks before that sequence. Every thread
+// gets the same result. THREADS threads, all of them.
+template <int THREADS, int CHUNK>
+__device__ int64_t find_sequence(const AttentionArgs& a, int units, int64_t target, int& seq, int64_t& before) {
+    __shared__ int64_t warp_sum[THREADS / 32];
+    __shared__ int64_t found_before;
+    __shared__ int found;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int per = (a.B + THREADS - 1) / THREADS, first = min(a.B, tid * per), last = min(a.B, first + per);
+    int64_t own = 0;
+    int low, end;
+    for (int b = first; b < last; ++b) own += sequence<CHUNK>(a, b, low, end);
+    int64_t scan = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(kFullMask, scan, o);
+        if (lane >= o) scan += v;
+    }
+    if (lane == 31) warp_sum[tid >> 5] = scan;
+    if (tid == 0) found = -1, found_before = 0;
+    __syncthreads();
+    int64_t total = 0, base = scan - own;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < (tid >> 5)) base += warp_sum[w];
+        total += warp_sum[w];
+    }
+    if (target >= base * units && target < (base + own) * units) {
+        for (int b = first; b < last; ++b) {
+            const int n = sequence<CHUNK>(a, b, low, end);
+            if (target < (base + n) * units) {
+                found = b;
+                found_before = base;
+                break;
+            }
+            base += n;
+        }
+    }
+    __syncthreads();
+    seq = found;
+    before = found_before;
+    return total;
+}
+
+// CTAs that share W chunks, and the first chunk of CTA i.
+__device__ __forceinline__ int sharers(const Plan& p, int64_t W) {
+    return static_cast<int>(min(static_cast<int64_t>(p.grid), (W + p.min_chunks - 1) / p.min_chunks));
+}
+__device__ __forceinline__ int64_t share_start(int64_t W, int ctas, int i) { return W * i / ctas; }
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+// 16 bytes to shared memory, of which the first `real` (16 or 0) are read and the rest are zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void load_matrices_transposed(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void multiply(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same_v<T, __half>)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Two e4m3 codes (the low 16 bits) as two fp16 values, exactly. The instruction issues at the rate of the
+// integer ones (2 clocks per warp and SM quarter), which would take seven for four codes.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t codes) {
+    uint32_t r;
+    asm("{ .reg .b16 c; cvt.u16.u32 c, %1; cvt.rn.f16x2.e4m3x2 %0, c; }" : "=r"(r) : "r"(codes));
+    return r;
+}
+template <typename M>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    if constexpr (std::is_same_v<M, __half>) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+// Left by each CTA of a split launch for the join kernel: the unit that began in it and goes on in later
+// CTAs, if there is one (seq -1 otherwise).
+struct Cut {
+    int seq, unit, last;   // last CTA that holds a part
+    int pad;
+};
+
+// What a ring slot holds, beside its keys and values.
+struct SlotInfo {
+    int unit;    // of its sequence; -1: no more chunks
+    int seq;
+    int chunk;   // index within (sequence, head)
+    int chunks;  // of that sequence
+};
+
+// Byte offsets of a key's and a value's row.
+struct alignas(16) RowAt {
+    int64_t key, value;
+};
+
+// T: type of q and out. FP8: the cache is e4m3, else T. DP: head_dim rounded up
+// to 64, 128 or 256 (the rest zeros). NT: eights of query heads per unit.
+template <typename T, bool FP8, int DP, int NT>
+struct Shape {
+    using M = std::conditional_t<FP8, __half, T>;   // type of the products' operands
+    static constexpr int kHeads = 8 * NT;
+    static constexpr int kCacheBytes = FP8 ? 1 : 2;
+    static constexpr int kRowBytes = DP * kCacheBytes;
+    static constexpr int kPieces = kRowBytes / 16;          // 16-byte pieces of a row
+    // Keys per chunk: 32 KB of keys and values (64 KB for 512-byte rows), 16 * kTiles keys a warp.
+    static constexpr int kTiles = kRowBytes <= 64 ? 4 : kRowBytes <= 128 ? 2 : 1;
+    static constexpr int kChunk = 16 * kWarps * kTiles;
+    static constexpr int kTile = kChunk * kRowBytes;        // bytes of a chunk's keys, or values
+    // Three slots: two CTAs a core keep 128 KB on the way, above what DRAM's latency needs at full rate.
+    static constexpr int kSlots = 3;
+    static constexpr int kQueryStride = DP + 8;             // 16-bit values; keeps fragment loads off one bank
+
+    struct Shared {
+        alignas(128) unsigned char ring[kSlots][2][kTile];  // a used-up slot also serves the join of the warps
+        alignas(16) T query_raw[kSlots][kHeads][DP];
+        alignas(16) M query[kHeads][kQueryStride];
+        RowAt at[kSlots + 1][kChunk];
+        unsigned real[kSlots + 1][kChunk / 32];             // bit per key: it exists
+        SlotInfo info[kSlots + 1];
+        float top[kWarps][kHeads], sum[kWarps][kHeads];
+        float query_scale[kHeads];
+    };
+    static_assert(kWarps * kHeads * DP * 4 <= 2 * kTile, "the join of the warps fits a slot");
+
+    // Byte offset of 16-byte piece c of row r: pieces are exchanged within 8 (4) so that the 8
+    // rows of a matrix load, and the 2 rows x 4 pieces of the e4m3 key loads, lie in different banks.
+    static __device__ __forceinline__ int place(int r, int c) {
+        if constexpr (kPieces >= 8) return r * kRowBytes + ((c ^ (((r & 1) << 2) | ((r >> 1) & 3))) << 4);
+        return r * kRowBytes + ((c ^ ((r >> 1) & 3)) << 4);
+    }
+};
+
+template <typename T, bool FP8, int DP, int NT>
+__global__ void __launch_bounds__(kThreads) attention_kernel(AttentionArgs a, Plan p) {
+    using S = Shape<T, FP8, DP, NT>;
+    using M = typename S::M;
+    extern __shared__ __align__(128) unsigned char shared_bytes[];
+    typename S::Shared& sh = *reinterpret_cast<typename S::Shared*>(shared_bytes);
+    constexpr int kSlots = S::kSlots, kInfos = kSlots + 1, kChunk = S::kChunk, kTiles = S::kTiles;
+    dependent_entry();
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int D = a.head_dim, group = a.num_heads / a.num_kv_heads;
+    Cut* cuts = static_cast<Cut*>(a.workspace);   // [grid], then the parts
+    float* part = reinterpret_cast<float*>(cuts + p.grid);
+
+    // ---- this CTA's chunks: `left` of them from (seq, unit, chunk) on
+    int seq, unit, chunk, chunks, low, end;
+    int64_t left;
+    if (p.split) {
+        int64_t before;
+        const int64_t total = find_sequence<kThreads, kChunk>(a, p.units, -1, seq, before);
+        const int64_t W = total * p.units;
+        const int ctas = sharers(p, W);
+        // sequences without keys: zeros
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+            if (sequence<kChunk>(a, b, low, end) > 0) continue;
+            for (int i = tid; i < a.num_heads * D; i += kThreads)
+                static_cast<T*>(a.out)[b * a.out_ld + i] = from_float<T>(0.0f);
+            if (a.lse)
+                for (int h = tid; h < a.num_heads; h += kThreads) a.lse[static_cast<int64_t>(b) * a.num_heads + h] = -INFINITY;
+        }
+        if (tid == 0) cuts[blockIdx.x].seq = -1;
+        if (static_cast<int>(blockIdx.x) >= ctas) return;
+        const int64_t start = share_start(W, ctas, blockIdx.x);
+        left = share_start(W, ctas, blockIdx.x + 1) - start;
+        __syncthreads();
+        find_sequence<kThreads, kChunk>(a, p.units, start, seq, before);
+        chunks = sequence<kChunk>(a, seq, low, end);
+        const int64_t in = start - before * p.units;
+        unit = static_cast<int>(in / chunks);
+        chunk = static_cast<int>(in % chunks);
+        // the unit that holds this share's last chunk, if it began here and goes on behind it
+        int last_seq;
+        __syncthreads();
+        find_sequence<kThreads, kChunk>(a, p.units, start + left - 1, last_seq, before);
+        int lo, en;
+        const int n = sequence<kChunk>(a, last_seq, lo, en);
+        const int64_t base = before * p.units, last_unit = (start + left - 1 - base) / n;
+        const int64_t from = base + last_unit * n, behind = from + n;
+        if (tid == 0 && from >= start && behind > start + left)
+            // the CTA whose share holds position x is the largest i with W i / ctas (rounded down) <= x
+            cuts[blockIdx.x] = {last_seq, static_cast<int>(last_unit), static_cast<int>((behind * ctas - 1) / W), 0};
+    } else {
+        const int64_t all = static_cast<int64_t>(a.B) * p.units;
+        int64_t u = share_start(all, gridDim.x, blockIdx.x);
+        const int64_t stop = share_start(all, gridDim.x, blockIdx.x + 1);
+        seq = -1;
+        left = 0;
+        unit = chunk = chunks = low = end = 0;
+        for (; u < stop; ++u) {
+            const int b = static_cast<int>(u / p.units), w = static_cast<int>(u % p.units);
+            int lo, en;
+            const int n = sequence<kChunk>(a, b, lo, en);
+            left += n;
+            if (n > 0) {
+                if (seq < 0) seq = b, unit = w, chunks = n, low = lo, end = en;
+                continue;
+            }
+            // no keys: zeros
+            const int h0 = w / p.blocks * group + w % p.blocks * S::kHeads, heads = min(S::kHeads, group - w % p.blocks * S::kHeads);
+            for (int i = tid; i < heads * D; i += kThreads)
+                static_cast<T*>(a.out)[b * a.out_ld + static_cast<int64_t>(h0) * D + i] = from_float<T>(0.0f);
+            if (a.lse && tid < heads) a.lse[static_cast<int64_t>(b) * a.num_heads + h0 + tid] = -INFINITY;
+        }
+    }
+
+    // ---- ring. A chunk's rows are looked up in the block table (look_up, which only issues the loads, and
+    // note, which writes the rows' places) one chunk before copies() starts their way to the ring slot.
+    // A thread looks up rows tid, tid + 128; with 64 keys a chunk, each half of the block every other chunk's.
+    constexpr int kLookups = (kChunk + kThreads - 1) / kThreads;
+    int64_t located = 0;
+    int note_slot = 0;
+    int32_t page_id[kLookups];
+    int page_place[kLookups];
+    const auto look_row = [&](int k) {
+        if constexpr (kChunk >= kThreads) return tid + k * kThreads;
+        return (tid + static_cast<int>(located & 1) * kChunk) % kThreads;
+    };
+    const auto look_up = [&]() {
+        if (located >= left) return;
+#pragma unroll
+        for (int k = 0; k < kLookups; ++k) {
+            page_id[k] = -1;
+            const int r = look_row(k), i = low + chunk * kChunk + r;
+            if (r < kChunk && i < end) {
+                const int pg = page_of(p, i);
+                page_id[k] = a.table[seq * a.table_ld + pg];
+                page_place[k] = i - pg * a.page_size;
+            }
+        }
+    };
+    const auto note = [&]() {
+        if (located < left) {
+            const int h = unit / p.blocks;
+#pragma unroll
+            for (int k = 0; k < kLookups; ++k) {
+                const int r = look_row(k);
+                const bool real = page_id[k] >= 0 && page_id[k] < a.num_pages;
+                if (r < kChunk) {   // (whole warps)
+                    RowAt at{0, 0};
+                    if (real) {
+                        at.key = (page_id[k] * a.k_page + page_place[k] * a.k_slot + h * a.k_head) * S::kCacheBytes;
+                        at.value = (page_id[k] * a.v_page + page_place[k] * a.v_slot + h * a.v_head) * S::kCacheBytes;
+                    }
+                    sh.at[note_slot][r] = at;
+                    const unsigned mask = __ballot_sync(kFullMask, real);
+                    if (lane == 0) sh.real[note_slot][r >> 5] = mask;
+                }
+            }
+            if (tid == 0) sh.info[note_slot] = {unit, seq, chunk, chunks};
+            if (++chunk == chunks) {
+                chunk = 0;
+                if (++unit == p.units && located + 1 < left) {
+                    unit = 0;
+                    do chunks = sequence<kChunk>(a, ++seq, low, end);
+                    while (chunks == 0);
+                }
+            }
+        } else if (tid == 0) {
+            sh.info[note_slot].unit = -1;
+        }
+        ++located;
+        note_slot = note_slot + 1 == kInfos ? 0 : note_slot + 1;
+    };
+    const auto all_real = [&](int slot) {
+        unsigned m = ~0u;
+#pragma unroll
+        for (int i = 0; i < kChunk / 32; ++i) m &= sh.real[slot][i];
+        return m == ~0u;
+    };
+
+    const int piece = tid % S::kPieces, piece_bytes = piece * 16 < D * S::kCacheBytes ? 16 : 0;   // a piece past head_dim: zeros
+    // (a cache without pages may be NULL: then nothing is read, at any valid address)
+    const unsigned char* key_base = static_cast<const unsigned char*>(a.k ? a.k : a.q) + (piece_bytes ? piece * 16 : 0);
+    const unsigned char* value_base = static_cast<const unsigned char*>(a.v ? a.v : a.q) + (piece_bytes ? piece * 16 : 0);
+    int copy_slot = 0, copy_info = 0;
+    bool copied_any = false;
+    const auto copies = [&]() {
+        const SlotInfo in = sh.info[copy_info];
+        if (in.unit >= 0) {
+            constexpr int kRows = kThreads / S::kPieces;
+            const int row = tid / S::kPieces;
+            const uint32_t slot_addr = smem_addr(sh.ring[copy_slot][0]), first = slot_addr + S::place(row, piece);
+            const auto to = [&](int r) {   // 8 rows on, the exchange of pieces is the same
+                return kRows % 8 == 0 ? first + r * S::kRowBytes : slot_addr + S::place(r + row, piece);
+            };
+            if (all_real(copy_info)) {
+#pragma unroll
+                for (int r = 0; r < kChunk; r += kRows) {
+                    const RowAt at = sh.at[copy_info][r + row];
+                    copy16(to(r), key_base + at.key, piece_bytes);
+                    copy16(to(r) + S::kTile, value_base + at.value, piece_bytes);
+                }
+            } else {
+#pragma unroll 2
+                for (int r = 0; r < kChunk; r += kRows) {
+                    const RowAt at = sh.at[copy_info][r + row];
+                    const int bytes = (sh.real[copy_info][(r + row) >> 5] >> ((r + row) & 31)) & 1 ? piece_bytes : 0;
+                    copy16(to(r), key_base + at.key, bytes);
+                    copy16(to(r) + S::kTile, value_base + at.value, bytes);
+                }
+            }
+            if (!copied_any || in.chunk == 0) {   // a segment starts: its queries
+                const int h0 = in.unit / p.blocks * group + in.unit % p.blocks * S::kHeads;
+                const int heads = min(S::kHeads, group - in.unit % p.blocks * S::kHeads);
+                const T* q = static_cast<const T*>(a.q) + in.seq * a.q_ld + static_cast<int64_t>(h0) * D;
+                for (int i = tid; i < S::kHeads * (DP / 8); i += kThreads) {
+                    const int h = i / (DP / 8), c = i % (DP / 8) * 8;
+                    const bool real = h < heads && c < D;
+                    copy16(smem_addr(&sh.query_raw[copy_slot][h][c]), q + (real ? h * D + c : 0), real ? 16 : 0);
+                }
+            }
+            copied_any = true;
+        }
+        copy_commit();
+        copy_slot = copy_slot + 1 == kSlots ? 0 : copy_slot + 1;
+        copy_info = copy_info + 1 == kInfos ? 0 : copy_info + 1;
+    };
+
+#pragma unroll 1
+    for (int i = 0; i < kSlots; ++i) {
+        look_up();
+        note();
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < kSlots - 1; ++i) copies();
+
+    // ---- the pass over the chunks
+    float o[DP / 16][NT][4];                   // O^T: rows d, columns heads
+    float top[NT][2], sum[NT][2], c2[NT][2];   // of heads 8 nt + 2 t, + 1
+    uint32_t qf[DP / 16][NT][2];
+    int slot = 0, info = 0, first_chunk = 0;
+    bool fresh = true;
+    for (int64_t n = 0; n < left; ++n) {
+        copy_wait<kSlots - 2>();
+        __syncthreads();
+        const SlotInfo in = sh.info[info];
+        copies();
+        look_up();
+        if (fresh || in.chunk == 0) {
+            // a segment starts: queries to the products' type, fresh statistics
+            fresh = false;
+            first_chunk = in.chunk;
+            for (int h = warp; h < S::kHeads; h += kWarps) {
+                const T* raw = sh.query_raw[slot][h];
+                float scale = 1.0f;
+                if constexpr (FP8) {
+                    // a power of two that brings the head's largest query to [2^14, 2^15): fp16 then holds every
+                    // one of them to 2^-11, or to 2^-39 of the largest, whatever its type's range
+                    float big = 0.0f;
+                    for (int d = lane; d < DP; d += 32) big = fmaxf(big, fabsf(to_float(raw[d])));
+#pragma unroll
+                    for (int s = 16; s; s >>= 1) big = fmaxf(big, __shfl_xor_sync(kFullMask, big, s));
+                    const int e = big > 0.0f && big < INFINITY ? min(14 - ilogbf(big), 126) : 0;
+                    const float up = __int_as_float((e + 127) << 23);
+                    for (int d = lane; d < DP; d += 32) sh.query[h][d] = __float2half_rn(to_float(raw[d]) * up);
+                    scale = __int_as_float((127 - e) << 23);
+                } else {
+                    for (int d = lane * 8; d < DP; d += 256)
+                        *reinterpret_cast<uint4*>(&sh.query[h][d]) = *reinterpret_cast<const uint4*>(&raw[d]);
+                }
+                if (lane == 0) sh.query_scale[h] = scale;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    top[nt][j] = -INFINITY;
+                    sum[nt][j] = 0.0f;
+                    c2[nt][j] = a.score_scale * sh.query_scale[8 * nt + 2 * t + j] * 1.4426950408889634f;
+                }
+#pragma unroll
+            for (int m = 0; m < DP / 16; ++m)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[m][nt][j] = 0.0f;
+            // queries as the products' column operand: value pairs of step k; an e4m3 key load brings 16
+            // neighbouring values a lane, so its steps run through the head in that order
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        qf[k][nt][j] = *reinterpret_cast<const uint32_t*>(
+                            sh.query[8 * nt + g] +
+                            (FP8 ? (k / 4) * 64 + 16 * t + (k % 4) * 4 + 2 * j : 16 * k + 2 * t + 8 * j));
+        }
+        // S^T = K Q^T for this warp's keys r0 .. r0 + 16 kTiles - 1
+        const unsigned char* keys = sh.ring[slot][0];
+        const unsigned char* values = sh.ring[slot][1];
+        const int r0 = warp * 16 * kTiles;
+        float s[kTiles][NT][4];
+#pragma unroll
+        for (int kt = 0; kt < kTiles; ++kt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[kt][nt][0] = s[kt][nt][1] = s[kt][nt][2] = s[kt][nt][3] = 0.0f;
+        if constexpr (FP8) {
+#pragma unroll
+            for (int j = 0; j < DP / 64; ++j)
+#pragma unroll
+                for (int kt = 0; kt < kTiles; ++kt) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(keys + S::place(r0 + 16 * kt + g, 4 * j + t));
+                    const uint4 y = *reinterpret_cast<const uint4*>(keys + S::place(r0 + 16 * kt + g + 8, 4 * j + t));
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t af[4] = {e4m3_pair(xs[i]), e4m3_pair(ys[i]), e4m3_pair(xs[i] >> 16), e4m3_pair(ys[i] >> 16)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) multiply<M>(s[kt][nt], af, qf[4 * j + i][nt][0], qf[4 * j + i][nt][1]);
+                    }
+                }
+        } else {
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                for (int kt = 0; kt < kTiles; ++kt) {
+                    uint32_t af[4];
+                    load_matrices(af, smem_addr(keys + S::place(r0 + 16 * kt + (lane & 15), 2 * k + (lane >> 4))));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) multiply<M>(s[kt][nt], af, qf[k][nt][0], qf[k][nt][1]);
+                }
+        }
+        // softmax: this lane's keys r0 + 16 kt + g and + 8 (s[..][0, 1] and [2, 3]) for two heads. The maximum that
+        // the weights refer to follows the running one only when a score passes it by more than kSlack: the weights
+        // stay below 2^kSlack, which fp16 and fp32 hold as well, and most chunks need no exchange between lanes.
+        constexpr float kSlack = 8.0f;
+#pragma unroll
+        for (int kt = 0; kt < kTiles; ++kt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[kt][nt][j] *= c2[nt][j & 1];
+        if (!all_real(info)) {
+#pragma unroll
+            for (int kt = 0; kt < kTiles; ++kt) {
+                const unsigned mask = sh.real[info][(r0 + 16 * kt) >> 5] >> ((r0 + 16 * kt) & 31);
+                const bool in0 = (mask >> g) & 1, in1 = (mask >> (g + 8)) & 1;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (!in0) s[kt][nt][j] = -INFINITY;
+                        if (!in1) s[kt][nt][2 + j] = -INFINITY;
+                    }
+            }
+        }
+        bool over = false;
+#pragma unroll
+        for (int kt = 0; kt < kTiles; ++kt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) over |= s[kt][nt][j] > top[nt][j & 1] + kSlack;
+        if (__any_sync(kFullMask, over)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float fade[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float m = top[nt][j];
+#pragma unroll
+                    for (int kt = 0; kt < kTiles; ++kt) m = fmaxf(m, fmaxf(s[kt][nt][j], s[kt][nt][2 + j]));
+                    m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 4));
+                    m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 8));
+                    m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 16));
+                    fade[j] = exp2_fast(top[nt][j] - (m == -INFINITY ? 0.0f : m));
+                    top[nt][j] = m;
+                    sum[nt][j] *= fade[j];
+                }
+#pragma unroll
+                for (int m = 0; m < DP / 16; ++m) {
+                    o[m][nt][0] *= fade[0], o[m][nt][1] *= fade[1];
+                    o[m][nt][2] *= fade[0], o[m][nt][3] *= fade[1];
+                }
+            }
+        }
+        uint32_t pf[kTiles][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            // nothing seen yet: all weights 0
+            const float base[2] = {top[nt][0] == -INFINITY ? 0.0f : top[nt][0], top[nt][1] == -INFINITY ? 0.0f : top[nt][1]};
+#pragma unroll
+            for (int kt = 0; kt < kTiles; ++kt) {
+                float pr[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) pr[j] = exp2_fast(s[kt][nt][j] - base[j & 1]);
+                sum[nt][0] += pr[0] + pr[2];
+                sum[nt][1] += pr[1] + pr[3];
+                pf[kt][nt][0] = transpose8x8(pack<M>(pr[0], pr[1]));
+                pf[kt][nt][1] = transpose8x8(pack<M>(pr[2], pr[3]));
+            }
+        }
+        // O^T += V^T P^T
+        if constexpr (FP8) {
+#pragma unroll
+            for (int m = 0; m < DP / 16; m += 2)
+#pragma unroll
+                for (int kt = 0; kt < kTiles; ++kt) {
+                    // four 8 x 8 matrices of value pairs: keys 0-7 and 8-15 of 16 values, then of the next 16
+                    uint32_t v[4];
+                    load_matrices_transposed(v, smem_addr(values + S::place(r0 + 16 * kt + (lane & 15), m + (lane >> 4))));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        // bytes (key, value): (0,0) (0,1) (1,0) (1,1); row g of the tile is value 2 g, row g + 8 value 2 g + 1
+                        const uint32_t u0 = __byte_perm(v[2 * i], 0, 0x3120), u1 = __byte_perm(v[2 * i + 1], 0, 0x3120);
+                        const uint32_t af[4] = {e4m3_pair(u0), e4m3_pair(u0 >> 16), e4m3_pair(u1), e4m3_pair(u1 >> 16)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) multiply<M>(o[m + i][nt], af, pf[kt][nt][0], pf[kt][nt][1]);
+                    }
+                }
+        } else {
+#pragma unroll
+            for (int m = 0; m < DP / 16; ++m)
+#pragma unroll
+                for (int kt = 0; kt < kTiles; ++kt) {
+                    uint32_t af[4];
+                    load_matrices_transposed(
+                        af, smem_addr(values + S::place(r0 + 16 * kt + (lane & 7) + ((lane >> 4) << 3), 2 * m + ((lane >> 3) & 1))));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) multiply<M>(o[m][nt], af, pf[kt][nt][0], pf[kt][nt][1]);
+                }
+        }
+
+        if (n + 1 == left || in.chunk + 1 == in.chunks) {
+            // ---- the segment ends: join the warps, in their order, through the slot just used up, and write
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float l = sum[nt][j];
+                    l += __shfl_xor_sync(kFullMask, l, 4);
+                    l += __shfl_xor_sync(kFullMask, l, 8);
+                    l += __shfl_xor_sync(kFullMask, l, 16);
+                    if (g == 0) sh.top[warp][8 * nt + 2 * t + j] = top[nt][j], sh.sum[warp][8 * nt + 2 * t + j] = l;
+                }
+            __syncthreads();
+            float* stage = reinterpret_cast<float*>(sh.ring[slot][0]);   // [kWarps][kHeads][DP]
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float fade[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float m = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sh.top[w][8 * nt + 2 * t + j]);
+                    fade[j] = exp2_fast(top[nt][j] - (m == -INFINITY ? 0.0f : m));
+                }
+                // heads 2 t apart by a multiple of 32 words: value index exchanged by t * 8 to keep off one bank
+#pragma unroll
+                for (int m = 0; m < DP / 16; ++m)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int d = 16 * m + (FP8 ? 2 * g + (j >> 1) : g + 8 * (j >> 1));
+                        stage[(warp * S::kHeads + 8 * nt + 2 * t + (j & 1)) * DP + (d ^ (t << 3))] = o[m][nt][j] * fade[j & 1];
+                    }
+            }
+            __syncthreads();
+            const int hb = in.unit % p.blocks;
+            const int h0 = in.unit / p.blocks * group + hb * S::kHeads, heads = min(S::kHeads, group - hb * S::kHeads);
+            const bool whole = first_chunk == 0 && in.chunk + 1 == in.chunks;
+            // a part goes to this CTA's place 0 if the unit began in an earlier CTA, else to place 1
+            float* to = part + (static_cast<int64_t>(blockIdx.x) * 2 + (first_chunk > 0 ? 0 : 1)) * S::kHeads * (DP + 2);
+            for (int i = tid; i < heads * (DP / 4); i += kThreads) {
+                const int h = i / (DP / 4), d = i % (DP / 4) * 4;
+                const float* from = stage + h * DP + (d ^ (((h >> 1) & 3) << 3));
+                float4 x = *reinterpret_cast<const float4*>(from);
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) {
+                    const float4 y = *reinterpret_cast<const float4*>(from + w * S::kHeads * DP);
+                    x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                }
+                float m = -INFINITY, l = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sh.top[w][h]);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) l += sh.sum[w][h] * exp2_fast(sh.top[w][h] - (m == -INFINITY ? 0.0f : m));
+                if (whole) {
+                    if (d < D) {
+                        const float r = l == 0.0f ? 0.0f : p.out_scale / l;
+                        T* out = static_cast<T*>(a.out) + in.seq * a.out_ld + static_cast<int64_t>(h0 + h) * D + d;
+                        *reinterpret_cast<uint2*>(out) = make_uint2(pack<T>(x.x * r, x.y * r), pack<T>(x.z * r, x.w * r));
+                    }
+                    if (d == 0 && a.lse)
+                        a.lse[static_cast<int64_t>(in.seq) * a.num_heads + h0 + h] =
+                            l == 0.0f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+                } else {
+                    *reinterpret_cast<float4*>(to + h * DP + d) = x;
+                    if (d == 0) to[S::kHeads * DP + 2 * h] = m, to[S::kHeads * DP + 2 * h + 1] = l;
+                }
+            }
+            // (the slot and the statistics are written again only behind the next chunk's barrier)
+        }
+        slot = slot + 1 == kSlots ? 0 : slot + 1;
+        info = info + 1 == kInfos ? 0 : info + 1;
+        note();
+    }
+    copy_wait<0>();
+}
+
+// Joins the parts of the units that several CTAs shared, in the CTAs' order. Block (i, h): head h of the
+// unit that began in CTA i and went on behind it, if there is one.
+template <typename T, int DP, int NT>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, Plan p) {
+    constexpr int kHeads = 8 * NT, kVecs = DP / 4, kLanes = kJoinThreads / kVecs, kPart = kHeads * (DP + 2);
+    __shared__ float weight[kMaxGrid];
+    __shared__ float red[kJoinThreads / 32];
+    __shared__ float4 acc[kLanes][kVecs];
+    __shared__ float lsum[kLanes];
+    dependent_entry();
+    const Cut cut = static_cast<const Cut*>(a.workspace)[blockIdx.x];
+    const int group = a.num_heads / a.num_kv_heads, h = blockIdx.y, in_group = cut.unit % p.blocks * kHeads + h;
+    if (cut.seq < 0 || in_group >= group) return;
+    const int tid = threadIdx.x, D = a.head_dim, i0 = blockIdx.x, parts = cut.last - i0 + 1;
+    const int head = cut.unit / p.blocks * group + in_group;
+    // CTA i0's place 1, the later ones' place 0
+    const float* base = reinterpret_cast<const float*>(static_cast<const Cut*>(a.workspace) + p.grid) +
+                        static_cast<int64_t>(i0) * 2 * kPart;
+    const auto part = [&](int i) { return base + (i == 0 ? kPart : i * 2 * kPart); };
+    float m = -INFINITY;
+    for (int i = tid; i < parts; i += kJoinThreads) {
+        weight[i] = part(i)[kHeads * DP + 2 * h];
+        m = fmaxf(m, weight[i]);
+    }
+#pragma unroll
+    for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, s));
+    if ((tid & 31) == 0) red[tid >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[w]);
+    const float from = m == -INFINITY ? 0.0f : m;
+    for (int i = tid; i < parts; i += kJoinThreads) weight[i] = exp2_fast(weight[i] - from);
+    __syncthreads();
+    const int v = tid % kVecs, first = tid / kVecs;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float l = 0.0f;
+#pragma unroll 4
+    for (int i = first; i < parts; i += kLanes) {
+        const float4 y = *reinterpret_cast<const float4*>(part(i) + h * DP + 4 * v);
+        const float w = weight[i];
+        x.x += w * y.x, x.y += w * y.y, x.z += w * y.z, x.w += w * y.w;
+        l += w * part(i)[kHeads * DP + 2 * h + 1];
+    }
+    acc[first][v] = x;
+    if (v == 0) lsum[first] = l;
+    __syncthreads();
+    if (first != 0) return;
+    l = 0.0f;
+    x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < kLanes; ++i) {
+        l += lsum[i];
+        const float4 y = acc[i][v];
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    }
+    if (4 * v < D) {
+        const float r = l == 0.0f ? 0.0f : p.out_scale / l;
+        T* out = static_cast<T*>(a.out) + cut.seq * a.out_ld + static_cast<int64_t>(head) * D + 4 * v;
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack<T>(x.x * r, x.y * r), pack<T>(x.z * r, x.w * r));
+    }
+    if (v == 0 && a.lse)
+        a.lse[static_cast<int64_t>(cut.seq) * a.num_heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+}
+
+template <typename T, bool FP8, int DP, int NT>
+cudaError_t launch_shape(const AttentionArgs& a, Plan p, int sms, cudaStream_t stream) {
+    using S = Shape<T, FP8, DP, NT>;
+    constexpr int smem = static_cast<int>(sizeof(typename S::Shared));
+    constexpr int resident = (227 * 1024) / (smem + 1024) < 4 ? (227 * 1024) / (smem + 1024) : 4;
+    static_assert(resident >= 1, "the ring must fit");
+    cudaError_t err = cudaFuncSetAttribute(attention_kernel<T, FP8, DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    const int64_t all = static_cast<int64_t>(a.B) * p.units;
+    const int64_t most = (static_cast<int64_t>(a.max_pages) * a.page_size + S::kChunk - 1) / S::kChunk;
+    const int64_t full = static_cast<int64_t>(sms) * resident;
+    p.grid = static_cast<int>(full < kMaxGrid ? full : kMaxGrid);
+    p.min_chunks = 4;
+    // sequences of at most min_chunks chunks are not worth cutting: whole units to each CTA and no join
+    p.split = most > p.min_chunks;
+    const int64_t useful = p.split ? (all * most + p.min_chunks - 1) / p.min_chunks : all;
+    if (useful < p.grid) p.grid = static_cast<int>(useful > 0 ? useful : 1);
+    err = launch_dependent(attention_kernel<T, FP8, DP, NT>, dim3(p.grid), dim3(kThreads), smem, stream, a, p);
+    if (err != cudaSuccess || !p.split) return err;
+    return launch_dependent(join_kernel<T, DP, NT>, dim3(p.grid, 8 * NT), dim3(kJoinThreads), 0, stream, a, p);
+}
+
+// Eights of query heads per unit: all of a cache head's, as far as the accumulators and the query
+// fragments (3/8 dp registers a thread for each eight) fit the register file. More heads make several
+// units, which read the keys and values again, mostly from L2.
+inline int eights(int group, int dp) {
+    const int nt = group <= 8 ? 1 : group <= 16 ? 2 : 4;
+    return nt * dp <= 256 ? nt : 256 / dp;
+}
+
+template <typename T, bool FP8>
+cudaError_t launch_type(const AttentionArgs& a, int sms, cudaStream_t stream) {
+    const int dp = a.head_dim <= 64 ? 64 : a.head_dim <= 128 ? 128 : 256;
+    const int group = a.num_heads / a.num_kv_heads, nt = eights(group, dp);
+    Plan p{};
+    p.blocks = (group + 8 * nt - 1) / (8 * nt);
+    p.units = a.num_kv_heads * p.blocks;
+    p.out_scale = FP8 ? a.v_scale : 1.0f;
+    int log = 0;
+    while ((int64_t{1} << log) < a.page_size) ++log;
+    p.page_shift = 31 + log;
+    p.page_mul = static_cast<unsigned>(((uint64_t{1} << p.page_shift) + a.page_size - 1) / a.page_size);
+    if (dp == 64)
+        return nt == 1   ? launch_shape<T, FP8, 64, 1>(a, p, sms, stream)
+               : nt == 2 ? launch_shape<T, FP8, 64, 2>(a, p, sms, stream)
+                         : launch_shape<T, FP8, 64, 4>(a, p, sms, stream);
+    if (dp == 128)
+        return nt == 1 ? launch_shape<T, FP8, 128, 1>(a, p, sms, stream) : launch_shape<T, FP8, 128, 2>(a, p, sms, stream);
+    return launch_shape<T, FP8, 256, 1>(a, p, sms, stream);
+}
+
+// One per (type, cache type), each in a translation unit of its own.
+cudaError_t launch_bf16(const AttentionArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_bf16_e4m3(const AttentionArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_fp16(const AttentionArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_fp16_e4m3(const AttentionArgs& a, int sms, cudaStream_t stream);
+
+}  // namespace attn
+}  // namespace ep

@@ -19,14 +19,14 @@ cudaError_t sm_count(int* sms) {
 
 }  // namespace
 
-// Two parts per CTA of the largest grid (four a core), each the heads of a unit
+// Two parts per CTA of the largest grid, each the heads of a unit
 // with their statistics.
 int64_t paged_attention_workspace(int, int num_heads, int num_kv_heads, int head_dim) {
     int sms = 0;
     if (sm_count(&sms) != cudaSuccess) return -1;
     const int dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
     const int eights = attn::eights(num_heads / num_kv_heads, dp);
-    const int64_t grid = 4 * sms < attn::kMaxGrid ? 4 * sms : attn::kMaxGrid;
+    const int64_t grid = attn::kMaxResident * sms < attn::kMaxGrid ? attn::kMaxResident * sms : attn::kMaxGrid;
     return grid * static_cast<int64_t>(sizeof(attn::Cut)) +
            grid * 2 * 8 * eights * (dp + 2) * static_cast<int64_t>(sizeof(float));
 }

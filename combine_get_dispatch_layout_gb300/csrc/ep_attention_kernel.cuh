@@ -18,8 +18,8 @@
 // The products run transposed, keys as the matrix instruction's 16 rows and
 // query heads as its 8 columns: S^T = K Q^T, O^T = V^T P^T. One cache head is
 // shared by few query heads (8 is common); as the 16-row operand they would
-// leave half the instruction empty. A warp takes a quarter of each chunk with
-// statistics of its own; the four warps join when a segment (a CTA's part of one
+// leave half the instruction empty. A warp takes its share of each chunk with
+// statistics of its own; the warps join when a segment (a CTA's part of one
 // sequence and head) ends.
 #pragma once
 
@@ -32,9 +32,8 @@
 namespace ep {
 namespace attn {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kJoinThreads = 256;
+constexpr int kMaxResident = 4; // CTAs a core, at most (the workspace is sized for this)
 constexpr int kMaxGrid = 1024;  // CTAs of the main kernel, and so parts of one sequence
 
 struct Plan {
@@ -45,6 +44,7 @@ struct Plan {
     unsigned page_mul, page_shift;  // i / page_size = (umulhi(i, page_mul) + ...) as page_of
     int min_chunks;  // a CTA's share is at least this many chunks
     float out_scale; // of O / l
+    int by_unit;     // join blocks belong to units (else to the CTAs a unit began in)
 };
 
 // Quotient by the page size for 0 <= i < 2^31: with L = ceil(log2 d) and
@@ -63,15 +63,27 @@ __device__ __forceinline__ int sequence(const AttentionArgs& a, int b, int& low,
     return (end - low) / CHUNK + ((end - low) % CHUNK != 0);
 }
 
-// Exclusive prefix of the sequences' chunks: total over all B, and for
-// `target` (a position in chunk space divided by `units`, see below) the
-// sequence that holds it and the chunks before that sequence. Every thread
-// gets the same result. THREADS threads, all of them.
+// CTAs that share W chunks, and the first chunk of CTA i.
+__device__ __forceinline__ int sharers(const Plan& p, int64_t W) {
+    return static_cast<int>(min(static_cast<int64_t>(p.grid), (W + p.min_chunks - 1) / p.min_chunks));
+}
+__device__ __forceinline__ int64_t share_start(int64_t W, int ctas, int i) { return W * i / ctas; }
+
+// All sequences' chunks laid end to end, each sequence's once per unit: a CTA's share of them.
+struct Share {
+    int64_t all;               // chunks in all (W)
+    int64_t start, count;      // this CTA's
+    int ctas;                  // CTAs that have one
+    int seq[2];                // the sequences of its first and its last chunk
+    int64_t before[2];         // chunks before those sequences
+};
+
+// Computed by a prefix sum over the sequences' chunks; every thread gets the same result.
 template <int THREADS, int CHUNK>
-__device__ int64_t find_sequence(const AttentionArgs& a, int units, int64_t target, int& seq, int64_t& before) {
+__device__ Share find_share(const AttentionArgs& a, const Plan& p) {
     __shared__ int64_t warp_sum[THREADS / 32];
-    __shared__ int64_t found_before;
-    __shared__ int found;
+    __shared__ int64_t found_before[2];
+    __shared__ int found[2];
     const int tid = threadIdx.x, lane = tid & 31;
     const int per = (a.B + THREADS - 1) / THREADS, first = min(a.B, tid * per), last = min(a.B, first + per);
     int64_t own = 0;
@@ -84,7 +96,6 @@ __device__ int64_t find_sequence(const AttentionArgs& a, int units, int64_t targ
         if (lane >= o) scan += v;
     }
     if (lane == 31) warp_sum[tid >> 5] = scan;
-    if (tid == 0) found = -1, found_before = 0;
     __syncthreads();
     int64_t total = 0, base = scan - own;
 #pragma unroll
@@ -92,28 +103,28 @@ __device__ int64_t find_sequence(const AttentionArgs& a, int units, int64_t targ
         if (w < (tid >> 5)) base += warp_sum[w];
         total += warp_sum[w];
     }
-    if (target >= base * units && target < (base + own) * units) {
+    Share s{};
+    s.all = total * p.units;
+    s.ctas = sharers(p, s.all);
+    if (static_cast<int>(blockIdx.x) >= s.ctas) return s;   // the whole block
+    s.start = share_start(s.all, s.ctas, blockIdx.x);
+    s.count = share_start(s.all, s.ctas, blockIdx.x + 1) - s.start;
+    base *= p.units;
+    const int64_t ends[2] = {s.start, s.start + s.count - 1};
+    if (ends[1] >= base && ends[0] < base + own * p.units) {
         for (int b = first; b < last; ++b) {
-            const int n = sequence<CHUNK>(a, b, low, end);
-            if (target < (base + n) * units) {
-                found = b;
-                found_before = base;
-                break;
-            }
+            const int64_t n = static_cast<int64_t>(sequence<CHUNK>(a, b, low, end)) * p.units;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (ends[i] >= base && ends[i] < base + n) found[i] = b, found_before[i] = base;
             base += n;
         }
     }
     __syncthreads();
-    seq = found;
-    before = found_before;
-    return total;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) s.seq[i] = found[i], s.before[i] = found_before[i];
+    return s;
 }
-
-// CTAs that share W chunks, and the first chunk of CTA i.
-__device__ __forceinline__ int sharers(const Plan& p, int64_t W) {
-    return static_cast<int>(min(static_cast<int64_t>(p.grid), (W + p.min_chunks - 1) / p.min_chunks));
-}
-__device__ __forceinline__ int64_t share_start(int64_t W, int ctas, int i) { return W * i / ctas; }
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 // 16 bytes to shared memory, of which the first `real` (16 or 0) are read and the rest are zeros.
@@ -202,28 +213,28 @@ template <typename T, bool FP8, int DP, int NT>
 struct Shape {
     using M = std::conditional_t<FP8, __half, T>;   // type of the products' operands
     static constexpr int kHeads = 8 * NT;
+    // Warps: kKeyWarps shares of a chunk's keys times NT eights of heads. Codes have to be unpacked for half the
+    // bytes, so an e4m3 cache needs more warps to keep up with DRAM.
+    static constexpr int kKeyWarps = FP8 && NT == 1 && DP <= 128 ? 8 : 4;
+    static constexpr int kThreads = 32 * kKeyWarps * NT;
     static constexpr int kCacheBytes = FP8 ? 1 : 2;
     static constexpr int kRowBytes = DP * kCacheBytes;
     static constexpr int kPieces = kRowBytes / 16;          // 16-byte pieces of a row
-    // Keys per chunk: 32 KB of keys and values (64 KB for 512-byte rows), 16 * kTiles keys a warp.
-    static constexpr int kTiles = kRowBytes <= 64 ? 4 : kRowBytes <= 128 ? 2 : 1;
-    static constexpr int kChunk = 16 * kWarps * kTiles;
+    // Keys per chunk: 32 KB of keys and values (64 KB for 512-byte rows), 16 kTiles keys a warp.
+    static constexpr int kChunk = kRowBytes <= 64 ? 256 : kRowBytes <= 128 ? 128 : 64;
+    static constexpr int kTiles = kChunk / (16 * kKeyWarps);
     static constexpr int kTile = kChunk * kRowBytes;        // bytes of a chunk's keys, or values
     // Three slots: two CTAs a core keep 128 KB on the way, above what DRAM's latency needs at full rate.
     static constexpr int kSlots = 3;
-    static constexpr int kQueryStride = DP + 8;             // 16-bit values; keeps fragment loads off one bank
 
     struct Shared {
         alignas(128) unsigned char ring[kSlots][2][kTile];  // a used-up slot also serves the join of the warps
-        alignas(16) T query_raw[kSlots][kHeads][DP];
-        alignas(16) M query[kHeads][kQueryStride];
         RowAt at[kSlots + 1][kChunk];
         unsigned real[kSlots + 1][kChunk / 32];             // bit per key: it exists
         SlotInfo info[kSlots + 1];
-        float top[kWarps][kHeads], sum[kWarps][kHeads];
-        float query_scale[kHeads];
+        float top[kKeyWarps][kHeads], sum[kKeyWarps][kHeads];
     };
-    static_assert(kWarps * kHeads * DP * 4 <= 2 * kTile, "the join of the warps fits a slot");
+    static_assert(kKeyWarps * kHeads * DP * 4 <= 2 * kTile, "the join of the warps fits a slot");
 
     // Byte offset of 16-byte piece c of row r: pieces are exchanged within 8 (4) so that the 8
     // rows of a matrix load, and the 2 rows x 4 pieces of the e4m3 key loads, lie in different banks.
@@ -234,15 +245,17 @@ struct Shape {
 };
 
 template <typename T, bool FP8, int DP, int NT>
-__global__ void __launch_bounds__(kThreads) attention_kernel(AttentionArgs a, Plan p) {
+__global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_kernel(AttentionArgs a, Plan p) {
     using S = Shape<T, FP8, DP, NT>;
     using M = typename S::M;
     extern __shared__ __align__(128) unsigned char shared_bytes[];
     typename S::Shared& sh = *reinterpret_cast<typename S::Shared*>(shared_bytes);
     constexpr int kSlots = S::kSlots, kInfos = kSlots + 1, kChunk = S::kChunk, kTiles = S::kTiles;
+    constexpr int kWarps = S::kKeyWarps, kThreads = S::kThreads;
     dependent_entry();
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int warp = (tid >> 5) % kWarps, eight = (tid >> 5) / kWarps;   // share of the keys, of the heads
     const int D = a.head_dim, group = a.num_heads / a.num_kv_heads;
     Cut* cuts = static_cast<Cut*>(a.workspace);   // [grid], then the parts
     float* part = reinterpret_cast<float*>(cuts + p.grid);
@@ -251,10 +264,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(AttentionArgs a, Pl
     int seq, unit, chunk, chunks, low, end;
     int64_t left;
     if (p.split) {
-        int64_t before;
-        const int64_t total = find_sequence<kThreads, kChunk>(a, p.units, -1, seq, before);
-        const int64_t W = total * p.units;
-        const int ctas = sharers(p, W);
+        const Share share = find_share<kThreads, kChunk>(a, p);
         // sequences without keys: zeros
         for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
             if (sequence<kChunk>(a, b, low, end) > 0) continue;
@@ -263,27 +273,27 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(AttentionArgs a, Pl
             if (a.lse)
                 for (int h = tid; h < a.num_heads; h += kThreads) a.lse[static_cast<int64_t>(b) * a.num_heads + h] = -INFINITY;
         }
-        if (tid == 0) cuts[blockIdx.x].seq = -1;
-        if (static_cast<int>(blockIdx.x) >= ctas) return;
-        const int64_t start = share_start(W, ctas, blockIdx.x);
-        left = share_start(W, ctas, blockIdx.x + 1) - start;
-        __syncthreads();
-        find_sequence<kThreads, kChunk>(a, p.units, start, seq, before);
+        if (static_cast<int>(blockIdx.x) >= share.ctas) {
+            if (tid == 0) cuts[blockIdx.x].seq = -1;
+            return;
+        }
+        left = share.count;
+        if (tid == 0) {
+            // the unit that holds this share's last chunk, if it began here and goes on behind it
+            int lo, en;
+            const int n = sequence<kChunk>(a, share.seq[1], lo, en);
+            const int64_t last_unit = (share.start + left - 1 - share.before[1]) / n;
+            const int64_t from = share.before[1] + last_unit * n, behind = from + n;
+            Cut cut{-1, 0, 0, 0};
+            if (from >= share.start && behind > share.start + left)
+                // the CTA whose share holds position x is the largest i with all i / ctas (rounded down) <= x
+                cut = {share.seq[1], static_cast<int>(last_unit), static_cast<int>((behind * share.ctas - 1) / share.all), 0};
+            cuts[blockIdx.x] = cut;
+        }
+        seq = share.seq[0];
         chunks = sequence<kChunk>(a, seq, low, end);
-        const int64_t in = start - before * p.units;
-        unit = static_cast<int>(in / chunks);
-        chunk = static_cast<int>(in % chunks);
-        // the unit that holds this share's last chunk, if it began here and goes on behind it
-        int last_seq;
-        __syncthreads();
-        find_sequence<kThreads, kChunk>(a, p.units, start + left - 1, last_seq, before);
-        int lo, en;
-        const int n = sequence<kChunk>(a, last_seq, lo, en);
-        const int64_t base = before * p.units, last_unit = (start + left - 1 - base) / n;
-        const int64_t from = base + last_unit * n, behind = from + n;
-        if (tid == 0 && from >= start && behind > start + left)
-            // the CTA whose share holds position x is the largest i with W i / ctas (rounded down) <= x
-            cuts[blockIdx.x] = {last_seq, static_cast<int>(last_unit), static_cast<int>((behind * ctas - 1) / W), 0};
+        unit = static_cast<int>((share.start - share.before[0]) / chunks);
+        chunk = static_cast<int>((share.start - share.before[0]) % chunks);
     } else {
         const int64_t all = static_cast<int64_t>(a.B) * p.units;
         int64_t u = share_start(all, gridDim.x, blockIdx.x);
@@ -310,7 +320,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(AttentionArgs a, Pl
 
     // ---- ring. A chunk's rows are looked up in the block table (look_up, which only issues the loads, and
     // note, which writes the rows' places) one chunk before copies() starts their way to the ring slot.
-    // A thread looks up rows tid, tid + 128; with 64 keys a chunk, each half of the block every other chunk's.
+    // Rows by thread; with fewer rows than threads, other warps for every chunk.
     constexpr int kLookups = (kChunk + kThreads - 1) / kThreads;
     int64_t located = 0;
     int note_slot = 0;
@@ -318,7 +328,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(AttentionArgs a, Pl
     int page_place[kLookups];
     const auto look_row = [&](int k) {
         if constexpr (kChunk >= kThreads) return tid + k * kThreads;
-        return (tid + static_cast<int>(located & 1) * kChunk) % kThreads;
+        return (tid + static_cast<int>(located) * kChunk) & (kThreads - 1);
     };
     const auto look_up = [&]() {
         if (located >= left) return;
@@ -378,7 +388,6 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(AttentionArgs a, Pl
     const unsigned char* key_base = static_cast<const unsigned char*>(a.k ? a.k : a.q) + (piece_bytes ? piece * 16 : 0);
     const unsigned char* value_base = static_cast<const unsigned char*>(a.v ? a.v : a.q) + (piece_bytes ? piece * 16 : 0);
     int copy_slot = 0, copy_info = 0;
-    bool copied_any = false;
     const auto copies = [&]() {
         const SlotInfo in = sh.info[copy_info];
         if (in.unit >= 0) {
@@ -404,17 +413,6 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(AttentionArgs a, Pl
                     copy16(to(r) + S::kTile, value_base + at.value, bytes);
                 }
             }
-            if (!copied_any || in.chunk == 0) {   // a segment starts: its queries
-                const int h0 = in.unit / p.blocks * group + in.unit % p.blocks * S::kHeads;
-                const int heads = min(S::kHeads, group - in.unit % p.blocks * S::kHeads);
-                const T* q = static_cast<const T*>(a.q) + in.seq * a.q_ld + static_cast<int64_t>(h0) * D;
-                for (int i = tid; i < S::kHeads * (DP / 8); i += kThreads) {
-                    const int h = i / (DP / 8), c = i % (DP / 8) * 8;
-                    const bool real = h < heads && c < D;
-                    copy16(smem_addr(&sh.query_raw[copy_slot][h][c]), q + (real ? h * D + c : 0), real ? 16 : 0);
-                }
-            }
-            copied_any = true;
         }
         copy_commit();
         copy_slot = copy_slot + 1 == kSlots ? 0 : copy_slot + 1;
@@ -431,9 +429,22 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(AttentionArgs a, Pl
     for (int i = 0; i < kSlots - 1; ++i) copies();
 
     // ---- the pass over the chunks
-    float o[DP / 16][NT][4];                   // O^T: rows d, columns heads
-    float top[NT][2], sum[NT][2], c2[NT][2];   // of heads 8 nt + 2 t, + 1
-    uint32_t qf[DP / 16][NT][2];
+    float o[DP / 16][4];             // O^T: rows d, columns heads
+    float top[2], sum[2], c2[2];     // of the warp's heads 2 t, 2 t + 1
+    uint32_t qf[DP / 16][2];
+    // Queries as the products' column operand: value pairs of step k for head g. An e4m3 key load brings 16
+    // neighbouring values a lane, so its steps run through the head in that order.
+    const auto load_queries = [&](const SlotInfo& in) {
+        const int in_group = in.unit % p.blocks * S::kHeads + 8 * eight + g;
+        const T* q = static_cast<const T*>(a.q) + in.seq * a.q_ld + static_cast<int64_t>(in.unit / p.blocks * group + in_group) * D;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int d = FP8 ? (k / 4) * 64 + 16 * t + (k % 4) * 4 + 2 * j : 16 * k + 2 * t + 8 * j;
+                qf[k][j] = in_group < group && d < D ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
+            }
+    };
     int slot = 0, info = 0, first_chunk = 0;
     bool fresh = true;
     for (int64_t n = 0; n < left; ++n) {
@@ -443,65 +454,52 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(AttentionArgs a, Pl
         copies();
         look_up();
         if (fresh || in.chunk == 0) {
-            // a segment starts: queries to the products' type, fresh statistics
+            // a segment starts: its queries, fresh statistics
             fresh = false;
             first_chunk = in.chunk;
-            for (int h = warp; h < S::kHeads; h += kWarps) {
-                const T* raw = sh.query_raw[slot][h];
-                float scale = 1.0f;
-                if constexpr (FP8) {
-                    // a power of two that brings the head's largest query to [2^14, 2^15): fp16 then holds every
-                    // one of them to 2^-11, or to 2^-39 of the largest, whatever its type's range
-                    float big = 0.0f;
-                    for (int d = lane; d < DP; d += 32) big = fmaxf(big, fabsf(to_float(raw[d])));
+            load_queries(in);
+            float scale[2] = {1.0f, 1.0f};
+            if constexpr (FP8) {
+                // a power of two brings the head's largest query to [2^14, 2^15): fp16 then holds every one of
+                // them to 2^-11, or to 2^-39 of the largest, whatever its type's range
+                const auto value = [](uint32_t pair, int j) {
+                    const uint16_t half = static_cast<uint16_t>(j ? pair >> 16 : pair);
+                    return to_float(*reinterpret_cast<const T*>(&half));
+                };
+                float big = 0.0f;
 #pragma unroll
-                    for (int s = 16; s; s >>= 1) big = fmaxf(big, __shfl_xor_sync(kFullMask, big, s));
-                    const int e = big > 0.0f && big < INFINITY ? min(14 - ilogbf(big), 126) : 0;
-                    const float up = __int_as_float((e + 127) << 23);
-                    for (int d = lane; d < DP; d += 32) sh.query[h][d] = __float2half_rn(to_float(raw[d]) * up);
-                    scale = __int_as_float((127 - e) << 23);
-                } else {
-                    for (int d = lane * 8; d < DP; d += 256)
-                        *reinterpret_cast<uint4*>(&sh.query[h][d]) = *reinterpret_cast<const uint4*>(&raw[d]);
-                }
-                if (lane == 0) sh.query_scale[h] = scale;
+                for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) big = fmaxf(big, fabsf(value(qf[k][j >> 1], j & 1)));
+                big = fmaxf(big, __shfl_xor_sync(kFullMask, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(kFullMask, big, 2));
+                const int e = big > 0.0f && big < INFINITY ? min(14 - ilogbf(big), 126) : 0;
+                const float up = __int_as_float((e + 127) << 23), down = __int_as_float((127 - e) << 23);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) qf[k][j] = pack<M>(value(qf[k][j], 0) * up, value(qf[k][j], 1) * up);
+                scale[0] = __shfl_sync(kFullMask, down, 8 * t);      // of heads 2 t and 2 t + 1
+                scale[1] = __shfl_sync(kFullMask, down, 8 * t + 4);
             }
-            __syncthreads();
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    top[nt][j] = -INFINITY;
-                    sum[nt][j] = 0.0f;
-                    c2[nt][j] = a.score_scale * sh.query_scale[8 * nt + 2 * t + j] * 1.4426950408889634f;
-                }
+            for (int j = 0; j < 2; ++j) {
+                top[j] = -INFINITY;
+                sum[j] = 0.0f;
+                c2[j] = a.score_scale * scale[j] * 1.4426950408889634f;
+            }
 #pragma unroll
             for (int m = 0; m < DP / 16; ++m)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) o[m][nt][j] = 0.0f;
-            // queries as the products' column operand: value pairs of step k; an e4m3 key load brings 16
-            // neighbouring values a lane, so its steps run through the head in that order
-#pragma unroll
-            for (int k = 0; k < DP / 16; ++k)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        qf[k][nt][j] = *reinterpret_cast<const uint32_t*>(
-                            sh.query[8 * nt + g] +
-                            (FP8 ? (k / 4) * 64 + 16 * t + (k % 4) * 4 + 2 * j : 16 * k + 2 * t + 8 * j));
+                for (int j = 0; j < 4; ++j) o[m][j] = 0.0f;
         }
         // S^T = K Q^T for this warp's keys r0 .. r0 + 16 kTiles - 1
         const unsigned char* keys = sh.ring[slot][0];
         const unsigned char* values = sh.ring[slot][1];
         const int r0 = warp * 16 * kTiles;
-        float s[kTiles][NT][4];
+        float s[kTiles][4];
 #pragma unroll
-        for (int kt = 0; kt < kTiles; ++kt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[kt][nt][0] = s[kt][nt][1] = s[kt][nt][2] = s[kt][nt][3] = 0.0f;
+        for (int kt = 0; kt < kTiles; ++kt) s[kt][0] = s[kt][1] = s[kt][2] = s[kt][3] = 0.0f;
         if constexpr (FP8) {
 #pragma unroll
             for (int j = 0; j < DP / 64; ++j)
@@ -513,8 +511,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(AttentionArgs a, Pl
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t af[4] = {e4m3_pair(xs[i]), e4m3_pair(ys[i]), e4m3_pair(xs[i] >> 16), e4m3_pair(ys[i] >> 16)};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) multiply<M>(s[kt][nt], af, qf[4 * j + i][nt][0], qf[4 * j + i][nt][1]);
+                        multiply<M>(s[kt], af, qf[4 * j + i][0], qf[4 * j + i][1]);
                     }
                 }
         } else {
@@ -524,79 +521,59 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(AttentionArgs a, Pl
                 for (int kt = 0; kt < kTiles; ++kt) {
                     uint32_t af[4];
                     load_matrices(af, smem_addr(keys + S::place(r0 + 16 * kt + (lane & 15), 2 * k + (lane >> 4))));
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) multiply<M>(s[kt][nt], af, qf[k][nt][0], qf[k][nt][1]);
+                    multiply<M>(s[kt], af, qf[k][0], qf[k][1]);
                 }
         }
-        // softmax: this lane's keys r0 + 16 kt + g and + 8 (s[..][0, 1] and [2, 3]) for two heads. The maximum that
+        // softmax: this lane's keys r0 + 16 kt + g and + 8 (s[kt][0, 1] and [2, 3]) for two heads. The maximum that
         // the weights refer to follows the running one only when a score passes it by more than kSlack: the weights
         // stay below 2^kSlack, which fp16 and fp32 hold as well, and most chunks need no exchange between lanes.
         constexpr float kSlack = 8.0f;
 #pragma unroll
         for (int kt = 0; kt < kTiles; ++kt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[kt][nt][j] *= c2[nt][j & 1];
+            for (int j = 0; j < 4; ++j) s[kt][j] *= c2[j & 1];
         if (!all_real(info)) {
 #pragma unroll
             for (int kt = 0; kt < kTiles; ++kt) {
                 const unsigned mask = sh.real[info][(r0 + 16 * kt) >> 5] >> ((r0 + 16 * kt) & 31);
-                const bool in0 = (mask >> g) & 1, in1 = (mask >> (g + 8)) & 1;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if (!in0) s[kt][nt][j] = -INFINITY;
-                        if (!in1) s[kt][nt][2 + j] = -INFINITY;
-                    }
+                if (!((mask >> g) & 1)) s[kt][0] = s[kt][1] = -INFINITY;
+                if (!((mask >> (g + 8)) & 1)) s[kt][2] = s[kt][3] = -INFINITY;
             }
         }
         bool over = false;
 #pragma unroll
         for (int kt = 0; kt < kTiles; ++kt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) over |= s[kt][nt][j] > top[nt][j & 1] + kSlack;
+            for (int j = 0; j < 4; ++j) over |= s[kt][j] > top[j & 1] + kSlack;
         if (__any_sync(kFullMask, over)) {
+            float fade[2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float fade[2];
+            for (int j = 0; j < 2; ++j) {
+                float m = top[j];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float m = top[nt][j];
-#pragma unroll
-                    for (int kt = 0; kt < kTiles; ++kt) m = fmaxf(m, fmaxf(s[kt][nt][j], s[kt][nt][2 + j]));
-                    m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 4));
-                    m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 8));
-                    m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 16));
-                    fade[j] = exp2_fast(top[nt][j] - (m == -INFINITY ? 0.0f : m));
-                    top[nt][j] = m;
-                    sum[nt][j] *= fade[j];
-                }
-#pragma unroll
-                for (int m = 0; m < DP / 16; ++m) {
-                    o[m][nt][0] *= fade[0], o[m][nt][1] *= fade[1];
-                    o[m][nt][2] *= fade[0], o[m][nt][3] *= fade[1];
-                }
+                for (int kt = 0; kt < kTiles; ++kt) m = fmaxf(m, fmaxf(s[kt][j], s[kt][2 + j]));
+                m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 4));
+                m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 8));
+                m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 16));
+                fade[j] = exp2_fast(top[j] - (m == -INFINITY ? 0.0f : m));
+                top[j] = m;
+                sum[j] *= fade[j];
             }
+#pragma unroll
+            for (int m = 0; m < DP / 16; ++m) o[m][0] *= fade[0], o[m][1] *= fade[1], o[m][2] *= fade[0], o[m][3] *= fade[1];
         }
-        uint32_t pf[kTiles][NT][2];
+        uint32_t pf[kTiles][2];
+        // (nothing seen yet: all weights 0)
+        const float base[2] = {top[0] == -INFINITY ? 0.0f : top[0], top[1] == -INFINITY ? 0.0f : top[1]};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            // nothing seen yet: all weights 0
-            const float base[2] = {top[nt][0] == -INFINITY ? 0.0f : top[nt][0], top[nt][1] == -INFINITY ? 0.0f : top[nt][1]};
+        for (int kt = 0; kt < kTiles; ++kt) {
+            float pr[4];
 #pragma unroll
-            for (int kt = 0; kt < kTiles; ++kt) {
-                float pr[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) pr[j] = exp2_fast(s[kt][nt][j] - base[j & 1]);
-                sum[nt][0] += pr[0] + pr[2];
-                sum[nt][1] += pr[1] + pr[3];
-                pf[kt][nt][0] = transpose8x8(pack<M>(pr[0], pr[1]));
-                pf[kt][nt][1] = transpose8x8(pack<M>(pr[2], pr[3]));
-            }
+            for (int j = 0; j < 4; ++j) pr[j] = exp2_fast(s[kt][j] - base[j & 1]);
+            sum[0] += pr[0] + pr[2];
+            sum[1] += pr[1] + pr[3];
+            pf[kt][0] = transpose8x8(pack<M>(pr[0], pr[1]));
+            pf[kt][1] = transpose8x8(pack<M>(pr[2], pr[3]));
         }
         // O^T += V^T P^T
         if constexpr (FP8) {
@@ -612,8 +589,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(AttentionArgs a, Pl
                         // bytes (key, value): (0,0) (0,1) (1,0) (1,1); row g of the tile is value 2 g, row g + 8 value 2 g + 1
                         const uint32_t u0 = __byte_perm(v[2 * i], 0, 0x3120), u1 = __byte_perm(v[2 * i + 1], 0, 0x3120);
                         const uint32_t af[4] = {e4m3_pair(u0), e4m3_pair(u0 >> 16), e4m3_pair(u1), e4m3_pair(u1 >> 16)};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) multiply<M>(o[m + i][nt], af, pf[kt][nt][0], pf[kt][nt][1]);
+                        multiply<M>(o[m + i], af, pf[kt][0], pf[kt][1]);
                     }
                 }
         } else {
@@ -624,44 +600,39 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(AttentionArgs a, Pl
                     uint32_t af[4];
                     load_matrices_transposed(
                         af, smem_addr(values + S::place(r0 + 16 * kt + (lane & 7) + ((lane >> 4) << 3), 2 * m + ((lane >> 3) & 1))));
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) multiply<M>(o[m][nt], af, pf[kt][nt][0], pf[kt][nt][1]);
+                    multiply<M>(o[m], af, pf[kt][0], pf[kt][1]);
                 }
         }
 
         if (n + 1 == left || in.chunk + 1 == in.chunks) {
             // ---- the segment ends: join the warps, in their order, through the slot just used up, and write
+            const int head0 = 8 * eight + 2 * t;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float l = sum[nt][j];
-                    l += __shfl_xor_sync(kFullMask, l, 4);
-                    l += __shfl_xor_sync(kFullMask, l, 8);
-                    l += __shfl_xor_sync(kFullMask, l, 16);
-                    if (g == 0) sh.top[warp][8 * nt + 2 * t + j] = top[nt][j], sh.sum[warp][8 * nt + 2 * t + j] = l;
-                }
+            for (int j = 0; j < 2; ++j) {
+                float l = sum[j];
+                l += __shfl_xor_sync(kFullMask, l, 4);
+                l += __shfl_xor_sync(kFullMask, l, 8);
+                l += __shfl_xor_sync(kFullMask, l, 16);
+                if (g == 0) sh.top[warp][head0 + j] = top[j], sh.sum[warp][head0 + j] = l;
+            }
             __syncthreads();
             float* stage = reinterpret_cast<float*>(sh.ring[slot][0]);   // [kWarps][kHeads][DP]
+            float fade[2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float fade[2];
+            for (int j = 0; j < 2; ++j) {
+                float m = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float m = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sh.top[w][8 * nt + 2 * t + j]);
-                    fade[j] = exp2_fast(top[nt][j] - (m == -INFINITY ? 0.0f : m));
-                }
-                // heads 2 t apart by a multiple of 32 words: value index exchanged by t * 8 to keep off one bank
-#pragma unroll
-                for (int m = 0; m < DP / 16; ++m)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int d = 16 * m + (FP8 ? 2 * g + (j >> 1) : g + 8 * (j >> 1));
-                        stage[(warp * S::kHeads + 8 * nt + 2 * t + (j & 1)) * DP + (d ^ (t << 3))] = o[m][nt][j] * fade[j & 1];
-                    }
+                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sh.top[w][head0 + j]);
+                fade[j] = exp2_fast(top[j] - (m == -INFINITY ? 0.0f : m));
             }
+            // heads 2 t apart by a multiple of 32 words: value index exchanged by t * 8 to keep off one bank
+#pragma unroll
+            for (int m = 0; m < DP / 16; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int d = 16 * m + (FP8 ? 2 * g + (j >> 1) : g + 8 * (j >> 1));
+                    stage[(warp * S::kHeads + head0 + (j & 1)) * DP + (d ^ (t << 3))] = o[m][j] * fade[j & 1];
+                }
             __syncthreads();
             const int hb = in.unit % p.blocks;
             const int h0 = in.unit / p.blocks * group + hb * S::kHeads, heads = min(S::kHeads, group - hb * S::kHeads);
@@ -705,25 +676,77 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(AttentionArgs a, Pl
     copy_wait<0>();
 }
 
-// Joins the parts of the units that several CTAs shared, in the CTAs' order. Block (i, h): head h of the
-// unit that began in CTA i and went on behind it, if there is one.
+// Joins the parts of the units that several CTAs shared, in the CTAs' order. With many sequences most units
+// have few parts, and waves of blocks would cost more than the loads: blocks (i, *) serve the unit that
+// began in CTA i and went on behind it, if there is one, the first of them all of its heads (another block
+// each if the parts are many). With few long sequences (by_unit) the parts are many: blocks (u, *) serve
+// unit u, each 32 values of one head, its threads over values and parts.
 template <typename T, int DP, int NT>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, Plan p) {
-    constexpr int kHeads = 8 * NT, kVecs = DP / 4, kLanes = kJoinThreads / kVecs, kPart = kHeads * (DP + 2);
+    constexpr int kHeads = 8 * NT, kVecs = DP / 4, kLanes = kJoinThreads / kVecs, kPart = kHeads * (DP + 2), kFew = 8;
     __shared__ float weight[kMaxGrid];
     __shared__ float red[kJoinThreads / 32];
-    __shared__ float4 acc[kLanes][kVecs];
-    __shared__ float lsum[kLanes];
+    __shared__ float4 acc[kJoinThreads];
+    __shared__ float lsum[kJoinThreads / 8];
+    __shared__ int found;
     dependent_entry();
-    const Cut cut = static_cast<const Cut*>(a.workspace)[blockIdx.x];
-    const int group = a.num_heads / a.num_kv_heads, h = blockIdx.y, in_group = cut.unit % p.blocks * kHeads + h;
-    if (cut.seq < 0 || in_group >= group) return;
-    const int tid = threadIdx.x, D = a.head_dim, i0 = blockIdx.x, parts = cut.last - i0 + 1;
-    const int head = cut.unit / p.blocks * group + in_group;
+    const int tid = threadIdx.x, D = a.head_dim;
+    int i0 = blockIdx.x;
+    if (p.by_unit) {
+        if (tid == 0) found = -1;
+        __syncthreads();
+        for (int i = tid; i < p.grid; i += kJoinThreads) {
+            const Cut c = static_cast<const Cut*>(a.workspace)[i];
+            if (c.seq >= 0 && static_cast<int64_t>(c.seq) * p.units + c.unit == blockIdx.x) found = i;
+        }
+        __syncthreads();
+        i0 = found;
+        if (i0 < 0) return;
+    }
+    const Cut cut = static_cast<const Cut*>(a.workspace)[i0];
+    if (cut.seq < 0) return;
+    const int group = a.num_heads / a.num_kv_heads, first_head = cut.unit % p.blocks * kHeads;   // within the group
+    const int parts = cut.last - i0 + 1;
     // CTA i0's place 1, the later ones' place 0
     const float* base = reinterpret_cast<const float*>(static_cast<const Cut*>(a.workspace) + p.grid) +
                         static_cast<int64_t>(i0) * 2 * kPart;
     const auto part = [&](int i) { return base + (i == 0 ? kPart : i * 2 * kPart); };
+    const int vecs = p.by_unit ? 8 : kVecs, lanes = kJoinThreads / vecs, lane = tid / vecs;
+    const int v = tid % vecs + (p.by_unit ? blockIdx.y % (DP / 32) * 8 : 0);
+    const auto write = [&](int h, const float4& x, float m, float l) {
+        const int head = cut.unit / p.blocks * group + first_head + h;
+        if (4 * v < D) {
+            const float r = l == 0.0f ? 0.0f : p.out_scale / l;
+            T* out = static_cast<T*>(a.out) + cut.seq * a.out_ld + static_cast<int64_t>(head) * D + 4 * v;
+            *reinterpret_cast<uint2*>(out) = make_uint2(pack<T>(x.x * r, x.y * r), pack<T>(x.z * r, x.w * r));
+        }
+        if (v == 0 && a.lse)
+            a.lse[static_cast<int64_t>(cut.seq) * a.num_heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+    };
+    if (!p.by_unit && parts <= kFew) {
+        if (blockIdx.y != 0) return;
+        for (int h = lane; h < kHeads && first_head + h < group; h += kLanes) {
+            float m = -INFINITY, tops[kFew], l = 0.0f;
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f), y[kFew];
+#pragma unroll
+            for (int i = 0; i < kFew; ++i)
+                if (i < parts) {
+                    y[i] = *reinterpret_cast<const float4*>(part(i) + h * DP + 4 * v);
+                    m = fmaxf(m, tops[i] = part(i)[kHeads * DP + 2 * h]);
+                }
+#pragma unroll
+            for (int i = 0; i < kFew; ++i)
+                if (i < parts) {
+                    const float w = exp2_fast(tops[i] - (m == -INFINITY ? 0.0f : m));
+                    x.x += w * y[i].x, x.y += w * y[i].y, x.z += w * y[i].z, x.w += w * y[i].w;
+                    l += w * part(i)[kHeads * DP + 2 * h + 1];
+                }
+            write(h, x, m, l);
+        }
+        return;
+    }
+    const int h = p.by_unit ? blockIdx.y / (DP / 32) : blockIdx.y;
+    if (first_head + h >= group) return;
     float m = -INFINITY;
     for (int i = tid; i < parts; i += kJoinThreads) {
         weight[i] = part(i)[kHeads * DP + 2 * h];
@@ -735,60 +758,71 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, Pla
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[w]);
-    const float from = m == -INFINITY ? 0.0f : m;
-    for (int i = tid; i < parts; i += kJoinThreads) weight[i] = exp2_fast(weight[i] - from);
+    for (int i = tid; i < parts; i += kJoinThreads) weight[i] = exp2_fast(weight[i] - (m == -INFINITY ? 0.0f : m));
     __syncthreads();
-    const int v = tid % kVecs, first = tid / kVecs;
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float l = 0.0f;
-#pragma unroll 4
-    for (int i = first; i < parts; i += kLanes) {
+#pragma unroll 8
+    for (int i = lane; i < parts; i += lanes) {
         const float4 y = *reinterpret_cast<const float4*>(part(i) + h * DP + 4 * v);
         const float w = weight[i];
         x.x += w * y.x, x.y += w * y.y, x.z += w * y.z, x.w += w * y.w;
         l += w * part(i)[kHeads * DP + 2 * h + 1];
     }
-    acc[first][v] = x;
-    if (v == 0) lsum[first] = l;
+    acc[tid] = x;
+    if (tid % vecs == 0) lsum[lane] = l;
     __syncthreads();
-    if (first != 0) return;
+    if (lane != 0) return;
     l = 0.0f;
     x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int i = 0; i < kLanes; ++i) {
+#pragma unroll 4
+    for (int i = 0; i < lanes; ++i) {
         l += lsum[i];
-        const float4 y = acc[i][v];
+        const float4 y = acc[i * vecs + tid];
         x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
     }
-    if (4 * v < D) {
-        const float r = l == 0.0f ? 0.0f : p.out_scale / l;
-        T* out = static_cast<T*>(a.out) + cut.seq * a.out_ld + static_cast<int64_t>(head) * D + 4 * v;
-        *reinterpret_cast<uint2*>(out) = make_uint2(pack<T>(x.x * r, x.y * r), pack<T>(x.z * r, x.w * r));
-    }
-    if (v == 0 && a.lse)
-        a.lse[static_cast<int64_t>(cut.seq) * a.num_heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+    write(h, x, m, l);
+}
+
+// CTAs of the kernel that the current device holds at once; its shared memory limit is raised on the way.
+// Fixed properties, looked up once per device (a race writes the same value twice).
+template <typename Kernel>
+cudaError_t resident_ctas(Kernel kernel, int threads, int smem, int sms, int* known, int* ctas) {
+    constexpr int kDevices = 64;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < kDevices && (*ctas = __atomic_load_n(&known[dev], __ATOMIC_RELAXED)) > 0) return cudaSuccess;
+    int per_sm = 0;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err == cudaSuccess) err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+    if (err != cudaSuccess) return err;
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    *ctas = (per_sm < kMaxResident ? per_sm : kMaxResident) * sms;
+    if (*ctas > kMaxGrid) *ctas = kMaxGrid;
+    if (dev < kDevices) __atomic_store_n(&known[dev], *ctas, __ATOMIC_RELAXED);
+    return cudaSuccess;
 }
 
 template <typename T, bool FP8, int DP, int NT>
 cudaError_t launch_shape(const AttentionArgs& a, Plan p, int sms, cudaStream_t stream) {
     using S = Shape<T, FP8, DP, NT>;
     constexpr int smem = static_cast<int>(sizeof(typename S::Shared));
-    constexpr int resident = (227 * 1024) / (smem + 1024) < 4 ? (227 * 1024) / (smem + 1024) : 4;
-    static_assert(resident >= 1, "the ring must fit");
-    cudaError_t err = cudaFuncSetAttribute(attention_kernel<T, FP8, DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static int known[64];
+    cudaError_t err = resident_ctas(attention_kernel<T, FP8, DP, NT>, S::kThreads, smem, sms, known, &p.grid);
     if (err != cudaSuccess) return err;
     const int64_t all = static_cast<int64_t>(a.B) * p.units;
     const int64_t most = (static_cast<int64_t>(a.max_pages) * a.page_size + S::kChunk - 1) / S::kChunk;
-    const int64_t full = static_cast<int64_t>(sms) * resident;
-    p.grid = static_cast<int>(full < kMaxGrid ? full : kMaxGrid);
     p.min_chunks = 4;
     // sequences of at most min_chunks chunks are not worth cutting: whole units to each CTA and no join
     p.split = most > p.min_chunks;
     const int64_t useful = p.split ? (all * most + p.min_chunks - 1) / p.min_chunks : all;
     if (useful < p.grid) p.grid = static_cast<int>(useful > 0 ? useful : 1);
-    err = launch_dependent(attention_kernel<T, FP8, DP, NT>, dim3(p.grid), dim3(kThreads), smem, stream, a, p);
+    err = launch_dependent(attention_kernel<T, FP8, DP, NT>, dim3(p.grid), dim3(S::kThreads), smem, stream, a, p);
     if (err != cudaSuccess || !p.split) return err;
-    return launch_dependent(join_kernel<T, DP, NT>, dim3(p.grid, 8 * NT), dim3(kJoinThreads), 0, stream, a, p);
+    p.by_unit = all * 4 <= p.grid;
+    const dim3 join_grid = p.by_unit ? dim3(static_cast<unsigned>(all), 8 * NT * (DP / 32)) : dim3(p.grid, 8 * NT);
+    return launch_dependent(join_kernel<T, DP, NT>, join_grid, dim3(kJoinThreads), 0, stream, a, p);
 }
 
 // Eights of query heads per unit: all of a cache head's, as far as the accumulators and the query

@@ -425,7 +425,7 @@ def ep_handle_destroy(handle: Handle) -> None:
 
 from . import layer  # noqa: E402  (needs the names above)
 from .layer import (EP_ACT_NONE, EP_ACT_SWIGLU, EP_SCORE_SIGMOID, EP_SCORE_SOFTMAX, ep_expert_w4,  # noqa: E402,F401
-                    ep_kv_append, ep_paged_attention, ep_paged_attention_workspace, ep_router_topk,
+                    ep_expert_w4_workspace, ep_kv_append, ep_paged_attention, ep_paged_attention_workspace, ep_router_topk,
                     ep_router_topk_backward)
 
 EXPORTS = EXPORTS + layer.EXPORTS

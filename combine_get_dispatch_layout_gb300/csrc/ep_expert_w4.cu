@@ -1,26 +1,38 @@
 // The experts' products on dispatched rows: 4-bit weights, group scales.
 //
 // Mathematics. y[n, o] = sum over groups g of s[g, o] * sum over i in g of
-// (code[o, i] - zero[g, o]) x[n, i]. code - zero is a whole number of at most
-// five bits, exact in bf16 and fp16, so the inner sums run through the matrix
-// instructions with exact products and fp32 sums, and the scale multiplies a
-// group's sum in fp32: no weight is rounded.
+// (code[o, i] - zero[g, o]) x[n, i]. The inner sums run through the 5th-generation
+// tensor cores on e4m3 operands with fp32 sums:
+//  - a code 0 .. 15 in a byte IS the e4m3 number code * 2^-9 (subnormal up to 7,
+//    the first binade from 8 on), so unpacking eight codes is two masks and one
+//    shift. (As bf16 operands of mma.sync they take 11 instructions, and that
+//    kernel ran at 37 % of the memory rate, bound by instruction issue; e4m3
+//    operands of mma.sync are converted to fp16 by further instructions.)
+//  - x is taken as a sum of e4m3 numbers, two for bf16 and three for fp16, after
+//    a power of two has brought the largest input of the group to [128, 256).
+//    Four significant bits each make up the 8 or 11 of x, exactly, down to
+//    e4m3's smallest step: what is left off is below 2^-17 of the group's
+//    largest. The parts of a row are columns of the product's narrow side, which
+//    has to be 16 wide in any case.
+//  - the zero point enters as zero * (sum of the group's inputs), in fp32.
+// Scales multiply a group's sum in fp32. y is rounded once.
 //
 // What bounds it: with few rows per expert each weight is used a few times, so
-// reading the codes (half a byte each) once is the floor. Next to that come the
-// integer instructions that unpack them (seven a word of eight codes, 2 clocks
-// each a warp and SM quarter: 14 of the 22 clocks that DRAM takes for 128
-// bytes a quarter), so the unpacking is kept to a mask, a shift and one
-// subtraction per pair, and every unpacked fragment serves all rows at once.
+// reading the codes (half a byte each) once is the floor. Instruction issue is
+// next: about 6 instructions a word of 8 codes of the 22 clocks that DRAM takes
+// for 128 bytes an SM quarter.
 //
-// Layout. Weight rows are the instruction's 16 rows, dispatched rows its 8
-// columns. The order of a product's inputs is free: a thread takes 8
-// neighbouring codes of a weight row and the same 8 inputs of x, in the order
-// in which masks leave the codes ((0, 4), (1, 5), (2, 6), (3, 7)), so the codes
-// are used in the plain layout in which they are stored. A persistent CTA
-// walks its items (an expert, a tile of weight rows, at most 8 NT rows of x)
-// through one ring of asynchronous copies that runs on across items; its warps
-// split tile rows and inputs, 64 inputs each a stage, and join at an item's end.
+// Layout. A tile of 128 weight rows is the product's 128 lanes: thread = weight
+// row = TMEM lane, for unpacking (shared memory to TMEM operand A), for the
+// scales (one a thread) and for the sums (tcgen05.ld, one column a row of x). A
+// persistent CTA walks its items (an expert, a tile, at most NR rows of x); one
+// warp fills a ring of stages (256 inputs: 16 KB of codes by TMA) that runs on
+// across items, two warpgroups take half a stage each. The first weights are
+// on their way while split_kernel still runs. Where there are few items, the
+// CTAs of a cluster share an item's inputs and join through distributed shared
+// memory.
+#include <cuda.h>
+
 #include <type_traits>
 
 #include "ep_layer.cuh"
@@ -28,83 +40,137 @@
 namespace ep {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kStages = 4;
-constexpr int kSlice = 64;   // inputs of a warp per stage
+constexpr int kThreads = 288;          // two warpgroups and the warp that loads
+constexpr int kConsumers = 256;
+constexpr int kRows = 128;             // weight rows of a tile
+constexpr int kIn = 256;               // inputs of a stage, 128 a warpgroup
+constexpr int kWeightBytes = kRows * kIn / 2;
+constexpr int kSplitThreads = 256;
+constexpr int kMostSplit = 8;          // CTAs of a cluster that share an item
 
-// Tile shapes. Large: 128 weight rows, warps 2 (rows) x 4 (inputs), 256 inputs a stage: x is read once for
-// 128 rows. Small: 32 rows, 8 warps over 512 inputs: four times as many items where there are few.
-template <bool SMALL>
-struct Tile {
-    static constexpr int kMTiles = SMALL ? 2 : 4;          // 16-row tiles of a warp
-    static constexpr int kRowWarps = SMALL ? 1 : 2;
-    static constexpr int kInWarps = 8 / kRowWarps;
-    static constexpr int kRows = 16 * kMTiles * kRowWarps;
-    static constexpr int kIn = kSlice * kInWarps;          // inputs of a stage
-    static constexpr int kRowBytes = kIn / 2;
-    static constexpr int kPieces = kRowBytes / 16;         // 16-byte pieces of a weight row
-    static constexpr int kCopies = kRows * kPieces / kThreads;
-    static constexpr int kXPieces = kIn * 2 / 16;
-    static constexpr int kXRows = kThreads / kXPieces;     // rows of x that one pass of the threads copies
+// How x is split: parts, and places for them (the product's narrow side is a multiple of 16).
+template <typename T>
+struct Parts {
+    static constexpr int kCount = std::is_same_v<T, __half> ? 3 : 2;
+    static constexpr int kPlaces = std::is_same_v<T, __half> ? 4 : 2;
 };
 
-template <bool SMALL, int NT>
-struct Stage {
-    using L = Tile<SMALL>;
-    static constexpr int kWeights = L::kRows * L::kRowBytes;
-    static constexpr int kX = 8 * NT * L::kIn * 2;
-    // scale (16 bits) and zero point (as the unpacked pairs hold it) of each row and group
-    static constexpr int kScales = L::kRows * (L::kIn / 32) * 4;
-    // the weights of a used-up stage also hold a quarter of the partial sums at an item's end
-    static_assert((L::kInWarps + 3) / 4 * 8 * NT * L::kRows * 4 <= kWeights, "");
+constexpr int power_of_two(int n) { return n <= 32 ? 32 : 2 * power_of_two((n + 1) / 2); }
+
+// T: type of x, scales and y. NR: rows of x of an item. GROUP: inputs that share a scale.
+template <typename T, int NR, int GROUP>
+struct Shape {
+    static constexpr int kN = NR * Parts<T>::kPlaces;          // columns of the product
+    static constexpr int kGroups = 128 / GROUP;                // of a warpgroup's half of a stage
+    static constexpr int kXBytes = kN * 128;                   // x of half a stage
+    static constexpr int kStats = 2 * kGroups * NR;            // float2s of a stage
+    static constexpr int kSumCols = kN * kGroups;
+    // columns of TMEM: operand A twice for both warpgroups, sums twice too where that leaves room for two CTAs a core
+    static constexpr int kSumBuffers = 128 + 4 * kSumCols <= 256 ? 2 : 1;
+    static constexpr int kTmem = power_of_two(128 + 2 * kSumBuffers * kSumCols);
+    static constexpr int kStageBytes = kWeightBytes + 2 * kXBytes + kStats * 8;
+    // two CTAs a core where TMEM (512 columns) allows it
+    static constexpr int kResident = kTmem <= 256 ? 2 : 1;
+    static constexpr int kFixed = NR * kRows * 4 + 2048;       // join buffer, barriers, alignment
+    static constexpr int kTable = 4 * (EP_MAX_EXPERTS + 1) + 1024;   // first_pass, at most (two CTAs have room for a quarter)
+    static constexpr int kFit = (227 * 1024 / kResident - 1024 - kFixed - kTable / (kResident * kResident)) / kStageBytes;
+    static constexpr int kStages = kFit > 8 ? 8 : kFit;
+    static_assert(kStages >= 2 && kN % 16 == 0 && kN <= 256 && kTmem <= 512, "");
 };
 
 struct Plan {
-    int tiles;      // of an expert
-    int slots;      // CTAs that the device holds at once (the grid)
-    int stages;     // of an item
-    int groups;     // of a weight row
-    int log_group;
+    int tiles;       // of an expert
+    int slots;       // CTAs of the grid
+    int split;       // CTAs that share an item
+    int stages;      // of an item
+    int groups;      // of a weight row
+    const float2* stats;   // [rows][groups]: power of two, 2^-9 * sum, of a group's inputs
 };
 
-template <typename T>
-__device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b) {
-    if constexpr (std::is_same_v<T, __half>) {
-        const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-        return *reinterpret_cast<const uint32_t*>(&r);
-    } else {
-        const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
-        return *reinterpret_cast<const uint32_t*>(&r);
-    }
-}
-
-// A code in the low mantissa bits under this exponent is 128 + code (bf16), 1024 + code (fp16).
-template <typename T>
-constexpr uint32_t kBias = std::is_same_v<T, __half> ? 0x6400u : 0x4300u;
-
-// Pair k of a word's codes, (k, k + 4), minus the zero point: exact.
-template <typename T>
-__device__ __forceinline__ uint32_t unpack(uint32_t word, int k, uint32_t zero) {
-    return minus<T>(((word >> (4 * k)) & 0x000f000fu) | (kBias<T> * 0x10001u), zero);
-}
-
-template <typename T>
-__device__ __forceinline__ void multiply(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if constexpr (std::is_same_v<T, __half>)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
+// ------------------------------------------------------------------ PTX
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-// 16 bytes to shared memory, of which the first `real` (16 or 0) are read and the rest are zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int real) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
+
+__device__ __forceinline__ void barrier_init(uint32_t bar, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
+__device__ __forceinline__ void barrier_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void barrier_expect(uint32_t bar, int bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+// Every wait ends: after far more tries than any load takes, `dead` is set, the CTA runs through the rest
+// without waiting, and its outputs are NaN.
+__device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+    for (int i = 0; i < (1 << 22); ++i) {
+        if (barrier_try(bar, parity)) return;
+        if ((i & 1023) == 1023 && *dead) return;
+    }
+    *dead = 1;
+}
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int real) {   // zeros where real is 0
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(128) : "memory"); }
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 3, %0;" ::"n"(kConsumers) : "memory"); }
+
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+        "r"(r[31])
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_load8(uint32_t at, float (&r)[8]) {
+    uint32_t u[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "r"(at)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(u[i]);
+}
+__device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// sums [128 lanes][N] (+)= A [128 lanes][32 inputs, TMEM] * B [32 inputs][N, shared memory]^T
+__device__ __forceinline__ void multiply(uint32_t sums, uint32_t a, uint64_t b, uint32_t shape, bool add) {
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p; }" ::"r"(sums),
+                 "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+                 : "memory");
+}
+__device__ __forceinline__ void multiply_done(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Rows of 128 bytes along the inputs, 128-byte swizzle: 8 rows are 1024 bytes.
+__device__ __forceinline__ uint64_t operand(uint32_t addr) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+
+// ------------------------------------------------------------------ rows and items
 
 // First row and number of real rows of expert e, within [0, rows).
 __device__ __forceinline__ int expert_rows(const W4Args& a, int e, int& first) {
@@ -122,34 +188,120 @@ struct Item {
     int expert, row, rows, col;   // col: first output column of the tile
 };
 
-// T: type of x, scales and y. NT: eights of x rows of an item. SLICES: a warp's 64 inputs of a stage are one slice of
-// a group (1), or two groups of 32 (2).
-template <typename T, bool SMALL, int NT, int SLICES>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) expert_w4_kernel(W4Args a, Plan p) {
-    using L = Tile<SMALL>;
-    using S = Stage<SMALL, NT>;
-    constexpr int kSpan = kSlice / SLICES;          // inputs that share a thread's scale
-    constexpr int kWords = kSpan / 32;              // words of codes a thread takes of them
-    constexpr int kItemRows = 8 * NT;
-    extern __shared__ __align__(128) unsigned char shared_bytes[];
-    unsigned char* const weights = shared_bytes;                               // [kStages][kWeights]
-    unsigned char* const inputs = weights + kStages * S::kWeights;             // [kStages][kX]
-    uint32_t* const scales = reinterpret_cast<uint32_t*>(inputs + kStages * S::kX);   // [kStages][groups of a stage][kRows]
-    int* const first_pass = reinterpret_cast<int*>(scales + kStages * (S::kScales / 4 / (SLICES == 2 ? 1 : 2)));  // [E + 1]
-    constexpr int kScaleWords = S::kScales / 4 / (SLICES == 2 ? 1 : 2);   // a group has 64 inputs at least with one slice
-    __shared__ int warp_sum[kThreads / 32];
+// Four values as e4m3 codes in a word, each reduced by what its code stands for.
+__device__ __forceinline__ uint32_t take_part(float (&v)[4]) {
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(v[i], v[i + 1]), __NV_SATFINITE, __NV_E4M3);
+        const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+        v[i] -= f.x;
+        v[i + 1] -= f.y;
+        word |= static_cast<uint32_t>(c) << (8 * i);
+    }
+    return word;
+}
+
+// x as sums of e4m3 numbers, a plane [rows][I] for each part; of 8 neighbouring inputs the even ones come first, as
+// masks leave the codes. A thread takes 8 inputs, GROUP / 8 threads share a power of two. An infinite or NaN
+// input makes its group's power of two or sum NaN, and so every product with it.
+template <typename T, int GROUP>
+__global__ void __launch_bounds__(kSplitThreads) split_kernel(W4Args a, unsigned char* to, float2* stats) {
     dependent_entry();
+    const int per_row = a.I / 8;
+    const int last = a.offsets ? min(max(a.offsets[a.E], 0), a.rows) : a.rows;   // rows behind belong to nobody
+    const int64_t all = static_cast<int64_t>(last) * per_row, plane = static_cast<int64_t>(a.rows) * a.I;
+    // (a group's threads are of one warp: per_row is a multiple of GROUP / 8)
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSplitThreads + threadIdx.x; i - threadIdx.x % 32 < all;
+         i += static_cast<int64_t>(gridDim.x) * kSplitThreads) {
+        const bool in = i < all;
+        const int64_t row = in ? i / per_row : 0;
+        const int c = in ? static_cast<int>(i - row * per_row) : 0;
+        Vec8<T> v;
+        v.raw = make_uint4(0, 0, 0, 0);
+        if (in) v.raw = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + row * a.x_ld + c * 8);
+        float big = 0.0f, even[4], odd[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            even[k] = to_float(v.v[2 * k]);
+            odd[k] = to_float(v.v[2 * k + 1]);
+            big = fmaxf(big, fmaxf(fabsf(even[k]), fabsf(odd[k])));
+        }
+#pragma unroll
+        for (int o = 1; o < GROUP / 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(kFullMask, big, o));
+        const bool finite = big < INFINITY;
+        const int e = big > 0.0f && finite ? min(7 - ilogbf(big), 126) : 0;
+        const float up = __int_as_float((e + 127) << 23);
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            even[k] *= up;
+            odd[k] *= up;
+            sum += even[k] + odd[k];
+        }
+#pragma unroll
+        for (int k = 0; k < Parts<T>::kCount; ++k) {
+            uint2 w;
+            w.x = take_part(even);
+            w.y = take_part(odd);
+            if (in) *reinterpret_cast<uint2*>(to + k * plane + i * 8) = w;
+        }
+        // the sum of what the parts stand for: the inputs' less what is left of them
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum -= even[k] + odd[k];
+#pragma unroll
+        for (int o = 1; o < GROUP / 8; o <<= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
+        if (in && c % (GROUP / 8) == 0)
+            stats[row * (a.I / GROUP) + c / (GROUP / 8)] =
+                make_float2(finite ? __int_as_float((127 - e) << 23) : __int_as_float(0x7fffffff), sum * 0.001953125f);
+    }
+}
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int row_warp = warp % L::kRowWarps, in_warp = warp / L::kRowWarps;
-    const int cols = a.swiglu ? a.O / 2 : a.O, tile_cols = a.swiglu ? L::kRows / 2 : L::kRows;
+template <typename T, int NR, int GROUP>
+__global__ void __launch_bounds__(kThreads, (Shape<T, NR, GROUP>::kResident))
+    expert_w4_kernel(W4Args a, Plan p, const __grid_constant__ CUtensorMap weight_map, const __grid_constant__ CUtensorMap x_map) {
+    using S = Shape<T, NR, GROUP>;
+    constexpr int kStages = S::kStages, kGroups = S::kGroups;
+    extern __shared__ unsigned char shared_bytes[];
+    // [kStages] weights (rows of 128 bytes, 128-byte swizzle), [kStages] x (two halves [kN][128 bytes]), then stats, the
+    // join buffer [NR][kRows], barriers, first_pass [E + 1]
+    unsigned char* const weights = shared_bytes + (1024 - smem_addr(shared_bytes) % 1024) % 1024;
+    unsigned char* const inputs = weights + kStages * kWeightBytes;
+    float2* const stats = reinterpret_cast<float2*>(inputs + kStages * 2 * S::kXBytes);   // [kStages][2][kGroups][NR]
+    float* const join = reinterpret_cast<float*>(stats + kStages * S::kStats);
+    uint64_t* const barriers = reinterpret_cast<uint64_t*>(join + NR * kRows);
+    const uint32_t full = smem_addr(barriers), empty = full + 8 * kStages, done = empty + 8 * kStages;   // done: [2][2]
+    uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(barriers + 2 * kStages + 4);
+    volatile int* const dead = reinterpret_cast<volatile int*>(tmem_at + 1);
+    int* const first_pass = reinterpret_cast<int*>(tmem_at + 2);
+    __shared__ int warp_sum[kThreads / 32];
+    // Everything before split_kernel, which this kernel follows, is complete once this one runs: split_kernel lets it
+    // start only after it has waited for that itself. So all but split_kernel's own outputs can be read at once, and
+    // griddepcontrol.wait comes before those (in the loading warp; the others see them through its barriers).
 
-    // ---- items: an expert's rows in passes of kItemRows, each pass over all tiles; a tile's passes follow each
-    // other, so the weights of the second come from L2
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cols = a.swiglu ? a.O / 2 : a.O, tile_cols = a.swiglu ? kRows / 2 : kRows;
+    const int rank = blockIdx.x % p.split;
+
+    if (warp == kConsumers / 32) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_at)), "n"(S::kTmem) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if (lane == 0) {
+            *dead = 0;
+            for (int i = 0; i < kStages; ++i) {
+                barrier_init(full + 8 * i, 33);                  // the TMA loads' thread and 32 lanes' copies
+                barrier_init(empty + 8 * i, kConsumers / 32);
+            }
+            for (int i = 0; i < 4; ++i) barrier_init(done + 8 * i, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+    }
+    // ---- items: an expert's rows in passes of NR, each pass over all tiles; a tile's passes follow each other, so
+    // the weights of the second come from L2
     {
         const int per = (a.E + kThreads - 1) / kThreads, lo = min(a.E, tid * per), hi = min(a.E, lo + per);
         int own = 0, first;
-        for (int e = lo; e < hi; ++e) own += (expert_rows(a, e, first) + kItemRows - 1) / kItemRows;
+        for (int e = lo; e < hi; ++e) own += (expert_rows(a, e, first) + NR - 1) / NR;
         int scan = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -164,20 +316,24 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) expert_w4_kernel(W4
             if (w < warp) base += warp_sum[w];
         for (int e = lo; e < hi; ++e) {
             first_pass[e] = base;
-            base += (expert_rows(a, e, first) + kItemRows - 1) / kItemRows;
+            base += (expert_rows(a, e, first) + NR - 1) / NR;
         }
         if (hi == a.E && lo < hi) first_pass[a.E] = base;
+        tmem_fence_before();
         __syncthreads();
+        tmem_fence_after();
     }
+    const uint32_t tmem = *tmem_at;
     const int64_t items = static_cast<int64_t>(first_pass[a.E]) * p.tiles;
-    // as many CTAs as share the items evenly: all of them wait on the same DRAM, so an SM with one CTA less costs nothing
-    const int64_t each = (items + p.slots - 1) / p.slots;
-    const int64_t item0 = each * blockIdx.x, item1 = min(items, item0 + each);
-    if (item0 >= item1) return;
-    const int64_t steps = (item1 - item0) * p.stages;
+    // as many clusters as share the items evenly: all of them wait on the same DRAM, so an SM with one CTA less costs nothing
+    const int clusters = p.slots / p.split;
+    const int64_t each = (items + clusters - 1) / clusters;
+    const int64_t item0 = min(items, each * (blockIdx.x / p.split)), item1 = min(items, item0 + each);
+    // this CTA's stages of every item
+    const int stage0 = p.stages * rank / p.split, stage1 = p.stages * (rank + 1) / p.split;
 
     const auto decode = [&](int64_t it) {
-        int lo = 0, hi = a.E - 1;   // the last expert whose first item is not behind `it`, with passes of its own
+        int lo = 0, hi = a.E - 1;   // the last expert whose first item is not behind `it`: it has passes of its own
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
             if (static_cast<int64_t>(first_pass[mid]) * p.tiles <= it) lo = mid;
@@ -189,319 +345,371 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) expert_w4_kernel(W4
         int first;
         const int n = expert_rows(a, lo, first), pass = in % passes;
         r.expert = lo;
-        r.row = first + pass * kItemRows;
-        r.rows = min(kItemRows, n - pass * kItemRows);
+        r.row = first + pass * NR;
+        r.rows = min(NR, n - pass * NR);
         r.col = in / passes * tile_cols;
         return r;
     };
-    // weight row of the tile's row r, or -1 past the end: with an activation the tile's halves are gate and up rows
-    const auto weight_row = [&](int col, int r) {
-        if (!a.swiglu) return col + r < a.O ? col + r : -1;
-        const int j = col + (r < L::kRows / 2 ? r : r - L::kRows / 2);
-        return j >= cols ? -1 : r < L::kRows / 2 ? j : cols + j;
-    };
 
-    // ---- the copies of a stage. Thread's pieces of the weights: rows tid / kPieces + k * kThreads / kPieces, of x
-    // likewise. Pieces of a row are exchanged so that fragment loads meet no bank twice: of the weights by
-    // ((row & 3) << 1 | row >> 2 & 1) (a load takes 4 rows x 32 bytes or 8 x 16), of x by 5 for odd rows.
-    int64_t load_item = item0;
-    int load_stage = 0, load_slot = 0;
-    const unsigned char* weight_at[L::kCopies];
-    bool weight_real[L::kCopies];
-    const unsigned char* x_at = nullptr;
-    Item li{};
-    const int piece = tid % L::kPieces, piece_row = tid / L::kPieces;
-    const int x_piece = tid % L::kXPieces, x_row = tid / L::kXPieces;
-    constexpr int kXCopies = kItemRows / L::kXRows;
-    // scales of a stage: entries tid + k * kThreads of [groups][rows], held in registers while they load
-    const int stage_groups = L::kIn >> p.log_group;   // 2 .. 16
-    constexpr int kScaleLoads = (kScaleWords + kThreads - 1) / kThreads;
-    uint16_t scale_in[kScaleLoads];
-    uint8_t zero_in[kScaleLoads];
-    int scale_row[kScaleLoads];
-    const uint16_t* scale_at = nullptr;
-    const uint8_t* zero_at = nullptr;
-
-    const auto load = [&](int64_t step) {   // issues the copies and the scale loads of the next stage
-        if (step >= steps) return;
-        if (load_stage == 0) {
-            li = decode(load_item);
-#pragma unroll
-            for (int k = 0; k < L::kCopies; ++k) {
-                const int o = weight_row(li.col, piece_row + k * (kThreads / L::kPieces));
-                weight_real[k] = o >= 0;
-                weight_at[k] = a.w + (static_cast<int64_t>(li.expert) * a.O + max(o, 0)) * (a.I / 2) + piece * 16;
+    if (warp == kConsumers / 32) {
+        // ---- the loading warp
+        const auto load_weights = [&](const Item& it, int stage, int slot) {
+            if (lane != 0) return;
+            const uint32_t bar = full + 8 * slot, to = smem_addr(weights) + slot * kWeightBytes;
+            barrier_expect(bar, kWeightBytes + 2 * NR * Parts<T>::kCount * 128);
+            load_tile(to, &weight_map, stage * (kIn / 2), it.col, it.expert, bar);
+            if (a.swiglu) load_tile(to + kWeightBytes / 2, &weight_map, stage * (kIn / 2), cols + it.col, it.expert, bar);
+        };
+        const auto load_inputs = [&](const Item& it, int stage, int slot) {
+            const uint32_t bar = full + 8 * slot;
+            if (lane == 0)
+                for (int h = 0; h < 2; ++h)
+                    load_tile(smem_addr(inputs) + (slot * 2 + h) * S::kXBytes, &x_map, stage * kIn + h * 128, it.row, 0, bar);
+            for (int i = lane; i < S::kStats; i += 32) {
+                const int n = i % NR, grp = stage * (kIn / GROUP) + i / NR;
+                const bool in = n < it.rows && grp < p.groups;
+                copy8(smem_addr(stats + slot * S::kStats + i), p.stats + (in ? static_cast<int64_t>(it.row + n) * p.groups + grp : 0), in ? 8 : 0);
             }
-            x_at = static_cast<const unsigned char*>(a.x) + (static_cast<int64_t>(li.row + x_row) * a.x_ld + x_piece * 8) * 2;
-#pragma unroll
-            for (int k = 0; k < kScaleLoads; ++k) scale_row[k] = weight_row(li.col, (tid + k * kThreads) % L::kRows);
-            const int64_t at = static_cast<int64_t>(li.expert) * p.groups * a.O;
-            scale_at = static_cast<const uint16_t*>(a.scales) + at;
-            zero_at = a.zeros ? a.zeros + at : nullptr;
+            copies_arrive(bar);
+        };
+        const int64_t steps = (item1 - item0) * (stage1 - stage0);
+        const int first_steps = static_cast<int>(min(steps, static_cast<int64_t>(kStages)));
+        int64_t item = item0;
+        int stage = stage0;
+        Item it{};
+        const auto next = [&]() {
+            if (++stage == stage1) stage = stage0, ++item;
+        };
+        for (int i = 0; i < first_steps; ++i, next()) {
+            if (i == 0 || stage == stage0) it = decode(item);
+            load_weights(it, stage, i);
         }
-        const uint32_t to = smem_addr(weights + load_slot * S::kWeights);
-        const bool piece_in = load_stage * L::kRowBytes + piece * 16 < a.I / 2;
-#pragma unroll
-        for (int k = 0; k < L::kCopies; ++k) {
-            const int r = piece_row + k * (kThreads / L::kPieces);
-            copy16(to + r * L::kRowBytes + ((piece ^ ((r & 3) << 1 | ((r >> 2) & 1))) << 4),
-                   piece_in ? weight_at[k] + load_stage * L::kRowBytes : a.w, piece_in && weight_real[k] ? 16 : 0);
-        }
-        const uint32_t xto = smem_addr(inputs + load_slot * S::kX);
-        const bool x_in = load_stage * L::kIn + x_piece * 8 < a.I;
-#pragma unroll
-        for (int k = 0; k < kXCopies; ++k) {
-            const int r = x_row + k * L::kXRows;
-            if (r < li.rows)   // (rows that are not there leave garbage in columns that are not written)
-                copy16(xto + r * (L::kIn * 2) + ((x_piece ^ ((r & 1) * 5)) << 4),
-                       x_in ? x_at + (static_cast<int64_t>(k) * L::kXRows * a.x_ld + load_stage * L::kIn) * 2 : a.x, x_in ? 16 : 0);
-        }
-#pragma unroll
-        for (int k = 0; k < kScaleLoads; ++k) {
-            const int i = tid + k * kThreads, grp = load_stage * stage_groups + i / L::kRows;
-            scale_in[k] = 0;
-            zero_in[k] = 8;
-            if (i < stage_groups * L::kRows && grp < p.groups && scale_row[k] >= 0) {
-                const int64_t at = static_cast<int64_t>(grp) * a.O + scale_row[k];
-                scale_in[k] = scale_at[at];
-                if (zero_at) zero_in[k] = zero_at[at];
+        dependent_entry();
+        item = item0, stage = stage0;
+        for (int64_t i = 0; i < steps; ++i, next()) {
+            const int slot = static_cast<int>(i % kStages);
+            if (i == 0 || stage == stage0) it = decode(item);
+            if (i >= kStages) {
+                barrier_wait(empty + 8 * slot, (i / kStages + 1) & 1, dead);
+                load_weights(it, stage, slot);
             }
+            load_inputs(it, stage, slot);
         }
-    };
-    const auto loaded = [&](int64_t step) {   // the scales to their slot, once here
-        if (step < steps) {
-            uint32_t* to = scales + load_slot * kScaleWords;
-#pragma unroll
-            for (int k = 0; k < kScaleLoads; ++k) {
-                const int i = tid + k * kThreads;
-                if (i < stage_groups * L::kRows) to[i] = scale_in[k] | (kBias<T> + zero_in[k]) << 16;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (p.split > 1)   // two cluster barriers an item, as the warpgroups have
+            for (int64_t i = item0; i < item1; ++i) {
+                asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+                asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
             }
-            if (++load_stage == p.stages) load_stage = 0, ++load_item;
-        }
-        load_slot = (load_slot + 1) % kStages;
-    };
-
-#pragma unroll 1
-    for (int i = 0; i < kStages - 1; ++i) {
-        load(i);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        loaded(i);
-    }
-
-    float acc[L::kMTiles][NT][4];
-    Item ci{};
-    int64_t item = item0;
-    int stage = 0, slot = 0, eights = 0;
-    for (int64_t step = 0; step < steps; ++step) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-        __syncthreads();
-        load(step + kStages - 1);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (stage == 0) {
-            ci = decode(item);
-            eights = (ci.rows + 7) / 8;
-#pragma unroll
-            for (int m = 0; m < L::kMTiles; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.0f;
-        }
-        const unsigned char* ws = weights + slot * S::kWeights;
-        const unsigned char* xs = inputs + slot * S::kX;
-        const uint32_t* ss = scales + slot * kScaleWords;
-#pragma unroll
-        for (int sub = 0; sub < SLICES; ++sub) {
-            const int in0 = in_warp * kSlice + sub * kSpan;   // inputs [in0, in0 + kSpan) of the stage
-            // x: 8 kWords neighbouring inputs of row 8 n + g, in the order of the unpacked codes
-            uint32_t xf[NT][kWords][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (n > 0 && n >= eights) break;
-#pragma unroll
-                for (int w = 0; w < kWords; ++w) {
-                    const int r = 8 * n + g, pc = in0 / 8 + t * kWords + w;
-                    const uint4 v = *reinterpret_cast<const uint4*>(xs + r * (L::kIn * 2) + ((pc ^ ((r & 1) * 5)) << 4));
-                    xf[n][w][0] = __byte_perm(v.x, v.z, 0x5410);   // (0, 4)
-                    xf[n][w][1] = __byte_perm(v.x, v.z, 0x7632);   // (1, 5)
-                    xf[n][w][2] = __byte_perm(v.y, v.w, 0x5410);   // (2, 6)
-                    xf[n][w][3] = __byte_perm(v.y, v.w, 0x7632);   // (3, 7)
-                }
+    } else {
+        // ---- a warpgroup: unpack half a stage, multiply, and take in the sums of the half before
+        const int wg = warp >> 2, row = tid & 127;      // row: of the tile; its TMEM lane
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // lane 32 * (warp % 4) in an address's upper half
+        const uint32_t operand_at = tmem + wg * 64, sums_at = tmem + 128 + wg * S::kSumBuffers * S::kSumCols;
+        constexpr uint32_t kShape = (1u << 4) | (static_cast<uint32_t>(S::kN / 8) << 17) | (static_cast<uint32_t>(kRows / 16) << 24);
+        int slot = 0, buffer = 0;
+        uint32_t full_parity = 0, done_parity = 0;   // of done: a bit a buffer
+        for (int64_t item = item0; item < item1; ++item) {
+            const Item it = decode(item);
+            int o;   // this thread's weight row; with an activation the tile's halves are gate and up rows
+            if (a.swiglu) {
+                const int j = it.col + (row & 63);
+                o = j >= cols ? -1 : row < 64 ? j : cols + j;
+            } else {
+                o = it.col + row < cols ? it.col + row : -1;
             }
-            const uint32_t* sg = ss + (in0 >> p.log_group) * L::kRows;
+            const int64_t scale_base = static_cast<int64_t>(it.expert) * p.groups * a.O + max(o, 0);
+            T scale[kGroups], scale_next[kGroups];
+            uint8_t zero[kGroups], zero_next[kGroups];
+            const auto load_scales = [&](int stage) {
 #pragma unroll
-            for (int m = 0; m < L::kMTiles; ++m) {
-                const int r0 = (row_warp * L::kMTiles + m) * 16 + g;
-                uint32_t word[2][kWords];
-                uint32_t zero[2];
-                float scale[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = r0 + 8 * h;
-                    const int byte = in0 / 2 + t * 4 * kWords;
-                    const unsigned char* from = ws + r * L::kRowBytes + (((byte >> 4) ^ ((r & 3) << 1 | ((r >> 2) & 1))) << 4) + (byte & 15);
-                    if constexpr (kWords == 2) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(from);
-                        word[h][0] = v.x, word[h][1] = v.y;
-                    } else {
-                        word[h][0] = *reinterpret_cast<const uint32_t*>(from);
+                for (int i = 0; i < kGroups; ++i) {
+                    const int grp = (stage * kIn + wg * 128) / GROUP + i;
+                    scale_next[i] = from_float<T>(0.0f);
+                    zero_next[i] = 8;
+                    if (o >= 0 && grp < p.groups) {
+                        scale_next[i] = static_cast<const T*>(a.scales)[scale_base + static_cast<int64_t>(grp) * a.O];
+                        if (a.zeros) zero_next[i] = a.zeros[scale_base + static_cast<int64_t>(grp) * a.O];
                     }
-                    const uint32_t sz = sg[r];
-                    zero[h] = __byte_perm(sz, sz, 0x3232);
-                    if constexpr (std::is_same_v<T, __half>) scale[h] = __half2float(__ushort_as_half(static_cast<unsigned short>(sz)));
-                    else scale[h] = __uint_as_float(sz << 16);
                 }
-                float sum[NT][4];
+            };
+            float acc[NR];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) sum[n][0] = sum[n][1] = sum[n][2] = sum[n][3] = 0.0f;
+            for (int n = 0; n < NR; ++n) acc[n] = 0.0f;
+            // takes in the sums of the half stage that was multiplied into buffer b, its slot s
+            const auto sums_of = [&](int b) { return S::kSumBuffers == 2 ? sums_at + b * S::kSumCols : sums_at; };
+            const auto take_sums = [&](int b, int s) {
+                barrier_wait(done + 8 * (wg * 2 + b), (done_parity >> b) & 1, dead);
+                done_parity ^= 1u << b;
+                tmem_fence_after();
 #pragma unroll
-                for (int w = 0; w < kWords; ++w)
+                for (int i = 0; i < kGroups; ++i) {
+                    const float sc = to_float(scale[i]), z = static_cast<float>(zero[i]);
+                    const float2* st = stats + s * S::kStats + (wg * kGroups + i) * NR;
 #pragma unroll
-                    for (int k = 0; k < 4; k += 2) {
-                        const uint32_t af[4] = {unpack<T>(word[0][w], k, zero[0]), unpack<T>(word[1][w], k, zero[1]),
-                                                unpack<T>(word[0][w], k + 1, zero[0]), unpack<T>(word[1][w], k + 1, zero[1])};
+                    for (int n0 = 0; n0 < NR; n0 += 8) {
+                        float v[Parts<T>::kCount][8];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            if (n > 0 && n >= eights) break;
-                            multiply<T>(sum[n], af, xf[n][w][k], xf[n][w][k + 1]);
+                        for (int k = 0; k < Parts<T>::kCount; ++k)
+                            tmem_load8(sums_of(b) + lanes + i * S::kN + k * NR + n0, v[k]);
+                        tmem_load_wait();
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) {
+                            float sum = v[0][n] + v[1][n];
+                            if constexpr (Parts<T>::kCount == 3) sum += v[2][n];
+                            const float2 f = st[n0 + n];
+                            acc[n0 + n] += (sc * f.x) * (sum - z * f.y);
                         }
                     }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    acc[m][n][0] += scale[0] * sum[n][0];
-                    acc[m][n][1] += scale[0] * sum[n][1];
-                    acc[m][n][2] += scale[1] * sum[n][2];
-                    acc[m][n][3] += scale[1] * sum[n][3];
                 }
-            }
-        }
-        if (++stage == p.stages) {
-            // ---- the item's end: the warps' partial sums join by halves, through the weights of the stage just
-            // used up, in a fixed order; sums[x row][weight row], weight rows exchanged by 8 t to keep off one bank
-            stage = 0;
-            ++item;
-            constexpr int kStride = L::kRows;
-            float* sums = reinterpret_cast<float*>(weights + slot * S::kWeights);
-            const auto place = [&](int m, int n, int j) {
-                return (8 * n + 2 * t + (j & 1)) * kStride + (((row_warp * L::kMTiles + m) * 16 + g + 8 * (j >> 1)) ^ (t << 3));
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) barrier_arrive(empty + 8 * s);
             };
-            __syncthreads();
+            load_scales(stage0);
+            int before = -1;
+            for (int stage = stage0; stage < stage1; ++stage) {
+                barrier_wait(full + 8 * slot, full_parity, dead);
+                const unsigned char* w = weights + slot * kWeightBytes + row * 128;
+                uint32_t codes[32];
 #pragma unroll
-            for (int half = L::kInWarps / 2; half >= 1; half /= 2) {
-                for (int turn = 0; turn < (half > 1 ? 2 : 1); ++turn) {
-                    // at most kInWarps / 4 partial sums at a time fit the area
-                    const int part = half > 1 ? half / 2 : 1;
-                    const int from = half + turn * part;
-                    if (in_warp >= from && in_warp < from + part) {
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(w + (((4 * wg + j) ^ (row & 7)) << 4));
+                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int m = 0; m < L::kMTiles; ++m)
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) sums[(in_warp - from) * kItemRows * kStride + place(m, n, j)] = acc[m][n][j];
+                    for (int k = 0; k < 4; ++k) {
+                        codes[8 * j + 2 * k] = u[k] & 0x0f0f0f0fu;
+                        codes[8 * j + 2 * k + 1] = (u[k] >> 4) & 0x0f0f0f0fu;
                     }
-                    __syncthreads();
-                    const int to = from - half;
-                    if (in_warp >= to && in_warp < to + part) {
+                }
+                // (the products that read this operand buffer last have been waited for in take_sums)
+                tmem_store32(operand_at + lanes + buffer * 32, codes);
+                if (S::kSumBuffers == 1 && before >= 0) take_sums(buffer ^ 1, before);
+                tmem_fence_before();
+                group_sync(1 + wg);
+                if ((tid & 127) == 0) {
+                    tmem_fence_after();
+                    const uint64_t b = operand(smem_addr(inputs) + (slot * 2 + wg) * S::kXBytes);
 #pragma unroll
-                        for (int m = 0; m < L::kMTiles; ++m)
+                    for (int i = 0; i < kGroups; ++i)
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
+                        for (int k = 0; k < GROUP / 32; ++k) {
+                            const int step = i * (GROUP / 32) + k;
+                            multiply(sums_of(buffer) + i * S::kN, operand_at + buffer * 32 + step * 8, b + step * 2, kShape, k > 0);
+                        }
+                    multiply_done(done + 8 * (wg * 2 + buffer));
+                }
+                if (S::kSumBuffers == 2 && before >= 0) take_sums(buffer ^ 1, before);
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) acc[m][n][j] += sums[(in_warp - to) * kItemRows * kStride + place(m, n, j)];
-                    }
-                    __syncthreads();
+                for (int i = 0; i < kGroups; ++i) scale[i] = scale_next[i], zero[i] = zero_next[i];
+                if (stage + 1 < stage1) load_scales(stage + 1);
+                before = slot;
+                buffer ^= 1;
+                if (++slot == kStages) slot = 0, full_parity ^= 1;
+            }
+            if (before >= 0) take_sums(buffer ^ 1, before);
+
+            // ---- the item's end: the warpgroups join, then the cluster's CTAs, in their order; codes count as code * 2^-9
+            if (wg == 1) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n) join[n * kRows + row] = acc[n];
+            }
+            consumers_sync();
+            if (wg == 0) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n) acc[n] = 512.0f * (acc[n] + join[n * kRows + row]);
+                if (*dead) {
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) acc[n] = __int_as_float(0x7fffffff);
                 }
             }
-            if (in_warp == 0) {
+            if (p.split > 1) {
+                if (wg == 0) {   // (its own entries of the join buffer: no one else reads them before the cluster's barrier)
 #pragma unroll
-                for (int m = 0; m < L::kMTiles; ++m)
+                    for (int n = 0; n < NR; ++n) join[n * kRows + row] = acc[n];
+                }
+                asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+                if (wg == 0 && rank == 0) {
+                    for (int r = 1; r < p.split; ++r) {
+                        uint32_t from;
+                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(smem_addr(join)), "r"(r));
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) sums[place(m, n, j)] = acc[m][n][j];
+                        for (int n = 0; n < NR; ++n) {
+                            float v;
+                            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(from + (n * kRows + row) * 4) : "memory");
+                            acc[n] += v;
+                        }
+                    }
+                }
+                asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
             }
-            __syncthreads();
-            T* y = static_cast<T*>(a.y) + static_cast<int64_t>(ci.row) * a.y_ld + ci.col;
-            const int wide = min(tile_cols, cols - ci.col);
-            for (int i = tid; i < ci.rows * tile_cols; i += kThreads) {
-                const int n = i / tile_cols, c = i % tile_cols;
-                if (c >= wide) continue;
-                const int x = ((n >> 1) & 3) << 3;
-                float v = sums[n * kStride + (c ^ x)];
-                if (a.swiglu) v = v / (1.0f + expf(-v)) * sums[n * kStride + ((L::kRows / 2 + c) ^ x)];
-                y[n * a.y_ld + c] = from_float<T>(v);
+            if (rank == 0) {
+                T* y = static_cast<T*>(a.y) + static_cast<int64_t>(it.row) * a.y_ld + it.col;
+                if (a.swiglu) {
+                    if (wg == 0 && row >= 64) {
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) join[n * kRows + row] = acc[n];
+                    }
+                    if (wg == 0) {
+                        group_sync(1);
+                        if (row < 64 && o >= 0) {
+#pragma unroll
+                            for (int n = 0; n < NR; ++n)
+                                if (n < it.rows)
+                                    y[n * a.y_ld + row] =
+                                        from_float<T>(acc[n] / (1.0f + expf(-acc[n])) * join[n * kRows + 64 + row]);
+                        }
+                    }
+                } else if (wg == 0 && o >= 0) {
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+                        if (n < it.rows) y[n * a.y_ld + row] = from_float<T>(acc[n]);
+                }
             }
-            // (the area is written again only behind the next step's barrier)
+            consumers_sync();   // the join buffer is free again
         }
-        slot = (slot + 1) % kStages;
-        loaded(step + kStages - 1);
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    if (warp == kConsumers / 32) {
+        tmem_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmem) : "memory");
+    }
 }
 
-// Resident CTAs per device of one kernel, with its shared memory limit raised: fixed for a size of shared
-// memory, looked up when a larger one than before comes (a race writes the same values).
+// ------------------------------------------------------------------ host
+
+// cuTensorMapEncodeTiled, through the runtime (the library does not link the driver's).
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encoder() {
+    static EncodeFn known = nullptr;   // a race writes the same value
+    EncodeFn fn = __atomic_load_n(&known, __ATOMIC_RELAXED);
+    if (fn) return fn;
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+        return nullptr;
+    fn = reinterpret_cast<EncodeFn>(p);
+    __atomic_store_n(&known, fn, __ATOMIC_RELAXED);
+    return fn;
+}
+
+// Bytes [z][y][x], read in boxes of 128 x box_y x box_z; zeros past the ends.
+cudaError_t byte_map(CUtensorMap* map, const void* base, int64_t x, int64_t y, int64_t z, int box_y, int box_z) {
+    const EncodeFn encode = encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(x), static_cast<cuuint64_t>(y), static_cast<cuuint64_t>(z)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(x), static_cast<cuuint64_t>(x * y)};
+    const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_y), static_cast<cuuint32_t>(box_z)}, step[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+// SMs of the current device, with the kernel's shared memory limit raised for at least this size: looked up when a
+// larger size than before comes (a race writes the same values).
 template <typename Kernel>
-cudaError_t prepare_kernel(Kernel kernel, int smem, int* known_smem, int* known_ctas, int* ctas) {
+cudaError_t prepare_kernel(Kernel kernel, int smem, int* known_smem, int* known_sms, int* sms) {
     constexpr int kDevices = 64;
-    int dev = 0, sms = 0, per_sm = 0;
+    int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (dev < kDevices && __atomic_load_n(&known_smem[dev], __ATOMIC_ACQUIRE) >= smem) {
-        *ctas = __atomic_load_n(&known_ctas[dev], __ATOMIC_RELAXED);
+        *sms = __atomic_load_n(&known_sms[dev], __ATOMIC_RELAXED);
         return cudaSuccess;
     }
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (err == cudaSuccess) err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
-    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
     if (err != cudaSuccess) return err;
-    if (per_sm < 1) return cudaErrorInvalidConfiguration;
-    *ctas = per_sm * sms;
     if (dev < kDevices) {
-        __atomic_store_n(&known_ctas[dev], *ctas, __ATOMIC_RELAXED);
+        __atomic_store_n(&known_sms[dev], *sms, __ATOMIC_RELAXED);
         __atomic_store_n(&known_smem[dev], smem, __ATOMIC_RELEASE);
     }
     return cudaSuccess;
 }
 
-template <typename T, bool SMALL, int NT, int SLICES>
-cudaError_t launch_shape(const W4Args& a, cudaStream_t stream) {
-    using L = Tile<SMALL>;
-    using S = Stage<SMALL, NT>;
-    static int known_smem[64], known_ctas[64];
-    const int smem = kStages * (S::kWeights + S::kX + S::kScales / (SLICES == 2 ? 1 : 2)) + (a.E + 1) * 4;
-    Plan p{};
-    cudaError_t err = prepare_kernel(expert_w4_kernel<T, SMALL, NT, SLICES>, smem, known_smem, known_ctas, &p.slots);
-    if (err != cudaSuccess) return err;
-    const int tile_cols = a.swiglu ? L::kRows / 2 : L::kRows, cols = a.swiglu ? a.O / 2 : a.O;
-    p.tiles = (cols + tile_cols - 1) / tile_cols;
-    p.stages = (a.I + L::kIn - 1) / L::kIn;
-    p.groups = a.I / a.group;
-    p.log_group = a.group == 32 ? 5 : a.group == 64 ? 6 : 7;
-    const int64_t most = (static_cast<int64_t>(a.rows) / (8 * NT) + (a.rows < a.E ? a.rows : a.E)) * p.tiles;   // items at most
-    const int grid = static_cast<int>(most < p.slots ? (most > 0 ? most : 1) : p.slots);
-    p.slots = grid;
-    return launch_dependent(expert_w4_kernel<T, SMALL, NT, SLICES>, dim3(grid), dim3(kThreads), smem, stream, a, p);
+int64_t plane_bytes(int64_t rows, int I) { return rows * I; }   // I is a multiple of 32
+int64_t split_bytes(int64_t rows, int I, int dtype) {
+    return plane_bytes(rows, I) * (dtype == EP_DTYPE_FP16 ? Parts<__half>::kCount : Parts<__nv_bfloat16>::kCount);
 }
 
-template <typename T, bool SMALL, int NT>
-cudaError_t launch_slices(const W4Args& a, cudaStream_t stream) {
-    return a.group == 32 ? launch_shape<T, SMALL, NT, 2>(a, stream) : launch_shape<T, SMALL, NT, 1>(a, stream);
+template <typename T, int NR, int GROUP>
+cudaError_t launch_shape(const W4Args& a, const unsigned char* x, const float2* stats, cudaStream_t stream) {
+    using S = Shape<T, NR, GROUP>;
+    static int known_smem[64], known_sms[64];
+    const int smem = S::kStages * S::kStageBytes + S::kFixed + (a.E + 1) * 4;
+    Plan p{};
+    int sms = 0;
+    cudaError_t err = prepare_kernel(expert_w4_kernel<T, NR, GROUP>, smem, known_smem, known_sms, &sms);
+    if (err != cudaSuccess) return err;
+    const int tile_cols = a.swiglu ? kRows / 2 : kRows, cols = a.swiglu ? a.O / 2 : a.O;
+    p.tiles = (cols + tile_cols - 1) / tile_cols;
+    p.stages = (a.I + kIn - 1) / kIn;
+    p.groups = a.I / GROUP;
+    p.stats = stats;
+    p.slots = sms * S::kResident;
+    // items at most; with fewer than half the CTAs' number, clusters share them
+    const int64_t most = (static_cast<int64_t>(a.rows) / NR + (a.rows < a.E ? a.rows : a.E)) * p.tiles;
+    p.split = 1;
+    while (p.split < kMostSplit && 2 * p.split <= p.stages && most * 2 * p.split <= p.slots) p.split *= 2;
+    const int64_t clusters = most < p.slots / p.split ? most : p.slots / p.split;
+    p.slots = static_cast<int>(clusters) * p.split;
+    CUtensorMap weight_map, x_map;
+    err = byte_map(&weight_map, a.w, a.I / 2, a.O, a.E, tile_cols, 1);
+    if (err == cudaSuccess) err = byte_map(&x_map, x, a.I, a.rows, Parts<T>::kCount, NR, Parts<T>::kCount);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.slots);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, expert_w4_kernel<T, NR, GROUP>, a, p, weight_map, x_map);
+}
+
+template <typename T, int GROUP>
+cudaError_t launch_group(const W4Args& a, void* workspace, int dtype, cudaStream_t stream) {
+    float2* stats = static_cast<float2*>(workspace);
+    const int64_t stats_bytes = (static_cast<int64_t>(a.rows) * (a.I / GROUP) * 8 + 15) / 16 * 16;
+    unsigned char* x = static_cast<unsigned char*>(workspace) + stats_bytes;
+    const int64_t blocks = (static_cast<int64_t>(a.rows) * (a.I / 8) + kSplitThreads - 1) / kSplitThreads;
+    const cudaError_t err = launch_dependent(split_kernel<T, GROUP>, dim3(static_cast<unsigned>(blocks < 8192 ? blocks : 8192)),
+                                             dim3(kSplitThreads), 0, stream, a, x, stats);
+    if (err != cudaSuccess) return err;
+    // rows of an item: 8, or 16 where experts have more than 8 rows on average
+    const int used = a.rows < a.E ? a.rows : a.E, mean = (a.rows + used - 1) / used;
+    if constexpr (!(std::is_same_v<T, __half> && GROUP == 32))   // (16 rows of three parts in groups of 32 outgrow TMEM)
+        if (mean > 4 && a.rows > 8) return launch_shape<T, 16, GROUP>(a, x, stats, stream);
+    return launch_shape<T, 8, GROUP>(a, x, stats, stream);
 }
 
 template <typename T>
-cudaError_t launch_type(const W4Args& a, cudaStream_t stream) {
-    // experts that may have rows, and the rows one of them has on average
-    const int used = a.rows < a.E ? a.rows : a.E, mean = (a.rows + used - 1) / used;
-    const bool small = static_cast<int64_t>(used) * ((a.O + 127) / 128) < 1024;
-    if (small) return mean <= 2 || a.rows <= 8 ? launch_slices<T, true, 1>(a, stream) : launch_slices<T, true, 2>(a, stream);
-    if (mean <= 2 || a.rows <= 8) return launch_slices<T, false, 1>(a, stream);
-    return mean <= 12 ? launch_slices<T, false, 2>(a, stream) : launch_slices<T, false, 4>(a, stream);
+cudaError_t launch_type(const W4Args& a, void* workspace, int dtype, cudaStream_t stream) {
+    return a.group == 32   ? launch_group<T, 32>(a, workspace, dtype, stream)
+           : a.group == 64 ? launch_group<T, 64>(a, workspace, dtype, stream)
+                           : launch_group<T, 128>(a, workspace, dtype, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_expert_w4(const W4Args& a, int dtype, cudaStream_t stream) {
-    return dtype == EP_DTYPE_BF16 ? launch_type<__nv_bfloat16>(a, stream) : launch_type<__half>(a, stream);
+int64_t expert_w4_workspace(int64_t rows, int I, int group, int dtype) {
+    return (rows * (I / group) * 8 + 15) / 16 * 16 + split_bytes(rows, I, dtype);
+}
+
+cudaError_t launch_expert_w4(const W4Args& a, void* workspace, int dtype, cudaStream_t stream) {
+    return dtype == EP_DTYPE_BF16 ? launch_type<__nv_bfloat16>(a, workspace, dtype, stream)
+                                  : launch_type<__half>(a, workspace, dtype, stream);
 }
 
 }  // namespace ep

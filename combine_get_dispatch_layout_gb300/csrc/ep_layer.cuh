@@ -107,6 +107,7 @@ struct W4Args {
     int64_t x_ld, y_ld;
     void* y;
 };
-cudaError_t launch_expert_w4(const W4Args& a, int dtype, cudaStream_t stream);
+cudaError_t launch_expert_w4(const W4Args& a, void* workspace, int dtype, cudaStream_t stream);
+int64_t expert_w4_workspace(int64_t rows, int I, int group, int dtype);
 
 }  // namespace ep

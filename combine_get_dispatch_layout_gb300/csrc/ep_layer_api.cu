@@ -236,9 +236,17 @@ ep_status_t ep_paged_attention(const void* q, const void* k_cache, const void* v
     return status_of(ep::launch_paged_attention(a, config->dtype, cache->dtype, static_cast<cudaStream_t>(stream)));
 }
 
+int64_t ep_expert_w4_workspace(int64_t rows, int I, int group_size, int dtype) {
+    if (rows < 0 || rows >= (int64_t{1} << 31) || (group_size != 32 && group_size != 64 && group_size != 128) ||
+        I < group_size || I % group_size != 0 || !half_type(dtype))
+        return -1;
+    return ep::expert_w4_workspace(rows, I, group_size, dtype);
+}
+
 ep_status_t ep_expert_w4(const void* x, int64_t rows, int I, const uint8_t* weights, const void* scales,
                          const uint8_t* zeros, const int32_t* expert_offsets, const int32_t* expert_counts, int E,
-                         int O, const ep_w4_config_t* config, void* y, void* stream) {
+                         int O, const ep_w4_config_t* config, void* y, void* workspace, int64_t workspace_bytes,
+                         void* stream) {
     ApiRange range("ep_expert_w4");
     if (!config || !half_type(config->dtype) || rows < 0 || rows >= (int64_t{1} << 31)) return EP_ERR_INVALID_ARG;
     const int group = config->group_size;
@@ -251,6 +259,8 @@ ep_status_t ep_expert_w4(const void* x, int64_t rows, int I, const uint8_t* weig
     if (rows == 0) return EP_OK;
     if (!x || !weights || !scales || !y || !aligned(x, 16) || !aligned(weights, 16) || !aligned(scales, 2) ||
         !aligned(y, 2) || !aligned(expert_offsets, 4) || !aligned(expert_counts, 4))
+        return EP_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < ep::expert_w4_workspace(rows, I, group, config->dtype))
         return EP_ERR_INVALID_ARG;
     ep::W4Args a{};
     a.x = x;
@@ -268,7 +278,7 @@ ep_status_t ep_expert_w4(const void* x, int64_t rows, int I, const uint8_t* weig
     a.x_ld = config->x_ld;
     a.y_ld = config->y_ld;
     a.y = y;
-    return status_of(ep::launch_expert_w4(a, config->dtype, static_cast<cudaStream_t>(stream)));
+    return status_of(ep::launch_expert_w4(a, workspace, config->dtype, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -13,13 +13,14 @@ import ctypes
 
 import torch
 
-from . import (EP_DTYPE_BF16, EP_DTYPE_FP8_E4M3, EP_DTYPE_FP16, EP_DTYPE_FP32, _check, _stream, lib)
+from . import (EP_DTYPE_BF16, EP_DTYPE_FP8_E4M3, EP_DTYPE_FP16, EP_DTYPE_FP32, EP_ERR_INVALID_ARG, EPError, _check,
+               _stream, lib)
 
 EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
 EP_ACT_NONE, EP_ACT_SWIGLU = 0, 1
 
 EXPORTS = ("ep_router_topk", "ep_router_topk_backward", "ep_kv_append", "ep_paged_attention",
-           "ep_paged_attention_workspace", "ep_expert_w4")
+           "ep_paged_attention_workspace", "ep_expert_w4", "ep_expert_w4_workspace")
 
 _i32, _i64, _f32, _P = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
@@ -63,7 +64,8 @@ def declare(L) -> None:
     L.ep_kv_append.argtypes = [_P, _P, _P, _P, _P, _P, _i32, ref(AppendConfig), _P, _P, _P, ref(Cache), _P, _P]
     L.ep_paged_attention.argtypes = [_P, _P, _P, ref(Cache), _P, _P, _i32, ref(AttentionConfig), _P, _P, _P, _i64, _P]
     L.ep_paged_attention_workspace.argtypes = [_i32, _i32, _i32, _i32]
-    L.ep_expert_w4.argtypes = [_P, _i64, _i32, _P, _P, _P, _P, _P, _i32, _i32, ref(W4Config), _P, _P]
+    L.ep_expert_w4.argtypes = [_P, _i64, _i32, _P, _P, _P, _P, _P, _i32, _i32, ref(W4Config), _P, _P, _i64, _P]
+    L.ep_expert_w4_workspace.argtypes = [_i64, _i32, _i32, _i32]
     for name in EXPORTS:
         getattr(L, name).restype = _i64 if name.endswith("workspace") else _i32
 
@@ -215,12 +217,14 @@ def ep_paged_attention(q, k_cache, v_cache, block_table, seq_lens, out, workspac
 
 
 def ep_expert_w4(x, weights, scales, y, expert_offsets=None, expert_counts=None, zeros=None,
-                 activation: int = EP_ACT_NONE, stream=None) -> None:
+                 activation: int = EP_ACT_NONE, workspace=None, stream=None) -> None:
     """y [rows, O] (O/2 columns with EP_ACT_SWIGLU) = x [rows, I] times each
     row's expert's weights [E, O, I/2] uint8, two 4-bit codes a byte, with
     scales [E, I/group, O] of x's type and zeros [E, I/group, O] uint8 (8
     if None). Rows belong to experts by expert_offsets [E + 1] int32 (None: one
-    expert); with expert_counts [E] int32 only each expert's first rows count."""
+    expert); with expert_counts [E] int32 only each expert's first rows count.
+    Without a workspace (ep_expert_w4_workspace bytes) one is taken from torch's
+    allocator for the call, on the current stream only."""
     rows, I = x.shape
     E, O, half = weights.shape
     groups = scales.shape[1]
@@ -229,10 +233,26 @@ def ep_expert_w4(x, weights, scales, y, expert_offsets=None, expert_counts=None,
     xp, xld = _rows(x, x.dtype, (rows, I), "x")
     yp, yld = _rows(y, x.dtype, (rows, O // 2 if activation == EP_ACT_SWIGLU else O), "y")
     cfg = W4Config(_dtype(x, _FLOATS, "x"), I // groups, activation, xld, yld)
+    if workspace is None:
+        if stream is not None:
+            raise ValueError("a call on a stream of its own needs a workspace")
+        workspace = torch.empty(max(ep_expert_w4_workspace(x, scales), 0), dtype=torch.uint8, device=x.device)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     _check(lib().ep_expert_w4(xp, rows, I, _dense(weights, torch.uint8, (E, O, half), "weights"),
                               _dense(scales, x.dtype, (E, groups, O), "scales"),
                               _dense(zeros, torch.uint8, (E, groups, O), "zeros"),
                               _dense(expert_offsets, torch.int32, (E + 1,), "expert_offsets"),
                               _dense(expert_counts, torch.int32, (E,), "expert_counts"), E, O, cfg, yp,
+                              _on_gpu(workspace, "workspace"), workspace.numel() * workspace.element_size(),
                               _stream(stream)),
            "ep_expert_w4")
+
+
+def ep_expert_w4_workspace(x, scales) -> int:
+    """Bytes of workspace that ep_expert_w4 needs for tensors of these shapes."""
+    rows, I = x.shape
+    size = lib().ep_expert_w4_workspace(rows, I, I // max(scales.shape[1], 1), _dtype(x, _FLOATS, "x"))
+    if size < 0:
+        raise EPError(EP_ERR_INVALID_ARG, "ep_expert_w4_workspace")
+    return size

@@ -237,13 +237,21 @@ typedef struct {
  *  E, O           experts and weight rows; O even with EP_ACT_SWIGLU, whose y
  *                 has O/2 columns: gate = weight row j, up = row O/2 + j.
  *  y              device, [rows, O or O/2].
- * Products are exact and sums fp32 (the group's scale multiplies the group's
- * sum); y is rounded once, after the activation. rows and offsets are taken
- * as at most `rows`; rows < 2^31.
+ *  workspace      device, 16-byte aligned, ep_expert_w4_workspace bytes;
+ *                 contents need no initialising and are not kept.
+ * Each input is taken to within 2^-17 of the largest of the 64 (32 with groups
+ * of 32) neighbours that share its power of two; products and sums are fp32, a
+ * group's scale multiplies the group's sum, and y is rounded once, after the
+ * activation. An infinite input makes its row of y NaN. Offsets are taken as
+ * at most `rows`; rows < 2^31.
  */
 EP_API ep_status_t ep_expert_w4(const void* x, int64_t rows, int I, const uint8_t* weights, const void* scales,
                                 const uint8_t* zeros, const int32_t* expert_offsets, const int32_t* expert_counts,
-                                int E, int O, const ep_w4_config_t* config, void* y, void* stream);
+                                int E, int O, const ep_w4_config_t* config, void* y, void* workspace,
+                                int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that ep_expert_w4 needs; -1 for invalid sizes. */
+EP_API int64_t ep_expert_w4_workspace(int64_t rows, int I, int group_size, int dtype);
 
 #ifdef __cplusplus
 }

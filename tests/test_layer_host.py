@@ -144,11 +144,11 @@ def test_attention_workspace_rejects(ep):
 
 def experts(ep, **kw):
     a = dict(x=16, rows=4, I=128, w=16, s=16, z=None, off=16, cnt=None, E=2, O=10, y=16, dtype=0, group=64, act=0,
-             x_ld=128, y_ld=10, cfg=True)
+             x_ld=128, y_ld=10, cfg=True, work=16, size=1 << 40)
     a.update(kw)
     cfg = ep.layer.W4Config(a["dtype"], a["group"], a["act"], a["x_ld"], a["y_ld"])
     return ep.lib().ep_expert_w4(a["x"], a["rows"], a["I"], a["w"], a["s"], a["z"], a["off"], a["cnt"], a["E"], a["O"],
-                                 cfg if a["cfg"] else None, a["y"], None)
+                                 cfg if a["cfg"] else None, a["y"], a["work"], a["size"], None)
 
 
 @pytest.mark.parametrize("kw", [dict(x=None), dict(x=24), dict(rows=-1), dict(rows=1 << 31), dict(I=0), dict(I=96),
@@ -156,9 +156,14 @@ def experts(ep, **kw):
                                 dict(cnt=18), dict(off=None, E=1, cnt=16), dict(E=0), dict(E=4097), dict(O=0), dict(y=None),
                                 dict(y=17), dict(dtype=1), dict(dtype=4), dict(group=16), dict(group=256, I=256, x_ld=256),
                                 dict(group=48, I=96, x_ld=96), dict(act=2), dict(act=1, O=9), dict(x_ld=120),
-                                dict(x_ld=132), dict(y_ld=9), dict(cfg=False)])
+                                dict(x_ld=132), dict(y_ld=9), dict(cfg=False), dict(work=None), dict(work=24), dict(size=100)])
 def test_experts_reject(ep, kw):
     assert experts(ep, **kw) == INVALID
+
+
+def test_experts_workspace_rejects(ep):
+    for args in [(-1, 128, 64, 0), (1 << 31, 128, 64, 0), (4, 96, 64, 0), (4, 0, 64, 0), (4, 128, 16, 0), (4, 128, 64, 1)]:
+        assert ep.lib().ep_expert_w4_workspace(*args) == -1
 
 
 def test_empty_calls_need_nothing(ep):

@@ -12,8 +12,8 @@
 //    a power of two has brought the largest input of the group to [128, 256).
 //    Four significant bits each make up the 8 or 11 of x, exactly, down to
 //    e4m3's smallest step: what is left off is below 2^-17 of the group's
-//    largest. The parts of a row are columns of the product's narrow side, which
-//    has to be 16 wide in any case.
+//    largest. The product's narrow side is 16 wide at least: the parts of 8 rows
+//    share it, those of more rows are added into the same sums.
 //  - the zero point enters as zero * (sum of the group's inputs), in fp32.
 // Scales multiply a group's sum in fp32. y is rounded once.
 //
@@ -25,12 +25,13 @@
 // Layout. A tile of 128 weight rows is the product's 128 lanes: thread = weight
 // row = TMEM lane, for unpacking (shared memory to TMEM operand A), for the
 // scales (one a thread) and for the sums (tcgen05.ld, one column a row of x). A
-// persistent CTA walks its items (an expert, a tile, at most NR rows of x); one
+// persistent CTA walks its items (an expert, a tile, at most NR rows of x). One
 // warp fills a ring of stages (256 inputs: 16 KB of codes by TMA) that runs on
-// across items, two warpgroups take half a stage each. The first weights are
-// on their way while split_kernel still runs. Where there are few items, the
-// CTAs of a cluster share an item's inputs and join through distributed shared
-// memory.
+// across items; two warpgroups take half a stage each: they unpack it, hand it
+// to the warp that issues the products, and take in the sums of the half before
+// meanwhile. The first weights are on their way while split_kernel still runs.
+// Where there are few items, the CTAs of a cluster share an item's inputs and
+// join through distributed shared memory.
 #include <cuda.h>
 
 #include <type_traits>
@@ -40,35 +41,36 @@
 namespace ep {
 namespace {
 
-constexpr int kThreads = 288;          // two warpgroups and the warp that loads
+constexpr int kThreads = 320;          // two warpgroups, a warp that loads, a warp that issues products
 constexpr int kConsumers = 256;
+constexpr int kLoader = kConsumers / 32, kIssuer = kLoader + 1;   // warps
 constexpr int kRows = 128;             // weight rows of a tile
 constexpr int kIn = 256;               // inputs of a stage, 128 a warpgroup
 constexpr int kWeightBytes = kRows * kIn / 2;
 constexpr int kSplitThreads = 256;
 constexpr int kMostSplit = 8;          // CTAs of a cluster that share an item
 
-// How x is split: parts, and places for them (the product's narrow side is a multiple of 16).
+// Parts that x is split into.
 template <typename T>
-struct Parts {
-    static constexpr int kCount = std::is_same_v<T, __half> ? 3 : 2;
-    static constexpr int kPlaces = std::is_same_v<T, __half> ? 4 : 2;
-};
+constexpr int kParts = std::is_same_v<T, __half> ? 3 : 2;
 
 constexpr int power_of_two(int n) { return n <= 32 ? 32 : 2 * power_of_two((n + 1) / 2); }
 
 // T: type of x, scales and y. NR: rows of x of an item. GROUP: inputs that share a scale.
 template <typename T, int NR, int GROUP>
 struct Shape {
-    static constexpr int kN = NR * Parts<T>::kPlaces;          // columns of the product
+    static constexpr bool kSideBySide = NR == 8;               // two parts of 8 rows in one product
+    static_assert(NR % 16 == 0 || (kSideBySide && kParts<T> == 2), "");
+    static constexpr int kN = kSideBySide ? 16 : NR;           // columns of the product
+    static constexpr int kProducts = kSideBySide ? 1 : kParts<T>;
     static constexpr int kGroups = 128 / GROUP;                // of a warpgroup's half of a stage
-    static constexpr int kXBytes = kN * 128;                   // x of half a stage
-    static constexpr int kStats = 2 * kGroups * NR;            // float2s of a stage
+    static constexpr int kXBytes = NR * kParts<T> * 128;       // x of half a stage
+    static constexpr int kStats = 2 * kGroups * NR * 2;        // floats of a stage
     static constexpr int kSumCols = kN * kGroups;
     // columns of TMEM: operand A twice for both warpgroups, sums twice too where that leaves room for two CTAs a core
     static constexpr int kSumBuffers = 128 + 4 * kSumCols <= 256 ? 2 : 1;
     static constexpr int kTmem = power_of_two(128 + 2 * kSumBuffers * kSumCols);
-    static constexpr int kStageBytes = kWeightBytes + 2 * kXBytes + kStats * 8;
+    static constexpr int kStageBytes = kWeightBytes + 2 * kXBytes + kStats * 4;
     // two CTAs a core where TMEM (512 columns) allows it
     static constexpr int kResident = kTmem <= 256 ? 2 : 1;
     static constexpr int kFixed = NR * kRows * 4 + 2048;       // join buffer, barriers, alignment
@@ -84,7 +86,7 @@ struct Plan {
     int split;       // CTAs that share an item
     int stages;      // of an item
     int groups;      // of a weight row
-    const float2* stats;   // [rows][groups]: power of two, 2^-9 * sum, of a group's inputs
+    const float* stats;    // [rows][groups][2]: power of two, 2^-9 * sum, of a group's inputs
 };
 
 // ------------------------------------------------------------------ PTX
@@ -123,8 +125,8 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int real) {   // zeros where real is 0
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int real) {   // zeros where real is 0
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
 }
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -145,14 +147,12 @@ __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32
         : "memory");
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_load8(uint32_t at, float (&r)[8]) {
-    uint32_t u[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&u)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+                   "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
                  : "r"(at)
                  : "memory");
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(u[i]);
 }
 __device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // sums [128 lanes][N] (+)= A [128 lanes][32 inputs, TMEM] * B [32 inputs][N, shared memory]^T
@@ -163,6 +163,33 @@ __device__ __forceinline__ void multiply(uint32_t sums, uint32_t a, uint64_t b, 
 }
 __device__ __forceinline__ void multiply_done(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Two fp32 numbers in one register pair, and arithmetic on both.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t both(float v) { return pair(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ float2 apart(uint64_t v) {
+    uint32_t lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+    return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 // Rows of 128 bytes along the inputs, 128-byte swizzle: 8 rows are 1024 bytes.
 __device__ __forceinline__ uint64_t operand(uint32_t addr) {
@@ -240,7 +267,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(W4Args a, unsigned
             sum += even[k] + odd[k];
         }
 #pragma unroll
-        for (int k = 0; k < Parts<T>::kCount; ++k) {
+        for (int k = 0; k < kParts<T>; ++k) {
             uint2 w;
             w.x = take_part(even);
             w.y = take_part(odd);
@@ -263,15 +290,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, NR, GROUP>::kResident))
     using S = Shape<T, NR, GROUP>;
     constexpr int kStages = S::kStages, kGroups = S::kGroups;
     extern __shared__ unsigned char shared_bytes[];
-    // [kStages] weights (rows of 128 bytes, 128-byte swizzle), [kStages] x (two halves [kN][128 bytes]), then stats, the
-    // join buffer [NR][kRows], barriers, first_pass [E + 1]
+    // [kStages] weights (rows of 128 bytes, 128-byte swizzle), [kStages] x (two halves [parts][NR][128 bytes]), stats, the
+    // join buffer [NR][kRows], barriers, first_pass [E + 1]. stats: [kStages][2][kGroups] of NR / 2 pairs of rows, a pair's
+    // two powers of two, then its two sums
     unsigned char* const weights = shared_bytes + (1024 - smem_addr(shared_bytes) % 1024) % 1024;
     unsigned char* const inputs = weights + kStages * kWeightBytes;
-    float2* const stats = reinterpret_cast<float2*>(inputs + kStages * 2 * S::kXBytes);   // [kStages][2][kGroups][NR]
+    float* const stats = reinterpret_cast<float*>(inputs + kStages * 2 * S::kXBytes);
     float* const join = reinterpret_cast<float*>(stats + kStages * S::kStats);
     uint64_t* const barriers = reinterpret_cast<uint64_t*>(join + NR * kRows);
-    const uint32_t full = smem_addr(barriers), empty = full + 8 * kStages, done = empty + 8 * kStages;   // done: [2][2]
-    uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(barriers + 2 * kStages + 4);
+    const uint32_t full = smem_addr(barriers), empty = full + 8 * kStages;
+    const uint32_t ready = empty + 8 * kStages, done = ready + 32;   // [2 warpgroups][2 buffers]
+    uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(barriers + 2 * kStages + 8);
     volatile int* const dead = reinterpret_cast<volatile int*>(tmem_at + 1);
     int* const first_pass = reinterpret_cast<int*>(tmem_at + 2);
     __shared__ int warp_sum[kThreads / 32];
@@ -283,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, NR, GROUP>::kResident))
     const int cols = a.swiglu ? a.O / 2 : a.O, tile_cols = a.swiglu ? kRows / 2 : kRows;
     const int rank = blockIdx.x % p.split;
 
-    if (warp == kConsumers / 32) {
+    if (warp == kLoader) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_at)), "n"(S::kTmem) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         if (lane == 0) {
@@ -292,7 +321,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, NR, GROUP>::kResident))
                 barrier_init(full + 8 * i, 33);                  // the TMA loads' thread and 32 lanes' copies
                 barrier_init(empty + 8 * i, kConsumers / 32);
             }
-            for (int i = 0; i < 4; ++i) barrier_init(done + 8 * i, 1);
+            for (int i = 0; i < 4; ++i) {
+                barrier_init(ready + 8 * i, 4);
+                barrier_init(done + 8 * i, 1);
+            }
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
     }
@@ -351,12 +383,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, NR, GROUP>::kResident))
         return r;
     };
 
-    if (warp == kConsumers / 32) {
-        // ---- the loading warp
+    const int64_t steps = (item1 - item0) * (stage1 - stage0);
+
+    if (warp == kLoader) {
         const auto load_weights = [&](const Item& it, int stage, int slot) {
             if (lane != 0) return;
             const uint32_t bar = full + 8 * slot, to = smem_addr(weights) + slot * kWeightBytes;
-            barrier_expect(bar, kWeightBytes + 2 * NR * Parts<T>::kCount * 128);
+            barrier_expect(bar, kWeightBytes + 2 * S::kXBytes);
             load_tile(to, &weight_map, stage * (kIn / 2), it.col, it.expert, bar);
             if (a.swiglu) load_tile(to + kWeightBytes / 2, &weight_map, stage * (kIn / 2), cols + it.col, it.expert, bar);
         };
@@ -366,13 +399,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, NR, GROUP>::kResident))
                 for (int h = 0; h < 2; ++h)
                     load_tile(smem_addr(inputs) + (slot * 2 + h) * S::kXBytes, &x_map, stage * kIn + h * 128, it.row, 0, bar);
             for (int i = lane; i < S::kStats; i += 32) {
-                const int n = i % NR, grp = stage * (kIn / GROUP) + i / NR;
+                const int n = i / 4 % (NR / 2) * 2 + (i & 1), which = (i >> 1) & 1, grp = stage * (kIn / GROUP) + i / (2 * NR);
                 const bool in = n < it.rows && grp < p.groups;
-                copy8(smem_addr(stats + slot * S::kStats + i), p.stats + (in ? static_cast<int64_t>(it.row + n) * p.groups + grp : 0), in ? 8 : 0);
+                copy4(smem_addr(stats + slot * S::kStats + i),
+                      p.stats + (in ? (static_cast<int64_t>(it.row + n) * p.groups + grp) * 2 + which : 0), in ? 4 : 0);
             }
             copies_arrive(bar);
         };
-        const int64_t steps = (item1 - item0) * (stage1 - stage0);
         const int first_steps = static_cast<int>(min(steps, static_cast<int64_t>(kStages)));
         int64_t item = item0;
         int stage = stage0;
@@ -396,17 +429,41 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, NR, GROUP>::kResident))
             load_inputs(it, stage, slot);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if (p.split > 1)   // two cluster barriers an item, as the warpgroups have
-            for (int64_t i = item0; i < item1; ++i) {
-                asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
-                asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+    } else if (warp == kIssuer) {
+        if (lane == 0) {
+            constexpr uint32_t kShape = (1u << 4) | (static_cast<uint32_t>(S::kN / 8) << 17) | (static_cast<uint32_t>(kRows / 16) << 24);
+            int slot = 0, buffer = 0;
+            uint32_t full_parity = 0, ready_parity = 0;
+            for (int64_t i = 0; i < steps; ++i) {
+                barrier_wait(full + 8 * slot, full_parity, dead);
+                for (int wg = 0; wg < 2; ++wg) {
+                    barrier_wait(ready + 8 * (wg * 2 + buffer), ready_parity, dead);
+                    tmem_fence_after();
+                    const uint32_t a_at = tmem + wg * 64 + buffer * 32;
+                    const uint32_t sums = tmem + 128 + (wg * S::kSumBuffers + (S::kSumBuffers == 2 ? buffer : 0)) * S::kSumCols;
+                    const uint64_t b = operand(smem_addr(inputs) + (slot * 2 + wg) * S::kXBytes);
+#pragma unroll
+                    for (int grp = 0; grp < kGroups; ++grp)
+#pragma unroll
+                        for (int part = 0; part < S::kProducts; ++part)
+#pragma unroll
+                            for (int k = 0; k < GROUP / 32; ++k) {
+                                const int step = grp * (GROUP / 32) + k;
+                                multiply(sums + grp * S::kN, a_at + step * 8, b + step * 2 + part * (NR * 128 / 16), kShape, part > 0 || k > 0);
+                            }
+                    multiply_done(done + 8 * (wg * 2 + buffer));
+                }
+                buffer ^= 1;
+                if (buffer == 0) ready_parity ^= 1;
+                if (++slot == kStages) slot = 0, full_parity ^= 1;
             }
+        }
+        __syncwarp();
     } else {
-        // ---- a warpgroup: unpack half a stage, multiply, and take in the sums of the half before
+        // ---- a warpgroup: unpack half a stage, take in the sums of the half before
         const int wg = warp >> 2, row = tid & 127;      // row: of the tile; its TMEM lane
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // lane 32 * (warp % 4) in an address's upper half
-        const uint32_t operand_at = tmem + wg * 64, sums_at = tmem + 128 + wg * S::kSumBuffers * S::kSumCols;
-        constexpr uint32_t kShape = (1u << 4) | (static_cast<uint32_t>(S::kN / 8) << 17) | (static_cast<uint32_t>(kRows / 16) << 24);
+        const uint32_t operand_at = tmem + wg * 64 + lanes, sums_at = tmem + 128 + wg * S::kSumBuffers * S::kSumCols + lanes;
         int slot = 0, buffer = 0;
         uint32_t full_parity = 0, done_parity = 0;   // of done: a bit a buffer
         for (int64_t item = item0; item < item1; ++item) {
@@ -433,33 +490,29 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, NR, GROUP>::kResident))
                     }
                 }
             };
-            float acc[NR];
+            uint64_t acc2[NR / 2];   // rows 2 n, 2 n + 1
 #pragma unroll
-            for (int n = 0; n < NR; ++n) acc[n] = 0.0f;
+            for (int n = 0; n < NR / 2; ++n) acc2[n] = 0;
             // takes in the sums of the half stage that was multiplied into buffer b, its slot s
-            const auto sums_of = [&](int b) { return S::kSumBuffers == 2 ? sums_at + b * S::kSumCols : sums_at; };
             const auto take_sums = [&](int b, int s) {
                 barrier_wait(done + 8 * (wg * 2 + b), (done_parity >> b) & 1, dead);
                 done_parity ^= 1u << b;
                 tmem_fence_after();
 #pragma unroll
                 for (int i = 0; i < kGroups; ++i) {
-                    const float sc = to_float(scale[i]), z = static_cast<float>(zero[i]);
-                    const float2* st = stats + s * S::kStats + (wg * kGroups + i) * NR;
+                    const uint64_t sc = both(to_float(scale[i])), z = both(-static_cast<float>(zero[i]));
+                    const float* st = stats + s * S::kStats + (wg * kGroups + i) * (NR * 2);
+                    uint32_t v[S::kN / 16][16];
 #pragma unroll
-                    for (int n0 = 0; n0 < NR; n0 += 8) {
-                        float v[Parts<T>::kCount][8];
+                    for (int k = 0; k < S::kN / 16; ++k)
+                        tmem_load16(sums_at + (S::kSumBuffers == 2 ? b * S::kSumCols : 0) + i * S::kN + 16 * k, v[k]);
+                    tmem_load_wait();
 #pragma unroll
-                        for (int k = 0; k < Parts<T>::kCount; ++k)
-                            tmem_load8(sums_of(b) + lanes + i * S::kN + k * NR + n0, v[k]);
-                        tmem_load_wait();
-#pragma unroll
-                        for (int n = 0; n < 8; ++n) {
-                            float sum = v[0][n] + v[1][n];
-                            if constexpr (Parts<T>::kCount == 3) sum += v[2][n];
-                            const float2 f = st[n0 + n];
-                            acc[n0 + n] += (sc * f.x) * (sum - z * f.y);
-                        }
+                    for (int n = 0; n < NR / 2; ++n) {
+                        uint64_t sum = pair(v[n / 8][n % 8 * 2], v[n / 8][n % 8 * 2 + 1]);
+                        if constexpr (S::kSideBySide) sum = add2(sum, pair(v[0][8 + 2 * n], v[0][8 + 2 * n + 1]));
+                        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(st + 4 * n);
+                        acc2[n] = fma2(mul2(sc, f.x), fma2(z, f.y, sum), acc2[n]);
                     }
                 }
                 tmem_fence_before();
@@ -483,22 +536,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, NR, GROUP>::kResident))
                     }
                 }
                 // (the products that read this operand buffer last have been waited for in take_sums)
-                tmem_store32(operand_at + lanes + buffer * 32, codes);
+                tmem_store32(operand_at + buffer * 32, codes);
                 if (S::kSumBuffers == 1 && before >= 0) take_sums(buffer ^ 1, before);
                 tmem_fence_before();
-                group_sync(1 + wg);
-                if ((tid & 127) == 0) {
-                    tmem_fence_after();
-                    const uint64_t b = operand(smem_addr(inputs) + (slot * 2 + wg) * S::kXBytes);
-#pragma unroll
-                    for (int i = 0; i < kGroups; ++i)
-#pragma unroll
-                        for (int k = 0; k < GROUP / 32; ++k) {
-                            const int step = i * (GROUP / 32) + k;
-                            multiply(sums_of(buffer) + i * S::kN, operand_at + buffer * 32 + step * 8, b + step * 2, kShape, k > 0);
-                        }
-                    multiply_done(done + 8 * (wg * 2 + buffer));
-                }
+                __syncwarp();
+                if (lane == 0) barrier_arrive(ready + 8 * (wg * 2 + buffer));
                 if (S::kSumBuffers == 2 && before >= 0) take_sums(buffer ^ 1, before);
 #pragma unroll
                 for (int i = 0; i < kGroups; ++i) scale[i] = scale_next[i], zero[i] = zero_next[i];
@@ -509,6 +551,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, NR, GROUP>::kResident))
             }
             if (before >= 0) take_sums(buffer ^ 1, before);
 
+            float acc[NR];
+#pragma unroll
+            for (int n = 0; n < NR / 2; ++n) {
+                const float2 v = apart(acc2[n]);
+                acc[2 * n] = v.x, acc[2 * n + 1] = v.y;
+            }
             // ---- the item's end: the warpgroups join, then the cluster's CTAs, in their order; codes count as code * 2^-9
             if (wg == 1) {
 #pragma unroll
@@ -569,8 +617,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, NR, GROUP>::kResident))
             consumers_sync();   // the join buffer is free again
         }
     }
+    // (with clusters each has one item at most, so the other warps are through with it)
+    if (warp >= kLoader && p.split > 1 && item0 < item1) {
+        asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+    }
     __syncthreads();
-    if (warp == kConsumers / 32) {
+    if (warp == kLoader) {
         tmem_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmem) : "memory");
     }
@@ -632,9 +685,8 @@ cudaError_t prepare_kernel(Kernel kernel, int smem, int* known_smem, int* known_
     return cudaSuccess;
 }
 
-int64_t plane_bytes(int64_t rows, int I) { return rows * I; }   // I is a multiple of 32
 int64_t split_bytes(int64_t rows, int I, int dtype) {
-    return plane_bytes(rows, I) * (dtype == EP_DTYPE_FP16 ? Parts<__half>::kCount : Parts<__nv_bfloat16>::kCount);
+    return rows * I * (dtype == EP_DTYPE_FP16 ? kParts<__half> : kParts<__nv_bfloat16>);
 }
 
 template <typename T, int NR, int GROUP>
@@ -650,7 +702,7 @@ cudaError_t launch_shape(const W4Args& a, const unsigned char* x, const float2* 
     p.tiles = (cols + tile_cols - 1) / tile_cols;
     p.stages = (a.I + kIn - 1) / kIn;
     p.groups = a.I / GROUP;
-    p.stats = stats;
+    p.stats = reinterpret_cast<const float*>(stats);
     p.slots = sms * S::kResident;
     // items at most; with fewer than half the CTAs' number, clusters share them
     const int64_t most = (static_cast<int64_t>(a.rows) / NR + (a.rows < a.E ? a.rows : a.E)) * p.tiles;
@@ -660,7 +712,7 @@ cudaError_t launch_shape(const W4Args& a, const unsigned char* x, const float2* 
     p.slots = static_cast<int>(clusters) * p.split;
     CUtensorMap weight_map, x_map;
     err = byte_map(&weight_map, a.w, a.I / 2, a.O, a.E, tile_cols, 1);
-    if (err == cudaSuccess) err = byte_map(&x_map, x, a.I, a.rows, Parts<T>::kCount, NR, Parts<T>::kCount);
+    if (err == cudaSuccess) err = byte_map(&x_map, x, a.I, a.rows, kParts<T>, NR, kParts<T>);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.slots);
@@ -687,11 +739,11 @@ cudaError_t launch_group(const W4Args& a, void* workspace, int dtype, cudaStream
     const cudaError_t err = launch_dependent(split_kernel<T, GROUP>, dim3(static_cast<unsigned>(blocks < 8192 ? blocks : 8192)),
                                              dim3(kSplitThreads), 0, stream, a, x, stats);
     if (err != cudaSuccess) return err;
-    // rows of an item: 8, or 16 where experts have more than 8 rows on average
+    // rows of an item: 8, or 16 where experts have more than 4 rows on average (a second pass over a tile costs more)
     const int used = a.rows < a.E ? a.rows : a.E, mean = (a.rows + used - 1) / used;
-    if constexpr (!(std::is_same_v<T, __half> && GROUP == 32))   // (16 rows of three parts in groups of 32 outgrow TMEM)
-        if (mean > 4 && a.rows > 8) return launch_shape<T, 16, GROUP>(a, x, stats, stream);
-    return launch_shape<T, 8, GROUP>(a, x, stats, stream);
+    if constexpr (kParts<T> == 2)
+        if (mean <= 4 || a.rows <= 8) return launch_shape<T, 8, GROUP>(a, x, stats, stream);
+    return launch_shape<T, 16, GROUP>(a, x, stats, stream);
 }
 
 template <typename T>

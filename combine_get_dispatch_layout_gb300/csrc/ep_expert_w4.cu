@@ -1,37 +1,41 @@
 // The experts' products on dispatched rows: 4-bit weights, group scales.
 //
 // Mathematics. y[n, o] = sum over groups g of s[g, o] * sum over i in g of
-// (code[o, i] - zero[g, o]) x[n, i]. code - zero is a whole number of at most five
-// bits and exact in fp16; x is exact in fp16 once a power of two has brought the
-// row's largest input to [2^14, 2^15) (down to 2^-28 of it, below that to
-// 2^-39 of it). So the inner sums run through the fp16 matrix instruction with
-// exact products and fp32 sums, and the scale multiplies a group's sum in fp32:
-// no weight is rounded.
+// (code[o, i] - zero[g, o]) x[n, i]. The inner sums run through the 5th-generation
+// tensor cores on e4m3 operands with fp32 sums:
+//  - a code 0 .. 15 in a byte IS the e4m3 number code * 2^-9 (subnormal up to 7,
+//    the first binade from 8 on), so unpacking eight codes is two masks and one
+//    shift. (As bf16 operands of mma.sync they take 11 instructions, and that
+//    kernel ran at 37 % of the memory rate, bound by instruction issue; e4m3
+//    operands of mma.sync are converted to fp16 by further instructions.)
+//  - x is taken as a sum of e4m3 numbers, two for bf16 and three for fp16, after
+//    a power of two has brought the largest input of the group to [128, 256).
+//    Four significant bits each make up the 8 or 11 of x, exactly, down to
+//    e4m3's smallest step: what is left off is below 2^-17 of the group's
+//    largest. The parts lie side by side in the product's narrow side; only
+//    where TMEM has no room for the columns (groups of 32, or fp16 in groups of
+//    64) they are added into the same sums.
+//  - the zero point enters as zero * (sum of the group's inputs), in fp32.
+// Scales multiply a group's sum in fp32. y is rounded once.
 //
 // What bounds it: with few rows per expert each weight is used a few times, so
-// reading the codes (half a byte each) once is the floor: 22 clocks for 128 bytes
-// an SM quarter. Next is instruction issue: a word of eight codes takes five
-// logic instructions (two nibble pairs under an fp16 exponent, one shift, two
-// more), four fp16 ones for the zero points, and a matrix instruction for each 8
-// rows. Measured on the way, for 256 tokens: bf16 operands (three shifts, loads
-// and copies by all warps) 1562 us, bound by issue; codes as e4m3 numbers
-// through tcgen05.mma with the unpacked operand in TMEM 925 us, bound by TMEM,
-// which takes the unpacked operand in and out (a product of 128 x 32 inputs 54
-// clocks however narrow).
+// reading the codes (half a byte each) once is the floor. Instruction issue is
+// next: about 6 instructions a word of 8 codes of the 22 clocks that DRAM takes
+// for 128 bytes an SM quarter.
 //
-// Layout. Weight rows are the instruction's 16 rows, dispatched rows its 8
-// columns. The order of a product's inputs is free: a thread takes neighbouring
-// codes of a weight row, in the order in which masks leave them ((0, 4), (1, 5),
-// (2, 6), (3, 7) of a word), and x is written in the order in which the threads
-// ask for it (order_kernel), so the codes are used in the plain layout in which
-// they are stored. One persistent CTA a core walks its items (an expert, 512
-// weight rows, at most 8 NT rows of x). One warp fills the rings by TMA, straight on
-// across items: stages of 256 inputs, 64 KB of codes; x, which comes from L2, is
-// shared by all 512 rows (with 128 rows it was half as much traffic again as the
-// codes, and the ring alone could not pass 77 % of the memory rate). Sixteen
-// warps take 32 rows each and never wait for each other. The first weights are on
-// their way while order_kernel still runs. Where there are few items, the CTAs of
-// a cluster share an item's inputs and join through distributed shared memory.
+// Layout. 128 weight rows are the product's 128 lanes: thread = weight row =
+// TMEM lane, for unpacking (shared memory to TMEM operand A), for the scales
+// (one a thread) and for the sums (tcgen05.ld, one column a row of x). One
+// persistent CTA a core walks its items (an expert, 512 weight rows, at most NR
+// rows of x). One warp fills the rings by TMA, straight on across items: stages
+// of 256 inputs, 64 KB of codes; x, which comes from L2, is shared by all 512
+// rows (with 128 rows it was half as much traffic again as the codes, and the
+// ring alone could not pass 77 % of the memory rate). Four warpgroups take 128
+// rows each: they unpack half a stage, hand it to the warp that issues the
+// products, and take in the sums of the half before meanwhile. The first weights
+// are on their way while split_kernel still runs. Where there are few items, the
+// CTAs of a cluster share an item's inputs and join through distributed shared
+// memory.
 #include <cuda.h>
 
 #include <type_traits>
@@ -41,33 +45,44 @@
 namespace ep {
 namespace {
 
-constexpr int kWarps = 16;                         // that multiply
-constexpr int kConsumers = 32 * kWarps;
-constexpr int kLoader = kWarps;                    // the warp that loads
-constexpr int kThreads = kConsumers + 32;
-constexpr int kWarpRows = 32;                      // weight rows of a warp: two of the instruction
+constexpr int kGroupsOfWarps = 4;                  // warpgroups
+constexpr int kConsumers = 128 * kGroupsOfWarps;
+constexpr int kLoader = kConsumers / 32, kIssuer = kLoader + 1;   // warps
+constexpr int kThreads = kConsumers + 64;
+constexpr int kTileRows = 128;                     // weight rows of a warpgroup
 constexpr int kIn = 256;                           // inputs of a stage
-constexpr int kWarpBytes = kWarpRows * kIn / 2;
-constexpr int kWeightBytes = kWarps * kWarpBytes;
-constexpr int kWeightSlots = 3, kXSlots = 3;
-constexpr int kOrderThreads = 256;
+constexpr int kTileBytes = kTileRows * kIn / 2;
+constexpr int kWeightBytes = kGroupsOfWarps * kTileBytes;
+constexpr int kWeightSlots = 3;
+constexpr int kSplitThreads = 256;
 constexpr int kMostSplit = 8;                      // CTAs of a cluster that share an item
 constexpr int kTable = 1024;                       // entries of the table of experts' passes
 
-// NT: eights of rows of x of an item. GROUP: inputs that share a scale; a thread takes GROUP / 32 words of a row.
-template <int NT, int GROUP>
+// Parts that x is split into.
+template <typename T>
+constexpr int kParts = std::is_same_v<T, __half> ? 3 : 2;
+
+// T: type of x, scales and y. NR: rows of x of an item. GROUP: inputs that share a scale.
+template <typename T, int NR, int GROUP>
 struct Shape {
-    static constexpr int kXBytes = NT * 8 * kIn * 2;           // x of a stage
-    static constexpr int kShared = 1024 + kWeightSlots * kWeightBytes + kXSlots * kXBytes + 256 + (kTable + 1) * 4;
+    static_assert(NR == 16 || (NR == 8 && kParts<T> == 2), "");
+    static constexpr bool kSideBySide = 64 + NR * kParts<T> * (128 / GROUP) <= 128;   // the parts are columns of one product
+    static constexpr int kN = kSideBySide ? NR * kParts<T> : NR;   // columns of the product
+    static_assert(kN % 16 == 0, "");
+    static constexpr int kProducts = kSideBySide ? 1 : kParts<T>;
+    static constexpr int kGroups = 128 / GROUP;                // of half a stage
+    static constexpr int kBlock = kParts<T> * 1024;            // 8 rows of x, 128 inputs: [part][8][128 bytes]
+    static constexpr int kXBytes = NR / 8 * kBlock;            // x of half a stage
+    static constexpr int kXSlots = kParts<T> == 3 ? 2 : 3;
+    static constexpr int kStats = 2 * kGroups * NR * 2;        // floats of a stage
+    static constexpr int kSumCols = kN * kGroups;
+    // columns of TMEM of a warpgroup: operand A twice, sums twice where there is room
+    static constexpr int kSumBuffers = 64 + 2 * kSumCols <= 128 ? 2 : 1;
+    static constexpr int kCols = 64 + kSumBuffers * kSumCols;
+    static_assert(kCols <= 128, "");
+    static constexpr int kTmem = 512;
+    static constexpr int kShared = 1024 + kWeightSlots * kWeightBytes + kXSlots * (2 * kXBytes + kStats * 4) + 512 + (kTable + 1) * 4;
     static_assert(kShared <= 227 * 1024 - 256, "");
-    // Row of the instruction g, of 8, is weight row place(g): loads of 16 (8) bytes by 8 (16) lanes then find 2 (4)
-    // rows that the 128-byte swizzle, which exchanges 16-byte pieces by the row's number, keeps on different banks.
-    static __device__ __forceinline__ int place(int g) {
-        if constexpr (GROUP == 128) return x_place(g);
-        return (g & 3) * 2 + (g >> 2);
-    }
-    // Column g is row x_place(g) of the eight, for the same reason (x is always loaded 16 bytes by 8 lanes).
-    static __device__ __forceinline__ int x_place(int g) { return (g & 1) * 4 + (g >> 1); }
 };
 
 struct Plan {
@@ -77,7 +92,7 @@ struct Plan {
     int split;       // CTAs that share an item
     int stages;      // of an item
     int groups;      // of a weight row
-    const float* factor;   // [rows]: what x was divided by
+    const float* stats;    // [rows][groups][2]: power of two, 2^-9 * sum, of a group's inputs
 };
 
 // ------------------------------------------------------------------ PTX
@@ -116,25 +131,85 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
 }
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int real) {   // zeros where real is 0
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void multiply(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t bits(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
-__device__ __forceinline__ __half2 halves(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 
-// Two codes of a word as fp16 numbers less the zero point: in the low mantissa bits under the exponent of 1024 they
-// read 1024 + code, four bits further up 1024 + 16 code. low = -(1024 + zero), high = -(64 + zero), both exact.
-__device__ __forceinline__ uint32_t low_pair(uint32_t w, __half2 low) {
-    return bits(__hadd2(halves((w & 0x000f000fu) | 0x64006400u), low));
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+        "r"(r[31])
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ uint32_t high_pair(uint32_t w, __half2 high) {
-    return bits(__hfma2(halves((w & 0x00f000f0u) | 0x64006400u), halves(0x2c002c00u), high));   // * 1/16
+__device__ __forceinline__ void tmem_load8(uint32_t at, uint32_t (&u)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// sums [128 lanes][N] (+)= A [128 lanes][32 inputs, TMEM] * B [32 inputs][N, shared memory]^T
+__device__ __forceinline__ void multiply(uint32_t sums, uint32_t a, uint64_t b, uint32_t shape, bool add) {
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p; }" ::"r"(sums),
+                 "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+                 : "memory");
+}
+__device__ __forceinline__ void multiply_done(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Two fp32 numbers in one register pair, and arithmetic on both.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t both(float v) { return pair(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ float2 apart(uint64_t v) {
+    uint32_t lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+    return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// Rows of 128 bytes along the inputs, 128-byte swizzle: 8 rows are 1024 bytes, the next 8 lie `stride` further on.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, int stride) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (1ull << 16) | (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+
+// One lane of a converged warp. The compiler then knows that what follows is one thread's, and issues a product every
+// 16 clocks; behind `lane == 0` it took 54 to 150 (operands moved to uniform registers one by one).
+__device__ __forceinline__ bool elected() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
 }
 
 // ------------------------------------------------------------------ rows and items
@@ -155,97 +230,130 @@ struct Item {
     int expert, row, rows, col;   // col: first output column of the tile
 };
 
-// x as fp16, a row divided by a power of two (bf16 only), in the order in which the threads of expert_w4_kernel ask for
-// it: the eights of a group of 128 (64, 32), thread by thread before word by word there, are written word by word. Of an
-// eight the pairs (0, 4), (1, 5), (2, 6), (3, 7). One block a row.
+// Four values as e4m3 codes in a word, each reduced by what its code stands for.
+__device__ __forceinline__ uint32_t take_part(float (&v)[4]) {
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(v[i], v[i + 1]), __NV_SATFINITE, __NV_E4M3);
+        const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+        v[i] -= f.x;
+        v[i + 1] -= f.y;
+        word |= static_cast<uint32_t>(c) << (8 * i);
+    }
+    return word;
+}
+
+// x as sums of e4m3 numbers, a plane [rows][I] for each part; of 8 neighbouring inputs the even ones come first, as
+// masks leave the codes. A thread takes 8 inputs, GROUP / 8 threads share a power of two. An infinite or NaN
+// input makes its group's power of two or sum NaN, and so every product with it.
 template <typename T, int GROUP>
-__global__ void __launch_bounds__(kOrderThreads) order_kernel(W4Args a, uint4* to, float* factor) {
+__global__ void __launch_bounds__(kSplitThreads) split_kernel(W4Args a, unsigned char* to, float2* stats) {
     dependent_entry();
-    constexpr bool kScaled = std::is_same_v<T, __nv_bfloat16>;
-    constexpr int kWords = GROUP / 32, kEights = GROUP / 8;
-    __shared__ float biggest[kOrderThreads / 32];
-    const int last = a.offsets ? min(max(a.offsets[a.E], 0), a.rows) : a.rows;   // rows behind belong to nobody
     const int per_row = a.I / 8;
-    for (int row = blockIdx.x; row < last; row += gridDim.x) {
-        const T* from = static_cast<const T*>(a.x) + static_cast<int64_t>(row) * a.x_ld;
-        float up = 1.0f;
-        if constexpr (kScaled) {
-            float big = 0.0f;
-            for (int c = threadIdx.x; c < per_row; c += kOrderThreads) {
-                Vec8<T> v;
-                v.raw = *reinterpret_cast<const uint4*>(from + c * 8);
+    const int last = a.offsets ? min(max(a.offsets[a.E], 0), a.rows) : a.rows;   // rows behind belong to nobody
+    const int64_t all = static_cast<int64_t>(last) * per_row, plane = static_cast<int64_t>(a.rows) * a.I;
+    // (a group's threads are of one warp: per_row is a multiple of GROUP / 8)
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSplitThreads + threadIdx.x; i - threadIdx.x % 32 < all;
+         i += static_cast<int64_t>(gridDim.x) * kSplitThreads) {
+        const bool in = i < all;
+        const int64_t row = in ? i / per_row : 0;
+        const int c = in ? static_cast<int>(i - row * per_row) : 0;
+        Vec8<T> v;
+        v.raw = make_uint4(0, 0, 0, 0);
+        if (in) v.raw = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + row * a.x_ld + c * 8);
+        float big = 0.0f, even[4], odd[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(to_float(v.v[k])));
-            }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(kFullMask, big, o));
-            if (threadIdx.x % 32 == 0) biggest[threadIdx.x / 32] = big;
-            __syncthreads();
-#pragma unroll
-            for (int w = 0; w < kOrderThreads / 32; ++w) big = fmaxf(big, biggest[w]);
-            __syncthreads();
-            const int e = big > 0.0f && big < INFINITY ? min(14 - ilogbf(big), 126) : 0;
-            up = __int_as_float((e + 127) << 23);
-            if (threadIdx.x == 0) factor[row] = __int_as_float((127 - e) << 23);
+        for (int k = 0; k < 4; ++k) {
+            even[k] = to_float(v.v[2 * k]);
+            odd[k] = to_float(v.v[2 * k + 1]);
+            big = fmaxf(big, fmaxf(fabsf(even[k]), fabsf(odd[k])));
         }
-        for (int c = threadIdx.x; c < per_row; c += kOrderThreads) {
-            Vec8<T> v;
-            v.raw = *reinterpret_cast<const uint4*>(from + c * 8);
-            uint32_t w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if constexpr (kScaled) w[k] = bits(__floats2half2_rn(to_float(v.v[k]) * up, to_float(v.v[k + 4]) * up));
-                else w[k] = bits(__halves2half2(v.v[k], v.v[k + 4]));
-            }
-            const int in = c % kEights;   // thread in / kWords, word in % kWords
-            to[static_cast<int64_t>(row) * per_row + c - in + in % kWords * 4 + in / kWords] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int o = 1; o < GROUP / 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(kFullMask, big, o));
+        const bool finite = big < INFINITY;
+        const int e = big > 0.0f && finite ? min(7 - ilogbf(big), 126) : 0;
+        const float up = __int_as_float((e + 127) << 23);
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            even[k] *= up;
+            odd[k] *= up;
+            sum += even[k] + odd[k];
         }
+#pragma unroll
+        for (int k = 0; k < kParts<T>; ++k) {
+            uint2 w;
+            w.x = take_part(even);
+            w.y = take_part(odd);
+            if (in) *reinterpret_cast<uint2*>(to + k * plane + i * 8) = w;
+        }
+        // the sum of what the parts stand for: the inputs' less what is left of them
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum -= even[k] + odd[k];
+#pragma unroll
+        for (int o = 1; o < GROUP / 8; o <<= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
+        if (in && c % (GROUP / 8) == 0)
+            stats[row * (a.I / GROUP) + c / (GROUP / 8)] =
+                make_float2(finite ? __int_as_float((127 - e) << 23) : __int_as_float(0x7fffffff), sum * 0.001953125f);
     }
 }
 
-template <typename T, int NT, int GROUP, bool ZEROS>
+template <typename T, int NR, int GROUP>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_w4_kernel(W4Args a, Plan p, const __grid_constant__ CUtensorMap weight_map, const __grid_constant__ CUtensorMap x_map) {
-    using S = Shape<NT, GROUP>;
-    constexpr int kItemRows = 8 * NT;
+    using S = Shape<T, NR, GROUP>;
+    constexpr int kGroups = S::kGroups, kXSlots = S::kXSlots;
     extern __shared__ unsigned char shared_bytes[];
-    // weights: [kWeightSlots][warp][32 rows][128 bytes], 128-byte swizzle; inputs: [kXSlots][64 inputs][NT][8 rows][128 bytes],
-    // likewise; barriers; the table of passes
+    // weights: [kWeightSlots][warpgroup][128 rows][128 bytes], 128-byte swizzle; inputs: [kXSlots][half][NR / 8][part][8 rows]
+    // [128 bytes], likewise; stats: [kXSlots][half][kGroups] of NR / 2 pairs of rows, a pair's two powers of two, then its
+    // two sums; barriers; the table of passes
     unsigned char* const weights = shared_bytes + (1024 - smem_addr(shared_bytes) % 1024) % 1024;
     unsigned char* const inputs = weights + kWeightSlots * kWeightBytes;
-    uint64_t* const barriers = reinterpret_cast<uint64_t*>(inputs + kXSlots * S::kXBytes);
+    float* const stats = reinterpret_cast<float*>(inputs + kXSlots * 2 * S::kXBytes);
+    uint64_t* const barriers = reinterpret_cast<uint64_t*>(stats + kXSlots * S::kStats);
     const uint32_t w_full = smem_addr(barriers), w_empty = w_full + 8 * kWeightSlots;
     const uint32_t x_full = w_empty + 8 * kWeightSlots, x_empty = x_full + 8 * kXSlots;
-    volatile int* const dead = reinterpret_cast<volatile int*>(barriers + 2 * (kWeightSlots + kXSlots));
-    int* const table = reinterpret_cast<int*>(barriers + 32);
-    static_assert(2 * (kWeightSlots + kXSlots) < 32, "");
+    const uint32_t ready = x_empty + 8 * kXSlots, done = ready + 16 * kGroupsOfWarps;   // [warpgroup][2 operand buffers]
+    uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(barriers) + 120;
+    volatile int* const dead = reinterpret_cast<volatile int*>(tmem_at + 1);
+    int* const table = reinterpret_cast<int*>(barriers) + 128;
+    static_assert((2 * kWeightSlots + 2 * kXSlots + 4 * kGroupsOfWarps) * 2 <= 120, "");
     __shared__ int warp_sum[kThreads / 32];
-    // Everything before order_kernel, which this kernel follows, is complete once this one runs: order_kernel lets it
-    // start only after it has waited for that itself. So all but order_kernel's own outputs can be read at once, and
+    // Everything before split_kernel, which this kernel follows, is complete once this one runs: split_kernel lets it
+    // start only after it has waited for that itself. So all but split_kernel's own outputs can be read at once, and
     // griddepcontrol.wait comes before those (in the loading warp; the others see them through its barriers).
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cols = a.swiglu ? a.O / 2 : a.O;
-    const int warp_cols = a.swiglu ? kWarpRows / 2 : kWarpRows;   // output columns of a warp
+    const int tile_cols = a.swiglu ? kTileRows / 2 : kTileRows;   // output columns of a warpgroup
     const int rank = blockIdx.x % p.split;
 
-    if (tid == kConsumers) {
-        *dead = 0;
-        for (int i = 0; i < kWeightSlots; ++i) {
-            barrier_init(w_full + 8 * i, 1);
-            barrier_init(w_empty + 8 * i, kWarps);
+    if (warp == kLoader) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_at)), "n"(S::kTmem) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if (lane == 0) {
+            *dead = 0;
+            for (int i = 0; i < kWeightSlots; ++i) {
+                barrier_init(w_full + 8 * i, 1);
+                barrier_init(w_empty + 8 * i, kConsumers / 32);
+            }
+            for (int i = 0; i < kXSlots; ++i) {
+                barrier_init(x_full + 8 * i, 33);                // the TMA loads' thread and 32 lanes' copies
+                barrier_init(x_empty + 8 * i, kConsumers / 32);
+            }
+            for (int i = 0; i < 2 * kGroupsOfWarps; ++i) {
+                barrier_init(ready + 8 * i, 4);
+                barrier_init(done + 8 * i, 1);
+            }
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
-        for (int i = 0; i < kXSlots; ++i) {
-            barrier_init(x_full + 8 * i, 1);
-            barrier_init(x_empty + 8 * i, kWarps);
-        }
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    // ---- items: an expert's rows in passes of 8 NT, each pass over all tiles; a tile's passes follow each other, so
+    // ---- items: an expert's rows in passes of NR, each pass over all tiles; a tile's passes follow each other, so
     // the weights of the second come from L2
     const auto passes_of = [&](int e) {
         int first;
-        return (expert_rows(a, e, first) + kItemRows - 1) / kItemRows;
+        return (expert_rows(a, e, first) + NR - 1) / NR;
     };
     const int entries = ((a.E - 1) >> p.table_shift) + 1;
     {
@@ -270,8 +378,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             base += passes_of(e);
         }
         if (hi == entries && lo < hi) table[entries] = base;
+        tmem_fence_before();
         __syncthreads();
+        tmem_fence_after();
     }
+    const uint32_t tmem = __shfl_sync(kFullMask, *tmem_at, 0);
+    const bool leader = elected();
     const int64_t items = static_cast<int64_t>(table[entries]) * p.tiles;
     // as many clusters as share the items evenly: all of them wait on the same DRAM, so an idle SM costs nothing
     const int clusters = p.slots / p.split;
@@ -297,9 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int first;
         const int n = expert_rows(a, e, first), pass = static_cast<int>(in % passes);
         r.expert = e;
-        r.row = first + pass * kItemRows;
-        r.rows = min(kItemRows, n - pass * kItemRows);
-        r.col = static_cast<int>(in / passes) * (kWarps * warp_cols);
+        r.row = first + pass * NR;
+        r.rows = min(NR, n - pass * NR);
+        r.col = static_cast<int>(in / passes) * (kGroupsOfWarps * tile_cols);
         return r;
     };
     const int64_t steps = (item1 - item0) * (stage1 - stage0);
@@ -309,21 +421,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t bar = w_full + 8 * slot, to = smem_addr(weights) + slot * kWeightBytes;
             if (lane == 0) barrier_expect(bar, kWeightBytes);
             __syncwarp();
-            // a box: with an activation the 16 gate and the 16 up rows of a warp, else 128 rows
+            // with an activation a box is the 16 gate and the 16 up rows of a warp, else the 128 rows of a warpgroup
             if (a.swiglu) {
-                if (lane < kWarps) load_box(to + lane * kWarpBytes, &weight_map, stage * (kIn / 2), it.col + lane * 16, 0, it.expert, bar);
-            } else if (lane < kWarps / 4) {
-                load_box(to + lane * 4 * kWarpBytes, &weight_map, stage * (kIn / 2), it.col + lane * 128, 0, it.expert, bar);
+                if (lane < kConsumers / 32)
+                    load_box(to + lane * (kTileBytes / 4), &weight_map, stage * (kIn / 2), it.col + lane * 16, 0, it.expert, bar);
+            } else if (lane < kGroupsOfWarps) {
+                load_box(to + lane * kTileBytes, &weight_map, stage * (kIn / 2), it.col + lane * kTileRows, 0, it.expert, bar);
             }
         };
         const auto load_inputs = [&](const Item& it, int stage, int slot) {
             const uint32_t bar = x_full + 8 * slot;
-            const int eights = (it.rows + 7) / 8;   // (rows that are not there leave garbage in columns that are not written)
-            if (lane == 0) barrier_expect(bar, eights * 8 * kIn * 2);
+            const int blocks = (it.rows + 7) / 8;   // (rows that are not there leave garbage in columns that are not written)
+            if (lane == 0) barrier_expect(bar, 2 * blocks * S::kBlock);
             __syncwarp();
-            if (lane < 4 * eights)
-                load_box(smem_addr(inputs) + slot * S::kXBytes + (lane / eights * NT + lane % eights) * 1024, &x_map,
-                         (stage * kIn + lane / eights * 64) * 2, it.row + lane % eights * 8, 0, 0, bar);
+            if (lane < 2 * blocks)
+                load_box(smem_addr(inputs) + (slot * 2 + lane / blocks) * S::kXBytes + lane % blocks * S::kBlock, &x_map,
+                         stage * kIn + lane / blocks * 128, it.row + lane % blocks * 8, 0, 0, bar);
+            for (int i = lane; i < S::kStats; i += 32) {
+                const int n = i / 4 % (NR / 2) * 2 + (i & 1), which = (i >> 1) & 1, grp = stage * (kIn / GROUP) + i / (2 * NR);
+                const bool in = n < it.rows && grp < p.groups;
+                copy4(smem_addr(stats + slot * S::kStats + i),
+                      p.stats + (in ? (static_cast<int64_t>(it.row + n) * p.groups + grp) * 2 + which : 0), in ? 4 : 0);
+            }
+            copies_arrive(bar);
         };
         struct Cursor {
             int64_t item;
@@ -360,190 +480,208 @@ __global__ void __launch_bounds__(kThreads, 1)
             barrier_wait(w_empty + 8 * w.slot, w.parity, dead);
             load_weights(w.at, w.stage, w.slot);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == kIssuer) {
+        if (leader) {
+            constexpr uint32_t kShape = (1u << 4) | (static_cast<uint32_t>(S::kN / 8) << 17) | (static_cast<uint32_t>(kTileRows / 16) << 24);
+            // columns: 8 rows' parts, then the next 8 rows'; or the 16 rows of one part
+            constexpr int kStride = S::kSideBySide ? 1024 : S::kBlock;
+            int slot = 0;
+            uint32_t parity = 0, ready_parity = 0;
+            for (int64_t i = 0; i < steps; ++i) {
+                barrier_wait(x_full + 8 * slot, parity, dead);
+                for (int half = 0; half < 2; ++half) {
+                    const uint64_t b = operand(smem_addr(inputs) + (slot * 2 + half) * S::kXBytes, kStride);
+                    // products that add to the same sums wait for each other: those of the warpgroups take turns
+                    for (int wg = 0; wg < kGroupsOfWarps; ++wg) barrier_wait(ready + 8 * (wg * 2 + half), ready_parity, dead);
+                    tmem_fence_after();
+#pragma unroll
+                    for (int part = 0; part < S::kProducts; ++part)
+#pragma unroll
+                        for (int k = 0; k < GROUP / 32; ++k)
+#pragma unroll
+                            for (int grp = 0; grp < kGroups; ++grp)
+#pragma unroll
+                                for (int wg = 0; wg < kGroupsOfWarps; ++wg) {
+                                    const int step = grp * (GROUP / 32) + k;
+                                    const uint32_t a_at = tmem + wg * 128 + half * 32;
+                                    const uint32_t sums = tmem + wg * 128 + 64 + (S::kSumBuffers == 2 ? half * S::kSumCols : 0);
+                                    multiply(sums + grp * S::kN, a_at + step * 8, b + step * 2 + part * (1024 / 16), kShape, part > 0 || k > 0);
+                                }
+                    for (int wg = 0; wg < kGroupsOfWarps; ++wg) multiply_done(done + 8 * (wg * 2 + half));
+                }
+                ready_parity ^= 1;
+                if (++slot == kXSlots) slot = 0, parity ^= 1;
+            }
+        }
+        __syncwarp();
     } else {
-        // ---- a warp: 32 weight rows, two of the instruction's 16 (with an activation gate and up rows)
-        const int g = lane >> 2, t = lane & 3, row0 = S::place(g);   // weight rows row0, + 8, + 16, + 24
-        constexpr int kWords = GROUP / 32;                           // of a row and group, a thread's
-        int w_slot = 0, x_slot = 0;
-        uint32_t w_parity = 0, x_parity = 0;
+        // ---- a warpgroup: unpack half a stage, take in the sums of the half before
+        const int wg = warp >> 2, row = tid & 127;      // row: of the tile; its TMEM lane
+        const uint32_t mine = tmem + wg * 128 + (static_cast<uint32_t>(warp & 3) << 21);   // lane 32 * (warp % 4), upper half
+        int w_slot = 0, x_slot = 0, stat_slot = 0;
+        uint32_t w_parity = 0, x_parity = 0, done_parity = 0;
         for (int64_t item = item0; item < item1; ++item) {
             const Item it = decode(item);
-            const int col0 = it.col + warp * warp_cols;
-            // this lane's row for the scales; the lanes exchange them
-            const int mine = a.swiglu ? col0 + (lane & 15) : col0 + lane;
-            const bool real = mine < cols;
-            const int o = a.swiglu && lane >= 16 ? cols + mine : mine;
+            // this thread's output column and weight row; with an activation a warp's lanes are 16 gate and 16 up rows
+            int col, o;
+            if (a.swiglu) {
+                col = it.col + warp * 16 + (lane & 15);
+                o = lane < 16 ? col : cols + col;
+            } else {
+                o = col = it.col + wg * kTileRows + row;
+            }
+            const bool real = col < cols;
+            const int64_t scale_base = static_cast<int64_t>(it.expert) * p.groups * a.O + (real ? o : 0);
+            const T* scale_at = static_cast<const T*>(a.scales) + scale_base + static_cast<int64_t>(stage0) * (kIn / GROUP) * a.O;
+            const uint8_t* zero_at = a.zeros ? a.zeros + scale_base + static_cast<int64_t>(stage0) * (kIn / GROUP) * a.O : nullptr;
             int grp_next = stage0 * (kIn / GROUP);
-            const int64_t scale_base = (static_cast<int64_t>(it.expert) * p.groups + grp_next) * a.O + (real ? o : 0);
-            const T* scale_at = static_cast<const T*>(a.scales) + scale_base;
-            const uint8_t* zero_at = ZEROS ? a.zeros + scale_base : nullptr;
-            T scale_next = from_float<T>(0.0f);
-            uint8_t zero_next = 8;
-            const auto load_scales = [&]() {   // of the next group
-                if (real && grp_next < p.groups) {
-                    scale_next = *scale_at;
-                    if constexpr (ZEROS) zero_next = *zero_at;
-                } else {
-                    scale_next = from_float<T>(0.0f);
+            T scale[kGroups], scale_next[kGroups];
+            uint8_t zero[kGroups], zero_next[kGroups];
+            const auto load_scales = [&]() {   // of the next half stage
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i) {
+                    scale_next[i] = from_float<T>(0.0f);
+                    zero_next[i] = 8;
+                    if (real && grp_next < p.groups) {
+                        scale_next[i] = *scale_at;
+                        if (zero_at) zero_next[i] = *zero_at;
+                    }
+                    ++grp_next;
+                    scale_at += a.O;
+                    if (zero_at) zero_at += a.O;
                 }
-                ++grp_next;
-                scale_at += a.O;
-                if constexpr (ZEROS) zero_at += a.O;
             };
-            float acc[2][NT][4];
+            uint64_t acc2[NR / 2];   // rows 2 n, 2 n + 1
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int n = 0; n < NR / 2; ++n) acc2[n] = 0;
+            // takes in the sums of half `half` of the stage whose x is in slot s
+            const auto take_sums = [&](int half, int s) {
+                barrier_wait(done + 8 * (wg * 2 + half), (done_parity >> half) & 1, dead);
+                done_parity ^= 1u << half;
+                tmem_fence_after();
+                constexpr int kBlockParts = S::kSideBySide ? kParts<T> : 1;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.0f;
-            const bool both = NT == 1 || it.rows > 8;
+                for (int i = 0; i < kGroups; ++i) {
+                    const uint64_t sc = both(to_float(scale[i])), z = both(-static_cast<float>(zero[i]));
+#pragma unroll
+                    for (int b = 0; b < NR / 8; ++b) {   // 8 rows
+                        if (b == 1 && it.rows <= 8) break;
+                        const uint32_t at = mine + 64 + (S::kSumBuffers == 2 ? half * S::kSumCols : 0) + i * S::kN + b * 8 * kBlockParts;
+                        uint32_t v[kBlockParts][8];
+#pragma unroll
+                        for (int k = 0; k < kBlockParts; ++k) tmem_load8(at + 8 * k, v[k]);
+                        tmem_load_wait();
+                        const float* st = stats + s * S::kStats + (half * kGroups + i) * (NR * 2) + b * 16;
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            uint64_t sum = pair(v[0][2 * n], v[0][2 * n + 1]);
+#pragma unroll
+                            for (int k = 1; k < kBlockParts; ++k) sum = add2(sum, pair(v[k][2 * n], v[k][2 * n + 1]));
+                            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(st + 4 * n);
+                            acc2[b * 4 + n] = fma2(mul2(sc, f.x), fma2(z, f.y, sum), acc2[b * 4 + n]);
+                        }
+                    }
+                }
+                tmem_fence_before();
+                if (half == 1) {
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(x_empty + 8 * s);
+                }
+            };
             load_scales();
+            bool before = false;
             for (int stage = stage0; stage < stage1; ++stage) {
                 barrier_wait(w_full + 8 * w_slot, w_parity, dead);
-                barrier_wait(x_full + 8 * x_slot, x_parity, dead);
-                const unsigned char* w = weights + w_slot * kWeightBytes + warp * kWarpBytes + row0 * 128;
-                const unsigned char* x = inputs + x_slot * S::kXBytes + S::x_place(g) * 128;
+                const unsigned char* w = weights + w_slot * kWeightBytes + wg * kTileBytes + row * 128;
 #pragma unroll
-                for (int grp = 0; grp < kIn / GROUP; ++grp) {
-                    // scales and zero points of this thread's rows
-                    float scale[4];
-                    __half2 low[4], high[4];
-                    {
-                        const uint32_t packed = *reinterpret_cast<const uint16_t*>(&scale_next) | static_cast<uint32_t>(zero_next) << 16;
-                        load_scales();
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t codes[32];
 #pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            const uint32_t sz = __shfl_sync(kFullMask, packed, row0 + 8 * h);
-                            const uint16_t s16 = static_cast<uint16_t>(sz);
-                            scale[h] = to_float(*reinterpret_cast<const T*>(&s16));
-                            if constexpr (ZEROS) {   // 1024 + zero and 64 + zero, by their bits, negative
-                                const uint32_t z = sz >> 16, lo = 0xe400u | z, hi = 0xd400u | z << 4;
-                                low[h] = halves(lo | lo << 16);
-                                high[h] = halves(hi | hi << 16);
-                            } else {
-                                low[h] = halves(0xe408e408u);    // -1032
-                                high[h] = halves(0xd480d480u);   // -72
-                            }
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(w + (((4 * half + j) ^ (row & 7)) << 4));
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            codes[8 * j + 2 * k] = u[k] & 0x0f0f0f0fu;
+                            codes[8 * j + 2 * k + 1] = (u[k] >> 4) & 0x0f0f0f0fu;
                         }
                     }
-                    // codes: kWords neighbouring words of each of the four rows
-                    uint32_t word[4][kWords];
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const int byte = grp * (GROUP / 2) + t * 4 * kWords;
-                        const unsigned char* from = w + h * 1024 + (((byte >> 4) ^ row0) << 4) + (byte & 15);
-                        if constexpr (kWords == 4) {
-                            const uint4 v = *reinterpret_cast<const uint4*>(from);
-                            word[h][0] = v.x, word[h][1] = v.y, word[h][2] = v.z, word[h][3] = v.w;
-                        } else if constexpr (kWords == 2) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(from);
-                            word[h][0] = v.x, word[h][1] = v.y;
-                        } else {
-                            word[h][0] = *reinterpret_cast<const uint32_t*>(from);
-                        }
+                    // (the products that read this operand buffer last have been waited for in take_sums)
+                    tmem_store32(mine + half * 32, codes);
+                    if (S::kSumBuffers == 1 && before) take_sums(half ^ 1, half == 0 ? stat_slot : x_slot);
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        barrier_arrive(ready + 8 * (wg * 2 + half));
+                        if (half == 1) barrier_arrive(w_empty + 8 * w_slot);
                     }
-                    float sum[2][NT][4];
-#pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) sum[m][n][0] = sum[m][n][1] = sum[m][n][2] = sum[m][n][3] = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < kWords; ++k) {
-                        uint4 xf[NT];
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            const int at = grp * (GROUP / 8) + k * 4 + t;   // piece of the row's 32
-                            if (n == 0 || both)
-                                xf[n] = *reinterpret_cast<const uint4*>(x + ((at >> 3) * NT + n) * 1024 + (((at & 7) ^ S::x_place(g)) << 4));
-                        }
-#pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            const uint32_t u0 = word[2 * m][k], u1 = word[2 * m + 1][k];
-                            const uint32_t a0[4] = {low_pair(u0, low[2 * m]), low_pair(u1, low[2 * m + 1]), high_pair(u0, high[2 * m]),
-                                                    high_pair(u1, high[2 * m + 1])};
-                            const uint32_t a1[4] = {low_pair(u0 >> 8, low[2 * m]), low_pair(u1 >> 8, low[2 * m + 1]),
-                                                    high_pair(u0 >> 8, high[2 * m]), high_pair(u1 >> 8, high[2 * m + 1])};
-                            multiply(sum[m][0], a0, xf[0].x, xf[0].y);
-                            multiply(sum[m][0], a1, xf[0].z, xf[0].w);
-                            if constexpr (NT == 2) {
-                                if (both) {
-                                    multiply(sum[m][1], a0, xf[1].x, xf[1].y);
-                                    multiply(sum[m][1], a1, xf[1].z, xf[1].w);
-                                }
-                            }
-                        }
+                    if (half == 0) {   // (the sums' statistics come with x)
+                        barrier_wait(x_full + 8 * x_slot, x_parity, dead);
                     }
+                    if (S::kSumBuffers == 2 && before) take_sums(half ^ 1, half == 0 ? stat_slot : x_slot);
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[m][n][j] += scale[2 * m + (j >> 1)] * sum[m][n][j];
+                    for (int i = 0; i < kGroups; ++i) scale[i] = scale_next[i], zero[i] = zero_next[i];
+                    load_scales();
+                    before = true;
                 }
-                __syncwarp();
-                if (lane == 0) {
-                    barrier_arrive(w_empty + 8 * w_slot);
-                    barrier_arrive(x_empty + 8 * x_slot);
-                }
+                stat_slot = x_slot;
                 if (++w_slot == kWeightSlots) w_slot = 0, w_parity ^= 1;
                 if (++x_slot == kXSlots) x_slot = 0, x_parity ^= 1;
             }
-            // ---- the item's end: a cluster's CTAs join, in their order
+            if (before) take_sums(1, stat_slot);
+
+            // ---- the item's end: a cluster's CTAs join, in their order; codes count as code * 2^-9
+            float acc[NR];
+#pragma unroll
+            for (int n = 0; n < NR / 2; ++n) {
+                const float2 v = apart(acc2[n]);
+                acc[2 * n] = 512.0f * v.x, acc[2 * n + 1] = 512.0f * v.y;
+            }
             if (*dead) {
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[m][n][j] = __int_as_float(0x7fffffff);
+                for (int n = 0; n < NR; ++n) acc[n] = __int_as_float(0x7fffffff);
             }
             if (p.split > 1) {   // (each cluster has one item at most: the ring is used up and serves the join)
-                float* const join = reinterpret_cast<float*>(weights);   // [8 NT][kConsumers]
+                float* const join = reinterpret_cast<float*>(weights);   // [NR][kConsumers]
                 consumers_sync();
 #pragma unroll
-                for (int i = 0; i < 8 * NT; ++i) join[i * kConsumers + tid] = acc[i / (4 * NT)][i / 4 % NT][i & 3];
+                for (int n = 0; n < NR; ++n) join[n * kConsumers + tid] = acc[n];
                 cluster_sync();
                 if (rank == 0) {
                     for (int r = 1; r < p.split; ++r) {
                         uint32_t from;
                         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(smem_addr(join)), "r"(r));
 #pragma unroll
-                        for (int i = 0; i < 8 * NT; ++i) {
+                        for (int n = 0; n < NR; ++n) {
                             float v;
-                            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(from + (i * kConsumers + tid) * 4) : "memory");
-                            acc[i / (4 * NT)][i / 4 % NT][i & 3] += v;
+                            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(from + (n * kConsumers + tid) * 4) : "memory");
+                            acc[n] += v;
                         }
                     }
                 }
                 cluster_sync();
             }
             if (rank == 0) {
+                T* y = static_cast<T*>(a.y) + static_cast<int64_t>(it.row) * a.y_ld + col;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int r = 8 * n + S::x_place(2 * t + j);
-                        if (r >= it.rows) continue;
-                        float factor = 1.0f;
-                        if constexpr (std::is_same_v<T, __nv_bfloat16>) factor = __ldcg(p.factor + it.row + r);
-                        T* y = static_cast<T*>(a.y) + static_cast<int64_t>(it.row + r) * a.y_ld + col0;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int c = row0 + 8 * h;
-                            const float v = acc[0][n][2 * h + j] * factor, u = acc[1][n][2 * h + j] * factor;
-                            if (a.swiglu) {
-                                if (col0 + c < cols) y[c] = from_float<T>(v / (1.0f + expf(-v)) * u);
-                            } else {
-                                if (col0 + c < cols) y[c] = from_float<T>(v);
-                                if (col0 + 16 + c < cols) y[16 + c] = from_float<T>(u);
-                            }
-                        }
-                    }
+                for (int n = 0; n < NR; ++n) {
+                    if (n == 8 && it.rows <= 8) break;
+                    float v = acc[n];
+                    if (a.swiglu) v = v / (1.0f + expf(-v)) * __shfl_xor_sync(kFullMask, v, 16);   // gate lanes: silu(gate) * up
+                    if (n < it.rows && real && (!a.swiglu || lane < 16)) y[n * a.y_ld] = from_float<T>(v);
+                }
             }
         }
     }
-    if (warp == kLoader && p.split > 1 && item0 < item1) {   // (as the other warps do)
+    if (warp >= kLoader && p.split > 1 && item0 < item1) {   // (as the warpgroups do)
         cluster_sync();
         cluster_sync();
+    }
+    __syncthreads();
+    if (warp == kLoader) {
+        tmem_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmem) : "memory");
     }
 }
 
@@ -597,35 +735,40 @@ cudaError_t prepare_kernel(Kernel kernel, int smem, int* known, int* sms) {
     return err;
 }
 
-template <typename T, int NT, int GROUP, bool ZEROS>
-cudaError_t launch_shape(const W4Args& a, const uint4* x, const float* factor, cudaStream_t stream) {
-    using S = Shape<NT, GROUP>;
+int64_t split_bytes(int64_t rows, int I, int dtype) {
+    return rows * I * (dtype == EP_DTYPE_FP16 ? kParts<__half> : kParts<__nv_bfloat16>);
+}
+
+template <typename T, int NR, int GROUP>
+cudaError_t launch_shape(const W4Args& a, const unsigned char* x, const float2* stats, cudaStream_t stream) {
+    using S = Shape<T, NR, GROUP>;
     static int known[64];
+    constexpr int smem = S::kShared;
     Plan p{};
     int sms = 0;
-    cudaError_t err = prepare_kernel(expert_w4_kernel<T, NT, GROUP, ZEROS>, S::kShared, known, &sms);
+    cudaError_t err = prepare_kernel(expert_w4_kernel<T, NR, GROUP>, smem, known, &sms);
     if (err != cudaSuccess) return err;
-    const int cols = a.swiglu ? a.O / 2 : a.O, cta_cols = a.swiglu ? kConsumers / 2 : kConsumers;
+    const int cols = a.swiglu ? a.O / 2 : a.O, cta_cols = kGroupsOfWarps * (a.swiglu ? kTileRows / 2 : kTileRows);
     p.tiles = (cols + cta_cols - 1) / cta_cols;
     while (((a.E - 1) >> p.table_shift) + 1 > kTable) ++p.table_shift;
     p.stages = (a.I + kIn - 1) / kIn;
     p.groups = a.I / GROUP;
-    p.factor = factor;
+    p.stats = reinterpret_cast<const float*>(stats);
     p.slots = sms;
     // items at most; with fewer than half the CTAs' number, clusters share them
-    const int64_t most = (static_cast<int64_t>(a.rows) / (8 * NT) + (a.rows < a.E ? a.rows : a.E)) * p.tiles;
+    const int64_t most = (static_cast<int64_t>(a.rows) / NR + (a.rows < a.E ? a.rows : a.E)) * p.tiles;
     p.split = 1;
     while (p.split < kMostSplit && 2 * p.split <= p.stages && most * 2 * p.split <= p.slots) p.split *= 2;
     const int64_t clusters = most < p.slots / p.split ? most : p.slots / p.split;
     p.slots = static_cast<int>(clusters) * p.split;
     CUtensorMap weight_map, x_map;
-    err = a.swiglu ? byte_map(&weight_map, a.w, a.I / 2, cols, 2, a.E, 16, 2) : byte_map(&weight_map, a.w, a.I / 2, a.O, 1, a.E, 128, 1);
-    if (err == cudaSuccess) err = byte_map(&x_map, x, static_cast<int64_t>(a.I) * 2, a.rows, 1, 1, 8, 1);
+    err = a.swiglu ? byte_map(&weight_map, a.w, a.I / 2, cols, 2, a.E, 16, 2) : byte_map(&weight_map, a.w, a.I / 2, a.O, 1, a.E, kTileRows, 1);
+    if (err == cudaSuccess) err = byte_map(&x_map, x, a.I, a.rows, kParts<T>, 1, 8, kParts<T>);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.slots);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::kShared;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -635,37 +778,41 @@ cudaError_t launch_shape(const W4Args& a, const uint4* x, const float* factor, c
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, expert_w4_kernel<T, NT, GROUP, ZEROS>, a, p, weight_map, x_map);
+    return cudaLaunchKernelEx(&cfg, expert_w4_kernel<T, NR, GROUP>, a, p, weight_map, x_map);
 }
 
 template <typename T, int GROUP>
-cudaError_t launch_group(const W4Args& a, void* workspace, cudaStream_t stream) {
-    uint4* x = static_cast<uint4*>(workspace);
-    float* factor = reinterpret_cast<float*>(x + static_cast<int64_t>(a.rows) * (a.I / 8));
-    const cudaError_t err = launch_dependent(order_kernel<T, GROUP>, dim3(a.rows < 65536 ? a.rows : 65536), dim3(kOrderThreads), 0,
-                                             stream, a, x, factor);
+cudaError_t launch_group(const W4Args& a, void* workspace, int dtype, cudaStream_t stream) {
+    float2* stats = static_cast<float2*>(workspace);
+    const int64_t stats_bytes = (static_cast<int64_t>(a.rows) * (a.I / GROUP) * 8 + 15) / 16 * 16;
+    unsigned char* x = static_cast<unsigned char*>(workspace) + stats_bytes;
+    const int64_t blocks = (static_cast<int64_t>(a.rows) * (a.I / 8) + kSplitThreads - 1) / kSplitThreads;
+    const cudaError_t err = launch_dependent(split_kernel<T, GROUP>, dim3(static_cast<unsigned>(blocks < 8192 ? blocks : 8192)),
+                                             dim3(kSplitThreads), 0, stream, a, x, stats);
     if (err != cudaSuccess) return err;
     // rows of an item: 8, or 16 where experts have more than 4 rows on average (a second pass over a tile costs more)
     const int used = a.rows < a.E ? a.rows : a.E, mean = (a.rows + used - 1) / used;
-    if (mean <= 4 || a.rows <= 8)
-        return a.zeros ? launch_shape<T, 1, GROUP, true>(a, x, factor, stream) : launch_shape<T, 1, GROUP, false>(a, x, factor, stream);
-    return a.zeros ? launch_shape<T, 2, GROUP, true>(a, x, factor, stream) : launch_shape<T, 2, GROUP, false>(a, x, factor, stream);
+    if constexpr (kParts<T> == 2)
+        if (mean <= 4 || a.rows <= 8) return launch_shape<T, 8, GROUP>(a, x, stats, stream);
+    return launch_shape<T, 16, GROUP>(a, x, stats, stream);
 }
 
 template <typename T>
-cudaError_t launch_type(const W4Args& a, void* workspace, cudaStream_t stream) {
-    return a.group == 32   ? launch_group<T, 32>(a, workspace, stream)
-           : a.group == 64 ? launch_group<T, 64>(a, workspace, stream)
-                           : launch_group<T, 128>(a, workspace, stream);
+cudaError_t launch_type(const W4Args& a, void* workspace, int dtype, cudaStream_t stream) {
+    return a.group == 32   ? launch_group<T, 32>(a, workspace, dtype, stream)
+           : a.group == 64 ? launch_group<T, 64>(a, workspace, dtype, stream)
+                           : launch_group<T, 128>(a, workspace, dtype, stream);
 }
 
 }  // namespace
 
-// x in its order, and the power of two of each row.
-int64_t expert_w4_workspace(int64_t rows, int I) { return rows * I * 2 + rows * 4; }
+int64_t expert_w4_workspace(int64_t rows, int I, int group, int dtype) {
+    return (rows * (I / group) * 8 + 15) / 16 * 16 + split_bytes(rows, I, dtype);
+}
 
 cudaError_t launch_expert_w4(const W4Args& a, void* workspace, int dtype, cudaStream_t stream) {
-    return dtype == EP_DTYPE_BF16 ? launch_type<__nv_bfloat16>(a, workspace, stream) : launch_type<__half>(a, workspace, stream);
+    return dtype == EP_DTYPE_BF16 ? launch_type<__nv_bfloat16>(a, workspace, dtype, stream)
+                                  : launch_type<__half>(a, workspace, dtype, stream);
 }
 
 }  // namespace ep

@@ -108,6 +108,6 @@ struct W4Args {
     void* y;
 };
 cudaError_t launch_expert_w4(const W4Args& a, void* workspace, int dtype, cudaStream_t stream);
-int64_t expert_w4_workspace(int64_t rows, int I);
+int64_t expert_w4_workspace(int64_t rows, int I, int group, int dtype);
 
 }  // namespace ep

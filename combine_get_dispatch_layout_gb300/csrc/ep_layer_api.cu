@@ -240,7 +240,7 @@ int64_t ep_expert_w4_workspace(int64_t rows, int I, int group_size, int dtype) {
     if (rows < 0 || rows >= (int64_t{1} << 31) || (group_size != 32 && group_size != 64 && group_size != 128) ||
         I < group_size || I % group_size != 0 || !half_type(dtype))
         return -1;
-    return ep::expert_w4_workspace(rows, I);
+    return ep::expert_w4_workspace(rows, I, group_size, dtype);
 }
 
 ep_status_t ep_expert_w4(const void* x, int64_t rows, int I, const uint8_t* weights, const void* scales,
@@ -260,7 +260,7 @@ ep_status_t ep_expert_w4(const void* x, int64_t rows, int I, const uint8_t* weig
     if (!x || !weights || !scales || !y || !aligned(x, 16) || !aligned(weights, 16) || !aligned(scales, 2) ||
         !aligned(y, 2) || !aligned(expert_offsets, 4) || !aligned(expert_counts, 4))
         return EP_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < ep::expert_w4_workspace(rows, I))
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < ep::expert_w4_workspace(rows, I, group, config->dtype))
         return EP_ERR_INVALID_ARG;
     ep::W4Args a{};
     a.x = x;

@@ -82,6 +82,14 @@ def _dtype(t, known, what: str) -> int:
     return d
 
 
+# A decode step makes these calls for a few microseconds of GPU work each, so the checks are kept to a few
+# attribute reads a tensor, and the current stream is read without building a Stream object (2.8 us).
+def _raw_stream(stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _stream(stream)
+
+
 def _on_gpu(t, what: str) -> int:
     """Address of a tensor whose strides the call is given."""
     if not t.is_cuda and t.numel() > 0 and not t.is_pinned():
@@ -93,23 +101,24 @@ def _dense(t, dtype, shape, what: str):
     """Address of a contiguous tensor of this type and shape (None stays None)."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    return _on_gpu(t, what)
+    return t.data_ptr() if t.is_cuda else _on_gpu(t, what)
 
 
 def _rows(t, dtype, shape, what: str) -> tuple[int, int]:
     """(address, elements from row to row) of a tensor whose rows are dense."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    strides = t.stride()
     step = 1
-    for size, stride in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and stride != step:
+    for k in range(len(shape) - 1, 0, -1):
+        if strides[k] != step and shape[k] != 1:
             raise ValueError(f"{what}: all but the first dimension must be contiguous")
-        step *= size
-    return _on_gpu(t, what), t.stride(0) if shape[0] > 1 else -(-step // 8) * 8
+        step *= shape[k]
+    return t.data_ptr() if t.is_cuda else _on_gpu(t, what), strides[0] if shape[0] > 1 else -(-step // 8) * 8
 
 
 def ep_router_topk(logits, topk_idx, topk_weights, bias=None, score: int = EP_SCORE_SOFTMAX, renormalize: bool = True,
@@ -123,7 +132,7 @@ def ep_router_topk(logits, topk_idx, topk_weights, bias=None, score: int = EP_SC
     p, ld = _rows(logits, logits.dtype, (T, E), "logits")
     _check(lib().ep_router_topk(p, ld, _dense(bias, torch.float32, (E,), "bias"), T, E, K, cfg,
                                 _dense(topk_idx, torch.int64, (T, K), "topk_idx"),
-                                _dense(topk_weights, torch.float32, (T, K), "topk_weights"), _stream(stream)),
+                                _dense(topk_weights, torch.float32, (T, K), "topk_weights"), _raw_stream(stream)),
            "ep_router_topk")
 
 
@@ -137,15 +146,16 @@ def ep_router_topk_backward(logits, topk_idx, grad_weights, grad_logits, score: 
     gp, gld = _rows(grad_logits, logits.dtype, (T, E), "grad_logits")
     _check(lib().ep_router_topk_backward(p, ld, _dense(topk_idx, torch.int64, (T, K), "topk_idx"),
                                          _dense(grad_weights, torch.float32, (T, K), "grad_weights"), T, E, K, cfg,
-                                         gp, gld, _stream(stream)),
+                                         gp, gld, _raw_stream(stream)),
            "ep_router_topk_backward")
 
 
 def _cache(k_cache, v_cache, k_scale: float, v_scale: float, heads: int, dim: int) -> Cache:
     """ep_cache_t of two [pages, page_size, heads, dim] tensors, in any order of the first three in memory."""
-    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or k_cache.dim() != 4:
+    shape = k_cache.shape
+    if shape != v_cache.shape or k_cache.dtype is not v_cache.dtype or len(shape) != 4:
         raise ValueError("k_cache and v_cache must be [pages, page_size, kv_heads, head_dim] of one type")
-    pages, page, h, d = k_cache.shape
+    pages, page, h, d = shape
     if h != heads or d != dim:
         raise ValueError(f"cache rows are [{h}, {d}], the call's are [{heads}, {dim}]")
     ks, vs = k_cache.stride(), v_cache.stride()
@@ -178,7 +188,7 @@ def ep_kv_append(q, k, v, positions, slots, cos_sin, q_out, k_cache, v_cache, in
                               _dense(slots, torch.int64, (T,), "slots"),
                               _dense(cos_sin, torch.float32, (most, rot), "cos_sin"), T, cfg, qop,
                               _on_gpu(k_cache, "k_cache"), _on_gpu(v_cache, "v_cache"), cache,
-                              _dense(device_error, torch.int32, (1,), "device_error"), _stream(stream)),
+                              _dense(device_error, torch.int32, (1,), "device_error"), _raw_stream(stream)),
            "ep_kv_append")
 
 
@@ -212,7 +222,7 @@ def ep_paged_attention(q, k_cache, v_cache, block_table, seq_lens, out, workspac
     _check(lib().ep_paged_attention(qp, _on_gpu(k_cache, "k_cache"), _on_gpu(v_cache, "v_cache"), cache, tp,
                                     _dense(seq_lens, torch.int32, (B,), "seq_lens"), B, cfg, op,
                                     _dense(lse, torch.float32, (B, h), "lse"), _on_gpu(workspace, "workspace"),
-                                    workspace.numel() * workspace.element_size(), _stream(stream)),
+                                    workspace.numel() * workspace.element_size(), _raw_stream(stream)),
            "ep_paged_attention")
 
 
@@ -245,7 +255,7 @@ def ep_expert_w4(x, weights, scales, y, expert_offsets=None, expert_counts=None,
                               _dense(expert_offsets, torch.int32, (E + 1,), "expert_offsets"),
                               _dense(expert_counts, torch.int32, (E,), "expert_counts"), E, O, cfg, yp,
                               _on_gpu(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-                              _stream(stream)),
+                              _raw_stream(stream)),
            "ep_expert_w4")
 
 

@@ -1,131 +1,205 @@
 // Append of keys and values to a paged cache, the position's rotation applied
 // to queries and keys on the way.
+//
+// Each value is read and written once, so memory bounds it. One block a token;
+// a thread keeps its place in a head, and with it the place's cosines and sines
+// in registers, and walks over the token's heads, two ahead of the stores. A
+// pair is always one thread's, so queries may be turned in place. What counts is
+// how many tokens are on the way at once, for each waits for its position, then
+// its angles, then its values: 8 blocks of 128 threads a core (64 registers) take
+// 57 us for 8192 tokens of 64 + 8 + 8 heads of 128 (5.7 TB/s), 2 blocks of 256
+// threads that load four heads ahead 103 us.
+#include <type_traits>
+
 #include "ep_layer.cuh"
 
 namespace ep {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kAhead = 2;   // heads that a thread has loaded before it stores the first
 
-// Eight fp32 values as one row piece of the destination type.
-template <typename C>
-__device__ __forceinline__ void store8(C* dst, const float (&f)[8]) {
-    Vec8<C> o;
+// How a head is cut up.
+enum Mode {
+    kHalves8,     // pairs (i, i + rot/2), rot/2 a multiple of 8: 8 values of either half together
+    kHalves4,     // the same with a multiple of 4
+    kNeighbours,  // pairs (2i, 2i + 1), rot a multiple of 8: 8 values
+    kSingle       // any other rotary_dim: one pair, or one value behind them
+};
+
+// W neighbouring values, and their places in memory.
+template <int W>
+using Raw = std::conditional_t<W == 8, uint4, uint2>;
+
+template <typename T, int W>
+__device__ __forceinline__ void unpack(const Raw<W>& raw, float (&f)[W]) {
+    const T* v = reinterpret_cast<const T*>(&raw);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o.v[i] = from_float<C>(f[i]);
-    *reinterpret_cast<uint4*>(dst) = o.raw;
+    for (int i = 0; i < W; ++i) f[i] = to_float(v[i]);
+}
+// fp32 values as a piece of a row of the destination type, times inv for e4m3.
+template <typename C, int W>
+__device__ __forceinline__ void store(C* dst, const float (&f)[W], float inv) {
+    if constexpr (std::is_same_v<C, __nv_fp8_e4m3>) {
+        uint32_t w[W / 4];
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i)
+            w[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i] * inv, f[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3) |
+                   static_cast<uint32_t>(
+                       __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2] * inv, f[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3))
+                       << 16;
+        if constexpr (W == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t*>(dst) = w[0];
+    } else {
+        Raw<W> o;
+#pragma unroll
+        for (int i = 0; i < W; ++i) reinterpret_cast<C*>(&o)[i] = from_float<C>(f[i]);
+        *reinterpret_cast<Raw<W>*>(dst) = o;
+    }
+}
+template <typename C>
+__device__ __forceinline__ void store1(C* dst, float f, float) {
+    *dst = from_float<C>(f);
 }
 template <>
-__device__ __forceinline__ void store8(__nv_fp8_e4m3* dst, const float (&f)[8]) {
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i], f[4 * i + 1]), __NV_SATFINITE, __NV_E4M3) |
-               static_cast<uint32_t>(
-                   __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2], f[4 * i + 3]), __NV_SATFINITE, __NV_E4M3))
-                   << 16;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+__device__ __forceinline__ void store1(__nv_fp8_e4m3* dst, float f, float inv) {
+    dst->__x = __nv_cvt_float_to_fp8(f * inv, __NV_SATFINITE, __NV_E4M3);
 }
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* src, float (&f)[8]) {
-    Vec8<T> r;
-    r.raw = *reinterpret_cast<const uint4*>(src);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = to_float(r.v[i]);
-}
-
-// Elements c .. c + 7 of a head, turned. table: the position's cosines, then
-// sines. Element i of the turned part belongs to angle i mod half (halves
-// paired) or i / 2 (neighbours paired); the first of a pair takes a cos - b
-// sin, the second b cos + a sin.
-template <typename T>
-__device__ __forceinline__ void turned8(const T* head, int c, const float* table, int rot, int interleaved,
-                                        float (&f)[8]) {
-    load8(head + c, f);
-    if (c >= rot) return;
-    const int half = rot / 2;
-    float own[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) own[i] = f[i];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int d = c + i;
-        if (d >= rot) break;
-        if (interleaved) {
-            const float cs = table[d / 2], sn = table[half + d / 2];
-            f[i] = (i & 1) ? own[i] * cs + own[i ^ 1] * sn : own[i] * cs - own[i ^ 1] * sn;
-        } else {
-            const bool first = d < half;
-            const float other = to_float(head[first ? d + half : d - half]);
-            const int g = first ? d : d - half;
-            f[i] = first ? own[i] * table[g] - other * table[half + g] : own[i] * table[g] + other * table[half + g];
-        }
-    }
-}
-
-// One block per token: its threads share out the eight-element pieces of the
-// token's query, key and value heads. (q_out may be q: a block's loads of a
-// head end before its stores only within a thread, so queries are turned
-// through shared memory.)
-template <typename T, typename C>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
-    extern __shared__ char smem[];
+template <typename T, typename C, Mode MODE>
+__global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(AppendArgs a) {
     dependent_entry();
     const int64_t t = blockIdx.x;
-    const int D = a.head_dim, per_head = D / 8;
-    const int64_t pos = a.rotary_dim ? a.positions[t] : 0, slot = a.slots[t];
-    const bool pos_ok = pos >= 0 && (a.rotary_dim == 0 || pos < a.max_position);
+    const int D = a.head_dim, rot = a.rotary_dim, half = rot / 2, tid = threadIdx.x;
+    const int64_t pos = rot ? a.positions[t] : 0, slot = a.slots[t];
+    const bool pos_ok = pos >= 0 && (rot == 0 || pos < a.max_position);
     const bool slot_ok = slot >= 0 && slot < a.num_slots;
-    if (threadIdx.x == 0 && a.error && (!pos_ok || (!slot_ok && slot != -1))) *a.error = EP_ERR_INVALID_ARG;
-    const float* table = a.cos_sin + (pos_ok ? pos : 0) * a.rotary_dim;
+    if (tid == 0 && a.error && (!pos_ok || (!slot_ok && slot != -1))) *a.error = EP_ERR_INVALID_ARG;
+    const float* table = a.cos_sin + (pos_ok ? pos : 0) * rot;
+    const int64_t page = slot_ok ? slot / a.page_size : 0, place = slot_ok ? slot - page * a.page_size : 0;
+    const bool cached = pos_ok && slot_ok;
+    C* const keys = static_cast<C*>(a.k_cache) + page * a.k_page + place * a.k_slot;
+    C* const values = static_cast<C*>(a.v_cache) + page * a.v_page + place * a.v_slot;
+    const T* const q = static_cast<const T*>(a.q) + t * a.q_ld;
+    const T* const k = static_cast<const T*>(a.k) + t * a.k_ld;
+    const T* const v = static_cast<const T*>(a.v) + t * a.v_ld;
+    T* const q_out = static_cast<T*>(a.q_out) + t * a.q_out_ld;
 
-    T* heads = reinterpret_cast<T*>(smem);
-    const T* q = static_cast<const T*>(a.q) + t * a.q_ld;
-    for (int i = threadIdx.x; i < a.num_heads * per_head; i += kThreads)
-        reinterpret_cast<uint4*>(heads)[i] = reinterpret_cast<const uint4*>(q)[i];
-    __syncthreads();
-    T* q_out = static_cast<T*>(a.q_out) + t * a.q_out_ld;
-    for (int i = threadIdx.x; i < a.num_heads * per_head; i += kThreads) {
-        float f[8] = {};
-        if (pos_ok) turned8(heads + (i / per_head) * D, i % per_head * 8, table, a.rotary_dim, a.interleaved, f);
-        store8(q_out + i * 8, f);
-    }
-    if (!pos_ok || !slot_ok) return;
-    const int64_t page = slot / a.page_size, place = slot % a.page_size;
-    for (int i = threadIdx.x; i < 2 * a.num_kv_heads * per_head; i += kThreads) {
-        const bool key = i < a.num_kv_heads * per_head;
-        const int j = key ? i : i - a.num_kv_heads * per_head;
-        const int h = j / per_head, c = j % per_head * 8;
-        float f[8];
-        C* dst;
-        float inv;
-        if (key) {
-            turned8(static_cast<const T*>(a.k) + t * a.k_ld + h * D, c, table, a.rotary_dim, a.interleaved, f);
-            dst = static_cast<C*>(a.k_cache) + page * a.k_page + place * a.k_slot + h * a.k_head + c;
-            inv = a.k_inv_scale;
-        } else {
-            load8(static_cast<const T*>(a.v) + t * a.v_ld + h * D + c, f);
-            dst = static_cast<C*>(a.v_cache) + page * a.v_page + place * a.v_slot + h * a.v_head + c;
-            inv = a.v_inv_scale;
+    const int heads = a.num_heads + (cached ? a.num_kv_heads : 0);   // queries, then keys
+    if constexpr (MODE == kSingle) {
+        const int per_head = half + D - rot;
+        for (int i = tid; i < heads * per_head; i += kThreads) {
+            const int h = i / per_head, c = i % per_head;
+            const bool key = h >= a.num_heads;
+            const T* from = key ? k + (h - a.num_heads) * D : q + h * D;
+            int first = c, second = -1;
+            float x, y = 0.0f;
+            if (c < half) {
+                first = a.interleaved ? 2 * c : c;
+                second = a.interleaved ? 2 * c + 1 : c + half;
+                const float p = to_float(from[first]), r = to_float(from[second]), cs = table[c], sn = table[half + c];
+                x = p * cs - r * sn;
+                y = r * cs + p * sn;
+            } else {
+                first = c + half;
+                x = to_float(from[first]);
+            }
+            if (key) {
+                C* to = keys + (h - a.num_heads) * a.k_head;
+                store1(to + first, x, a.k_inv_scale);
+                if (second >= 0) store1(to + second, y, a.k_inv_scale);
+            } else {
+                q_out[h * D + first] = from_float<T>(pos_ok ? x : 0.0f);
+                if (second >= 0) q_out[h * D + second] = from_float<T>(pos_ok ? y : 0.0f);
+            }
         }
-        if constexpr (sizeof(C) == 1) {
+    } else {
+        constexpr bool kHalves = MODE != kNeighbours;
+        constexpr int W = MODE == kHalves4 ? 4 : 8, kAngles = kHalves ? W : 4;
+        const int turned = half / kAngles, per_head = turned + (D - rot) / W;
+        const int step = kThreads / per_head, c = tid % per_head, h0 = tid / per_head;
+        if (h0 < step) {
+            const bool turn = c < turned, two = kHalves && turn;
+            const int first = turn ? c * W : rot + (c - turned) * W;
+            float cs[kAngles], sn[kAngles];
+            if (turn) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[k] *= inv;
+                for (int i = 0; i < kAngles; ++i) cs[i] = table[c * kAngles + i], sn[i] = table[half + c * kAngles + i];
+            }
+            for (int base = h0; base < heads; base += kAhead * step) {
+                Raw<W> one[kAhead], other[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int h = base + u * step;
+                    if (h >= heads) break;
+                    const T* from = (h >= a.num_heads ? k + (h - a.num_heads) * D : q + h * D) + first;
+                    one[u] = *reinterpret_cast<const Raw<W>*>(from);
+                    if (two) other[u] = *reinterpret_cast<const Raw<W>*>(from + half);
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int h = base + u * step;
+                    if (h >= heads) break;
+                    float x[W], y[W], p[W], r[W];
+                    unpack<T, W>(one[u], p);
+                    if (two) {
+                        unpack<T, W>(other[u], r);
+#pragma unroll
+                        for (int i = 0; i < W; ++i) {
+                            x[i] = p[i] * cs[i % kAngles] - r[i] * sn[i % kAngles];
+                            y[i] = r[i] * cs[i % kAngles] + p[i] * sn[i % kAngles];
+                        }
+                    } else if (turn) {   // kNeighbours
+#pragma unroll
+                        for (int i = 0; i < W; i += 2) {
+                            x[i] = p[i] * cs[i / 2] - p[i + 1] * sn[i / 2];
+                            x[i + 1] = p[i + 1] * cs[i / 2] + p[i] * sn[i / 2];
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < W; ++i) x[i] = p[i];
+                    }
+                    if (h >= a.num_heads) {
+                        C* to = keys + (h - a.num_heads) * a.k_head + first;
+                        store<C, W>(to, x, a.k_inv_scale);
+                        if (two) store<C, W>(to + half, y, a.k_inv_scale);
+                    } else {
+                        if (!pos_ok) {
+#pragma unroll
+                            for (int i = 0; i < W; ++i) x[i] = y[i] = 0.0f;
+                        }
+                        store<T, W>(q_out + h * D + first, x, 1.0f);
+                        if (two) store<T, W>(q_out + h * D + first + half, y, 1.0f);
+                    }
+                }
+            }
         }
-        store8(dst, f);
+    }
+    if (!cached) return;
+    const int per_head = D / 8;
+    for (int i = tid; i < a.num_kv_heads * per_head; i += kThreads) {
+        const int h = i / per_head, c = i % per_head * 8;
+        const uint4 raw = *reinterpret_cast<const uint4*>(v + h * D + c);
+        C* to = values + h * a.v_head + c;
+        if constexpr (sizeof(C) == 2) {
+            *reinterpret_cast<uint4*>(to) = raw;
+        } else {
+            float f[8];
+            unpack<T, 8>(raw, f);
+            store<C, 8>(to, f, a.v_inv_scale);
+        }
     }
 }
 
 template <typename T, typename C>
 cudaError_t launch(const AppendArgs& a, cudaStream_t stream) {
-    const size_t smem = static_cast<size_t>(a.num_heads) * a.head_dim * sizeof(T);
-    if (smem > 48 * 1024) {
-        const cudaError_t err = cudaFuncSetAttribute(
-            kv_append_kernel<T, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (err != cudaSuccess) return err;
-    }
-    return launch_dependent(kv_append_kernel<T, C>, dim3(a.T), dim3(kThreads), smem, stream, a);
+    // a head is cut into at most kThreads pieces
+    const int rot = a.rotary_dim;
+    auto* kernel = a.interleaved   ? (rot % 8 == 0 ? kv_append_kernel<T, C, kNeighbours> : kv_append_kernel<T, C, kSingle>)
+                   : rot % 16 == 0 ? kv_append_kernel<T, C, kHalves8>
+                   : rot % 8 == 0 && a.head_dim <= 4 * kThreads ? kv_append_kernel<T, C, kHalves4>
+                                                                : kv_append_kernel<T, C, kSingle>;
+    return launch_dependent(kernel, dim3(a.T), dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace

@@ -53,6 +53,7 @@ struct RouterBackwardArgs {
     const void* logits;
     int64_t ld;
     const int64_t* idx;
+    int64_t idx_ld;
     const float* grad_w;
     int T, E, K;
     int score, renormalize;

@@ -78,12 +78,12 @@ ep_status_t ep_router_topk(const void* logits, int64_t logits_ld, const float* b
     return status_of(ep::launch_router_topk(a, config->logits_dtype, static_cast<cudaStream_t>(stream)));
 }
 
-ep_status_t ep_router_topk_backward(const void* logits, int64_t logits_ld, const int64_t* topk_idx,
+ep_status_t ep_router_topk_backward(const void* logits, int64_t logits_ld, const int64_t* topk_idx, int64_t topk_ld,
                                     const float* grad_weights, int T, int E, int K, const ep_router_config_t* config,
                                     void* grad_logits, int64_t grad_ld, void* stream) {
     ApiRange range("ep_router_topk_backward");
     if (!router_config_ok(config) || T < 0 || E < 1 || E > EP_MAX_EXPERTS || K < 1 || K > EP_MAX_TOPK ||
-        logits_ld < E || grad_ld < E)
+        logits_ld < E || grad_ld < E || topk_ld < K)
         return EP_ERR_INVALID_ARG;
     if (T == 0) return EP_OK;
     const size_t bytes = type_bytes(config->logits_dtype);
@@ -94,6 +94,7 @@ ep_status_t ep_router_topk_backward(const void* logits, int64_t logits_ld, const
     a.logits = logits;
     a.ld = logits_ld;
     a.idx = topk_idx;
+    a.idx_ld = topk_ld;
     a.grad_w = grad_weights;
     a.T = T;
     a.E = E;

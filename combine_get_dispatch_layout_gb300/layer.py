@@ -60,7 +60,7 @@ def declare(L) -> None:
     """Argument types of this module's entry points on a loaded library."""
     ref = ctypes.POINTER
     L.ep_router_topk.argtypes = [_P, _i64, _P, _i32, _i32, _i32, ref(RouterConfig), _P, _P, _P]
-    L.ep_router_topk_backward.argtypes = [_P, _i64, _P, _P, _i32, _i32, _i32, ref(RouterConfig), _P, _i64, _P]
+    L.ep_router_topk_backward.argtypes = [_P, _i64, _P, _i64, _P, _i32, _i32, _i32, ref(RouterConfig), _P, _i64, _P]
     L.ep_kv_append.argtypes = [_P, _P, _P, _P, _P, _P, _i32, ref(AppendConfig), _P, _P, _P, ref(Cache), _P, _P]
     L.ep_paged_attention.argtypes = [_P, _P, _P, ref(Cache), _P, _P, _i32, ref(AttentionConfig), _P, _P, _P, _i64, _P]
     L.ep_paged_attention_workspace.argtypes = [_i32, _i32, _i32, _i32]
@@ -144,7 +144,8 @@ def ep_router_topk_backward(logits, topk_idx, grad_weights, grad_logits, score: 
     cfg = RouterConfig(_dtype(logits, _LOGITS, "logits"), score, bool(renormalize), scale, 1, 1, 1)
     p, ld = _rows(logits, logits.dtype, (T, E), "logits")
     gp, gld = _rows(grad_logits, logits.dtype, (T, E), "grad_logits")
-    _check(lib().ep_router_topk_backward(p, ld, _dense(topk_idx, torch.int64, (T, K), "topk_idx"),
+    ip, ild = _rows(topk_idx, torch.int64, (T, K), "topk_idx")
+    _check(lib().ep_router_topk_backward(p, ld, ip, ild,
                                          _dense(grad_weights, torch.float32, (T, K), "grad_weights"), T, E, K, cfg,
                                          gp, gld, _raw_stream(stream)),
            "ep_router_topk_backward")

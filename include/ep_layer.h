@@ -79,8 +79,9 @@ EP_API ep_status_t ep_router_topk(const void* logits, int64_t logits_ld, const f
 
 /*
  * ep_router_topk_backward -- grad_logits of a loss with gradient grad_weights
- * [T, K] (fp32) at topk_weights, for the experts in topk_idx (the selection
- * itself is not differentiated; an id outside [0, E) contributes nothing).
+ * [T, K] (fp32) at topk_weights, for the experts in topk_idx ([T, K], rows
+ * topk_ld >= K apart: a slice of a full sort serves). (The selection
+ * itself is not differentiated; an id outside [0, E) contributes nothing.)
  * With g = scale * grad_weights and the scores p of the same logits:
  *   softmax                   p_j ([j chosen] g_j - sum_k g_k p_k), all j
  *   softmax, renormalised     q_j (g_j - sum_k g_k q_k), chosen j, else 0
@@ -92,7 +93,7 @@ EP_API ep_status_t ep_router_topk(const void* logits, int64_t logits_ld, const f
  * and scale.
  */
 EP_API ep_status_t ep_router_topk_backward(const void* logits, int64_t logits_ld, const int64_t* topk_idx,
-                                           const float* grad_weights, int T, int E, int K,
+                                           int64_t topk_ld, const float* grad_weights, int T, int E, int K,
                                            const ep_router_config_t* config, void* grad_logits, int64_t grad_ld,
                                            void* stream);
 

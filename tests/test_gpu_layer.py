@@ -268,6 +268,33 @@ def test_router_backward_repeated_and_invalid_experts(ep):
         within(grad, want, 1e-5)
 
 
+def test_router_backward_takes_a_slice_of_a_sort(ep):
+    logits, g = randn(gen(16), 20, 64), randn(gen(17), 20, 6)
+    order = logits.sort(dim=1, descending=True, stable=True).indices
+    grad = torch.full_like(logits, math.nan)
+    ep.ep_router_topk_backward(logits, order[:, :6], g, grad, renormalize=False)
+    within(grad, backward_reference(logits, order[:, :6].cpu(), g, 0, False, 1.0), 1e-5)
+
+
+@pytest.mark.parametrize("E,groups", [(60, 4), (96, 3), (1024, 8), (320, 10), (512, 16), (40, 5), (64, 2)])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_router_group_sizes(ep, E, groups, group_top):
+    """Groups that are and are not powers of two, rows in registers and in shared memory. A row's logits are all different,
+    8 / E apart: no two scores are within rounding of each other."""
+    g = gen(E)
+    logits = torch.stack([(torch.randperm(E, generator=g) - E // 2) * (8.0 / E) for _ in range(23)]).cuda()
+    logits[3, ::2] = -math.inf
+    want_idx, want = router_reference(logits, 4, 1, True, 1.0, groups=groups, keep=2, group_top=group_top)
+    idx, w = run_router(ep, logits, 4, score=1, num_groups=groups, topk_groups=2, group_top=group_top)
+    if group_top == 2:   # the sums of two sigmoids of different groups may be that near
+        top2 = torch.sigmoid(logits.double()).view(23, groups, -1).topk(2, dim=2).values.sum(2)
+        far = (top2.sort(1).values.diff(dim=1).min(1).values > 1e-5).cpu()
+        assert int(far.sum()) > 4
+        idx, w, want_idx, want = idx[far], w[far], want_idx[far], want[far]
+    assert torch.equal(idx, want_idx)
+    within(w, want, router_tolerance(logits, want))
+
+
 def test_router_backward_strided_rows(ep):
     wide = randn(gen(14), 12, 77)
     out = torch.full((12, 90), 5.0, device="cuda")

@@ -53,7 +53,7 @@ def router(ep, **kw):
     L = ep.lib()
     return (L.ep_router_topk(a["logits"], a["ld"], a["bias"], a["T"], a["E"], a["K"], cfg if a["cfg"] else None,
                              a["idx"], a["w"], None),
-            L.ep_router_topk_backward(a["logits"], a["ld"], a["idx"], a["w"], a["T"], a["E"], a["K"],
+            L.ep_router_topk_backward(a["logits"], a["ld"], a["idx"], 2, a["w"], a["T"], a["E"], a["K"],
                                       cfg if a["cfg"] else None, a["logits"], a["ld"], None))
 
 
@@ -69,6 +69,11 @@ def test_router_rejects(ep, kw):
                                 dict(groups=4, keep=0), dict(groups=4, keep=5), dict(top=3), dict(top=-1)])
 def test_router_rejects_groups_and_bias(ep, kw):
     assert router(ep, **kw)[0] == INVALID
+
+
+def test_router_backward_rejects_short_index_rows(ep):
+    cfg = ep.layer.RouterConfig(ep.EP_DTYPE_FP32, 0, 1, 1.0, 1, 1, 1)
+    assert ep.lib().ep_router_topk_backward(16, 8, 16, 1, 16, 4, 8, 2, cfg, 16, 8, None) == INVALID
 
 
 def test_empty_router_needs_nothing(ep):

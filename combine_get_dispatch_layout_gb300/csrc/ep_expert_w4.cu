@@ -118,12 +118,15 @@ __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
 }
 // Every wait ends: after far more tries than any load takes, `dead` is set, the CTA runs through the rest
 // without waiting, and its outputs are NaN.
-__device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+__device__ __noinline__ void barrier_wait_long(uint32_t bar, uint32_t parity, volatile int* dead) {
     for (int i = 0; i < (1 << 22); ++i) {
         if (barrier_try(bar, parity)) return;
         if ((i & 1023) == 1023 && *dead) return;
     }
     *dead = 1;
+}
+__device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+    if (!barrier_try(bar, parity)) barrier_wait_long(bar, parity, dead);
 }
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
     asm volatile(
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(W4Args a, unsigned
     }
 }
 
-template <typename T, int NR, int GROUP>
+template <typename T, int NR, int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_w4_kernel(W4Args a, Plan p, const __grid_constant__ CUtensorMap weight_map, const __grid_constant__ CUtensorMap x_map) {
     using S = Shape<T, NR, GROUP>;
@@ -492,23 +495,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 barrier_wait(x_full + 8 * slot, parity, dead);
                 for (int half = 0; half < 2; ++half) {
                     const uint64_t b = operand(smem_addr(inputs) + (slot * 2 + half) * S::kXBytes, kStride);
-                    // products that add to the same sums wait for each other: those of the warpgroups take turns
-                    for (int wg = 0; wg < kGroupsOfWarps; ++wg) barrier_wait(ready + 8 * (wg * 2 + half), ready_parity, dead);
-                    tmem_fence_after();
+                    for (int wg = 0; wg < kGroupsOfWarps; ++wg) {
+                        barrier_wait(ready + 8 * (wg * 2 + half), ready_parity, dead);
+                        tmem_fence_after();
+                        const uint32_t a_at = tmem + wg * 128 + half * 32;
+                        const uint32_t sums = tmem + wg * 128 + 64 + (S::kSumBuffers == 2 ? half * S::kSumCols : 0);
 #pragma unroll
-                    for (int part = 0; part < S::kProducts; ++part)
+                        for (int part = 0; part < S::kProducts; ++part)
 #pragma unroll
-                        for (int k = 0; k < GROUP / 32; ++k)
+                            for (int k = 0; k < GROUP / 32; ++k)
 #pragma unroll
-                            for (int grp = 0; grp < kGroups; ++grp)
-#pragma unroll
-                                for (int wg = 0; wg < kGroupsOfWarps; ++wg) {
+                                for (int grp = 0; grp < kGroups; ++grp) {
                                     const int step = grp * (GROUP / 32) + k;
-                                    const uint32_t a_at = tmem + wg * 128 + half * 32;
-                                    const uint32_t sums = tmem + wg * 128 + 64 + (S::kSumBuffers == 2 ? half * S::kSumCols : 0);
                                     multiply(sums + grp * S::kN, a_at + step * 8, b + step * 2 + part * (1024 / 16), kShape, part > 0 || k > 0);
                                 }
-                    for (int wg = 0; wg < kGroupsOfWarps; ++wg) multiply_done(done + 8 * (wg * 2 + half));
+                        multiply_done(done + 8 * (wg * 2 + half));
+                    }
                 }
                 ready_parity ^= 1;
                 if (++slot == kXSlots) slot = 0, parity ^= 1;
@@ -532,24 +534,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o = col = it.col + wg * kTileRows + row;
             }
             const bool real = col < cols;
-            const int64_t scale_base = static_cast<int64_t>(it.expert) * p.groups * a.O + (real ? o : 0);
-            const T* scale_at = static_cast<const T*>(a.scales) + scale_base + static_cast<int64_t>(stage0) * (kIn / GROUP) * a.O;
-            const uint8_t* zero_at = a.zeros ? a.zeros + scale_base + static_cast<int64_t>(stage0) * (kIn / GROUP) * a.O : nullptr;
+            // Scales are loaded half a stage ahead. A row past the tile's end takes another's, and a group past the inputs'
+            // end the last one's: those sums are zero, or not written.
             int grp_next = stage0 * (kIn / GROUP);
+            const int64_t scale_base = (static_cast<int64_t>(it.expert) * p.groups + grp_next) * a.O + (real ? o : 0);
+            const T* scale_at = static_cast<const T*>(a.scales) + scale_base;
+            const uint8_t* zero_at = ZEROS ? a.zeros + scale_base : nullptr;
             T scale[kGroups], scale_next[kGroups];
-            uint8_t zero[kGroups], zero_next[kGroups];
-            const auto load_scales = [&]() {   // of the next half stage
+            uint8_t zero[kGroups] = {}, zero_next[kGroups] = {};
+            const auto load_scales = [&]() {
 #pragma unroll
                 for (int i = 0; i < kGroups; ++i) {
-                    scale_next[i] = from_float<T>(0.0f);
-                    zero_next[i] = 8;
-                    if (real && grp_next < p.groups) {
-                        scale_next[i] = *scale_at;
-                        if (zero_at) zero_next[i] = *zero_at;
+                    const int64_t on = ++grp_next < p.groups ? a.O : 0;
+                    scale_next[i] = *scale_at;
+                    scale_at += on;
+                    if constexpr (ZEROS) {
+                        zero_next[i] = *zero_at;
+                        zero_at += on;
                     }
-                    ++grp_next;
-                    scale_at += a.O;
-                    if (zero_at) zero_at += a.O;
                 }
             };
             uint64_t acc2[NR / 2];   // rows 2 n, 2 n + 1
@@ -563,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr int kBlockParts = S::kSideBySide ? kParts<T> : 1;
 #pragma unroll
                 for (int i = 0; i < kGroups; ++i) {
-                    const uint64_t sc = both(to_float(scale[i])), z = both(-static_cast<float>(zero[i]));
+                    const uint64_t sc = both(to_float(scale[i])), z = both(ZEROS ? -static_cast<float>(zero[i]) : -8.0f);
 #pragma unroll
                     for (int b = 0; b < NR / 8; ++b) {   // 8 rows
                         if (b == 1 && it.rows <= 8) break;
@@ -593,13 +595,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool before = false;
             for (int stage = stage0; stage < stage1; ++stage) {
                 barrier_wait(w_full + 8 * w_slot, w_parity, dead);
-                const unsigned char* w = weights + w_slot * kWeightBytes + wg * kTileBytes + row * 128;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     uint32_t codes[32];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(w + (((4 * half + j) ^ (row & 7)) << 4));
+                        const uint4 v = *reinterpret_cast<const uint4*>(weights + w_slot * kWeightBytes + wg * kTileBytes + row * 128 + (((4 * half + j) ^ (row & 7)) << 4));
                         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -642,35 +643,40 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int n = 0; n < NR; ++n) acc[n] = __int_as_float(0x7fffffff);
             }
+            int n0 = 0, n1 = it.rows;   // the rows that this CTA writes
             if (p.split > 1) {   // (each cluster has one item at most: the ring is used up and serves the join)
                 float* const join = reinterpret_cast<float*>(weights);   // [NR][kConsumers]
                 consumers_sync();
 #pragma unroll
                 for (int n = 0; n < NR; ++n) join[n * kConsumers + tid] = acc[n];
                 cluster_sync();
-                if (rank == 0) {
-                    for (int r = 1; r < p.split; ++r) {
-                        uint32_t from;
-                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(smem_addr(join)), "r"(r));
+                n0 = NR / p.split * rank;   // (the split divides 8)
+                n1 = min(it.rows, n0 + NR / p.split);
 #pragma unroll
-                        for (int n = 0; n < NR; ++n) {
-                            float v;
-                            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(from + (n * kConsumers + tid) * 4) : "memory");
-                            acc[n] += v;
-                        }
+                for (int n = 0; n < NR; ++n) {
+                    if (n < n0 || n >= n1) continue;
+                    float v[kMostSplit];
+#pragma unroll
+                    for (int r = 0; r < kMostSplit; ++r) {
+                        v[r] = 0.0f;
+                        if (r >= p.split) continue;
+                        uint32_t from;
+                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(smem_addr(join + n * kConsumers + tid)), "r"(r));
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(from) : "memory");
                     }
+                    acc[n] = 0.0f;
+#pragma unroll
+                    for (int r = 0; r < kMostSplit; ++r) acc[n] += v[r];
                 }
                 cluster_sync();
             }
-            if (rank == 0) {
-                T* y = static_cast<T*>(a.y) + static_cast<int64_t>(it.row) * a.y_ld + col;
+            T* y = static_cast<T*>(a.y) + static_cast<int64_t>(it.row) * a.y_ld + col;
 #pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    if (n == 8 && it.rows <= 8) break;
-                    float v = acc[n];
-                    if (a.swiglu) v = v / (1.0f + expf(-v)) * __shfl_xor_sync(kFullMask, v, 16);   // gate lanes: silu(gate) * up
-                    if (n < it.rows && real && (!a.swiglu || lane < 16)) y[n * a.y_ld] = from_float<T>(v);
-                }
+            for (int n = 0; n < NR; ++n) {
+                if (n < n0 || n >= n1) continue;
+                float v = acc[n];
+                if (a.swiglu) v = v / (1.0f + expf(-v)) * __shfl_xor_sync(kFullMask, v, 16);   // gate lanes: silu(gate) * up
+                if (real && (!a.swiglu || lane < 16)) y[n * a.y_ld] = from_float<T>(v);
             }
         }
     }
@@ -739,14 +745,14 @@ int64_t split_bytes(int64_t rows, int I, int dtype) {
     return rows * I * (dtype == EP_DTYPE_FP16 ? kParts<__half> : kParts<__nv_bfloat16>);
 }
 
-template <typename T, int NR, int GROUP>
+template <typename T, int NR, int GROUP, bool ZEROS>
 cudaError_t launch_shape(const W4Args& a, const unsigned char* x, const float2* stats, cudaStream_t stream) {
     using S = Shape<T, NR, GROUP>;
     static int known[64];
     constexpr int smem = S::kShared;
     Plan p{};
     int sms = 0;
-    cudaError_t err = prepare_kernel(expert_w4_kernel<T, NR, GROUP>, smem, known, &sms);
+    cudaError_t err = prepare_kernel(expert_w4_kernel<T, NR, GROUP, ZEROS>, smem, known, &sms);
     if (err != cudaSuccess) return err;
     const int cols = a.swiglu ? a.O / 2 : a.O, cta_cols = kGroupsOfWarps * (a.swiglu ? kTileRows / 2 : kTileRows);
     p.tiles = (cols + cta_cols - 1) / cta_cols;
@@ -778,7 +784,7 @@ cudaError_t launch_shape(const W4Args& a, const unsigned char* x, const float2* 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, expert_w4_kernel<T, NR, GROUP>, a, p, weight_map, x_map);
+    return cudaLaunchKernelEx(&cfg, expert_w4_kernel<T, NR, GROUP, ZEROS>, a, p, weight_map, x_map);
 }
 
 template <typename T, int GROUP>
@@ -793,8 +799,9 @@ cudaError_t launch_group(const W4Args& a, void* workspace, int dtype, cudaStream
     // rows of an item: 8, or 16 where experts have more than 4 rows on average (a second pass over a tile costs more)
     const int used = a.rows < a.E ? a.rows : a.E, mean = (a.rows + used - 1) / used;
     if constexpr (kParts<T> == 2)
-        if (mean <= 4 || a.rows <= 8) return launch_shape<T, 8, GROUP>(a, x, stats, stream);
-    return launch_shape<T, 16, GROUP>(a, x, stats, stream);
+        if (mean <= 4 || a.rows <= 8)
+            return a.zeros ? launch_shape<T, 8, GROUP, true>(a, x, stats, stream) : launch_shape<T, 8, GROUP, false>(a, x, stats, stream);
+    return a.zeros ? launch_shape<T, 16, GROUP, true>(a, x, stats, stream) : launch_shape<T, 16, GROUP, false>(a, x, stats, stream);
 }
 
 template <typename T>

@@ -126,7 +126,6 @@ __device__ Share find_share(const AttentionArgs& a, const Plan& p) {
     return s;
 }
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 // 16 bytes to shared memory, of which the first `real` (16 or 0) are read and the rest are zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
@@ -431,10 +430,11 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
     // ---- the pass over the chunks
     float o[DP / 16][4];             // O^T: rows d, columns heads
     float top[2], sum[2], c2[2];     // of the warp's heads 2 t, 2 t + 1
-    uint32_t qf[DP / 16][2];
+    constexpr bool kQueriesAhead = !FP8 && DP <= 128;   // (an e4m3 kernel has no registers left for them)
+    uint32_t qf[DP / 16][2], q_next[kQueriesAhead ? DP / 16 : 1][2];
     // Queries as the products' column operand: value pairs of step k for head g. An e4m3 key load brings 16
     // neighbouring values a lane, so its steps run through the head in that order.
-    const auto load_queries = [&](const SlotInfo& in) {
+    const auto load_queries = [&](const SlotInfo& in, uint32_t (&to)[DP / 16][2]) {
         const int in_group = in.unit % p.blocks * S::kHeads + 8 * eight + g;
         const T* q = static_cast<const T*>(a.q) + in.seq * a.q_ld + static_cast<int64_t>(in.unit / p.blocks * group + in_group) * D;
 #pragma unroll
@@ -442,11 +442,14 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int d = FP8 ? (k / 4) * 64 + 16 * t + (k % 4) * 4 + 2 * j : 16 * k + 2 * t + 8 * j;
-                qf[k][j] = in_group < group && d < D ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
+                to[k][j] = in_group < group && d < D ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
             }
     };
     int slot = 0, info = 0, first_chunk = 0;
     bool fresh = true;
+    if constexpr (kQueriesAhead) {
+        if (left > 0) load_queries(sh.info[0], q_next);
+    }
     for (int64_t n = 0; n < left; ++n) {
         copy_wait<kSlots - 2>();
         __syncthreads();
@@ -457,7 +460,12 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
             // a segment starts: its queries, fresh statistics
             fresh = false;
             first_chunk = in.chunk;
-            load_queries(in);
+            if constexpr (kQueriesAhead) {
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) qf[k][0] = q_next[k][0], qf[k][1] = q_next[k][1];
+            } else {
+                load_queries(in, qf);
+            }
             float scale[2] = {1.0f, 1.0f};
             if constexpr (FP8) {
                 // a power of two brings the head's largest query to [2^14, 2^15): fp16 then holds every one of
@@ -492,6 +500,13 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
             for (int m = 0; m < DP / 16; ++m)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[m][j] = 0.0f;
+        }
+        if constexpr (kQueriesAhead) {
+            // the next segment's queries, a chunk ahead: with short sequences each would wait for memory
+            if (n + 1 < left) {
+                const SlotInfo next = sh.info[info + 1 == kInfos ? 0 : info + 1];
+                if (next.chunk == 0) load_queries(next, q_next);
+            }
         }
         // S^T = K Q^T for this warp's keys r0 .. r0 + 16 kTiles - 1
         const unsigned char* keys = sh.ring[slot][0];
@@ -562,7 +577,9 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
 #pragma unroll
             for (int m = 0; m < DP / 16; ++m) o[m][0] *= fade[0], o[m][1] *= fade[1], o[m][2] *= fade[0], o[m][3] *= fade[1];
         }
-        uint32_t pf[kTiles][2];
+        // A bf16 weight is taken as the sum of two: rounded once, its 8 bits would add as much error as the output's.
+        constexpr int kWeightParts = std::is_same_v<M, __half> ? 1 : 2;
+        uint32_t pf[kTiles][kWeightParts][2];
         // (nothing seen yet: all weights 0)
         const float base[2] = {top[0] == -INFINITY ? 0.0f : top[0], top[1] == -INFINITY ? 0.0f : top[1]};
 #pragma unroll
@@ -572,8 +589,15 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
             for (int j = 0; j < 4; ++j) pr[j] = exp2_fast(s[kt][j] - base[j & 1]);
             sum[0] += pr[0] + pr[2];
             sum[1] += pr[1] + pr[3];
-            pf[kt][0] = transpose8x8(pack<M>(pr[0], pr[1]));
-            pf[kt][1] = transpose8x8(pack<M>(pr[2], pr[3]));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t w = pack<M>(pr[2 * j], pr[2 * j + 1]);
+                pf[kt][0][j] = transpose8x8(w);
+                if constexpr (kWeightParts == 2) {
+                    const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
+                    pf[kt][1][j] = transpose8x8(pack<M>(pr[2 * j] - lo, pr[2 * j + 1] - hi));
+                }
+            }
         }
         // O^T += V^T P^T
         if constexpr (FP8) {
@@ -589,7 +613,7 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
                         // bytes (key, value): (0,0) (0,1) (1,0) (1,1); row g of the tile is value 2 g, row g + 8 value 2 g + 1
                         const uint32_t u0 = __byte_perm(v[2 * i], 0, 0x3120), u1 = __byte_perm(v[2 * i + 1], 0, 0x3120);
                         const uint32_t af[4] = {e4m3_pair(u0), e4m3_pair(u0 >> 16), e4m3_pair(u1), e4m3_pair(u1 >> 16)};
-                        multiply<M>(o[m + i], af, pf[kt][0], pf[kt][1]);
+                        multiply<M>(o[m + i], af, pf[kt][0][0], pf[kt][0][1]);
                     }
                 }
         } else {
@@ -600,7 +624,8 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
                     uint32_t af[4];
                     load_matrices_transposed(
                         af, smem_addr(values + S::place(r0 + 16 * kt + (lane & 7) + ((lane >> 4) << 3), 2 * m + ((lane >> 3) & 1))));
-                    multiply<M>(o[m], af, pf[kt][0], pf[kt][1]);
+#pragma unroll
+                    for (int k = 0; k < kWeightParts; ++k) multiply<M>(o[m], af, pf[kt][k][0], pf[kt][k][1]);
                 }
         }
 

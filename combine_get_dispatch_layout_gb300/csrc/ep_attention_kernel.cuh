@@ -147,6 +147,9 @@ __device__ __forceinline__ void load_matrices_transposed(uint32_t (&r)[4], uint3
                  : "r"(addr)
                  : "memory");
 }
+__device__ __forceinline__ void load_words(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -261,7 +264,7 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
 
     // ---- this CTA's chunks: `left` of them from (seq, unit, chunk) on
     int seq, unit, chunk, chunks, low, end;
-    int64_t left;
+    int left;   // (a share stays below 2^31 chunks: 2^31 keys a sequence and head at most, 64 a chunk)
     if (p.split) {
         const Share share = find_share<kThreads, kChunk>(a, p);
         // sequences without keys: zeros
@@ -276,7 +279,7 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
             if (tid == 0) cuts[blockIdx.x].seq = -1;
             return;
         }
-        left = share.count;
+        left = static_cast<int>(share.count);
         if (tid == 0) {
             // the unit that holds this share's last chunk, if it began here and goes on behind it
             int lo, en;
@@ -321,13 +324,13 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
     // note, which writes the rows' places) one chunk before copies() starts their way to the ring slot.
     // Rows by thread; with fewer rows than threads, other warps for every chunk.
     constexpr int kLookups = (kChunk + kThreads - 1) / kThreads;
-    int64_t located = 0;
+    int located = 0;
     int note_slot = 0;
     int32_t page_id[kLookups];
     int page_place[kLookups];
     const auto look_row = [&](int k) {
         if constexpr (kChunk >= kThreads) return tid + k * kThreads;
-        return (tid + static_cast<int>(located) * kChunk) & (kThreads - 1);
+        return (tid + located * kChunk) & (kThreads - 1);
     };
     const auto look_up = [&]() {
         if (located >= left) return;
@@ -342,6 +345,7 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
             }
         }
     };
+    const bool alike = a.k_page == a.v_page && a.k_slot == a.v_slot && a.k_head == a.v_head;
     const auto note = [&]() {
         if (located < left) {
             const int h = unit / p.blocks;
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
                     RowAt at{0, 0};
                     if (real) {
                         at.key = (page_id[k] * a.k_page + page_place[k] * a.k_slot + h * a.k_head) * S::kCacheBytes;
-                        at.value = (page_id[k] * a.v_page + page_place[k] * a.v_slot + h * a.v_head) * S::kCacheBytes;
+                        at.value = alike ? at.key : (page_id[k] * a.v_page + page_place[k] * a.v_slot + h * a.v_head) * S::kCacheBytes;
                     }
                     sh.at[note_slot][r] = at;
                     const unsigned mask = __ballot_sync(kFullMask, real);
@@ -428,6 +432,17 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
     for (int i = 0; i < kSlots - 1; ++i) copies();
 
     // ---- the pass over the chunks
+    // This thread's places in a slot's keys and values; the exchange of pieces repeats every 8 of them (128 bytes).
+    constexpr int kPlaces = S::kPieces >= 8 ? 4 : 2;
+    const uint32_t ring_at = smem_addr(sh.ring[0][0]);
+    const int r0 = warp * 16 * kTiles;
+    uint32_t key_place[kPlaces], value_place[kPlaces];
+#pragma unroll
+    for (int i = 0; i < kPlaces; ++i) {
+        key_place[i] = FP8 ? S::place(r0 + g, (4 * i + t) % S::kPieces) : S::place(r0 + (lane & 15), 2 * i + (lane >> 4));
+        value_place[i] = S::kTile + (FP8 ? S::place(r0 + (lane & 15), 2 * i + (lane >> 4))
+                                         : S::place(r0 + (lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)));
+    }
     float o[DP / 16][4];             // O^T: rows d, columns heads
     float top[2], sum[2], c2[2];     // of the warp's heads 2 t, 2 t + 1
     constexpr bool kQueriesAhead = !FP8 && DP <= 128;   // (an e4m3 kernel has no registers left for them)
@@ -450,7 +465,7 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
     if constexpr (kQueriesAhead) {
         if (left > 0) load_queries(sh.info[0], q_next);
     }
-    for (int64_t n = 0; n < left; ++n) {
+    for (int n = 0; n < left; ++n) {
         copy_wait<kSlots - 2>();
         __syncthreads();
         const SlotInfo in = sh.info[info];
@@ -509,9 +524,7 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
             }
         }
         // S^T = K Q^T for this warp's keys r0 .. r0 + 16 kTiles - 1
-        const unsigned char* keys = sh.ring[slot][0];
-        const unsigned char* values = sh.ring[slot][1];
-        const int r0 = warp * 16 * kTiles;
+        const uint32_t slot_at = ring_at + slot * (2 * S::kTile);
         float s[kTiles][4];
 #pragma unroll
         for (int kt = 0; kt < kTiles; ++kt) s[kt][0] = s[kt][1] = s[kt][2] = s[kt][3] = 0.0f;
@@ -520,9 +533,10 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
             for (int j = 0; j < DP / 64; ++j)
 #pragma unroll
                 for (int kt = 0; kt < kTiles; ++kt) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(keys + S::place(r0 + 16 * kt + g, 4 * j + t));
-                    const uint4 y = *reinterpret_cast<const uint4*>(keys + S::place(r0 + 16 * kt + g + 8, 4 * j + t));
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+                    const uint32_t at = slot_at + key_place[j % 2] + j / 2 * 128 + kt * 16 * S::kRowBytes;
+                    uint32_t xs[4], ys[4];
+                    load_words(xs, at);
+                    load_words(ys, at + 8 * S::kRowBytes);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t af[4] = {e4m3_pair(xs[i]), e4m3_pair(ys[i]), e4m3_pair(xs[i] >> 16), e4m3_pair(ys[i] >> 16)};
@@ -535,7 +549,7 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
 #pragma unroll
                 for (int kt = 0; kt < kTiles; ++kt) {
                     uint32_t af[4];
-                    load_matrices(af, smem_addr(keys + S::place(r0 + 16 * kt + (lane & 15), 2 * k + (lane >> 4))));
+                    load_matrices(af, slot_at + key_place[k % kPlaces] + k / 4 * 128 + kt * 16 * S::kRowBytes);
                     multiply<M>(s[kt], af, qf[k][0], qf[k][1]);
                 }
         }
@@ -607,7 +621,7 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
                 for (int kt = 0; kt < kTiles; ++kt) {
                     // four 8 x 8 matrices of value pairs: keys 0-7 and 8-15 of 16 values, then of the next 16
                     uint32_t v[4];
-                    load_matrices_transposed(v, smem_addr(values + S::place(r0 + 16 * kt + (lane & 15), m + (lane >> 4))));
+                    load_matrices_transposed(v, slot_at + value_place[m / 2 % kPlaces] + m / 8 * 128 + kt * 16 * S::kRowBytes);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         // bytes (key, value): (0,0) (0,1) (1,0) (1,1); row g of the tile is value 2 g, row g + 8 value 2 g + 1
@@ -622,8 +636,7 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
 #pragma unroll
                 for (int kt = 0; kt < kTiles; ++kt) {
                     uint32_t af[4];
-                    load_matrices_transposed(
-                        af, smem_addr(values + S::place(r0 + 16 * kt + (lane & 7) + ((lane >> 4) << 3), 2 * m + ((lane >> 3) & 1))));
+                    load_matrices_transposed(af, slot_at + value_place[m % kPlaces] + m / 4 * 128 + kt * 16 * S::kRowBytes);
 #pragma unroll
                     for (int k = 0; k < kWeightParts; ++k) multiply<M>(o[m], af, pf[kt][k][0], pf[kt][k][1]);
                 }

@@ -933,3 +933,92 @@ def test_on_another_stream_and_in_a_graph(ep):
     torch.cuda.synchronize()
     for t, want in zip((idx, wt, out, y), replayed):
         assert torch.equal(t, want)
+
+
+def dequantised(codes, scales, e, group):
+    O, I = codes.shape[1], 2 * codes.shape[2]
+    code = torch.stack((codes[e] & 15, codes[e] >> 4), -1).view(O, I).double().cpu()
+    return (code - 8) * scales[e].double().cpu().t().repeat_interleave(group, 1)
+
+
+def test_decode_layer_example(ep):
+    """The example's layer, step by step, against each part's definition on the part's own inputs."""
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    import decode_layer
+    T, group = 5, 64
+    layer = decode_layer.DecodeLayer(T, hidden=256, heads=8, kv_heads=2, dim=64, experts=12, topk=3, inner=128, page=4,
+                                     max_len=16, group=group)
+    g = gen(70)
+    for step in range(6):
+        x = randn(g, T, 256, dtype=torch.bfloat16)
+        cache = layer.k_cache.clone()
+        y = layer.attention(x)
+        h = decode_layer.norm(x)
+        want, tol = experts_reference(h, layer.w_qkv, layer.s_qkv, None, [(0, 0, T)], group, False)
+        within(layer.qkv, want, tol + want.abs() * U[torch.bfloat16] * 1.01)
+        lens = layer.seq_lens
+        assert lens.tolist() == [step + 1] * T
+        changed = (layer.k_cache != cache).flatten(1).any(1).nonzero()[:, 0].tolist()
+        assert sorted(changed) == sorted(layer.block_table[:, step // 4].tolist())
+        check_attention(ep, layer.q, layer.k_cache, layer.v_cache, layer.block_table, lens)
+        want, tol = experts_reference(layer.attended.flatten(1), layer.w_out, layer.s_out, None, [(0, 0, T)], group, False)
+        within(layer.projected, want, tol + want.abs() * U[torch.bfloat16] * 1.01)
+        assert torch.equal(y, x + layer.projected)
+
+        z = layer.mixture(y)
+        h = decode_layer.norm(y)
+        want_idx, want_w = router_reference(h @ layer.gate.t(), 3, 0, True, 1.0)
+        assert torch.equal(layer.idx.cpu(), want_idx)
+        within(layer.weights, want_w, 1e-5)
+        off = layer.offsets.tolist()
+        assert off[-1] == 3 * T
+        slots = sorted((int(e), t, k) for t in range(T) for k, e in enumerate(want_idx[t]))
+        assert torch.equal(layer.received, torch.stack([h[t] for _, t, _ in slots]))
+        ranges = [(e, off[e], off[e + 1]) for e in range(12)]
+        want, tol = experts_reference(layer.received, layer.w_up, layer.s_up, None, ranges, group, True)
+        within(layer.activated, want, tol + want.abs() * U[torch.bfloat16] * 1.01)
+        want, tol = experts_reference(layer.activated, layer.w_down, layer.s_down, None, ranges, group, False)
+        within(layer.returned, want, tol + want.abs() * U[torch.bfloat16] * 1.01)
+        want = torch.zeros(T, 256, dtype=torch.float64)
+        for row, (_, t, k) in enumerate(slots):
+            want[t] += layer.weights[t, k].double().cpu() * layer.returned[row].double().cpu()
+        within(layer.combined, want, want.abs() * U[torch.bfloat16] * 1.01 + 1e-6)
+        assert torch.equal(z, y + layer.combined)
+    layer.handle.destroy()
+
+
+def test_decode_layer_example_runs_as_a_program():
+    r = subprocess.run([sys.executable, os.path.join(ROOT, "examples", "decode_layer.py"), "--tokens", "8", "--steps", "4"],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    assert "outputs finite: True" in r.stdout
+
+
+@pytest.mark.parametrize("score,renorm", [(0, True), (0, False), (1, True), (1, False)])
+def test_router_gradient_through_the_combine(ep, score, renorm):
+    """Router, layout, dispatch, identity experts, combine, and all their gradients: the logits' gradient of
+    sum(out * c) against autograd in 64 bits on the same rows."""
+    g = gen(80)
+    T, E, K, H = 40, 16, 4, 128
+    x, c = randn(g, T, H, dtype=torch.bfloat16), randn(g, T, H, dtype=torch.bfloat16)
+    logits = randn(g, T, E, scale=1.5)
+    idx, w = torch.empty(T, K, dtype=torch.int64, device="cuda"), torch.empty(T, K, device="cuda")
+    ep.ep_router_topk(logits, idx, w, score=score, renormalize=renorm, scale=1.25)
+    cnt, ntr = torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    itr, off = torch.empty(T, 1, dtype=torch.uint8, device="cuda"), torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    h = ep.ep_layout(idx, E, 1, cnt, ntr, itr, off)
+    rows = torch.empty(T * K, H, dtype=torch.bfloat16, device="cuda")
+    ep.ep_dispatch(h, x, ep.EP_DTYPE_BF16, rows, T * K)
+    expert = torch.repeat_interleave(torch.arange(E, device="cuda"), cnt.long())
+    y = (rows.float() * (1 + 0.1 * expert[:, None])).bfloat16()        # experts that differ
+    grad_w = torch.empty(T, K, device="cuda")
+    ep.ep_combine_backward(h, c, y, topk_weights=w, grad_topk_weights=grad_w)
+    grad = torch.empty_like(logits)
+    ep.ep_router_topk_backward(logits, idx, grad_w, grad, score=score, renormalize=renorm, scale=1.25)
+    row_of = torch.empty(T, K, dtype=torch.int32, device="cuda")
+    ep.ep_handle_copy_row_of_slot(h, row_of)
+    dots = torch.einsum("tkh,th->tk", y[row_of.long()].double(), c.double()).cpu()
+    want = backward_reference(logits, idx.cpu(), dots, score, renorm, 1.25)
+    size = float(dots.abs().max())
+    within(grad, want, size * 4e-5)     # the dots are fp32 sums of H products, the scores good to 1e-6
+    h.destroy()

@@ -1,19 +1,31 @@
 // Router: top-k experts per token from the logits, their weights, and the
 // gradient of the weights back to the logits.
 //
-// One warp a token. Up to 512 experts the token's keys stay in registers (V a
-// lane, expert 32 j + lane), so the row is read once; K rounds of a warp-wide
-// maximum pick the experts, each lane rescanning its own V keys. Larger rows go
-// through shared memory. Memory bounds neither (a row is a kilobyte): what
-// counts is the chain of each warp's steps, and with few tokens the launch.
+// Up to 512 experts a token's keys stay in registers, V neighbouring experts a
+// lane, so the row is read once; K rounds of a maximum over the token's lanes
+// pick the experts, the winning lane alone looking through its own keys again.
+// Larger rows, and groups that are not a power of two of lanes, go through
+// shared memory, a warp a token. Memory bounds neither (a row is a kilobyte):
+// what counts is the instructions a token, the chain of each warp's steps, and
+// with few tokens the launch. Measured, launches in a graph: 256 tokens, 256
+// fp32 experts, top 8: 3.3 us; 16384 tokens, 64 bf16 experts in 8 groups, top 6:
+// 8.4 us; the gradient for 8192 tokens, 256 fp32 experts: 6.1 us, 2.9 TB/s.
 #include <math.h>
+#include <string.h>
+
+#include <type_traits>
 
 #include "ep_layer.cuh"
 
 namespace ep {
 namespace {
 
-constexpr int kWarps = 4;   // tokens per block
+constexpr int kWarps = 4;   // of a block
+// From this many tokens on, rows of up to 128 experts share a warp (4 or 2 of them): the rounds' instructions are
+// what counts then. Below, a token's own warp has the shorter chain. Two forms, a warp's share against a whole warp:
+// 64 experts in groups, top 6: 8.4 / 10.6 us at 16384 tokens, 3.8 / 4.1 at 4096, 3.5 / 3.3 at 2048;
+// 128 experts: 10.8 / 13.2 at 16384, 4.8 / 5.0 at 4096, 4.0 / 3.8 at 2048. (256 experts, two rows a warp: no gain.)
+constexpr int kManyTokens = 4096;
 
 // A key as an unsigned integer in the same order (-0 with +0); 0 stands for
 // an expert that cannot be used (-infinity and NaN: the lowest finite value
@@ -27,15 +39,39 @@ __device__ __forceinline__ uint32_t ordered(float f) {
 // The number that a key above 0 stands for.
 __device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k); }
 
+// Over the LANES neighbouring lanes of a token; the whole warp calls them.
+template <int LANES = 32>
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
+    for (int o = LANES / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
     return v;
 }
+template <int LANES = 32>
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    for (int o = LANES / 2; o; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
     return v;
+}
+
+// N numbers from `p` on, in pieces of up to 16 bytes where `wide` says that p allows them.
+template <int N, typename T>
+__device__ __forceinline__ void load_row(const T* p, bool wide, T (&out)[N]) {
+    constexpr int kBytes = N * static_cast<int>(sizeof(T));
+    using Piece = std::conditional_t<(kBytes >= 16), uint4, std::conditional_t<kBytes == 8, uint2, uint32_t>>;
+    if (wide) {
+#pragma unroll
+        for (int i = 0; i < kBytes / static_cast<int>(sizeof(Piece)); ++i) {
+            const Piece piece = reinterpret_cast<const Piece*>(p)[i];
+            memcpy(out + i * (sizeof(Piece) / sizeof(T)), &piece, sizeof(Piece));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) out[i] = p[i];
+    }
+}
+template <typename T>
+__device__ __forceinline__ bool rows_aligned(const T* p, int64_t ld) {
+    return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * sizeof(T))) & 15) == 0;
 }
 
 // exp(l - m) for l <= m with m possibly infinite: the logits that equal the
@@ -54,15 +90,16 @@ __device__ __forceinline__ float sigmoid(float l) {
 // an expert was chosen), up to a factor common to the token when only ratios
 // count (renormalize): sigmoid(l) * exp(-c) with c = min(0, largest logit)
 // cannot underflow for all of them at once.
+template <int LANES>
 __device__ __forceinline__ float chosen_score(float l, bool on, int score, int renormalize, float row_max,
                                               float row_sum) {
     if (score == EP_SCORE_SOFTMAX) {
         if (!renormalize) return on ? exp_below(l, row_max) / row_sum : 0.0f;
-        const float m = warp_max(on ? l : -INFINITY);
+        const float m = warp_max<LANES>(on ? l : -INFINITY);
         return on ? exp_below(l, m) : 0.0f;
     }
     if (!renormalize) return on ? sigmoid(l) : 0.0f;
-    const float c = fminf(0.0f, warp_max(on ? l : -INFINITY));
+    const float c = fminf(0.0f, warp_max<LANES>(on ? l : -INFINITY));
     if (!on) return 0.0f;
     return l >= 0.0f ? 1.0f / (1.0f + expf(-l)) : expf(l - c) / (1.0f + expf(l));
 }
@@ -95,43 +132,52 @@ __device__ __forceinline__ unsigned kept_groups(uint32_t score, int groups, int 
 }
 
 // The weights of the chosen experts (lane k: the k-th, its logit l), and both outputs.
+template <int LANES = 32>
 __device__ __forceinline__ void write_choice(const RouterArgs& a, int t, int lane, int mine, float l, float row_max, float row_sum) {
     const bool on = mine >= 0;
-    float w = chosen_score(l, on, a.score, a.renormalize, row_max, row_sum);
+    float w = chosen_score<LANES>(l, on, a.score, a.renormalize, row_max, row_sum);
     if (a.renormalize) {
-        const float total = warp_sum(w);
+        const float total = warp_sum<LANES>(w);
         if (on) w /= total;
     }
-    if (lane < a.K) {
+    if (lane < a.K && t < a.T) {
         a.idx[static_cast<int64_t>(t) * a.K + lane] = mine;
         a.weights[static_cast<int64_t>(t) * a.K + lane] = on ? w * a.scale : 0.0f;
     }
 }
 
-// Keys in registers. Groups of experts that are not a power of two up to 32 go through router_topk_kernel.
-template <typename T, int V>
+// Keys in registers: LANES lanes a token, 32 / LANES tokens a warp, experts V lane to V lane + V - 1 with lane `lane`,
+// so that a lane's first largest key and the lowest lane that has it are the lowest expert of that key.
+template <typename T, int LANES, int V>
 __global__ void __launch_bounds__(32 * kWarps) router_topk_registers_kernel(RouterArgs a) {
     dependent_entry();
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (t >= a.T) return;
-    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    const int lane = threadIdx.x % LANES;
+    const int t = (blockIdx.x * kWarps * 32 + threadIdx.x) / LANES;
+    if ((t & ~(32 / LANES - 1)) >= a.T) return;   // (the warp's first token)
+    // lanes past the last token go through the motions on its row
+    const T* row = static_cast<const T*>(a.logits) + min(t, a.T - 1) * a.ld;
     const bool by_score = a.bias != nullptr || (a.num_groups > 1 && a.group_top == 2);
+    const int first = V * lane;
     float l[V];
+    if (first + V <= a.E) {
+        T raw[V];
+        load_row<V>(row + first, rows_aligned(static_cast<const T*>(a.logits), a.ld), raw);
 #pragma unroll
-    for (int j = 0; j < V; ++j) l[j] = 32 * j + lane < a.E ? usable(to_float(row[32 * j + lane])) : -INFINITY;
+        for (int j = 0; j < V; ++j) l[j] = usable(to_float(raw[j]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) l[j] = first + j < a.E ? usable(to_float(row[first + j])) : -INFINITY;
+    }
     float m = 0.0f, sum = 1.0f;
     if (a.score == EP_SCORE_SOFTMAX && (by_score || !a.renormalize)) {
         m = l[0];
 #pragma unroll
         for (int j = 1; j < V; ++j) m = fmaxf(m, l[j]);
-        m = warp_max(m);
+        m = warp_max<LANES>(m);
         sum = 0.0f;
-        if (m > -INFINITY) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) sum += exp_below(l[j], m);
-        }
-        sum = warp_sum(sum);
+        for (int j = 0; j < V; ++j) sum += m > -INFINITY ? exp_below(l[j], m) : 0.0f;
+        sum = warp_sum<LANES>(sum);
     }
     uint32_t keys[V];
 #pragma unroll
@@ -139,58 +185,70 @@ __global__ void __launch_bounds__(32 * kWarps) router_topk_registers_kernel(Rout
         float key = l[j];
         if (by_score && key > -INFINITY) {
             key = a.score == EP_SCORE_SOFTMAX ? exp_below(l[j], m) / sum : sigmoid(l[j]);
-            if (a.bias) key += a.bias[32 * j + lane];
+            if (a.bias) key += a.bias[first + j];
         }
         keys[j] = ordered(key);
     }
     if (a.num_groups > 1) {
-        // n neighbouring lanes hold a group: its two largest keys by exchange, then lane g takes group g's
-        const int n = a.E / a.num_groups;
-        uint32_t score = 0;
+        // a group is `span` whole lanes: the lane's two largest keys, then the span's by exchange
+        const int span = a.E / a.num_groups / V;
+        uint32_t one = 0, two = 0;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            uint32_t first = keys[j], second = 0;
-            for (int o = 1; o < n; o <<= 1) {
-                const uint32_t f = __shfl_xor_sync(kFullMask, first, o), s = __shfl_xor_sync(kFullMask, second, o);
-                second = max(min(first, f), max(second, s));
-                first = max(first, f);
-            }
-            const uint32_t g = group_score(first, second, a.group_top);
-            const uint32_t taken = __shfl_sync(kFullMask, g, lane * n & 31);
-            if (lane * n >> 5 == j) score = taken;
+            two = max(two, min(one, keys[j]));
+            one = max(one, keys[j]);
         }
-        const unsigned kept = kept_groups(score, a.num_groups, a.topk_groups, lane);
-        const int log = 31 - __clz(n);
+        for (int o = 1; o < span; o <<= 1) {
+            const uint32_t f = __shfl_xor_sync(kFullMask, one, o), s = __shfl_xor_sync(kFullMask, two, o);
+            two = max(min(one, f), max(two, s));
+            one = max(one, f);
+        }
+        const uint32_t score = group_score(one, two, a.group_top);
+        int before = 0;
+        for (int j = 0; j < LANES; j += span) {
+            const uint32_t o = __shfl_sync(kFullMask, score, j, LANES);
+            before += o > score || (o == score && j + span <= lane);
+        }
+        if (before >= a.topk_groups) {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (!((kept >> min(31, (32 * j + lane) >> log)) & 1)) keys[j] = 0;
+            for (int j = 0; j < V; ++j) keys[j] = 0;
+        }
     }
     int mine = -1;
     uint32_t my_key = 0;
     uint32_t best = 0;
-    int at = 0;
     const auto scan = [&]() {
         best = 0;
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (keys[j] > best) best = keys[j], at = 32 * j + lane;
+        for (int j = 0; j < V; ++j) best = max(best, keys[j]);
     };
     scan();
     for (int k = 0; k < a.K; ++k) {
-        const uint32_t top = __reduce_max_sync(kFullMask, best);
-        if (top == 0) break;
-        const int e = __reduce_min_sync(kFullMask, best == top ? at : 0x7fffffff);
-        if (lane == k) mine = e, my_key = top;
-        if (e == at && best == top) {
+        // (no two lanes compare experts: the lowest lane with the largest key holds the lowest expert of it)
+        uint32_t top = best;
+        if constexpr (LANES == 32) {
+            top = __reduce_max_sync(kFullMask, best);
+        } else {
+#pragma unroll
+            for (int o = LANES / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(kFullMask, top, o));
+        }
+        const unsigned have = __ballot_sync(kFullMask, best == top) >> ((threadIdx.x & 31) - lane);
+        const int winner = __ffs(have) - 1;
+        if (!__any_sync(kFullMask, top != 0)) break;
+        int at = 0;
+        if (lane == winner) {
+            bool found = false;
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                if (32 * j + lane == e) keys[j] = 0;
+                if (!found && keys[j] == top) found = true, at = first + j, keys[j] = 0;
             scan();
         }
+        const int e = __shfl_sync(kFullMask, at, winner, LANES);
+        if (lane == k && top != 0) mine = e, my_key = top;
     }
     // (a key that is the logit gives it back; otherwise the row has it)
     const float chosen = mine < 0 ? 0.0f : by_score ? usable(to_float(row[mine])) : value_of(my_key);
-    write_choice(a, t, lane, mine, chosen, m, sum);
+    write_choice<LANES>(a, t, lane, mine, chosen, m, sum);
 }
 
 // One warp per token; the token's keys live in shared memory. K rounds of a
@@ -297,7 +355,7 @@ __global__ void __launch_bounds__(32 * kWarps) router_backward_kernel(RouterBack
             row_statistics(row, a.E, lane, m, sum);
         }
     }
-    float p = chosen_score(l, on, a.score, a.renormalize, m, sum);
+    float p = chosen_score<32>(l, on, a.score, a.renormalize, m, sum);
     if (a.renormalize) {
         const float total = warp_sum(p);
         p = on ? p / total : 0.0f;
@@ -329,17 +387,30 @@ __global__ void __launch_bounds__(32 * kWarps) router_backward_kernel(RouterBack
     if (on) out[e] = from_float<T>(dense ? total - mean * p : total);
 }
 
+template <typename T, int LANES, int V>
+cudaError_t launch_topk_registers(const RouterArgs& a, cudaStream_t stream) {
+    constexpr int kTokens = kWarps * 32 / LANES;
+    return launch_dependent(router_topk_registers_kernel<T, LANES, V>, dim3((a.T + kTokens - 1) / kTokens), dim3(32 * kWarps), 0,
+                            stream, a);
+}
+
 template <typename T>
 cudaError_t launch_topk(const RouterArgs& a, cudaStream_t stream) {
-    const dim3 grid((a.T + kWarps - 1) / kWarps), block(32 * kWarps);
-    const int n = a.E / a.num_groups;
-    if (a.E <= 512 && (a.num_groups == 1 || (n <= 32 && (n & (n - 1)) == 0))) {
-        auto* kernel = a.E <= 64    ? router_topk_registers_kernel<T, 2>
-                       : a.E <= 128 ? router_topk_registers_kernel<T, 4>
-                       : a.E <= 256 ? router_topk_registers_kernel<T, 8>
-                                    : router_topk_registers_kernel<T, 16>;
-        return launch_dependent(kernel, grid, block, 0, stream, a);
+    // the register kernel wants a group to be a power of two of lanes
+    const auto fits = [&](int V) {
+        if (a.num_groups == 1) return true;
+        const int n = a.E / a.num_groups, span = n / V;
+        return n % V == 0 && (span & (span - 1)) == 0;
+    };
+    if (a.T >= kManyTokens) {
+        if (a.E <= 64 && a.K <= 8 && fits(8)) return launch_topk_registers<T, 8, 8>(a, stream);
+        if (a.E <= 128 && a.K <= 16 && fits(8)) return launch_topk_registers<T, 16, 8>(a, stream);
     }
+    if (a.E <= 64 && fits(2)) return launch_topk_registers<T, 32, 2>(a, stream);
+    if (a.E <= 128 && fits(4)) return launch_topk_registers<T, 32, 4>(a, stream);
+    if (a.E <= 256 && fits(8)) return launch_topk_registers<T, 32, 8>(a, stream);
+    if (a.E <= 512 && fits(16)) return launch_topk_registers<T, 32, 16>(a, stream);
+    const dim3 grid((a.T + kWarps - 1) / kWarps), block(32 * kWarps);
     const size_t smem = sizeof(uint32_t) * kWarps * a.E;
     if (smem > 48 * 1024) {
         const cudaError_t err = cudaFuncSetAttribute(router_topk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,

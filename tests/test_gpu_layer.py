@@ -178,6 +178,53 @@ def test_router_strided_and_misaligned_rows(ep):
         within(w, want, router_tolerance(logits, want))
 
 
+@pytest.mark.parametrize("T,E,K", [(4096, 64, 8), (4099, 64, 6), (4097, 37, 8), (4098, 128, 16), (4101, 100, 9), (4096, 1, 1),
+                                   (4103, 64, 9), (4102, 128, 17)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score,renorm", [(0, True), (0, False), (1, True)])
+def test_router_many_tokens(ep, T, E, K, dtype, score, renorm):
+    """Rows that share a warp (and ones whose K keeps them from it), some of them with few experts to use or none."""
+    g = gen(T + E + K)
+    logits = randn(g, T, E, dtype=dtype, scale=2.0)
+    logits[torch.rand(T, E, generator=g).cuda() < 0.3] = -math.inf
+    logits[1::7] = -math.inf
+    want_idx, want = router_reference(logits, K, score, renorm, 1.5)
+    idx, w = run_router(ep, logits, K, score=score, renormalize=renorm, scale=1.5)
+    assert torch.equal(idx, want_idx)
+    within(w, want, router_tolerance(logits, want))
+
+
+@pytest.mark.parametrize("E,groups,keep", [(64, 8, 4), (64, 2, 1), (64, 32, 5), (128, 16, 3), (128, 8, 8), (96, 3, 2), (96, 12, 5)])
+def test_router_many_tokens_in_groups(ep, E, groups, keep):
+    T = 4099
+    wide = randn(gen(E + groups), T, E + 3, dtype=torch.bfloat16, scale=2.0)
+    for logits in (wide[:, :E].contiguous(), wide[:, 1:1 + E]):
+        want_idx, want = router_reference(logits, 6, 1, True, 2.5, groups=groups, keep=keep, group_top=1)
+        idx, w = run_router(ep, logits, 6, score=1, scale=2.5, num_groups=groups, topk_groups=keep, group_top=1)
+        assert torch.equal(idx, want_idx)
+        within(w, want, router_tolerance(logits, want))
+
+
+@pytest.mark.parametrize("E,groups", [(64, 1), (64, 8), (128, 4)])
+def test_router_many_tokens_with_a_bias(ep, E, groups):
+    """As the bias test above: only rows with no two keys, and no two sums of a group's two largest, closer than 5e-6."""
+    g = gen(17 + E + groups)
+    logits = (torch.randint(-24, 25, (16384, E), generator=g) / 8.0).cuda()
+    bias = (torch.randperm(E, generator=g) / 512.0).cuda()
+    key = torch.sigmoid(logits.double()) + bias.double()
+    near = key.sort(1).values.diff(dim=1).min(1).values > 5e-6
+    if groups > 1:
+        top2 = key.view(-1, groups, E // groups).topk(2, dim=2).values.sum(2)
+        near &= top2.sort(1).values.diff(dim=1).min(1).values > 5e-6
+    logits = logits[near]
+    assert logits.shape[0] > 4096
+    logits = logits[:4100]
+    want_idx, want = router_reference(logits, 6, 1, True, 1.0, bias, groups, max(1, groups // 2), 2)
+    idx, w = run_router(ep, logits, 6, bias=bias, score=1, num_groups=groups, topk_groups=max(1, groups // 2), group_top=2)
+    assert torch.equal(idx, want_idx)
+    within(w, want, router_tolerance(logits, want))
+
+
 def test_router_feeds_the_layout(ep):
     """A router with unusable experts gives slots of -1, which the layout drops."""
     logits = randn(gen(6), 50, 16)

@@ -1,4 +1,5 @@
-// The experts' products on dispatched rows: 4-bit weights, group scales.
+// The experts' products on dispatched rows: 4-bit weights, group scales. (Up to
+// 8 rows in all mostly go through ep_expert_w4_few.cu.)
 //
 // Mathematics. y[n, o] = sum over groups g of s[g, o] * sum over i in g of
 // (code[o, i] - zero[g, o]) x[n, i]. The inner sums run through the 5th-generation
@@ -36,11 +37,10 @@
 // are on their way while split_kernel still runs. Where there are few items, the
 // CTAs of a cluster share an item's inputs and join through distributed shared
 // memory.
-#include <cuda.h>
 
 #include <type_traits>
 
-#include "ep_layer.cuh"
+#include "ep_w4.cuh"
 
 namespace ep {
 namespace {
@@ -97,12 +97,6 @@ struct Plan {
 
 // ------------------------------------------------------------------ PTX
 
-__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-        : "memory");
-}
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, int real) {   // zeros where real is 0
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
 }
@@ -182,18 +176,6 @@ __device__ __forceinline__ bool elected() {
 }
 
 // ------------------------------------------------------------------ rows and items
-
-// First row and number of real rows of expert e, within [0, rows).
-__device__ __forceinline__ int expert_rows(const W4Args& a, int e, int& first) {
-    if (!a.offsets) {
-        first = 0;
-        return a.rows;
-    }
-    first = min(max(a.offsets[e], 0), a.rows);
-    int n = min(max(a.offsets[e + 1], 0), a.rows) - first;
-    if (a.counts) n = min(n, a.counts[e]);
-    return max(n, 0);
-}
 
 struct Item {
     int expert, row, rows, col;   // col: first output column of the tile
@@ -677,21 +659,6 @@ EncodeFn encoder() {
     return fn;
 }
 
-// Bytes [w][z][y][x], read in boxes of 128 x box_y x box_z; zeros past the ends.
-cudaError_t byte_map(CUtensorMap* map, const void* base, int64_t x, int64_t y, int64_t z, int64_t w, int box_y, int box_z) {
-    const EncodeFn encode = encoder();
-    if (!encode) return cudaErrorNotSupported;
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(x), static_cast<cuuint64_t>(y), static_cast<cuuint64_t>(z),
-                                static_cast<cuuint64_t>(w)};
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(x), static_cast<cuuint64_t>(x * y), static_cast<cuuint64_t>(x * y * z)};
-    const cuuint32_t box[4] = {128, static_cast<cuuint32_t>(box_y), static_cast<cuuint32_t>(box_z), 1}, step[4] = {1, 1, 1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? cudaSuccess
-               : cudaErrorInvalidValue;
-}
-
 // SMs of the current device, with the kernel's shared memory limit raised: looked up once per device (a race writes
 // the same values).
 template <typename Kernel>
@@ -779,11 +746,26 @@ cudaError_t launch_type(const W4Args& a, void* workspace, int dtype, cudaStream_
 
 }  // namespace
 
+cudaError_t byte_map(CUtensorMap* map, const void* base, int64_t x, int64_t y, int64_t z, int64_t w, int box_y, int box_z) {
+    const EncodeFn encode = encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(x), static_cast<cuuint64_t>(y), static_cast<cuuint64_t>(z),
+                                static_cast<cuuint64_t>(w)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(x), static_cast<cuuint64_t>(x * y), static_cast<cuuint64_t>(x * y * z)};
+    const cuuint32_t box[4] = {128, static_cast<cuuint32_t>(box_y), static_cast<cuuint32_t>(box_z), 1}, step[4] = {1, 1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
 int64_t expert_w4_workspace(int64_t rows, int I, int group, int dtype) {
     return (rows * (I / group) * 8 + 15) / 16 * 16 + split_bytes(rows, I, dtype);
 }
 
 cudaError_t launch_expert_w4(const W4Args& a, void* workspace, int dtype, cudaStream_t stream) {
+    if (expert_w4_few(a)) return launch_expert_w4_few(a, dtype, stream);
     return dtype == EP_DTYPE_BF16 ? launch_type<__nv_bfloat16>(a, workspace, dtype, stream)
                                   : launch_type<__half>(a, workspace, dtype, stream);
 }

@@ -240,8 +240,8 @@ typedef struct {
  *  y              device, [rows, O or O/2].
  *  workspace      device, 16-byte aligned, ep_expert_w4_workspace bytes;
  *                 contents need no initialising and are not kept.
- * Each input is taken to within 2^-17 of the largest of the 64 (32 with groups
- * of 32) neighbours that share its power of two; products and sums are fp32, a
+ * Each input is taken to within 2^-17 of the largest of the group (of
+ * group_size inputs) that it is in; products and sums are fp32, a
  * group's scale multiplies the group's sum, and y is rounded once, after the
  * activation. An infinite input makes its row of y NaN. Offsets are taken as
  * at most `rows`; rows < 2^31.

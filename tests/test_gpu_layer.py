@@ -844,6 +844,68 @@ def test_experts_infinite_and_nan_rows_stay_in_their_rows(ep):
     assert bool(y[2].isnan().all()) and not bool(y[6].isfinite().any())
 
 
+@pytest.mark.parametrize("counts", [[8], [1, 1, 1, 1, 1, 1, 1, 1], [0, 5, 0, 3], [0, 0, 2, 1, 0, 4], [0, 0, 0]])
+@pytest.mark.parametrize("I,O,group", [(32, 17, 32), (128, 64, 128), (384, 130, 128), (320, 50, 64), (1056, 256, 32), (2048, 1000, 128)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_experts_few_rows(ep, counts, I, O, group, dtype, zeros):
+    """Up to 8 rows in all go through a kernel of their own; inputs over many powers of two."""
+    x, w, s, z, off = experts_inputs(I + O + 1, counts, I, O, group, dtype, zeros, pad=0 if sum(counts) else 3)
+    x *= 2.0 ** (torch.arange(x.shape[0], device="cuda")[:, None] % 5 * 2 - 6)
+    x *= 2.0 ** (torch.arange(I, device="cuda") // 128 % 3 * 3.0)
+    check_experts(ep, x, w, s, z, off, group)
+    if O % 2 == 0:
+        check_experts(ep, x / 32, w, s, z, off, group, swiglu=True)
+
+
+def test_experts_few_rows_of_an_aligned_layout(ep):
+    """Gaps between the experts' rows."""
+    x, w, s, z, _ = experts_inputs(55, [2, 2, 0, 4], 256, 70, 64, torch.bfloat16, True)
+    off = torch.tensor([0, 2, 4, 4, 8], dtype=torch.int32, device="cuda")
+    cnt = torch.tensor([1, 2, 0, 3], dtype=torch.int32, device="cuda")
+    x[1], x[7] = math.nan, math.inf
+    y = check_experts(ep, x, w, s, z, off, 64, counts=cnt, ranges=[(0, 0, 1), (1, 2, 4), (3, 4, 7)])
+    assert bool(y[1].isnan().all()) and bool(y[7].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_experts_few_rows_infinite_and_nan(ep, dtype):
+    x, w, s, z, off = experts_inputs(56, [5, 3], 256, 48, 64, dtype, False)
+    clean = check_experts(ep, x, w, s, z, off, 64)
+    x[2, 7], x[6, 200], x[7, 3] = math.nan, math.inf, -math.inf
+    y = torch.empty_like(clean)
+    ep.ep_expert_w4(x, w, s, y, expert_offsets=off)
+    keep = [0, 1, 3, 4, 5]
+    assert torch.equal(y[keep], clean[keep])
+    assert bool(y[[2, 6, 7]].isnan().all())
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_experts_few_rows_of_many_outputs(ep, swiglu):
+    """Tiles in several batches for each block, and more experts than threads."""
+    x, w, s, z, off = experts_inputs(57, [2], 64, 90002, 64, torch.bfloat16, True)
+    check_experts(ep, x, w, s, z, off, 64, swiglu=swiglu)
+    x, w, s, z, off = experts_inputs(58, [0] * 600 + [2] + [0] * 30 + [1], 64, 20, 32, torch.float16, True)
+    check_experts(ep, x, w, s, z, off, 32, swiglu=swiglu)
+
+
+def test_experts_few_rows_past_32_bit_offsets(ep):
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB")
+    E, O, I = 160, 8192, 8192          # 5 GiB of codes
+    w = torch.empty(E, O, I // 2, dtype=torch.uint8, device="cuda")
+    w[150].random_(0, 256)
+    s = torch.full((E, I // 128, O), 0.01, dtype=torch.bfloat16, device="cuda")
+    x = randn(gen(59), 2, I, dtype=torch.bfloat16)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[151:] = 2
+    y = torch.empty(2, O, dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_w4(x, w, s, y, expert_offsets=off)
+    part = slice(O - 300, O)
+    want, tol = experts_reference(x, w[150:151, part], s[150:151, :, part], None, [(0, 0, 2)], 128, False)
+    within(y[:, part], want, tol + want.abs() * U[torch.bfloat16] * 1.01)
+
+
 def test_experts_weights_past_32_bit_offsets(ep):
     """Codes behind the first 2^32 bytes."""
     if torch.cuda.mem_get_info()[0] < 16 << 30:

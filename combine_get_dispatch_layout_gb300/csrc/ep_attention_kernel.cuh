@@ -173,10 +173,10 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 // Two e4m3 codes (the low 16 bits) as two fp16 values, exactly. The instruction issues at the rate of the
 // integer ones (2 clocks per warp and SM quarter), which would take seven for four codes.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t codes) {
-    uint32_t r;
-    asm("{ .reg .b16 c; cvt.u16.u32 c, %1; cvt.rn.f16x2.e4m3x2 %0, c; }" : "=r"(r) : "r"(codes));
-    return r;
+__device__ __forceinline__ void e4m3_values(uint32_t codes, uint32_t& first, uint32_t& second) {
+    asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %2; cvt.rn.f16x2.e4m3x2 %0, lo; cvt.rn.f16x2.e4m3x2 %1, hi; }"
+        : "=r"(first), "=r"(second)
+        : "r"(codes));
 }
 template <typename M>
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
@@ -539,7 +539,9 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
                     load_words(ys, at + 8 * S::kRowBytes);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint32_t af[4] = {e4m3_pair(xs[i]), e4m3_pair(ys[i]), e4m3_pair(xs[i] >> 16), e4m3_pair(ys[i] >> 16)};
+                        uint32_t af[4];
+                        e4m3_values(xs[i], af[0], af[2]);
+                        e4m3_values(ys[i], af[1], af[3]);
                         multiply<M>(s[kt], af, qf[4 * j + i][0], qf[4 * j + i][1]);
                     }
                 }
@@ -626,7 +628,9 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
                     for (int i = 0; i < 2; ++i) {
                         // bytes (key, value): (0,0) (0,1) (1,0) (1,1); row g of the tile is value 2 g, row g + 8 value 2 g + 1
                         const uint32_t u0 = __byte_perm(v[2 * i], 0, 0x3120), u1 = __byte_perm(v[2 * i + 1], 0, 0x3120);
-                        const uint32_t af[4] = {e4m3_pair(u0), e4m3_pair(u0 >> 16), e4m3_pair(u1), e4m3_pair(u1 >> 16)};
+                        uint32_t af[4];
+                        e4m3_values(u0, af[0], af[1]);
+                        e4m3_values(u1, af[2], af[3]);
                         multiply<M>(o[m + i], af, pf[kt][0][0], pf[kt][0][1]);
                     }
                 }

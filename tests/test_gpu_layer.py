@@ -691,6 +691,17 @@ def test_attention_many_short_sequences(ep):
     check_attention(ep, *attention_inputs(26, lens, 4, 2, 64, 16, torch.bfloat16))
 
 
+@pytest.mark.parametrize("cache", [None, torch.float8_e4m3fn])
+@pytest.mark.parametrize("h,n", [(4, 2), (9, 1), (8, 8)])
+@pytest.mark.parametrize("seed", range(6))
+def test_attention_very_uneven_lengths(ep, cache, h, n, seed):
+    """Sequences of no keys, of one and of thousands side by side: shares that end anywhere in a unit, or before its first key."""
+    rng = torch.Generator().manual_seed(100 + seed)
+    lens = [int(torch.randint(0, top, (1,), generator=rng)) for top in (2, 70, 2, 5000, 300, 1, 130, 2, 2, 900, 40, 2000, 3)]
+    lens = lens * (1 + seed % 3) + [1] * (seed * 7)
+    check_attention(ep, *attention_inputs(200 + seed, lens, h, n, 64, 16, torch.bfloat16, cache))
+
+
 def test_attention_long_sequence_splits(ep):
     for lens in ([100001], [70000, 1, 300]):
         check_attention(ep, *attention_inputs(27, lens, 8, 2, 64, 64, torch.float16))

@@ -21,6 +21,13 @@
 // leave half the instruction empty. A warp takes its share of each chunk with
 // statistics of its own; the warps join when a segment (a CTA's part of one
 // sequence and head) ends.
+//
+// Measured, launches in a graph, join kernel included, heads of 128: one
+// sequence of 131071 keys, 8 cache heads, bf16: 86.7 us (6.2 TB/s); 64 of up to
+// 4096 keys, 64 query heads: 88.9 us (5.7 TB/s); 128 of up to 8192 over an e4m3
+// cache: 169 us (6.0 TB/s), all of 8192: 330 us (6.5 TB/s); one of 129 keys:
+// 6.3 us. What is over the time at the full rate is start, join and each
+// segment's end: 15 us (24 with e4m3) where a CTA has 3 or 4 segments.
 #pragma once
 
 #include <math.h>
@@ -42,7 +49,6 @@ struct Plan {
     int units;       // units of one sequence: cache heads * head blocks
     int blocks;      // head blocks per cache head
     unsigned page_mul, page_shift;  // i / page_size = (umulhi(i, page_mul) + ...) as page_of
-    int min_chunks;  // a CTA's share is at least this many chunks
     float out_scale; // of O / l
     int by_unit;     // join blocks belong to units (else to the CTAs a unit began in)
 };
@@ -65,7 +71,7 @@ __device__ __forceinline__ int sequence(const AttentionArgs& a, int b, int& low,
 
 // CTAs that share a work of W, and the first place of CTA i.
 __device__ __forceinline__ int sharers(const Plan& p, int64_t W) {
-    return static_cast<int>(min(static_cast<int64_t>(p.grid), (W + p.min_chunks - 1) / p.min_chunks));
+    return static_cast<int>(min(static_cast<int64_t>(p.grid), W));
 }
 __device__ __forceinline__ int64_t share_start(int64_t W, int ctas, int i) { return W * i / ctas; }
 
@@ -185,8 +191,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// Two e4m3 codes (the low 16 bits) as two fp16 values, exactly. The instruction issues at the rate of the
-// integer ones (2 clocks per warp and SM quarter), which would take seven for four codes.
+// Four e4m3 codes as two pairs of fp16 values, exactly. The instruction issues at the rate of the integer ones (2 clocks
+// per warp and SM quarter), which would take seven for four codes.
 __device__ __forceinline__ void e4m3_values(uint32_t codes, uint32_t& first, uint32_t& second) {
     asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %2; cvt.rn.f16x2.e4m3x2 %0, lo; cvt.rn.f16x2.e4m3x2 %1, hi; }"
         : "=r"(first), "=r"(second)
@@ -230,7 +236,7 @@ struct Shape {
     using M = std::conditional_t<FP8, __half, T>;   // type of the products' operands
     static constexpr int kHeads = 8 * NT;
     // Warps: kKeyWarps shares of a chunk's keys times NT eights of heads. Codes have to be unpacked for half the
-    // bytes, so an e4m3 cache needs more warps to keep up with DRAM.
+    // bytes, so an e4m3 cache gets more warps (8: 169.6 us, 4: 170.7 us for 128 sequences of up to 8192).
     static constexpr int kKeyWarps = FP8 && NT == 1 && DP <= 128 ? 8 : 4;
     static constexpr int kThreads = 32 * kKeyWarps * NT;
     static constexpr int kCacheBytes = FP8 ? 1 : 2;
@@ -745,7 +751,8 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
 // Joins the parts of the units that several CTAs shared, in the CTAs' order. With many sequences most units
 // have few parts, and waves of blocks would cost more than the loads: blocks (i, *) serve the unit that
 // began in CTA i and went on behind it, if there is one, the first of them all of its heads (another block
-// each if the parts are many). With few long sequences (by_unit) the parts are many: blocks (u, *) serve
+// each if the parts are many: up to kFew are joined from registers, which takes 64 sequences of up to 4096
+// keys from 92.9 to 88.9 us). With few long sequences (by_unit) the parts are many: blocks (u, *) serve
 // unit u, each 32 values of one head, its threads over values and parts.
 template <typename T, int DP, int NT>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, Plan p) {
@@ -879,14 +886,16 @@ cudaError_t launch_shape(const AttentionArgs& a, Plan p, int sms, cudaStream_t s
     if (err != cudaSuccess) return err;
     const int64_t all = static_cast<int64_t>(a.B) * p.units;
     const int64_t most = (static_cast<int64_t>(a.max_pages) * a.page_size + S::kChunk - 1) / S::kChunk;
-    p.min_chunks = 4;
-    // sequences of at most min_chunks chunks are not worth cutting: whole units to each CTA and no join
-    p.split = most > p.min_chunks;
-    const int64_t useful = p.split ? (all * most + p.min_chunks - 1) / p.min_chunks : all;
+    // More units than CTAs: equal shares of their chunks, unless all have one; whole units / shares, us: 1000 sequences of up
+    // to 100 bf16 keys, 8 heads: 119 / 105, of up to 200: 159 / 128. Fewer units: shares, whose join is another launch, only
+    // where units have many chunks; 16 sequences of up to 300 keys: 8.9 / 11.7, one of 450: 11.6 / 10.1.
+    p.split = most > (all > p.grid ? 1 : 6);
+    const int64_t useful = p.split ? all * (most + kBegin) : all;
     if (useful < p.grid) p.grid = static_cast<int>(useful > 0 ? useful : 1);
     err = launch_dependent(attention_kernel<T, FP8, DP, NT>, dim3(p.grid), dim3(S::kThreads), smem, stream, a, p);
     if (err != cudaSuccess || !p.split) return err;
-    p.by_unit = all * 4 <= p.grid;
+    // (by CTA / by unit, us: 8 units of 131071 keys 87.4 / 86.6, one unit 28.6 / 24.3, 32 units of 8000 keys 31.8 / 34.3)
+    p.by_unit = all * 16 <= p.grid;
     const dim3 join_grid = p.by_unit ? dim3(static_cast<unsigned>(all), 8 * NT * (DP / 32)) : dim3(p.grid, 8 * NT);
     return launch_dependent(join_kernel<T, DP, NT>, join_grid, dim3(kJoinThreads), 0, stream, a, p);
 }

@@ -37,6 +37,11 @@
 // are on their way while split_kernel still runs. Where there are few items, the
 // CTAs of a cluster share an item's inputs and join through distributed shared
 // memory.
+//
+// Measured, launches in a graph, bf16, groups of 128, 256 experts of 4096 x 7168
+// with the activation, top 8: 256 tokens 702 us (5.6 TB/s), 128 tokens 636 us
+// (6.0), 64 tokens 552 us (6.1). Clusters of up to 16 instead of 8: 19.9 us against
+// 12.0 for one 4096 x 4096 matrix.
 
 #include <type_traits>
 
@@ -729,7 +734,8 @@ cudaError_t launch_group(const W4Args& a, void* workspace, int dtype, cudaStream
     const cudaError_t err = launch_dependent(split_kernel<T, GROUP>, dim3(static_cast<unsigned>(blocks < 8192 ? blocks : 8192)),
                                              dim3(kSplitThreads), 0, stream, a, x, stats);
     if (err != cudaSuccess) return err;
-    // rows of an item: 8, or 16 where experts have more than 4 rows on average (a second pass over a tile costs more)
+    // rows of an item: 8, or 16 where experts have more than 4 rows on average: a second pass over a tile costs more than
+    // columns that stay empty (256 tokens, 8 rows an expert: 935 us with 8, 773 with 16 when that was measured)
     const int used = a.rows < a.E ? a.rows : a.E, mean = (a.rows + used - 1) / used;
     if constexpr (kParts<T> == 2)
         if (mean <= 4 || a.rows <= 8)

@@ -25,9 +25,9 @@
 // Measured, launches in a graph, join kernel included, heads of 128: one
 // sequence of 131071 keys, 8 cache heads, bf16: 86.7 us (6.2 TB/s); 64 of up to
 // 4096 keys, 64 query heads: 88.9 us (5.7 TB/s); 128 of up to 8192 over an e4m3
-// cache: 169 us (6.0 TB/s), all of 8192: 330 us (6.5 TB/s); one of 129 keys:
+// cache: 167 us (6.0 TB/s), all of 8192: 330 us (6.5 TB/s); one of 129 keys:
 // 6.3 us. What is over the time at the full rate is start, join and each
-// segment's end: 15 us (24 with e4m3) where a CTA has 3 or 4 segments.
+// segment's end: 15 us (20 with e4m3) where a CTA has 3 or 4 segments.
 #pragma once
 
 #include <math.h>
@@ -150,6 +150,9 @@ __device__ Share find_share(const AttentionArgs& a, const Plan& p) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
 }
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int real) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
@@ -248,13 +251,18 @@ struct Shape {
     static constexpr int kTile = kChunk * kRowBytes;        // bytes of a chunk's keys, or values
     // Three slots: two CTAs a core keep 128 KB on the way, above what DRAM's latency needs at full rate.
     static constexpr int kSlots = 3;
+    // An e4m3 kernel has no registers for the next segment's queries: they come to shared memory with its first chunk.
+    // (Where that room would cost the second CTA a core, they are loaded when the segment begins.)
+    static constexpr bool kQueriesShared = FP8 && NT == 1 && DP <= 128;
+    static constexpr int kQueryWords = DP / 2 + 4;   // of a head
 
     struct Shared {
         alignas(128) unsigned char ring[kSlots][2][kTile];  // a used-up slot also serves the join of the warps
         RowAt at[kSlots + 1][kChunk];
         unsigned real[kSlots + 1][kChunk / 32];             // bit per key: it exists
         SlotInfo info[kSlots + 1];
-        float top[kKeyWarps][kHeads], sum[kKeyWarps][kHeads];
+        alignas(16) float top[kHeads][kKeyWarps], sum[kHeads][kKeyWarps];
+        alignas(16) uint32_t q[kQueriesShared ? kSlots : 1][kQueriesShared ? kHeads : 1][kQueryWords];
     };
     static_assert(kKeyWarps * kHeads * DP * 4 <= 2 * kTile, "the join of the warps fits a slot");
 
@@ -421,9 +429,23 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
     const unsigned char* key_base = static_cast<const unsigned char*>(a.k ? a.k : a.q) + (piece_bytes ? piece * 16 : 0);
     const unsigned char* value_base = static_cast<const unsigned char*>(a.v ? a.v : a.q) + (piece_bytes ? piece * 16 : 0);
     int copy_slot = 0, copy_info = 0;
+    bool copied = false;
     const auto copies = [&]() {
         const SlotInfo in = sh.info[copy_info];
         if (in.unit >= 0) {
+            if constexpr (S::kQueriesShared) {
+                if (in.chunk == 0 || !copied) {
+                    const int first_head = in.unit % p.blocks * S::kHeads;   // within the group
+                    const T* q = static_cast<const T*>(a.q) + in.seq * a.q_ld + static_cast<int64_t>(in.unit / p.blocks * group + first_head) * D;
+#pragma unroll
+                    for (int i = tid; i < S::kHeads * DP / 2; i += kThreads) {
+                        const int h = i / (DP / 2), d = i % (DP / 2) * 2;
+                        const bool real = first_head + h < group && d < D;
+                        copy4(smem_addr(&sh.q[copy_slot][h][d / 2]), real ? q + h * D + d : q, real ? 4 : 0);
+                    }
+                }
+                copied = true;
+            }
             constexpr int kRows = kThreads / S::kPieces;
             const int row = tid / S::kPieces;
             const uint32_t slot_addr = smem_addr(sh.ring[copy_slot][0]), first = slot_addr + S::place(row, piece);
@@ -508,6 +530,12 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
             if constexpr (kQueriesAhead) {
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) qf[k][0] = q_next[k][0], qf[k][1] = q_next[k][1];
+            } else if constexpr (S::kQueriesShared) {
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    const uint2 w = *reinterpret_cast<const uint2*>(&sh.q[slot][g][(k / 4) * 32 + 8 * t + (k % 4) * 2]);
+                    qf[k][0] = w.x, qf[k][1] = w.y;
+                }
             } else {
                 load_queries(in, qf);
             }
@@ -681,11 +709,10 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
             const int head0 = 8 * eight + 2 * t;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float l = sum[j];
-                l += __shfl_xor_sync(kFullMask, l, 4);
-                l += __shfl_xor_sync(kFullMask, l, 8);
-                l += __shfl_xor_sync(kFullMask, l, 16);
-                if (g == 0) sh.top[warp][head0 + j] = top[j], sh.sum[warp][head0 + j] = l;
+                sum[j] += __shfl_xor_sync(kFullMask, sum[j], 4);
+                sum[j] += __shfl_xor_sync(kFullMask, sum[j], 8);
+                sum[j] += __shfl_xor_sync(kFullMask, sum[j], 16);
+                if (g == 0) sh.top[head0 + j][warp] = top[j];
             }
             __syncthreads();
             float* stage = reinterpret_cast<float*>(sh.ring[slot][0]);   // [kWarps][kHeads][DP]
@@ -694,8 +721,9 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
             for (int j = 0; j < 2; ++j) {
                 float m = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sh.top[w][head0 + j]);
+                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sh.top[head0 + j][w]);
                 fade[j] = exp2_fast(top[j] - (m == -INFINITY ? 0.0f : m));
+                if (g == 0) sh.sum[head0 + j][warp] = sum[j] * fade[j];
             }
             // heads 2 t apart by a multiple of 32 words: value index exchanged by t * 8 to keep off one bank
 #pragma unroll
@@ -720,11 +748,15 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
                     const float4 y = *reinterpret_cast<const float4*>(from + w * S::kHeads * DP);
                     x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
                 }
-                float m = -INFINITY, l = 0.0f;
+                float l = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sh.top[w][h]);
+                for (int w = 0; w < kWarps; ++w) l += sh.sum[h][w];
+                const auto largest = [&]() {
+                    float m = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) l += sh.sum[w][h] * exp2_fast(sh.top[w][h] - (m == -INFINITY ? 0.0f : m));
+                    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sh.top[h][w]);
+                    return m;
+                };
                 if (whole) {
                     if (d < D) {
                         const float r = l == 0.0f ? 0.0f : p.out_scale / l;
@@ -733,10 +765,10 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
                     }
                     if (d == 0 && a.lse)
                         a.lse[static_cast<int64_t>(in.seq) * a.num_heads + h0 + h] =
-                            l == 0.0f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+                            l == 0.0f ? -INFINITY : 0.6931471805599453f * (largest() + log2f(l));
                 } else {
                     *reinterpret_cast<float4*>(to + h * DP + d) = x;
-                    if (d == 0) to[S::kHeads * DP + 2 * h] = m, to[S::kHeads * DP + 2 * h + 1] = l;
+                    if (d == 0) to[S::kHeads * DP + 2 * h] = largest(), to[S::kHeads * DP + 2 * h + 1] = l;
                 }
             }
             // (the slot and the statistics are written again only behind the next chunk's barrier)

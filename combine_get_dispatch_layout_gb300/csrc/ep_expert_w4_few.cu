@@ -124,20 +124,21 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
         const int steps = count * blocks, step0 = static_cast<int>(static_cast<int64_t>(steps) * warp / kWarps);
         const int step1 = static_cast<int>(static_cast<int64_t>(steps) * (warp + 1) / kWarps);
 
-        // the weight rows of lanes with row g and g + 8 of tile t0 + k; past the end the last one's, not written
+        // where this lane's weight rows g and g + 8 of a tile are read next; past the end the last one's, not written
         struct Rows {
-            const uint8_t *w0, *w1;
-            int64_t s0, s1;
+            const uint8_t *codes[2], *zeros[2];
+            const T* scales[2];
         };
-        const auto rows_of = [&](int i, int tile) {
-            const int col = tile * tile_cols;
-            const int o0 = min(col + g, cols - 1), o1 = a.swiglu ? cols + o0 : min(col + g + 8, cols - 1);
-            const int64_t e = entry[i].expert;
-            Rows r;
-            r.w0 = a.w + (e * a.O + o0) * (a.I / 2) + t * (GROUP / 8);
-            r.w1 = a.w + (e * a.O + o1) * (a.I / 2) + t * (GROUP / 8);
-            r.s0 = e * groups * a.O + o0;
-            r.s1 = e * groups * a.O + o1;
+        const auto rows_of = [&](int i, int tile, int block) {
+            const int o0 = min(tile * tile_cols + g, cols - 1), o1 = a.swiglu ? cols + o0 : min(tile * tile_cols + g + 8, cols - 1);
+            const int64_t e = entry[i].expert, first_group = (e * groups + block * kGroups) * a.O;
+            Rows r{};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                r.codes[k] = a.w + (e * a.O + (k ? o1 : o0)) * (a.I / 2) + block * (kBlock / 2) + t * (GROUP / 8);
+                r.scales[k] = static_cast<const T*>(a.scales) + first_group + (k ? o1 : o0);
+                if constexpr (ZEROS) r.zeros[k] = a.zeros + first_group + (k ? o1 : o0);
+            }
             return r;
         };
         uint32_t codes[kAhead][kGroups][2][kWords];
@@ -147,28 +148,30 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
         const int tile0 = static_cast<int>(t0 + k0 - static_cast<int64_t>(entry0) * tiles);
         int load_step = step0, load_entry = entry0, load_tile = tile0, load_block = step0 - k0 * blocks;
         Rows at{};
-        if (step0 < step1) at = rows_of(load_entry, load_tile);
+        if (step0 < step1) at = rows_of(load_entry, load_tile, load_block);
         const auto load = [&](int slot) {
             if (load_step >= step1) return;
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
-                const int grp = load_block * kGroups + j;
-                if (j > 0 && grp >= groups) break;
-                load_codes(codes[slot][j][0], at.w0 + grp * (GROUP / 2));
-                load_codes(codes[slot][j][1], at.w1 + grp * (GROUP / 2));
-                const int64_t on = static_cast<int64_t>(grp) * a.O;
-                scale[slot][j][0] = static_cast<const T*>(a.scales)[at.s0 + on];
-                scale[slot][j][1] = static_cast<const T*>(a.scales)[at.s1 + on];
-                if constexpr (ZEROS) {
-                    zero[slot][j][0] = a.zeros[at.s0 + on];
-                    zero[slot][j][1] = a.zeros[at.s1 + on];
+                if (j > 0 && load_block * kGroups + j >= groups) break;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    load_codes(codes[slot][j][k], at.codes[k] + j * (GROUP / 2));
+                    scale[slot][j][k] = *at.scales[k];
+                    at.scales[k] += a.O;
+                    if constexpr (ZEROS) {
+                        zero[slot][j][k] = *at.zeros[k];
+                        at.zeros[k] += a.O;
+                    }
                 }
             }
+            at.codes[0] += kBlock / 2;
+            at.codes[1] += kBlock / 2;
             ++load_step;
             if (++load_block == blocks) {
                 load_block = 0;
                 if (++load_tile == tiles) load_tile = 0, ++load_entry;
-                if (load_step < step1) at = rows_of(load_entry, load_tile);
+                if (load_step < step1) at = rows_of(load_entry, load_tile, 0);
             }
         };
 #pragma unroll
@@ -237,9 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
             const Entry it = entry[in_entry];
             const int local = it.local - row0;
             // (columns past the rows take another's: they are not written)
-            x_at = inputs + (local + min(g, it.rows - 1)) * x_stride + t * 16;
-            stats_at[0] = stats + (local + min(2 * t, it.rows - 1)) * groups;
-            stats_at[1] = stats + (local + min(2 * t + 1, it.rows - 1)) * groups;
+            x_at = inputs + (local + min(g, it.rows - 1)) * x_stride + t * 16 + block * (kBlock * 2);
+            stats_at[0] = stats + (local + min(2 * t, it.rows - 1)) * groups + block * kGroups;
+            stats_at[1] = stats + (local + min(2 * t + 1, it.rows - 1)) * groups + block * kGroups;
         };
         if (step0 < step1) begin();
         for (int step = step0; step < step1; step += kAhead) {
@@ -248,18 +251,17 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
                 if (step + slot >= step1) break;
 #pragma unroll
                 for (int j = 0; j < kGroups; ++j) {
-                    const int grp = block * kGroups + j;
-                    if (j > 0 && grp >= groups) break;
+                    if (j > 0 && block * kGroups + j >= groups) break;
                     float even[4] = {}, odd[4] = {};
 #pragma unroll
                     for (int w = 0; w < kWords; ++w) {
-                        const uint4 b = *reinterpret_cast<const uint4*>(x_at + (grp * kWords + w) * 64);
+                        const uint4 b = *reinterpret_cast<const uint4*>(x_at + (j * kWords + w) * 64);
                         const uint32_t u0 = codes[slot][j][0][w], u1 = codes[slot][j][1][w];
                         const uint32_t v0 = u0 >> 8, v1 = u1 >> 8;
                         multiply(even, u0 & kLow, u1 & kLow, v0 & kLow, v1 & kLow, b.x, b.y);
                         multiply(odd, u0 & kHigh, u1 & kHigh, v0 & kHigh, v1 & kHigh, b.z, b.w);
                     }
-                    const float2 st[2] = {stats_at[0][grp], stats_at[1][grp]};
+                    const float2 st[2] = {stats_at[0][j], stats_at[1][j]};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float z = ZEROS ? static_cast<float>(zero[slot][j][i >> 1]) : 8.0f;
@@ -267,6 +269,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
                         total[i] = fmaf(to_float(scale[slot][j][i >> 1]) * st[i & 1].x, sum, total[i]);
                     }
                 }
+                x_at += kBlock * 2;
+                stats_at[0] += kGroups;
+                stats_at[1] += kGroups;
                 load(slot);
                 if (++block == blocks || step + slot + 1 == step1) {
                     // slot k + warp: warps with later tiles are later ones

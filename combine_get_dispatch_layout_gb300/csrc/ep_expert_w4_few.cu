@@ -14,16 +14,16 @@
 // What bounds it: each weight is used once or a few times, so DRAM, and below
 // some megabytes the chain launch, offsets, first weights, join. So there is one
 // launch, no operand passes through shared memory but x (read from L2 by every
-// CTA), and a warp has two steps of 16 rows x 256 inputs in flight. A CTA takes
+// CTA), and a warp has five steps of 16 rows x 128 inputs in flight. A CTA takes
 // whole tiles of 16 rows; its warps share their inputs evenly, end to end over
 // the tiles, and join once for a batch of tiles, in the warps' order.
-// Measured, launches in a graph: 4096 x 4096, 4 rows of fp16: 7.3 us (1.2 TB/s);
-// 8 experts of 4096 x 7168, a row each, with the activation: 32 us (3.8 TB/s),
-// of which about 9 are start and join; the rest, 5 TB/s, is the unpacking
-// instructions (integer ones take two clocks; the same loads without products:
-// 5.7 TB/s). Tried: the codes by TMA into a ring of each warp, 54.2 us against
-// 54.7 for 16 experts; 8, 12, 24 and 32 warps a block: 38.6, 34.2, 32.2, 38.8 us
-// against 32.0 with 16 for 8 experts.
+// Measured, launches in a graph: 4096 x 4096, 4 rows of fp16: 7.7 us (1.1 TB/s);
+// 8 experts of 4096 x 7168, a row each, with the activation: 29 us (4.2 TB/s),
+// of which about 7 are start and join; the rest, 5.4 TB/s, is the loads' latency and
+// the unpacking instructions (integer ones take two clocks). Two steps of 256
+// inputs in flight: 31.3 us, six of 128 29.0; prefetches of 128 bytes to L2 instead
+// of 256: 30.4. Of an earlier form (32.0): 8, 12, 24 and 32 warps a block instead
+// of 16: 38.6, 34.2, 32.2, 38.8; the codes by TMA into a ring of each warp: 32.1.
 #include <math.h>
 #include <string.h>
 
@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kTile = 16;                // weight rows
-constexpr int kBlock = 256;              // inputs of a step
+constexpr int kBlock = 128;              // inputs of a step
 constexpr int kBatch = 32;               // tiles of a batch at most
 constexpr int kEntries = kFewRows;       // experts with rows: no more than there are rows
 constexpr int kJoinBytes = (kBatch + kWarps - 1) * kTile * 8 * 4;
@@ -50,13 +50,13 @@ struct Entry {
 };
 
 __device__ __forceinline__ void load_codes(uint32_t (&r)[4], const uint8_t* p) {
-    asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "l"(p));
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "l"(p));
 }
 __device__ __forceinline__ void load_codes(uint32_t (&r)[2], const uint8_t* p) {
-    asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p));
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p));
 }
 __device__ __forceinline__ void load_codes(uint32_t (&r)[1], const uint8_t* p) {
-    asm volatile("ld.global.nc.L1::no_allocate.L2::128B.u32 %0, [%1];" : "=r"(r[0]) : "l"(p));
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.u32 %0, [%1];" : "=r"(r[0]) : "l"(p));
 }
 __device__ __forceinline__ void multiply(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
@@ -69,7 +69,7 @@ template <typename T, int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, int tiles, int x_stride) {
     constexpr int kGroups = kBlock / GROUP;   // of a step
     constexpr int kWords = GROUP / 32;        // words of 8 codes: a lane's of a row, of a group
-    constexpr int kAhead = GROUP == 32 ? 1 : 2;
+    constexpr int kAhead = GROUP == 32 ? 2 : GROUP == 64 ? 4 - ZEROS : 5 - ZEROS;   // steps, as the registers allow
     extern __shared__ __align__(16) unsigned char shared_bytes[];
     __shared__ int2 found[kEntries];          // expert whose rows begin in this row, and their number
     __shared__ Entry entry[kEntries];
@@ -362,9 +362,9 @@ cudaError_t launch_type(const W4Args& a, cudaStream_t stream) {
 
 // Up to 8 rows, and codes of less than 1 MiB times the group's size. Beyond, the other kernel's higher rate makes up for
 // its second launch and its longer start. This one / the other, us: groups of 128: 4096 x 4096, 4 rows of fp16: 7.8 / 11.9;
-// 8 experts of 4096 x 7168 (117 MB), a bf16 row each: 31.9 / 34.2; one of 65536 x 4096 (134 MB), 4 rows: 36.9 / 33.2.
-// Groups of 64: 16384 x 4096 (33 MB), 8 rows: 20.1 / 19.3, 117 MB: 40.8 / 36.6. Groups of 32: 2 experts (29 MB):
-// 20.7 / 36.1, 4 experts: 31.8 / 28.5.
+// 8 experts of 4096 x 7168 (117 MB), a bf16 row each: 29.0 / 34.2; one of 65536 x 4096 (134 MB), 4 bf16 rows: 34.4 / 33.9.
+// Groups of 64: 4096 x 4096, 8 rows: 10.0 / 13.1, 117 MB: 37.7 / 36.6. Groups of 32: 2 experts (29 MB): 20.7 / 36.1,
+// 4 experts (59 MB): 29.0 / 28.3, 8 experts: 57.2 / 46.3.
 bool expert_w4_few(const W4Args& a) {
     if (a.rows > kFewRows || shared_bytes_of(a) > kShared) return false;
     const int64_t bytes = static_cast<int64_t>(a.rows < a.E ? a.rows : a.E) * a.O * (a.I / 2);

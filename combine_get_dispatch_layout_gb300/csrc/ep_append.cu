@@ -3,12 +3,13 @@
 //
 // Each value is read and written once, so memory bounds it. One block a token;
 // a thread keeps its place in a head, and with it the place's cosines and sines
-// in registers, and walks over the token's heads, two ahead of the stores. A
-// pair is always one thread's, so queries may be turned in place. What counts is
-// how many tokens are on the way at once, for each waits for its position, then
-// its angles, then its values: 8 blocks of 128 threads a core (64 registers) take
-// 57 us for 8192 tokens of 64 + 8 + 8 heads of 128 (5.7 TB/s), 2 blocks of 256
-// threads that load four heads ahead 103 us.
+// in registers, and walks over the token's heads with three under way, the first
+// of them before it knows the position. A pair is always one thread's, so queries
+// may be turned in place. What counts is how much is on the way at once, for each
+// token waits for its position, then its angles: 7 blocks of 128 threads a core (72
+// registers) take 54.6 us for 8192 tokens of 64 + 8 + 8 heads of 128 (5.9 TB/s);
+// 8 blocks with two heads 54.8, 6 with four 57.4, 8 with one 62.2; heads loaded
+// behind the position, two at a time: 56.8.
 #include <type_traits>
 
 #include "ep_layer.cuh"
@@ -17,7 +18,7 @@ namespace ep {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kAhead = 2;   // heads that a thread has loaded before it stores the first
+constexpr int kAhead = 3;   // heads that a thread has under way
 
 // How a head is cut up.
 enum Mode {
@@ -67,10 +68,36 @@ __device__ __forceinline__ void store1(__nv_fp8_e4m3* dst, float f, float inv) {
 }
 
 template <typename T, typename C, Mode MODE>
-__global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 7) kv_append_kernel(AppendArgs a) {
     dependent_entry();
     const int64_t t = blockIdx.x;
     const int D = a.head_dim, rot = a.rotary_dim, half = rot / 2, tid = threadIdx.x;
+    const T* const q = static_cast<const T*>(a.q) + t * a.q_ld;
+    const T* const k = static_cast<const T*>(a.k) + t * a.k_ld;
+    const T* const v = static_cast<const T*>(a.v) + t * a.v_ld;
+    T* const q_out = static_cast<T*>(a.q_out) + t * a.q_out_ld;
+
+    constexpr bool kHalves = MODE == kHalves8 || MODE == kHalves4;
+    constexpr int W = MODE == kHalves4 ? 4 : 8, kAngles = kHalves ? W : 4;
+    // ---- a thread's first heads are under way before the position is known
+    const int turned = half / kAngles, pieces = turned + (D - rot) / W;   // of a head
+    const int step = MODE == kSingle ? 0 : kThreads / pieces, c = MODE == kSingle ? 0 : tid % pieces, h0 = MODE == kSingle ? 0 : tid / pieces;
+    const bool turn = c < turned, two = kHalves && turn;
+    const int first = turn ? c * W : rot + (c - turned) * W;
+    Raw<W> one[kAhead], other[kAhead];
+    const auto load = [&](int u, int h) {
+        if (h >= a.num_heads + a.num_kv_heads) return;
+        const T* from = (h >= a.num_heads ? k + (h - a.num_heads) * D : q + h * D) + first;
+        one[u] = *reinterpret_cast<const Raw<W>*>(from);
+        if (two) other[u] = *reinterpret_cast<const Raw<W>*>(from + half);
+    };
+    if constexpr (MODE != kSingle) {
+        if (h0 < step) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) load(u, h0 + u * step);
+        }
+    }
+
     const int64_t pos = rot ? a.positions[t] : 0, slot = a.slots[t];
     const bool pos_ok = pos >= 0 && (rot == 0 || pos < a.max_position);
     const bool slot_ok = slot >= 0 && slot < a.num_slots;
@@ -80,11 +107,6 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(AppendArgs a) {
     const bool cached = pos_ok && slot_ok;
     C* const keys = static_cast<C*>(a.k_cache) + page * a.k_page + place * a.k_slot;
     C* const values = static_cast<C*>(a.v_cache) + page * a.v_page + place * a.v_slot;
-    const T* const q = static_cast<const T*>(a.q) + t * a.q_ld;
-    const T* const k = static_cast<const T*>(a.k) + t * a.k_ld;
-    const T* const v = static_cast<const T*>(a.v) + t * a.v_ld;
-    T* const q_out = static_cast<T*>(a.q_out) + t * a.q_out_ld;
-
     const int heads = a.num_heads + (cached ? a.num_kv_heads : 0);   // queries, then keys
     if constexpr (MODE == kSingle) {
         const int per_head = half + D - rot;
@@ -114,36 +136,22 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(AppendArgs a) {
             }
         }
     } else {
-        constexpr bool kHalves = MODE != kNeighbours;
-        constexpr int W = MODE == kHalves4 ? 4 : 8, kAngles = kHalves ? W : 4;
-        const int turned = half / kAngles, per_head = turned + (D - rot) / W;
-        const int step = kThreads / per_head, c = tid % per_head, h0 = tid / per_head;
         if (h0 < step) {
-            const bool turn = c < turned, two = kHalves && turn;
-            const int first = turn ? c * W : rot + (c - turned) * W;
             float cs[kAngles], sn[kAngles];
             if (turn) {
 #pragma unroll
                 for (int i = 0; i < kAngles; ++i) cs[i] = table[c * kAngles + i], sn[i] = table[half + c * kAngles + i];
             }
             for (int base = h0; base < heads; base += kAhead * step) {
-                Raw<W> one[kAhead], other[kAhead];
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const int h = base + u * step;
-                    if (h >= heads) break;
-                    const T* from = (h >= a.num_heads ? k + (h - a.num_heads) * D : q + h * D) + first;
-                    one[u] = *reinterpret_cast<const Raw<W>*>(from);
-                    if (two) other[u] = *reinterpret_cast<const Raw<W>*>(from + half);
-                }
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
                     const int h = base + u * step;
                     if (h >= heads) break;
                     float x[W], y[W], p[W], r[W];
                     unpack<T, W>(one[u], p);
+                    if (two) unpack<T, W>(other[u], r);
+                    load(u, h + kAhead * step);
                     if (two) {
-                        unpack<T, W>(other[u], r);
 #pragma unroll
                         for (int i = 0; i < W; ++i) {
                             x[i] = p[i] * cs[i % kAngles] - r[i] * sn[i % kAngles];

@@ -344,7 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // as many clusters as share the items evenly: all of them wait on the same DRAM, so an idle SM costs nothing
     const int clusters = p.slots / p.split;
     const int64_t each = (items + clusters - 1) / clusters;
-    const int64_t item0 = min(items, each * (blockIdx.x / p.split)), item1 = min(items, item0 + each);
+    const int64_t item0 = min(items, each * (blockIdx.x / p.split));
+    // (a cluster joins once: more than one item for it come of offsets that contradict one another)
+    const int64_t item1 = min(items, item0 + (p.split > 1 ? min(each, int64_t{1}) : each));
     // this CTA's stages of every item
     const int stage0 = p.stages * rank / p.split, stage1 = p.stages * (rank + 1) / p.split;
 
@@ -357,10 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         int64_t in = it - static_cast<int64_t>(table[lo]) * p.tiles;
         int e = lo << p.table_shift, passes = passes_of(e);
-        while (in >= static_cast<int64_t>(passes) * p.tiles) {   // (an entry of several experts)
+        while (in >= static_cast<int64_t>(passes) * p.tiles && e + 1 < a.E) {   // (an entry of several experts)
             in -= static_cast<int64_t>(passes) * p.tiles;
             passes = passes_of(++e);
         }
+        passes = max(passes, 1);   // (0, and an item behind the last one, come of offsets that contradict one another)
         Item r;
         int first;
         const int n = expert_rows(a, e, first), pass = static_cast<int>(in % passes);
@@ -664,18 +667,42 @@ EncodeFn encoder() {
     return fn;
 }
 
-// SMs of the current device, with the kernel's shared memory limit raised: looked up once per device (a race writes
-// the same values).
+// A device's SMs, and how many clusters of 2, 4 and 8 CTAs of a kernel it holds at once.
+struct Room {
+    int sms, clusters[3];
+};
+
+// Of the current device, with the kernel's shared memory limit raised: looked up once per device (a race writes the
+// same values, `ready` after them).
 template <typename Kernel>
-cudaError_t prepare_kernel(Kernel kernel, int smem, int* known, int* sms) {
+cudaError_t prepare_kernel(Kernel kernel, int smem, Room* known, int* ready, Room* room) {
     constexpr int kDevices = 64;
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
-    if (dev < kDevices && (*sms = __atomic_load_n(&known[dev], __ATOMIC_RELAXED)) > 0) return cudaSuccess;
+    if (dev < kDevices && __atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE)) {
+        *room = known[dev];
+        return cudaSuccess;
+    }
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (err == cudaSuccess) err = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-    if (err == cudaSuccess && dev < kDevices) __atomic_store_n(&known[dev], *sms, __ATOMIC_RELAXED);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&room->sms, cudaDevAttrMultiProcessorCount, dev);
+    for (int i = 0; i < 3 && err == cudaSuccess; ++i) {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2 << i;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(room->sms / (2 << i) * (2 << i));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        err = cudaOccupancyMaxActiveClusters(&room->clusters[i], kernel, &cfg);
+    }
+    if (err == cudaSuccess && dev < kDevices) {
+        known[dev] = *room;
+        __atomic_store_n(&ready[dev], 1, __ATOMIC_RELEASE);
+    }
     return err;
 }
 
@@ -686,11 +713,12 @@ int64_t split_bytes(int64_t rows, int I, int dtype) {
 template <typename T, int NR, int GROUP, bool ZEROS>
 cudaError_t launch_shape(const W4Args& a, const unsigned char* x, const float2* stats, cudaStream_t stream) {
     using S = Shape<T, NR, GROUP>;
-    static int known[64];
+    static Room known[64];
+    static int ready[64];
     constexpr int smem = S::kShared;
     Plan p{};
-    int sms = 0;
-    cudaError_t err = prepare_kernel(expert_w4_kernel<T, NR, GROUP, ZEROS>, smem, known, &sms);
+    Room room{};
+    cudaError_t err = prepare_kernel(expert_w4_kernel<T, NR, GROUP, ZEROS>, smem, known, ready, &room);
     if (err != cudaSuccess) return err;
     const int cols = a.swiglu ? a.O / 2 : a.O, cta_cols = kGroupsOfWarps * (a.swiglu ? kTileRows / 2 : kTileRows);
     p.tiles = (cols + cta_cols - 1) / cta_cols;
@@ -698,11 +726,14 @@ cudaError_t launch_shape(const W4Args& a, const unsigned char* x, const float2* 
     p.stages = (a.I + kIn - 1) / kIn;
     p.groups = a.I / GROUP;
     p.stats = reinterpret_cast<const float*>(stats);
-    p.slots = sms;
-    // items at most; with fewer than half the CTAs' number, clusters share them
-    const int64_t most = (static_cast<int64_t>(a.rows) / NR + (a.rows < a.E ? a.rows : a.E)) * p.tiles;
+    p.slots = room.sms;
+    // items at most: an expert of n rows has (n + NR - 1) / NR passes; with few, clusters share them, all at
+    // once on the device (4096 x 4096, us: 64 rows, 32 items, 16.9 by clusters of 4, 22.7 of 2; 32 rows, 16 items, of
+    // which not all fit as clusters of 8, 16.5 by 4, 23.8 by 8)
+    const int64_t used = a.rows < a.E ? a.rows : a.E;
+    const int64_t most = (a.rows + used * (NR - 1)) / NR * p.tiles;
     p.split = 1;
-    while (p.split < kMostSplit && 2 * p.split <= p.stages && most * 2 * p.split <= p.slots) p.split *= 2;
+    for (int i = 0; p.split < kMostSplit && 2 * p.split <= p.stages && most <= room.clusters[i]; ++i) p.split *= 2;
     const int64_t clusters = most < p.slots / p.split ? most : p.slots / p.split;
     p.slots = static_cast<int>(clusters) * p.split;
     CUtensorMap weight_map, x_map;

@@ -811,6 +811,16 @@ def test_experts_dense_and_long_rows(ep, rows, swiglu):
         check_experts(ep, x, w, s, z, off, group, swiglu=swiglu, offsets=False)
 
 
+@pytest.mark.parametrize("rows", [9, 16, 17, 31, 32, 33, 64, 65, 100])
+@pytest.mark.parametrize("experts", [1, 3])
+def test_experts_shared_items(ep, rows, experts):
+    """Numbers of items at which clusters of 8, 4 and 2 blocks share each, and one at which none does."""
+    for O, I in ((512, 2048), (1030, 1024), (4096, 512)):
+        counts = [rows] if experts == 1 else [rows // 2, 0, rows - rows // 2]
+        x, w, s, z, off = experts_inputs(rows + O, counts, I, O, 128, torch.float16, True)
+        check_experts(ep, x, w, s, z, off, 128)
+
+
 def test_experts_strided_rows(ep):
     x, w, s, z, off = experts_inputs(50, [3, 4], 128, 36, 64, torch.float16, False)
     wide = torch.zeros(7, 160, dtype=torch.float16, device="cuda")

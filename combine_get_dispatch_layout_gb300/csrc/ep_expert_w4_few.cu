@@ -361,10 +361,10 @@ cudaError_t launch_type(const W4Args& a, cudaStream_t stream) {
 }  // namespace
 
 // Up to 8 rows, and codes of less than 1 MiB times the group's size. Beyond, the other kernel's higher rate makes up for
-// its second launch and its longer start. This one / the other, us: groups of 128: 4096 x 4096, 4 rows of fp16: 7.8 / 11.9;
-// 8 experts of 4096 x 7168 (117 MB), a bf16 row each: 29.0 / 34.2; one of 65536 x 4096 (134 MB), 4 bf16 rows: 34.4 / 33.9.
-// Groups of 64: 4096 x 4096, 8 rows: 10.0 / 13.1, 117 MB: 37.7 / 36.6. Groups of 32: 2 experts (29 MB): 20.7 / 36.1,
-// 4 experts (59 MB): 29.0 / 28.3, 8 experts: 57.2 / 46.3.
+// its second launch and its longer start. This one / the other, us: groups of 128: 4096 x 4096, 4 rows of fp16: 7.8 / 11.8;
+// 8 experts of 4096 x 7168 (117 MB), a bf16 row each: 29.0 / 34.3; one of 65536 x 4096 (134 MB), 4 bf16 rows: 34.4 / 34.2.
+// Groups of 64: 4096 x 4096, 8 rows: 10.0 / 12.7, 117 MB: 37.7 / 36.4. Groups of 32: 2 experts (29 MB): 19.7 / 25.2,
+// 4 experts (59 MB): 29.0 / 28.0, 8 experts: 57.2 / 46.3.
 bool expert_w4_few(const W4Args& a) {
     if (a.rows > kFewRows || shared_bytes_of(a) > kShared) return false;
     const int64_t bytes = static_cast<int64_t>(a.rows < a.E ? a.rows : a.E) * a.O * (a.I / 2);

@@ -44,6 +44,9 @@ constexpr int kJoinBytes = (kBatch + kWarps - 1) * kTile * 8 * 4;
 // Codes in fp16: bits 0 to 3 alone are the subnormal number code * 2^-24, bits 4 to 7 alone 16 times that.
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 constexpr float kUnit = 5.9604644775390625e-8f;
+// Half of these bits go back with a group's power of two, where they cannot overflow, half behind the join: sums over
+// groups so stand for y * 2^-12, normal numbers wherever y is well above the type's smallest.
+constexpr int kHalfBits = 12;
 
 struct Entry {
     int expert, row, rows, local;   // local: rows of the entries before
@@ -75,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
     __shared__ Entry entry[kEntries];
     __shared__ int row_of[kEntries], entries_found;
     // x: [rows] rows of x_stride bytes, the inputs of a step in the order in which lanes take them; stats: [rows][groups],
-    // a power of two and 2^-24 * sum; join: [slots][16][8]
+    // 2^12 over the power of two and 2^-24 * sum; join: [slots][16][8]
     unsigned char* const inputs = shared_bytes;
     const int groups = a.I / GROUP, blocks = (a.I + kBlock - 1) / kBlock;
     float2* const stats = reinterpret_cast<float2*>(inputs + a.rows * x_stride);
@@ -199,13 +202,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
 #pragma unroll
                     for (int k = 0; k < 8; ++k) f[k] = to_float(v[u].v[k]);
                     if constexpr (!std::is_same_v<T, __half>) {
-                        float big = 0.0f;
+                        // (magnitudes in the order of their bits, two to a word; NaN lies above infinity)
+                        const uint4 raw = v[u].raw;
+                        uint32_t big = __vmaxu2(__vmaxu2(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu), __vmaxu2(raw.z & 0x7fff7fffu, raw.w & 0x7fff7fffu));
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(f[k]));
-#pragma unroll
-                        for (int o = 1; o < GROUP / 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(kFullMask, big, o));
-                        finite = big < INFINITY;
-                        e = big > 0.0f && finite ? min(14 - ilogbf(big), 126) : 0;
+                        for (int o = 1; o < GROUP / 8; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(kFullMask, big, o));
+                        const int exponent = static_cast<int>(max(big & 0xffffu, big >> 16) >> 7);   // + 127; subnormal numbers have 0
+                        finite = exponent < 255;
+                        e = finite ? min(14 + 127 - exponent, 126) : 0;
                     }
                     const float up = __int_as_float((e + 127) << 23);
                     __half2 h[4];   // (0, 4) (2, 6) (1, 5) (3, 7)
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
                     memcpy(&packed, h, 16);
                     *reinterpret_cast<uint4*>(inputs + r * x_stride + (grp * kWords + inside % kWords) * 64 + inside / kWords * 16) = packed;
                     if (inside == 0)
-                        stats[r * groups + grp] = make_float2(finite ? __int_as_float((127 - e) << 23) : __int_as_float(0x7fffffff), sum * kUnit);
+                        stats[r * groups + grp] = make_float2(finite ? __int_as_float((127 + kHalfBits - e) << 23) : __int_as_float(0x7fffffff), sum * kUnit);
                 }
             }
             have0 = row0, have1 = row1;
@@ -304,8 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
                 v0 += from[0];
                 v1 += from[64];
             }
-            v0 *= 1.0f / kUnit;
-            v1 *= 1.0f / kUnit;
+            v0 *= 1 << kHalfBits;
+            v1 *= 1 << kHalfBits;
             const int col = static_cast<int>((t0 + tile) - static_cast<int64_t>(en) * tiles) * tile_cols + r;
             T* y = static_cast<T*>(a.y) + (it.row + n) * a.y_ld + col;
             if (a.swiglu) {

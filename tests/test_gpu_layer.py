@@ -901,6 +901,17 @@ def test_experts_few_rows_infinite_and_nan(ep, dtype):
     assert bool(y[[2, 6, 7]].isnan().all())
 
 
+@pytest.mark.parametrize("rows", [3, 12])
+@pytest.mark.parametrize("power", [-100, -60, 60, 100])
+def test_experts_powers_of_two(ep, rows, power):
+    """bf16 rows times a power of two give outputs times the same power, bit for bit: nothing on the way over- or underflows."""
+    x, w, s, z, off = experts_inputs(60, [rows], 512, 48, 64, torch.bfloat16, True)
+    y, moved = (torch.empty(rows, 48, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ep.ep_expert_w4(x, w, s, y, expert_offsets=off, zeros=z)
+    ep.ep_expert_w4(x * 2.0 ** power, w, s, moved, expert_offsets=off, zeros=z)
+    assert torch.equal(moved, y * 2.0 ** power)
+
+
 @pytest.mark.parametrize("swiglu", [False, True])
 def test_experts_few_rows_of_many_outputs(ep, swiglu):
     """Tiles in several batches for each block, and more experts than threads."""

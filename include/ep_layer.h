@@ -193,7 +193,10 @@ typedef struct {
  *                 contents need no initialising and are not kept.
  * A sequence with no keys (length 0, every page masked) gives zeros. What lies
  * in the cache behind a sequence's end, NaN included, does not matter.
- * Scores, softmax statistics and sums are fp32. B * num_heads < 2^31.
+ * Scores, softmax statistics and sums are fp32. A softmax weight enters the
+ * products as the sum of two 16-bit numbers: within 2^-16 of itself over a bf16
+ * cache, within 2^-22 of itself or 2^-36 of the sequence's largest weight,
+ * whichever is more, over an fp16 or e4m3 cache. B * num_heads < 2^31.
  */
 EP_API ep_status_t ep_paged_attention(const void* q, const void* k_cache, const void* v_cache,
                                       const ep_cache_t* cache, const int32_t* block_table,

@@ -3,19 +3,20 @@
 //
 // Mathematics. y[n, o] = sum over groups g of s[g, o] * sum over i in g of
 // (code[o, i] - zero[g, o]) x[n, i]. The inner sums run through the 5th-generation
-// tensor cores on e4m3 operands with fp32 sums:
+// tensor cores on 8-bit operands with fp32 sums:
 //  - a code 0 .. 15 in a byte IS the e4m3 number code * 2^-9 (subnormal up to 7,
 //    the first binade from 8 on), so unpacking eight codes is two masks and one
 //    shift. (As bf16 operands of mma.sync they take 11 instructions, and that
 //    kernel ran at 37 % of the memory rate, bound by instruction issue; e4m3
 //    operands of mma.sync are converted to fp16 by further instructions.)
-//  - x is taken as a sum of e4m3 numbers, two for bf16 and three for fp16, after
-//    a power of two has brought the largest input of the group to [128, 256).
-//    Four significant bits each make up the 8 or 11 of x, exactly, down to
-//    e4m3's smallest step: what is left off is below 2^-17 of the group's
-//    largest. The parts lie side by side in the product's narrow side; only
-//    where TMEM has no room for the columns (groups of 32, or fp16 in groups of
-//    64) they are added into the same sums.
+//  - x is taken as a sum of 8-bit numbers, two for bf16 and three for fp16, after
+//    a power of two has brought the largest input of the group to [128, 256):
+//    an e4m3 number with the 4 leading bits, then e5m2 ones, each with the 3
+//    leading bits of what the ones before have left (rounded to nearest, so what
+//    is left has a bit less). They make up the 8 or 11 bits of x exactly, but for
+//    inputs so far below the group's largest that e5m2's smallest step counts:
+//    at most 2^-24 of the largest is left off. All are multiplied into the same
+//    sums, one after the other.
 //  - the zero point enters as zero * (sum of the group's inputs), in fp32.
 // Scales multiply a group's sum in fp32. y is rounded once.
 //
@@ -39,8 +40,9 @@
 // memory.
 //
 // Measured, launches in a graph, bf16, groups of 128, 256 experts of 4096 x 7168
-// with the activation, top 8: 256 tokens 702 us (5.6 TB/s), 128 tokens 636 us
-// (6.0), 64 tokens 552 us (6.1). Clusters of up to 16 instead of 8: 19.9 us against
+// with the activation, top 8: 256 tokens 700 us (5.6 TB/s; groups of 64 771, of 32
+// 1038; fp16 766), 128 tokens 636 us (6.0), 64 tokens 552 us (6.1). Parts of x as
+// columns of one product instead: 706 (822, 1036; 779). Clusters of up to 16 instead of 8: 19.9 us against
 // 12.0 for one 4096 x 4096 matrix.
 
 #include <type_traits>
@@ -71,10 +73,7 @@ constexpr int kParts = std::is_same_v<T, __half> ? 3 : 2;
 template <typename T, int NR, int GROUP>
 struct Shape {
     static_assert(NR == 16 || (NR == 8 && kParts<T> == 2), "");
-    static constexpr bool kSideBySide = 64 + NR * kParts<T> * (128 / GROUP) <= 128;   // the parts are columns of one product
-    static constexpr int kN = kSideBySide ? NR * kParts<T> : NR;   // columns of the product
-    static_assert(kN % 16 == 0, "");
-    static constexpr int kProducts = kSideBySide ? 1 : kParts<T>;
+    static constexpr int kN = 16;                              // columns of a product, the least there are: of 8 rows the others are garbage
     static constexpr int kGroups = 128 / GROUP;                // of half a stage
     static constexpr int kBlock = kParts<T> * 1024;            // 8 rows of x, 128 inputs: [part][8][128 bytes]
     static constexpr int kXBytes = NR / 8 * kBlock;            // x of half a stage
@@ -151,11 +150,6 @@ __device__ __forceinline__ float2 apart(uint64_t v) {
     asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
     return make_float2(__uint_as_float(lo), __uint_as_float(hi));
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -186,13 +180,13 @@ struct Item {
     int expert, row, rows, col;   // col: first output column of the tile
 };
 
-// Four values as e4m3 codes in a word, each reduced by what its code stands for.
-__device__ __forceinline__ uint32_t take_part(float (&v)[4]) {
+// Four values as 8-bit codes in a word, each reduced by what its code stands for.
+__device__ __forceinline__ uint32_t take_part(float (&v)[4], __nv_fp8_interpretation_t type) {
     uint32_t word = 0;
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
-        const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(v[i], v[i + 1]), __NV_SATFINITE, __NV_E4M3);
-        const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+        const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(v[i], v[i + 1]), __NV_SATFINITE, type);
+        const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, type)));
         v[i] -= f.x;
         v[i + 1] -= f.y;
         word |= static_cast<uint32_t>(c) << (8 * i);
@@ -200,7 +194,7 @@ __device__ __forceinline__ uint32_t take_part(float (&v)[4]) {
     return word;
 }
 
-// x as sums of e4m3 numbers, a plane [rows][I] for each part; of 8 neighbouring inputs the even ones come first, as
+// x as sums of 8-bit numbers, a plane [rows][I] for each part; of 8 neighbouring inputs the even ones come first, as
 // masks leave the codes. A thread takes 8 inputs, GROUP / 8 threads share a power of two. An infinite or NaN
 // input makes its group's power of two or sum NaN, and so every product with it.
 template <typename T, int GROUP>
@@ -240,8 +234,8 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(W4Args a, unsigned
 #pragma unroll
         for (int k = 0; k < kParts<T>; ++k) {
             uint2 w;
-            w.x = take_part(even);
-            w.y = take_part(odd);
+            w.x = take_part(even, k == 0 ? __NV_E4M3 : __NV_E5M2);
+            w.y = take_part(odd, k == 0 ? __NV_E4M3 : __NV_E5M2);
             if (in) *reinterpret_cast<uint2*>(to + k * plane + i * 8) = w;
         }
         // the sum of what the parts stand for: the inputs' less what is left of them
@@ -443,8 +437,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kIssuer) {
         if (leader) {
             constexpr uint32_t kShape = (1u << 4) | (static_cast<uint32_t>(S::kN / 8) << 17) | (static_cast<uint32_t>(kTileRows / 16) << 24);
-            // columns: 8 rows' parts, then the next 8 rows'; or the 16 rows of one part
-            constexpr int kStride = S::kSideBySide ? 1024 : S::kBlock;
+            constexpr uint32_t kLaterShape = kShape | (1u << 10);   // x as e5m2
+            // columns: 8 rows, then the next 8 (of an item of 8 rows whatever shared memory holds behind them)
+            constexpr int kStride = S::kBlock;
             int slot = 0;
             uint32_t parity = 0, ready_parity = 0;
             for (int64_t i = 0; i < steps; ++i) {
@@ -457,13 +452,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t a_at = tmem + wg * 128 + half * 32;
                         const uint32_t sums = tmem + wg * 128 + 64 + (S::kSumBuffers == 2 ? half * S::kSumCols : 0);
 #pragma unroll
-                        for (int part = 0; part < S::kProducts; ++part)
+                        for (int part = 0; part < kParts<T>; ++part)
 #pragma unroll
                             for (int k = 0; k < GROUP / 32; ++k)
 #pragma unroll
                                 for (int grp = 0; grp < kGroups; ++grp) {
                                     const int step = grp * (GROUP / 32) + k;
-                                    multiply(sums + grp * S::kN, a_at + step * 8, b + step * 2 + part * (1024 / 16), kShape, part > 0 || k > 0);
+                                    multiply(sums + grp * S::kN, a_at + step * 8, b + step * 2 + part * (1024 / 16),
+                                             part > 0 ? kLaterShape : kShape, part > 0 || k > 0);
                                 }
                         multiply_done(done + 8 * (wg * 2 + half));
                     }
@@ -518,24 +514,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 barrier_wait(done + 8 * (wg * 2 + half), (done_parity >> half) & 1, dead);
                 done_parity ^= 1u << half;
                 tmem_fence_after();
-                constexpr int kBlockParts = S::kSideBySide ? kParts<T> : 1;
 #pragma unroll
                 for (int i = 0; i < kGroups; ++i) {
                     const uint64_t sc = both(to_float(scale[i])), z = both(ZEROS ? -static_cast<float>(zero[i]) : -8.0f);
 #pragma unroll
                     for (int b = 0; b < NR / 8; ++b) {   // 8 rows
                         if (b == 1 && it.rows <= 8) break;
-                        const uint32_t at = mine + 64 + (S::kSumBuffers == 2 ? half * S::kSumCols : 0) + i * S::kN + b * 8 * kBlockParts;
-                        uint32_t v[kBlockParts][8];
-#pragma unroll
-                        for (int k = 0; k < kBlockParts; ++k) tmem_load8(at + 8 * k, v[k]);
+                        uint32_t v[8];
+                        tmem_load8(mine + 64 + (S::kSumBuffers == 2 ? half * S::kSumCols : 0) + i * S::kN + b * 8, v);
                         tmem_load_wait();
                         const float* st = stats + s * S::kStats + (half * kGroups + i) * (NR * 2) + b * 16;
 #pragma unroll
                         for (int n = 0; n < 4; ++n) {
-                            uint64_t sum = pair(v[0][2 * n], v[0][2 * n + 1]);
-#pragma unroll
-                            for (int k = 1; k < kBlockParts; ++k) sum = add2(sum, pair(v[k][2 * n], v[k][2 * n + 1]));
+                            const uint64_t sum = pair(v[2 * n], v[2 * n + 1]);
                             const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(st + 4 * n);
                             acc2[b * 4 + n] = fma2(mul2(sc, f.x), fma2(z, f.y, sum), acc2[b * 4 + n]);
                         }

@@ -243,7 +243,7 @@ typedef struct {
  *  y              device, [rows, O or O/2].
  *  workspace      device, 16-byte aligned, ep_expert_w4_workspace bytes;
  *                 contents need no initialising and are not kept.
- * Each input is taken to within 2^-17 of the largest of the group (of
+ * Each input is taken to within 2^-24 of the largest of the group (of
  * group_size inputs) that it is in; products and sums are fp32, a
  * group's scale multiplies the group's sum, and y is rounded once, after the
  * activation. An infinite input makes its row of y NaN. Offsets are taken as

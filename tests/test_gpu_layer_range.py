@@ -78,3 +78,37 @@ def test_attention_sum_of_many_keys_beside_a_large_one(ep, dtype, cache, above):
     tol = want * (relative + above * 4 * F32 + 4096 * F32 + U[dtype] * 1.01) + absolute * N
     within(out[0, 0], want, tol)
     within(lse[0, 0], torch.tensor(above + math.log1p(others), dtype=torch.float64), 4096 * F32 + above * 4 * F32)
+
+
+def experts_beside_large_inputs(counts, I, O, group, dtype, zeros, seed):
+    """x, codes, scales, zero points, offsets and the exact y: one input of each group is 4096 with codes that equal the zero
+    point, the others are odd multiples of a small step. All fp32 sums of these are exact (their 24 bits hold
+    them), so y is the exact sum, rounded once."""
+    bits, step = (8, 2.0 ** -6) if dtype == torch.bfloat16 else (10, 2.0 ** -7)
+    g, rows, E, groups = gen(seed), sum(counts), len(counts), I // group
+    x = (2 * torch.randint(0, 2 ** (bits - 1), (rows, I), generator=g) + 1).double() * step
+    x *= torch.randint(0, 2, (rows, I), generator=g) * 2 - 1
+    at = torch.arange(0, I, group) + torch.randint(0, group, (groups,), generator=g)
+    x[:, at] = 4096.0
+    assert torch.equal(x.to(dtype).double(), x)
+    zero = torch.randint(0, 16, (E, groups, O), generator=g) if zeros else torch.full((E, groups, O), 8)
+    code = torch.randint(0, 16, (E, O, I), generator=g)
+    code[:, :, at] = zero.transpose(1, 2)
+    scale = 2.0 ** torch.randint(-1, 2, (E, groups, O), generator=g).double()
+    dense = (code - zero.transpose(1, 2).repeat_interleave(group, 2)) * scale.transpose(1, 2).repeat_interleave(group, 2)
+    of = torch.repeat_interleave(torch.arange(E), torch.tensor(counts))
+    want = torch.stack([dense[of[r]] @ x[r] for r in range(rows)])
+    off = torch.tensor([0] + list(counts)).cumsum(0).to(torch.int32)
+    return (x.to(dtype).cuda(), (code[..., 0::2] | code[..., 1::2] << 4).to(torch.uint8).cuda(), scale.to(dtype).cuda(),
+            zero.to(torch.uint8).cuda() if zeros else None, off.cuda(), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("counts", [[3, 2, 4, 1], [12], [20, 0, 17]])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_experts_small_inputs_beside_large_ones(ep, dtype, group, counts, zeros):
+    x, w, s, z, off, want = experts_beside_large_inputs(counts, 512, 160, group, dtype, zeros, group + sum(counts))
+    y = torch.empty(want.shape, dtype=dtype, device="cuda")
+    ep.ep_expert_w4(x, w, s, y, expert_offsets=off, zeros=z)
+    assert torch.equal(y.cpu(), want.to(dtype))

@@ -1,13 +1,16 @@
 // The experts' products with 4-bit weights for few rows in all: one kernel,
 // weights straight from memory into registers.
 //
-// Mathematics, as in ep_expert_w4.cu: y[n, o] = sum over groups of
-// s[g, o] * (sum code * x - zero * sum x). Here the products run as mma.sync on
-// fp16 operands with fp32 sums, 16 weight rows by 8 rows of x. A code in the low
-// bits of a half word is the fp16 number code * 2^-24 (subnormal), and so four
-// bits further up 16 times that: eight codes take four masks and one shift, the
-// even inputs' products and the odd ones' being summed apart. fp16 inputs enter
-// as they are; bf16 inputs after a power of two has brought the largest of the
+// Mathematics: y[n, o] = sum over groups of s[g, o] * sum (code - zero) * x, as
+// mma.sync on fp16 operands with fp32 sums, 16 weight rows by 8 rows of x. A code
+// in the low bits of a half word is the fp16 number code * 2^-24 (subnormal), and
+// so four bits further up 16 times that: four masks and one shift part eight
+// codes, and four fused multiply-adds of two halves make (code - zero) * 2^-10 of
+// them, exactly. (The subnormal numbers themselves would do as operands, but the
+// tensor cores add products in 25 bits or so below the largest, and there a
+// subnormal operand counts as 2^-14 whatever its value: beside an input much
+// larger than the others, what falls off the others' products shows.) fp16 inputs
+// enter as they are; bf16 inputs after a power of two has brought the largest of the
 // group to [2^14, 2^15), so that fp16's 10 bits and its subnormals hold every
 // input down to 2^-39 of the largest.
 //
@@ -17,13 +20,16 @@
 // CTA), and a warp has five steps of 16 rows x 128 inputs in flight. A CTA takes
 // whole tiles of 16 rows; its warps share their inputs evenly, end to end over
 // the tiles, and join once for a batch of tiles, in the warps' order.
-// Measured, launches in a graph: 4096 x 4096, 4 rows of fp16: 7.7 us (1.1 TB/s);
-// 8 experts of 4096 x 7168, a row each, with the activation: 29 us (4.2 TB/s),
-// of which about 7 are start and join; the rest, 5.4 TB/s, is the loads' latency and
-// the unpacking instructions (integer ones take two clocks). Two steps of 256
-// inputs in flight: 31.3 us, six of 128 29.0; prefetches of 128 bytes to L2 instead
-// of 256: 30.4. Of an earlier form (32.0): 8, 12, 24 and 32 warps a block instead
-// of 16: 38.6, 34.2, 32.2, 38.8; the codes by TMA into a ring of each warp: 32.1.
+// Measured, launches in a graph: 4096 x 4096, 4 rows of fp16: 7.8 us (1.1 TB/s);
+// 8 experts of 4096 x 7168, a row each, with the activation: 29.9 us (4.1 TB/s),
+// of which about 7 are start and join. The rest runs at 5.1 TB/s with the issue
+// slots half used; the five steps in flight, 80 KB a core, would cover 1.7 us of
+// latency at the memory's rate. Codes as subnormal operands from bits 0 and 4, with
+// the loss above: 28.9 us; from bits 6 to 9, by one more shift for each mask: 31.3.
+// Of earlier forms: two steps of 256 inputs in flight: 31.3 us where six of 128
+// took 29.0, prefetches of 128 bytes to L2 instead of 256: 30.4; 8, 12, 24 and 32
+// warps a block instead of 16: 38.6, 34.2, 32.2, 38.8 where 16 took 32.0; the codes
+// by TMA into a ring of each warp: 32.1.
 #include <math.h>
 #include <string.h>
 
@@ -41,12 +47,10 @@ constexpr int kBatch = 32;               // tiles of a batch at most
 constexpr int kEntries = kFewRows;       // experts with rows: no more than there are rows
 constexpr int kJoinBytes = (kBatch + kWarps - 1) * kTile * 8 * 4;
 
-// Codes in fp16: bits 0 to 3 alone are the subnormal number code * 2^-24, bits 4 to 7 alone 16 times that.
-constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
-constexpr float kUnit = 5.9604644775390625e-8f;
-// Half of these bits go back with a group's power of two, where they cannot overflow, half behind the join: sums over
-// groups so stand for y * 2^-12, normal numbers wherever y is well above the type's smallest.
-constexpr int kHalfBits = 12;
+// Codes in fp16: bits 0 to 3 alone are the subnormal number code * 2^-24, bits 4 to 7 alone 16 times that; two of them
+// brought to code * 2^-kCodeBits.
+constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u, kLowUp = 0x74007400u, kHighUp = 0x64006400u;
+constexpr int kCodeBits = 10;
 
 struct Entry {
     int expert, row, rows, local;   // local: rows of the entries before
@@ -67,6 +71,12 @@ __device__ __forceinline__ void multiply(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(d[0]), "f"(d[1]), "f"(d[2]), "f"(d[3]));
 }
 
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
 // T: type of x, scales and y. GROUP: inputs that share a scale.
 template <typename T, int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, int tiles, int x_stride) {
@@ -77,12 +87,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
     __shared__ int2 found[kEntries];          // expert whose rows begin in this row, and their number
     __shared__ Entry entry[kEntries];
     __shared__ int row_of[kEntries], entries_found;
-    // x: [rows] rows of x_stride bytes, the inputs of a step in the order in which lanes take them; stats: [rows][groups],
-    // 2^12 over the power of two and 2^-24 * sum; join: [slots][16][8]
+    // x: [rows] rows of x_stride bytes, the inputs of a step in the order in which lanes take them; back: [rows][groups],
+    // what a group's sum of products is multiplied with; join: [slots][16][8]
     unsigned char* const inputs = shared_bytes;
     const int groups = a.I / GROUP, blocks = (a.I + kBlock - 1) / kBlock;
-    float2* const stats = reinterpret_cast<float2*>(inputs + a.rows * x_stride);
-    float* const join = reinterpret_cast<float*>(stats + a.rows * groups + (a.rows * groups & 1));
+    float* const back = reinterpret_cast<float*>(inputs + a.rows * x_stride);
+    float* const join = back + (a.rows * groups + 3) / 4 * 4;
     dependent_entry();
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -196,18 +206,19 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
                 for (int u = 0; u < kLoads; ++u) {
                     const int i = i0 + u * kThreads, r = i / per_row, c = i - r * per_row;
                     if (i - lane >= work) break;
-                    float f[8], sum = 0.0f;
-                    int e = 0;
-                    bool finite = true;
+                    float f[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) f[k] = to_float(v[u].v[k]);
-                    if constexpr (!std::is_same_v<T, __half>) {
-                        // (magnitudes in the order of their bits, two to a word; NaN lies above infinity)
-                        const uint4 raw = v[u].raw;
-                        uint32_t big = __vmaxu2(__vmaxu2(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu), __vmaxu2(raw.z & 0x7fff7fffu, raw.w & 0x7fff7fffu));
+                    // (magnitudes in the order of their bits, two to a word; NaN lies above infinity)
+                    const uint4 raw = v[u].raw;
+                    uint32_t big = __vmaxu2(__vmaxu2(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu), __vmaxu2(raw.z & 0x7fff7fffu, raw.w & 0x7fff7fffu));
 #pragma unroll
-                        for (int o = 1; o < GROUP / 8; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(kFullMask, big, o));
-                        const int exponent = static_cast<int>(max(big & 0xffffu, big >> 16) >> 7);   // + 127; subnormal numbers have 0
+                    for (int o = 1; o < GROUP / 8; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(kFullMask, big, o));
+                    big = max(big & 0xffffu, big >> 16);
+                    int e = 0;
+                    bool finite = big < 0x7c00u;   // fp16
+                    if constexpr (!std::is_same_v<T, __half>) {
+                        const int exponent = static_cast<int>(big >> 7);   // + 127; subnormal numbers have 0
                         finite = exponent < 255;
                         e = finite ? min(14 + 127 - exponent, 126) : 0;
                     }
@@ -217,18 +228,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
                     for (int k = 0; k < 4; ++k) {
                         const int from = (k & 1) * 2 + (k >> 1);
                         h[k] = __floats2half2_rn(f[from] * up, f[from + 4] * up);
-                        const float2 is = __half22float2(h[k]);
-                        sum += is.x + is.y;
                     }
-#pragma unroll
-                    for (int o = 1; o < GROUP / 8; o <<= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
                     if (i >= work) continue;
                     const int grp = c / (GROUP / 8), inside = c - grp * (GROUP / 8);
                     uint4 packed;
                     memcpy(&packed, h, 16);
                     *reinterpret_cast<uint4*>(inputs + r * x_stride + (grp * kWords + inside % kWords) * 64 + inside / kWords * 16) = packed;
-                    if (inside == 0)
-                        stats[r * groups + grp] = make_float2(finite ? __int_as_float((127 + kHalfBits - e) << 23) : __int_as_float(0x7fffffff), sum * kUnit);
+                    if (inside == 0) back[r * groups + grp] = __int_as_float(finite ? (127 + kCodeBits - e) << 23 : 0x7fffffff);
                 }
             }
             have0 = row0, have1 = row1;
@@ -239,14 +245,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
         int k = k0, in_entry = entry0, in_tile = tile0, block = step0 - k0 * blocks;
         float total[4] = {};
         const unsigned char* x_at = nullptr;
-        const float2* stats_at[2] = {};
+        const float* back_at[2] = {};
         const auto begin = [&]() {
             const Entry it = entry[in_entry];
             const int local = it.local - row0;
             // (columns past the rows take another's: they are not written)
             x_at = inputs + (local + min(g, it.rows - 1)) * x_stride + t * 16 + block * (kBlock * 2);
-            stats_at[0] = stats + (local + min(2 * t, it.rows - 1)) * groups + block * kGroups;
-            stats_at[1] = stats + (local + min(2 * t + 1, it.rows - 1)) * groups + block * kGroups;
+            back_at[0] = back + (local + min(2 * t, it.rows - 1)) * groups + block * kGroups;
+            back_at[1] = back + (local + min(2 * t + 1, it.rows - 1)) * groups + block * kGroups;
         };
         if (step0 < step1) begin();
         for (int step = step0; step < step1; step += kAhead) {
@@ -256,26 +262,30 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
 #pragma unroll
                 for (int j = 0; j < kGroups; ++j) {
                     if (j > 0 && block * kGroups + j >= groups) break;
-                    float even[4] = {}, odd[4] = {};
+                    float sum[4] = {};
+                    // -zero * 2^-kCodeBits, twice, of the two weight rows
+                    uint32_t nz[2] = {0xa000a000u, 0xa000a000u};
+                    if constexpr (ZEROS) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) nz[k] = fma2(zero[slot][j][k] * 0x00010001u, kLowUp ^ 0x80008000u, 0);
+                    }
 #pragma unroll
                     for (int w = 0; w < kWords; ++w) {
                         const uint4 b = *reinterpret_cast<const uint4*>(x_at + (j * kWords + w) * 64);
                         const uint32_t u0 = codes[slot][j][0][w], u1 = codes[slot][j][1][w];
                         const uint32_t v0 = u0 >> 8, v1 = u1 >> 8;
-                        multiply(even, u0 & kLow, u1 & kLow, v0 & kLow, v1 & kLow, b.x, b.y);
-                        multiply(odd, u0 & kHigh, u1 & kHigh, v0 & kHigh, v1 & kHigh, b.z, b.w);
+                        multiply(sum, fma2(u0 & kLow, kLowUp, nz[0]), fma2(u1 & kLow, kLowUp, nz[1]), fma2(v0 & kLow, kLowUp, nz[0]),
+                                 fma2(v1 & kLow, kLowUp, nz[1]), b.x, b.y);
+                        multiply(sum, fma2(u0 & kHigh, kHighUp, nz[0]), fma2(u1 & kHigh, kHighUp, nz[1]), fma2(v0 & kHigh, kHighUp, nz[0]),
+                                 fma2(v1 & kHigh, kHighUp, nz[1]), b.z, b.w);
                     }
-                    const float2 st[2] = {stats_at[0][j], stats_at[1][j]};
+                    const float bk[2] = {back_at[0][j], back_at[1][j]};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float z = ZEROS ? static_cast<float>(zero[slot][j][i >> 1]) : 8.0f;
-                        const float sum = fmaf(-z, st[i & 1].y, fmaf(odd[i], 0.0625f, even[i]));
-                        total[i] = fmaf(to_float(scale[slot][j][i >> 1]) * st[i & 1].x, sum, total[i]);
-                    }
+                    for (int i = 0; i < 4; ++i) total[i] = fmaf(to_float(scale[slot][j][i >> 1]), sum[i] * bk[i & 1], total[i]);
                 }
                 x_at += kBlock * 2;
-                stats_at[0] += kGroups;
-                stats_at[1] += kGroups;
+                back_at[0] += kGroups;
+                back_at[1] += kGroups;
                 load(slot);
                 if (++block == blocks || step + slot + 1 == step1) {
                     // slot k + warp: warps with later tiles are later ones
@@ -308,8 +318,6 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
                 v0 += from[0];
                 v1 += from[64];
             }
-            v0 *= 1 << kHalfBits;
-            v1 *= 1 << kHalfBits;
             const int col = static_cast<int>((t0 + tile) - static_cast<int64_t>(en) * tiles) * tile_cols + r;
             T* y = static_cast<T*>(a.y) + (it.row + n) * a.y_ld + col;
             if (a.swiglu) {
@@ -326,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
 int row_stride(int I) { return (2 * I + 63) / 128 * 128 + 64; }
 constexpr int kShared = 224 * 1024;
 int64_t shared_bytes_of(const W4Args& a) {
-    return static_cast<int64_t>(a.rows) * (row_stride(a.I) + a.I / a.group * 8) + 8 + kJoinBytes;
+    return static_cast<int64_t>(a.rows) * (row_stride(a.I) + a.I / a.group * 4) + 16 + kJoinBytes;
 }
 
 template <typename T, int GROUP, bool ZEROS>
@@ -365,10 +373,10 @@ cudaError_t launch_type(const W4Args& a, cudaStream_t stream) {
 }  // namespace
 
 // Up to 8 rows, and codes of less than 1 MiB times the group's size. Beyond, the other kernel's higher rate makes up for
-// its second launch and its longer start. This one / the other, us: groups of 128: 4096 x 4096, 4 rows of fp16: 7.8 / 11.8;
-// 8 experts of 4096 x 7168 (117 MB), a bf16 row each: 29.0 / 34.3; one of 65536 x 4096 (134 MB), 4 bf16 rows: 34.4 / 34.2.
-// Groups of 64: 4096 x 4096, 8 rows: 10.0 / 12.7, 117 MB: 37.7 / 36.4. Groups of 32: 2 experts (29 MB): 19.7 / 25.2,
-// 4 experts (59 MB): 29.0 / 28.0, 8 experts: 57.2 / 46.3.
+// its second launch and its longer start. This one / the other, us: groups of 128: 4096 x 4096, 4 rows of fp16: 7.8 / 12.4;
+// 8 experts of 4096 x 7168 (117 MB), a bf16 row each: 29.9 / 34.1; one of 65536 x 4096 (134 MB), 4 bf16 rows: 33.6 / 32.5.
+// Groups of 64: 4096 x 4096, 8 rows: 9.8 / 11.4, 4 experts (59 MB) 21.3 / 21.9, 117 MB: 37.0 / 35.8. Groups of 32: 2 experts
+// (29 MB): 19.1 / 23.7, 4 experts: 28.4 / 26.6, 8 experts: 55.8 / 43.8.
 bool expert_w4_few(const W4Args& a) {
     if (a.rows > kFewRows || shared_bytes_of(a) > kShared) return false;
     const int64_t bytes = static_cast<int64_t>(a.rows < a.E ? a.rows : a.E) * a.O * (a.I / 2);

@@ -105,7 +105,7 @@ def experts_beside_large_inputs(counts, I, O, group, dtype, zeros, seed):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("group", [32, 64, 128])
-@pytest.mark.parametrize("counts", [[3, 2, 4, 1], [12], [20, 0, 17]])
+@pytest.mark.parametrize("counts", [[3, 2, 4, 1], [12], [20, 0, 17], [1], [7], [0, 2, 1, 5]])
 @pytest.mark.parametrize("zeros", [False, True])
 def test_experts_small_inputs_beside_large_ones(ep, dtype, group, counts, zeros):
     x, w, s, z, off, want = experts_beside_large_inputs(counts, 512, 160, group, dtype, zeros, group + sum(counts))

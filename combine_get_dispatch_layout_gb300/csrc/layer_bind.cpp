@@ -91,7 +91,7 @@ void* dense(PyObject* o, at::ScalarType type, std::initializer_list<int64_t> sha
     if (!t->is_contiguous()) refuse("%s must be contiguous", what);
     return address(*t, what);
 }
-// Address and row distance of a tensor whose rows are dense.
+// Address and row distance of a tensor whose rows are dense and apart.
 struct Rows {
     void* at = nullptr;
     int64_t ld = 0;
@@ -103,6 +103,7 @@ Rows rows(const Tensor& t, at::ScalarType type, std::initializer_list<int64_t> s
         if (t.stride(k) != step && t.size(k) != 1) refuse("%s: all but the first dimension must be contiguous", what);
         step *= t.size(k);
     }
+    if (t.size(0) > 1 && t.stride(0) < step) refuse("%s: rows must not overlap", what);
     return {address(t, what), t.size(0) > 1 ? t.stride(0) : (step + 7) / 8 * 8};
 }
 
@@ -252,7 +253,7 @@ long paged_attention(PyObject* const* a) {
     c.num_kv_heads = size_of(n, "kv_heads");
     c.head_dim = size_of(d, "head_dim");
     c.max_pages = size_of(pages, "max_pages");
-    c.q_ld = qr.ld, c.out_ld = o.ld, c.table_ld = t.ld < pages ? pages : t.ld;
+    c.q_ld = qr.ld, c.out_ld = o.ld, c.table_ld = t.ld;
     c.scale = a[8] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(d))) : real(a[8]);
     c.window = small(a[9], "window");
     const Tensor& work = tensor(a[6], "workspace");

@@ -1,0 +1,39 @@
+"""CPU-only checks of the layer operators' binding: what it refuses before the
+library is called. No tensor here has an address that a kernel could use."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def ep():
+    from combine_get_dispatch_layout_gb300.build import build
+    import combine_get_dispatch_layout_gb300 as ep
+
+    build()
+    ep.lib()
+    return ep
+
+
+def empty(*shape, dtype=torch.bfloat16):
+    return torch.empty(*shape, dtype=dtype)
+
+
+def attend(ep, **kw):
+    cache = empty(0, 8, 1, 0)
+    a = dict(q=empty(2, 1, 0), k_cache=cache, v_cache=cache, block_table=empty(2, 0, dtype=torch.int32),
+             seq_lens=empty(0, dtype=torch.int32), out=empty(2, 1, 0), workspace=empty(0, dtype=torch.uint8), stream=0)
+    ep.ep_paged_attention(**{**a, **kw})
+
+
+@pytest.mark.parametrize("table", [torch.zeros(1, 3, dtype=torch.int32).expand(2, 3),
+                                   torch.zeros(8, dtype=torch.int32).as_strided((2, 3), (2, 1))])
+def test_rows_of_a_block_table_that_overlap_are_refused(ep, table):
+    """One table for all sequences, by expand(), has rows no distance apart: the kernel would read past it."""
+    with pytest.raises(ValueError, match="overlap"):
+        attend(ep, block_table=table)
+
+
+def test_other_rows_that_overlap_are_refused(ep):
+    idx, w = empty(2, 1, dtype=torch.int64), empty(2, 1, dtype=torch.float32)
+    with pytest.raises(ValueError, match="overlap"):
+        ep.ep_router_topk(empty(1, 8).expand(2, 8), idx, w, stream=0)

@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
 
@@ -283,17 +284,20 @@ long expert_w4(PyObject* const* a) {
     const Rows y = rows(tensor(a[3], "y"), x.scalar_type(), {n, c.activation == EP_ACT_SWIGLU ? O / 2 : O}, "y");
     c.x_ld = xr.ld, c.y_ld = y.ld;
     Tensor own;
-    void* work;
+    void* work = nullptr;
     int64_t bytes;
     if (const Tensor* t = optional_tensor(a[8], "workspace")) {
+        if (!t->is_cuda()) refuse("workspace must be a CUDA tensor");   // (tensor maps address it)
         if (!t->is_contiguous()) refuse("workspace must be contiguous");
         work = address(*t, "workspace");
         bytes = t->numel() * t->element_size();
     } else {
         if (a[9] != Py_None) refuse("a call on a stream of its own needs a workspace");
         bytes = library.expert_w4_workspace(n, size_of(I, "I"), c.group_size, c.dtype);
-        own = at::empty({bytes > 0 ? bytes : 0}, x.options().dtype(kByte));
-        work = own.data_ptr();
+        if (bytes > 0) {   // (x may be pinned host memory: its options are not the workspace's)
+            own = at::empty({bytes}, at::TensorOptions().dtype(kByte).device(at::kCUDA, c10::cuda::current_device()));
+            work = own.data_ptr();
+        }
     }
     return library.expert_w4(xr.at, n, size_of(I, "I"), static_cast<const uint8_t*>(dense(a[1], kByte, {E, O, I / 2}, "weights")),
                              dense(a[2], x.scalar_type(), {E, groups, O}, "scales"),

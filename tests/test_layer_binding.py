@@ -37,3 +37,10 @@ def test_other_rows_that_overlap_are_refused(ep):
     idx, w = empty(2, 1, dtype=torch.int64), empty(2, 1, dtype=torch.float32)
     with pytest.raises(ValueError, match="overlap"):
         ep.ep_router_topk(empty(1, 8).expand(2, 8), idx, w, stream=0)
+
+
+def test_a_workspace_of_the_host_is_refused(ep):
+    """Kernels that run after the call write it, and address it by tensor maps."""
+    with pytest.raises(ValueError, match="workspace"):
+        ep.ep_expert_w4(empty(0, 128), empty(0, 8, 64, dtype=torch.uint8), empty(0, 1, 8), empty(0, 8),
+                        workspace=empty(0, dtype=torch.uint8), stream=0)

@@ -56,6 +56,21 @@ const Tensor& tensor(PyObject* o, const char* what) {
     if (!t) refuse("%s must be a tensor, got None", what);
     return *t;
 }
+// All CUDA tensors of a call lie on one GPU, the current one: it is that one's stream, cores and limits that the call uses.
+void one_device(PyObject* const* args, Py_ssize_t count) {
+    int first = -1;
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        if (!THPVariable_Check(args[i])) continue;
+        const Tensor& t = THPVariable_Unpack(args[i]);
+        if (!t.is_cuda()) continue;
+        const int device = t.get_device();
+        if (first < 0) first = device;
+        if (device != first) refuse("tensors of one call on cuda:%d and on cuda:%d", first, device);
+    }
+    if (first < 0) return;
+    const int current = c10::cuda::current_device();
+    if (first != current) refuse("tensors on cuda:%d, the current device is cuda:%d", first, current);
+}
 void* address(const Tensor& t, const char* what) {
     if (!t.is_cuda() && t.numel() > 0 && !t.is_pinned()) refuse("%s must be a CUDA tensor or a pinned host tensor", what);
     return t.data_ptr();
@@ -319,6 +334,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t count) {
         return nullptr;
     }
     try {
+        one_device(args, count);
         return PyLong_FromLong(F(args));
     } catch (const Raised&) {
         return nullptr;

@@ -44,3 +44,13 @@ def test_a_workspace_of_the_host_is_refused(ep):
     with pytest.raises(ValueError, match="workspace"):
         ep.ep_expert_w4(empty(0, 128), empty(0, 8, 64, dtype=torch.uint8), empty(0, 1, 8), empty(0, 8),
                         workspace=empty(0, dtype=torch.uint8), stream=0)
+
+
+def test_tensors_on_two_gpus_are_refused(ep):
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    with FakeTensorMode():   # tensors that say where they are and have no memory
+        logits = torch.empty(4, 8, device="cuda:1")
+        idx, w = torch.empty(4, 2, dtype=torch.int64, device="cuda:0"), torch.empty(4, 2, device="cuda:0")
+    with pytest.raises(ValueError, match="cuda:1 and on cuda:0"):
+        ep.ep_router_topk(logits, idx, w, stream=0)

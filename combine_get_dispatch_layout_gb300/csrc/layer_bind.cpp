@@ -137,6 +137,11 @@ int size_of(int64_t n, const char* what) {
     if (n > INT32_MAX) refuse("%s is out of range", what);
     return static_cast<int>(n);
 }
+int truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Raised{};
+    return v;
+}
 float real(PyObject* o) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw Raised{};
@@ -181,7 +186,7 @@ long router_topk(PyObject* const* a) {
     ep_router_config_t c{};
     c.logits_dtype = type_code(logits, "logits", true, false);
     c.score = small(a[4], "score");
-    c.renormalize = PyObject_IsTrue(a[5]);
+    c.renormalize = truth(a[5]);
     c.scale = real(a[6]);
     c.num_groups = small(a[7], "num_groups");
     c.topk_groups = small(a[8], "topk_groups");
@@ -203,7 +208,7 @@ long router_topk_backward(PyObject* const* a) {
     ep_router_config_t c{};
     c.logits_dtype = type_code(logits, "logits", true, false);
     c.score = small(a[4], "score");
-    c.renormalize = PyObject_IsTrue(a[5]);
+    c.renormalize = truth(a[5]);
     c.scale = real(a[6]);
     const Rows l = rows(logits, logits.scalar_type(), {T, E}, "logits");
     const Rows i = rows(idx, kInt64, {T, K}, "topk_idx");
@@ -242,7 +247,7 @@ long kv_append(PyObject* const* a) {
     c.num_kv_heads = size_of(n, "kv_heads");
     c.head_dim = size_of(d, "head_dim");
     c.rotary_dim = size_of(rot, "rotary_dim");
-    c.interleaved = PyObject_IsTrue(a[9]);
+    c.interleaved = truth(a[9]);
     c.q_ld = qr.ld, c.k_ld = kr.ld, c.v_ld = vr.ld, c.q_out_ld = qo.ld;
     c.max_position = most;
     return library.kv_append(qr.at, kr.at, vr.at, static_cast<const int64_t*>(dense(a[3], kInt64, {T}, "positions")),

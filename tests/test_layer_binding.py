@@ -54,3 +54,12 @@ def test_tensors_on_two_gpus_are_refused(ep):
         idx, w = torch.empty(4, 2, dtype=torch.int64, device="cuda:0"), torch.empty(4, 2, device="cuda:0")
     with pytest.raises(ValueError, match="cuda:1 and on cuda:0"):
         ep.ep_router_topk(logits, idx, w, stream=0)
+
+
+def test_an_option_without_a_truth_value_is_refused_before_the_call(ep):
+    logits, idx, w = empty(0, 8), empty(0, 2, dtype=torch.int64), empty(0, 2, dtype=torch.float32)
+    ep.ep_router_topk(logits, idx, w, stream=0)
+    for call in (lambda o: ep.ep_router_topk(logits, idx, w, renormalize=o, stream=0),
+                 lambda o: ep.ep_router_topk_backward(logits, idx, w, logits, renormalize=o, stream=0)):
+        with pytest.raises(RuntimeError, match="ambiguous"):
+            call(torch.tensor([1, 1]))

@@ -84,7 +84,7 @@ def _bind():
         try:
             module = importlib.import_module("._layer_bind", __package__)
         except ImportError as e:
-            raise RuntimeError(f"the layer binding is not built; run {__package__}.build.build()") from e
+            raise RuntimeError(f"the layer binding is not built for this torch ({e}); run {__package__}.build.build()") from e
         module.open(_LIB_PATH)
         _bound = module
     return _bound

@@ -27,10 +27,11 @@ def test_a_block_table_shared_by_expansion_is_refused(ep):
         ep.ep_paged_attention(q, kc, vc, table[:1].expand(2, -1), lens, torch.empty_like(q), work)
 
 
-def test_tensors_on_another_gpu_than_the_current_one_are_refused(ep):
-    from torch._subclasses.fake_tensor import FakeTensorMode
+def test_tensors_on_another_gpu_than_the_current_one_are_refused(ep, monkeypatch):
+    from torch._subclasses import fake_tensor
 
-    with FakeTensorMode():   # tensors that say where they are and have no memory
+    monkeypatch.setattr(fake_tensor, "init_gpu_context", lambda *a: None)   # (the GPU need not exist)
+    with fake_tensor.FakeTensorMode():   # tensors that say where they are and have no memory
         logits, idx = torch.empty(4, 8, device="cuda:1"), torch.empty(4, 2, dtype=torch.int64, device="cuda:1")
         w = torch.empty(4, 2, device="cuda:1")
     with pytest.raises(ValueError, match="current device is cuda:0"):

@@ -46,10 +46,11 @@ def test_a_workspace_of_the_host_is_refused(ep):
                         workspace=empty(0, dtype=torch.uint8), stream=0)
 
 
-def test_tensors_on_two_gpus_are_refused(ep):
-    from torch._subclasses.fake_tensor import FakeTensorMode
+def test_tensors_on_two_gpus_are_refused(ep, monkeypatch):
+    from torch._subclasses import fake_tensor
 
-    with FakeTensorMode():   # tensors that say where they are and have no memory
+    monkeypatch.setattr(fake_tensor, "init_gpu_context", lambda *a: None)   # (the GPUs need not exist)
+    with fake_tensor.FakeTensorMode():   # tensors that say where they are and have no memory
         logits = torch.empty(4, 8, device="cuda:1")
         idx, w = torch.empty(4, 2, dtype=torch.int64, device="cuda:0"), torch.empty(4, 2, device="cuda:0")
     with pytest.raises(ValueError, match="cuda:1 and on cuda:0"):

@@ -131,6 +131,9 @@ __device__ __forceinline__ unsigned kept_groups(uint32_t score, int groups, int 
     return __ballot_sync(kFullMask, lane < groups && before < keep);
 }
 
+// Blocks of `tokens` tokens each.
+dim3 blocks_of(int T, int tokens) { return dim3(static_cast<unsigned>((static_cast<int64_t>(T) + tokens - 1) / tokens)); }
+
 // The weights of the chosen experts (lane k: the k-th, its logit l), and both outputs.
 template <int LANES = 32>
 __device__ __forceinline__ void write_choice(const RouterArgs& a, int t, int lane, int mine, float l, float row_max, float row_sum) {
@@ -152,7 +155,7 @@ template <typename T, int LANES, int V>
 __global__ void __launch_bounds__(32 * kWarps) router_topk_registers_kernel(RouterArgs a) {
     dependent_entry();
     const int lane = threadIdx.x % LANES;
-    const int t = (blockIdx.x * kWarps * 32 + threadIdx.x) / LANES;
+    const int t = blockIdx.x * (kWarps * 32 / LANES) + threadIdx.x / LANES;   // (below 2^31: a block's tokens divide that)
     if ((t & ~(32 / LANES - 1)) >= a.T) return;   // (the warp's first token)
     // lanes past the last token go through the motions on its row
     const T* row = static_cast<const T*>(a.logits) + min(t, a.T - 1) * a.ld;
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(32 * kWarps) router_backward_kernel(RouterBack
 template <typename T, int LANES, int V>
 cudaError_t launch_topk_registers(const RouterArgs& a, cudaStream_t stream) {
     constexpr int kTokens = kWarps * 32 / LANES;
-    return launch_dependent(router_topk_registers_kernel<T, LANES, V>, dim3((a.T + kTokens - 1) / kTokens), dim3(32 * kWarps), 0,
+    return launch_dependent(router_topk_registers_kernel<T, LANES, V>, blocks_of(a.T, kTokens), dim3(32 * kWarps), 0,
                             stream, a);
 }
 
@@ -410,7 +413,7 @@ cudaError_t launch_topk(const RouterArgs& a, cudaStream_t stream) {
     if (a.E <= 128 && fits(4)) return launch_topk_registers<T, 32, 4>(a, stream);
     if (a.E <= 256 && fits(8)) return launch_topk_registers<T, 32, 8>(a, stream);
     if (a.E <= 512 && fits(16)) return launch_topk_registers<T, 32, 16>(a, stream);
-    const dim3 grid((a.T + kWarps - 1) / kWarps), block(32 * kWarps);
+    const dim3 grid = blocks_of(a.T, kWarps), block(32 * kWarps);
     const size_t smem = sizeof(uint32_t) * kWarps * a.E;
     if (smem > 48 * 1024) {
         const cudaError_t err = cudaFuncSetAttribute(router_topk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -427,7 +430,7 @@ cudaError_t launch_backward(const RouterBackwardArgs& a, cudaStream_t stream) {
                    : a.E <= 256 ? router_backward_kernel<T, 8>
                    : a.E <= 512 ? router_backward_kernel<T, 16>
                                 : router_backward_kernel<T, 0>;
-    return launch_dependent(kernel, dim3((a.T + kWarps - 1) / kWarps), dim3(32 * kWarps), 0, stream, a);
+    return launch_dependent(kernel, blocks_of(a.T, kWarps), dim3(32 * kWarps), 0, stream, a);
 }
 
 }  // namespace

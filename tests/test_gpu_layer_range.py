@@ -112,3 +112,30 @@ def test_experts_small_inputs_beside_large_ones(ep, dtype, group, counts, zeros)
     y = torch.empty(want.shape, dtype=dtype, device="cuda")
     ep.ep_expert_w4(x, w, s, y, expert_offsets=off, zeros=z)
     assert torch.equal(y.cpu(), want.to(dtype))
+
+
+def test_router_tokens_past_32_bits_of_threads(ep):
+    """2^27 + 5 tokens, a warp each (groups of two experts): thread numbers pass 2^32."""
+    T, K = (1 << 27) + 5, 2
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB")
+    rows = torch.randn(7, 4, generator=gen(70)).half().cuda()
+    kw = dict(num_groups=2, topk_groups=1, renormalize=False)
+    idx, w = torch.empty(7, K, dtype=torch.int64, device="cuda"), torch.empty(7, K, device="cuda")
+    ep.ep_router_topk(rows, idx, w, **kw)
+    at = torch.arange(T, device="cuda") % 7
+    many_idx, many_w = torch.full((T, K), -7, dtype=torch.int64, device="cuda"), torch.full((T, K), math.nan, device="cuda")
+    ep.ep_router_topk(rows[at], many_idx, many_w, **kw)
+    for k in range(K):
+        assert torch.equal(many_idx[:, k], idx[:, k][at]) and torch.equal(many_w[:, k], w[:, k][at])
+
+
+def test_router_of_as_many_tokens_as_an_int_holds(ep):
+    T = (1 << 31) - 1
+    if torch.cuda.mem_get_info()[0] < 48 << 30:
+        pytest.skip("needs 48 GB")
+    logits = torch.zeros(T, 1, dtype=torch.bfloat16, device="cuda")
+    idx, w = torch.full((T, 1), -7, dtype=torch.int64, device="cuda"), torch.zeros(T, 1, device="cuda")
+    ep.ep_router_topk(logits, idx, w)
+    assert int(idx.min()) == 0 and int(idx.max()) == 0
+    assert float(w.min()) == 1.0 and float(w.max()) == 1.0

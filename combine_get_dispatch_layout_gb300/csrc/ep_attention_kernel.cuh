@@ -378,12 +378,13 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
     };
     const auto look_up = [&]() {
         if (located >= left) return;
+        const int first = low + chunk * kChunk, here = min(kChunk, end - first);   // (first + kChunk may pass 2^31)
 #pragma unroll
         for (int k = 0; k < kLookups; ++k) {
             page_id[k] = -1;
-            const int r = look_row(k), i = low + chunk * kChunk + r;
-            if (r < kChunk && i < end) {
-                const int pg = page_of(p, i);
+            const int r = look_row(k);
+            if (r < here) {
+                const int i = first + r, pg = page_of(p, i);
                 page_id[k] = a.table[seq * a.table_ld + pg];
                 page_place[k] = i - pg * a.page_size;
             }

@@ -9,7 +9,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_layer import F32, U, ep, gen, within  # noqa: F401  (ep: fixture)
+from test_gpu_layer import F32, U, check_attention, ep, gen, randn, within  # noqa: F401  (ep: fixture)
 
 pytestmark = pytest.mark.gpu
 E4M3 = torch.float8_e4m3fn
@@ -139,3 +139,17 @@ def test_router_of_as_many_tokens_as_an_int_holds(ep):
     ep.ep_router_topk(logits, idx, w)
     assert int(idx.min()) == 0 and int(idx.max()) == 0
     assert float(w.min()) == 1.0 and float(w.max()) == 1.0
+
+
+@pytest.mark.parametrize("dtype,cache,d", [(torch.bfloat16, torch.bfloat16, 8), (torch.float16, E4M3, 16), (torch.bfloat16, torch.bfloat16, 256)])
+@pytest.mark.parametrize("short", [0, 1, 100])
+def test_attention_window_at_the_end_of_2_to_the_31_places(ep, dtype, cache, d, short):
+    """The longest table that is taken has 2^31 - 2 places (one page, named 1386 times): in the window's last chunk the places
+    behind the end pass 2^31."""
+    pages, page, g = 1386, 1549411, gen(d + short)
+    assert pages * page == 2 ** 31 - 2
+    kc, vc = (randn(g, 1, page, 1, d).to(cache) for _ in range(2))
+    q = randn(g, 2, 4, d, dtype=dtype)
+    table = torch.zeros(2, pages, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([2 ** 31 - 2 - short, 2 ** 31 - 1], dtype=torch.int64).to(torch.int32).cuda()
+    check_attention(ep, q, kc, vc, table, lens, window=100)

@@ -153,3 +153,23 @@ def test_attention_window_at_the_end_of_2_to_the_31_places(ep, dtype, cache, d, 
     table = torch.zeros(2, pages, dtype=torch.int32, device="cuda")
     lens = torch.tensor([2 ** 31 - 2 - short, 2 ** 31 - 1], dtype=torch.int64).to(torch.int32).cuda()
     check_attention(ep, q, kc, vc, table, lens, window=100)
+
+
+@pytest.mark.parametrize("dtype,cache", CACHES)
+@pytest.mark.parametrize("above", [10, 18, 22])
+def test_attention_sums_beside_a_large_key_in_each_of_many_sequences(ep, dtype, cache, above):
+    """As above, with sequences enough that one block walks over each: what comes after the large key has it as its measure."""
+    B, N, page, d, at = 400, 4096, 64, 64, 3
+    kc, vc = torch.zeros(2, page, 1, d), torch.ones(2, page, 1, d)
+    kc[1, at, 0, 0] = above
+    vc[1, at] = 0.0
+    table = torch.zeros(B, N // page, dtype=torch.int32)
+    table[:, 0] = 1
+    q = torch.zeros(B, 1, d, dtype=dtype)
+    q[:, 0, 0] = 1.0
+    out, _ = attend(ep, q.cuda(), kc.to(cache).cuda(), vc.to(cache).cuda(), table.cuda(),
+                    torch.full((B,), N, dtype=torch.int32, device="cuda"), 1.0)
+    others = (N - 1) * math.exp(-above)
+    want = torch.full((B, d), others / (1 + others), dtype=torch.float64)
+    relative, absolute = weight_unit(cache)
+    within(out[:, 0], want, want * (relative + above * 4 * F32 + N * F32 + U[dtype] * 1.01) + absolute * N + 2.0 ** -25)

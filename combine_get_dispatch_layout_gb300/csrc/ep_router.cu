@@ -335,10 +335,11 @@ __global__ void __launch_bounds__(32 * kWarps) router_backward_kernel(RouterBack
         e64 = a.idx[t * a.idx_ld + lane];
         g = a.grad_w[static_cast<int64_t>(t) * a.K + lane] * a.scale;
     }
-    const bool on = e64 >= 0 && e64 < a.E;
+    // (an expert that the token cannot use has no score and no gradient, even where no other is left)
+    float l = e64 >= 0 && e64 < a.E ? usable(to_float(row[e64])) : -INFINITY;
+    const bool on = l > -INFINITY;
     const int e = on ? static_cast<int>(e64) : -1 - lane;
-    const float l = on ? usable(to_float(row[e])) : 0.0f;
-    if (!on) g = 0.0f;
+    if (!on) g = l = 0.0f;
 
     float m = 0.0f, sum = 1.0f;
     if (dense) {

@@ -81,7 +81,8 @@ EP_API ep_status_t ep_router_topk(const void* logits, int64_t logits_ld, const f
  * ep_router_topk_backward -- grad_logits of a loss with gradient grad_weights
  * [T, K] (fp32) at topk_weights, for the experts in topk_idx ([T, K], rows
  * topk_ld >= K apart: a slice of a full sort serves). (The selection
- * itself is not differentiated; an id outside [0, E) contributes nothing.)
+ * itself is not differentiated; an id outside [0, E), or of an expert whose
+ * logit is NaN or -infinity, contributes nothing.)
  * With g = scale * grad_weights and the scores p of the same logits:
  *   softmax                   p_j ([j chosen] g_j - sum_k g_k p_k), all j
  *   softmax, renormalised     q_j (g_j - sum_k g_k q_k), chosen j, else 0

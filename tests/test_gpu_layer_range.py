@@ -9,7 +9,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_layer import F32, U, check_attention, ep, gen, randn, within  # noqa: F401  (ep: fixture)
+from test_gpu_layer import F32, U, backward_reference, check_attention, ep, gen, randn, within  # noqa: F401  (ep: fixture)
 
 pytestmark = pytest.mark.gpu
 E4M3 = torch.float8_e4m3fn
@@ -173,3 +173,20 @@ def test_attention_sums_beside_a_large_key_in_each_of_many_sequences(ep, dtype, 
     want = torch.full((B, d), others / (1 + others), dtype=torch.float64)
     relative, absolute = weight_unit(cache)
     within(out[:, 0], want, want * (relative + above * 4 * F32 + N * F32 + U[dtype] * 1.01) + absolute * N + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("score,renorm", [(0, True), (0, False), (1, True), (1, False)])
+def test_router_backward_of_experts_that_cannot_be_used(ep, score, renorm):
+    """topk_idx may name experts that are masked (a routing made before the mask): they have no score and no gradient, in
+    rows where nothing is left too."""
+    E, K = 40, 4
+    logits, grad_w = randn(gen(80), 5, E), randn(gen(81), 5, K)
+    idx = torch.tensor([[0, 1, 2, 3], [39, 5, 5, 7], [4, 5, 6, 7], [8, 9, 10, 11], [-1, -1, -1, -1]])
+    logits[0], logits[1], logits[4] = -math.inf, math.nan, -math.inf
+    logits[2, 4:8] = -math.inf
+    logits[3, 8], logits[3, 11] = -math.inf, math.nan
+    grad = torch.full_like(logits, math.nan)
+    ep.ep_router_topk_backward(logits, idx.cuda(), grad_w, grad, score=score, renormalize=renorm)
+    want = torch.zeros(5, E, dtype=torch.float64)
+    want[3] = backward_reference(logits[3:4], idx[3:4], grad_w[3:4], score, renorm, 1.0)[0]
+    within(grad, want, 1e-5)

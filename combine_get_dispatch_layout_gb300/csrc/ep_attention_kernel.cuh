@@ -97,7 +97,8 @@ __device__ Share find_share(const AttentionArgs& a, const Plan& p) {
     __shared__ int64_t found_before[2], found_chunks[2];
     __shared__ int found[2];
     const int tid = threadIdx.x, lane = tid & 31;
-    const int per = (a.B + THREADS - 1) / THREADS, first = min(a.B, tid * per), last = min(a.B, first + per);
+    // (a.B may be 2^31 - 1: no sum here passes it)
+    const int per = (a.B - 1) / THREADS + 1, first = min(a.B, tid * per), last = first + min(per, a.B - first);
     const auto places = [](int n) { return n > 0 ? n + kBegin : 0; };
     int64_t own = 0, own_chunks = 0;
     int low, end;
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
     if (p.split) {
         const Share share = find_share<kThreads, kChunk>(a, p);
         // sequences without keys: zeros
-        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        for (unsigned b = blockIdx.x; b < static_cast<unsigned>(a.B); b += gridDim.x) {
             if (sequence<kChunk>(a, b, low, end) > 0) continue;
             for (int i = tid; i < a.num_heads * D; i += kThreads)
                 static_cast<T*>(a.out)[b * a.out_ld + i] = from_float<T>(0.0f);

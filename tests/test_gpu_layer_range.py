@@ -190,3 +190,26 @@ def test_router_backward_of_experts_that_cannot_be_used(ep, score, renorm):
     want = torch.zeros(5, E, dtype=torch.float64)
     want[3] = backward_reference(logits[3:4], idx[3:4], grad_w[3:4], score, renorm, 1.0)[0]
     within(grad, want, 1e-5)
+
+
+def test_attention_of_as_many_sequences_as_an_int_holds(ep):
+    """2^31 - 1 sequences of one head, three of them with keys: the blocks' walk over the sequences ends, and finds them all."""
+    B, page, d = (1 << 31) - 1, 1024, 8
+    if torch.cuda.mem_get_info()[0] < 120 << 30:
+        pytest.skip("needs 120 GB")
+    g = gen(90)
+    kc, vc = (randn(g, 3, page, 1, d).bfloat16() for _ in range(2))
+    some = torch.tensor([5, 1 << 30, B - 1])
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    table = torch.zeros(B, 1, dtype=torch.int32, device="cuda")
+    q, out = torch.zeros(B, 1, d, dtype=torch.bfloat16, device="cuda"), torch.ones(B, 1, d, dtype=torch.bfloat16, device="cuda")
+    few = dict(q=randn(g, 3, 1, d, dtype=torch.bfloat16), lens=torch.tensor([1000, 3, 700], dtype=torch.int32, device="cuda"),
+               table=torch.tensor([[2], [0], [1]], dtype=torch.int32, device="cuda"))
+    at = some.cuda()
+    lens[at], table[at], q[at] = few["lens"], few["table"], few["q"]
+    work = torch.empty(ep.ep_paged_attention_workspace(q, kc, table), dtype=torch.uint8, device="cuda")
+    ep.ep_paged_attention(q, kc, vc, table, lens, out, work)
+    want = check_attention(ep, few["q"], kc, vc, few["table"], few["lens"])
+    assert bool(((out[at].float() - want.float()).abs() <= want.float().abs() * 2.0 ** -6 + 1e-6).all())
+    out[at] = 0
+    assert not bool(out.view(torch.int64).any())

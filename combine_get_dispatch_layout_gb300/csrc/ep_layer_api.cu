@@ -117,6 +117,8 @@ ep_status_t ep_kv_append(const void* q, const void* k, const void* v, const int6
         config->num_kv_heads < 1 || !cache_ok(cache, config->dtype, D) || !aligned(device_error, 4) ||
         (rot > 0 && config->max_position < 1))
         return EP_ERR_INVALID_ARG;
+    const bool fp8 = cache->dtype == EP_DTYPE_FP8_E4M3;
+    if (fp8 && !(std::isfinite(1.0f / cache->k_scale) && std::isfinite(1.0f / cache->v_scale))) return EP_ERR_INVALID_ARG;
     const int64_t q_row = static_cast<int64_t>(config->num_heads) * D, kv_row = static_cast<int64_t>(config->num_kv_heads) * D;
     if (q_row + 2 * kv_row >= (int64_t{1} << 28) || config->k_ld < kv_row || config->v_ld < kv_row ||
         config->k_ld % 8 != 0 || config->v_ld % 8 != 0)
@@ -165,7 +167,6 @@ ep_status_t ep_kv_append(const void* q, const void* k, const void* v, const int6
     a.v_page = cache->v_page_stride;
     a.v_slot = cache->v_slot_stride;
     a.v_head = cache->v_head_stride;
-    const bool fp8 = cache->dtype == EP_DTYPE_FP8_E4M3;
     a.k_inv_scale = fp8 ? 1.0f / cache->k_scale : 1.0f;
     a.v_inv_scale = fp8 ? 1.0f / cache->v_scale : 1.0f;
     a.error = device_error;

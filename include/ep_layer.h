@@ -153,7 +153,8 @@ typedef struct {
  *                 rows are zero.
  * A pair (a, b) becomes (a cos - b sin, b cos + a sin), in fp32, rounded once
  * to the output type. An e4m3 cache stores round-to-nearest-even of
- * value * (1 / scale), saturating at +-448, NaN kept.
+ * value * (1 / scale), saturating at +-448, NaN kept; a scale whose reciprocal
+ * is not finite in fp32 is refused.
  */
 EP_API ep_status_t ep_kv_append(const void* q, const void* k, const void* v, const int64_t* positions,
                                 const int64_t* slots, const float* cos_sin, int T,

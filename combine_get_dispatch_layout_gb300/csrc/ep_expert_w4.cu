@@ -758,7 +758,7 @@ cudaError_t launch_group(const W4Args& a, void* workspace, int dtype, cudaStream
     if (err != cudaSuccess) return err;
     // rows of an item: 8, or 16 where experts have more than 4 rows on average: a second pass over a tile costs more than
     // columns that stay empty (256 tokens, 8 rows an expert: 935 us with 8, 773 with 16 when that was measured)
-    const int used = a.rows < a.E ? a.rows : a.E, mean = (a.rows + used - 1) / used;
+    const int used = a.rows < a.E ? a.rows : a.E, mean = (a.rows - 1) / used + 1;
     if constexpr (kParts<T> == 2)
         if (mean <= 4 || a.rows <= 8)
             return a.zeros ? launch_shape<T, 8, GROUP, true>(a, x, stats, stream) : launch_shape<T, 8, GROUP, false>(a, x, stats, stream);

@@ -22,6 +22,8 @@ inline bool half_type(int d) { return d == EP_DTYPE_BF16 || d == EP_DTYPE_FP16; 
 inline bool router_type(int d) { return half_type(d) || d == EP_DTYPE_FP32; }
 inline size_t type_bytes(int d) { return d == EP_DTYPE_FP32 ? 4 : d == EP_DTYPE_FP8_E4M3 ? 1 : 2; }
 
+constexpr int kMostSide = INT32_MAX - 511;   // rows, inputs and outputs of the experts: whole tiles of them are counted in an int
+
 bool router_config_ok(const ep_router_config_t* c) {
     return c && router_type(c->logits_dtype) && (c->score == EP_SCORE_SOFTMAX || c->score == EP_SCORE_SIGMOID) &&
            std::isfinite(c->scale);
@@ -239,8 +241,8 @@ ep_status_t ep_paged_attention(const void* q, const void* k_cache, const void* v
 }
 
 int64_t ep_expert_w4_workspace(int64_t rows, int I, int group_size, int dtype) {
-    if (rows < 0 || rows >= (int64_t{1} << 31) || (group_size != 32 && group_size != 64 && group_size != 128) ||
-        I < group_size || I % group_size != 0 || !half_type(dtype))
+    if (rows < 0 || rows > kMostSide || (group_size != 32 && group_size != 64 && group_size != 128) ||
+        I < group_size || I > kMostSide || I % group_size != 0 || !half_type(dtype))
         return -1;
     return ep::expert_w4_workspace(rows, I, group_size, dtype);
 }
@@ -250,12 +252,13 @@ ep_status_t ep_expert_w4(const void* x, int64_t rows, int I, const uint8_t* weig
                          int O, const ep_w4_config_t* config, void* y, void* workspace, int64_t workspace_bytes,
                          void* stream) {
     ApiRange range("ep_expert_w4");
-    if (!config || !half_type(config->dtype) || rows < 0 || rows >= (int64_t{1} << 31)) return EP_ERR_INVALID_ARG;
+    if (!config || !half_type(config->dtype) || rows < 0) return EP_ERR_INVALID_ARG;
     const int group = config->group_size;
     const bool swiglu = config->activation == EP_ACT_SWIGLU;
     if ((group != 32 && group != 64 && group != 128) || I < group || I % group != 0 || O < 1 ||
         (!swiglu && config->activation != EP_ACT_NONE) || (swiglu && O % 2 != 0) || E < 1 || E > EP_MAX_EXPERTS)
         return EP_ERR_INVALID_ARG;
+    if (rows > kMostSide || I > kMostSide || O > kMostSide) return EP_ERR_INVALID_ARG;
     if (config->x_ld < I || config->x_ld % 8 != 0 || config->y_ld < (swiglu ? O / 2 : O)) return EP_ERR_INVALID_ARG;
     if (!expert_offsets && (E != 1 || expert_counts)) return EP_ERR_INVALID_ARG;
     if (rows == 0) return EP_OK;

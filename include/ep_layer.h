@@ -249,7 +249,7 @@ typedef struct {
  * group_size inputs) that it is in; products and sums are fp32, a
  * group's scale multiplies the group's sum, and y is rounded once, after the
  * activation. An infinite input makes its row of y NaN. Offsets are taken as
- * at most `rows`; rows < 2^31.
+ * at most `rows`; rows, I and O are at most 2^31 - 512.
  */
 EP_API ep_status_t ep_expert_w4(const void* x, int64_t rows, int I, const uint8_t* weights, const void* scales,
                                 const uint8_t* zeros, const int32_t* expert_offsets, const int32_t* expert_counts,

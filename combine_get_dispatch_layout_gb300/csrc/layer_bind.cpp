@@ -60,7 +60,8 @@ const Tensor& tensor(PyObject* o, const char* what) {
 void one_device(PyObject* const* args, Py_ssize_t count) {
     int first = -1;
     for (Py_ssize_t i = 0; i < count; ++i) {
-        if (!THPVariable_Check(args[i])) continue;
+        // (numbers and None first: that something is no tensor takes 0.1 us to find out otherwise)
+        if (args[i] == Py_None || PyLong_Check(args[i]) || PyFloat_Check(args[i]) || !THPVariable_Check(args[i])) continue;
         const Tensor& t = THPVariable_Unpack(args[i]);
         if (!t.is_cuda()) continue;
         const int device = t.get_device();

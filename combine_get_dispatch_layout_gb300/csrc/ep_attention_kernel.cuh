@@ -23,10 +23,10 @@
 // sequence and head) ends.
 //
 // Measured, launches in a graph, join kernel included, heads of 128: one
-// sequence of 131071 keys, 8 cache heads, bf16: 86.7 us (6.2 TB/s); 64 of up to
-// 4096 keys, 64 query heads: 88.9 us (5.7 TB/s); 128 of up to 8192 over an e4m3
-// cache: 167 us (6.0 TB/s), all of 8192: 330 us (6.5 TB/s); one of 129 keys:
-// 6.3 us. What is over the time at the full rate is start, join and each
+// sequence of 131071 keys, 8 cache heads, bf16: 86.9 us (6.2 TB/s); 64 of up to
+// 4096 keys, 64 query heads: 89.1 us (5.7 TB/s), fp16 the same; 128 of up to 8192
+// over an e4m3 cache: 174 us (5.8 TB/s), all of 8192: 340 us (6.3 TB/s); one of 129
+// keys: 6.4 us. What is over the time at the full rate is start, join and each
 // segment's end: 15 us (20 with e4m3) where a CTA has 3 or 4 segments.
 #pragma once
 
@@ -78,7 +78,7 @@ __device__ __forceinline__ int64_t share_start(int64_t W, int ctas, int i) { ret
 // All sequences' units laid end to end, a unit of n chunks as kBegin + n places: to begin and to end one takes a CTA as
 // long as kBegin chunks, and with sequences of very different lengths equal shares of the chunks alone let those with
 // many short ones wait. (128 sequences of up to 8192 e4m3 keys, 8 heads: kBegin of 0, 1, 2, 3, 4:
-// 188, 179, 170, 168, 170 us; 64 of up to 4096 bf16 keys: 99.0, 88.6, 89.1, 89.6, 89.8 us.)
+// 188, 177, 174, 176, 178 us; 64 of up to 4096 bf16 keys: 97.9, 88.9, 88.9, 88.8, 89.9 us.)
 constexpr int kBegin = 2;
 
 struct Share {
@@ -246,7 +246,7 @@ struct Shape {
     using M = std::conditional_t<FP8, __half, T>;   // type of the products' operands
     static constexpr int kHeads = 8 * NT;
     // Warps: kKeyWarps shares of a chunk's keys times NT eights of heads. Codes have to be unpacked for half the
-    // bytes, so an e4m3 cache gets more warps (8: 169.6 us, 4: 170.7 us for 128 sequences of up to 8192).
+    // bytes, so an e4m3 cache gets more warps (8: 174.4 us, 4: 176.4 us for 128 sequences of up to 8192).
     static constexpr int kKeyWarps = FP8 && NT == 1 && DP <= 128 ? 8 : 4;
     static constexpr int kThreads = 32 * kKeyWarps * NT;
     static constexpr int kCacheBytes = FP8 ? 1 : 2;
@@ -661,7 +661,8 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
             for (int m = 0; m < DP / 16; ++m) o[m][0] *= fade[0], o[m][1] *= fade[1], o[m][2] *= fade[0], o[m][3] *= fade[1];
         }
         // A weight is taken as the sum of two: rounded once, its 8 or 11 bits would add as much error as the output's.
-        // (Over an e4m3 cache the second product costs at most 1 %: 182.4 us with one, 183.1 with both, 128 sequences.)
+        // (Over an e4m3 cache the second product costs 4 %: 167.3 us with one, 174.4 with both, 128 sequences of up to 8192;
+        // over a 16-bit one nothing.)
         constexpr int kWeightParts = 2;
         uint32_t pf[kTiles][kWeightParts][2];
         // (nothing seen yet: all weights 0)

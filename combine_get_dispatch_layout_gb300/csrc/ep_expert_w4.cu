@@ -45,6 +45,8 @@
 // columns of one product instead: 706 (822, 1036; 779). Clusters of up to 16 instead of 8: 19.9 us against
 // 12.0 for one 4096 x 4096 matrix.
 
+#include <cuda.h>
+
 #include <type_traits>
 
 #include "ep_w4.cuh"
@@ -101,6 +103,47 @@ struct Plan {
 
 // ------------------------------------------------------------------ PTX
 
+// Shared memory barriers (mbarrier) and asynchronous copies.
+__device__ __forceinline__ void barrier_init(uint32_t bar, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void barrier_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void barrier_expect(uint32_t bar, int bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+// Every wait ends: after far more tries than any load takes, `dead` is set, the CTA runs through the rest
+// without waiting, and its outputs are NaN.
+static __device__ __noinline__ void barrier_wait_long(uint32_t bar, uint32_t parity, volatile int* dead) {
+    for (int i = 0; i < (1 << 22); ++i) {
+        if (barrier_try(bar, parity)) return;
+        if ((i & 1023) == 1023 && *dead) return;
+    }
+    *dead = 1;
+}
+__device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+    if (!barrier_try(bar, parity)) barrier_wait_long(bar, parity, dead);
+}
+// Arrives once this thread's copies so far are complete.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, int real) {   // zeros where real is 0
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
 }
@@ -658,6 +701,21 @@ EncodeFn encoder() {
     return fn;
 }
 
+// Bytes [w][z][y][x] (x: 16-byte multiples), read in boxes of 128 x box_y x box_z with the 128-byte swizzle; zeros past the ends.
+cudaError_t byte_map(CUtensorMap* map, const void* base, int64_t x, int64_t y, int64_t z, int64_t w, int box_y, int box_z) {
+    const EncodeFn encode = encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(x), static_cast<cuuint64_t>(y), static_cast<cuuint64_t>(z),
+                                static_cast<cuuint64_t>(w)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(x), static_cast<cuuint64_t>(x * y), static_cast<cuuint64_t>(x * y * z)};
+    const cuuint32_t box[4] = {128, static_cast<cuuint32_t>(box_y), static_cast<cuuint32_t>(box_z), 1}, step[4] = {1, 1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
 // A device's SMs, and how many clusters of 2, 4 and 8 CTAs of a kernel it holds at once.
 struct Room {
     int sms, clusters[3];
@@ -773,20 +831,6 @@ cudaError_t launch_type(const W4Args& a, void* workspace, int dtype, cudaStream_
 }
 
 }  // namespace
-
-cudaError_t byte_map(CUtensorMap* map, const void* base, int64_t x, int64_t y, int64_t z, int64_t w, int box_y, int box_z) {
-    const EncodeFn encode = encoder();
-    if (!encode) return cudaErrorNotSupported;
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(x), static_cast<cuuint64_t>(y), static_cast<cuuint64_t>(z),
-                                static_cast<cuuint64_t>(w)};
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(x), static_cast<cuuint64_t>(x * y), static_cast<cuuint64_t>(x * y * z)};
-    const cuuint32_t box[4] = {128, static_cast<cuuint32_t>(box_y), static_cast<cuuint32_t>(box_z), 1}, step[4] = {1, 1, 1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? cudaSuccess
-               : cudaErrorInvalidValue;
-}
 
 int64_t expert_w4_workspace(int64_t rows, int I, int group, int dtype) {
     return (rows * (I / group) * 8 + 15) / 16 * 16 + split_bytes(rows, I, dtype);

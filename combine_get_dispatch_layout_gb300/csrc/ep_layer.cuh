@@ -36,42 +36,7 @@ union Vec8 {
     T v[8];
 };
 
-// ---- shared memory barriers (mbarrier) and asynchronous copies
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-
-__device__ __forceinline__ void barrier_init(uint32_t bar, int count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void barrier_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void barrier_expect(uint32_t bar, int bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(done)
-                 : "r"(bar), "r"(parity)
-                 : "memory");
-    return done != 0;
-}
-// Every wait ends: after far more tries than any load takes, `dead` is set, the CTA runs through the rest
-// without waiting, and its outputs are NaN.
-static __device__ __noinline__ void barrier_wait_long(uint32_t bar, uint32_t parity, volatile int* dead) {
-    for (int i = 0; i < (1 << 22); ++i) {
-        if (barrier_try(bar, parity)) return;
-        if ((i & 1023) == 1023 && *dead) return;
-    }
-    *dead = 1;
-}
-__device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
-    if (!barrier_try(bar, parity)) barrier_wait_long(bar, parity, dead);
-}
-// Arrives once this thread's copies so far are complete.
-__device__ __forceinline__ void copies_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
 
 struct RouterArgs {
     const void* logits;

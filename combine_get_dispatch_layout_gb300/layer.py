@@ -28,6 +28,9 @@ EXPORTS = ("ep_router_topk", "ep_router_topk_backward", "ep_kv_append", "ep_page
 _i32, _i64, _f32, _P = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
 
+# The C ABI's structures and argument types, for callers through ctypes (and for the check that they match the header);
+# the functions below go through the compiled marshalling.
+
 class RouterConfig(ctypes.Structure):
     """ep_router_config_t (include/ep_layer.h)."""
     _fields_ = [("logits_dtype", _i32), ("score", _i32), ("renormalize", _i32), ("scale", _f32),

@@ -22,8 +22,8 @@
 // the tiles, and join once for a batch of tiles, in the warps' order.
 // Measured, launches in a graph: 4096 x 4096, 4 rows of fp16: 7.8 us (1.1 TB/s);
 // 8 experts of 4096 x 7168, a row each, with the activation: 29.9 us (4.1 TB/s),
-// of which about 7 are start and join. The rest runs at 5.1 TB/s with the issue
-// slots half used; the five steps in flight, 80 KB a core, would cover 1.7 us of
+// of which about 7 are start and join. The rest runs at 5.1 TB/s with 55 % of
+// the issue slots used; the five steps in flight, 80 KB a core, would cover 1.7 us of
 // latency at the memory's rate. Codes as subnormal operands from bits 0 and 4, with
 // the loss above: 28.9 us; from bits 6 to 9, by one more shift for each mask: 31.3.
 // Of earlier forms: two steps of 256 inputs in flight: 31.3 us where six of 128

@@ -25,7 +25,7 @@
 // Measured, launches in a graph, join kernel included, heads of 128: one
 // sequence of 131071 keys, 8 cache heads, bf16: 86.9 us (6.2 TB/s); 64 of up to
 // 4096 keys, 64 query heads: 89.1 us (5.7 TB/s), fp16 the same; 128 of up to 8192
-// over an e4m3 cache: 174 us (5.8 TB/s), all of 8192: 340 us (6.3 TB/s); one of 129
+// over an e4m3 cache: 173 us (5.9 TB/s), all of 8192: 337 us (6.4 TB/s); one of 129
 // keys: 6.4 us. What is over the time at the full rate is start, join and each
 // segment's end: 15 us (20 with e4m3) where a CTA has 3 or 4 segments.
 #pragma once
@@ -50,6 +50,7 @@ struct Plan {
     int blocks;      // head blocks per cache head
     unsigned page_mul, page_shift;  // i / page_size = (umulhi(i, page_mul) + ...) as page_of
     float out_scale; // of O / l
+    float lift;      // the parts' sums are 2^lift times as large
     int by_unit;     // join blocks belong to units (else to the CTAs a unit began in)
 };
 
@@ -78,7 +79,7 @@ __device__ __forceinline__ int64_t share_start(int64_t W, int ctas, int i) { ret
 // All sequences' units laid end to end, a unit of n chunks as kBegin + n places: to begin and to end one takes a CTA as
 // long as kBegin chunks, and with sequences of very different lengths equal shares of the chunks alone let those with
 // many short ones wait. (128 sequences of up to 8192 e4m3 keys, 8 heads: kBegin of 0, 1, 2, 3, 4:
-// 188, 177, 174, 176, 178 us; 64 of up to 4096 bf16 keys: 97.9, 88.9, 88.9, 88.8, 89.9 us.)
+// 187, 175, 173, 174, 176 us; 64 of up to 4096 bf16 keys: 98.1, 88.7, 89.1, 89.1, 89.8 us.)
 constexpr int kBegin = 2;
 
 struct Share {
@@ -213,6 +214,9 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     }
 }
 
+// Weights that enter the products as M are 2^lift times as large.
+template <typename M>
+__host__ __device__ constexpr float lift() { return std::is_same_v<M, __half> ? 11.0f : 0.0f; }
 template <typename M>
 __device__ __forceinline__ float2 apart(uint32_t w) {
     if constexpr (std::is_same_v<M, __half>) return __half22float2(*reinterpret_cast<const __half2*>(&w));
@@ -246,7 +250,7 @@ struct Shape {
     using M = std::conditional_t<FP8, __half, T>;   // type of the products' operands
     static constexpr int kHeads = 8 * NT;
     // Warps: kKeyWarps shares of a chunk's keys times NT eights of heads. Codes have to be unpacked for half the
-    // bytes, so an e4m3 cache gets more warps (8: 174.4 us, 4: 176.4 us for 128 sequences of up to 8192).
+    // bytes, so an e4m3 cache gets more warps (8: 172.6 us, 4: 173.9 us for 128 sequences of up to 8192).
     static constexpr int kKeyWarps = FP8 && NT == 1 && DP <= 128 ? 8 : 4;
     static constexpr int kThreads = 32 * kKeyWarps * NT;
     static constexpr int kCacheBytes = FP8 ? 1 : 2;
@@ -625,7 +629,7 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
         // the weights refer to follows the running one only when a score passes it by more than kSlack: most chunks
         // need no exchange between lanes. An fp16 weight is 2^kLift times as large, below 2^15 then, so that fp16 has
         // its full precision down to 2^-25 of the largest weight: many keys far below one of them still add up.
-        constexpr float kSlack = std::is_same_v<M, __half> ? 4.0f : 8.0f, kLift = std::is_same_v<M, __half> ? 11.0f : 0.0f;
+        constexpr float kSlack = std::is_same_v<M, __half> ? 4.0f : 8.0f, kLift = lift<M>();
 #pragma unroll
         for (int kt = 0; kt < kTiles; ++kt)
 #pragma unroll
@@ -661,17 +665,17 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
             for (int m = 0; m < DP / 16; ++m) o[m][0] *= fade[0], o[m][1] *= fade[1], o[m][2] *= fade[0], o[m][3] *= fade[1];
         }
         // A weight is taken as the sum of two: rounded once, its 8 or 11 bits would add as much error as the output's.
-        // (Over an e4m3 cache the second product costs 4 %: 167.3 us with one, 174.4 with both, 128 sequences of up to 8192;
+        // (Over an e4m3 cache the second product costs 3 %: 167.3 us with one, 172.6 with both, 128 sequences of up to 8192;
         // over a 16-bit one nothing.)
         constexpr int kWeightParts = 2;
         uint32_t pf[kTiles][kWeightParts][2];
         // (nothing seen yet: all weights 0)
-        const float base[2] = {top[0] == -INFINITY ? 0.0f : top[0] - kLift, top[1] == -INFINITY ? 0.0f : top[1] - kLift};
+        const float base[2] = {top[0] == -INFINITY ? 0.0f : top[0], top[1] == -INFINITY ? 0.0f : top[1]};
 #pragma unroll
         for (int kt = 0; kt < kTiles; ++kt) {
             float pr[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) pr[j] = exp2_fast(s[kt][j] - base[j & 1]);
+            for (int j = 0; j < 4; ++j) pr[j] = exp2_fast((s[kt][j] - base[j & 1]) + kLift);   // (in this order: at most kSlack + kLift)
             sum[0] += pr[0] + pr[2];
             sum[1] += pr[1] + pr[3];
 #pragma unroll
@@ -722,7 +726,6 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
                 sum[j] += __shfl_xor_sync(kFullMask, sum[j], 4);
                 sum[j] += __shfl_xor_sync(kFullMask, sum[j], 8);
                 sum[j] += __shfl_xor_sync(kFullMask, sum[j], 16);
-                top[j] -= kLift;
                 if (g == 0) sh.top[head0 + j][warp] = top[j];
             }
             __syncthreads();
@@ -776,7 +779,7 @@ __global__ void __launch_bounds__((Shape<T, FP8, DP, NT>::kThreads)) attention_k
                     }
                     if (d == 0 && a.lse)
                         a.lse[static_cast<int64_t>(in.seq) * a.num_heads + h0 + h] =
-                            l == 0.0f ? -INFINITY : 0.6931471805599453f * (largest() + log2f(l));
+                            l == 0.0f ? -INFINITY : 0.6931471805599453f * (largest() + (log2f(l) - lift<M>()));
                 } else {
                     *reinterpret_cast<float4*>(to + h * DP + d) = x;
                     if (d == 0) to[S::kHeads * DP + 2 * h] = largest(), to[S::kHeads * DP + 2 * h + 1] = l;
@@ -837,7 +840,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionArgs a, Pla
             *reinterpret_cast<uint2*>(out) = make_uint2(pack<T>(x.x * r, x.y * r), pack<T>(x.z * r, x.w * r));
         }
         if (v == 0 && a.lse)
-            a.lse[static_cast<int64_t>(cut.seq) * a.num_heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+            a.lse[static_cast<int64_t>(cut.seq) * a.num_heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m + (log2f(l) - p.lift));
     };
     if (!p.by_unit && parts <= kFew) {
         if (blockIdx.y != 0) return;
@@ -959,6 +962,7 @@ cudaError_t launch_type(const AttentionArgs& a, int sms, cudaStream_t stream) {
     p.blocks = (group + 8 * nt - 1) / (8 * nt);
     p.units = a.num_kv_heads * p.blocks;
     p.out_scale = FP8 ? a.v_scale : 1.0f;
+    p.lift = lift<std::conditional_t<FP8, __half, T>>();
     int log = 0;
     while ((int64_t{1} << log) < a.page_size) ++log;
     p.page_shift = 31 + log;

@@ -9,7 +9,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_layer import F32, U, backward_reference, check_attention, ep, gen, randn, within  # noqa: F401  (ep: fixture)
+from test_gpu_layer import F32, U, attention_inputs, backward_reference, check_attention, ep, gen, randn, within  # noqa: F401  (ep: fixture)
 
 pytestmark = pytest.mark.gpu
 E4M3 = torch.float8_e4m3fn
@@ -213,3 +213,12 @@ def test_attention_of_as_many_sequences_as_an_int_holds(ep):
     assert bool(((out[at].float() - want.float()).abs() <= want.float().abs() * 2.0 ** -6 + 1e-6).all())
     out[at] = 0
     assert not bool(out.view(torch.int64).any())
+
+
+@pytest.mark.parametrize("dtype,cache", CACHES)
+@pytest.mark.parametrize("scale", [2.0 ** 14, 2.0 ** 19, 2.0 ** 21, 2.0 ** 22, 2.0 ** 23, 2.0 ** 24])
+def test_attention_scores_of_many_millions(ep, dtype, cache, scale):
+    """Scores whose unit in the last place is above 1: one key takes all the weight, and nothing overflows on the way."""
+    q, kc, vc, table, lens = attention_inputs(95, [300, 70, 1], 8, 2, 64, 16, dtype, cache)
+    out = check_attention(ep, q, kc, vc, table, lens, scale=scale)
+    assert bool(out.isfinite().all())

@@ -281,7 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_w4_few_kernel(W4Args a, in
                     }
                     const float bk[2] = {back_at[0][j], back_at[1][j]};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) total[i] = fmaf(to_float(scale[slot][j][i >> 1]), sum[i] * bk[i & 1], total[i]);
+                    for (int i = 0; i < 4; ++i)   // (the scale first: a group's sum by itself may pass fp32's range)
+                        total[i] = fmaf(to_float(scale[slot][j][i >> 1]) * bk[i & 1], sum[i], total[i]);
                 }
                 x_at += kBlock * 2;
                 back_at[0] += kGroups;

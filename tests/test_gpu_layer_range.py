@@ -9,7 +9,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_layer import F32, U, attention_inputs, backward_reference, check_attention, ep, gen, randn, within  # noqa: F401  (ep: fixture)
+from test_gpu_layer import F32, U, attention_inputs, backward_reference, check_attention, ep, experts_inputs, gen, randn, within  # noqa: F401  (ep: fixture)
 
 pytestmark = pytest.mark.gpu
 E4M3 = torch.float8_e4m3fn
@@ -222,3 +222,18 @@ def test_attention_scores_of_many_millions(ep, dtype, cache, scale):
     q, kc, vc, table, lens = attention_inputs(95, [300, 70, 1], 8, 2, 64, 16, dtype, cache)
     out = check_attention(ep, q, kc, vc, table, lens, scale=scale)
     assert bool(out.isfinite().all())
+
+
+@pytest.mark.parametrize("rows", [3, 12])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("power", [-112, 120, 123])
+def test_experts_near_the_ends_of_the_range(ep, rows, group, power):
+    """bf16 inputs whose groups' sums pass fp32's range before the scale brings them back, and tiny ones: y is 2^power times what
+    it is for inputs near 1."""
+    x, w, s, z, off = experts_inputs(rows + group, [rows], 512, 48, group, torch.bfloat16, True)
+    s = (s.float() * (2.0 ** -4 if power > 0 else 2.0 ** 4)).bfloat16()
+    y, scaled = (torch.empty(rows, 48, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ep.ep_expert_w4(x, w, s, y, expert_offsets=off, zeros=z)
+    ep.ep_expert_w4((x.double() * 2.0 ** power).bfloat16(), w, s, scaled, expert_offsets=off, zeros=z)
+    assert bool(scaled.isfinite().all())
+    assert torch.equal(scaled.double(), (y.double() * 2.0 ** power).bfloat16().double())

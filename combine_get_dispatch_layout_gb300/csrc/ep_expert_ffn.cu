@@ -1,0 +1,403 @@
+// The experts' gated feed-forward block in 16 bits and its gradients: grouped
+// products on the 5th-generation tensor cores, fp32 sums in TMEM.
+//
+// Mathematics, for an expert's rows (x [n, H], W1 [2F, H] gate above up, W2 [H, F]):
+//   gate_up = x W1^T,  act = silu(gate) * up,  y = act W2^T
+//   dact = dy W2,  dgate = dact up s (1 + gate (1 - s)),  dup = dact gate s,  s = 1 / (1 + exp(-gate))
+//   dx = [dgate dup] W1,  dW1 = [dgate dup]^T x,  dW2 = dy^T act
+// Each is one product D [128 lanes][columns] of a tile: the lanes are always the dimension that is contiguous in the
+// output (channels of a row), the columns its rows, so that one store pattern serves all, and few rows cost few
+// columns. Operands come as they lie in memory, contraction inward (K-major) or outward (MN-major), no transposes.
+#include "ep_expert_tiles.cuh"
+
+namespace ep {
+namespace {
+
+constexpr int kEpilogueWarps = 8;
+constexpr int kLoader = kEpilogueWarps, kIssuer = kLoader + 1;
+constexpr int kThreads = 32 * (kEpilogueWarps + 2);
+constexpr int kLanes = 128;
+constexpr int kStep = 64;                       // contraction of a stage: 128 bytes
+constexpr int kABytes = kLanes * kStep * 2;
+constexpr int kMostStages = 10;
+constexpr int kRing = 192 * 1024 + 8 * 1024;
+constexpr int kShared = 1024 + kRing + 512 + (kTileTable + 1) * 4;
+static_assert(kShared <= 227 * 1024 - 256, "");
+
+enum Product { kGateUp, kDown, kGradAct, kGradX, kGradW };
+
+struct Gemm {
+    ExpertRows g;
+    TilePlan plan;
+    int lanes;           // channels of the output
+    int inner;           // contraction (of kGradW: the expert's rows instead)
+    int columns;         // kGradW: rows of the output
+    int n_tiles;         // kGradW: tiles of them
+    int stages, stage_bytes, box;   // box: rows of a box of operand B (kGradW: of both)
+    void* out;
+    void* out2;          // kGateUp: gate and up, or NULL
+    const void* in;      // kGradAct: gate and up
+    int64_t out_ld, out2_ld, in_ld;
+    int out_fp32, accumulate;       // kGradW
+};
+
+template <typename T, int WHAT>
+__global__ void __launch_bounds__(kThreads, 1)
+    expert_gemm_kernel(Gemm a, const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map) {
+    extern __shared__ unsigned char shared_bytes[];
+    unsigned char* const ring = shared_bytes + (1024 - smem_addr(shared_bytes) % 1024) % 1024;
+    uint64_t* const barriers = reinterpret_cast<uint64_t*>(ring + kRing);
+    const uint32_t full = smem_addr(barriers), empty = full + 8 * kMostStages;
+    const uint32_t sums_full = empty + 8 * kMostStages, sums_empty = sums_full + 16;
+    uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(barriers) + 120;
+    volatile int* const dead = reinterpret_cast<volatile int*>(tmem_at + 1);
+    int* const table = reinterpret_cast<int*>(barriers) + 128;
+    static_assert((2 * kMostStages + 4) * 2 <= 120, "");
+    __shared__ int warp_sum[kThreads / 32];
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (warp == kLoader) {
+        tmem_alloc_all(smem_addr(tmem_at));
+        if (lane == 0) {
+            *dead = 0;
+            for (int i = 0; i < a.stages; ++i) {
+                barrier_init(full + 8 * i, 1);
+                barrier_init(empty + 8 * i, 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                barrier_init(sums_full + 8 * i, 1);
+                barrier_init(sums_empty + 8 * i, kEpilogueWarps);
+            }
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+    }
+    dependent_entry();
+    if constexpr (WHAT != kGradW) fill_table<kThreads>(a.g, a.plan, table, warp_sum);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = __shfl_sync(kFullMask, *tmem_at, 0);
+    const bool leader = elected();
+
+    // An item: `cols` columns (rows of the output) from `col` on, lanes from m * kLanes on, `steps` stages; of kGradW the
+    // contraction is over rows [row, row + rows).
+    struct Item {
+        int expert, m, col, cols, row, rows, steps;
+    };
+    const int64_t items = WHAT == kGradW ? static_cast<int64_t>(a.g.E) * a.plan.m_tiles * a.n_tiles : tile_count(a.g, a.plan, table);
+    const auto decode = [&](int64_t it) {
+        Item r;
+        if constexpr (WHAT == kGradW) {
+            const int per = a.plan.m_tiles * a.n_tiles, in = static_cast<int>(it % per);
+            r.expert = static_cast<int>(it / per);
+            r.m = in / a.n_tiles;
+            r.col = in % a.n_tiles * a.plan.cap;
+            r.cols = min(a.plan.cap, a.columns - r.col);
+            r.rows = rows_of(a.g, r.expert, r.row);
+            r.steps = (r.rows + kStep - 1) / kStep;
+        } else {
+            const Tile t = tile_at(a.g, a.plan, table, it);
+            r.expert = t.expert;
+            r.m = t.m;
+            r.col = r.row = t.row;
+            r.cols = r.rows = t.rows;
+            r.steps = (a.inner + kStep - 1) / kStep;
+        }
+        return r;
+    };
+
+    if (warp == kLoader) {
+        int slot = 0;
+        uint32_t parity = 1;   // (the first round of the ring waits for nothing)
+        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+            const Item it = decode(i);
+            const int a_boxes = WHAT == kGateUp ? 4 : WHAT == kDown ? 1 : 2;
+            const int b_boxes = WHAT == kGradW ? (it.cols + 63) / 64 : (max(it.cols, 1) + a.box - 1) / a.box;
+            for (int s = 0; s < it.steps; ++s) {
+                const uint32_t bar = full + 8 * slot, at_a = smem_addr(ring) + slot * a.stage_bytes, at_b = at_a + kABytes;
+                barrier_wait(empty + 8 * slot, parity, dead);
+                if constexpr (WHAT == kGradW) {
+                    // [64 channels] x [box rows] of both operands, boxes with real rows only
+                    const int down = (min(kStep, it.rows - s * kStep) + a.box - 1) / a.box, all = (2 + b_boxes) * down;
+                    if (lane == 0) barrier_expect(bar, all * a.box * 128);
+                    __syncwarp();
+                    if (lane < all) {
+                        const int k = lane % down, j = lane / down, row = it.row + s * kStep + k * a.box;
+                        if (j < 2) load_box(at_a + j * 8192 + k * a.box * 128, &a_map, it.m * kLanes + j * 64, row, 0, 0, bar);
+                        else load_box(at_b + (j - 2) * 8192 + k * a.box * 128, &b_map, it.col + (j - 2) * 64, row, 0, 0, bar);
+                    }
+                } else {
+                    if (lane == 0) barrier_expect(bar, kABytes + b_boxes * a.box * 128);
+                    __syncwarp();
+                    if (lane < a_boxes) {
+                        if (WHAT == kGateUp)   // the 16 gate and the 16 up rows of a warp
+                            load_box(at_a + lane * 4096, &a_map, s * kStep, it.m * (kLanes / 2) + lane * 16, 0, it.expert, bar);
+                        else if (WHAT == kDown)
+                            load_box(at_a, &a_map, s * kStep, it.m * kLanes, 0, it.expert, bar);
+                        else
+                            load_box(at_a + lane * 8192, &a_map, it.m * kLanes + lane * 64, s * kStep, 0, it.expert, bar);
+                    } else if (lane < a_boxes + b_boxes) {
+                        const int j = lane - a_boxes;
+                        load_box(at_b + j * a.box * 128, &b_map, s * kStep, it.row + j * a.box, 0, 0, bar);
+                    }
+                }
+                if (++slot == a.stages) slot = 0, parity ^= 1;
+            }
+        }
+    } else if (warp == kIssuer) {
+        // fp32 sums; operands' type; A outward, B outward; 128 lanes
+        constexpr uint32_t kType = std::is_same_v<T, __nv_bfloat16> ? 1u : 0u;
+        constexpr bool kAOut = WHAT >= kGradAct, kBOut = WHAT == kGradW;
+        constexpr uint32_t kShape = (1u << 4) | (kType << 7) | (kType << 10) | (kAOut ? 1u << 15 : 0u) | (kBOut ? 1u << 16 : 0u) |
+                                    (static_cast<uint32_t>(kLanes / 16) << 24);
+        int slot = 0, buffer = 0;
+        uint32_t parity = 0, sums_parity = 1;
+        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+            const Item it = decode(i);
+            if (it.steps == 0) continue;
+            const uint32_t shape = kShape | static_cast<uint32_t>(columns_of(it.cols) / 8) << 17;
+            const uint32_t sums = tmem + buffer * 256;
+            barrier_wait(sums_empty + 8 * buffer, sums_parity, dead);
+            for (int s = 0; s < it.steps; ++s) {
+                barrier_wait(full + 8 * slot, parity, dead);
+                const uint32_t at_a = smem_addr(ring) + slot * a.stage_bytes, at_b = at_a + kABytes;
+                int depth = kStep / 16;   // products of 16
+                if constexpr (WHAT == kGradW) {
+                    const int left = it.rows - s * kStep;
+                    if (left < kStep) {   // rows behind the expert's last belong to others: zeros instead, in both operands
+                        depth = (left + 15) / 16;
+                        const int blocks = 2 + (it.cols + 63) / 64;
+                        for (int j = lane; j < (depth * 16 - left) * blocks * 8; j += 32) {
+                            const int line = j / 8, row = left + line / blocks;
+                            *reinterpret_cast<uint4*>(ring + slot * a.stage_bytes + line % blocks * 8192 + row * 128 + j % 8 * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                }
+                tmem_fence_after();
+                if (leader) {
+                    const uint64_t da = kAOut ? operand_outward(at_a, 8192) : operand(at_a, 1024);
+                    const uint64_t db = kBOut ? operand_outward(at_b, 8192) : operand(at_b, 1024);
+                    for (int k = 0; k < depth; ++k)
+                        multiply_shared<false>(sums, da + k * (kAOut ? 128 : 2), db + k * (kBOut ? 128 : 2), shape, s > 0 || k > 0);
+                    multiply_done(empty + 8 * slot);
+                    if (s + 1 == it.steps) multiply_done(sums_full + 8 * buffer);
+                }
+                __syncwarp();
+                if (++slot == a.stages) slot = 0, parity ^= 1;
+            }
+            buffer ^= 1;
+            if (buffer == 0) sums_parity ^= 1;
+        }
+    } else {
+        const int half = warp >> 2;
+        int buffer = 0;
+        uint32_t parity = 0;
+        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+            const Item it = decode(i);
+            const uint32_t mine = tmem + buffer * 256 + (static_cast<uint32_t>(warp & 3) << 21);   // lane 32 * (warp % 4), upper half
+            if (it.steps > 0) {
+                barrier_wait(sums_full + 8 * buffer, parity, dead);
+                tmem_fence_after();
+            }
+            // this thread's channel; of gate and up a warp's lanes are 16 gate and 16 up rows
+            const int chan = WHAT == kGateUp ? it.m * (kLanes / 2) + (warp & 3) * 16 + (lane & 15) : it.m * kLanes + (warp & 3) * 32 + lane;
+            const bool real = chan < a.lanes;
+            for (int c0 = half * 32; c0 < it.cols; c0 += 64) {
+                uint32_t raw[32];
+                if (it.steps > 0) {
+                    tmem_load32(mine + c0, raw);
+                    tmem_load_wait();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) raw[j] = 0;
+                }
+                if (*dead) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) raw[j] = 0x7fffffff;
+                }
+                const int many = min(32, it.cols - c0);
+                if constexpr (WHAT == kGateUp) {
+                    const int64_t row = it.row + c0;
+                    if (a.out2 && real) {
+                        T* to = static_cast<T*>(a.out2) + row * a.out2_ld + (lane < 16 ? chan : a.lanes + chan);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < many) to[j * a.out2_ld] = from_float<T>(__uint_as_float(raw[j]));
+                    }
+                    T* to = static_cast<T*>(a.out) + (row + (lane >> 4)) * a.out_ld + chan;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {   // gate lanes take the even columns, up lanes the odd ones
+                        const float own = __uint_as_float(lane < 16 ? raw[j] : raw[j + 1]);
+                        const float got = __uint_as_float(__shfl_xor_sync(kFullMask, lane < 16 ? raw[j + 1] : raw[j], 16));
+                        const float act = lane < 16 ? silu(own) * got : silu(got) * own;
+                        if (real && j + (lane >> 4) < many) to[j * a.out_ld] = from_float<T>(act);
+                    }
+                } else if constexpr (WHAT == kGradAct) {
+                    if (real) {
+                        const int64_t row = it.row + c0;
+                        const T* from = static_cast<const T*>(a.in) + row * a.in_ld + chan;
+                        T* to = static_cast<T*>(a.out) + row * a.out_ld + chan;
+                        T gate[32], up[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < many) gate[j] = from[j * a.in_ld], up[j] = from[j * a.in_ld + a.lanes];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < many) {
+                                const float d = __uint_as_float(raw[j]), gt = to_float(gate[j]), s = 1.0f / (1.0f + expf(-gt));
+                                to[j * a.out_ld] = from_float<T>(d * to_float(up[j]) * s * (1.0f + gt * (1.0f - s)));
+                                to[j * a.out_ld + a.lanes] = from_float<T>(d * gt * s);
+                            }
+                    }
+                } else if constexpr (WHAT == kGradW) {
+                    if (real) {
+                        const int64_t at = (static_cast<int64_t>(it.expert) * a.columns + it.col + c0) * a.out_ld + chan;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < many) {
+                                float v = __uint_as_float(raw[j]);
+                                if (a.out_fp32) {
+                                    float* to = static_cast<float*>(a.out) + at + j * a.out_ld;
+                                    *to = a.accumulate ? *to + v : v;
+                                } else {
+                                    T* to = static_cast<T*>(a.out) + at + j * a.out_ld;
+                                    *to = from_float<T>(a.accumulate ? to_float(*to) + v : v);
+                                }
+                            }
+                    }
+                } else if (real) {
+                    T* to = static_cast<T*>(a.out) + (static_cast<int64_t>(it.row) + c0) * a.out_ld + chan;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j < many) to[j * a.out_ld] = from_float<T>(__uint_as_float(raw[j]));
+                }
+            }
+            if (it.steps > 0) {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) barrier_arrive(sums_empty + 8 * buffer);
+                buffer ^= 1;
+                if (buffer == 0) parity ^= 1;
+            }
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == kLoader) {
+        tmem_fence_after();
+        tmem_free_all(tmem);
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+template <typename T, int WHAT>
+cudaError_t launch_gemm(Gemm& a, const CUtensorMap& a_map, const CUtensorMap& b_map, cudaStream_t stream) {
+    static int known[64];
+    int sms = 0;
+    cudaError_t err = prepare_persistent(expert_gemm_kernel<T, WHAT>, kShared, known, &sms);
+    if (err != cudaSuccess) return err;
+    a.stage_bytes = kABytes + a.plan.cap * kStep * 2;
+    a.stages = kRing / a.stage_bytes < kMostStages ? kRing / a.stage_bytes : kMostStages;
+    const int64_t used = a.g.rows < a.g.E ? a.g.rows : a.g.E;
+    const int64_t most = WHAT == kGradW ? static_cast<int64_t>(a.g.E) * a.plan.m_tiles * a.n_tiles
+                                        : (a.g.rows + used * (a.plan.cap - 1)) / a.plan.cap * a.plan.m_tiles;
+    return launch_dependent(expert_gemm_kernel<T, WHAT>, dim3(static_cast<unsigned>(most < sms ? most : sms)), dim3(kThreads), kShared,
+                            stream, a, a_map, b_map);
+}
+
+Gemm gemm_of(const FfnArgs& f, int lanes, int lanes_of_tile, int inner) {
+    Gemm a{};
+    a.g = f.g;
+    a.lanes = lanes;
+    a.inner = inner;
+    a.plan.m_tiles = ceil_div(lanes, lanes_of_tile);
+    a.plan.chunk = 16;
+    while (((f.g.E - 1) >> a.plan.shift) + 1 > kTileTable) ++a.plan.shift;
+    const int64_t used = f.g.rows < f.g.E ? f.g.rows : f.g.E, mean = (f.g.rows - 1) / used + 1;
+    a.plan.cap = mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 112 ? 128 : 256;
+    a.box = a.plan.cap < 64 ? 16 : 64;
+    return a;
+}
+
+// Rows [rows][width] as operand B, contraction inward.
+cudaError_t rows_map(CUtensorMap* map, const FfnArgs& f, const void* x, int64_t width, int64_t ld, int box) {
+    return box_map(map, x, f.dtype, width, f.g.rows, 1, 1, ld * 2, ld * 2, ld * 2, box, 1);
+}
+
+template <typename T>
+cudaError_t forward(const FfnArgs& f, cudaStream_t stream) {
+    const int64_t H = f.H, F = f.F;
+    CUtensorMap am, bm;
+    Gemm a = gemm_of(f, f.F, kLanes / 2, f.H);
+    a.out = f.act, a.out_ld = f.act_ld;
+    a.out2 = f.gate_up, a.out2_ld = f.gate_up_ld;
+    cudaError_t err = box_map(&am, f.w_gate_up, f.dtype, H, F, 2, f.g.E, H * 2, F * H * 2, 2 * F * H * 2, 16, 2);
+    if (err == cudaSuccess) err = rows_map(&bm, f, f.x, H, f.x_ld, a.box);
+    if (err == cudaSuccess) err = launch_gemm<T, kGateUp>(a, am, bm, stream);
+    if (err != cudaSuccess || !f.y) return err;
+    a = gemm_of(f, f.H, kLanes, f.F);
+    a.out = f.y, a.out_ld = f.y_ld;
+    err = box_map(&am, f.w_down, f.dtype, F, H, 1, f.g.E, F * 2, F * H * 2, F * H * 2, kLanes, 1);
+    if (err == cudaSuccess) err = rows_map(&bm, f, f.act, F, f.act_ld, a.box);
+    return err == cudaSuccess ? launch_gemm<T, kDown>(a, am, bm, stream) : err;
+}
+
+// dW [E][columns][lanes] = (by [rows][columns])^T x [rows][lanes]
+template <typename T>
+cudaError_t weight_gradient(const FfnArgs& f, void* out, const void* x, int lanes, int64_t x_ld, const void* by, int columns, int64_t by_ld,
+                            cudaStream_t stream) {
+    CUtensorMap am, bm;
+    Gemm a = gemm_of(f, lanes, kLanes, 0);
+    a.box = f.g.rows / f.g.E < 64 ? 16 : 64;
+    a.plan.cap = 256;
+    a.columns = columns;
+    a.n_tiles = ceil_div(columns, a.plan.cap);
+    a.out = out, a.out_ld = lanes;
+    a.out_fp32 = f.grad_w_fp32, a.accumulate = f.accumulate;
+    cudaError_t err = rows_map(&am, f, x, lanes, x_ld, a.box);
+    if (err == cudaSuccess) err = rows_map(&bm, f, by, columns, by_ld, a.box);
+    return err == cudaSuccess ? launch_gemm<T, kGradW>(a, am, bm, stream) : err;
+}
+
+template <typename T>
+cudaError_t backward(const FfnArgs& f, cudaStream_t stream) {
+    const int64_t H = f.H, F = f.F;
+    CUtensorMap am, bm;
+    cudaError_t err = cudaSuccess;
+    if (f.g.rows > 0) {
+        Gemm a = gemm_of(f, f.F, kLanes, f.H);
+        a.in = f.gate_up, a.in_ld = f.gate_up_ld;
+        a.out = f.grad_gate_up, a.out_ld = f.grad_gate_up_ld;
+        err = box_map(&am, f.w_down, f.dtype, F, H, 1, f.g.E, F * 2, F * H * 2, F * H * 2, kStep, 1);
+        if (err == cudaSuccess) err = rows_map(&bm, f, f.grad_y, H, f.grad_y_ld, a.box);
+        if (err == cudaSuccess) err = launch_gemm<T, kGradAct>(a, am, bm, stream);
+        if (err == cudaSuccess && f.grad_x) {
+            a = gemm_of(f, f.H, kLanes, 2 * f.F);
+            a.out = f.grad_x, a.out_ld = f.grad_x_ld;
+            err = box_map(&am, f.w_gate_up, f.dtype, H, 2 * F, 1, f.g.E, H * 2, 2 * F * H * 2, 2 * F * H * 2, kStep, 1);
+            if (err == cudaSuccess) err = rows_map(&bm, f, f.grad_gate_up, 2 * F, f.grad_gate_up_ld, a.box);
+            if (err == cudaSuccess) err = launch_gemm<T, kGradX>(a, am, bm, stream);
+        }
+    }
+    if (err == cudaSuccess && f.grad_w_gate_up)
+        err = weight_gradient<T>(f, f.grad_w_gate_up, f.x, f.H, f.x_ld, f.grad_gate_up, 2 * f.F, f.grad_gate_up_ld, stream);
+    if (err == cudaSuccess && f.grad_w_down)
+        err = weight_gradient<T>(f, f.grad_w_down, f.act, f.F, f.act_ld, f.grad_y, f.H, f.grad_y_ld, stream);
+    return err;
+}
+
+}  // namespace
+
+cudaError_t launch_expert_ffn(const FfnArgs& f, cudaStream_t stream) {
+    return f.dtype == EP_DTYPE_BF16 ? forward<__nv_bfloat16>(f, stream) : forward<__half>(f, stream);
+}
+
+cudaError_t launch_expert_ffn_backward(const FfnArgs& f, cudaStream_t stream) {
+    return f.dtype == EP_DTYPE_BF16 ? backward<__nv_bfloat16>(f, stream) : backward<__half>(f, stream);
+}
+
+}  // namespace ep

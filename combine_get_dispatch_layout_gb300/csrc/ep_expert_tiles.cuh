@@ -1,0 +1,183 @@
+// What the kernels of the experts' products share: whose rows are whose, and
+// the walk of persistent CTAs over tiles of them.
+#pragma once
+
+#include "ep_tensor.cuh"
+
+namespace ep {
+namespace {
+
+constexpr int kTileTable = 1024;   // entries of the table of experts' tiles
+
+// First row and number of real rows of expert e, within [0, rows).
+__device__ __forceinline__ int rows_of(const ExpertRows& g, int e, int& first) {
+    if (!g.offsets) {
+        first = 0;
+        return g.rows;
+    }
+    first = min(max(g.offsets[e], 0), g.rows);
+    int n = min(max(g.offsets[e + 1], 0), g.rows) - first;
+    if (g.counts) n = min(n, g.counts[e]);
+    return max(n, 0);
+}
+
+// Tiles of an expert's product: m_tiles along the weights' rows, and along its own rows as many as `cap` rows a tile
+// make, of nearly equal width. All weight tiles are passed over for `chunk` tiles of rows at a time, so that the CTAs
+// at work together share the weights of few tiles and the inputs of few.
+struct TilePlan {
+    int m_tiles, cap, chunk;
+    int shift;   // an entry of the table stands for 2^shift experts
+};
+struct Tile {
+    int expert, m;     // m: tile of weight rows
+    int row, rows;     // the expert's rows of this tile
+};
+
+__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a - 1) / b + 1; }   // a >= 1
+
+// Width of the tiles of n rows, a multiple of 16. Equal widths where none is left without rows by the rounding.
+__device__ __forceinline__ int tile_width(int n, int tiles, int cap) {
+    return 16 * tiles < cap ? (ceil_div(n, tiles) + 15) / 16 * 16 : cap;
+}
+
+// Fills table[entry] with the tiles of rows before it, for all threads of the CTA (THREADS of them).
+template <int THREADS>
+__device__ __forceinline__ void fill_table(const ExpertRows& g, const TilePlan& p, int* table, int* warp_sum) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const auto tiles_of = [&](int e) {
+        int first;
+        return (rows_of(g, e, first) + p.cap - 1) / p.cap;
+    };
+    const int entries = ((g.E - 1) >> p.shift) + 1;
+    const int per = (entries + THREADS - 1) / THREADS, lo = min(entries, tid * per), hi = min(entries, lo + per);
+    const int e0 = lo << p.shift, e1 = min(g.E, hi << p.shift);
+    int own = 0;
+    for (int e = e0; e < e1; ++e) own += tiles_of(e);
+    int scan = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kFullMask, scan, o);
+        if (lane >= o) scan += v;
+    }
+    if (lane == 31) warp_sum[warp] = scan;
+    __syncthreads();
+    int base = scan - own;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w)
+        if (w < warp) base += warp_sum[w];
+    for (int e = e0; e < e1; ++e) {
+        if ((e & ((1 << p.shift) - 1)) == 0) table[e >> p.shift] = base;
+        base += tiles_of(e);
+    }
+    if (hi == entries && lo < hi) table[entries] = base;
+}
+
+__device__ __forceinline__ int64_t tile_count(const ExpertRows& g, const TilePlan& p, const int* table) {
+    return static_cast<int64_t>(table[((g.E - 1) >> p.shift) + 1]) * p.m_tiles;
+}
+
+// (Offsets that contradict one another can make tiles without rows, never one outside [0, rows).)
+__device__ __forceinline__ Tile tile_at(const ExpertRows& g, const TilePlan& p, const int* table, int64_t it) {
+    int lo = 0, hi = (g.E - 1) >> p.shift;   // the last entry whose first tile is not behind `it`
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (static_cast<int64_t>(table[mid]) * p.m_tiles <= it) lo = mid;
+        else hi = mid - 1;
+    }
+    int64_t in = it - static_cast<int64_t>(table[lo]) * p.m_tiles;
+    int first, e = lo << p.shift, n = rows_of(g, e, first), tiles = (n + p.cap - 1) / p.cap;
+    while (in >= static_cast<int64_t>(tiles) * p.m_tiles && e + 1 < g.E) {   // (an entry of several experts)
+        in -= static_cast<int64_t>(tiles) * p.m_tiles;
+        n = rows_of(g, ++e, first);
+        tiles = (n + p.cap - 1) / p.cap;
+    }
+    Tile t;
+    t.expert = e;
+    const int64_t per_chunk = static_cast<int64_t>(p.chunk) * p.m_tiles;
+    const int c = static_cast<int>(in / per_chunk), r = static_cast<int>(in - c * per_chunk);
+    const int wide = max(min(p.chunk, tiles - c * p.chunk), 1);
+    t.m = r / wide;
+    const int width = tile_width(max(n, 1), max(tiles, 1), p.cap);
+    const int64_t at = static_cast<int64_t>(c * p.chunk + r % wide) * width;
+    t.row = first + static_cast<int>(min(at, static_cast<int64_t>(n)));
+    t.rows = static_cast<int>(max(min(static_cast<int64_t>(width), n - at), static_cast<int64_t>(0)));
+    return t;
+}
+
+// Columns of the product for n rows of a tile.
+__device__ __forceinline__ int columns_of(int n) { return max((n + 15) / 16 * 16, 16); }
+
+__device__ __forceinline__ void tmem_alloc_all(uint32_t to) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(to) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_all(uint32_t tmem) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+        "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at)
+        : "memory");
+}
+// sums [128 lanes][N] (+)= A [128 lanes] * B [N columns]^T, both in shared memory.
+template <bool FP8>
+__device__ __forceinline__ void multiply_shared(uint32_t sums, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+    if constexpr (FP8)
+        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(sums),
+                     "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+                     : "memory");
+    else
+        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(sums),
+                     "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+                     : "memory");
+}
+
+__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
+
+// ------------------------------------------------------------------ host
+
+// [w][z][y][x] with x dense and y, z, w `stride` bytes apart (multiples of 16), read in boxes of 128 bytes x box_y x
+// box_z with the 128-byte swizzle; zeros past the ends.
+cudaError_t box_map(CUtensorMap* map, const void* base, int dtype, int64_t x, int64_t y, int64_t z, int64_t w, int64_t stride_y,
+                    int64_t stride_z, int64_t stride_w, int box_y, int box_z) {
+    const EncodeFn encode = encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const CUtensorMapDataType type = dtype == EP_DTYPE_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                     : dtype == EP_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                              : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const int box_x = type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 128 : 64;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(x), static_cast<cuuint64_t>(y), static_cast<cuuint64_t>(z),
+                                static_cast<cuuint64_t>(w)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(stride_y), static_cast<cuuint64_t>(stride_z),
+                                   static_cast<cuuint64_t>(stride_w)};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(box_x), static_cast<cuuint32_t>(box_y), static_cast<cuuint32_t>(box_z), 1},
+                     step[4] = {1, 1, 1, 1};
+    return encode(map, type, 4, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+// SMs of the current device, with the kernel's shared memory limit raised: looked up once per device (a race writes
+// the same value).
+template <typename Kernel>
+cudaError_t prepare_persistent(Kernel kernel, int smem, int* known, int* sms) {
+    constexpr int kDevices = 64;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < kDevices && (*sms = __atomic_load_n(&known[dev], __ATOMIC_ACQUIRE)) > 0) return cudaSuccess;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err == cudaSuccess && dev < kDevices) __atomic_store_n(&known[dev], *sms, __ATOMIC_RELEASE);
+    return err;
+}
+
+}  // namespace
+}  // namespace ep

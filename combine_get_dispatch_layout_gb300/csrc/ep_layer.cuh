@@ -113,4 +113,38 @@ struct W4Args {
 cudaError_t launch_expert_w4(const W4Args& a, void* workspace, int dtype, cudaStream_t stream);
 int64_t expert_w4_workspace(int64_t rows, int I, int group, int dtype);
 
+// Rows that belong to experts: as ep_layout* writes them, `rows` in all.
+struct ExpertRows {
+    const int32_t* offsets;
+    const int32_t* counts;
+    int rows, E;
+};
+
+struct FfnArgs {
+    ExpertRows g;
+    int H, F, dtype;
+    const void *x, *w_gate_up, *w_down;
+    void *act, *y, *gate_up;
+    const void* grad_y;
+    void *grad_gate_up, *grad_x, *grad_w_gate_up, *grad_w_down;
+    int64_t x_ld, act_ld, y_ld, gate_up_ld, grad_y_ld, grad_gate_up_ld, grad_x_ld;
+    int grad_w_fp32, accumulate;
+};
+cudaError_t launch_expert_ffn(const FfnArgs& f, cudaStream_t stream);
+cudaError_t launch_expert_ffn_backward(const FfnArgs& f, cudaStream_t stream);
+
+struct Fp8Args {
+    ExpertRows g;
+    int I, O, x_dtype, swiglu;
+    const void* x;
+    const void* x_scales;
+    const uint8_t* w;
+    const float* w_scales;
+    void* y;
+    void* y_scales;
+    int y_dtype, x_ue8m0, y_scale_mode;
+    int64_t x_ld, y_ld, x_scale_row, x_scale_block, y_scale_row, y_scale_block;
+};
+cudaError_t launch_expert_fp8(const Fp8Args& a, cudaStream_t stream);
+
 }  // namespace ep

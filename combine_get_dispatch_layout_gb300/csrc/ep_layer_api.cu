@@ -45,6 +45,24 @@ bool cache_ok(const ep_cache_t* c, int dtype, int dim) {
     return true;
 }
 
+// Rows that belong to experts; the arrays may be missing for one expert.
+bool experts_ok(const int32_t* offsets, const int32_t* counts, int64_t rows, int E) {
+    return rows >= 0 && rows <= kMostSide && E >= 1 && E <= EP_MAX_EXPERTS && (offsets || (E == 1 && !counts)) && aligned(offsets, 4) &&
+           aligned(counts, 4);
+}
+
+constexpr int64_t kMostStep = int64_t{1} << 38;   // elements between rows, and of an expert's weights: tensor maps hold 2^40 bytes
+
+// Rows of `width` 16-bit elements that start on 16 bytes.
+bool half_rows_ok(const void* p, int64_t ld, int64_t width) {
+    return p && aligned(p, 16) && ld >= width && ld % 8 == 0 && ld < kMostStep;
+}
+
+bool ffn_sizes_ok(const ep_ffn_config_t* c, int64_t rows, int H, int F, const int32_t* offsets, const int32_t* counts, int E) {
+    return c && half_type(c->dtype) && experts_ok(offsets, counts, rows, E) && H >= 8 && F >= 8 && H % 8 == 0 && F % 8 == 0 &&
+           H <= kMostSide && F <= kMostSide / 2 && static_cast<int64_t>(H) * F < kMostStep / 2;
+}
+
 }  // namespace
 
 extern "C" {
@@ -284,6 +302,134 @@ ep_status_t ep_expert_w4(const void* x, int64_t rows, int I, const uint8_t* weig
     a.y_ld = config->y_ld;
     a.y = y;
     return status_of(ep::launch_expert_w4(a, workspace, config->dtype, static_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_expert_fp8(const void* x, const void* x_scales, int64_t rows, int I, const uint8_t* weights,
+                          const float* weight_scales, const int32_t* expert_offsets, const int32_t* expert_counts, int E, int O,
+                          const ep_fp8_config_t* config, void* y, void* y_scales, void* stream) {
+    ApiRange range("ep_expert_fp8");
+    if (!config || !experts_ok(expert_offsets, expert_counts, rows, E)) return EP_ERR_INVALID_ARG;
+    const ep_fp8_config_t& c = *config;
+    const bool swiglu = c.activation == EP_ACT_SWIGLU, fp8_out = c.y_dtype == EP_DTYPE_FP8_E4M3;
+    const int cols = swiglu ? O / 2 : O;
+    if ((c.x_dtype != EP_DTYPE_FP8_E4M3 && c.x_dtype != EP_DTYPE_FP8_E5M2) || (!half_type(c.y_dtype) && !fp8_out) ||
+        (!swiglu && c.activation != EP_ACT_NONE) || c.x_scale_mode < EP_SCALE_FP32 || c.x_scale_mode > EP_SCALE_UE8M0)
+        return EP_ERR_INVALID_ARG;
+    if (I < 128 || I > kMostSide || I % 128 != 0 || O < 1 || O > kMostSide || (swiglu && O % 2 != 0) ||
+        static_cast<int64_t>(I) * O >= kMostStep)
+        return EP_ERR_INVALID_ARG;
+    if (c.x_ld < I || c.x_ld % 16 != 0 || c.x_ld >= kMostStep || c.y_ld < cols || c.x_scale_row < 0 || c.x_scale_block < 0)
+        return EP_ERR_INVALID_ARG;
+    if (fp8_out && (cols % 128 != 0 || c.y_scale_mode < EP_SCALE_FP32 || c.y_scale_mode > EP_SCALE_UE8M0 || c.y_scale_row < 1 ||
+                    c.y_scale_block < 1))
+        return EP_ERR_INVALID_ARG;
+    if (rows == 0) return EP_OK;
+    const bool x_ue8m0 = c.x_scale_mode == EP_SCALE_UE8M0;
+    if (!x || !x_scales || !weights || !weight_scales || !y || !aligned(x, 16) || !aligned(weights, 16) ||
+        !aligned(x_scales, x_ue8m0 ? 1 : 4) || !aligned(weight_scales, 4) || !aligned(y, fp8_out ? 1 : 2))
+        return EP_ERR_INVALID_ARG;
+    if (fp8_out && (!y_scales || !aligned(y_scales, c.y_scale_mode == EP_SCALE_UE8M0 ? 1 : 4))) return EP_ERR_INVALID_ARG;
+    ep::Fp8Args a{};
+    a.g = {expert_offsets, expert_counts, static_cast<int>(rows), E};
+    a.I = I;
+    a.O = O;
+    a.x_dtype = c.x_dtype;
+    a.swiglu = swiglu;
+    a.x = x;
+    a.x_scales = x_scales;
+    a.w = weights;
+    a.w_scales = weight_scales;
+    a.y = y;
+    a.y_scales = y_scales;
+    a.y_dtype = c.y_dtype;
+    a.x_ue8m0 = x_ue8m0;
+    a.y_scale_mode = c.y_scale_mode;
+    a.x_ld = c.x_ld;
+    a.y_ld = c.y_ld;
+    a.x_scale_row = c.x_scale_row;
+    a.x_scale_block = c.x_scale_block;
+    a.y_scale_row = c.y_scale_row;
+    a.y_scale_block = c.y_scale_block;
+    return status_of(ep::launch_expert_fp8(a, static_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_expert_ffn(const void* x, int64_t rows, int H, const void* w_gate_up, const void* w_down,
+                          const int32_t* expert_offsets, const int32_t* expert_counts, int E, int F,
+                          const ep_ffn_config_t* config, void* gate_up, void* act, void* y, void* stream) {
+    ApiRange range("ep_expert_ffn");
+    if (!ffn_sizes_ok(config, rows, H, F, expert_offsets, expert_counts, E)) return EP_ERR_INVALID_ARG;
+    if (rows == 0) return EP_OK;
+    if (!half_rows_ok(x, config->x_ld, H) || !half_rows_ok(act, config->act_ld, F) || !w_gate_up || !aligned(w_gate_up, 16) ||
+        (gate_up && !half_rows_ok(gate_up, config->gate_up_ld, 2 * static_cast<int64_t>(F))))
+        return EP_ERR_INVALID_ARG;
+    if (y && (!half_rows_ok(y, config->y_ld, H) || !w_down || !aligned(w_down, 16))) return EP_ERR_INVALID_ARG;
+    ep::FfnArgs f{};
+    f.g = {expert_offsets, expert_counts, static_cast<int>(rows), E};
+    f.H = H;
+    f.F = F;
+    f.dtype = config->dtype;
+    f.x = x;
+    f.w_gate_up = w_gate_up;
+    f.w_down = w_down;
+    f.gate_up = gate_up;
+    f.act = act;
+    f.y = y;
+    f.x_ld = config->x_ld;
+    f.gate_up_ld = config->gate_up_ld;
+    f.act_ld = config->act_ld;
+    f.y_ld = config->y_ld;
+    return status_of(ep::launch_expert_ffn(f, static_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_expert_ffn_backward(const void* grad_y, const void* x, const void* gate_up, const void* act, int64_t rows, int H,
+                                   const void* w_gate_up, const void* w_down, const int32_t* expert_offsets,
+                                   const int32_t* expert_counts, int E, int F, const ep_ffn_config_t* config, void* grad_gate_up,
+                                   void* grad_x, void* grad_w_gate_up, void* grad_w_down, void* stream) {
+    ApiRange range("ep_expert_ffn_backward");
+    if (!ffn_sizes_ok(config, rows, H, F, expert_offsets, expert_counts, E) ||
+        (config->grad_w_dtype != config->dtype && config->grad_w_dtype != EP_DTYPE_FP32))
+        return EP_ERR_INVALID_ARG;
+    const ep_ffn_config_t& c = *config;
+    if (!aligned(grad_w_gate_up, 16) || !aligned(grad_w_down, 16)) return EP_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (rows == 0) {
+        const size_t one = static_cast<size_t>(E) * H * F * type_bytes(c.grad_w_dtype);
+        if (c.accumulate) return EP_OK;
+        if (grad_w_gate_up && cudaMemsetAsync(grad_w_gate_up, 0, 2 * one, s) != cudaSuccess) return EP_ERR_CUDA;
+        if (grad_w_down && cudaMemsetAsync(grad_w_down, 0, one, s) != cudaSuccess) return EP_ERR_CUDA;
+        return EP_OK;
+    }
+    const int64_t wide = 2 * static_cast<int64_t>(F);
+    if (!half_rows_ok(grad_y, c.y_ld, H) || !half_rows_ok(gate_up, c.gate_up_ld, wide) ||
+        !half_rows_ok(grad_gate_up, c.grad_gate_up_ld, wide) || !w_down || !aligned(w_down, 16))
+        return EP_ERR_INVALID_ARG;
+    if (grad_x && (!half_rows_ok(grad_x, c.grad_x_ld, H) || !w_gate_up || !aligned(w_gate_up, 16))) return EP_ERR_INVALID_ARG;
+    if (grad_w_gate_up && !half_rows_ok(x, c.x_ld, H)) return EP_ERR_INVALID_ARG;
+    if (grad_w_down && !half_rows_ok(act, c.act_ld, F)) return EP_ERR_INVALID_ARG;
+    ep::FfnArgs f{};
+    f.g = {expert_offsets, expert_counts, static_cast<int>(rows), E};
+    f.H = H;
+    f.F = F;
+    f.dtype = c.dtype;
+    f.x = x;
+    f.w_gate_up = w_gate_up;
+    f.w_down = w_down;
+    f.gate_up = const_cast<void*>(gate_up);
+    f.act = const_cast<void*>(act);
+    f.grad_y = grad_y;
+    f.grad_gate_up = grad_gate_up;
+    f.grad_x = grad_x;
+    f.grad_w_gate_up = grad_w_gate_up;
+    f.grad_w_down = grad_w_down;
+    f.x_ld = c.x_ld;
+    f.gate_up_ld = c.gate_up_ld;
+    f.act_ld = c.act_ld;
+    f.grad_y_ld = c.y_ld;
+    f.grad_x_ld = c.grad_x_ld;
+    f.grad_gate_up_ld = c.grad_gate_up_ld;
+    f.grad_w_fp32 = c.grad_w_dtype == EP_DTYPE_FP32;
+    f.accumulate = c.accumulate != 0;
+    return status_of(ep::launch_expert_ffn_backward(f, s));
 }
 
 }  // extern "C"

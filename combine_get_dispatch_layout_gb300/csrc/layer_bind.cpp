@@ -15,6 +15,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
 
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
 #include <string>
@@ -39,12 +40,15 @@ struct Library {
     decltype(&ep_paged_attention) paged_attention = nullptr;
     decltype(&ep_expert_w4) expert_w4 = nullptr;
     decltype(&ep_expert_w4_workspace) expert_w4_workspace = nullptr;
+    decltype(&ep_expert_fp8) expert_fp8 = nullptr;
+    decltype(&ep_expert_ffn) expert_ffn = nullptr;
+    decltype(&ep_expert_ffn_backward) expert_ffn_backward = nullptr;
 } library;
 
 using Tensor = at::Tensor;
 constexpr auto kBf16 = at::ScalarType::BFloat16, kFp16 = at::ScalarType::Half, kFp32 = at::ScalarType::Float,
                kInt64 = at::ScalarType::Long, kInt32 = at::ScalarType::Int, kByte = at::ScalarType::Byte,
-               kE4m3 = at::ScalarType::Float8_e4m3fn;
+               kE4m3 = at::ScalarType::Float8_e4m3fn, kE5m2 = at::ScalarType::Float8_e5m2, kE8m0 = at::ScalarType::Float8_e8m0fnu;
 
 const Tensor* optional_tensor(PyObject* o, const char* what) {
     if (o == Py_None) return nullptr;
@@ -122,6 +126,44 @@ Rows rows(const Tensor& t, at::ScalarType type, std::initializer_list<int64_t> s
     }
     if (t.size(0) > 1 && t.stride(0) < step) refuse("%s: rows must not overlap", what);
     return {address(t, what), t.size(0) > 1 ? t.stride(0) : (step + 7) / 8 * 8};
+}
+
+// Refuses a tensor that tensor maps or later kernels address and that is not the GPU's.
+const Tensor& on_gpu(const Tensor& t, const char* what) {
+    if (!t.is_cuda() && t.numel() > 0) refuse("%s must be a CUDA tensor", what);
+    return t;
+}
+Rows gpu_rows(PyObject* o, at::ScalarType type, std::initializer_list<int64_t> shape, const char* what) {
+    return rows(on_gpu(tensor(o, what), what), type, shape, what);
+}
+Rows gpu_rows_or_none(PyObject* o, at::ScalarType type, std::initializer_list<int64_t> shape, const char* what) {
+    return o == Py_None ? Rows{} : gpu_rows(o, type, shape, what);
+}
+void* gpu_dense(PyObject* o, at::ScalarType type, std::initializer_list<int64_t> shape, const char* what) {
+    if (const Tensor* t = optional_tensor(o, what)) on_gpu(*t, what);
+    return dense(o, type, shape, what);
+}
+// Scales [rows, blocks], fp32 or exponent bytes, in any order in memory.
+struct Scales {
+    void* at = nullptr;
+    int64_t row = 0, block = 0;
+    bool bytes = false;
+};
+Scales scales(PyObject* o, int64_t n, int64_t blocks, bool written, const char* what) {
+    const Tensor& t = on_gpu(tensor(o, what), what);
+    const auto type = t.scalar_type();
+    const bool bytes = type == kByte || type == kE8m0;
+    expect(t, bytes ? type : kFp32, {n, blocks}, what);
+    Scales s{t.data_ptr(), t.stride(0), t.stride(1), bytes};
+    // (of a dimension of one the stride says nothing)
+    if (n <= 1) s.row = std::max<int64_t>(s.row, 1);
+    if (blocks <= 1) s.block = std::max<int64_t>(s.block, 1);
+    if (written && n > 0 && blocks > 0) {
+        const bool by_row = (n == 1 || s.row > s.block * (blocks - 1)) && s.block >= 1;
+        const bool by_block = (blocks == 1 || s.block > s.row * (n - 1)) && s.row >= 1;
+        if (!by_row && !by_block) refuse("%s must not overlap", what);
+    }
+    return s;
 }
 
 int64_t whole(PyObject* o) {
@@ -328,6 +370,94 @@ long expert_w4(PyObject* const* a) {
                              size_of(O, "O"), &c, y.at, work, bytes, stream_of(a[9]));
 }
 
+// (x, x_scales, weights, weight_scales, y, y_scales, expert_offsets, expert_counts, activation, scale_mode, stream)
+long expert_fp8(PyObject* const* a) {
+    const Tensor &x = on_gpu(tensor(a[0], "x"), "x"), &w = tensor(a[2], "weights"), &y = tensor(a[4], "y");
+    dimensions(x, 2, "x");
+    dimensions(w, 3, "weights");
+    const int64_t n = x.size(0), I = x.size(1), E = w.size(0), O = w.size(1), blocks = I / 128;
+    ep_fp8_config_t c{};
+    if (x.scalar_type() != kE4m3 && x.scalar_type() != kE5m2) refuse("x: %s is not supported", c10::toString(x.scalar_type()));
+    c.x_dtype = x.scalar_type() == kE4m3 ? EP_DTYPE_FP8_E4M3 : EP_DTYPE_FP8_E5M2;
+    c.y_dtype = type_code(y, "y", false, true);
+    c.activation = small(a[8], "activation");
+    const int64_t cols = c.activation == EP_ACT_SWIGLU ? O / 2 : O;
+    const Rows xr = rows(x, x.scalar_type(), {n, I}, "x"), yr = gpu_rows(a[4], y.scalar_type(), {n, cols}, "y");
+    c.x_ld = n > 1 ? xr.ld : (xr.ld + 15) / 16 * 16;
+    c.y_ld = yr.ld;
+    const Scales xs = scales(a[1], n, blocks, false, "x_scales");
+    c.x_scale_mode = xs.bytes ? EP_SCALE_UE8M0 : EP_SCALE_FP32;
+    c.x_scale_row = xs.row, c.x_scale_block = xs.block;
+    Scales ys;
+    if (c.y_dtype == EP_DTYPE_FP8_E4M3) {
+        ys = scales(a[5], n, cols / 128, true, "y_scales");
+        c.y_scale_mode = ys.bytes ? EP_SCALE_UE8M0 : small(a[9], "scale_mode");
+        if (!ys.bytes && c.y_scale_mode == EP_SCALE_UE8M0) refuse("y_scales of exponents must be bytes");
+        c.y_scale_row = ys.row, c.y_scale_block = ys.block;
+    }
+    tensor(a[3], "weight_scales");
+    return library.expert_fp8(xr.at, xs.at, n, size_of(I, "I"), static_cast<const uint8_t*>(gpu_dense(a[2], kE4m3, {E, O, I}, "weights")),
+                              static_cast<const float*>(gpu_dense(a[3], kFp32, {E, (O + 127) / 128, blocks}, "weight_scales")),
+                              static_cast<const int32_t*>(dense(a[6], kInt32, {E + 1}, "expert_offsets")),
+                              static_cast<const int32_t*>(dense(a[7], kInt32, {E}, "expert_counts")), size_of(E, "E"), size_of(O, "O"),
+                              &c, yr.at, ys.at, stream_of(a[10]));
+}
+
+// Sizes of a gated block: x or grad_y [rows, H], a row tensor of width F (or 2F), E from the offsets' or the weights' tensor.
+struct Block {
+    int64_t n, H, E, F;
+    at::ScalarType type;
+};
+Block block_of(const Tensor& x, const char* what, const Tensor& act, const char* act_what, int64_t parts, const Tensor& w, const char* w_what) {
+    dimensions(x, 2, what);
+    dimensions(act, 2, act_what);
+    dimensions(w, 3, w_what);
+    return {x.size(0), x.size(1), w.size(0), act.size(1) / parts, x.scalar_type()};
+}
+
+// (x, w_gate_up, w_down, act, y, gate_up, expert_offsets, expert_counts, stream)
+long expert_ffn(PyObject* const* a) {
+    const Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w_gate_up"), &act = tensor(a[3], "act");
+    const Block b = block_of(x, "x", act, "act", 1, w, "w_gate_up");
+    ep_ffn_config_t c{};
+    c.grad_w_dtype = c.dtype = type_code(x, "x", false, false);
+    const Rows xr = gpu_rows(a[0], b.type, {b.n, b.H}, "x"), ar = gpu_rows(a[3], b.type, {b.n, b.F}, "act");
+    const Rows yr = gpu_rows_or_none(a[4], b.type, {b.n, b.H}, "y"), gr = gpu_rows_or_none(a[5], b.type, {b.n, 2 * b.F}, "gate_up");
+    if ((a[4] == Py_None) != (a[2] == Py_None)) refuse("w_down and y go together");
+    c.x_ld = xr.ld, c.act_ld = ar.ld, c.y_ld = yr.ld, c.gate_up_ld = gr.ld;
+    return library.expert_ffn(xr.at, b.n, size_of(b.H, "H"), gpu_dense(a[1], b.type, {b.E, 2 * b.F, b.H}, "w_gate_up"),
+                              gpu_dense(a[2], b.type, {b.E, b.H, b.F}, "w_down"),
+                              static_cast<const int32_t*>(dense(a[6], kInt32, {b.E + 1}, "expert_offsets")),
+                              static_cast<const int32_t*>(dense(a[7], kInt32, {b.E}, "expert_counts")), size_of(b.E, "E"),
+                              size_of(b.F, "F"), &c, gr.at, ar.at, yr.at, stream_of(a[8]));
+}
+
+// (grad_y, x, gate_up, act, w_gate_up, w_down, grad_gate_up, grad_x, grad_w_gate_up, grad_w_down, expert_offsets, expert_counts,
+//  accumulate, stream)
+long expert_ffn_backward(PyObject* const* a) {
+    const Tensor &dy = tensor(a[0], "grad_y"), &gate_up = tensor(a[2], "gate_up"), &w = tensor(a[5], "w_down");
+    const Block b = block_of(dy, "grad_y", gate_up, "gate_up", 2, w, "w_down");
+    ep_ffn_config_t c{};
+    c.grad_w_dtype = c.dtype = type_code(dy, "grad_y", false, false);
+    const Rows yr = gpu_rows(a[0], b.type, {b.n, b.H}, "grad_y"), gr = gpu_rows(a[2], b.type, {b.n, 2 * b.F}, "gate_up");
+    const Rows xr = gpu_rows_or_none(a[1], b.type, {b.n, b.H}, "x"), ar = gpu_rows_or_none(a[3], b.type, {b.n, b.F}, "act");
+    const Rows dg = gpu_rows(a[6], b.type, {b.n, 2 * b.F}, "grad_gate_up"), dx = gpu_rows_or_none(a[7], b.type, {b.n, b.H}, "grad_x");
+    auto grad_type = b.type;   // the weights' gradients: both of the tensors' type or both fp32
+    for (const int i : {8, 9})
+        if (const Tensor* t = optional_tensor(a[i], "a weight gradient"))
+            if (t->scalar_type() == kFp32) grad_type = kFp32, c.grad_w_dtype = EP_DTYPE_FP32;
+    c.accumulate = truth(a[12]);
+    c.x_ld = xr.ld, c.act_ld = ar.ld, c.y_ld = yr.ld, c.gate_up_ld = gr.ld, c.grad_x_ld = dx.ld, c.grad_gate_up_ld = dg.ld;
+    return library.expert_ffn_backward(yr.at, xr.at, gr.at, ar.at, b.n, size_of(b.H, "H"),
+                                       gpu_dense(a[4], b.type, {b.E, 2 * b.F, b.H}, "w_gate_up"),
+                                       gpu_dense(a[5], b.type, {b.E, b.H, b.F}, "w_down"),
+                                       static_cast<const int32_t*>(dense(a[10], kInt32, {b.E + 1}, "expert_offsets")),
+                                       static_cast<const int32_t*>(dense(a[11], kInt32, {b.E}, "expert_counts")), size_of(b.E, "E"),
+                                       size_of(b.F, "F"), &c, dg.at, dx.at,
+                                       gpu_dense(a[8], grad_type, {b.E, 2 * b.F, b.H}, "grad_w_gate_up"),
+                                       gpu_dense(a[9], grad_type, {b.E, b.H, b.F}, "grad_w_down"), stream_of(a[13]));
+}
+
 // No exception leaves an entry point.
 template <long (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t count) {
@@ -372,7 +502,9 @@ PyObject* open_library(PyObject*, PyObject* path) {
     Library l;
     if (!look_up(handle, "ep_router_topk", &l.router_topk) || !look_up(handle, "ep_router_topk_backward", &l.router_topk_backward) ||
         !look_up(handle, "ep_kv_append", &l.kv_append) || !look_up(handle, "ep_paged_attention", &l.paged_attention) ||
-        !look_up(handle, "ep_expert_w4", &l.expert_w4) || !look_up(handle, "ep_expert_w4_workspace", &l.expert_w4_workspace))
+        !look_up(handle, "ep_expert_w4", &l.expert_w4) || !look_up(handle, "ep_expert_w4_workspace", &l.expert_w4_workspace) ||
+        !look_up(handle, "ep_expert_fp8", &l.expert_fp8) || !look_up(handle, "ep_expert_ffn", &l.expert_ffn) ||
+        !look_up(handle, "ep_expert_ffn_backward", &l.expert_ffn_backward))
         return nullptr;
     library = l;
     Py_RETURN_NONE;
@@ -385,6 +517,9 @@ PyMethodDef methods[] = {{"open", open_library, METH_O, nullptr},
                          ENTRY(kv_append, 14),
                          ENTRY(paged_attention, 13),
                          ENTRY(expert_w4, 10),
+                         ENTRY(expert_fp8, 11),
+                         ENTRY(expert_ffn, 9),
+                         ENTRY(expert_ffn_backward, 14),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,6 +1,7 @@
 """Binding of the layer operators (include/ep_layer.h): router top-k and its
 gradient, append to a paged cache, attention of one new token over it, and the
-experts' products with 4-bit weights.
+experts' products: with 4-bit weights, in 8-bit floating point, and the gated
+block in 16 bits with its gradients.
 
 As in the package itself, each function has the name of the C entry point and
 only marshals arguments; sizes, strides and types come from the tensors. What
@@ -17,13 +18,14 @@ import importlib
 
 import torch
 
-from . import EP_DTYPE_BF16, EP_DTYPE_FP16, EP_ERR_INVALID_ARG, EP_OK, _LIB_PATH, EPError, lib
+from . import EP_DTYPE_BF16, EP_DTYPE_FP16, EP_ERR_INVALID_ARG, EP_OK, EP_SCALE_FP32, _LIB_PATH, EPError, lib
 
 EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
 EP_ACT_NONE, EP_ACT_SWIGLU = 0, 1
 
 EXPORTS = ("ep_router_topk", "ep_router_topk_backward", "ep_kv_append", "ep_paged_attention",
-           "ep_paged_attention_workspace", "ep_expert_w4", "ep_expert_w4_workspace")
+           "ep_paged_attention_workspace", "ep_expert_w4", "ep_expert_w4_workspace", "ep_expert_fp8", "ep_expert_ffn",
+           "ep_expert_ffn_backward")
 
 _i32, _i64, _f32, _P = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
@@ -62,6 +64,19 @@ class W4Config(ctypes.Structure):
     _fields_ = [("dtype", _i32), ("group_size", _i32), ("activation", _i32), ("x_ld", _i64), ("y_ld", _i64)]
 
 
+class Fp8Config(ctypes.Structure):
+    """ep_fp8_config_t (include/ep_layer.h)."""
+    _fields_ = [("x_dtype", _i32), ("y_dtype", _i32), ("activation", _i32), ("x_scale_mode", _i32),
+                ("y_scale_mode", _i32), ("x_ld", _i64), ("y_ld", _i64), ("x_scale_row", _i64), ("x_scale_block", _i64),
+                ("y_scale_row", _i64), ("y_scale_block", _i64)]
+
+
+class FfnConfig(ctypes.Structure):
+    """ep_ffn_config_t (include/ep_layer.h)."""
+    _fields_ = [("dtype", _i32), ("grad_w_dtype", _i32), ("accumulate", _i32), ("x_ld", _i64), ("gate_up_ld", _i64),
+                ("act_ld", _i64), ("y_ld", _i64), ("grad_x_ld", _i64), ("grad_gate_up_ld", _i64)]
+
+
 def declare(L) -> None:
     """Argument types of this module's entry points on a loaded library."""
     ref = ctypes.POINTER
@@ -72,6 +87,10 @@ def declare(L) -> None:
     L.ep_paged_attention_workspace.argtypes = [_i32, _i32, _i32, _i32]
     L.ep_expert_w4.argtypes = [_P, _i64, _i32, _P, _P, _P, _P, _P, _i32, _i32, ref(W4Config), _P, _P, _i64, _P]
     L.ep_expert_w4_workspace.argtypes = [_i64, _i32, _i32, _i32]
+    L.ep_expert_fp8.argtypes = [_P, _P, _i64, _i32, _P, _P, _P, _P, _i32, _i32, ref(Fp8Config), _P, _P, _P]
+    L.ep_expert_ffn.argtypes = [_P, _i64, _i32, _P, _P, _P, _P, _i32, _i32, ref(FfnConfig), _P, _P, _P, _P]
+    L.ep_expert_ffn_backward.argtypes = [_P, _P, _P, _P, _i64, _i32, _P, _P, _P, _P, _i32, _i32, ref(FfnConfig), _P, _P,
+                                         _P, _P, _P]
     for name in EXPORTS:
         getattr(L, name).restype = _i64 if name.endswith("workspace") else _i32
 
@@ -165,3 +184,41 @@ def ep_expert_w4_workspace(x, scales) -> int:
     if size < 0:
         raise EPError(EP_ERR_INVALID_ARG, "ep_expert_w4_workspace")
     return size
+
+
+def ep_expert_fp8(x, x_scales, weights, weight_scales, y, expert_offsets=None, expert_counts=None,
+                  activation: int = EP_ACT_NONE, y_scales=None, scale_mode: int = EP_SCALE_FP32, stream=None) -> None:
+    """y [rows, O] (O/2 columns with EP_ACT_SWIGLU) = x [rows, I] (float8_e4m3fn
+    or float8_e5m2, the fp8 dispatch's bytes by .view()) with x_scales
+    [rows, I/128] (fp32, or uint8 exponents; a transposed view for column-major
+    scales) times each row's expert's weights [E, O, I] float8_e4m3fn with
+    weight_scales [E, ceil(O/128), I/128] fp32. y is bf16 or fp16, or
+    float8_e4m3fn with y_scales [rows, columns/128] (fp32 by scale_mode, or uint8
+    exponents), which the next call takes as x and x_scales. Rows belong to
+    experts by expert_offsets [E + 1] int32 (None: one expert); with
+    expert_counts [E] int32 only each expert's first rows count."""
+    _check((_bound or _bind()).expert_fp8(x, x_scales, weights, weight_scales, y, y_scales, expert_offsets, expert_counts,
+                                          activation, scale_mode, stream), "ep_expert_fp8")
+
+
+def ep_expert_ffn(x, w_gate_up, w_down, act, y, gate_up=None, expert_offsets=None, expert_counts=None,
+                  stream=None) -> None:
+    """act [rows, F] = silu(gate) * up with (gate, up) = w_gate_up [E, 2F, H] x
+    [rows, H], and y [rows, H] = w_down [E, H, F] act, by expert as in
+    ep_expert_fp8, all bf16 or all fp16. gate_up [rows, 2F], if given, gets gate
+    and up for the backward call. w_down and y may be None: act alone."""
+    _check((_bound or _bind()).expert_ffn(x, w_gate_up, w_down, act, y, gate_up, expert_offsets, expert_counts, stream),
+           "ep_expert_ffn")
+
+
+def ep_expert_ffn_backward(grad_y, x, gate_up, act, w_gate_up, w_down, grad_gate_up, grad_x=None, grad_w_gate_up=None,
+                           grad_w_down=None, expert_offsets=None, expert_counts=None, accumulate: bool = False,
+                           stream=None) -> None:
+    """Gradients of ep_expert_ffn from grad_y [rows, H]: grad_gate_up [rows, 2F]
+    and those of grad_x [rows, H], grad_w_gate_up [E, 2F, H] and grad_w_down
+    [E, H, F] that are given. The weights' are of the tensors' type or fp32, and
+    with accumulate they are added to what is there. x is needed for
+    grad_w_gate_up only, act for grad_w_down and w_gate_up for grad_x."""
+    _check((_bound or _bind()).expert_ffn_backward(grad_y, x, gate_up, act, w_gate_up, w_down, grad_gate_up, grad_x,
+                                                   grad_w_gate_up, grad_w_down, expert_offsets, expert_counts, accumulate,
+                                                   stream), "ep_expert_ffn_backward")

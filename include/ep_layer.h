@@ -12,6 +12,11 @@
  *                            that cache
  *   ep_expert_w4             the experts' products on dispatched rows with
  *                            4-bit weights and group scales
+ *   ep_expert_fp8            the same on rows of the fp8 dispatch, with 8-bit
+ *                            weights and block scales
+ *   ep_expert_ffn            the experts' gated feed-forward block in 16 bits
+ *   ep_expert_ffn_backward   its gradients (between ep_combine_backward and
+ *                            ep_dispatch_backward)
  *
  * The conventions of ep.h hold: device pointers owned by the caller, work
  * enqueued on `stream` and asynchronous, arguments checked on the host before
@@ -258,6 +263,114 @@ EP_API ep_status_t ep_expert_w4(const void* x, int64_t rows, int I, const uint8_
 
 /* Bytes of workspace that ep_expert_w4 needs; -1 for invalid sizes. */
 EP_API int64_t ep_expert_w4_workspace(int64_t rows, int I, int group_size, int dtype);
+
+/* ------------------------------------------------------- 8-bit experts */
+
+typedef struct {
+    int x_dtype;            /* EP_DTYPE_FP8_E4M3 or EP_DTYPE_FP8_E5M2            */
+    int y_dtype;            /* EP_DTYPE_BF16, EP_DTYPE_FP16 or EP_DTYPE_FP8_E4M3 */
+    int activation;         /* ep_activation_t                                 */
+    int x_scale_mode;       /* EP_SCALE_UE8M0: x_scales are exponent bytes; the
+                               other modes: fp32                               */
+    int y_scale_mode;       /* of an e4m3 y, as in ep_dispatch_ex               */
+    int64_t x_ld, y_ld;     /* elements from one row to the next                */
+    int64_t x_scale_row, x_scale_block;   /* scales from one row, one block of 128
+                               inputs, to the next: (I/128, 1) row-major, (1, ld)
+                               column-major                                    */
+    int64_t y_scale_row, y_scale_block;
+} ep_fp8_config_t;
+
+/*
+ * ep_expert_fp8 -- y[n] = W_e x[n] for the rows n of each expert e, with
+ *   x[n, i] = x_scales[n, i / 128] * code[n, i],
+ *   W_e[o, i] = weight_scales[e, o / 128, i / 128] * code[e, o, i].
+ *
+ *  x              device, codes [rows, I] in ep_dispatch's order, 16-byte aligned
+ *                 rows; I a multiple of 128.
+ *  x_scales       device, [rows, I/128] by the strides of the config.
+ *  weights        device, e4m3 codes [E, O, I], dense, 16-byte aligned.
+ *  weight_scales  device, fp32 [E, ceil(O / 128), I/128], dense.
+ *  expert_offsets, expert_counts, E
+ *                 as in ep_expert_w4.
+ *  O              weight rows; even with EP_ACT_SWIGLU, whose y has O/2 columns:
+ *                 gate = weight row j, up = row O/2 + j.
+ *  y              device, [rows, O or O/2], 16-bit, or e4m3 codes whose columns
+ *                 are a multiple of 128.
+ *  y_scales       device, with an e4m3 y: [rows, columns/128] by the strides of
+ *                 the config, fp32 or (EP_SCALE_UE8M0) exponent bytes. Scales and
+ *                 codes are those of ep_dispatch_ex for the fp32 results: amax of
+ *                 128 columns / 448, codes of result / scale. What it writes is
+ *                 what the next call reads as x. Ignored with a 16-bit y.
+ * The 128 products of a block are summed in fp32, the block's sum times its two
+ * scales is added in fp32, and y is rounded once, after the activation. A row
+ * with a NaN gives NaN. Rows that belong to no expert are not written. Offsets
+ * are taken as at most `rows`; rows, I and O are at most 2^31 - 512.
+ */
+EP_API ep_status_t ep_expert_fp8(const void* x, const void* x_scales, int64_t rows, int I, const uint8_t* weights,
+                                 const float* weight_scales, const int32_t* expert_offsets,
+                                 const int32_t* expert_counts, int E, int O, const ep_fp8_config_t* config, void* y,
+                                 void* y_scales, void* stream);
+
+/* ------------------------------------------------ gated block in 16 bits */
+
+typedef struct {
+    int dtype;              /* of all but the weights' gradients: EP_DTYPE_BF16
+                               or EP_DTYPE_FP16                                 */
+    int grad_w_dtype;       /* the weights' gradients: dtype or EP_DTYPE_FP32   */
+    int accumulate;         /* 0: the weights' gradients are written; 1: added to
+                               what is there                                   */
+    int64_t x_ld, gate_up_ld, act_ld, y_ld;     /* elements from one row to the next;
+                               grad_y has y_ld                                 */
+    int64_t grad_x_ld, grad_gate_up_ld;
+} ep_ffn_config_t;
+
+/*
+ * ep_expert_ffn -- for the rows n of each expert e
+ *   (gate, up) = W1_e x[n],  act[n] = silu(gate) * up,  y[n] = W2_e act[n].
+ *
+ *  x              device, [rows, H] in ep_dispatch's order. H and F multiples of 8;
+ *                 rows of x and of all other row tensors start on 16 bytes.
+ *  w_gate_up      device, [E, 2F, H], dense, 16-byte aligned: gate = weight row j,
+ *                 up = row F + j.
+ *  w_down         device, [E, H, F], dense, 16-byte aligned, or NULL with a NULL y.
+ *  expert_offsets, expert_counts, E
+ *                 as in ep_expert_w4.
+ *  gate_up        device, [rows, 2F] or NULL: gate and up, for the backward call.
+ *  act            device, [rows, F]: written, and read for y.
+ *  y              device, [rows, H], or NULL: act (and gate_up) only.
+ * Sums are fp32; act is rounded once after the activation of the fp32 gate and
+ * up, and y is the product of the rounded act. Rows that belong to no expert
+ * are not written. rows, H and 2F are at most 2^31 - 512.
+ */
+EP_API ep_status_t ep_expert_ffn(const void* x, int64_t rows, int H, const void* w_gate_up, const void* w_down,
+                                 const int32_t* expert_offsets, const int32_t* expert_counts, int E, int F,
+                                 const ep_ffn_config_t* config, void* gate_up, void* act, void* y, void* stream);
+
+/*
+ * ep_expert_ffn_backward -- the gradients of a loss with gradient grad_y at y:
+ *   dact = W2^T grad_y,  s = 1 / (1 + exp(-gate)),
+ *   grad_gate_up = (dact up s (1 + gate (1 - s)), dact gate s),
+ *   grad_x = W1^T grad_gate_up,
+ *   grad_w_gate_up[e] = sum over e's rows of grad_gate_up[n] x[n]^T,
+ *   grad_w_down[e] = sum over e's rows of grad_y[n] act[n]^T.
+ *
+ *  gate_up, act   as ep_expert_ffn wrote them.
+ *  grad_gate_up   device, [rows, 2F]: written, and read for the others (which are
+ *                 products of the rounded grad_gate_up).
+ *  grad_x         device, [rows, H], or NULL.
+ *  grad_w_gate_up, grad_w_down
+ *                 device, the weights' shapes, dense, 16-byte aligned, or NULL.
+ *                 Every element is written (added to, with config.accumulate);
+ *                 an expert without rows has zero gradients.
+ * Sums are fp32 and taken in a fixed order: the same inputs give the same bits.
+ * Rows that belong to no expert are not written and enter nothing. Without
+ * grad_x and grad_w_gate_up, grad_gate_up is still written.
+ */
+EP_API ep_status_t ep_expert_ffn_backward(const void* grad_y, const void* x, const void* gate_up, const void* act,
+                                          int64_t rows, int H, const void* w_gate_up, const void* w_down,
+                                          const int32_t* expert_offsets, const int32_t* expert_counts, int E, int F,
+                                          const ep_ffn_config_t* config, void* grad_gate_up, void* grad_x,
+                                          void* grad_w_gate_up, void* grad_w_down, void* stream);
 
 #ifdef __cplusplus
 }

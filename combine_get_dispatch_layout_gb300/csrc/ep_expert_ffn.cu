@@ -16,9 +16,9 @@ namespace {
 constexpr int kEpilogueWarps = 8;
 constexpr int kLoader = kEpilogueWarps, kIssuer = kLoader + 1;
 constexpr int kThreads = 32 * (kEpilogueWarps + 2);
-constexpr int kLanes = 128;
+constexpr int kLanes = 256;                     // of a pair: 128 in each CTA's TMEM
 constexpr int kStep = 64;                       // contraction of a stage: 128 bytes
-constexpr int kABytes = kLanes * kStep * 2;
+constexpr int kABytes = kLanes / 2 * kStep * 2;
 constexpr int kMostStages = 10;
 constexpr int kRing = 192 * 1024 + 8 * 1024;
 constexpr int kShared = 1024 + kRing + 512 + (kTileTable + 1) * 4;
@@ -48,14 +48,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned char* const ring = shared_bytes + (1024 - smem_addr(shared_bytes) % 1024) % 1024;
     uint64_t* const barriers = reinterpret_cast<uint64_t*>(ring + kRing);
     const uint32_t full = smem_addr(barriers), empty = full + 8 * kMostStages;
-    const uint32_t sums_full = empty + 8 * kMostStages, sums_empty = sums_full + 16;
+    const uint32_t other_full = empty + 8 * kMostStages;   // kGradW, an expert's last rows: the second CTA's half is ready
+    const uint32_t sums_full = other_full + 8 * kMostStages, sums_empty = sums_full + 16;
     uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(barriers) + 120;
     volatile int* const dead = reinterpret_cast<volatile int*>(tmem_at + 1);
     int* const table = reinterpret_cast<int*>(barriers) + 128;
-    static_assert((2 * kMostStages + 4) * 2 <= 120, "");
+    static_assert((3 * kMostStages + 4) * 2 <= 120, "");
     __shared__ int warp_sum[kThreads / 32];
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = pair_rank();
     if (warp == kLoader) {
         tmem_alloc_all(smem_addr(tmem_at));
         if (lane == 0) {
@@ -63,10 +64,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < a.stages; ++i) {
                 barrier_init(full + 8 * i, 1);
                 barrier_init(empty + 8 * i, 1);
+                barrier_init(other_full + 8 * i, 1);
             }
             for (int i = 0; i < 2; ++i) {
                 barrier_init(sums_full + 8 * i, 1);
-                barrier_init(sums_empty + 8 * i, kEpilogueWarps);
+                barrier_init(sums_empty + 8 * i, 2 * kEpilogueWarps);
             }
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
@@ -75,9 +77,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (WHAT != kGradW) fill_table<kThreads>(a.g, a.plan, table, warp_sum);
     tmem_fence_before();
     __syncthreads();
+    cluster_sync();   // (both CTAs' barriers are ready)
     tmem_fence_after();
     const uint32_t tmem = __shfl_sync(kFullMask, *tmem_at, 0);
     const bool leader = elected();
+
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
     // An item: `cols` columns (rows of the output) from `col` on, lanes from m * kLanes on, `steps` stages; of kGradW the
     // contraction is over rows [row, row + rows).
@@ -109,64 +114,72 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLoader) {
         int slot = 0;
         uint32_t parity = 1;   // (the first round of the ring waits for nothing)
-        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        for (int64_t i = pair; i < items; i += pairs) {
             const Item it = decode(i);
             const int a_boxes = WHAT == kGateUp ? 4 : WHAT == kDown ? 1 : 2;
-            const int b_boxes = WHAT == kGradW ? (it.cols + 63) / 64 : (max(it.cols, 1) + a.box - 1) / a.box;
+            const int half = columns_of(it.cols) / 2;   // columns of each CTA
+            const int b_boxes = WHAT == kGradW ? (half + 63) / 64 : (half + a.box - 1) / a.box;
+            const int lane0 = it.m * kLanes + rank * (kLanes / 2), col0 = it.col + rank * half;
             for (int s = 0; s < it.steps; ++s) {
-                const uint32_t bar = full + 8 * slot, at_a = smem_addr(ring) + slot * a.stage_bytes, at_b = at_a + kABytes;
+                // both CTAs' boxes count on the first one's barrier
+                const uint32_t bar = in_first(full + 8 * slot), at_a = smem_addr(ring) + slot * a.stage_bytes, at_b = at_a + kABytes;
                 barrier_wait(empty + 8 * slot, parity, dead);
                 if constexpr (WHAT == kGradW) {
                     // [64 channels] x [box rows] of both operands, boxes with real rows only
+                    // (a stage with rows of others behind the expert's is the second CTA's own until it has cleared them)
+                    const bool part = it.rows - s * kStep < kStep;
+                    const uint32_t to = part ? full + 8 * slot : bar;
                     const int down = (min(kStep, it.rows - s * kStep) + a.box - 1) / a.box, all = (2 + b_boxes) * down;
-                    if (lane == 0) barrier_expect(bar, all * a.box * 128);
+                    if (lane == 0 && (rank == 0 || part)) barrier_expect(full + 8 * slot, all * a.box * 128 * (part ? 1 : 2));
                     __syncwarp();
                     if (lane < all) {
                         const int k = lane % down, j = lane / down, row = it.row + s * kStep + k * a.box;
-                        if (j < 2) load_box(at_a + j * 8192 + k * a.box * 128, &a_map, it.m * kLanes + j * 64, row, 0, 0, bar);
-                        else load_box(at_b + (j - 2) * 8192 + k * a.box * 128, &b_map, it.col + (j - 2) * 64, row, 0, 0, bar);
+                        if (j < 2) load_box_pair(at_a + j * 8192 + k * a.box * 128, &a_map, lane0 + j * 64, row, 0, 0, to);
+                        else load_box_pair(at_b + (j - 2) * 8192 + k * a.box * 128, &b_map, col0 + (j - 2) * 64, row, 0, 0, to);
                     }
                 } else {
-                    if (lane == 0) barrier_expect(bar, kABytes + b_boxes * a.box * 128);
+                    if (lane == 0 && rank == 0) barrier_expect(full + 8 * slot, 2 * (kABytes + b_boxes * a.box * 128));
                     __syncwarp();
                     if (lane < a_boxes) {
                         if (WHAT == kGateUp)   // the 16 gate and the 16 up rows of a warp
-                            load_box(at_a + lane * 4096, &a_map, s * kStep, it.m * (kLanes / 2) + lane * 16, 0, it.expert, bar);
+                            load_box_pair(at_a + lane * 4096, &a_map, s * kStep, lane0 / 2 + lane * 16, 0, it.expert, bar);
                         else if (WHAT == kDown)
-                            load_box(at_a, &a_map, s * kStep, it.m * kLanes, 0, it.expert, bar);
+                            load_box_pair(at_a, &a_map, s * kStep, lane0, 0, it.expert, bar);
                         else
-                            load_box(at_a + lane * 8192, &a_map, it.m * kLanes + lane * 64, s * kStep, 0, it.expert, bar);
+                            load_box_pair(at_a + lane * 8192, &a_map, lane0 + lane * 64, s * kStep, 0, it.expert, bar);
                     } else if (lane < a_boxes + b_boxes) {
                         const int j = lane - a_boxes;
-                        load_box(at_b + j * a.box * 128, &b_map, s * kStep, it.row + j * a.box, 0, 0, bar);
+                        load_box_pair(at_b + j * a.box * 128, &b_map, s * kStep, col0 + j * a.box, 0, 0, bar);
                     }
                 }
                 if (++slot == a.stages) slot = 0, parity ^= 1;
             }
         }
     } else if (warp == kIssuer) {
-        // fp32 sums; operands' type; A outward, B outward; 128 lanes
+        // fp32 sums; operands' type; A outward, B outward; 256 lanes
         constexpr uint32_t kType = std::is_same_v<T, __nv_bfloat16> ? 1u : 0u;
         constexpr bool kAOut = WHAT >= kGradAct, kBOut = WHAT == kGradW;
         constexpr uint32_t kShape = (1u << 4) | (kType << 7) | (kType << 10) | (kAOut ? 1u << 15 : 0u) | (kBOut ? 1u << 16 : 0u) |
                                     (static_cast<uint32_t>(kLanes / 16) << 24);
         int slot = 0, buffer = 0;
-        uint32_t parity = 0, sums_parity = 1;
-        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        uint32_t parity = 0, sums_parity = 1, part_parity = 0;   // part_parity: a bit for each slot
+        // (the second CTA's warp has only the last stages of kGradW to see to)
+        for (int64_t i = pair; i < items && (rank == 0 || WHAT == kGradW); i += pairs) {
             const Item it = decode(i);
             if (it.steps == 0) continue;
             const uint32_t shape = kShape | static_cast<uint32_t>(columns_of(it.cols) / 8) << 17;
             const uint32_t sums = tmem + buffer * 256;
-            barrier_wait(sums_empty + 8 * buffer, sums_parity, dead);
+            if (rank == 0) barrier_wait(sums_empty + 8 * buffer, sums_parity, dead);
             for (int s = 0; s < it.steps; ++s) {
-                barrier_wait(full + 8 * slot, parity, dead);
                 const uint32_t at_a = smem_addr(ring) + slot * a.stage_bytes, at_b = at_a + kABytes;
                 int depth = kStep / 16;   // products of 16
+                if (rank == 0) barrier_wait(full + 8 * slot, parity, dead);
                 if constexpr (WHAT == kGradW) {
                     const int left = it.rows - s * kStep;
                     if (left < kStep) {   // rows behind the expert's last belong to others: zeros instead, in both operands
+                        if (rank == 1) barrier_wait(full + 8 * slot, (part_parity >> slot) & 1, dead);
                         depth = (left + 15) / 16;
-                        const int blocks = 2 + (it.cols + 63) / 64;
+                        const int blocks = 2 + (columns_of(it.cols) / 2 + 63) / 64;
                         for (int j = lane; j < (depth * 16 - left) * blocks * 8; j += 32) {
                             const int line = j / 8, row = left + line / blocks;
                             *reinterpret_cast<uint4*>(ring + slot * a.stage_bytes + line % blocks * 8192 + row * 128 + j % 8 * 16) =
@@ -174,16 +187,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
+                        if (rank == 1 && lane == 0) barrier_arrive_cluster(in_first(other_full + 8 * slot));
+                        if (rank == 0) barrier_wait_cluster(other_full + 8 * slot, (part_parity >> slot) & 1, dead);
+                        part_parity ^= 1u << slot;
                     }
                 }
                 tmem_fence_after();
-                if (leader) {
+                if (rank == 0 && leader) {
                     const uint64_t da = kAOut ? operand_outward(at_a, 8192) : operand(at_a, 1024);
                     const uint64_t db = kBOut ? operand_outward(at_b, 8192) : operand(at_b, 1024);
                     for (int k = 0; k < depth; ++k)
-                        multiply_shared<false>(sums, da + k * (kAOut ? 128 : 2), db + k * (kBOut ? 128 : 2), shape, s > 0 || k > 0);
-                    multiply_done(empty + 8 * slot);
-                    if (s + 1 == it.steps) multiply_done(sums_full + 8 * buffer);
+                        multiply_pair<false>(sums, da + k * (kAOut ? 128 : 2), db + k * (kBOut ? 128 : 2), shape, s > 0 || k > 0);
+                    pair_done(empty + 8 * slot);
+                    if (s + 1 == it.steps) pair_done(sums_full + 8 * buffer);
                 }
                 __syncwarp();
                 if (++slot == a.stages) slot = 0, parity ^= 1;
@@ -195,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int half = warp >> 2;
         int buffer = 0;
         uint32_t parity = 0;
-        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        for (int64_t i = pair; i < items; i += pairs) {
             const Item it = decode(i);
             const uint32_t mine = tmem + buffer * 256 + (static_cast<uint32_t>(warp & 3) << 21);   // lane 32 * (warp % 4), upper half
             if (it.steps > 0) {
@@ -203,7 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_fence_after();
             }
             // this thread's channel; of gate and up a warp's lanes are 16 gate and 16 up rows
-            const int chan = WHAT == kGateUp ? it.m * (kLanes / 2) + (warp & 3) * 16 + (lane & 15) : it.m * kLanes + (warp & 3) * 32 + lane;
+            const int lane0 = it.m * kLanes + rank * (kLanes / 2) + (warp & 3) * 32;
+            const int chan = WHAT == kGateUp ? lane0 / 2 + (lane & 15) : lane0 + lane;
             const bool real = chan < a.lanes;
             for (int c0 = half * 32; c0 < it.cols; c0 += 64) {
                 uint32_t raw[32];
@@ -247,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (j < many) {
-                                const float d = __uint_as_float(raw[j]), gt = to_float(gate[j]), s = 1.0f / (1.0f + expf(-gt));
+                                const float d = __uint_as_float(raw[j]), gt = to_float(gate[j]), s = sigmoid(gt);
                                 to[j * a.out_ld] = from_float<T>(d * to_float(up[j]) * s * (1.0f + gt * (1.0f - s)));
                                 to[j * a.out_ld + a.lanes] = from_float<T>(d * gt * s);
                             }
@@ -278,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (it.steps > 0) {
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) barrier_arrive(sums_empty + 8 * buffer);
+                if (lane == 0) barrier_arrive_pair(in_first(sums_empty + 8 * buffer));
                 buffer ^= 1;
                 if (buffer == 0) parity ^= 1;
             }
@@ -286,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tmem_fence_before();
     __syncthreads();
+    cluster_sync();   // (neither CTA leaves while the other may arrive on its barriers)
     if (warp == kLoader) {
         tmem_fence_after();
         tmem_free_all(tmem);
@@ -297,16 +315,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <typename T, int WHAT>
 cudaError_t launch_gemm(Gemm& a, const CUtensorMap& a_map, const CUtensorMap& b_map, cudaStream_t stream) {
     static int known[64];
-    int sms = 0;
-    cudaError_t err = prepare_persistent(expert_gemm_kernel<T, WHAT>, kShared, known, &sms);
+    int pairs = 0;
+    cudaError_t err = pairs_at_once(expert_gemm_kernel<T, WHAT>, kThreads, kShared, known, &pairs);
     if (err != cudaSuccess) return err;
-    a.stage_bytes = kABytes + a.plan.cap * kStep * 2;
+    a.stage_bytes = kABytes + a.plan.cap / 2 * kStep * 2;
     a.stages = kRing / a.stage_bytes < kMostStages ? kRing / a.stage_bytes : kMostStages;
     const int64_t used = a.g.rows < a.g.E ? a.g.rows : a.g.E;
     const int64_t most = WHAT == kGradW ? static_cast<int64_t>(a.g.E) * a.plan.m_tiles * a.n_tiles
                                         : (a.g.rows + used * (a.plan.cap - 1)) / a.plan.cap * a.plan.m_tiles;
-    return launch_dependent(expert_gemm_kernel<T, WHAT>, dim3(static_cast<unsigned>(most < sms ? most : sms)), dim3(kThreads), kShared,
-                            stream, a, a_map, b_map);
+    return launch_pairs(expert_gemm_kernel<T, WHAT>, static_cast<int>(most < pairs ? most : pairs), kThreads, kShared, stream, a, a_map,
+                        b_map);
 }
 
 Gemm gemm_of(const FfnArgs& f, int lanes, int lanes_of_tile, int inner) {
@@ -319,7 +337,7 @@ Gemm gemm_of(const FfnArgs& f, int lanes, int lanes_of_tile, int inner) {
     while (((f.g.E - 1) >> a.plan.shift) + 1 > kTileTable) ++a.plan.shift;
     const int64_t used = f.g.rows < f.g.E ? f.g.rows : f.g.E, mean = (f.g.rows - 1) / used + 1;
     a.plan.cap = mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 112 ? 128 : 256;
-    a.box = a.plan.cap < 64 ? 16 : 64;
+    a.box = a.plan.cap <= 64 ? 16 : 64;
     return a;
 }
 
@@ -341,7 +359,7 @@ cudaError_t forward(const FfnArgs& f, cudaStream_t stream) {
     if (err != cudaSuccess || !f.y) return err;
     a = gemm_of(f, f.H, kLanes, f.F);
     a.out = f.y, a.out_ld = f.y_ld;
-    err = box_map(&am, f.w_down, f.dtype, F, H, 1, f.g.E, F * 2, F * H * 2, F * H * 2, kLanes, 1);
+    err = box_map(&am, f.w_down, f.dtype, F, H, 1, f.g.E, F * 2, F * H * 2, F * H * 2, kLanes / 2, 1);
     if (err == cudaSuccess) err = rows_map(&bm, f, f.act, F, f.act_ld, a.box);
     return err == cudaSuccess ? launch_gemm<T, kDown>(a, am, bm, stream) : err;
 }

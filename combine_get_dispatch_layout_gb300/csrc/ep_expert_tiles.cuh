@@ -107,12 +107,71 @@ __device__ __forceinline__ Tile tile_at(const ExpertRows& g, const TilePlan& p, 
 // Columns of the product for n rows of a tile.
 __device__ __forceinline__ int columns_of(int n) { return max((n + 15) / 16 * 16, 16); }
 
+// ---- pairs: two CTAs of a cluster multiply as one, operand A's 256 rows and operand B's columns half in each. The first
+// issues for both; each has the sums of its own 128 rows in its TMEM.
+
+__device__ __forceinline__ uint32_t pair_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r & 1;
+}
+// Address, for the cluster, of the same place in a CTA's shared memory.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ uint32_t in_first(uint32_t addr) { return in_cta(addr, 0); }
+__device__ __forceinline__ void store_other(uint32_t addr, uint32_t rank, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(in_cta(addr, rank)), "f"(v) : "memory");
+}
+// On a barrier of either CTA. (Orders tensor memory, with the tcgen05 fences, and nothing else: ordering all memory for
+// the cluster took 2000 clocks a stage.)
+__device__ __forceinline__ void barrier_arrive_pair(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same, ordering what this thread has written, for barrier_wait_cluster.
+__device__ __forceinline__ void barrier_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool barrier_try_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+// As barrier_wait, for a barrier that the other CTA arrives on.
+__device__ __forceinline__ void barrier_wait_cluster(uint32_t bar, uint32_t parity, volatile int* dead) {
+    for (int i = 0; i < (1 << 22); ++i) {
+        if (barrier_try_cluster(bar, parity)) return;
+        if ((i & 1023) == 1023 && *dead) return;
+    }
+    *dead = 1;
+}
+// A box into this CTA's shared memory that counts on a barrier of either CTA.
+__device__ __forceinline__ void load_box_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_alloc_all(uint32_t to) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(to) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(to) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_free_all(uint32_t tmem) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&r)[32]) {
     asm volatile(
@@ -125,20 +184,40 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&r)[32]) {
         : "r"(at)
         : "memory");
 }
-// sums [128 lanes][N] (+)= A [128 lanes] * B [N columns]^T, both in shared memory.
+// sums [2 x 128 lanes][N] (+)= A [2 x 128 lanes] * B [2 x N / 2 columns]^T, all in the pair's shared memory.
 template <bool FP8>
-__device__ __forceinline__ void multiply_shared(uint32_t sums, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+__device__ __forceinline__ void multiply_pair(uint32_t sums, uint64_t a, uint64_t b, uint32_t shape, bool add) {
     if constexpr (FP8)
-        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(sums),
+        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(sums),
                      "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
                      : "memory");
     else
-        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(sums),
+        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(sums),
                      "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
                      : "memory");
 }
+// Arrives on both CTAs' barriers at this place once the products so far are done.
+__device__ __forceinline__ void pair_done(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"(static_cast<uint16_t>(3))
+                 : "memory");
+}
 
-__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
+// exp(v): 2^t for t = v log2(e) in two parts, so that large |v| lose nothing (about 2 units in the last place).
+__device__ __forceinline__ float exp_of(float v) {
+    const float t = v * 1.44269504f;
+    const float rest = fmaf(v, 1.44269504f, -t) + v * 1.92596299e-8f;
+    float e;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return e < INFINITY ? fmaf(e, rest * 0.69314718f, e) : e;
+}
+// 1 / (1 + exp(-v)); the approximate reciprocal is within 1 unit in the last place, and 0 of infinity
+__device__ __forceinline__ float sigmoid(float v) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp_of(-v)));
+    return r;
+}
+__device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 
 // ------------------------------------------------------------------ host
 
@@ -164,19 +243,51 @@ cudaError_t box_map(CUtensorMap* map, const void* base, int dtype, int64_t x, in
                : cudaErrorInvalidValue;
 }
 
-// SMs of the current device, with the kernel's shared memory limit raised: looked up once per device (a race writes
-// the same value).
+// Pairs of CTAs of a kernel that the current device holds at once, with the kernel's shared memory limit raised: looked up
+// once per device (a race writes the same value).
 template <typename Kernel>
-cudaError_t prepare_persistent(Kernel kernel, int smem, int* known, int* sms) {
+cudaError_t pairs_at_once(Kernel kernel, int threads, int smem, int* known, int* pairs) {
     constexpr int kDevices = 64;
-    int dev = 0;
+    int dev = 0, sms = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
-    if (dev < kDevices && (*sms = __atomic_load_n(&known[dev], __ATOMIC_ACQUIRE)) > 0) return cudaSuccess;
+    if (dev < kDevices && (*pairs = __atomic_load_n(&known[dev], __ATOMIC_ACQUIRE)) > 0) return cudaSuccess;
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (err == cudaSuccess) err = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-    if (err == cudaSuccess && dev < kDevices) __atomic_store_n(&known[dev], *sms, __ATOMIC_RELEASE);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sms / 2 * 2);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    err = cudaOccupancyMaxActiveClusters(pairs, kernel, &cfg);
+    if (err == cudaSuccess && *pairs < 1) err = cudaErrorInvalidConfiguration;
+    if (err == cudaSuccess && dev < kDevices) __atomic_store_n(&known[dev], *pairs, __ATOMIC_RELEASE);
     return err;
+}
+
+// Launches `pairs` clusters of two CTAs as a programmatic dependent of the work before.
+template <typename... Params, typename... Args>
+cudaError_t launch_pairs(void (*kernel)(Params...), int pairs, int threads, int smem, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace

@@ -39,6 +39,15 @@ static __device__ __noinline__ void barrier_wait_long(uint32_t bar, uint32_t par
 __device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
     if (!barrier_try(bar, parity)) barrier_wait_long(bar, parity, dead);
 }
+// The same without a call, for warps whose registers were moved to them by setmaxnreg: the assembler finds no allocation
+// for them around a function.
+__device__ __forceinline__ void barrier_wait_inline(uint32_t bar, uint32_t parity, volatile int* dead) {
+    for (int i = 0; i < (1 << 22); ++i) {
+        if (barrier_try(bar, parity)) return;
+        if ((i & 1023) == 1023 && *dead) return;
+    }
+    *dead = 1;
+}
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),

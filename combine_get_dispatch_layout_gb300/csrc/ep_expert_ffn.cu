@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t raw[32];
                 if (it.steps > 0) {
                     tmem_load32(mine + c0, raw);
-                    tmem_load_wait();
+                    tmem_loaded(raw);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) raw[j] = 0;

@@ -18,15 +18,21 @@ constexpr int kScaleBlocks = 2, kScaleSlots = 3;   // the ring of scales: blocks
 constexpr int kScaleSets = 3;                   // weight scales that a CTA's 128 weight rows have at most in a block
 constexpr int kMostStages = 10;
 
-template <int COLS>
+constexpr int kMostColumns = 96;                // rows of x that are columns, where rows may be lanes too
+
+// COLS: rows of x that are columns of a product, at most. LANES: tiles of more rows have them as lanes.
+template <int COLS, bool LANES>
 struct Shape {
-    static constexpr int kWide = COLS == 256;                // 128 sums a thread: registers move to the consumers
+    static_assert(!LANES || COLS == 128, "");
     static constexpr int kCols = COLS >= 128 ? COLS / 2 : COLS;   // columns of a consuming warp
+    static constexpr int kStride = LANES ? 256 : COLS;            // columns of a buffer of sums in TMEM
+    static constexpr int kBuffers = 512 / kStride < 4 ? 512 / kStride : 4;
     static constexpr int kConsumers = 32 * kParts * (COLS / kCols);
     static constexpr int kLoader = kConsumers / 32, kIssuer = kLoader + 1, kScaler = kLoader + 2;   // warps; two scalers
     static constexpr int kThreads = kConsumers + 128;
-    static constexpr int kBox = COLS / 2 < 32 ? COLS / 2 : 32;
-    static constexpr int kStageBytes = kABytes + COLS / 2 * kBlock;
+    static constexpr int kBox = COLS / 2 % 32 == 0 ? 32 : 16;
+    static_assert(COLS / 2 % kBox == 0, "");
+    static constexpr int kStageBytes = kABytes + (LANES ? 128 : COLS / 2) * kBlock;
     static constexpr int kStages = 192 * 1024 / kStageBytes < kMostStages ? 192 * 1024 / kStageBytes : kMostStages;
     static constexpr int kScales = kScaleSlots * kScaleBlocks * kScaleSets * COLS;   // floats
     static constexpr int kMost = (kParts + 1 + 2) * COLS;
@@ -49,11 +55,12 @@ __device__ __forceinline__ float power_of_two(float s) {
     return f == 0u || e == 255 ? s : __uint_as_float((e + 1u) << 23);
 }
 
-// COLS: rows of x of an item at most. SWIGLU: y = silu(gate) * up.
-template <int COLS, bool SWIGLU>
-__global__ void __launch_bounds__(Shape<COLS>::kThreads, 1)
-    expert_fp8_kernel(Fp8Args a, TilePlan plan, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map) {
-    using S = Shape<COLS>;
+// SWIGLU: y = silu(gate) * up.
+template <int COLS, bool LANES, bool SWIGLU>
+__global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
+    expert_fp8_kernel(Fp8Args a, TilePlan plan, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap w_half_map,
+                      const __grid_constant__ CUtensorMap x_map) {
+    using S = Shape<COLS, LANES>;
     constexpr int kConsumers = S::kConsumers, kLoader = S::kLoader, kIssuer = S::kIssuer, kScaler = S::kScaler, kThreads = S::kThreads;
     extern __shared__ unsigned char shared_bytes[];
     unsigned char* const ring = shared_bytes + (1024 - smem_addr(shared_bytes) % 1024) % 1024;
@@ -63,13 +70,13 @@ __global__ void __launch_bounds__(Shape<COLS>::kThreads, 1)
     float* const other_most = found + COLS;                                               // [2][COLS]: the other CTA's largest
     uint64_t* const barriers = reinterpret_cast<uint64_t*>(other_most + 2 * COLS);
     const uint32_t full = smem_addr(barriers), empty = full + 8 * kMostStages;
-    const uint32_t sums_full = empty + 8 * kMostStages, sums_empty = sums_full + 16;
-    const uint32_t scales_full = sums_empty + 16, scales_empty = scales_full + 8 * kScaleSlots;
+    const uint32_t sums_full = empty + 8 * kMostStages, sums_empty = sums_full + 32;
+    const uint32_t scales_full = sums_empty + 32, scales_empty = scales_full + 8 * kScaleSlots;
     const uint32_t most_full = scales_empty + 8 * kScaleSlots;
     uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(barriers) + 120;
     volatile int* const dead = reinterpret_cast<volatile int*>(tmem_at + 1);
     int* const table = reinterpret_cast<int*>(barriers) + 128;
-    static_assert((2 * kMostStages + 5 + 2 * kScaleSlots) * 2 <= 120, "");
+    static_assert((2 * kMostStages + 9 + 2 * kScaleSlots) * 2 <= 120, "");
     __shared__ int warp_sum[kThreads / 32];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = pair_rank();
@@ -81,7 +88,7 @@ __global__ void __launch_bounds__(Shape<COLS>::kThreads, 1)
                 barrier_init(full + 8 * i, 1);
                 barrier_init(empty + 8 * i, 1);
             }
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < S::kBuffers; ++i) {
                 barrier_init(sums_full + 8 * i, 1);
                 barrier_init(sums_empty + 8 * i, 2 * kConsumers / 32);
             }
@@ -111,19 +118,165 @@ __global__ void __launch_bounds__(Shape<COLS>::kThreads, 1)
         if (!SWIGLU) return row0 / kBlock;
         return set == 0 ? row0 / 2 / kBlock : (cols + row0 / 2) / kBlock + set - 1;
     };
+    // What an e4m3 output needs: the scale of a block whose largest value is `big`, its place, two values' codes.
+    const auto larger = [](float x, float y) { return x > y || x != x ? x : y; };   // (NaN stays)
+    const auto output_scale = [&](float big) {
+        if (big == 0.0f) return 0.0f;
+        float s = __fdiv_rn(big, 448.0f);
+        if (a.y_scale_mode != EP_SCALE_FP32 && s > 0.0f) s = power_of_two(s);
+        if (a.y_scale_mode == EP_SCALE_UE8M0 && s < __uint_as_float(0x00400000u)) s = __uint_as_float(0x00400000u);   // 2^-127
+        return s;
+    };
+    const auto write_scale = [&](int64_t row, int block, float s) {
+        const int64_t to = row * a.y_scale_row + block * a.y_scale_block;
+        if (a.y_scale_mode == EP_SCALE_UE8M0) static_cast<uint8_t*>(a.y_scales)[to] = static_cast<uint8_t>(__float_as_uint(s) >> 23);
+        else static_cast<float*>(a.y_scales)[to] = s;
+    };
+    const auto codes = [](float2 v, float s) -> uint32_t {
+        return s == 0.0f ? 0u : __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v.x, s), __fdiv_rn(v.y, s)), __NV_SATFINITE, __NV_E4M3);
+    };
     const int scale_rows = ceil_div(a.O, kBlock), sets = !SWIGLU ? 1 : cols % 64 == 0 ? 2 : 3;
 
     // (registers: 256 x 216 + 128 x 72 of the launch's 384 x 168)
     if (warp < kLoader) {
-        if constexpr (S::kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        if constexpr (LANES) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // 32 weight rows (the product's lanes) of the CTA's 128, columns c0 .. c0 + kCols
         constexpr int kCols = S::kCols;
         const int part = warp % kParts, c0 = warp / kParts * kCols;
         const uint32_t mine = tmem + c0 + (static_cast<uint32_t>(part) << 21);
         int buffer = 0, slot = 0;
         uint32_t parity = 0, scales_parity = 0, most_parity = 0;
+        // A tile whose rows of x are the lanes: a thread has one of them and 64 columns of each half of the 256 weight rows (gate
+        // and up of the same 64 channels). Its scales are two numbers a block.
+        const auto rows_as_lanes = [&](const Tile& it) {
+            const int r = rank * 128 + part * 32 + lane, h = warp / kParts;
+            const bool real = r < it.rows;
+            const int64_t row = it.row + static_cast<int64_t>(real ? r : 0);
+            const int first = SWIGLU ? it.m * 128 + h * 64 : it.m * kTileRows + h * 64;   // channel of column 0 of the first half
+            const int second = SWIGLU ? first : first + 128;
+            uint64_t acc[2][32];
+#pragma unroll
+            for (int n = 0; n < 32; ++n) acc[0][n] = acc[1][n] = 0;
+            const uint32_t from = tmem + h * 64 + (static_cast<uint32_t>(part) << 21);
+            for (int b = 0; b < blocks; ++b) {
+                if (b % kScaleBlocks == 0) barrier_wait_inline(scales_full + 8 * slot, scales_parity, dead);
+                const float* sx = scales + (slot * kScaleBlocks + b % kScaleBlocks) * (kScaleSets * COLS);
+                const float x_scale = sx[part * 32 + lane];
+                const uint64_t s0 = both(x_scale * sx[COLS + h]), s1 = both(x_scale * sx[COLS + 2 + h]);
+                barrier_wait_inline(sums_full + 8 * buffer, parity, dead);
+                tmem_fence_after();
+                const uint32_t at = from + buffer * S::kStride;
+                uint32_t raw[2][16];
+                tmem_load16(at, raw[0]);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {   // a chunk of sums is on its way while the one before is added
+                    tmem_loaded(raw[c & 1]);
+                    if (c < 7) {
+                        tmem_load16(at + (c + 1) / 4 * 128 + (c + 1) % 4 * 16, raw[(c + 1) & 1]);
+                    } else {
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0) barrier_arrive_pair(in_first(sums_empty + 8 * buffer));
+                    }
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {
+                        uint64_t& to = acc[c / 4][c % 4 * 8 + n];
+                        to = fma2(pair(raw[c & 1][2 * n], raw[c & 1][2 * n + 1]), c < 4 ? s0 : s1, to);
+                    }
+                }
+                if (b % kScaleBlocks == kScaleBlocks - 1 || b + 1 == blocks) {
+                    if (lane == 0) barrier_arrive(scales_empty + 8 * slot);
+                    if (++slot == kScaleSlots) slot = 0, scales_parity ^= 1;
+                }
+                if (++buffer == S::kBuffers) buffer = 0, parity ^= 1;
+            }
+            if (*dead) {
+#pragma unroll
+                for (int n = 0; n < 32; ++n) acc[0][n] = acc[1][n] = both(__int_as_float(0x7fffffff));
+            }
+            if constexpr (SWIGLU) {
+#pragma unroll
+                for (int n = 0; n < 32; ++n) {
+                    const float2 g = apart(acc[0][n]), u = apart(acc[1][n]);
+                    acc[0][n] = pair(__float_as_uint(silu(g.x) * u.x), __float_as_uint(silu(g.y) * u.y));
+                }
+            }
+            constexpr int kHalves = SWIGLU ? 1 : 2;
+            if (a.y_dtype != EP_DTYPE_FP8_E4M3) {
+                const bool bf16 = a.y_dtype == EP_DTYPE_BF16, wide = a.y_ld % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
+                if (!real) return;
+#pragma unroll
+                for (int half = 0; half < kHalves; ++half) {
+                    const int chan = half == 0 ? first : second;
+                    uint16_t* to = static_cast<uint16_t*>(a.y) + row * a.y_ld + chan;
+#pragma unroll
+                    for (int n = 0; n < 32; n += 4) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 v = apart(acc[half][n + k]);
+                            const __nv_bfloat162 vb = __floats2bfloat162_rn(v.x, v.y);
+                            const __half2 vh = __floats2half2_rn(v.x, v.y);
+                            w[k] = bf16 ? *reinterpret_cast<const uint32_t*>(&vb) : *reinterpret_cast<const uint32_t*>(&vh);
+                        }
+                        if (wide && chan + 2 * n + 8 <= cols) {
+                            *reinterpret_cast<uint4*>(to + 2 * n) = make_uint4(w[0], w[1], w[2], w[3]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                if (chan + 2 * n + k < cols) to[2 * n + k] = static_cast<uint16_t>(w[k / 2] >> (k % 2 * 16));
+                        }
+                    }
+                }
+                return;
+            }
+            // e4m3: the largest of 128 channels, of which another warp's thread has the other 64
+            float big[kHalves];
+#pragma unroll
+            for (int half = 0; half < kHalves; ++half) {
+                big[half] = 0.0f;
+#pragma unroll
+                for (int n = 0; n < 32; ++n) {
+                    const float2 v = apart(acc[half][n]);
+                    big[half] = larger(fabsf(v.x), larger(fabsf(v.y), big[half]));
+                }
+                most[(half * 2 + h) * 128 + part * 32 + lane] = big[half];
+            }
+            consumers_sync<kConsumers>();
+            const bool wide = a.y_ld % 16 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
+#pragma unroll
+            for (int half = 0; half < kHalves; ++half) {
+                const int chan = half == 0 ? first : second;
+                const float s = output_scale(larger(most[(half * 2 + (h ^ 1)) * 128 + part * 32 + lane], big[half]));
+                if (!real || chan >= cols) continue;   // (columns are a multiple of 128)
+                if (h == 0) write_scale(row, chan / kBlock, s);
+                uint8_t* to = static_cast<uint8_t*>(a.y) + row * a.y_ld + chan;
+#pragma unroll
+                for (int n = 0; n < 32; n += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 v = apart(acc[half][n + 2 * k]), u = apart(acc[half][n + 2 * k + 1]);
+                        w[k] = codes(v, s) | codes(u, s) << 16;
+                    }
+                    if (wide) {
+                        *reinterpret_cast<uint4*>(to + 2 * n) = make_uint4(w[0], w[1], w[2], w[3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) to[2 * n + k] = static_cast<uint8_t>(w[k / 4] >> (k % 4 * 8));
+                    }
+                }
+            }
+            consumers_sync<kConsumers>();   // (`most` is written again)
+        };
         for (int64_t i = pair_id; i < items; i += pairs) {
             const Tile it = tile_at(a.g, plan, table, i);
+            if constexpr (LANES) {
+                if (it.rows > kMostColumns) {
+                    rows_as_lanes(it);
+                    continue;
+                }
+            }
             const int many = it.rows - c0;   // of this warp's columns, those with a row
             // this thread's output channel and weight row; with the activation a warp's lanes are 16 gate and 16 up rows
             const int row0 = it.m * kTileRows + rank * (kTileRows / 2) + part * 32;
@@ -138,36 +291,30 @@ __global__ void __launch_bounds__(Shape<COLS>::kThreads, 1)
                 const float* sx = scales + ((slot * kScaleBlocks + b % kScaleBlocks) * kScaleSets + set) * COLS + c0;
                 barrier_wait_inline(sums_full + 8 * buffer, parity, dead);
                 tmem_fence_after();
-                // a chunk of sums is on its way while the one before is added
-                constexpr int kChunk = 32;
-                uint32_t raw[2][kChunk];
-                tmem_load32(mine + buffer * 256, raw[0]);
+                uint32_t raw[kCols];
 #pragma unroll
-                for (int c = 0; c < kCols; c += kChunk) {
-                    tmem_load_wait();
-                    if (c + kChunk < kCols) {
-                        if (c + kChunk < many) tmem_load32(mine + buffer * 256 + c + kChunk, raw[(c / kChunk + 1) & 1]);
-                    } else {   // (all are in registers)
-                        tmem_fence_before();
-                        __syncwarp();
-                        if (lane == 0) barrier_arrive_pair(in_first(sums_empty + 8 * buffer));
-                    }
+                for (int c = 0; c < kCols; c += 32) {
                     if (c >= many) continue;
-                    const uint32_t(&r)[kChunk] = raw[(c / kChunk) & 1];
+                    if (c + 32 <= kCols) tmem_load32(mine + buffer * S::kStride + c, raw + c);
+                    else tmem_load16(mine + buffer * S::kStride + c, raw + c);
+                }
+                tmem_loaded(raw);
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) barrier_arrive_pair(in_first(sums_empty + 8 * buffer));
 #pragma unroll
-                    for (int j = 0; j < kChunk; j += 4) {
-                        const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(sx + c + j);
-                        acc[(c + j) / 2] = fma2(pair(r[j], r[j + 1]), s.x, acc[(c + j) / 2]);
-                        acc[(c + j) / 2 + 1] = fma2(pair(r[j + 2], r[j + 3]), s.y, acc[(c + j) / 2 + 1]);
-                    }
+                for (int c = 0; c < kCols; c += 4) {
+                    if (c / 16 * 16 >= many) continue;
+                    const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(sx + c);
+                    acc[c / 2] = fma2(pair(raw[c], raw[c + 1]), s.x, acc[c / 2]);
+                    acc[c / 2 + 1] = fma2(pair(raw[c + 2], raw[c + 3]), s.y, acc[c / 2 + 1]);
                 }
                 __syncwarp();
                 if (b % kScaleBlocks == kScaleBlocks - 1 || b + 1 == blocks) {
                     if (lane == 0) barrier_arrive(scales_empty + 8 * slot);
                     if (++slot == kScaleSlots) slot = 0, scales_parity ^= 1;
                 }
-                buffer ^= 1;
-                if (buffer == 0) parity ^= 1;
+                if (++buffer == S::kBuffers) buffer = 0, parity ^= 1;
             }
 
             if (*dead) {
@@ -214,7 +361,6 @@ __global__ void __launch_bounds__(Shape<COLS>::kThreads, 1)
                 if ((lane & (SWIGLU ? 15 : 31)) == 0) most[part * COLS + c0 + n * kStep + odd] = big;
             }
             consumers_sync<kConsumers>();
-            const auto larger = [](float x, float y) { return x > y || x != x ? x : y; };   // (NaN stays)
             float big[COLS / kConsumers + 1];
 #pragma unroll
             for (int k = 0, n = tid; n < COLS; ++k, n += kConsumers) {
@@ -231,19 +377,10 @@ __global__ void __launch_bounds__(Shape<COLS>::kThreads, 1)
             for (int k = 0, n = tid; n < COLS; ++k, n += kConsumers) {
                 if (n >= it.rows) continue;
                 if (SWIGLU) big[k] = larger(other_most[most_parity * COLS + n], big[k]);
-                float s = 0.0f;
-                if (big[k] != 0.0f) {
-                    s = __fdiv_rn(big[k], 448.0f);
-                    if (a.y_scale_mode != EP_SCALE_FP32 && s > 0.0f) s = power_of_two(s);
-                    if (a.y_scale_mode == EP_SCALE_UE8M0) s = s < __uint_as_float(0x00400000u) ? __uint_as_float(0x00400000u) : s;
-                }
+                const float s = output_scale(big[k]);
                 found[n] = s;
                 const int block = SWIGLU ? it.m : it.m * 2 + rank;   // of 128 channels
-                if (block * kBlock < cols && (!SWIGLU || rank == 0)) {
-                    const int64_t to = (static_cast<int64_t>(it.row) + n) * a.y_scale_row + block * a.y_scale_block;
-                    if (a.y_scale_mode == EP_SCALE_UE8M0) static_cast<uint8_t*>(a.y_scales)[to] = static_cast<uint8_t>(__float_as_uint(s) >> 23);
-                    else static_cast<float*>(a.y_scales)[to] = s;
-                }
+                if (block * kBlock < cols && (!SWIGLU || rank == 0)) write_scale(static_cast<int64_t>(it.row) + n, block, s);
             }
             most_parity ^= 1;
             consumers_sync<kConsumers>();
@@ -254,11 +391,11 @@ __global__ void __launch_bounds__(Shape<COLS>::kThreads, 1)
 #pragma unroll
                 for (int n = 0; n < kResults; ++n, to += step)
                     if (n * kStep < left)
-                        *to = my[n * kStep] == 0.0f ? 0 : __nv_cvt_float_to_fp8(__fdiv_rn(v[n], my[n * kStep]), __NV_SATFINITE, __NV_E4M3);
+                        *to = static_cast<uint8_t>(codes(make_float2(v[n], 0.0f), my[n * kStep]));
             }
         }
     } else {
-        if constexpr (S::kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if constexpr (LANES) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kLoader) {
             int slot = 0;
             uint32_t parity = 1;
@@ -266,13 +403,25 @@ __global__ void __launch_bounds__(Shape<COLS>::kThreads, 1)
                 const Tile it = tile_at(a.g, plan, table, i);
                 const int half = columns_of(it.rows) / 2, a_boxes = SWIGLU ? 4 : 1, x_boxes = (half + S::kBox - 1) / S::kBox;
                 const int row0 = it.m * kTileRows + rank * (kTileRows / 2);
+                const bool lanes = LANES && it.rows > kMostColumns;
+                // with rows as lanes: boxes of this CTA's 128 rows (none of those behind the tile's), and of both
+                const int own = lanes ? (min(max(it.rows - rank * 128, 0), 128) + S::kBox - 1) / S::kBox : 0;
+                const int both_bytes = lanes ? 2 * kABytes + (it.rows + S::kBox - 1) / S::kBox * S::kBox * kBlock
+                                             : 2 * (kABytes + x_boxes * S::kBox * kBlock);
                 for (int b = 0; b < blocks; ++b) {
                     // both CTAs' boxes count on the first one's barrier
                     const uint32_t bar = in_first(full + 8 * slot), at_a = smem_addr(ring) + slot * S::kStageBytes, at_x = at_a + kABytes;
                     barrier_wait_inline(empty + 8 * slot, parity, dead);
-                    if (lane == 0 && rank == 0) barrier_expect(full + 8 * slot, 2 * (kABytes + x_boxes * S::kBox * kBlock));
+                    if (lane == 0 && rank == 0) barrier_expect(full + 8 * slot, both_bytes);
                     __syncwarp();
-                    if (lane < a_boxes) {
+                    if (lanes) {
+                        if (lane < own) {
+                            load_box_pair(at_a + lane * S::kBox * kBlock, &x_map, b * kBlock, it.row + rank * 128 + lane * S::kBox, 0, 0, bar);
+                        } else if (lane == 31) {   // the first CTA has the gate rows or the first half, the second the others
+                            if (SWIGLU) load_box_pair(at_x, &w_half_map, b * kBlock, it.m * (kTileRows / 2), rank, it.expert, bar);
+                            else load_box_pair(at_x, &w_map, b * kBlock, row0, 0, it.expert, bar);
+                        }
+                    } else if (lane < a_boxes) {
                         if (SWIGLU) load_box_pair(at_a + lane * 4096, &w_map, b * kBlock, row0 / 2 + lane * 16, 0, it.expert, bar);
                         else load_box_pair(at_a, &w_map, b * kBlock, row0, 0, it.expert, bar);
                     } else if (lane - a_boxes < x_boxes) {
@@ -284,12 +433,13 @@ __global__ void __launch_bounds__(Shape<COLS>::kThreads, 1)
             }
         } else if (warp == kIssuer && rank == 1) {   // (the first CTA's issues for both)
         } else if (warp == kIssuer) {
-            const uint32_t base = (1u << 4) | (a.x_dtype == EP_DTYPE_FP8_E5M2 ? 1u << 10 : 0u) | (static_cast<uint32_t>(kTileRows / 16) << 24);
+            const uint32_t base = (1u << 4) | (static_cast<uint32_t>(kTileRows / 16) << 24), e5m2 = a.x_dtype == EP_DTYPE_FP8_E5M2 ? 1u : 0u;
             int slot = 0, buffer = 0;
             uint32_t parity = 0, sums_parity = 1;
             for (int64_t i = pair_id; i < items; i += pairs) {
                 const Tile it = tile_at(a.g, plan, table, i);
-                const uint32_t shape = base | static_cast<uint32_t>(columns_of(it.rows) / 8) << 17;
+                const bool lanes = LANES && it.rows > kMostColumns;
+                const uint32_t shape = base | (lanes ? e5m2 << 7 : e5m2 << 10) | static_cast<uint32_t>((lanes ? 256 : columns_of(it.rows)) / 8) << 17;
                 for (int b = 0; b < blocks; ++b) {
                     barrier_wait_inline(full + 8 * slot, parity, dead);
                     barrier_wait_inline(sums_empty + 8 * buffer, sums_parity, dead);
@@ -298,57 +448,60 @@ __global__ void __launch_bounds__(Shape<COLS>::kThreads, 1)
                         const uint32_t at_a = smem_addr(ring) + slot * S::kStageBytes;
                         const uint64_t dw = operand(at_a, 1024), dx = operand(at_a + kABytes, 1024);
     #pragma unroll
-                        for (int k = 0; k < kBlock / 32; ++k) multiply_pair<true>(tmem + buffer * 256, dw + k * 2, dx + k * 2, shape, k > 0);
+                        for (int k = 0; k < kBlock / 32; ++k) multiply_pair<true>(tmem + buffer * S::kStride, dw + k * 2, dx + k * 2, shape, k > 0);
                         pair_done(empty + 8 * slot);
                         pair_done(sums_full + 8 * buffer);
                     }
                     __syncwarp();
                     if (++slot == S::kStages) slot = 0, parity ^= 1;
-                    buffer ^= 1;
-                    if (buffer == 0) sums_parity ^= 1;
+                    if (++buffer == S::kBuffers) buffer = 0, sums_parity ^= 1;
                 }
             }
         } else if (warp >= kScaler) {
-            // Products of the rows' and the weights' scales, for two blocks at a time, the two warps in turn; lanes run along what
-            // is dense in memory.
+            // Scales for two blocks at a time, the two warps in turn: products of the rows' and the weights' for rows as columns;
+            // for rows as lanes the CTA's rows', and behind them the weights' of the first and second half's 64-row quarters.
+            // Lanes run along what is dense in memory.
             int turn = warp - kScaler, slot = 0;
             uint32_t parity = 1;
             const bool by_rows = a.x_scale_block == 1;
             constexpr int kEach = kScaleBlocks * COLS / 32;
+            static_assert(kScaleBlocks == 2, "");
+            const int wk = lane / 4 % 2, wj = lane % 4;   // lanes 0 .. 7 load the weights' scales: block, which one
             for (int64_t i = pair_id; i < items; i += pairs) {
                 const Tile it = tile_at(a.g, plan, table, i);
-                const float* w_scales[kScaleSets];
-    #pragma unroll
-                for (int s = 0; s < kScaleSets; ++s)
-                    w_scales[s] = a.w_scales + (static_cast<int64_t>(it.expert) * scale_rows + min(scale_row(it.m, s), scale_rows - 1)) * blocks;
+                const bool lanes = LANES && it.rows > kMostColumns;
+                const int skip = lanes ? rank * 128 : 0, rows = it.rows - skip;
+                int o;
+                if (!lanes) o = scale_row(it.m, min(wj, kScaleSets - 1));
+                else if (SWIGLU) o = ((wj < 2 ? 0 : cols) + it.m * 128 + wj % 2 * 64) / kBlock;
+                else o = it.m * 2 + wj / 2;
+                const float* w_scales = a.w_scales + (static_cast<int64_t>(it.expert) * scale_rows + min(o, scale_rows - 1)) * blocks;
                 for (int b = 0; b < blocks; b += kScaleBlocks) {
                     if (turn == 0) {
                         float v[kEach];
-    #pragma unroll
+#pragma unroll
                         for (int j = 0; j < kEach; ++j) {
                             const int n = by_rows ? j * (32 / kScaleBlocks) + lane / kScaleBlocks : j * 32 % COLS + lane;
                             const int k = by_rows ? lane % kScaleBlocks : j * 32 / COLS;
                             v[j] = 0.0f;
-                            if (n < it.rows && b + k < blocks) {
-                                const int64_t from = (static_cast<int64_t>(it.row) + n) * a.x_scale_row + (b + k) * a.x_scale_block;
+                            if (n < rows && b + k < blocks) {
+                                const int64_t from = (static_cast<int64_t>(it.row) + skip + n) * a.x_scale_row + (b + k) * a.x_scale_block;
                                 v[j] = a.x_ue8m0 ? ue8m0(static_cast<const uint8_t*>(a.x_scales)[from]) : static_cast<const float*>(a.x_scales)[from];
                             }
                         }
-                        float w[kScaleBlocks][kScaleSets];
-    #pragma unroll
-                        for (int k = 0; k < kScaleBlocks; ++k)
-    #pragma unroll
-                            for (int s = 0; s < kScaleSets; ++s) w[k][s] = s < sets ? w_scales[s][min(b + k, blocks - 1)] : 0.0f;
+                        const float w = w_scales[min(b + wk, blocks - 1)];
                         barrier_wait_inline(scales_empty + 8 * slot, parity, dead);
-    #pragma unroll
+                        float* to = scales + slot * (kScaleBlocks * kScaleSets * COLS);
+                        if (lanes && lane < 8) to[wk * (kScaleSets * COLS) + COLS + wj] = w;
+#pragma unroll
                         for (int s = 0; s < kScaleSets; ++s) {
-                            if (s >= sets) continue;
-                            float* to = scales + (slot * kScaleBlocks * kScaleSets + s) * COLS;
-    #pragma unroll
+                            if (s >= (lanes ? 1 : sets)) continue;
+#pragma unroll
                             for (int j = 0; j < kEach; ++j) {
                                 const int n = by_rows ? j * (32 / kScaleBlocks) + lane / kScaleBlocks : j * 32 % COLS + lane;
                                 const int k = by_rows ? lane % kScaleBlocks : j * 32 / COLS;
-                                to[k * kScaleSets * COLS + n] = v[j] * (k == 0 ? w[0][s] : w[1][s]);
+                                const float factor = __shfl_sync(kFullMask, w, k * 4 + s);
+                                to[(k * kScaleSets + s) * COLS + n] = lanes ? v[j] : v[j] * factor;
                             }
                         }
                         __syncwarp();
@@ -369,39 +522,42 @@ __global__ void __launch_bounds__(Shape<COLS>::kThreads, 1)
     }
 }
 
-template <int COLS, bool SWIGLU>
-cudaError_t launch_columns(const Fp8Args& a, cudaStream_t stream) {
-    using S = Shape<COLS>;
+template <int COLS, bool LANES, bool SWIGLU>
+cudaError_t launch_shape(const Fp8Args& a, cudaStream_t stream) {
+    using S = Shape<COLS, LANES>;
     static int known[64];
     int pairs = 0;
-    cudaError_t err = pairs_at_once(expert_fp8_kernel<COLS, SWIGLU>, S::kThreads, S::kShared, known, &pairs);
+    cudaError_t err = pairs_at_once(expert_fp8_kernel<COLS, LANES, SWIGLU>, S::kThreads, S::kShared, known, &pairs);
     if (err != cudaSuccess) return err;
     const int64_t I = a.I, O = a.O, E = a.g.E;
     const int cols = SWIGLU ? a.O / 2 : a.O;
     TilePlan p{};
-    p.cap = COLS;
+    p.cap = LANES ? 256 : COLS;
+    p.whole = LANES;
     p.chunk = 16;
     p.m_tiles = ceil_div(cols, SWIGLU ? kTileRows / 2 : kTileRows);
     while (((a.g.E - 1) >> p.shift) + 1 > kTileTable) ++p.shift;
-    CUtensorMap w_map, x_map;
+    CUtensorMap w_map, w_half_map, x_map;
     err = SWIGLU ? box_map(&w_map, a.w, EP_DTYPE_FP8_E4M3, I, cols, 2, E, I, I * cols, I * O, 16, 2)
-                   : box_map(&w_map, a.w, EP_DTYPE_FP8_E4M3, I, O, 1, E, I, I * O, I * O, 128, 1);
-    if (err == cudaSuccess)
-        err = box_map(&x_map, a.x, EP_DTYPE_FP8_E4M3, I, a.g.rows, 1, 1, a.x_ld, a.x_ld, a.x_ld, S::kBox, 1);
+                 : box_map(&w_map, a.w, EP_DTYPE_FP8_E4M3, I, O, 1, E, I, I * O, I * O, 128, 1);
+    w_half_map = w_map;
+    if (SWIGLU && LANES && err == cudaSuccess) err = box_map(&w_half_map, a.w, EP_DTYPE_FP8_E4M3, I, cols, 2, E, I, I * cols, I * O, 128, 1);
+    if (err == cudaSuccess) err = box_map(&x_map, a.x, EP_DTYPE_FP8_E4M3, I, a.g.rows, 1, 1, a.x_ld, a.x_ld, a.x_ld, S::kBox, 1);
     if (err != cudaSuccess) return err;
     const int64_t used = a.g.rows < a.g.E ? a.g.rows : a.g.E;
-    const int64_t most = (a.g.rows + used * (COLS - 1)) / COLS * p.m_tiles;
-    return launch_pairs(expert_fp8_kernel<COLS, SWIGLU>, static_cast<int>(most < pairs ? most : pairs), S::kThreads, S::kShared, stream, a, p, w_map,
-                        x_map);
+    const int64_t most = (a.g.rows + used * (p.cap - 1)) / p.cap * p.m_tiles;
+    return launch_pairs(expert_fp8_kernel<COLS, LANES, SWIGLU>, static_cast<int>(most < pairs ? most : pairs), S::kThreads, S::kShared,
+                        stream, a, p, w_map, w_half_map, x_map);
 }
 
 template <bool SWIGLU>
 cudaError_t launch_activation(const Fp8Args& a, cudaStream_t stream) {
     const int used = a.g.rows < a.g.E ? a.g.rows : a.g.E, mean = (a.g.rows - 1) / used + 1;
-    return mean <= 24    ? launch_columns<32, SWIGLU>(a, stream)
-           : mean <= 48  ? launch_columns<64, SWIGLU>(a, stream)
-           : mean <= 112 ? launch_columns<128, SWIGLU>(a, stream)
-                         : launch_columns<256, SWIGLU>(a, stream);
+    if (mean <= 24) return launch_shape<32, false, SWIGLU>(a, stream);
+    if (mean <= 48) return launch_shape<64, false, SWIGLU>(a, stream);
+    // (64 neighbouring up rows have one scale)
+    if (SWIGLU && a.O / 2 % 64 != 0) return launch_shape<128, false, SWIGLU>(a, stream);
+    return launch_shape<128, true, SWIGLU>(a, stream);
 }
 
 }  // namespace

@@ -26,6 +26,7 @@ __device__ __forceinline__ int rows_of(const ExpertRows& g, int e, int& first) {
 // at work together share the weights of few tiles and the inputs of few.
 struct TilePlan {
     int m_tiles, cap, chunk;
+    int whole;   // tiles of `cap` rows and a rest, instead of equal ones
     int shift;   // an entry of the table stands for 2^shift experts
 };
 struct Tile {
@@ -36,8 +37,8 @@ struct Tile {
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a - 1) / b + 1; }   // a >= 1
 
 // Width of the tiles of n rows, a multiple of 16. Equal widths where none is left without rows by the rounding.
-__device__ __forceinline__ int tile_width(int n, int tiles, int cap) {
-    return 16 * tiles < cap ? (ceil_div(n, tiles) + 15) / 16 * 16 : cap;
+__device__ __forceinline__ int tile_width(int n, int tiles, int cap, int whole) {
+    return 16 * tiles < cap && !whole ? (ceil_div(n, tiles) + 15) / 16 * 16 : cap;
 }
 
 // Fills table[entry] with the tiles of rows before it, for all threads of the CTA (THREADS of them).
@@ -97,7 +98,7 @@ __device__ __forceinline__ Tile tile_at(const ExpertRows& g, const TilePlan& p, 
     const int c = static_cast<int>(in / per_chunk), r = static_cast<int>(in - c * per_chunk);
     const int wide = max(min(p.chunk, tiles - c * p.chunk), 1);
     t.m = r / wide;
-    const int width = tile_width(max(n, 1), max(tiles, 1), p.cap);
+    const int width = tile_width(max(n, 1), max(tiles, 1), p.cap, p.whole);
     const int64_t at = static_cast<int64_t>(c * p.chunk + r % wide) * width;
     t.row = first + static_cast<int>(min(at, static_cast<int64_t>(n)));
     t.rows = static_cast<int>(max(min(static_cast<int64_t>(width), n - at), static_cast<int64_t>(0)));
@@ -125,10 +126,10 @@ __device__ __forceinline__ uint32_t in_first(uint32_t addr) { return in_cta(addr
 __device__ __forceinline__ void store_other(uint32_t addr, uint32_t rank, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(in_cta(addr, rank)), "f"(v) : "memory");
 }
-// On a barrier of either CTA. (Orders tensor memory, with the tcgen05 fences, and nothing else: ordering all memory for
-// the cluster took 2000 clocks a stage.)
+// On a barrier of either CTA. (It orders no memory but, behind the tcgen05 fence, the tensor memory that has been read:
+// as a release for the CTA it held the thread for 1000 clocks, for the cluster for 2000.)
 __device__ __forceinline__ void barrier_arrive_pair(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // The same, ordering what this thread has written, for barrier_wait_cluster.
 __device__ __forceinline__ void barrier_arrive_cluster(uint32_t bar) {
@@ -165,15 +166,21 @@ __device__ __forceinline__ void tmem_alloc_all(uint32_t to) {
 __device__ __forceinline__ void tmem_free_all(uint32_t tmem) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
-__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&r)[16]) {
+// The loads into these registers are complete. (It orders nothing else, so loads from shared memory pass it.)
+template <int N>
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::);
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t* r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
           "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(at)
-        : "memory");
+        : "r"(at));
 }
-__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t* r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
         "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -181,8 +188,7 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&r)[32]) {
           "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
           "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
           "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(at)
-        : "memory");
+        : "r"(at));
 }
 // sums [2 x 128 lanes][N] (+)= A [2 x 128 lanes] * B [2 x N / 2 columns]^T, all in the pair's shared memory.
 template <bool FP8>

@@ -121,7 +121,7 @@ def run_fp8(ep, counts, I, O, swiglu=False, x_dtype=E4M3, ue8m0=False, columns=F
 
 
 @pytest.mark.parametrize("counts", COUNTS)
-@pytest.mark.parametrize("I,O", [(128, 2), (128, 256), (640, 130), (1024, 520), (256, 70)])
+@pytest.mark.parametrize("I,O", [(128, 2), (128, 256), (640, 130), (1024, 520), (256, 70), (384, 384)])
 @pytest.mark.parametrize("swiglu", [False, True])
 def test_fp8(ep, counts, I, O, swiglu):
     run_fp8(ep, counts, I, O, swiglu)

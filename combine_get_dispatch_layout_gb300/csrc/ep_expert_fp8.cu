@@ -14,39 +14,39 @@ constexpr int kBlock = 128;                     // inputs of a stage: 128 bytes,
 constexpr int kTileRows = 256;                  // weight rows of an item: 128 in each CTA of the pair
 constexpr int kParts = 4;                       // warps over a CTA's weight rows: 32 lanes each
 constexpr int kABytes = kTileRows / 2 * kBlock;
-constexpr int kScaleBlocks = 2, kScaleSlots = 3;   // the ring of scales: blocks of a slot
+constexpr int kGroups = 2;                      // groups of kParts warps: they take blocks, columns or channels in turn
+constexpr int kConsumers = 32 * kParts * kGroups;
+constexpr int kLoader = kConsumers / 32, kIssuer = kLoader + 1, kScaler = kLoader + 2;   // warps; two scalers
+constexpr int kThreads = kConsumers + 128;
+constexpr int kBuffers = 4;                     // of sums in TMEM, 64 or 128 columns apart
+constexpr int kScaleSlots = 4;                  // of the ring of scales
 constexpr int kScaleSets = 3;                   // weight scales that a CTA's 128 weight rows have at most in a block
+constexpr int kOut = 32;                        // columns that a group has in the end
 constexpr int kMostStages = 10;
-
-constexpr int kMostColumns = 96;                // rows of x that are columns, where rows may be lanes too
 
 // COLS: rows of x that are columns of a product, at most. LANES: tiles of more rows have them as lanes.
 template <int COLS, bool LANES>
 struct Shape {
-    static_assert(!LANES || COLS == 128, "");
-    static constexpr int kCols = COLS >= 128 ? COLS / 2 : COLS;   // columns of a consuming warp
-    static constexpr int kStride = LANES ? 256 : COLS;            // columns of a buffer of sums in TMEM
-    static constexpr int kBuffers = 512 / kStride < 4 ? 512 / kStride : 4;
-    static constexpr int kConsumers = 32 * kParts * (COLS / kCols);
-    static constexpr int kLoader = kConsumers / 32, kIssuer = kLoader + 1, kScaler = kLoader + 2;   // warps; two scalers
-    static constexpr int kThreads = kConsumers + 128;
-    static constexpr int kBox = COLS / 2 % 32 == 0 ? 32 : 16;
-    static_assert(COLS / 2 % kBox == 0, "");
+    static_assert(COLS == 32 || COLS == 64, "");
+    static constexpr int kStride = LANES ? 128 : 64;             // columns of a buffer; rows as lanes take two buffers
+    static constexpr int kRows = LANES ? 128 : COLS;             // rows of x whose scales a CTA needs
+    static constexpr int kScaleBlocks = LANES ? 2 : 4;           // blocks of a slot of the ring of scales
+    static constexpr int kScaleStep = kScaleSets * COLS;         // floats of a block in the ring of scales
+    static_assert(!LANES || kScaleStep >= 128 + 4, "");
+    static constexpr int kBox = COLS / 2;
     static constexpr int kStageBytes = kABytes + (LANES ? 128 : COLS / 2) * kBlock;
     static constexpr int kStages = 192 * 1024 / kStageBytes < kMostStages ? 192 * 1024 / kStageBytes : kMostStages;
-    static constexpr int kScales = kScaleSlots * kScaleBlocks * kScaleSets * COLS;   // floats
-    static constexpr int kMost = (kParts + 1 + 2) * COLS;
-    static constexpr int kShared = 1024 + kStages * kStageBytes + (kScales + kMost) * 4 + 512 + (kTileTable + 1) * 4;
+    static constexpr int kScales = kScaleSlots * kScaleBlocks * kScaleStep;   // floats
+    static constexpr int kJoin = kOut * 128;
+    static constexpr int kMost = kParts * 128 + 3 * COLS;
+    static constexpr int kShared = 1024 + kStages * kStageBytes + (kScales + kJoin + kMost) * 4 + 512 + (kTileTable + 1) * 4;
     static_assert(kShared <= 227 * 1024 - 256, "");
 };
 
 __device__ __forceinline__ float ue8m0(uint32_t byte) {
     return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fffffffu : byte << 23);
 }
-template <int THREADS>
-__device__ __forceinline__ void consumers_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
-}
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
 
 // Smallest power of two >= s (s > 0), as the dispatch's scales.
 __device__ __forceinline__ float power_of_two(float s) {
@@ -57,16 +57,17 @@ __device__ __forceinline__ float power_of_two(float s) {
 
 // SWIGLU: y = silu(gate) * up.
 template <int COLS, bool LANES, bool SWIGLU>
-__global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     expert_fp8_kernel(Fp8Args a, TilePlan plan, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap w_half_map,
                       const __grid_constant__ CUtensorMap x_map) {
     using S = Shape<COLS, LANES>;
-    constexpr int kConsumers = S::kConsumers, kLoader = S::kLoader, kIssuer = S::kIssuer, kScaler = S::kScaler, kThreads = S::kThreads;
+    constexpr int kScaleBlocks = S::kScaleBlocks;
     extern __shared__ unsigned char shared_bytes[];
     unsigned char* const ring = shared_bytes + (1024 - smem_addr(shared_bytes) % 1024) % 1024;
-    float* const scales = reinterpret_cast<float*>(ring + S::kStages * S::kStageBytes);   // [kScaleSlots][kScaleBlocks][kScaleSets][COLS]
-    float* const most = scales + S::kScales;                                              // [kParts][COLS]: largest by part
-    float* const found = most + kParts * COLS;                                            // [COLS]: the output's scales
+    float* const scales = reinterpret_cast<float*>(ring + S::kStages * S::kStageBytes);   // [kScaleSlots][kScaleBlocks][kScaleStep]
+    float* const join = scales + S::kScales;                                              // [kOut][128]
+    float* const most = join + S::kJoin;                                                  // [kParts][128]: largest by part
+    float* const found = most + kParts * 128;                                             // [COLS]: the output's scales
     float* const other_most = found + COLS;                                               // [2][COLS]: the other CTA's largest
     uint64_t* const barriers = reinterpret_cast<uint64_t*>(other_most + 2 * COLS);
     const uint32_t full = smem_addr(barriers), empty = full + 8 * kMostStages;
@@ -88,9 +89,9 @@ __global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
                 barrier_init(full + 8 * i, 1);
                 barrier_init(empty + 8 * i, 1);
             }
-            for (int i = 0; i < S::kBuffers; ++i) {
+            for (int i = 0; i < kBuffers; ++i) {
                 barrier_init(sums_full + 8 * i, 1);
-                barrier_init(sums_empty + 8 * i, 2 * kConsumers / 32);
+                barrier_init(sums_empty + 8 * i, 2 * kParts);   // a group of each CTA
             }
             barrier_init(most_full, kConsumers / 32);
             for (int i = 0; i < kScaleSlots; ++i) {
@@ -140,16 +141,15 @@ __global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
     // (registers: 256 x 216 + 128 x 72 of the launch's 384 x 168)
     if (warp < kLoader) {
         if constexpr (LANES) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        // 32 weight rows (the product's lanes) of the CTA's 128, columns c0 .. c0 + kCols
-        constexpr int kCols = S::kCols;
-        const int part = warp % kParts, c0 = warp / kParts * kCols;
-        const uint32_t mine = tmem + c0 + (static_cast<uint32_t>(part) << 21);
+        // 32 of the CTA's 128 lanes
+        const int part = warp % kParts, group = warp / kParts;
+        const uint32_t mine = tmem + (static_cast<uint32_t>(part) << 21);
         int buffer = 0, slot = 0;
-        uint32_t parity = 0, scales_parity = 0, most_parity = 0;
+        uint32_t parities = 0, scales_parity = 0, most_parity = 0;   // parities: a bit for each buffer
         // A tile whose rows of x are the lanes: a thread has one of them and 64 columns of each half of the 256 weight rows (gate
         // and up of the same 64 channels). Its scales are two numbers a block.
         const auto rows_as_lanes = [&](const Tile& it) {
-            const int r = rank * 128 + part * 32 + lane, h = warp / kParts;
+            const int r = rank * 128 + part * 32 + lane, h = group;
             const bool real = r < it.rows;
             const int64_t row = it.row + static_cast<int64_t>(real ? r : 0);
             const int first = SWIGLU ? it.m * 128 + h * 64 : it.m * kTileRows + h * 64;   // channel of column 0 of the first half
@@ -157,13 +157,14 @@ __global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
             uint64_t acc[2][32];
 #pragma unroll
             for (int n = 0; n < 32; ++n) acc[0][n] = acc[1][n] = 0;
-            const uint32_t from = tmem + h * 64 + (static_cast<uint32_t>(part) << 21);
+            const uint32_t from = mine + h * 64;
             for (int b = 0; b < blocks; ++b) {
                 if (b % kScaleBlocks == 0) barrier_wait_inline(scales_full + 8 * slot, scales_parity, dead);
-                const float* sx = scales + (slot * kScaleBlocks + b % kScaleBlocks) * (kScaleSets * COLS);
+                const float* sx = scales + (slot * kScaleBlocks + b % kScaleBlocks) * S::kScaleStep;
                 const float x_scale = sx[part * 32 + lane];
-                const uint64_t s0 = both(x_scale * sx[COLS + h]), s1 = both(x_scale * sx[COLS + 2 + h]);
-                barrier_wait_inline(sums_full + 8 * buffer, parity, dead);
+                const uint64_t s0 = both(x_scale * sx[128 + h]), s1 = both(x_scale * sx[128 + 2 + h]);
+                buffer = (buffer + 1) & 2;   // an even one
+                barrier_wait_inline(sums_full + 8 * buffer, (parities >> buffer) & 1, dead);
                 tmem_fence_after();
                 const uint32_t at = from + buffer * S::kStride;
                 uint32_t raw[2][16];
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
                     } else {
                         tmem_fence_before();
                         __syncwarp();
-                        if (lane == 0) barrier_arrive_pair(in_first(sums_empty + 8 * buffer));
+                        if (lane == 0) barrier_arrive_pair(in_first(sums_empty + 8 * (buffer + h)));   // (the issuer waits for both)
                     }
 #pragma unroll
                     for (int n = 0; n < 8; ++n) {
@@ -188,7 +189,8 @@ __global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
                     if (lane == 0) barrier_arrive(scales_empty + 8 * slot);
                     if (++slot == kScaleSlots) slot = 0, scales_parity ^= 1;
                 }
-                if (++buffer == S::kBuffers) buffer = 0, parity ^= 1;
+                parities ^= 1u << buffer;
+                buffer = (buffer + 2) & 3;
             }
             if (*dead) {
 #pragma unroll
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
                 }
                 most[(half * 2 + h) * 128 + part * 32 + lane] = big[half];
             }
-            consumers_sync<kConsumers>();
+            consumers_sync();
             const bool wide = a.y_ld % 16 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
 #pragma unroll
             for (int half = 0; half < kHalves; ++half) {
@@ -267,72 +269,101 @@ __global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
                     }
                 }
             }
-            consumers_sync<kConsumers>();   // (`most` is written again)
+            consumers_sync();   // (`most` is written again)
         };
         for (int64_t i = pair_id; i < items; i += pairs) {
             const Tile it = tile_at(a.g, plan, table, i);
             if constexpr (LANES) {
-                if (it.rows > kMostColumns) {
+                if (it.rows > COLS) {
                     rows_as_lanes(it);
                     continue;
                 }
             }
-            const int many = it.rows - c0;   // of this warp's columns, those with a row
             // this thread's output channel and weight row; with the activation a warp's lanes are 16 gate and 16 up rows
             const int row0 = it.m * kTileRows + rank * (kTileRows / 2) + part * 32;
             const int chan = SWIGLU ? row0 / 2 + (lane & 15) : row0 + lane;
             const bool real = chan < cols;
             const int set = SWIGLU && lane >= 16 && real ? (cols + chan) / kBlock - scale_row(it.m, 1) + 1 : 0;
-            uint64_t acc[kCols / 2];   // columns 2 n, 2 n + 1
+            const int there = max(it.rows, 1);   // (a tile without rows has a product all the same)
+            uint64_t acc[COLS / 2];   // columns 2 n, 2 n + 1; the groups take every other block each
 #pragma unroll
-            for (int n = 0; n < kCols / 2; ++n) acc[n] = 0;
+            for (int n = 0; n < COLS / 2; ++n) acc[n] = 0;
             for (int b = 0; b < blocks; ++b) {
                 if (b % kScaleBlocks == 0) barrier_wait_inline(scales_full + 8 * slot, scales_parity, dead);
-                const float* sx = scales + ((slot * kScaleBlocks + b % kScaleBlocks) * kScaleSets + set) * COLS + c0;
-                barrier_wait_inline(sums_full + 8 * buffer, parity, dead);
-                tmem_fence_after();
-                uint32_t raw[kCols];
+                if (b % kGroups == group) {
+                    const float* sx = scales + (slot * kScaleBlocks + b % kScaleBlocks) * S::kScaleStep + set * COLS;
+                    barrier_wait_inline(sums_full + 8 * buffer, (parities >> buffer) & 1, dead);
+                    tmem_fence_after();
 #pragma unroll
-                for (int c = 0; c < kCols; c += 32) {
-                    if (c >= many) continue;
-                    if (c + 32 <= kCols) tmem_load32(mine + buffer * S::kStride + c, raw + c);
-                    else tmem_load16(mine + buffer * S::kStride + c, raw + c);
-                }
-                tmem_loaded(raw);
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) barrier_arrive_pair(in_first(sums_empty + 8 * buffer));
+                    for (int c0 = 0; c0 < COLS; c0 += 32) {
+                        if (c0 >= there) continue;
+                        uint32_t raw[32];
+                        tmem_load16(mine + buffer * S::kStride + c0, raw);
+                        if (c0 + 16 < there) tmem_load16(mine + buffer * S::kStride + c0 + 16, raw + 16);
+                        tmem_loaded(raw);
+                        if (c0 + 32 >= there) {   // (all that there are)
+                            tmem_fence_before();
+                            __syncwarp();
+                            if (lane == 0) barrier_arrive_pair(in_first(sums_empty + 8 * buffer));
+                        }
 #pragma unroll
-                for (int c = 0; c < kCols; c += 4) {
-                    if (c / 16 * 16 >= many) continue;
-                    const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(sx + c);
-                    acc[c / 2] = fma2(pair(raw[c], raw[c + 1]), s.x, acc[c / 2]);
-                    acc[c / 2 + 1] = fma2(pair(raw[c + 2], raw[c + 3]), s.y, acc[c / 2 + 1]);
+                        for (int c = 0; c < 32; c += 4) {
+                            if (c0 + c / 16 * 16 >= there) continue;
+                            const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(sx + c0 + c);
+                            uint64_t *to = acc + (c0 + c) / 2;
+                            to[0] = fma2(pair(raw[c], raw[c + 1]), s.x, to[0]);
+                            to[1] = fma2(pair(raw[c + 2], raw[c + 3]), s.y, to[1]);
+                        }
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
                 if (b % kScaleBlocks == kScaleBlocks - 1 || b + 1 == blocks) {
                     if (lane == 0) barrier_arrive(scales_empty + 8 * slot);
                     if (++slot == kScaleSlots) slot = 0, scales_parity ^= 1;
                 }
-                if (++buffer == S::kBuffers) buffer = 0, parity ^= 1;
+                parities ^= 1u << buffer;
+                buffer = (buffer + 1) % kBuffers;
             }
-
+            // The groups' sums meet: columns 0 .. 31 in the first, the others in the second.
+            float* const meet = join + part * 32 + lane;
+            float sums[kOut];
+#pragma unroll
+            for (int g = 0; g < COLS / kOut; ++g) {
+                if (g > 0 && it.rows <= kOut) continue;
+                if (group != g) {
+#pragma unroll
+                    for (int n = 0; n < kOut / 2; ++n) {
+                        const float2 v = apart(acc[g * (kOut / 2) + n]);
+                        meet[2 * n * 128] = v.x, meet[(2 * n + 1) * 128] = v.y;
+                    }
+                }
+                consumers_sync();
+                if (group == g) {
+#pragma unroll
+                    for (int n = 0; n < kOut / 2; ++n) {   // (the first group's plus the second's, whichever adds)
+                        const float2 v = apart(acc[g * (kOut / 2) + n]);
+                        sums[2 * n] = v.x + meet[2 * n * 128], sums[2 * n + 1] = v.y + meet[(2 * n + 1) * 128];
+                    }
+                }
+                consumers_sync();
+            }
+            const int c0 = group * kOut, many = it.rows - c0;   // of this warp's columns, those with a row
             if (*dead) {
 #pragma unroll
-                for (int n = 0; n < kCols / 2; ++n) acc[n] = both(__int_as_float(0x7fffffff));
+                for (int n = 0; n < kOut; ++n) sums[n] = __int_as_float(0x7fffffff);
             }
             // Results: column n, or with the activation column 2 n + odd: gate lanes take the even one of two, up lanes the odd one.
-            constexpr int kResults = SWIGLU ? kCols / 2 : kCols;
+            constexpr int kResults = SWIGLU ? kOut / 2 : kOut;
             const int odd = SWIGLU ? lane >> 4 : 0;
             float v[kResults];
 #pragma unroll
-            for (int n = 0; n < kCols / 2; ++n) {
-                const float2 two = apart(acc[n]);
+            for (int n = 0; n < kResults; ++n) {
                 if constexpr (SWIGLU) {
-                    const float own = lane < 16 ? two.x : two.y, got = __shfl_xor_sync(kFullMask, lane < 16 ? two.y : two.x, 16);
+                    const float own = lane < 16 ? sums[2 * n] : sums[2 * n + 1];
+                    const float got = __shfl_xor_sync(kFullMask, lane < 16 ? sums[2 * n + 1] : sums[2 * n], 16);
                     v[n] = lane < 16 ? silu(own) * got : silu(got) * own;
                 } else {
-                    v[2 * n] = two.x, v[2 * n + 1] = two.y;
+                    v[n] = sums[n];
                 }
             }
             constexpr int kStep = SWIGLU ? 2 : 1;   // columns from one result to the next
@@ -358,14 +389,14 @@ __global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
             for (int n = 0; n < kResults; ++n) {
                 if (n * kStep >= many) continue;
                 const float big = largest(!SWIGLU ? kFullMask : lane < 16 ? 0x0000ffffu : 0xffff0000u, v[n]);
-                if ((lane & (SWIGLU ? 15 : 31)) == 0) most[part * COLS + c0 + n * kStep + odd] = big;
+                if ((lane & (SWIGLU ? 15 : 31)) == 0) most[part * 128 + c0 + n * kStep + odd] = big;
             }
-            consumers_sync<kConsumers>();
+            consumers_sync();
             float big[COLS / kConsumers + 1];
 #pragma unroll
             for (int k = 0, n = tid; n < COLS; ++k, n += kConsumers) {
                 big[k] = 0.0f;
-                for (int w = 0; w < kParts; ++w) big[k] = larger(most[w * COLS + n], big[k]);
+                for (int w = 0; w < kParts; ++w) big[k] = larger(most[w * 128 + n], big[k]);
                 if (SWIGLU) store_other(smem_addr(other_most + most_parity * COLS + n), rank ^ 1, big[k]);
             }
             if (SWIGLU) {   // (two buffers: the other CTA waits for this item's before it is done with the next one's)
@@ -383,7 +414,7 @@ __global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
                 if (block * kBlock < cols && (!SWIGLU || rank == 0)) write_scale(static_cast<int64_t>(it.row) + n, block, s);
             }
             most_parity ^= 1;
-            consumers_sync<kConsumers>();
+            consumers_sync();
             if (real) {
                 const float* my = found + c0 + odd;
                 uint8_t* to = static_cast<uint8_t*>(a.y) + row * a.y_ld + chan;
@@ -403,7 +434,7 @@ __global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
                 const Tile it = tile_at(a.g, plan, table, i);
                 const int half = columns_of(it.rows) / 2, a_boxes = SWIGLU ? 4 : 1, x_boxes = (half + S::kBox - 1) / S::kBox;
                 const int row0 = it.m * kTileRows + rank * (kTileRows / 2);
-                const bool lanes = LANES && it.rows > kMostColumns;
+                const bool lanes = LANES && it.rows > COLS;
                 // with rows as lanes: boxes of this CTA's 128 rows (none of those behind the tile's), and of both
                 const int own = lanes ? (min(max(it.rows - rank * 128, 0), 128) + S::kBox - 1) / S::kBox : 0;
                 const int both_bytes = lanes ? 2 * kABytes + (it.rows + S::kBox - 1) / S::kBox * S::kBox * kBlock
@@ -435,14 +466,20 @@ __global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
         } else if (warp == kIssuer) {
             const uint32_t base = (1u << 4) | (static_cast<uint32_t>(kTileRows / 16) << 24), e5m2 = a.x_dtype == EP_DTYPE_FP8_E5M2 ? 1u : 0u;
             int slot = 0, buffer = 0;
-            uint32_t parity = 0, sums_parity = 1;
+            uint32_t parity = 0, parities = 15;   // parities: a bit for each buffer of sums
             for (int64_t i = pair_id; i < items; i += pairs) {
                 const Tile it = tile_at(a.g, plan, table, i);
-                const bool lanes = LANES && it.rows > kMostColumns;
+                const bool lanes = LANES && it.rows > COLS;
                 const uint32_t shape = base | (lanes ? e5m2 << 7 : e5m2 << 10) | static_cast<uint32_t>((lanes ? 256 : columns_of(it.rows)) / 8) << 17;
                 for (int b = 0; b < blocks; ++b) {
                     barrier_wait_inline(full + 8 * slot, parity, dead);
-                    barrier_wait_inline(sums_empty + 8 * buffer, sums_parity, dead);
+                    if (lanes) {
+                        buffer = (buffer + 1) & 2;   // an even one and the next
+                        barrier_wait_inline(sums_empty + 8 * buffer + 8, (parities >> (buffer + 1)) & 1, dead);
+                        parities ^= 2u << buffer;
+                    }
+                    barrier_wait_inline(sums_empty + 8 * buffer, (parities >> buffer) & 1, dead);
+                    parities ^= 1u << buffer;
                     tmem_fence_after();
                     if (leader) {
                         const uint32_t at_a = smem_addr(ring) + slot * S::kStageBytes;
@@ -454,7 +491,7 @@ __global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
                     }
                     __syncwarp();
                     if (++slot == S::kStages) slot = 0, parity ^= 1;
-                    if (++buffer == S::kBuffers) buffer = 0, sums_parity ^= 1;
+                    buffer = (buffer + (lanes ? 2 : 1)) % kBuffers;
                 }
             }
         } else if (warp >= kScaler) {
@@ -464,12 +501,13 @@ __global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
             int turn = warp - kScaler, slot = 0;
             uint32_t parity = 1;
             const bool by_rows = a.x_scale_block == 1;
-            constexpr int kEach = kScaleBlocks * COLS / 32;
-            static_assert(kScaleBlocks == 2, "");
-            const int wk = lane / 4 % 2, wj = lane % 4;   // lanes 0 .. 7 load the weights' scales: block, which one
+            constexpr int kEach = kScaleBlocks * S::kRows / 32;
+            const int wk = lane / 4 % kScaleBlocks, wj = lane % 4;   // lanes 0 .. 15 load the weights' scales: block, which one
+            const auto row_of = [&](int j) { return by_rows ? j * (32 / kScaleBlocks) + lane / kScaleBlocks : j * 32 % S::kRows + lane; };
+            const auto block_of = [&](int j) { return by_rows ? lane % kScaleBlocks : j * 32 / S::kRows; };
             for (int64_t i = pair_id; i < items; i += pairs) {
                 const Tile it = tile_at(a.g, plan, table, i);
-                const bool lanes = LANES && it.rows > kMostColumns;
+                const bool lanes = LANES && it.rows > COLS;
                 const int skip = lanes ? rank * 128 : 0, rows = it.rows - skip;
                 int o;
                 if (!lanes) o = scale_row(it.m, min(wj, kScaleSets - 1));
@@ -481,8 +519,7 @@ __global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
                         float v[kEach];
 #pragma unroll
                         for (int j = 0; j < kEach; ++j) {
-                            const int n = by_rows ? j * (32 / kScaleBlocks) + lane / kScaleBlocks : j * 32 % COLS + lane;
-                            const int k = by_rows ? lane % kScaleBlocks : j * 32 / COLS;
+                            const int n = row_of(j), k = block_of(j);
                             v[j] = 0.0f;
                             if (n < rows && b + k < blocks) {
                                 const int64_t from = (static_cast<int64_t>(it.row) + skip + n) * a.x_scale_row + (b + k) * a.x_scale_block;
@@ -491,17 +528,16 @@ __global__ void __launch_bounds__(Shape<COLS, LANES>::kThreads, 1)
                         }
                         const float w = w_scales[min(b + wk, blocks - 1)];
                         barrier_wait_inline(scales_empty + 8 * slot, parity, dead);
-                        float* to = scales + slot * (kScaleBlocks * kScaleSets * COLS);
-                        if (lanes && lane < 8) to[wk * (kScaleSets * COLS) + COLS + wj] = w;
+                        float* to = scales + slot * (kScaleBlocks * S::kScaleStep);
+                        if (lanes && lane < 4 * kScaleBlocks) to[wk * S::kScaleStep + 128 + wj] = w;
 #pragma unroll
                         for (int s = 0; s < kScaleSets; ++s) {
                             if (s >= (lanes ? 1 : sets)) continue;
 #pragma unroll
                             for (int j = 0; j < kEach; ++j) {
-                                const int n = by_rows ? j * (32 / kScaleBlocks) + lane / kScaleBlocks : j * 32 % COLS + lane;
-                                const int k = by_rows ? lane % kScaleBlocks : j * 32 / COLS;
+                                const int n = row_of(j), k = block_of(j);
                                 const float factor = __shfl_sync(kFullMask, w, k * 4 + s);
-                                to[(k * kScaleSets + s) * COLS + n] = lanes ? v[j] : v[j] * factor;
+                                if (lanes || n < COLS) to[k * S::kScaleStep + s * COLS + n] = lanes ? v[j] : v[j] * factor;
                             }
                         }
                         __syncwarp();
@@ -527,7 +563,7 @@ cudaError_t launch_shape(const Fp8Args& a, cudaStream_t stream) {
     using S = Shape<COLS, LANES>;
     static int known[64];
     int pairs = 0;
-    cudaError_t err = pairs_at_once(expert_fp8_kernel<COLS, LANES, SWIGLU>, S::kThreads, S::kShared, known, &pairs);
+    cudaError_t err = pairs_at_once(expert_fp8_kernel<COLS, LANES, SWIGLU>, kThreads, S::kShared, known, &pairs);
     if (err != cudaSuccess) return err;
     const int64_t I = a.I, O = a.O, E = a.g.E;
     const int cols = SWIGLU ? a.O / 2 : a.O;
@@ -546,7 +582,7 @@ cudaError_t launch_shape(const Fp8Args& a, cudaStream_t stream) {
     if (err != cudaSuccess) return err;
     const int64_t used = a.g.rows < a.g.E ? a.g.rows : a.g.E;
     const int64_t most = (a.g.rows + used * (p.cap - 1)) / p.cap * p.m_tiles;
-    return launch_pairs(expert_fp8_kernel<COLS, LANES, SWIGLU>, static_cast<int>(most < pairs ? most : pairs), S::kThreads, S::kShared,
+    return launch_pairs(expert_fp8_kernel<COLS, LANES, SWIGLU>, static_cast<int>(most < pairs ? most : pairs), kThreads, S::kShared,
                         stream, a, p, w_map, w_half_map, x_map);
 }
 
@@ -554,10 +590,9 @@ template <bool SWIGLU>
 cudaError_t launch_activation(const Fp8Args& a, cudaStream_t stream) {
     const int used = a.g.rows < a.g.E ? a.g.rows : a.g.E, mean = (a.g.rows - 1) / used + 1;
     if (mean <= 24) return launch_shape<32, false, SWIGLU>(a, stream);
-    if (mean <= 48) return launch_shape<64, false, SWIGLU>(a, stream);
     // (64 neighbouring up rows have one scale)
-    if (SWIGLU && a.O / 2 % 64 != 0) return launch_shape<128, false, SWIGLU>(a, stream);
-    return launch_shape<128, true, SWIGLU>(a, stream);
+    if (mean <= 48 || (SWIGLU && a.O / 2 % 64 != 0)) return launch_shape<64, false, SWIGLU>(a, stream);
+    return launch_shape<64, true, SWIGLU>(a, stream);
 }
 
 }  // namespace

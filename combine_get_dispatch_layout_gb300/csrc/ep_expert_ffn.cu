@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t da = kAOut ? operand_outward(at_a, 8192) : operand(at_a, 1024);
                     const uint64_t db = kBOut ? operand_outward(at_b, 8192) : operand(at_b, 1024);
                     for (int k = 0; k < depth; ++k)
-                        multiply_pair<false>(sums, da + k * (kAOut ? 128 : 2), db + k * (kBOut ? 128 : 2), shape, s > 0 || k > 0);
+                        multiply_pair(sums, da + k * (kAOut ? 128 : 2), db + k * (kBOut ? 128 : 2), shape, s > 0 || k > 0);
                     pair_done(empty + 8 * slot);
                     if (s + 1 == it.steps) pair_done(sums_full + 8 * buffer);
                 }

@@ -3,42 +3,40 @@
 //
 // Mathematics. y[n, o] = sum over blocks b of sx[n, b] sw[o / 128, b] * sum over i in b of cx[n, i] cw[o, i]. The inner
 // sums, 128 products of two codes, run through the tensor cores with fp32 sums; each is then scaled and added in fp32
-// registers, so no scale is rounded and the sums of blocks are plain fp32. With the activation: silu(gate) * up. An fp8
-// output is quantised as the dispatch quantises: amax of 128 channels / 448, codes by IEEE division.
+// registers. With the activation: silu(gate) * up. An fp8 output is quantised as the dispatch quantises: amax of 128
+// channels / 448, codes by IEEE division.
 #include "ep_expert_tiles.cuh"
 
 namespace ep {
 namespace {
 
 constexpr int kBlock = 128;                     // inputs of a stage: 128 bytes, one scale
-constexpr int kTileRows = 256;                  // weight rows of an item: 128 in each CTA of the pair
-constexpr int kParts = 4;                       // warps over a CTA's weight rows: 32 lanes each
-constexpr int kABytes = kTileRows / 2 * kBlock;
-constexpr int kGroups = 2;                      // groups of kParts warps: they take blocks, columns or channels in turn
+constexpr int kTileRows = 256;                  // weight rows of an item: two halves of 128, gate and up with the activation
+constexpr int kParts = 4;                       // warps over 128 lanes
+constexpr int kGroups = 2;                      // groups of kParts warps: they take blocks or columns in turn
 constexpr int kConsumers = 32 * kParts * kGroups;
 constexpr int kLoader = kConsumers / 32, kIssuer = kLoader + 1, kScaler = kLoader + 2;   // warps; two scalers
 constexpr int kThreads = kConsumers + 128;
-constexpr int kBuffers = 4;                     // of sums in TMEM, 64 or 128 columns apart
+constexpr int kWBytes = kTileRows * kBlock;
+constexpr int kBuffers = 4;                     // of sums in TMEM, 128 columns apart
 constexpr int kScaleSlots = 4;                  // of the ring of scales
-constexpr int kScaleSets = 3;                   // weight scales that a CTA's 128 weight rows have at most in a block
-constexpr int kOut = 32;                        // columns that a group has in the end
-constexpr int kMostStages = 10;
+constexpr int kChunk = 16;                      // columns that a group has in the end, of 2 * kChunk
+constexpr int kMostStages = 6;
 
 // COLS: rows of x that are columns of a product, at most. LANES: tiles of more rows have them as lanes.
 template <int COLS, bool LANES>
 struct Shape {
     static_assert(COLS == 32 || COLS == 64, "");
-    static constexpr int kStride = LANES ? 128 : 64;             // columns of a buffer; rows as lanes take two buffers
-    static constexpr int kRows = LANES ? 128 : COLS;             // rows of x whose scales a CTA needs
+    static constexpr bool kMoved = COLS == 64;                   // up to 128 sums a thread: registers move to the consumers
+    static constexpr int kRows = LANES ? 128 : COLS;             // rows of x of an item
     static constexpr int kScaleBlocks = LANES ? 2 : 4;           // blocks of a slot of the ring of scales
-    static constexpr int kScaleStep = kScaleSets * COLS;         // floats of a block in the ring of scales
-    static_assert(!LANES || kScaleStep >= 128 + 4, "");
+    static constexpr int kScaleStep = kRows + 4;                 // floats of a block: the rows' scales, up to four of the weights'
     static constexpr int kBox = COLS / 2;
-    static constexpr int kStageBytes = kABytes + (LANES ? 128 : COLS / 2) * kBlock;
+    static constexpr int kStageBytes = kWBytes + kRows * kBlock;
     static constexpr int kStages = 192 * 1024 / kStageBytes < kMostStages ? 192 * 1024 / kStageBytes : kMostStages;
     static constexpr int kScales = kScaleSlots * kScaleBlocks * kScaleStep;   // floats
-    static constexpr int kJoin = kOut * 128;
-    static constexpr int kMost = kParts * 128 + 3 * COLS;
+    static constexpr int kJoin = 2 * kChunk * 128;
+    static constexpr int kMost = 4 * 128 + 2 * kParts * COLS + 2 * COLS;
     static constexpr int kShared = 1024 + kStages * kStageBytes + (kScales + kJoin + kMost) * 4 + 512 + (kTileTable + 1) * 4;
     static_assert(kShared <= 227 * 1024 - 256, "");
 };
@@ -58,31 +56,29 @@ __device__ __forceinline__ float power_of_two(float s) {
 // SWIGLU: y = silu(gate) * up.
 template <int COLS, bool LANES, bool SWIGLU>
 __global__ void __launch_bounds__(kThreads, 1)
-    expert_fp8_kernel(Fp8Args a, TilePlan plan, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap w_half_map,
-                      const __grid_constant__ CUtensorMap x_map) {
+    expert_fp8_kernel(Fp8Args a, TilePlan plan, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map) {
     using S = Shape<COLS, LANES>;
     constexpr int kScaleBlocks = S::kScaleBlocks;
     extern __shared__ unsigned char shared_bytes[];
     unsigned char* const ring = shared_bytes + (1024 - smem_addr(shared_bytes) % 1024) % 1024;
     float* const scales = reinterpret_cast<float*>(ring + S::kStages * S::kStageBytes);   // [kScaleSlots][kScaleBlocks][kScaleStep]
-    float* const join = scales + S::kScales;                                              // [kOut][128]
-    float* const most = join + S::kJoin;                                                  // [kParts][128]: largest by part
-    float* const found = most + kParts * 128;                                             // [COLS]: the output's scales
-    float* const other_most = found + COLS;                                               // [2][COLS]: the other CTA's largest
-    uint64_t* const barriers = reinterpret_cast<uint64_t*>(other_most + 2 * COLS);
+    float* const join = scales + S::kScales;                                              // [kGroups][kChunk][128]
+    float* const most = join + S::kJoin;                                                  // the largest: [2][2][128] rows as lanes,
+    float* const column_most = most + 4 * 128;                                            // [2 halves][kParts][COLS] as columns
+    float* const found = column_most + 2 * kParts * COLS;                                 // [2 halves][COLS]: the output's scales
+    uint64_t* const barriers = reinterpret_cast<uint64_t*>(found + 2 * COLS);
     const uint32_t full = smem_addr(barriers), empty = full + 8 * kMostStages;
-    const uint32_t sums_full = empty + 8 * kMostStages, sums_empty = sums_full + 32;
-    const uint32_t scales_full = sums_empty + 32, scales_empty = scales_full + 8 * kScaleSlots;
-    const uint32_t most_full = scales_empty + 8 * kScaleSlots;
+    const uint32_t sums_full = empty + 8 * kMostStages, sums_empty = sums_full + 8 * kBuffers;
+    const uint32_t scales_full = sums_empty + 8 * kBuffers, scales_empty = scales_full + 8 * kScaleSlots;
     uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(barriers) + 120;
     volatile int* const dead = reinterpret_cast<volatile int*>(tmem_at + 1);
     int* const table = reinterpret_cast<int*>(barriers) + 128;
-    static_assert((2 * kMostStages + 9 + 2 * kScaleSlots) * 2 <= 120, "");
+    static_assert((2 * kMostStages + 2 * kBuffers + 2 * kScaleSlots) * 2 <= 120, "");
     __shared__ int warp_sum[kThreads / 32];
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = pair_rank();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (warp == kLoader) {
-        tmem_alloc_all(smem_addr(tmem_at));
+        tmem_alloc_one(smem_addr(tmem_at));
         if (lane == 0) {
             *dead = 0;
             for (int i = 0; i < S::kStages; ++i) {
@@ -91,9 +87,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int i = 0; i < kBuffers; ++i) {
                 barrier_init(sums_full + 8 * i, 1);
-                barrier_init(sums_empty + 8 * i, 2 * kParts);   // a group of each CTA
+                barrier_init(sums_empty + 8 * i, kParts);   // a group
             }
-            barrier_init(most_full, kConsumers / 32);
             for (int i = 0; i < kScaleSlots; ++i) {
                 barrier_init(scales_full + 8 * i, 1);
                 barrier_init(scales_empty + 8 * i, kConsumers / 32);
@@ -105,20 +100,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     fill_table<kThreads>(a.g, plan, table, warp_sum);
     tmem_fence_before();
     __syncthreads();
-    cluster_sync();   // (both CTAs' barriers are ready)
     tmem_fence_after();
     const uint32_t tmem = __shfl_sync(kFullMask, *tmem_at, 0);
     const bool leader = elected();
     const int blocks = a.I / kBlock, cols = SWIGLU ? a.O / 2 : a.O;
     const int64_t items = tile_count(a.g, plan, table);
-    const int pair_id = blockIdx.x / 2, pairs = gridDim.x / 2;
 
-    // Weight scales of a block that this CTA's rows of tile m have: those of the gate rows (or all), then of the up rows.
-    const auto scale_row = [&](int m, int set) {
-        const int row0 = m * kTileRows + rank * (kTileRows / 2);
-        if (!SWIGLU) return row0 / kBlock;
-        return set == 0 ? row0 / 2 / kBlock : (cols + row0 / 2) / kBlock + set - 1;
-    };
+    // First channel of an item's halves (of gate and up they are the same ones), and their first weight rows.
+    const auto channel = [&](int m, int half) { return SWIGLU ? m * 128 : m * kTileRows + half * 128; };
+    const auto weight_row = [&](int m, int half) { return SWIGLU ? half * cols + m * 128 : m * kTileRows + half * 128; };
+
     // What an e4m3 output needs: the scale of a block whose largest value is `big`, its place, two values' codes.
     const auto larger = [](float x, float y) { return x > y || x != x ? x : y; };   // (NaN stays)
     const auto output_scale = [&](float big) {
@@ -136,39 +127,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto codes = [](float2 v, float s) -> uint32_t {
         return s == 0.0f ? 0u : __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v.x, s), __fdiv_rn(v.y, s)), __NV_SATFINITE, __NV_E4M3);
     };
-    const int scale_rows = ceil_div(a.O, kBlock), sets = !SWIGLU ? 1 : cols % 64 == 0 ? 2 : 3;
 
     // (registers: 256 x 216 + 128 x 72 of the launch's 384 x 168)
     if (warp < kLoader) {
-        if constexpr (LANES) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        // 32 of the CTA's 128 lanes
+        if constexpr (S::kMoved) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int part = warp % kParts, group = warp / kParts;
-        const uint32_t mine = tmem + (static_cast<uint32_t>(part) << 21);
+        const uint32_t mine = tmem + (static_cast<uint32_t>(part) << 21);   // lanes 32 * part, upper half
         int buffer = 0, slot = 0;
-        uint32_t parities = 0, scales_parity = 0, most_parity = 0;   // parities: a bit for each buffer
+        uint32_t parities = 0, scales_parity = 0;   // parities: a bit for each buffer
         // A tile whose rows of x are the lanes: a thread has one of them and 64 columns of each half of the 256 weight rows (gate
         // and up of the same 64 channels). Its scales are two numbers a block.
         const auto rows_as_lanes = [&](const Tile& it) {
-            const int r = rank * 128 + part * 32 + lane, h = group;
+            const int r = part * 32 + lane, h = group;
             const bool real = r < it.rows;
             const int64_t row = it.row + static_cast<int64_t>(real ? r : 0);
-            const int first = SWIGLU ? it.m * 128 + h * 64 : it.m * kTileRows + h * 64;   // channel of column 0 of the first half
-            const int second = SWIGLU ? first : first + 128;
+            const int first = channel(it.m, 0) + h * 64, second = channel(it.m, 1) + h * 64;
             uint64_t acc[2][32];
 #pragma unroll
             for (int n = 0; n < 32; ++n) acc[0][n] = acc[1][n] = 0;
-            const uint32_t from = mine + h * 64;
-            for (int b = 0; b < blocks; ++b) {
+            // the scales of a block are fetched while the sums of the one before are on their way
+            float s0, s1;
+            const auto fetch = [&](int b) {
                 if (b % kScaleBlocks == 0) barrier_wait_inline(scales_full + 8 * slot, scales_parity, dead);
                 const float* sx = scales + (slot * kScaleBlocks + b % kScaleBlocks) * S::kScaleStep;
-                const float x_scale = sx[part * 32 + lane];
-                const uint64_t s0 = both(x_scale * sx[128 + h]), s1 = both(x_scale * sx[128 + 2 + h]);
-                buffer = (buffer + 1) & 2;   // an even one
+                const float x_scale = sx[r];
+                s0 = x_scale * sx[S::kRows + h], s1 = x_scale * sx[S::kRows + 2 + h];
+                if (b % kScaleBlocks == kScaleBlocks - 1 || b + 1 == blocks) {
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(scales_empty + 8 * slot);
+                    if (++slot == kScaleSlots) slot = 0, scales_parity ^= 1;
+                }
+            };
+            fetch(0);
+            for (int b = 0; b < blocks; ++b) {
+                buffer = (buffer + 1) & 2;   // an even one and the next
                 barrier_wait_inline(sums_full + 8 * buffer, (parities >> buffer) & 1, dead);
                 tmem_fence_after();
-                const uint32_t at = from + buffer * S::kStride;
+                const uint32_t at = mine + buffer * 128 + h * 64;
                 uint32_t raw[2][16];
                 tmem_load16(at, raw[0]);
+                const uint64_t f0 = both(s0), f1 = both(s1);
+                if (b + 1 < blocks) fetch(b + 1);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {   // a chunk of sums is on its way while the one before is added
                     tmem_loaded(raw[c & 1]);
@@ -177,20 +176,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         tmem_fence_before();
                         __syncwarp();
-                        if (lane == 0) barrier_arrive_pair(in_first(sums_empty + 8 * (buffer + h)));   // (the issuer waits for both)
+                        if (lane == 0) barrier_arrive(sums_empty + 8 * (buffer + h));   // (the issuer waits for both)
                     }
 #pragma unroll
                     for (int n = 0; n < 8; ++n) {
                         uint64_t& to = acc[c / 4][c % 4 * 8 + n];
-                        to = fma2(pair(raw[c & 1][2 * n], raw[c & 1][2 * n + 1]), c < 4 ? s0 : s1, to);
+                        to = fma2(pair(raw[c & 1][2 * n], raw[c & 1][2 * n + 1]), c < 4 ? f0 : f1, to);
                     }
                 }
-                if (b % kScaleBlocks == kScaleBlocks - 1 || b + 1 == blocks) {
-                    if (lane == 0) barrier_arrive(scales_empty + 8 * slot);
-                    if (++slot == kScaleSlots) slot = 0, scales_parity ^= 1;
-                }
                 parities ^= 1u << buffer;
-                buffer = (buffer + 2) & 3;
+                buffer = (buffer + 2) % kBuffers;
             }
             if (*dead) {
 #pragma unroll
@@ -271,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             consumers_sync();   // (`most` is written again)
         };
-        for (int64_t i = pair_id; i < items; i += pairs) {
+        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
             const Tile it = tile_at(a.g, plan, table, i);
             if constexpr (LANES) {
                 if (it.rows > COLS) {
@@ -279,40 +274,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                     continue;
                 }
             }
-            // this thread's output channel and weight row; with the activation a warp's lanes are 16 gate and 16 up rows
-            const int row0 = it.m * kTileRows + rank * (kTileRows / 2) + part * 32;
-            const int chan = SWIGLU ? row0 / 2 + (lane & 15) : row0 + lane;
-            const bool real = chan < cols;
-            const int set = SWIGLU && lane >= 16 && real ? (cols + chan) / kBlock - scale_row(it.m, 1) + 1 : 0;
+            // A tile whose rows of x are columns: a thread has a channel of each half (gate and up of one).
             const int there = max(it.rows, 1);   // (a tile without rows has a product all the same)
-            uint64_t acc[COLS / 2];   // columns 2 n, 2 n + 1; the groups take every other block each
+            const int first = channel(it.m, 0) + part * 32 + lane, second = channel(it.m, 1) + part * 32 + lane;
+            // its second weight scale is the third of the ring where up rows of a tile lie in two blocks
+            const int w_second = SWIGLU && second < cols ? 1 + (cols + second) / kBlock - weight_row(it.m, 1) / kBlock : 1;
+            uint64_t acc[2][COLS / 2];   // columns 2 n, 2 n + 1; the groups take every other block each
 #pragma unroll
-            for (int n = 0; n < COLS / 2; ++n) acc[n] = 0;
+            for (int n = 0; n < COLS / 2; ++n) acc[0][n] = acc[1][n] = 0;
             for (int b = 0; b < blocks; ++b) {
                 if (b % kScaleBlocks == 0) barrier_wait_inline(scales_full + 8 * slot, scales_parity, dead);
                 if (b % kGroups == group) {
-                    const float* sx = scales + (slot * kScaleBlocks + b % kScaleBlocks) * S::kScaleStep + set * COLS;
+                    const float* sx = scales + (slot * kScaleBlocks + b % kScaleBlocks) * S::kScaleStep;
+                    const uint64_t w[2] = {both(sx[S::kRows]), both(sx[S::kRows + w_second])};
                     barrier_wait_inline(sums_full + 8 * buffer, (parities >> buffer) & 1, dead);
                     tmem_fence_after();
 #pragma unroll
-                    for (int c0 = 0; c0 < COLS; c0 += 32) {
+                    for (int c0 = 0; c0 < COLS; c0 += 16) {
                         if (c0 >= there) continue;
-                        uint32_t raw[32];
-                        tmem_load16(mine + buffer * S::kStride + c0, raw);
-                        if (c0 + 16 < there) tmem_load16(mine + buffer * S::kStride + c0 + 16, raw + 16);
-                        tmem_loaded(raw);
-                        if (c0 + 32 >= there) {   // (all that there are)
+                        uint32_t raw[2][16];
+                        tmem_load16(mine + buffer * 128 + c0, raw[0]);
+                        tmem_load16(mine + buffer * 128 + 64 + c0, raw[1]);
+                        tmem_loaded(raw[0]);
+                        tmem_loaded(raw[1]);
+                        if (c0 + 16 >= there) {   // (all that there are)
                             tmem_fence_before();
                             __syncwarp();
-                            if (lane == 0) barrier_arrive_pair(in_first(sums_empty + 8 * buffer));
+                            if (lane == 0) barrier_arrive(sums_empty + 8 * buffer);
                         }
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            if (c0 + c / 16 * 16 >= there) continue;
+                        for (int c = 0; c < 16; c += 4) {
                             const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(sx + c0 + c);
-                            uint64_t *to = acc + (c0 + c) / 2;
-                            to[0] = fma2(pair(raw[c], raw[c + 1]), s.x, to[0]);
-                            to[1] = fma2(pair(raw[c + 2], raw[c + 3]), s.y, to[1]);
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                uint64_t* to = acc[half] + (c0 + c) / 2;
+                                to[0] = fma2(pair(raw[half][c], raw[half][c + 1]), mul2(s.x, w[half]), to[0]);
+                                to[1] = fma2(pair(raw[half][c + 2], raw[half][c + 3]), mul2(s.y, w[half]), to[1]);
+                            }
                         }
                     }
                     __syncwarp();
@@ -324,150 +322,114 @@ __global__ void __launch_bounds__(kThreads, 1)
                 parities ^= 1u << buffer;
                 buffer = (buffer + 1) % kBuffers;
             }
-            // The groups' sums meet: columns 0 .. 31 in the first, the others in the second.
-            float* const meet = join + part * 32 + lane;
-            float sums[kOut];
+            // The groups' sums meet, of 2 * kChunk columns at a time: the first group has the first kChunk of them in the end,
+            // the second the others. results[k][.]: column (2 k + group) * kChunk on.
+            constexpr int kHalves = SWIGLU ? 1 : 2, kPairs = COLS / (2 * kChunk);
+            float results[kPairs][kHalves][kChunk];
 #pragma unroll
-            for (int g = 0; g < COLS / kOut; ++g) {
-                if (g > 0 && it.rows <= kOut) continue;
-                if (group != g) {
+            for (int k = 0; k < kPairs; ++k) {
+                if (2 * k * kChunk >= there) continue;
+                float gate[kChunk];
 #pragma unroll
-                    for (int n = 0; n < kOut / 2; ++n) {
-                        const float2 v = apart(acc[g * (kOut / 2) + n]);
-                        meet[2 * n * 128] = v.x, meet[(2 * n + 1) * 128] = v.y;
+                for (int half = 0; half < 2; ++half) {
+                    float own[kChunk];
+#pragma unroll
+                    for (int n = 0; n < kChunk; n += 2) {   // (constant places in registers, whichever group it is)
+                        const float2 p = apart(acc[half][(2 * k * kChunk + n) / 2]), q = apart(acc[half][((2 * k + 1) * kChunk + n) / 2]);
+                        own[n] = group == 0 ? p.x : q.x, own[n + 1] = group == 0 ? p.y : q.y;
+                        float* to = join + ((group ^ 1) * kChunk + n) * 128 + part * 32 + lane;
+                        to[0] = group == 0 ? q.x : p.x, to[128] = group == 0 ? q.y : p.y;
                     }
-                }
-                consumers_sync();
-                if (group == g) {
+                    consumers_sync();
 #pragma unroll
-                    for (int n = 0; n < kOut / 2; ++n) {   // (the first group's plus the second's, whichever adds)
-                        const float2 v = apart(acc[g * (kOut / 2) + n]);
-                        sums[2 * n] = v.x + meet[2 * n * 128], sums[2 * n + 1] = v.y + meet[(2 * n + 1) * 128];
+                    for (int n = 0; n < kChunk; ++n) {
+                        float v = own[n] + join[(group * kChunk + n) * 128 + part * 32 + lane];
+                        if (*dead) v = __int_as_float(0x7fffffff);
+                        if (!SWIGLU) results[k][half % kHalves][n] = v;
+                        else if (half == 0) gate[n] = v;
+                        else results[k][0][n] = silu(gate[n]) * v;
                     }
-                }
-                consumers_sync();
-            }
-            const int c0 = group * kOut, many = it.rows - c0;   // of this warp's columns, those with a row
-            if (*dead) {
-#pragma unroll
-                for (int n = 0; n < kOut; ++n) sums[n] = __int_as_float(0x7fffffff);
-            }
-            // Results: column n, or with the activation column 2 n + odd: gate lanes take the even one of two, up lanes the odd one.
-            constexpr int kResults = SWIGLU ? kOut / 2 : kOut;
-            const int odd = SWIGLU ? lane >> 4 : 0;
-            float v[kResults];
-#pragma unroll
-            for (int n = 0; n < kResults; ++n) {
-                if constexpr (SWIGLU) {
-                    const float own = lane < 16 ? sums[2 * n] : sums[2 * n + 1];
-                    const float got = __shfl_xor_sync(kFullMask, lane < 16 ? sums[2 * n + 1] : sums[2 * n], 16);
-                    v[n] = lane < 16 ? silu(own) * got : silu(got) * own;
-                } else {
-                    v[n] = sums[n];
+                    consumers_sync();
                 }
             }
-            constexpr int kStep = SWIGLU ? 2 : 1;   // columns from one result to the next
-            const int64_t row = static_cast<int64_t>(it.row) + c0 + odd;
-            const int left = many - odd;
+            const auto column = [&](int k, int n) { return (2 * k + group) * kChunk + n; };
             if (a.y_dtype != EP_DTYPE_FP8_E4M3) {
-                if (!real) continue;
-                uint16_t* to = static_cast<uint16_t*>(a.y) + row * a.y_ld + chan;
-                const int64_t step = kStep * a.y_ld;
                 const bool bf16 = a.y_dtype == EP_DTYPE_BF16;
 #pragma unroll
-                for (int n = 0; n < kResults; ++n, to += step)
-                    if (n * kStep < left)
-                        *to = bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v[n])) : __half_as_ushort(__float2half_rn(v[n]));
+                for (int k = 0; k < kPairs; ++k)
+#pragma unroll
+                    for (int half = 0; half < kHalves; ++half) {
+                        const int chan = half == 0 ? first : second;
+                        uint16_t* to = static_cast<uint16_t*>(a.y) + (static_cast<int64_t>(it.row) + column(k, 0)) * a.y_ld + chan;
+                        if (chan >= cols) continue;
+#pragma unroll
+                        for (int n = 0; n < kChunk; ++n, to += a.y_ld)
+                            if (column(k, n) < it.rows)
+                                *to = bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(results[k][half][n]))
+                                           : __half_as_ushort(__float2half_rn(results[k][half][n]));
+                    }
                 continue;
             }
-            // ---- e4m3: the largest of each column's 128 channels (with the activation half of them in the other CTA), its
-            // scale, codes
-            const auto largest = [&](uint32_t mask, float v) {   // (of numbers that are not negative the bits compare as they do)
-                return __uint_as_float(__reduce_max_sync(mask, real ? __float_as_uint(fabsf(v)) : 0u));
-            };
+            // ---- e4m3: the largest of each column's 128 channels, its scale, codes
 #pragma unroll
-            for (int n = 0; n < kResults; ++n) {
-                if (n * kStep >= many) continue;
-                const float big = largest(!SWIGLU ? kFullMask : lane < 16 ? 0x0000ffffu : 0xffff0000u, v[n]);
-                if ((lane & (SWIGLU ? 15 : 31)) == 0) most[part * 128 + c0 + n * kStep + odd] = big;
+            for (int k = 0; k < kPairs; ++k)
+#pragma unroll
+                for (int half = 0; half < kHalves; ++half)
+#pragma unroll
+                    for (int n = 0; n < kChunk; ++n) {
+                        if (column(k, n) >= it.rows) continue;
+                        // (of numbers that are not negative the bits compare as they do; columns are a multiple of 128)
+                        const uint32_t big = __reduce_max_sync(kFullMask, __float_as_uint(fabsf(results[k][half][n])));
+                        if (lane == 0) column_most[(half * kParts + part) * COLS + column(k, n)] = __uint_as_float(big);
+                    }
+            consumers_sync();
+            if (tid < kHalves * COLS && tid % COLS < it.rows) {
+                const int half = tid / COLS, n = tid % COLS, chan = channel(it.m, half);
+                float big = 0.0f;
+                for (int w = 0; w < kParts; ++w) big = larger(column_most[(half * kParts + w) * COLS + n], big);
+                const float s = output_scale(big);
+                found[tid] = s;
+                if (chan < cols) write_scale(static_cast<int64_t>(it.row) + n, chan / kBlock, s);
             }
             consumers_sync();
-            float big[COLS / kConsumers + 1];
 #pragma unroll
-            for (int k = 0, n = tid; n < COLS; ++k, n += kConsumers) {
-                big[k] = 0.0f;
-                for (int w = 0; w < kParts; ++w) big[k] = larger(most[w * 128 + n], big[k]);
-                if (SWIGLU) store_other(smem_addr(other_most + most_parity * COLS + n), rank ^ 1, big[k]);
-            }
-            if (SWIGLU) {   // (two buffers: the other CTA waits for this item's before it is done with the next one's)
-                __syncwarp();
-                if (lane == 0) barrier_arrive_cluster(in_cta(most_full, rank ^ 1));
-                barrier_wait_cluster(most_full, most_parity, dead);
-            }
+            for (int k = 0; k < kPairs; ++k)
 #pragma unroll
-            for (int k = 0, n = tid; n < COLS; ++k, n += kConsumers) {
-                if (n >= it.rows) continue;
-                if (SWIGLU) big[k] = larger(other_most[most_parity * COLS + n], big[k]);
-                const float s = output_scale(big[k]);
-                found[n] = s;
-                const int block = SWIGLU ? it.m : it.m * 2 + rank;   // of 128 channels
-                if (block * kBlock < cols && (!SWIGLU || rank == 0)) write_scale(static_cast<int64_t>(it.row) + n, block, s);
-            }
-            most_parity ^= 1;
-            consumers_sync();
-            if (real) {
-                const float* my = found + c0 + odd;
-                uint8_t* to = static_cast<uint8_t*>(a.y) + row * a.y_ld + chan;
-                const int64_t step = kStep * a.y_ld;
+                for (int half = 0; half < kHalves; ++half) {
+                    const int chan = half == 0 ? first : second;
+                    if (chan >= cols) continue;
+                    uint8_t* to = static_cast<uint8_t*>(a.y) + (static_cast<int64_t>(it.row) + column(k, 0)) * a.y_ld + chan;
 #pragma unroll
-                for (int n = 0; n < kResults; ++n, to += step)
-                    if (n * kStep < left)
-                        *to = static_cast<uint8_t>(codes(make_float2(v[n], 0.0f), my[n * kStep]));
-            }
+                    for (int n = 0; n < kChunk; ++n, to += a.y_ld)
+                        if (column(k, n) < it.rows)
+                            *to = static_cast<uint8_t>(codes(make_float2(results[k][half][n], 0.0f), found[half * COLS + column(k, n)]));
+                }
         }
     } else {
-        if constexpr (LANES) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if constexpr (S::kMoved) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kLoader) {
             int slot = 0;
-            uint32_t parity = 1;
-            for (int64_t i = pair_id; i < items; i += pairs) {
+            uint32_t parity = 1;   // (the first round of the ring waits for nothing)
+            for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
                 const Tile it = tile_at(a.g, plan, table, i);
-                const int half = columns_of(it.rows) / 2, a_boxes = SWIGLU ? 4 : 1, x_boxes = (half + S::kBox - 1) / S::kBox;
-                const int row0 = it.m * kTileRows + rank * (kTileRows / 2);
-                const bool lanes = LANES && it.rows > COLS;
-                // with rows as lanes: boxes of this CTA's 128 rows (none of those behind the tile's), and of both
-                const int own = lanes ? (min(max(it.rows - rank * 128, 0), 128) + S::kBox - 1) / S::kBox : 0;
-                const int both_bytes = lanes ? 2 * kABytes + (it.rows + S::kBox - 1) / S::kBox * S::kBox * kBlock
-                                             : 2 * (kABytes + x_boxes * S::kBox * kBlock);
+                const int x_boxes = (max(it.rows, 1) + S::kBox - 1) / S::kBox;
                 for (int b = 0; b < blocks; ++b) {
-                    // both CTAs' boxes count on the first one's barrier
-                    const uint32_t bar = in_first(full + 8 * slot), at_a = smem_addr(ring) + slot * S::kStageBytes, at_x = at_a + kABytes;
+                    const uint32_t bar = full + 8 * slot, at_w = smem_addr(ring) + slot * S::kStageBytes, at_x = at_w + kWBytes;
                     barrier_wait_inline(empty + 8 * slot, parity, dead);
-                    if (lane == 0 && rank == 0) barrier_expect(full + 8 * slot, both_bytes);
+                    if (lane == 0) barrier_expect(bar, kWBytes + x_boxes * S::kBox * kBlock);
                     __syncwarp();
-                    if (lanes) {
-                        if (lane < own) {
-                            load_box_pair(at_a + lane * S::kBox * kBlock, &x_map, b * kBlock, it.row + rank * 128 + lane * S::kBox, 0, 0, bar);
-                        } else if (lane == 31) {   // the first CTA has the gate rows or the first half, the second the others
-                            if (SWIGLU) load_box_pair(at_x, &w_half_map, b * kBlock, it.m * (kTileRows / 2), rank, it.expert, bar);
-                            else load_box_pair(at_x, &w_map, b * kBlock, row0, 0, it.expert, bar);
-                        }
-                    } else if (lane < a_boxes) {
-                        if (SWIGLU) load_box_pair(at_a + lane * 4096, &w_map, b * kBlock, row0 / 2 + lane * 16, 0, it.expert, bar);
-                        else load_box_pair(at_a, &w_map, b * kBlock, row0, 0, it.expert, bar);
-                    } else if (lane - a_boxes < x_boxes) {
-                        const int j = lane - a_boxes;
-                        load_box_pair(at_x + j * S::kBox * kBlock, &x_map, b * kBlock, it.row + rank * half + j * S::kBox, 0, 0, bar);
-                    }
+                    if (lane == 0) load_box(at_w, &w_map, b * kBlock, SWIGLU ? it.m * 128 : it.m * kTileRows, 0, it.expert, bar);
+                    else if (lane <= x_boxes)
+                        load_box(at_x + (lane - 1) * S::kBox * kBlock, &x_map, b * kBlock, it.row + (lane - 1) * S::kBox, 0, 0, bar);
                     if (++slot == S::kStages) slot = 0, parity ^= 1;
                 }
             }
-        } else if (warp == kIssuer && rank == 1) {   // (the first CTA's issues for both)
         } else if (warp == kIssuer) {
-            const uint32_t base = (1u << 4) | (static_cast<uint32_t>(kTileRows / 16) << 24), e5m2 = a.x_dtype == EP_DTYPE_FP8_E5M2 ? 1u : 0u;
+            const uint32_t e5m2 = a.x_dtype == EP_DTYPE_FP8_E5M2 ? 1u : 0u;
+            const uint32_t base = (1u << 4) | (128u / 16 << 24);   // fp32 sums, 128 lanes
             int slot = 0, buffer = 0;
             uint32_t parity = 0, parities = 15;   // parities: a bit for each buffer of sums
-            for (int64_t i = pair_id; i < items; i += pairs) {
+            for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
                 const Tile it = tile_at(a.g, plan, table, i);
                 const bool lanes = LANES && it.rows > COLS;
                 const uint32_t shape = base | (lanes ? e5m2 << 7 : e5m2 << 10) | static_cast<uint32_t>((lanes ? 256 : columns_of(it.rows)) / 8) << 17;
@@ -482,12 +444,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     parities ^= 1u << buffer;
                     tmem_fence_after();
                     if (leader) {
-                        const uint32_t at_a = smem_addr(ring) + slot * S::kStageBytes;
-                        const uint64_t dw = operand(at_a, 1024), dx = operand(at_a + kABytes, 1024);
-    #pragma unroll
-                        for (int k = 0; k < kBlock / 32; ++k) multiply_pair<true>(tmem + buffer * S::kStride, dw + k * 2, dx + k * 2, shape, k > 0);
-                        pair_done(empty + 8 * slot);
-                        pair_done(sums_full + 8 * buffer);
+                        const uint32_t at_w = smem_addr(ring) + slot * S::kStageBytes;
+                        const uint64_t dw = operand(at_w, 1024), dx = operand(at_w + kWBytes, 1024);
+                        const uint32_t sums = tmem + buffer * 128;
+                        if (lanes) {
+#pragma unroll
+                            for (int k = 0; k < kBlock / 32; ++k) multiply_one(sums, dx + k * 2, dw + k * 2, shape, k > 0);
+                        } else {
+#pragma unroll
+                            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                                for (int k = 0; k < kBlock / 32; ++k)
+                                    multiply_one(sums + half * 64, dw + half * (128 * kBlock / 16) + k * 2, dx + k * 2, shape, k > 0);
+                        }
+                        multiply_done(empty + 8 * slot);
+                        multiply_done(sums_full + 8 * buffer);
                     }
                     __syncwarp();
                     if (++slot == S::kStages) slot = 0, parity ^= 1;
@@ -495,25 +466,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         } else if (warp >= kScaler) {
-            // Scales for two blocks at a time, the two warps in turn: products of the rows' and the weights' for rows as columns;
-            // for rows as lanes the CTA's rows', and behind them the weights' of the first and second half's 64-row quarters.
-            // Lanes run along what is dense in memory.
+            // The rows' scales for some blocks at a time, the two warps in turn, and behind them the weights' (rows as columns:
+            // the first half's, the second half's one or two; rows as lanes: of 64 weight rows each). Lanes run along what is
+            // dense in memory.
             int turn = warp - kScaler, slot = 0;
             uint32_t parity = 1;
             const bool by_rows = a.x_scale_block == 1;
+            const int scale_rows = ceil_div(a.O, kBlock);
             constexpr int kEach = kScaleBlocks * S::kRows / 32;
-            const int wk = lane / 4 % kScaleBlocks, wj = lane % 4;   // lanes 0 .. 15 load the weights' scales: block, which one
+            const int wk = lane / 4 % kScaleBlocks, wj = lane % 4;   // the first lanes load the weights' scales: block, which one
             const auto row_of = [&](int j) { return by_rows ? j * (32 / kScaleBlocks) + lane / kScaleBlocks : j * 32 % S::kRows + lane; };
             const auto block_of = [&](int j) { return by_rows ? lane % kScaleBlocks : j * 32 / S::kRows; };
-            for (int64_t i = pair_id; i < items; i += pairs) {
+            for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
                 const Tile it = tile_at(a.g, plan, table, i);
                 const bool lanes = LANES && it.rows > COLS;
-                const int skip = lanes ? rank * 128 : 0, rows = it.rows - skip;
-                int o;
-                if (!lanes) o = scale_row(it.m, min(wj, kScaleSets - 1));
-                else if (SWIGLU) o = ((wj < 2 ? 0 : cols) + it.m * 128 + wj % 2 * 64) / kBlock;
-                else o = it.m * 2 + wj / 2;
-                const float* w_scales = a.w_scales + (static_cast<int64_t>(it.expert) * scale_rows + min(o, scale_rows - 1)) * blocks;
+                const int o = lanes ? weight_row(it.m, wj / 2) + wj % 2 * 64 : wj == 0 ? weight_row(it.m, 0) : weight_row(it.m, 1) + (wj - 1) * 128;
+                const float* w_scales = a.w_scales + (static_cast<int64_t>(it.expert) * scale_rows + min(o / kBlock, scale_rows - 1)) * blocks;
                 for (int b = 0; b < blocks; b += kScaleBlocks) {
                     if (turn == 0) {
                         float v[kEach];
@@ -521,25 +489,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int j = 0; j < kEach; ++j) {
                             const int n = row_of(j), k = block_of(j);
                             v[j] = 0.0f;
-                            if (n < rows && b + k < blocks) {
-                                const int64_t from = (static_cast<int64_t>(it.row) + skip + n) * a.x_scale_row + (b + k) * a.x_scale_block;
+                            if (n < it.rows && b + k < blocks) {
+                                const int64_t from = (static_cast<int64_t>(it.row) + n) * a.x_scale_row + (b + k) * a.x_scale_block;
                                 v[j] = a.x_ue8m0 ? ue8m0(static_cast<const uint8_t*>(a.x_scales)[from]) : static_cast<const float*>(a.x_scales)[from];
                             }
                         }
                         const float w = w_scales[min(b + wk, blocks - 1)];
                         barrier_wait_inline(scales_empty + 8 * slot, parity, dead);
                         float* to = scales + slot * (kScaleBlocks * S::kScaleStep);
-                        if (lanes && lane < 4 * kScaleBlocks) to[wk * S::kScaleStep + 128 + wj] = w;
+                        if (lane < 4 * kScaleBlocks) to[wk * S::kScaleStep + S::kRows + wj] = w;
 #pragma unroll
-                        for (int s = 0; s < kScaleSets; ++s) {
-                            if (s >= (lanes ? 1 : sets)) continue;
-#pragma unroll
-                            for (int j = 0; j < kEach; ++j) {
-                                const int n = row_of(j), k = block_of(j);
-                                const float factor = __shfl_sync(kFullMask, w, k * 4 + s);
-                                if (lanes || n < COLS) to[k * S::kScaleStep + s * COLS + n] = lanes ? v[j] : v[j] * factor;
-                            }
-                        }
+                        for (int j = 0; j < kEach; ++j) to[block_of(j) * S::kScaleStep + row_of(j)] = v[j];
                         __syncwarp();
                         if (lane == 0) barrier_arrive(scales_full + 8 * slot);
                     }
@@ -551,10 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tmem_fence_before();
     __syncthreads();
-    cluster_sync();   // (neither CTA leaves while the other may arrive on its barriers)
     if (warp == kLoader) {
         tmem_fence_after();
-        tmem_free_all(tmem);
+        tmem_free_one(tmem);
     }
 }
 
@@ -562,28 +521,26 @@ template <int COLS, bool LANES, bool SWIGLU>
 cudaError_t launch_shape(const Fp8Args& a, cudaStream_t stream) {
     using S = Shape<COLS, LANES>;
     static int known[64];
-    int pairs = 0;
-    cudaError_t err = pairs_at_once(expert_fp8_kernel<COLS, LANES, SWIGLU>, kThreads, S::kShared, known, &pairs);
+    int sms = 0;
+    cudaError_t err = prepare_persistent(expert_fp8_kernel<COLS, LANES, SWIGLU>, S::kShared, known, &sms);
     if (err != cudaSuccess) return err;
     const int64_t I = a.I, O = a.O, E = a.g.E;
     const int cols = SWIGLU ? a.O / 2 : a.O;
     TilePlan p{};
-    p.cap = LANES ? 256 : COLS;
+    p.cap = S::kRows;
     p.whole = LANES;
     p.chunk = 16;
     p.m_tiles = ceil_div(cols, SWIGLU ? kTileRows / 2 : kTileRows);
     while (((a.g.E - 1) >> p.shift) + 1 > kTileTable) ++p.shift;
-    CUtensorMap w_map, w_half_map, x_map;
-    err = SWIGLU ? box_map(&w_map, a.w, EP_DTYPE_FP8_E4M3, I, cols, 2, E, I, I * cols, I * O, 16, 2)
-                 : box_map(&w_map, a.w, EP_DTYPE_FP8_E4M3, I, O, 1, E, I, I * O, I * O, 128, 1);
-    w_half_map = w_map;
-    if (SWIGLU && LANES && err == cudaSuccess) err = box_map(&w_half_map, a.w, EP_DTYPE_FP8_E4M3, I, cols, 2, E, I, I * cols, I * O, 128, 1);
+    CUtensorMap w_map, x_map;
+    err = SWIGLU ? box_map(&w_map, a.w, EP_DTYPE_FP8_E4M3, I, cols, 2, E, I, I * cols, I * O, 128, 2)
+                 : box_map(&w_map, a.w, EP_DTYPE_FP8_E4M3, I, O, 1, E, I, I * O, I * O, kTileRows, 1);
     if (err == cudaSuccess) err = box_map(&x_map, a.x, EP_DTYPE_FP8_E4M3, I, a.g.rows, 1, 1, a.x_ld, a.x_ld, a.x_ld, S::kBox, 1);
     if (err != cudaSuccess) return err;
     const int64_t used = a.g.rows < a.g.E ? a.g.rows : a.g.E;
     const int64_t most = (a.g.rows + used * (p.cap - 1)) / p.cap * p.m_tiles;
-    return launch_pairs(expert_fp8_kernel<COLS, LANES, SWIGLU>, static_cast<int>(most < pairs ? most : pairs), kThreads, S::kShared,
-                        stream, a, p, w_map, w_half_map, x_map);
+    return launch_dependent(expert_fp8_kernel<COLS, LANES, SWIGLU>, dim3(static_cast<unsigned>(most < sms ? most : sms)), dim3(kThreads),
+                            S::kShared, stream, a, p, w_map, x_map);
 }
 
 template <bool SWIGLU>

@@ -108,6 +108,20 @@ __device__ __forceinline__ Tile tile_at(const ExpertRows& g, const TilePlan& p, 
 // Columns of the product for n rows of a tile.
 __device__ __forceinline__ int columns_of(int n) { return max((n + 15) / 16 * 16, 16); }
 
+__device__ __forceinline__ void tmem_alloc_one(uint32_t to) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(to) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_one(uint32_t tmem) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+// sums [128 lanes][N] (+)= A [128 lanes] * B [N columns]^T, 8-bit operands in shared memory.
+__device__ __forceinline__ void multiply_one(uint32_t sums, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(sums),
+                 "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+                 : "memory");
+}
+
 // ---- pairs: two CTAs of a cluster multiply as one, operand A's 256 rows and operand B's columns half in each. The first
 // issues for both; each has the sums of its own 128 rows in its TMEM.
 
@@ -191,16 +205,10 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t* r) {
         : "r"(at));
 }
 // sums [2 x 128 lanes][N] (+)= A [2 x 128 lanes] * B [2 x N / 2 columns]^T, all in the pair's shared memory.
-template <bool FP8>
 __device__ __forceinline__ void multiply_pair(uint32_t sums, uint64_t a, uint64_t b, uint32_t shape, bool add) {
-    if constexpr (FP8)
-        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(sums),
-                     "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
-                     : "memory");
-    else
-        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(sums),
-                     "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
-                     : "memory");
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(sums), "l"(a),
+                 "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+                 : "memory");
 }
 // Arrives on both CTAs' barriers at this place once the products so far are done.
 __device__ __forceinline__ void pair_done(uint32_t bar) {
@@ -247,6 +255,21 @@ cudaError_t box_map(CUtensorMap* map, const void* base, int dtype, int64_t x, in
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
                : cudaErrorInvalidValue;
+}
+
+// SMs of the current device, with the kernel's shared memory limit raised: looked up once per device (a race writes
+// the same value).
+template <typename Kernel>
+cudaError_t prepare_persistent(Kernel kernel, int smem, int* known, int* sms) {
+    constexpr int kDevices = 64;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < kDevices && (*sms = __atomic_load_n(&known[dev], __ATOMIC_ACQUIRE)) > 0) return cudaSuccess;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err == cudaSuccess && dev < kDevices) __atomic_store_n(&known[dev], *sms, __ATOMIC_RELEASE);
+    return err;
 }
 
 // Pairs of CTAs of a kernel that the current device holds at once, with the kernel's shared memory limit raised: looked up

@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             fetch(0);
+            buffer = (buffer + 1) & 2;   // an even one and the next
             for (int b = 0; b < blocks; ++b) {
-                buffer = (buffer + 1) & 2;   // an even one and the next
                 barrier_wait_inline(sums_full + 8 * buffer, (parities >> buffer) & 1, dead);
                 tmem_fence_after();
                 const uint32_t at = mine + buffer * 128 + h * 64;
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 parities ^= 1u << buffer;
-                buffer = (buffer + 2) % kBuffers;
+                buffer ^= 2;
             }
             if (*dead) {
 #pragma unroll
@@ -407,43 +407,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         if constexpr (S::kMoved) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        // (the loader and the issuer are one thread each: the compiler knows it behind elect.sync, and waits cost it less)
         if (warp == kLoader) {
-            int slot = 0;
-            uint32_t parity = 1;   // (the first round of the ring waits for nothing)
-            for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-                const Tile it = tile_at(a.g, plan, table, i);
-                const int x_boxes = (max(it.rows, 1) + S::kBox - 1) / S::kBox;
-                for (int b = 0; b < blocks; ++b) {
-                    const uint32_t bar = full + 8 * slot, at_w = smem_addr(ring) + slot * S::kStageBytes, at_x = at_w + kWBytes;
-                    barrier_wait_inline(empty + 8 * slot, parity, dead);
-                    if (lane == 0) barrier_expect(bar, kWBytes + x_boxes * S::kBox * kBlock);
-                    __syncwarp();
-                    if (lane == 0) load_box(at_w, &w_map, b * kBlock, SWIGLU ? it.m * 128 : it.m * kTileRows, 0, it.expert, bar);
-                    else if (lane <= x_boxes)
-                        load_box(at_x + (lane - 1) * S::kBox * kBlock, &x_map, b * kBlock, it.row + (lane - 1) * S::kBox, 0, 0, bar);
-                    if (++slot == S::kStages) slot = 0, parity ^= 1;
+            if (leader) {
+                int slot = 0;
+                uint32_t parity = 1;   // (the first round of the ring waits for nothing)
+                for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+                    const Tile it = tile_at(a.g, plan, table, i);
+                    const int x_boxes = (max(it.rows, 1) + S::kBox - 1) / S::kBox;
+                    for (int b = 0; b < blocks; ++b) {
+                        const uint32_t bar = full + 8 * slot, at_w = smem_addr(ring) + slot * S::kStageBytes, at_x = at_w + kWBytes;
+                        barrier_wait_inline(empty + 8 * slot, parity, dead);
+                        barrier_expect(bar, kWBytes + x_boxes * S::kBox * kBlock);
+                        load_box(at_w, &w_map, b * kBlock, SWIGLU ? it.m * 128 : it.m * kTileRows, 0, it.expert, bar);
+                        for (int j = 0; j < x_boxes; ++j)
+                            load_box(at_x + j * S::kBox * kBlock, &x_map, b * kBlock, it.row + j * S::kBox, 0, 0, bar);
+                        if (++slot == S::kStages) slot = 0, parity ^= 1;
+                    }
                 }
             }
+            __syncwarp();
         } else if (warp == kIssuer) {
-            const uint32_t e5m2 = a.x_dtype == EP_DTYPE_FP8_E5M2 ? 1u : 0u;
-            const uint32_t base = (1u << 4) | (128u / 16 << 24);   // fp32 sums, 128 lanes
-            int slot = 0, buffer = 0;
-            uint32_t parity = 0, parities = 15;   // parities: a bit for each buffer of sums
-            for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-                const Tile it = tile_at(a.g, plan, table, i);
-                const bool lanes = LANES && it.rows > COLS;
-                const uint32_t shape = base | (lanes ? e5m2 << 7 : e5m2 << 10) | static_cast<uint32_t>((lanes ? 256 : columns_of(it.rows)) / 8) << 17;
-                for (int b = 0; b < blocks; ++b) {
-                    barrier_wait_inline(full + 8 * slot, parity, dead);
-                    if (lanes) {
-                        buffer = (buffer + 1) & 2;   // an even one and the next
-                        barrier_wait_inline(sums_empty + 8 * buffer + 8, (parities >> (buffer + 1)) & 1, dead);
-                        parities ^= 2u << buffer;
-                    }
-                    barrier_wait_inline(sums_empty + 8 * buffer, (parities >> buffer) & 1, dead);
-                    parities ^= 1u << buffer;
-                    tmem_fence_after();
-                    if (leader) {
+            if (leader) {
+                const uint32_t e5m2 = a.x_dtype == EP_DTYPE_FP8_E5M2 ? 1u : 0u;
+                const uint32_t base = (1u << 4) | (128u / 16 << 24);   // fp32 sums, 128 lanes
+                int slot = 0, buffer = 0;
+                uint32_t parity = 0, parities = 15;   // parities: a bit for each buffer of sums
+                for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+                    const Tile it = tile_at(a.g, plan, table, i);
+                    const bool lanes = LANES && it.rows > COLS;
+                    const uint32_t shape = base | (lanes ? e5m2 << 7 : e5m2 << 10) | static_cast<uint32_t>((lanes ? 256 : columns_of(it.rows)) / 8) << 17;
+                    for (int b = 0; b < blocks; ++b) {
+                        if (lanes) {
+                            buffer = (buffer + 1) & 2;   // an even one and the next
+                            barrier_wait_inline(sums_empty + 8 * buffer + 8, (parities >> (buffer + 1)) & 1, dead);
+                            parities ^= 2u << buffer;
+                        }
+                        barrier_wait_inline(sums_empty + 8 * buffer, (parities >> buffer) & 1, dead);
+                        parities ^= 1u << buffer;
+                        barrier_wait_inline(full + 8 * slot, parity, dead);
+                        tmem_fence_after();
                         const uint32_t at_w = smem_addr(ring) + slot * S::kStageBytes;
                         const uint64_t dw = operand(at_w, 1024), dx = operand(at_w + kWBytes, 1024);
                         const uint32_t sums = tmem + buffer * 128;
@@ -457,14 +460,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int k = 0; k < kBlock / 32; ++k)
                                     multiply_one(sums + half * 64, dw + half * (128 * kBlock / 16) + k * 2, dx + k * 2, shape, k > 0);
                         }
-                        multiply_done(empty + 8 * slot);
                         multiply_done(sums_full + 8 * buffer);
+                        multiply_done(empty + 8 * slot);
+                        if (++slot == S::kStages) slot = 0, parity ^= 1;
+                        buffer = (buffer + (lanes ? 2 : 1)) % kBuffers;
                     }
-                    __syncwarp();
-                    if (++slot == S::kStages) slot = 0, parity ^= 1;
-                    buffer = (buffer + (lanes ? 2 : 1)) % kBuffers;
                 }
             }
+            __syncwarp();
         } else if (warp >= kScaler) {
             // The rows' scales for some blocks at a time, the two warps in turn, and behind them the weights' (rows as columns:
             // the first half's, the second half's one or two; rows as lanes: of 64 weight rows each). Lanes run along what is

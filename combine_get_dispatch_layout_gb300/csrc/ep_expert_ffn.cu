@@ -14,8 +14,8 @@ namespace ep {
 namespace {
 
 constexpr int kEpilogueWarps = 8;
-constexpr int kLoader = kEpilogueWarps, kIssuer = kLoader + 1;
-constexpr int kThreads = 32 * (kEpilogueWarps + 2);
+constexpr int kLoader = kEpilogueWarps, kIssuer = kLoader + 1, kCleaner = kLoader + 2;   // warps
+constexpr int kThreads = 32 * (kEpilogueWarps + 3);
 constexpr int kLanes = 256;                     // of a pair: 128 in each CTA's TMEM
 constexpr int kStep = 64;                       // contraction of a stage: 128 bytes
 constexpr int kABytes = kLanes / 2 * kStep * 2;
@@ -48,12 +48,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned char* const ring = shared_bytes + (1024 - smem_addr(shared_bytes) % 1024) % 1024;
     uint64_t* const barriers = reinterpret_cast<uint64_t*>(ring + kRing);
     const uint32_t full = smem_addr(barriers), empty = full + 8 * kMostStages;
-    const uint32_t other_full = empty + 8 * kMostStages;   // kGradW, an expert's last rows: the second CTA's half is ready
-    const uint32_t sums_full = other_full + 8 * kMostStages, sums_empty = sums_full + 16;
+    // kGradW, an expert's last rows: a CTA's half is there, both are clean
+    const uint32_t part_full = empty + 8 * kMostStages, clean = part_full + 8 * kMostStages;
+    const uint32_t sums_full = clean + 8 * kMostStages, sums_empty = sums_full + 16;
     uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(barriers) + 120;
     volatile int* const dead = reinterpret_cast<volatile int*>(tmem_at + 1);
     int* const table = reinterpret_cast<int*>(barriers) + 128;
-    static_assert((3 * kMostStages + 4) * 2 <= 120, "");
+    static_assert((4 * kMostStages + 4) * 2 <= 120, "");
     __shared__ int warp_sum[kThreads / 32];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = pair_rank();
@@ -64,7 +65,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < a.stages; ++i) {
                 barrier_init(full + 8 * i, 1);
                 barrier_init(empty + 8 * i, 1);
-                barrier_init(other_full + 8 * i, 1);
+                barrier_init(part_full + 8 * i, 1);
+                barrier_init(clean + 8 * i, 2);
             }
             for (int i = 0; i < 2; ++i) {
                 barrier_init(sums_full + 8 * i, 1);
@@ -111,101 +113,123 @@ __global__ void __launch_bounds__(kThreads, 1)
         return r;
     };
 
+    // kGradW: whether a stage has rows of others among the 16 of a product behind the expert's last, and zeros are wanted there.
+    const auto unclean = [&](const Item& it, int s) { return WHAT == kGradW && it.rows - s * kStep < kStep && it.rows % 16 != 0; };
+
+    // (the loader and the issuer are one thread each: the compiler knows it behind elect.sync, and waits cost it less)
     if (warp == kLoader) {
-        int slot = 0;
-        uint32_t parity = 1;   // (the first round of the ring waits for nothing)
-        for (int64_t i = pair; i < items; i += pairs) {
-            const Item it = decode(i);
-            const int a_boxes = WHAT == kGateUp ? 4 : WHAT == kDown ? 1 : 2;
-            const int half = columns_of(it.cols) / 2;   // columns of each CTA
-            const int b_boxes = WHAT == kGradW ? (half + 63) / 64 : (half + a.box - 1) / a.box;
-            const int lane0 = it.m * kLanes + rank * (kLanes / 2), col0 = it.col + rank * half;
-            for (int s = 0; s < it.steps; ++s) {
-                // both CTAs' boxes count on the first one's barrier
-                const uint32_t bar = in_first(full + 8 * slot), at_a = smem_addr(ring) + slot * a.stage_bytes, at_b = at_a + kABytes;
-                barrier_wait(empty + 8 * slot, parity, dead);
-                if constexpr (WHAT == kGradW) {
-                    // [64 channels] x [box rows] of both operands, boxes with real rows only
-                    // (a stage with rows of others behind the expert's is the second CTA's own until it has cleared them)
-                    const bool part = it.rows - s * kStep < kStep;
-                    const uint32_t to = part ? full + 8 * slot : bar;
-                    const int down = (min(kStep, it.rows - s * kStep) + a.box - 1) / a.box, all = (2 + b_boxes) * down;
-                    if (lane == 0 && (rank == 0 || part)) barrier_expect(full + 8 * slot, all * a.box * 128 * (part ? 1 : 2));
-                    __syncwarp();
-                    if (lane < all) {
-                        const int k = lane % down, j = lane / down, row = it.row + s * kStep + k * a.box;
-                        if (j < 2) load_box_pair(at_a + j * 8192 + k * a.box * 128, &a_map, lane0 + j * 64, row, 0, 0, to);
-                        else load_box_pair(at_b + (j - 2) * 8192 + k * a.box * 128, &b_map, col0 + (j - 2) * 64, row, 0, 0, to);
-                    }
-                } else {
-                    if (lane == 0 && rank == 0) barrier_expect(full + 8 * slot, 2 * (kABytes + b_boxes * a.box * 128));
-                    __syncwarp();
-                    if (lane < a_boxes) {
-                        if (WHAT == kGateUp)   // the 16 gate and the 16 up rows of a warp
-                            load_box_pair(at_a + lane * 4096, &a_map, s * kStep, lane0 / 2 + lane * 16, 0, it.expert, bar);
-                        else if (WHAT == kDown)
+        if (leader) {
+            int slot = 0;
+            uint32_t parity = 1;   // (the first round of the ring waits for nothing)
+            for (int64_t i = pair; i < items; i += pairs) {
+                const Item it = decode(i);
+                const int half = columns_of(it.cols) / 2;   // columns of each CTA
+                const int b_boxes = WHAT == kGradW ? (half + 63) / 64 : (half + a.box - 1) / a.box;
+                const int lane0 = it.m * kLanes + rank * (kLanes / 2), col0 = it.col + rank * half;
+                for (int s = 0; s < it.steps; ++s) {
+                    // both CTAs' boxes count on the first one's barrier
+                    const uint32_t mine = full + 8 * slot, at_a = smem_addr(ring) + slot * a.stage_bytes, at_b = at_a + kABytes;
+                    const uint32_t bar = in_first(mine);
+                    barrier_wait_inline(empty + 8 * slot, parity, dead);
+                    if constexpr (WHAT == kGradW) {
+                        // [64 channels] x [box rows] of both operands, boxes with real rows only
+                        // (a stage that has to be cleaned first counts on a barrier of each CTA's own)
+                        const bool own = unclean(it, s);
+                        const uint32_t to = own ? part_full + 8 * slot : bar;
+                        const int down = (min(kStep, it.rows - s * kStep) + a.box - 1) / a.box, all = (2 + b_boxes) * down;
+                        if (rank == 0 || own) barrier_expect(own ? to : mine, all * a.box * 128 * (own ? 1 : 2));
+                        for (int k = 0; k < down; ++k) {
+                            const int row = it.row + s * kStep + k * a.box, at = k * a.box * 128;
+                            for (int j = 0; j < 2; ++j) load_box_pair(at_a + j * 8192 + at, &a_map, lane0 + j * 64, row, 0, 0, to);
+                            for (int j = 0; j < b_boxes; ++j) load_box_pair(at_b + j * 8192 + at, &b_map, col0 + j * 64, row, 0, 0, to);
+                        }
+                    } else {
+                        if (rank == 0) barrier_expect(mine, 2 * (kABytes + b_boxes * a.box * 128));
+                        if constexpr (WHAT == kGateUp) {   // the 16 gate and the 16 up rows of each warp
+                            for (int j = 0; j < 4; ++j)
+                                load_box_pair(at_a + j * 4096, &a_map, s * kStep, lane0 / 2 + j * 16, 0, it.expert, bar);
+                        } else if constexpr (WHAT == kDown) {
                             load_box_pair(at_a, &a_map, s * kStep, lane0, 0, it.expert, bar);
-                        else
-                            load_box_pair(at_a + lane * 8192, &a_map, lane0 + lane * 64, s * kStep, 0, it.expert, bar);
-                    } else if (lane < a_boxes + b_boxes) {
-                        const int j = lane - a_boxes;
-                        load_box_pair(at_b + j * a.box * 128, &b_map, s * kStep, col0 + j * a.box, 0, 0, bar);
+                        } else {
+                            for (int j = 0; j < 2; ++j)
+                                load_box_pair(at_a + j * 8192, &a_map, lane0 + j * 64, s * kStep, 0, it.expert, bar);
+                        }
+                        for (int j = 0; j < b_boxes; ++j)
+                            load_box_pair(at_b + j * a.box * 128, &b_map, s * kStep, col0 + j * a.box, 0, 0, bar);
                     }
+                    if (++slot == a.stages) slot = 0, parity ^= 1;
                 }
-                if (++slot == a.stages) slot = 0, parity ^= 1;
             }
         }
+        __syncwarp();
     } else if (warp == kIssuer) {
-        // fp32 sums; operands' type; A outward, B outward; 256 lanes
-        constexpr uint32_t kType = std::is_same_v<T, __nv_bfloat16> ? 1u : 0u;
-        constexpr bool kAOut = WHAT >= kGradAct, kBOut = WHAT == kGradW;
-        constexpr uint32_t kShape = (1u << 4) | (kType << 7) | (kType << 10) | (kAOut ? 1u << 15 : 0u) | (kBOut ? 1u << 16 : 0u) |
-                                    (static_cast<uint32_t>(kLanes / 16) << 24);
-        int slot = 0, buffer = 0;
-        uint32_t parity = 0, sums_parity = 1, part_parity = 0;   // part_parity: a bit for each slot
-        // (the second CTA's warp has only the last stages of kGradW to see to)
-        for (int64_t i = pair; i < items && (rank == 0 || WHAT == kGradW); i += pairs) {
-            const Item it = decode(i);
-            if (it.steps == 0) continue;
-            const uint32_t shape = kShape | static_cast<uint32_t>(columns_of(it.cols) / 8) << 17;
-            const uint32_t sums = tmem + buffer * 256;
-            if (rank == 0) barrier_wait(sums_empty + 8 * buffer, sums_parity, dead);
-            for (int s = 0; s < it.steps; ++s) {
-                const uint32_t at_a = smem_addr(ring) + slot * a.stage_bytes, at_b = at_a + kABytes;
-                int depth = kStep / 16;   // products of 16
-                if (rank == 0) barrier_wait(full + 8 * slot, parity, dead);
-                if constexpr (WHAT == kGradW) {
-                    const int left = it.rows - s * kStep;
-                    if (left < kStep) {   // rows behind the expert's last belong to others: zeros instead, in both operands
-                        if (rank == 1) barrier_wait(full + 8 * slot, (part_parity >> slot) & 1, dead);
-                        depth = (left + 15) / 16;
-                        const int blocks = 2 + (columns_of(it.cols) / 2 + 63) / 64;
-                        for (int j = lane; j < (depth * 16 - left) * blocks * 8; j += 32) {
-                            const int line = j / 8, row = left + line / blocks;
-                            *reinterpret_cast<uint4*>(ring + slot * a.stage_bytes + line % blocks * 8192 + row * 128 + j % 8 * 16) =
+        if (leader && rank == 0) {   // (it issues for both CTAs)
+            // fp32 sums; operands' type; A outward, B outward; 256 lanes
+            constexpr uint32_t kType = std::is_same_v<T, __nv_bfloat16> ? 1u : 0u;
+            constexpr bool kAOut = WHAT >= kGradAct, kBOut = WHAT == kGradW;
+            constexpr uint32_t kShape = (1u << 4) | (kType << 7) | (kType << 10) | (kAOut ? 1u << 15 : 0u) | (kBOut ? 1u << 16 : 0u) |
+                                        (static_cast<uint32_t>(kLanes / 16) << 24);
+            int slot = 0, buffer = 0;
+            uint32_t parities = 0, sums_parity = 1, clean_parity = 0;   // parities, clean_parity: a bit for each slot
+            for (int64_t i = pair; i < items; i += pairs) {
+                const Item it = decode(i);
+                if (it.steps == 0) continue;
+                const uint32_t shape = kShape | static_cast<uint32_t>(columns_of(it.cols) / 8) << 17;
+                const uint32_t sums = tmem + buffer * 256;
+                barrier_wait_inline(sums_empty + 8 * buffer, sums_parity, dead);
+                for (int s = 0; s < it.steps; ++s) {
+                    const uint32_t at_a = smem_addr(ring) + slot * a.stage_bytes, at_b = at_a + kABytes;
+                    const uint64_t da = kAOut ? operand_outward(at_a, 8192) : operand(at_a, 1024);
+                    const uint64_t db = kBOut ? operand_outward(at_b, 8192) : operand(at_b, 1024);
+                    if (unclean(it, s)) {
+                        barrier_wait_cluster(clean + 8 * slot, (clean_parity >> slot) & 1, dead);
+                        clean_parity ^= 1u << slot;
+                    } else {
+                        barrier_wait_inline(full + 8 * slot, (parities >> slot) & 1, dead);
+                        parities ^= 1u << slot;
+                    }
+                    tmem_fence_after();
+                    const int depth = WHAT == kGradW ? min((it.rows - s * kStep + 15) / 16, kStep / 16) : kStep / 16;   // products of 16
+                    if (WHAT != kGradW || depth == kStep / 16) {
+#pragma unroll
+                        for (int k = 0; k < kStep / 16; ++k)
+                            multiply_pair(sums, da + k * (kAOut ? 128 : 2), db + k * (kBOut ? 128 : 2), shape, s > 0 || k > 0);
+                    } else {
+                        for (int k = 0; k < depth; ++k) multiply_pair(sums, da + k * 128, db + k * 128, shape, s > 0 || k > 0);
+                    }
+                    pair_done(empty + 8 * slot);
+                    if (s + 1 == it.steps) pair_done(sums_full + 8 * buffer);
+                    if (++slot == a.stages) slot = 0;
+                }
+                buffer ^= 1;
+                if (buffer == 0) sums_parity ^= 1;
+            }
+        }
+        __syncwarp();
+    } else if (warp == kCleaner) {
+        // Rows behind an expert's last belong to others: zeros instead, in both operands, some stages before their product.
+        if constexpr (WHAT == kGradW) {
+            int slot = 0;
+            uint32_t parities = 0;   // a bit for each slot
+            for (int64_t i = pair; i < items; i += pairs) {
+                const Item it = decode(i);
+                for (int s = 0; s < it.steps; ++s) {
+                    if (unclean(it, s)) {
+                        barrier_wait_inline(part_full + 8 * slot, (parities >> slot) & 1, dead);
+                        parities ^= 1u << slot;
+                        const int left = it.rows - s * kStep, end = (left + 15) / 16 * 16, lines = 2 + (columns_of(it.cols) / 2 + 63) / 64;
+                        for (int j = lane; j < (end - left) * lines * 8; j += 32) {
+                            const int line = j / 8, row = left + line / lines;
+                            *reinterpret_cast<uint4*>(ring + slot * a.stage_bytes + line % lines * 8192 + row * 128 + j % 8 * 16) =
                                 make_uint4(0, 0, 0, 0);
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
-                        if (rank == 1 && lane == 0) barrier_arrive_cluster(in_first(other_full + 8 * slot));
-                        if (rank == 0) barrier_wait_cluster(other_full + 8 * slot, (part_parity >> slot) & 1, dead);
-                        part_parity ^= 1u << slot;
+                        if (lane == 0) barrier_arrive_cluster(in_first(clean + 8 * slot));
                     }
+                    if (++slot == a.stages) slot = 0;
                 }
-                tmem_fence_after();
-                if (rank == 0 && leader) {
-                    const uint64_t da = kAOut ? operand_outward(at_a, 8192) : operand(at_a, 1024);
-                    const uint64_t db = kBOut ? operand_outward(at_b, 8192) : operand(at_b, 1024);
-                    for (int k = 0; k < depth; ++k)
-                        multiply_pair(sums, da + k * (kAOut ? 128 : 2), db + k * (kBOut ? 128 : 2), shape, s > 0 || k > 0);
-                    pair_done(empty + 8 * slot);
-                    if (s + 1 == it.steps) pair_done(sums_full + 8 * buffer);
-                }
-                __syncwarp();
-                if (++slot == a.stages) slot = 0, parity ^= 1;
             }
-            buffer ^= 1;
-            if (buffer == 0) sums_parity ^= 1;
         }
     } else {
         const int half = warp >> 2;

@@ -20,8 +20,13 @@ constexpr int kLanes = 256;                     // of a pair: 128 in each CTA's 
 constexpr int kStep = 64;                       // contraction of a stage: 128 bytes
 constexpr int kABytes = kLanes / 2 * kStep * 2;
 constexpr int kMostStages = 10;
-constexpr int kRing = 192 * 1024 + 8 * 1024;
-constexpr int kShared = 1024 + kRing + 512 + (kTileTable + 1) * 4;
+constexpr int kRing = 192 * 1024;
+// Outputs leave through shared memory: chunks of kChunk rows of 128 channels (gate and up of 64), of which two fit for each
+// half of the epilogue's warps, and for the activation rows of 64 channels, apart so that two rows lie in other banks.
+constexpr int kChunk = 16;
+constexpr int kRowBytes = 256, kActBytes = 160;
+constexpr int kOutBytes = 2 * kChunk * kRowBytes, kHalfBytes = kOutBytes + 2 * kChunk * kActBytes;
+constexpr int kShared = 1024 + kRing + 2 * kHalfBytes + 512 + (kTileTable + 1) * 4;
 static_assert(kShared <= 227 * 1024 - 256, "");
 
 enum Product { kGateUp, kDown, kGradAct, kGradX, kGradW };
@@ -46,7 +51,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     expert_gemm_kernel(Gemm a, const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map) {
     extern __shared__ unsigned char shared_bytes[];
     unsigned char* const ring = shared_bytes + (1024 - smem_addr(shared_bytes) % 1024) % 1024;
-    uint64_t* const barriers = reinterpret_cast<uint64_t*>(ring + kRing);
+    uint64_t* const barriers = reinterpret_cast<uint64_t*>(ring + kRing + 2 * kHalfBytes);
     const uint32_t full = smem_addr(barriers), empty = full + 8 * kMostStages;
     // kGradW, an expert's last rows: a CTA's half is there, both are clean
     const uint32_t part_full = empty + 8 * kMostStages, clean = part_full + 8 * kMostStages;
@@ -232,72 +237,44 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        const int half = warp >> 2;
-        int buffer = 0;
+        const int half = warp >> 2, part = warp & 3;   // of the chunks of columns; of the lanes
+        unsigned char* const out = ring + kRing + half * kHalfBytes;
+        unsigned char* const act_out = out + kOutBytes;
+        const auto half_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); };
+        const bool staged = WHAT != kGradW || !(a.out_fp32 || a.accumulate);
+        int buffer = 0, chunk = 0;
         uint32_t parity = 0;
         for (int64_t i = pair; i < items; i += pairs) {
             const Item it = decode(i);
-            const uint32_t mine = tmem + buffer * 256 + (static_cast<uint32_t>(warp & 3) << 21);   // lane 32 * (warp % 4), upper half
+            const uint32_t mine = tmem + buffer * 256 + (static_cast<uint32_t>(part) << 21);   // lane 32 * part, upper half
             if (it.steps > 0) {
                 barrier_wait(sums_full + 8 * buffer, parity, dead);
                 tmem_fence_after();
             }
-            // this thread's channel; of gate and up a warp's lanes are 16 gate and 16 up rows
-            const int lane0 = it.m * kLanes + rank * (kLanes / 2) + (warp & 3) * 32;
-            const int chan = WHAT == kGateUp ? lane0 / 2 + (lane & 15) : lane0 + lane;
+            // the CTA's first channel, this thread's; of gate and up a warp's lanes are 16 gate and 16 up rows
+            const int tile = it.m * kLanes + rank * (kLanes / 2), chan0 = WHAT == kGateUp ? tile / 2 : tile;
+            const int chan = WHAT == kGateUp ? chan0 + part * 16 + (lane & 15) : chan0 + part * 32 + lane;
             const bool real = chan < a.lanes;
-            for (int c0 = half * 32; c0 < it.cols; c0 += 64) {
-                uint32_t raw[32];
+            const int bytes = min(WHAT == kGateUp ? 64 : 128, a.lanes - chan0) * 2;   // of a row of this CTA (a multiple of 16)
+            for (int c0 = half * kChunk; c0 < it.cols; c0 += 2 * kChunk, ++chunk) {
+                uint32_t raw[kChunk];
                 if (it.steps > 0) {
-                    tmem_load32(mine + c0, raw);
+                    tmem_load16(mine + c0, raw);
                     tmem_loaded(raw);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) raw[j] = 0;
+                    for (int j = 0; j < kChunk; ++j) raw[j] = 0;
                 }
                 if (*dead) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) raw[j] = 0x7fffffff;
+                    for (int j = 0; j < kChunk; ++j) raw[j] = 0x7fffffff;
                 }
-                const int many = min(32, it.cols - c0);
-                if constexpr (WHAT == kGateUp) {
-                    const int64_t row = it.row + c0;
-                    if (a.out2 && real) {
-                        T* to = static_cast<T*>(a.out2) + row * a.out2_ld + (lane < 16 ? chan : a.lanes + chan);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < many) to[j * a.out2_ld] = from_float<T>(__uint_as_float(raw[j]));
-                    }
-                    T* to = static_cast<T*>(a.out) + (row + (lane >> 4)) * a.out_ld + chan;
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {   // gate lanes take the even columns, up lanes the odd ones
-                        const float own = __uint_as_float(lane < 16 ? raw[j] : raw[j + 1]);
-                        const float got = __uint_as_float(__shfl_xor_sync(kFullMask, lane < 16 ? raw[j + 1] : raw[j], 16));
-                        const float act = lane < 16 ? silu(own) * got : silu(got) * own;
-                        if (real && j + (lane >> 4) < many) to[j * a.out_ld] = from_float<T>(act);
-                    }
-                } else if constexpr (WHAT == kGradAct) {
-                    if (real) {
-                        const int64_t row = it.row + c0;
-                        const T* from = static_cast<const T*>(a.in) + row * a.in_ld + chan;
-                        T* to = static_cast<T*>(a.out) + row * a.out_ld + chan;
-                        T gate[32], up[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < many) gate[j] = from[j * a.in_ld], up[j] = from[j * a.in_ld + a.lanes];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < many) {
-                                const float d = __uint_as_float(raw[j]), gt = to_float(gate[j]), s = sigmoid(gt);
-                                to[j * a.out_ld] = from_float<T>(d * to_float(up[j]) * s * (1.0f + gt * (1.0f - s)));
-                                to[j * a.out_ld + a.lanes] = from_float<T>(d * gt * s);
-                            }
-                    }
-                } else if constexpr (WHAT == kGradW) {
+                const int many = min(kChunk, it.cols - c0);
+                if (WHAT == kGradW && !staged) {
                     if (real) {
                         const int64_t at = (static_cast<int64_t>(it.expert) * a.columns + it.col + c0) * a.out_ld + chan;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
+                        for (int j = 0; j < kChunk; ++j)
                             if (j < many) {
                                 float v = __uint_as_float(raw[j]);
                                 if (a.out_fp32) {
@@ -305,16 +282,77 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     *to = a.accumulate ? *to + v : v;
                                 } else {
                                     T* to = static_cast<T*>(a.out) + at + j * a.out_ld;
-                                    *to = from_float<T>(a.accumulate ? to_float(*to) + v : v);
+                                    *to = from_float<T>(to_float(*to) + v);
                                 }
                             }
                     }
-                } else if (real) {
-                    T* to = static_cast<T*>(a.out) + (static_cast<int64_t>(it.row) + c0) * a.out_ld + chan;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j < many) to[j * a.out_ld] = from_float<T>(__uint_as_float(raw[j]));
+                    continue;
                 }
+                const int64_t row0 = WHAT == kGradW ? static_cast<int64_t>(it.expert) * a.columns + it.col + c0 : static_cast<int64_t>(it.row) + c0;
+                T gate[kChunk], up[kChunk];
+                if (WHAT == kGradAct && real) {
+                    const T* from = static_cast<const T*>(a.in) + row0 * a.in_ld + chan;
+#pragma unroll
+                    for (int j = 0; j < kChunk; ++j)
+                        if (j < many) gate[j] = from[j * a.in_ld], up[j] = from[j * a.in_ld + a.lanes];
+                }
+                // the copies out of this chunk's place have been read (kGradAct has both places for its two outputs)
+                if (lane < 4) {
+                    if (WHAT == kGradAct) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                }
+                half_sync();
+                const int place = WHAT == kGradAct ? 0 : chunk & 1;
+                unsigned char* const to = out + place * (kChunk * kRowBytes);
+                unsigned char* const act_to = act_out + place * (kChunk * kActBytes);
+                if constexpr (WHAT == kGateUp) {
+                    if (a.out2) {
+                        T* at = reinterpret_cast<T*>(to + (lane < 16 ? 0 : 128)) + part * 16 + (lane & 15);
+#pragma unroll
+                        for (int j = 0; j < kChunk; ++j) at[j * (kRowBytes / 2)] = from_float<T>(__uint_as_float(raw[j]));
+                    }
+                    T* at = reinterpret_cast<T*>(act_to + (lane >> 4) * kActBytes) + part * 16 + (lane & 15);
+#pragma unroll
+                    for (int j = 0; j < kChunk; j += 2) {   // gate lanes take the even columns, up lanes the odd ones
+                        const float own = __uint_as_float(lane < 16 ? raw[j] : raw[j + 1]);
+                        const float got = __uint_as_float(__shfl_xor_sync(kFullMask, lane < 16 ? raw[j + 1] : raw[j], 16));
+                        at[j * (kActBytes / 2)] = from_float<T>(lane < 16 ? silu(own) * got : silu(got) * own);
+                    }
+                } else {
+                    T* at = reinterpret_cast<T*>(to) + part * 32 + lane;
+#pragma unroll
+                    for (int j = 0; j < kChunk; ++j) {
+                        const float d = __uint_as_float(raw[j]);
+                        if constexpr (WHAT == kGradAct) {
+                            const float gt = to_float(gate[j]), s = sigmoid(gt);
+                            at[j * (kRowBytes / 2)] = from_float<T>(d * to_float(up[j]) * s * (1.0f + gt * (1.0f - s)));
+                            at[(kChunk + j) * (kRowBytes / 2)] = from_float<T>(d * gt * s);
+                        } else {
+                            at[j * (kRowBytes / 2)] = from_float<T>(d);
+                        }
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                half_sync();
+                if (lane < 4) {   // a row each
+                    const int j = part * 4 + lane;
+                    if (j < many && bytes > 0) {
+                        T* at = static_cast<T*>(a.out) + (row0 + j) * a.out_ld + chan0;
+                        if constexpr (WHAT == kGateUp) {
+                            copy_out(at, act_to + j * kActBytes, bytes);
+                            if (a.out2) {
+                                T* both = static_cast<T*>(a.out2) + (row0 + j) * a.out2_ld + chan0;
+                                copy_out(both, to + j * kRowBytes, bytes);
+                                copy_out(both + a.lanes, to + j * kRowBytes + 128, bytes);
+                            }
+                        } else {
+                            copy_out(at, to + j * kRowBytes, bytes);
+                            if constexpr (WHAT == kGradAct) copy_out(at + a.lanes, to + (kChunk + j) * kRowBytes, bytes);
+                        }
+                    }
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                }
+                __syncwarp();
             }
             if (it.steps > 0) {
                 tmem_fence_before();
@@ -324,6 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (buffer == 0) parity ^= 1;
             }
         }
+        if (lane < 4) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
     tmem_fence_before();
     __syncthreads();

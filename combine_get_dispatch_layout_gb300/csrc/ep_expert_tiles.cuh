@@ -217,6 +217,11 @@ __device__ __forceinline__ void pair_done(uint32_t bar) {
                  : "memory");
 }
 
+// Shared memory to global memory, both on 16 bytes, a multiple of 16 of them; it counts in the thread's bulk groups.
+__device__ __forceinline__ void copy_out(void* to, const void* from, int bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(smem_addr(from)), "r"(bytes) : "memory");
+}
+
 // exp(v): 2^t for t = v log2(e) in two parts, so that large |v| lose nothing (about 2 units in the last place).
 __device__ __forceinline__ float exp_of(float v) {
     const float t = v * 1.44269504f;

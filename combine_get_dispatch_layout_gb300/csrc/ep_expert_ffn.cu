@@ -26,7 +26,7 @@ constexpr int kRing = 192 * 1024;
 constexpr int kChunk = 16;
 constexpr int kRowBytes = 256, kActBytes = 160;
 constexpr int kOutBytes = 2 * kChunk * kRowBytes, kHalfBytes = kOutBytes + 2 * kChunk * kActBytes;
-constexpr int kShared = 1024 + kRing + 2 * kHalfBytes + 512 + (kTileTable + 1) * 4;
+constexpr int kShared = 1024 + kRing + 2 * kHalfBytes + 512 + static_cast<int>(sizeof(Tables));
 static_assert(kShared <= 227 * 1024 - 256, "");
 
 enum Product { kGateUp, kDown, kGradAct, kGradX, kGradW };
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sums_full = clean + 8 * kMostStages, sums_empty = sums_full + 16;
     uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(barriers) + 120;
     volatile int* const dead = reinterpret_cast<volatile int*>(tmem_at + 1);
-    int* const table = reinterpret_cast<int*>(barriers) + 128;
+    Tables* const table = reinterpret_cast<Tables*>(barriers + 64);
     static_assert((4 * kMostStages + 4) * 2 <= 120, "");
     __shared__ int warp_sum[kThreads / 32];
 
@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     dependent_entry();
-    if constexpr (WHAT != kGradW) fill_table<kThreads>(a.g, a.plan, table, warp_sum);
+    if constexpr (WHAT != kGradW) fill_tables<kThreads>(a.g, a.plan, table, warp_sum);
+    else fill_rows<kThreads>(a.g, table);
     tmem_fence_before();
     __syncthreads();
     cluster_sync();   // (both CTAs' barriers are ready)
@@ -100,12 +101,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto decode = [&](int64_t it) {
         Item r;
         if constexpr (WHAT == kGradW) {
-            const int per = a.plan.m_tiles * a.n_tiles, in = static_cast<int>(it % per);
-            r.expert = static_cast<int>(it / per);
-            r.m = in / a.n_tiles;
-            r.col = in % a.n_tiles * a.plan.cap;
+            const int64_t per = static_cast<int64_t>(a.plan.m_tiles) * a.n_tiles;
+            r.expert = items < INT32_MAX ? static_cast<int>(it) / static_cast<int>(per) : static_cast<int>(it / per);
+            const int64_t in = it - r.expert * per;
+            r.m = items < INT32_MAX ? static_cast<int>(in) / a.n_tiles : static_cast<int>(in / a.n_tiles);
+            r.col = static_cast<int>(in - static_cast<int64_t>(r.m) * a.n_tiles) * a.plan.cap;
             r.cols = min(a.plan.cap, a.columns - r.col);
-            r.rows = rows_of(a.g, r.expert, r.row);
+            r.rows = rows_of(a.g, table, r.expert, r.row);
             r.steps = (r.rows + kStep - 1) / kStep;
         } else {
             const Tile t = tile_at(a.g, a.plan, table, it);
@@ -244,18 +246,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool staged = WHAT != kGradW || !(a.out_fp32 || a.accumulate);
         int buffer = 0, chunk = 0;
         uint32_t parity = 0;
+        // kGradAct: this thread's pieces of gate's and up's rows of a chunk of columns
+        uint4 ahead[4] = {};
+        const auto fetch = [&](const Item& it, int c0, int chan0, int bytes) {
+            const int piece_at = tid % 16 * 16;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = (tid & 127) / 16 + k % 2 * 8;
+                const T* row = static_cast<const T*>(a.in) + (static_cast<int64_t>(it.row) + c0 + j) * a.in_ld + chan0 + (k < 2 ? 0 : a.lanes);
+                if (c0 + j < it.cols && piece_at < bytes) ahead[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row) + piece_at);
+            }
+        };
         for (int64_t i = pair; i < items; i += pairs) {
             const Item it = decode(i);
             const uint32_t mine = tmem + buffer * 256 + (static_cast<uint32_t>(part) << 21);   // lane 32 * part, upper half
-            if (it.steps > 0) {
-                barrier_wait(sums_full + 8 * buffer, parity, dead);
-                tmem_fence_after();
-            }
             // the CTA's first channel, this thread's; of gate and up a warp's lanes are 16 gate and 16 up rows
             const int tile = it.m * kLanes + rank * (kLanes / 2), chan0 = WHAT == kGateUp ? tile / 2 : tile;
             const int chan = WHAT == kGateUp ? chan0 + part * 16 + (lane & 15) : chan0 + part * 32 + lane;
             const bool real = chan < a.lanes;
             const int bytes = min(WHAT == kGateUp ? 64 : 128, a.lanes - chan0) * 2;   // of a row of this CTA (a multiple of 16)
+            if (WHAT == kGradAct && half * kChunk < it.cols) fetch(it, half * kChunk, chan0, bytes);
+            if (it.steps > 0) {
+                barrier_wait(sums_full + 8 * buffer, parity, dead);
+                tmem_fence_after();
+            }
             for (int c0 = half * kChunk; c0 < it.cols; c0 += 2 * kChunk, ++chunk) {
                 uint32_t raw[kChunk];
                 if (it.steps > 0) {
@@ -289,22 +303,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     continue;
                 }
                 const int64_t row0 = WHAT == kGradW ? static_cast<int64_t>(it.expert) * a.columns + it.col + c0 : static_cast<int64_t>(it.row) + c0;
-                T gate[kChunk], up[kChunk];
-                if (WHAT == kGradAct && real) {
-                    const T* from = static_cast<const T*>(a.in) + row0 * a.in_ld + chan;
-#pragma unroll
-                    for (int j = 0; j < kChunk; ++j)
-                        if (j < many) gate[j] = from[j * a.in_ld], up[j] = from[j * a.in_ld + a.lanes];
-                }
-                // the copies out of this chunk's place have been read (kGradAct has both places for its two outputs)
-                if (lane < 4) {
-                    if (WHAT == kGradAct) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                    else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                }
-                half_sync();
-                const int place = WHAT == kGradAct ? 0 : chunk & 1;
+                const int place = WHAT == kGradAct ? 0 : chunk & 1;   // (kGradAct has both places: gate and up, or their gradients)
                 unsigned char* const to = out + place * (kChunk * kRowBytes);
                 unsigned char* const act_to = act_out + place * (kChunk * kActBytes);
+                // 16-byte pieces of the rows: this thread's are of rows `piece / 16` and that plus 8
+                const int piece_row = (tid & 127) / 16, piece_at = tid % 16 * 16;
                 if constexpr (WHAT == kGateUp) {
                     if (a.out2) {
                         T* at = reinterpret_cast<T*>(to + (lane < 16 ? 0 : 128)) + part * 16 + (lane & 15);
@@ -318,41 +321,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float got = __uint_as_float(__shfl_xor_sync(kFullMask, lane < 16 ? raw[j + 1] : raw[j], 16));
                         at[j * (kActBytes / 2)] = from_float<T>(lane < 16 ? silu(own) * got : silu(got) * own);
                     }
+                    half_sync();
+                    const int row = (tid & 127) / 8, byte = tid % 8 * 16;
+                    if (row < many && byte < bytes)
+                        *reinterpret_cast<uint4*>(reinterpret_cast<char*>(static_cast<T*>(a.out) + (row0 + row) * a.out_ld + chan0) + byte) =
+                            *reinterpret_cast<const uint4*>(act_to + row * kActBytes + byte);
+                    if (a.out2) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int j = piece_row + 8 * k, at_byte = piece_at & 127;
+                            T* both = static_cast<T*>(a.out2) + (row0 + j) * a.out2_ld + chan0 + (piece_at < 128 ? 0 : a.lanes);
+                            if (j < many && at_byte < bytes)
+                                *reinterpret_cast<uint4*>(reinterpret_cast<char*>(both) + at_byte) =
+                                    *reinterpret_cast<const uint4*>(to + j * kRowBytes + piece_at);
+                        }
+                    }
                 } else {
                     T* at = reinterpret_cast<T*>(to) + part * 32 + lane;
+                    if constexpr (WHAT == kGradAct) {
+                        // gate and up come as the gradients leave, a chunk ahead
 #pragma unroll
-                    for (int j = 0; j < kChunk; ++j) {
-                        const float d = __uint_as_float(raw[j]);
-                        if constexpr (WHAT == kGradAct) {
-                            const float gt = to_float(gate[j]), s = sigmoid(gt);
-                            at[j * (kRowBytes / 2)] = from_float<T>(d * to_float(up[j]) * s * (1.0f + gt * (1.0f - s)));
-                            at[(kChunk + j) * (kRowBytes / 2)] = from_float<T>(d * gt * s);
-                        } else {
-                            at[j * (kRowBytes / 2)] = from_float<T>(d);
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<uint4*>(to + (k / 2 * kChunk + piece_row + k % 2 * 8) * kRowBytes + piece_at) = ahead[k];
+                        half_sync();
+                        if (c0 + 2 * kChunk < it.cols) fetch(it, c0 + 2 * kChunk, chan0, bytes);
+#pragma unroll
+                        for (int j = 0; j < kChunk; ++j) {
+                            const float d = __uint_as_float(raw[j]);
+                            T &g = at[j * (kRowBytes / 2)], &u = at[(kChunk + j) * (kRowBytes / 2)];
+                            const float gate = to_float(g), up = to_float(u), s = sigmoid(gate);
+                            g = from_float<T>(d * up * s * (1.0f + gate * (1.0f - s)));
+                            u = from_float<T>(d * gate * s);
                         }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kChunk; ++j) at[j * (kRowBytes / 2)] = from_float<T>(__uint_as_float(raw[j]));
                     }
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                half_sync();
-                if (lane < 4) {   // a row each
-                    const int j = part * 4 + lane;
-                    if (j < many && bytes > 0) {
-                        T* at = static_cast<T*>(a.out) + (row0 + j) * a.out_ld + chan0;
-                        if constexpr (WHAT == kGateUp) {
-                            copy_out(at, act_to + j * kActBytes, bytes);
-                            if (a.out2) {
-                                T* both = static_cast<T*>(a.out2) + (row0 + j) * a.out2_ld + chan0;
-                                copy_out(both, to + j * kRowBytes, bytes);
-                                copy_out(both + a.lanes, to + j * kRowBytes + 128, bytes);
-                            }
-                        } else {
-                            copy_out(at, to + j * kRowBytes, bytes);
-                            if constexpr (WHAT == kGradAct) copy_out(at + a.lanes, to + (kChunk + j) * kRowBytes, bytes);
-                        }
+                    half_sync();
+#pragma unroll
+                    for (int k = 0; k < (WHAT == kGradAct ? 4 : 2); ++k) {
+                        const int j = piece_row + k % 2 * 8;
+                        T* row = static_cast<T*>(a.out) + (row0 + j) * a.out_ld + chan0 + (k < 2 ? 0 : a.lanes);
+                        if (j < many && piece_at < bytes)
+                            *reinterpret_cast<uint4*>(reinterpret_cast<char*>(row) + piece_at) =
+                                *reinterpret_cast<const uint4*>(to + (k / 2 * kChunk + j) * kRowBytes + piece_at);
                     }
-                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    if constexpr (WHAT == kGradAct) half_sync();   // (there is no second place)
                 }
-                __syncwarp();
             }
             if (it.steps > 0) {
                 tmem_fence_before();
@@ -362,8 +377,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (buffer == 0) parity ^= 1;
             }
         }
-        if (lane < 4) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-        __syncwarp();
     }
     tmem_fence_before();
     __syncthreads();
@@ -434,7 +447,8 @@ cudaError_t weight_gradient(const FfnArgs& f, void* out, const void* x, int lane
                             cudaStream_t stream) {
     CUtensorMap am, bm;
     Gemm a = gemm_of(f, lanes, kLanes, 0);
-    a.box = f.g.rows / f.g.E < 64 ? 16 : 64;
+    const int mean = f.g.rows / f.g.E;
+    a.box = mean < 32 ? 16 : mean < 256 ? 32 : 64;
     a.plan.cap = 256;
     a.columns = columns;
     a.n_tiles = ceil_div(columns, a.plan.cap);

@@ -37,7 +37,7 @@ struct Shape {
     static constexpr int kScales = kScaleSlots * kScaleBlocks * kScaleStep;   // floats
     static constexpr int kJoin = 2 * kChunk * 128;
     static constexpr int kMost = 4 * 128 + 2 * kParts * COLS + 2 * COLS;
-    static constexpr int kShared = 1024 + kStages * kStageBytes + (kScales + kJoin + kMost) * 4 + 512 + (kTileTable + 1) * 4;
+    static constexpr int kShared = 1024 + kStages * kStageBytes + (kScales + kJoin + kMost) * 4 + 512 + static_cast<int>(sizeof(Tables));
     static_assert(kShared <= 227 * 1024 - 256, "");
 };
 
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t scales_full = sums_empty + 8 * kBuffers, scales_empty = scales_full + 8 * kScaleSlots;
     uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(barriers) + 120;
     volatile int* const dead = reinterpret_cast<volatile int*>(tmem_at + 1);
-    int* const table = reinterpret_cast<int*>(barriers) + 128;
+    Tables* const table = reinterpret_cast<Tables*>(barriers + 64);
     static_assert((2 * kMostStages + 2 * kBuffers + 2 * kScaleSlots) * 2 <= 120, "");
     __shared__ int warp_sum[kThreads / 32];
 
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     dependent_entry();
-    fill_table<kThreads>(a.g, plan, table, warp_sum);
+    fill_tables<kThreads>(a.g, plan, table, warp_sum);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();

@@ -8,6 +8,13 @@ namespace ep {
 namespace {
 
 constexpr int kTileTable = 1024;   // entries of the table of experts' tiles
+constexpr int kRowTable = 256;     // experts whose rows are kept in shared memory, if there are no more
+
+// In shared memory: tiles before an expert, and the experts' first rows and numbers of rows.
+struct Tables {
+    int tiles[kTileTable + 1];
+    int2 rows[kRowTable];
+};
 
 // First row and number of real rows of expert e, within [0, rows).
 __device__ __forceinline__ int rows_of(const ExpertRows& g, int e, int& first) {
@@ -19,6 +26,23 @@ __device__ __forceinline__ int rows_of(const ExpertRows& g, int e, int& first) {
     int n = min(max(g.offsets[e + 1], 0), g.rows) - first;
     if (g.counts) n = min(n, g.counts[e]);
     return max(n, 0);
+}
+
+// The same from the table.
+__device__ __forceinline__ int rows_of(const ExpertRows& g, const Tables* t, int e, int& first) {
+    if (g.E > kRowTable) return rows_of(g, e, first);
+    const int2 r = t->rows[e];
+    first = r.x;
+    return r.y;
+}
+template <int THREADS>
+__device__ __forceinline__ void fill_rows(const ExpertRows& g, Tables* t) {
+    if (g.E > kRowTable) return;
+    for (int e = threadIdx.x; e < g.E; e += THREADS) {
+        int first;
+        const int n = rows_of(g, e, first);
+        t->rows[e] = make_int2(first, n);
+    }
 }
 
 // Tiles of an expert's product: m_tiles along the weights' rows, and along its own rows as many as `cap` rows a tile
@@ -41,9 +65,11 @@ __device__ __forceinline__ int tile_width(int n, int tiles, int cap, int whole) 
     return 16 * tiles < cap && !whole ? (ceil_div(n, tiles) + 15) / 16 * 16 : cap;
 }
 
-// Fills table[entry] with the tiles of rows before it, for all threads of the CTA (THREADS of them).
+// Fills the tables, by all threads of the CTA (THREADS of them); they are there after the next barrier.
 template <int THREADS>
-__device__ __forceinline__ void fill_table(const ExpertRows& g, const TilePlan& p, int* table, int* warp_sum) {
+__device__ __forceinline__ void fill_tables(const ExpertRows& g, const TilePlan& p, Tables* t, int* warp_sum) {
+    fill_rows<THREADS>(g, t);
+    int* const table = t->tiles;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const auto tiles_of = [&](int e) {
         int first;
@@ -73,12 +99,13 @@ __device__ __forceinline__ void fill_table(const ExpertRows& g, const TilePlan& 
     if (hi == entries && lo < hi) table[entries] = base;
 }
 
-__device__ __forceinline__ int64_t tile_count(const ExpertRows& g, const TilePlan& p, const int* table) {
-    return static_cast<int64_t>(table[((g.E - 1) >> p.shift) + 1]) * p.m_tiles;
+__device__ __forceinline__ int64_t tile_count(const ExpertRows& g, const TilePlan& p, const Tables* t) {
+    return static_cast<int64_t>(t->tiles[((g.E - 1) >> p.shift) + 1]) * p.m_tiles;
 }
 
 // (Offsets that contradict one another can make tiles without rows, never one outside [0, rows).)
-__device__ __forceinline__ Tile tile_at(const ExpertRows& g, const TilePlan& p, const int* table, int64_t it) {
+__device__ __forceinline__ Tile tile_at(const ExpertRows& g, const TilePlan& p, const Tables* tables, int64_t it) {
+    const int* const table = tables->tiles;
     int lo = 0, hi = (g.E - 1) >> p.shift;   // the last entry whose first tile is not behind `it`
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -86,16 +113,16 @@ __device__ __forceinline__ Tile tile_at(const ExpertRows& g, const TilePlan& p, 
         else hi = mid - 1;
     }
     int64_t in = it - static_cast<int64_t>(table[lo]) * p.m_tiles;
-    int first, e = lo << p.shift, n = rows_of(g, e, first), tiles = (n + p.cap - 1) / p.cap;
+    int first, e = lo << p.shift, n = rows_of(g, tables, e, first), tiles = (n + p.cap - 1) / p.cap;
     while (in >= static_cast<int64_t>(tiles) * p.m_tiles && e + 1 < g.E) {   // (an entry of several experts)
         in -= static_cast<int64_t>(tiles) * p.m_tiles;
-        n = rows_of(g, ++e, first);
+        n = rows_of(g, tables, ++e, first);
         tiles = (n + p.cap - 1) / p.cap;
     }
     Tile t;
     t.expert = e;
     const int64_t per_chunk = static_cast<int64_t>(p.chunk) * p.m_tiles;
-    const int c = static_cast<int>(in / per_chunk), r = static_cast<int>(in - c * per_chunk);
+    const int c = in < per_chunk ? 0 : static_cast<int>(in / per_chunk), r = static_cast<int>(in - c * per_chunk);
     const int wide = max(min(p.chunk, tiles - c * p.chunk), 1);
     t.m = r / wide;
     const int width = tile_width(max(n, 1), max(tiles, 1), p.cap, p.whole);
@@ -215,11 +242,6 @@ __device__ __forceinline__ void pair_done(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
                  "h"(static_cast<uint16_t>(3))
                  : "memory");
-}
-
-// Shared memory to global memory, both on 16 bytes, a multiple of 16 of them; it counts in the thread's bulk groups.
-__device__ __forceinline__ void copy_out(void* to, const void* from, int bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(smem_addr(from)), "r"(bytes) : "memory");
 }
 
 // exp(v): 2^t for t = v log2(e) in two parts, so that large |v| lose nothing (about 2 units in the last place).

@@ -29,7 +29,11 @@ constexpr int kOutBytes = 2 * kChunk * kRowBytes, kHalfBytes = kOutBytes + 2 * k
 constexpr int kShared = 1024 + kRing + 2 * kHalfBytes + 512 + static_cast<int>(sizeof(Tables));
 static_assert(kShared <= 227 * 1024 - 256, "");
 
-enum Product { kGateUp, kDown, kGradAct, kGradX, kGradW };
+enum Product { kNone = -1, kGateUp, kDown, kGradAct, kGradX, kGradW };
+template <int WHAT>
+struct Kind {
+    static constexpr int value = WHAT;
+};
 
 struct Gemm {
     ExpertRows g;
@@ -46,9 +50,53 @@ struct Gemm {
     int out_fp32, accumulate;       // kGradW
 };
 
-template <typename T, int WHAT>
+// An item: `cols` columns (rows of the output) from `col` on, lanes from m * kLanes on, `steps` stages; of kGradW the
+// contraction is over rows [row, row + rows).
+struct Item {
+    int expert, m, col, cols, row, rows, steps;
+};
+
+template <int WHAT>
+__device__ __forceinline__ int64_t items_of(const Gemm& a, const Tables* table) {
+    if constexpr (WHAT == kGradW) return static_cast<int64_t>(a.g.E) * a.plan.m_tiles * a.n_tiles;
+    else return a.plan.m_tiles > 0 ? tile_count(a.g, a.plan, table) : 0;
+}
+
+template <int WHAT>
+__device__ __forceinline__ Item item_at(const Gemm& a, const Tables* table, int64_t it, int64_t items) {
+    Item r;
+    if constexpr (WHAT == kGradW) {
+        const int64_t per = static_cast<int64_t>(a.plan.m_tiles) * a.n_tiles;
+        r.expert = items < INT32_MAX ? static_cast<int>(it) / static_cast<int>(per) : static_cast<int>(it / per);
+        const int64_t in = it - r.expert * per;
+        r.m = items < INT32_MAX ? static_cast<int>(in) / a.n_tiles : static_cast<int>(in / a.n_tiles);
+        r.col = static_cast<int>(in - static_cast<int64_t>(r.m) * a.n_tiles) * a.plan.cap;
+        r.cols = min(a.plan.cap, a.columns - r.col);
+        r.rows = rows_of(a.g, table, r.expert, r.row);
+        r.steps = (r.rows + kStep - 1) / kStep;
+    } else {
+        const Tile t = tile_at(a.g, a.plan, table, it);
+        r.expert = t.expert;
+        r.m = t.m;
+        r.col = r.row = t.row;
+        r.cols = r.rows = t.rows;
+        r.steps = (a.inner + kStep - 1) / kStep;
+    }
+    return r;
+}
+
+// kGradW: whether a stage has rows of others among the 16 of a product behind the expert's last, and zeros are wanted there.
+template <int WHAT>
+__device__ __forceinline__ bool unclean(const Item& it, int s) {
+    return WHAT == kGradW && it.rows - s * kStep < kStep && it.rows % 16 != 0;
+}
+
+// One product, or two that do not depend on each other, the second's items after the first's (kNone: no second).
+template <typename T, int FIRST, int SECOND>
 __global__ void __launch_bounds__(kThreads, 1)
-    expert_gemm_kernel(Gemm a, const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map) {
+    expert_gemm_kernel(const __grid_constant__ Gemm first, const __grid_constant__ Gemm second, const __grid_constant__ CUtensorMap first_a_map,
+                       const __grid_constant__ CUtensorMap first_b_map, const __grid_constant__ CUtensorMap second_a_map,
+                       const __grid_constant__ CUtensorMap second_b_map) {
     extern __shared__ unsigned char shared_bytes[];
     unsigned char* const ring = shared_bytes + (1024 - smem_addr(shared_bytes) % 1024) % 1024;
     uint64_t* const barriers = reinterpret_cast<uint64_t*>(ring + kRing + 2 * kHalfBytes);
@@ -67,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc_all(smem_addr(tmem_at));
         if (lane == 0) {
             *dead = 0;
-            for (int i = 0; i < a.stages; ++i) {
+            for (int i = 0; i < first.stages; ++i) {
                 barrier_init(full + 8 * i, 1);
                 barrier_init(empty + 8 * i, 1);
                 barrier_init(part_full + 8 * i, 1);
@@ -81,8 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     dependent_entry();
-    if constexpr (WHAT != kGradW) fill_tables<kThreads>(a.g, a.plan, table, warp_sum);
-    else fill_rows<kThreads>(a.g, table);
+    fill_tables<kThreads>(first.g, first.plan, table, warp_sum);
     tmem_fence_before();
     __syncthreads();
     cluster_sync();   // (both CTAs' barriers are ready)
@@ -92,44 +139,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
-    // An item: `cols` columns (rows of the output) from `col` on, lanes from m * kLanes on, `steps` stages; of kGradW the
-    // contraction is over rows [row, row + rows).
-    struct Item {
-        int expert, m, col, cols, row, rows, steps;
-    };
-    const int64_t items = WHAT == kGradW ? static_cast<int64_t>(a.g.E) * a.plan.m_tiles * a.n_tiles : tile_count(a.g, a.plan, table);
-    const auto decode = [&](int64_t it) {
-        Item r;
-        if constexpr (WHAT == kGradW) {
-            const int64_t per = static_cast<int64_t>(a.plan.m_tiles) * a.n_tiles;
-            r.expert = items < INT32_MAX ? static_cast<int>(it) / static_cast<int>(per) : static_cast<int>(it / per);
-            const int64_t in = it - r.expert * per;
-            r.m = items < INT32_MAX ? static_cast<int>(in) / a.n_tiles : static_cast<int>(in / a.n_tiles);
-            r.col = static_cast<int>(in - static_cast<int64_t>(r.m) * a.n_tiles) * a.plan.cap;
-            r.cols = min(a.plan.cap, a.columns - r.col);
-            r.rows = rows_of(a.g, table, r.expert, r.row);
-            r.steps = (r.rows + kStep - 1) / kStep;
-        } else {
-            const Tile t = tile_at(a.g, a.plan, table, it);
-            r.expert = t.expert;
-            r.m = t.m;
-            r.col = r.row = t.row;
-            r.cols = r.rows = t.rows;
-            r.steps = (a.inner + kStep - 1) / kStep;
+    // A role over all items of this pair; what it keeps (places in rings, parities) goes on from the first product to the second.
+    const auto walk = [&](auto role) {
+        const int64_t n = items_of<FIRST>(first, table);
+        role(Kind<FIRST>{}, first, first_a_map, first_b_map, static_cast<int64_t>(pair), n);
+        if constexpr (SECOND != kNone) {
+            const int64_t start = (pair - n % pairs + pairs) % pairs;   // (the turn of the pairs goes on)
+            role(Kind<SECOND>{}, second, second_a_map, second_b_map, start, items_of<SECOND>(second, table));
         }
-        return r;
     };
-
-    // kGradW: whether a stage has rows of others among the 16 of a product behind the expert's last, and zeros are wanted there.
-    const auto unclean = [&](const Item& it, int s) { return WHAT == kGradW && it.rows - s * kStep < kStep && it.rows % 16 != 0; };
 
     // (the loader and the issuer are one thread each: the compiler knows it behind elect.sync, and waits cost it less)
     if (warp == kLoader) {
         if (leader) {
             int slot = 0;
             uint32_t parity = 1;   // (the first round of the ring waits for nothing)
-            for (int64_t i = pair; i < items; i += pairs) {
-                const Item it = decode(i);
+            walk([&](auto kind, const Gemm& a, const CUtensorMap& a_map, const CUtensorMap& b_map, int64_t start, int64_t items) {
+              constexpr int WHAT = decltype(kind)::value;
+              for (int64_t i = start; i < items; i += pairs) {
+                const Item it = item_at<WHAT>(a, table, i, items);
                 const int half = columns_of(it.cols) / 2;   // columns of each CTA
                 const int b_boxes = WHAT == kGradW ? (half + 63) / 64 : (half + a.box - 1) / a.box;
                 const int lane0 = it.m * kLanes + rank * (kLanes / 2), col0 = it.col + rank * half;
@@ -141,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if constexpr (WHAT == kGradW) {
                         // [64 channels] x [box rows] of both operands, boxes with real rows only
                         // (a stage that has to be cleaned first counts on a barrier of each CTA's own)
-                        const bool own = unclean(it, s);
+                        const bool own = unclean<WHAT>(it, s);
                         const uint32_t to = own ? part_full + 8 * slot : bar;
                         const int down = (min(kStep, it.rows - s * kStep) + a.box - 1) / a.box, all = (2 + b_boxes) * down;
                         if (rank == 0 || own) barrier_expect(own ? to : mine, all * a.box * 128 * (own ? 1 : 2));
@@ -166,20 +194,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (++slot == a.stages) slot = 0, parity ^= 1;
                 }
-            }
+              }
+            });
         }
         __syncwarp();
     } else if (warp == kIssuer) {
         if (leader && rank == 0) {   // (it issues for both CTAs)
-            // fp32 sums; operands' type; A outward, B outward; 256 lanes
-            constexpr uint32_t kType = std::is_same_v<T, __nv_bfloat16> ? 1u : 0u;
-            constexpr bool kAOut = WHAT >= kGradAct, kBOut = WHAT == kGradW;
-            constexpr uint32_t kShape = (1u << 4) | (kType << 7) | (kType << 10) | (kAOut ? 1u << 15 : 0u) | (kBOut ? 1u << 16 : 0u) |
-                                        (static_cast<uint32_t>(kLanes / 16) << 24);
             int slot = 0, buffer = 0;
             uint32_t parities = 0, sums_parity = 1, clean_parity = 0;   // parities, clean_parity: a bit for each slot
-            for (int64_t i = pair; i < items; i += pairs) {
-                const Item it = decode(i);
+            walk([&](auto kind, const Gemm& a, const CUtensorMap&, const CUtensorMap&, int64_t start, int64_t items) {
+              constexpr int WHAT = decltype(kind)::value;
+              // fp32 sums; operands' type; A outward, B outward; 256 lanes
+              constexpr uint32_t kType = std::is_same_v<T, __nv_bfloat16> ? 1u : 0u;
+              constexpr bool kAOut = WHAT >= kGradAct, kBOut = WHAT == kGradW;
+              constexpr uint32_t kShape = (1u << 4) | (kType << 7) | (kType << 10) | (kAOut ? 1u << 15 : 0u) | (kBOut ? 1u << 16 : 0u) |
+                                              (static_cast<uint32_t>(kLanes / 16) << 24);
+              for (int64_t i = start; i < items; i += pairs) {
+                const Item it = item_at<WHAT>(a, table, i, items);
                 if (it.steps == 0) continue;
                 const uint32_t shape = kShape | static_cast<uint32_t>(columns_of(it.cols) / 8) << 17;
                 const uint32_t sums = tmem + buffer * 256;
@@ -188,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t at_a = smem_addr(ring) + slot * a.stage_bytes, at_b = at_a + kABytes;
                     const uint64_t da = kAOut ? operand_outward(at_a, 8192) : operand(at_a, 1024);
                     const uint64_t db = kBOut ? operand_outward(at_b, 8192) : operand(at_b, 1024);
-                    if (unclean(it, s)) {
+                    if (unclean<WHAT>(it, s)) {
                         barrier_wait_cluster(clean + 8 * slot, (clean_parity >> slot) & 1, dead);
                         clean_parity ^= 1u << slot;
                     } else {
@@ -210,42 +241,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 buffer ^= 1;
                 if (buffer == 0) sums_parity ^= 1;
-            }
+              }
+            });
         }
         __syncwarp();
     } else if (warp == kCleaner) {
         // Rows behind an expert's last belong to others: zeros instead, in both operands, some stages before their product.
-        if constexpr (WHAT == kGradW) {
+        if constexpr (FIRST == kGradW || SECOND == kGradW) {
             int slot = 0;
             uint32_t parities = 0;   // a bit for each slot
-            for (int64_t i = pair; i < items; i += pairs) {
-                const Item it = decode(i);
-                for (int s = 0; s < it.steps; ++s) {
-                    if (unclean(it, s)) {
-                        barrier_wait_inline(part_full + 8 * slot, (parities >> slot) & 1, dead);
-                        parities ^= 1u << slot;
-                        const int left = it.rows - s * kStep, end = (left + 15) / 16 * 16, lines = 2 + (columns_of(it.cols) / 2 + 63) / 64;
-                        for (int j = lane; j < (end - left) * lines * 8; j += 32) {
-                            const int line = j / 8, row = left + line / lines;
-                            *reinterpret_cast<uint4*>(ring + slot * a.stage_bytes + line % lines * 8192 + row * 128 + j % 8 * 16) =
-                                make_uint4(0, 0, 0, 0);
+            walk([&](auto kind, const Gemm& a, const CUtensorMap&, const CUtensorMap&, int64_t start, int64_t items) {
+              constexpr int WHAT = decltype(kind)::value;
+              for (int64_t i = start; i < items; i += pairs) {
+                const Item it = item_at<WHAT>(a, table, i, items);
+                if constexpr (WHAT != kGradW) {
+                    slot = (slot + it.steps) % a.stages;
+                } else {
+                    for (int s = 0; s < it.steps; ++s) {
+                        if (unclean<WHAT>(it, s)) {
+                            barrier_wait_inline(part_full + 8 * slot, (parities >> slot) & 1, dead);
+                            parities ^= 1u << slot;
+                            const int left = it.rows - s * kStep, end = (left + 15) / 16 * 16, lines = 2 + (columns_of(it.cols) / 2 + 63) / 64;
+                            for (int j = lane; j < (end - left) * lines * 8; j += 32) {
+                                const int line = j / 8, row = left + line / lines;
+                                *reinterpret_cast<uint4*>(ring + slot * a.stage_bytes + line % lines * 8192 + row * 128 + j % 8 * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                            }
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            __syncwarp();
+                            if (lane == 0) barrier_arrive_cluster(in_first(clean + 8 * slot));
                         }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) barrier_arrive_cluster(in_first(clean + 8 * slot));
+                        if (++slot == a.stages) slot = 0;
                     }
-                    if (++slot == a.stages) slot = 0;
                 }
-            }
+              }
+            });
         }
     } else {
         const int half = warp >> 2, part = warp & 3;   // of the chunks of columns; of the lanes
         unsigned char* const out = ring + kRing + half * kHalfBytes;
         unsigned char* const act_out = out + kOutBytes;
         const auto half_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); };
-        const bool staged = WHAT != kGradW || !(a.out_fp32 || a.accumulate);
         int buffer = 0, chunk = 0;
         uint32_t parity = 0;
+        walk([&](auto kind, const Gemm& a, const CUtensorMap&, const CUtensorMap&, int64_t start, int64_t items) {
+        constexpr int WHAT = decltype(kind)::value;
+        const bool staged = WHAT != kGradW || !(a.out_fp32 || a.accumulate);
         // kGradAct: this thread's pieces of gate's and up's rows of a chunk of columns
         uint4 ahead[4] = {};
         const auto fetch = [&](const Item& it, int c0, int chan0, int bytes) {
@@ -257,8 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c0 + j < it.cols && piece_at < bytes) ahead[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row) + piece_at);
             }
         };
-        for (int64_t i = pair; i < items; i += pairs) {
-            const Item it = decode(i);
+        for (int64_t i = start; i < items; i += pairs) {
+            const Item it = item_at<WHAT>(a, table, i, items);
             const uint32_t mine = tmem + buffer * 256 + (static_cast<uint32_t>(part) << 21);   // lane 32 * part, upper half
             // the CTA's first channel, this thread's; of gate and up a warp's lanes are 16 gate and 16 up rows
             const int tile = it.m * kLanes + rank * (kLanes / 2), chan0 = WHAT == kGateUp ? tile / 2 : tile;
@@ -377,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (buffer == 0) parity ^= 1;
             }
         }
+        });
     }
     tmem_fence_before();
     __syncthreads();
@@ -389,32 +431,48 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ host
 
-template <typename T, int WHAT>
-cudaError_t launch_gemm(Gemm& a, const CUtensorMap& a_map, const CUtensorMap& b_map, cudaStream_t stream) {
+// A product with its operands' maps.
+struct Operands {
+    Gemm gemm{};
+    CUtensorMap a_map, b_map;
+};
+
+template <typename T, int FIRST, int SECOND>
+cudaError_t launch_gemms(Operands& first, Operands& second, cudaStream_t stream) {
     static int known[64];
     int pairs = 0;
-    cudaError_t err = pairs_at_once(expert_gemm_kernel<T, WHAT>, kThreads, kShared, known, &pairs);
+    cudaError_t err = pairs_at_once(expert_gemm_kernel<T, FIRST, SECOND>, kThreads, kShared, known, &pairs);
     if (err != cudaSuccess) return err;
-    a.stage_bytes = kABytes + a.plan.cap / 2 * kStep * 2;
-    a.stages = kRing / a.stage_bytes < kMostStages ? kRing / a.stage_bytes : kMostStages;
-    const int64_t used = a.g.rows < a.g.E ? a.g.rows : a.g.E;
-    const int64_t most = WHAT == kGradW ? static_cast<int64_t>(a.g.E) * a.plan.m_tiles * a.n_tiles
-                                        : (a.g.rows + used * (a.plan.cap - 1)) / a.plan.cap * a.plan.m_tiles;
-    return launch_pairs(expert_gemm_kernel<T, WHAT>, static_cast<int>(most < pairs ? most : pairs), kThreads, kShared, stream, a, a_map,
-                        b_map);
+    // one ring serves both
+    const auto stage = [](const Gemm& a) { return kABytes + a.plan.cap / 2 * kStep * 2; };
+    const int bytes = SECOND != kNone && stage(second.gemm) > stage(first.gemm) ? stage(second.gemm) : stage(first.gemm);
+    int64_t items = 0;
+    for (Gemm* a : {&first.gemm, &second.gemm}) {
+        a->stage_bytes = bytes;
+        a->stages = kRing / bytes < kMostStages ? kRing / bytes : kMostStages;
+        const int64_t used = a->g.rows < a->g.E ? a->g.rows : a->g.E;
+        if (a->columns > 0) items += static_cast<int64_t>(a->g.E) * a->plan.m_tiles * a->n_tiles;
+        else if (a->plan.m_tiles > 0) items += (a->g.rows + used * (a->plan.cap - 1)) / a->plan.cap * a->plan.m_tiles;
+    }
+    if (items == 0) return cudaSuccess;
+    return launch_pairs(expert_gemm_kernel<T, FIRST, SECOND>, static_cast<int>(items < pairs ? items : pairs), kThreads, kShared, stream,
+                        first.gemm, second.gemm, first.a_map, first.b_map, second.a_map, second.b_map);
 }
 
-Gemm gemm_of(const FfnArgs& f, int lanes, int lanes_of_tile, int inner) {
+// A product whose output has `lanes` channels, `of_tile` of them a tile; none without an output.
+Gemm gemm_of(const FfnArgs& f, void* out, int64_t out_ld, int lanes, int of_tile, int inner) {
     Gemm a{};
     a.g = f.g;
     a.lanes = lanes;
     a.inner = inner;
-    a.plan.m_tiles = ceil_div(lanes, lanes_of_tile);
+    a.plan.m_tiles = out ? ceil_div(lanes, of_tile) : 0;
     a.plan.chunk = 16;
     while (((f.g.E - 1) >> a.plan.shift) + 1 > kTileTable) ++a.plan.shift;
     const int64_t used = f.g.rows < f.g.E ? f.g.rows : f.g.E, mean = (f.g.rows - 1) / used + 1;
     a.plan.cap = mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 112 ? 128 : 256;
     a.box = a.plan.cap <= 64 ? 16 : 64;
+    a.out = out;
+    a.out_ld = out_ld;
     return a;
 }
 
@@ -422,68 +480,62 @@ Gemm gemm_of(const FfnArgs& f, int lanes, int lanes_of_tile, int inner) {
 cudaError_t rows_map(CUtensorMap* map, const FfnArgs& f, const void* x, int64_t width, int64_t ld, int box) {
     return box_map(map, x, f.dtype, width, f.g.rows, 1, 1, ld * 2, ld * 2, ld * 2, box, 1);
 }
+// Weights [E][rows][width] in boxes of 64 x box.
+cudaError_t weights_map(CUtensorMap* map, const FfnArgs& f, const void* w, int64_t rows, int64_t width, int box) {
+    return box_map(map, w, f.dtype, width, rows, 1, f.g.E, width * 2, rows * width * 2, rows * width * 2, box, 1);
+}
 
 template <typename T>
 cudaError_t forward(const FfnArgs& f, cudaStream_t stream) {
     const int64_t H = f.H, F = f.F;
-    CUtensorMap am, bm;
-    Gemm a = gemm_of(f, f.F, kLanes / 2, f.H);
-    a.out = f.act, a.out_ld = f.act_ld;
-    a.out2 = f.gate_up, a.out2_ld = f.gate_up_ld;
-    cudaError_t err = box_map(&am, f.w_gate_up, f.dtype, H, F, 2, f.g.E, H * 2, F * H * 2, 2 * F * H * 2, 16, 2);
-    if (err == cudaSuccess) err = rows_map(&bm, f, f.x, H, f.x_ld, a.box);
-    if (err == cudaSuccess) err = launch_gemm<T, kGateUp>(a, am, bm, stream);
+    Operands p{}, none{};
+    p.gemm = gemm_of(f, f.act, f.act_ld, f.F, kLanes / 2, f.H);
+    p.gemm.out2 = f.gate_up, p.gemm.out2_ld = f.gate_up_ld;
+    cudaError_t err = box_map(&p.a_map, f.w_gate_up, f.dtype, H, F, 2, f.g.E, H * 2, F * H * 2, 2 * F * H * 2, 16, 2);
+    if (err == cudaSuccess) err = rows_map(&p.b_map, f, f.x, H, f.x_ld, p.gemm.box);
+    if (err == cudaSuccess) err = launch_gemms<T, kGateUp, kNone>(p, none, stream);
     if (err != cudaSuccess || !f.y) return err;
-    a = gemm_of(f, f.H, kLanes, f.F);
-    a.out = f.y, a.out_ld = f.y_ld;
-    err = box_map(&am, f.w_down, f.dtype, F, H, 1, f.g.E, F * 2, F * H * 2, F * H * 2, kLanes / 2, 1);
-    if (err == cudaSuccess) err = rows_map(&bm, f, f.act, F, f.act_ld, a.box);
-    return err == cudaSuccess ? launch_gemm<T, kDown>(a, am, bm, stream) : err;
+    p.gemm = gemm_of(f, f.y, f.y_ld, f.H, kLanes, f.F);
+    err = weights_map(&p.a_map, f, f.w_down, H, F, kLanes / 2);
+    if (err == cudaSuccess) err = rows_map(&p.b_map, f, f.act, F, f.act_ld, p.gemm.box);
+    return err == cudaSuccess ? launch_gemms<T, kDown, kNone>(p, none, stream) : err;
 }
 
 // dW [E][columns][lanes] = (by [rows][columns])^T x [rows][lanes]
-template <typename T>
-cudaError_t weight_gradient(const FfnArgs& f, void* out, const void* x, int lanes, int64_t x_ld, const void* by, int columns, int64_t by_ld,
-                            cudaStream_t stream) {
-    CUtensorMap am, bm;
-    Gemm a = gemm_of(f, lanes, kLanes, 0);
+cudaError_t weight_gradient(Operands* p, const FfnArgs& f, void* out, const void* x, int lanes, int64_t x_ld, const void* by, int columns,
+                            int64_t by_ld) {
+    Gemm& a = p->gemm = gemm_of(f, out, lanes, lanes, kLanes, 0);
+    if (!out) return cudaSuccess;
     const int mean = f.g.rows / f.g.E;
     a.box = mean < 32 ? 16 : mean < 256 ? 32 : 64;
     a.plan.cap = 256;
     a.columns = columns;
     a.n_tiles = ceil_div(columns, a.plan.cap);
-    a.out = out, a.out_ld = lanes;
     a.out_fp32 = f.grad_w_fp32, a.accumulate = f.accumulate;
-    cudaError_t err = rows_map(&am, f, x, lanes, x_ld, a.box);
-    if (err == cudaSuccess) err = rows_map(&bm, f, by, columns, by_ld, a.box);
-    return err == cudaSuccess ? launch_gemm<T, kGradW>(a, am, bm, stream) : err;
+    const cudaError_t err = rows_map(&p->a_map, f, x, lanes, x_ld, a.box);
+    return err == cudaSuccess ? rows_map(&p->b_map, f, by, columns, by_ld, a.box) : err;
 }
 
+// Two launches of two products each that do not depend on each other: their ends and starts cost once.
 template <typename T>
 cudaError_t backward(const FfnArgs& f, cudaStream_t stream) {
     const int64_t H = f.H, F = f.F;
-    CUtensorMap am, bm;
-    cudaError_t err = cudaSuccess;
-    if (f.g.rows > 0) {
-        Gemm a = gemm_of(f, f.F, kLanes, f.H);
-        a.in = f.gate_up, a.in_ld = f.gate_up_ld;
-        a.out = f.grad_gate_up, a.out_ld = f.grad_gate_up_ld;
-        err = box_map(&am, f.w_down, f.dtype, F, H, 1, f.g.E, F * 2, F * H * 2, F * H * 2, kStep, 1);
-        if (err == cudaSuccess) err = rows_map(&bm, f, f.grad_y, H, f.grad_y_ld, a.box);
-        if (err == cudaSuccess) err = launch_gemm<T, kGradAct>(a, am, bm, stream);
-        if (err == cudaSuccess && f.grad_x) {
-            a = gemm_of(f, f.H, kLanes, 2 * f.F);
-            a.out = f.grad_x, a.out_ld = f.grad_x_ld;
-            err = box_map(&am, f.w_gate_up, f.dtype, H, 2 * F, 1, f.g.E, H * 2, 2 * F * H * 2, 2 * F * H * 2, kStep, 1);
-            if (err == cudaSuccess) err = rows_map(&bm, f, f.grad_gate_up, 2 * F, f.grad_gate_up_ld, a.box);
-            if (err == cudaSuccess) err = launch_gemm<T, kGradX>(a, am, bm, stream);
-        }
+    Operands p{}, w{};
+    p.gemm = gemm_of(f, f.grad_gate_up, f.grad_gate_up_ld, f.F, kLanes, f.H);
+    p.gemm.in = f.gate_up, p.gemm.in_ld = f.gate_up_ld;
+    cudaError_t err = weights_map(&p.a_map, f, f.w_down, H, F, kStep);
+    if (err == cudaSuccess) err = rows_map(&p.b_map, f, f.grad_y, H, f.grad_y_ld, p.gemm.box);
+    if (err == cudaSuccess) err = weight_gradient(&w, f, f.grad_w_down, f.act, f.F, f.act_ld, f.grad_y, f.H, f.grad_y_ld);
+    if (err == cudaSuccess) err = launch_gemms<T, kGradAct, kGradW>(p, w, stream);
+    if (err != cudaSuccess || (!f.grad_x && !f.grad_w_gate_up)) return err;
+    p.gemm = gemm_of(f, f.grad_x, f.grad_x_ld, f.H, kLanes, 2 * f.F);
+    if (f.grad_x) {
+        err = weights_map(&p.a_map, f, f.w_gate_up, 2 * F, H, kStep);
+        if (err == cudaSuccess) err = rows_map(&p.b_map, f, f.grad_gate_up, 2 * F, f.grad_gate_up_ld, p.gemm.box);
     }
-    if (err == cudaSuccess && f.grad_w_gate_up)
-        err = weight_gradient<T>(f, f.grad_w_gate_up, f.x, f.H, f.x_ld, f.grad_gate_up, 2 * f.F, f.grad_gate_up_ld, stream);
-    if (err == cudaSuccess && f.grad_w_down)
-        err = weight_gradient<T>(f, f.grad_w_down, f.act, f.F, f.act_ld, f.grad_y, f.H, f.grad_y_ld, stream);
-    return err;
+    if (err == cudaSuccess)
+        err = weight_gradient(&w, f, f.grad_w_gate_up, f.x, f.H, f.x_ld, f.grad_gate_up, 2 * f.F, f.grad_gate_up_ld);
+    return err == cudaSuccess ? launch_gemms<T, kGradX, kGradW>(p, w, stream) : err;
 }
 
 }  // namespace

@@ -42,7 +42,8 @@ struct Gemm {
     int inner;           // contraction (of kGradW: the expert's rows instead)
     int columns;         // kGradW: rows of the output
     int n_tiles;         // kGradW: tiles of them
-    int stages, stage_bytes, box;   // box: rows of a box of operand B (kGradW: of both)
+    int atoms;           // kStep deep parts of a stage (kGradW: 1)
+    int stages, stage_bytes, atom_bytes, box;   // box: rows of a box of operand B (kGradW: of both)
     void* out;
     void* out2;          // kGateUp: gate and up, or NULL
     const void* in;      // kGradAct: gate and up
@@ -80,7 +81,7 @@ __device__ __forceinline__ Item item_at(const Gemm& a, const Tables* table, int6
         r.m = t.m;
         r.col = r.row = t.row;
         r.cols = r.rows = t.rows;
-        r.steps = (a.inner + kStep - 1) / kStep;
+        r.steps = (a.inner + kStep * a.atoms - 1) / (kStep * a.atoms);
     }
     return r;
 }
@@ -110,7 +111,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert((4 * kMostStages + 4) * 2 <= 120, "");
     __shared__ int warp_sum[kThreads / 32];
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = pair_rank();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = cluster_rank();
+    if (warp == kCleaner && elected()) {
+        prefetch_map(&first_a_map);
+        prefetch_map(&first_b_map);
+        if constexpr (SECOND != kNone) {
+            prefetch_map(&second_a_map);
+            prefetch_map(&second_b_map);
+        }
+    }
     if (warp == kLoader) {
         tmem_alloc_all(smem_addr(tmem_at));
         if (lane == 0) {
@@ -179,18 +188,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int j = 0; j < b_boxes; ++j) load_box_pair(at_b + j * 8192 + at, &b_map, col0 + j * 64, row, 0, 0, to);
                         }
                     } else {
-                        if (rank == 0) barrier_expect(mine, 2 * (kABytes + b_boxes * a.box * 128));
-                        if constexpr (WHAT == kGateUp) {   // the 16 gate and the 16 up rows of each warp
-                            for (int j = 0; j < 4; ++j)
-                                load_box_pair(at_a + j * 4096, &a_map, s * kStep, lane0 / 2 + j * 16, 0, it.expert, bar);
-                        } else if constexpr (WHAT == kDown) {
-                            load_box_pair(at_a, &a_map, s * kStep, lane0, 0, it.expert, bar);
-                        } else {
-                            for (int j = 0; j < 2; ++j)
-                                load_box_pair(at_a + j * 8192, &a_map, lane0 + j * 64, s * kStep, 0, it.expert, bar);
+                        if (rank == 0) barrier_expect(mine, 2 * a.atoms * (kABytes + b_boxes * a.box * 128));
+                        for (int part = 0; part < a.atoms; ++part) {   // (zeros behind the contraction's end)
+                            const int k = (s * a.atoms + part) * kStep;
+                            const uint32_t to_a = at_a + part * a.atom_bytes, to_b = to_a + kABytes;
+                            if constexpr (WHAT == kGateUp) {   // the 16 gate and the 16 up rows of each warp
+                                for (int j = 0; j < 4; ++j) load_box_pair(to_a + j * 4096, &a_map, k, lane0 / 2 + j * 16, 0, it.expert, bar);
+                            } else if constexpr (WHAT == kDown) {
+                                load_box_pair(to_a, &a_map, k, lane0, 0, it.expert, bar);
+                            } else {
+                                for (int j = 0; j < 2; ++j) load_box_pair(to_a + j * 8192, &a_map, lane0 + j * 64, k, 0, it.expert, bar);
+                            }
+                            for (int j = 0; j < b_boxes; ++j) load_box_pair(to_b + j * a.box * 128, &b_map, k, col0 + j * a.box, 0, 0, bar);
                         }
-                        for (int j = 0; j < b_boxes; ++j)
-                            load_box_pair(at_b + j * a.box * 128, &b_map, s * kStep, col0 + j * a.box, 0, 0, bar);
                     }
                     if (++slot == a.stages) slot = 0, parity ^= 1;
                 }
@@ -229,9 +239,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_fence_after();
                     const int depth = WHAT == kGradW ? min((it.rows - s * kStep + 15) / 16, kStep / 16) : kStep / 16;   // products of 16
                     if (WHAT != kGradW || depth == kStep / 16) {
+                        for (int part = 0; part < (WHAT == kGradW ? 1 : a.atoms); ++part) {
+                            const uint64_t on = part * (a.atom_bytes / 16);
 #pragma unroll
-                        for (int k = 0; k < kStep / 16; ++k)
-                            multiply_pair(sums, da + k * (kAOut ? 128 : 2), db + k * (kBOut ? 128 : 2), shape, s > 0 || k > 0);
+                            for (int k = 0; k < kStep / 16; ++k)
+                                multiply_pair(sums, da + on + k * (kAOut ? 128 : 2), db + on + k * (kBOut ? 128 : 2), shape,
+                                              s > 0 || part > 0 || k > 0);
+                        }
                     } else {
                         for (int k = 0; k < depth; ++k) multiply_pair(sums, da + k * 128, db + k * 128, shape, s > 0 || k > 0);
                     }
@@ -439,13 +453,19 @@ struct Operands {
 
 template <typename T, int FIRST, int SECOND>
 cudaError_t launch_gemms(Operands& first, Operands& second, cudaStream_t stream) {
-    static int known[64];
-    int pairs = 0;
-    cudaError_t err = pairs_at_once(expert_gemm_kernel<T, FIRST, SECOND>, kThreads, kShared, known, &pairs);
+    static ClusterRoom known[64];
+    static int ready[64];
+    ClusterRoom room{};
+    cudaError_t err = cluster_room(expert_gemm_kernel<T, FIRST, SECOND>, kThreads, kShared, known, ready, &room);
     if (err != cudaSuccess) return err;
-    // one ring serves both
-    const auto stage = [](const Gemm& a) { return kABytes + a.plan.cap / 2 * kStep * 2; };
-    const int bytes = SECOND != kNone && stage(second.gemm) > stage(first.gemm) ? stage(second.gemm) : stage(first.gemm);
+    const int pairs = room.clusters[1];
+    first.gemm.atoms = first.gemm.plan.cap <= 64 ? 2 : 1;
+    second.gemm.atoms = 1;
+    int bytes = 0;   // one ring serves both
+    for (Gemm* a : {&first.gemm, &second.gemm}) {
+        a->atom_bytes = kABytes + a->plan.cap / 2 * kStep * 2;
+        if (a->atoms * a->atom_bytes > bytes) bytes = a->atoms * a->atom_bytes;
+    }
     int64_t items = 0;
     for (Gemm* a : {&first.gemm, &second.gemm}) {
         a->stage_bytes = bytes;
@@ -455,8 +475,8 @@ cudaError_t launch_gemms(Operands& first, Operands& second, cudaStream_t stream)
         else if (a->plan.m_tiles > 0) items += (a->g.rows + used * (a->plan.cap - 1)) / a->plan.cap * a->plan.m_tiles;
     }
     if (items == 0) return cudaSuccess;
-    return launch_pairs(expert_gemm_kernel<T, FIRST, SECOND>, static_cast<int>(items < pairs ? items : pairs), kThreads, kShared, stream,
-                        first.gemm, second.gemm, first.a_map, first.b_map, second.a_map, second.b_map);
+    return launch_clusters(expert_gemm_kernel<T, FIRST, SECOND>, static_cast<int>(items < pairs ? items : pairs), 2, kThreads, kShared, stream,
+                              first.gemm, second.gemm, first.a_map, first.b_map, second.a_map, second.b_map);
 }
 
 // A product whose output has `lanes` channels, `of_tile` of them a tile; none without an output.

@@ -20,8 +20,8 @@ constexpr int kThreads = kConsumers + 128;
 constexpr int kWBytes = kTileRows * kBlock;
 constexpr int kBuffers = 4;                     // of sums in TMEM, 128 columns apart
 constexpr int kScaleSlots = 4;                  // of the ring of scales
-constexpr int kChunk = 16;                      // columns that a group has in the end, of 2 * kChunk
 constexpr int kMostStages = 6;
+constexpr int kMostSplit = 8;                   // CTAs of a cluster that share an item
 
 // COLS: rows of x that are columns of a product, at most. LANES: tiles of more rows have them as lanes.
 template <int COLS, bool LANES>
@@ -35,8 +35,9 @@ struct Shape {
     static constexpr int kStageBytes = kWBytes + kRows * kBlock;
     static constexpr int kStages = 192 * 1024 / kStageBytes < kMostStages ? 192 * 1024 / kStageBytes : kMostStages;
     static constexpr int kScales = kScaleSlots * kScaleBlocks * kScaleStep;   // floats
-    static constexpr int kJoin = 2 * kChunk * 128;
-    static constexpr int kMost = 4 * 128 + 2 * kParts * COLS + 2 * COLS;
+    static constexpr int kChunk = LANES ? 8 : 16;                // columns whose sums meet at a time
+    static constexpr int kJoin = kGroups * 2 * kChunk * 128;
+    static constexpr int kMost = 4 * 128;
     static constexpr int kShared = 1024 + kStages * kStageBytes + (kScales + kJoin + kMost) * 4 + 512 + static_cast<int>(sizeof(Tables));
     static_assert(kShared <= 227 * 1024 - 256, "");
 };
@@ -56,17 +57,16 @@ __device__ __forceinline__ float power_of_two(float s) {
 // SWIGLU: y = silu(gate) * up.
 template <int COLS, bool LANES, bool SWIGLU>
 __global__ void __launch_bounds__(kThreads, 1)
-    expert_fp8_kernel(Fp8Args a, TilePlan plan, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map) {
+    expert_fp8_kernel(Fp8Args a, TilePlan plan, int split, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map) {
     using S = Shape<COLS, LANES>;
-    constexpr int kScaleBlocks = S::kScaleBlocks;
+    constexpr int kScaleBlocks = S::kScaleBlocks, kChunk = S::kChunk;
     extern __shared__ unsigned char shared_bytes[];
     unsigned char* const ring = shared_bytes + (1024 - smem_addr(shared_bytes) % 1024) % 1024;
     float* const scales = reinterpret_cast<float*>(ring + S::kStages * S::kStageBytes);   // [kScaleSlots][kScaleBlocks][kScaleStep]
-    float* const join = scales + S::kScales;                                              // [kGroups][kChunk][128]
-    float* const most = join + S::kJoin;                                                  // the largest: [2][2][128] rows as lanes,
-    float* const column_most = most + 4 * 128;                                            // [2 halves][kParts][COLS] as columns
-    float* const found = column_most + 2 * kParts * COLS;                                 // [2 halves][COLS]: the output's scales
-    uint64_t* const barriers = reinterpret_cast<uint64_t*>(found + 2 * COLS);
+    float* const join = scales + S::kScales;                                              // [kGroups][2 halves][kChunk][128]
+    // the largest: [2][2][128] of rows as lanes; [kGroups][2][2 halves][kParts] of rows as columns
+    float* const most = join + S::kJoin;
+    uint64_t* const barriers = reinterpret_cast<uint64_t*>(most + S::kMost);
     const uint32_t full = smem_addr(barriers), empty = full + 8 * kMostStages;
     const uint32_t sums_full = empty + 8 * kMostStages, sums_empty = sums_full + 8 * kBuffers;
     const uint32_t scales_full = sums_empty + 8 * kBuffers, scales_empty = scales_full + 8 * kScaleSlots;
@@ -77,6 +77,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int warp_sum[kThreads / 32];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (warp == kScaler && elected()) {
+        prefetch_map(&w_map);
+        prefetch_map(&x_map);
+    }
     if (warp == kLoader) {
         tmem_alloc_one(smem_addr(tmem_at));
         if (lane == 0) {
@@ -105,6 +109,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool leader = elected();
     const int blocks = a.I / kBlock, cols = SWIGLU ? a.O / 2 : a.O;
     const int64_t items = tile_count(a.g, plan, table);
+    // CTAs of a cluster that share items have one each at most, of which each takes some of the blocks.
+    const int sharer = split > 1 ? cluster_rank() : 0;
+    const int block0 = static_cast<int>(static_cast<int64_t>(blocks) * sharer / split), block1 = static_cast<int>(static_cast<int64_t>(blocks) * (sharer + 1) / split);
+    const int64_t item0 = blockIdx.x / split, item_step = split > 1 ? items : gridDim.x;
 
     // First channel of an item's halves (of gate and up they are the same ones), and their first weight rows.
     const auto channel = [&](int m, int half) { return SWIGLU ? m * 128 : m * kTileRows + half * 128; };
@@ -266,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             consumers_sync();   // (`most` is written again)
         };
-        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        for (int64_t i = item0; i < items; i += item_step) {
             const Tile it = tile_at(a.g, plan, table, i);
             if constexpr (LANES) {
                 if (it.rows > COLS) {
@@ -282,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t acc[2][COLS / 2];   // columns 2 n, 2 n + 1; the groups take every other block each
 #pragma unroll
             for (int n = 0; n < COLS / 2; ++n) acc[0][n] = acc[1][n] = 0;
-            for (int b = 0; b < blocks; ++b) {
+            for (int b = 0; b < block1 - block0; ++b) {
                 if (b % kScaleBlocks == 0) barrier_wait_inline(scales_full + 8 * slot, scales_parity, dead);
                 if (b % kGroups == group) {
                     const float* sx = scales + (slot * kScaleBlocks + b % kScaleBlocks) * S::kScaleStep;
@@ -315,95 +323,94 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (b % kScaleBlocks == kScaleBlocks - 1 || b + 1 == blocks) {
+                if (b % kScaleBlocks == kScaleBlocks - 1 || b + 1 == block1 - block0) {
                     if (lane == 0) barrier_arrive(scales_empty + 8 * slot);
                     if (++slot == kScaleSlots) slot = 0, scales_parity ^= 1;
                 }
                 parities ^= 1u << buffer;
                 buffer = (buffer + 1) % kBuffers;
             }
-            // The groups' sums meet, of 2 * kChunk columns at a time: the first group has the first kChunk of them in the end,
-            // the second the others. results[k][.]: column (2 k + group) * kChunk on.
-            constexpr int kHalves = SWIGLU ? 1 : 2, kPairs = COLS / (2 * kChunk);
-            float results[kPairs][kHalves][kChunk];
-#pragma unroll
-            for (int k = 0; k < kPairs; ++k) {
-                if (2 * k * kChunk >= there) continue;
-                float gate[kChunk];
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float own[kChunk];
-#pragma unroll
-                    for (int n = 0; n < kChunk; n += 2) {   // (constant places in registers, whichever group it is)
-                        const float2 p = apart(acc[half][(2 * k * kChunk + n) / 2]), q = apart(acc[half][((2 * k + 1) * kChunk + n) / 2]);
-                        own[n] = group == 0 ? p.x : q.x, own[n + 1] = group == 0 ? p.y : q.y;
-                        float* to = join + ((group ^ 1) * kChunk + n) * 128 + part * 32 + lane;
-                        to[0] = group == 0 ? q.x : p.x, to[128] = group == 0 ? q.y : p.y;
-                    }
-                    consumers_sync();
-#pragma unroll
-                    for (int n = 0; n < kChunk; ++n) {
-                        float v = own[n] + join[(group * kChunk + n) * 128 + part * 32 + lane];
-                        if (*dead) v = __int_as_float(0x7fffffff);
-                        if (!SWIGLU) results[k][half % kHalves][n] = v;
-                        else if (half == 0) gate[n] = v;
-                        else results[k][0][n] = silu(gate[n]) * v;
-                    }
-                    consumers_sync();
+            // The groups' sums meet in shared memory, kChunk columns at a time; then a group finishes every other column. (Loops
+            // that are not unrolled: of a small call most of the time would go into fetching the code.)
+            const int chan = part * 32 + lane;
+            int turn = 0;
+            const auto finish = [&](int column, float one, float two) {   // the two halves' sums of this thread's channels
+                if (SWIGLU) one = silu(one) * two;
+                const int64_t row = static_cast<int64_t>(it.row) + column;
+                if (a.y_dtype != EP_DTYPE_FP8_E4M3) {
+                    uint16_t* to = static_cast<uint16_t*>(a.y) + row * a.y_ld;
+                    const auto code = [&](float v) {
+                        return a.y_dtype == EP_DTYPE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+                    };
+                    if (first < cols) to[first] = code(one);
+                    if (!SWIGLU && second < cols) to[second] = code(two);
+                    return;
                 }
-            }
-            const auto column = [&](int k, int n) { return (2 * k + group) * kChunk + n; };
-            if (a.y_dtype != EP_DTYPE_FP8_E4M3) {
-                const bool bf16 = a.y_dtype == EP_DTYPE_BF16;
-#pragma unroll
-                for (int k = 0; k < kPairs; ++k)
-#pragma unroll
-                    for (int half = 0; half < kHalves; ++half) {
-                        const int chan = half == 0 ? first : second;
-                        uint16_t* to = static_cast<uint16_t*>(a.y) + (static_cast<int64_t>(it.row) + column(k, 0)) * a.y_ld + chan;
-                        if (chan >= cols) continue;
-#pragma unroll
-                        for (int n = 0; n < kChunk; ++n, to += a.y_ld)
-                            if (column(k, n) < it.rows)
-                                *to = bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(results[k][half][n]))
-                                           : __half_as_ushort(__float2half_rn(results[k][half][n]));
-                    }
-                continue;
-            }
-            // ---- e4m3: the largest of each column's 128 channels, its scale, codes
-#pragma unroll
-            for (int k = 0; k < kPairs; ++k)
-#pragma unroll
-                for (int half = 0; half < kHalves; ++half)
-#pragma unroll
-                    for (int n = 0; n < kChunk; ++n) {
-                        if (column(k, n) >= it.rows) continue;
-                        // (of numbers that are not negative the bits compare as they do; columns are a multiple of 128)
-                        const uint32_t big = __reduce_max_sync(kFullMask, __float_as_uint(fabsf(results[k][half][n])));
-                        if (lane == 0) column_most[(half * kParts + part) * COLS + column(k, n)] = __uint_as_float(big);
-                    }
-            consumers_sync();
-            if (tid < kHalves * COLS && tid % COLS < it.rows) {
-                const int half = tid / COLS, n = tid % COLS, chan = channel(it.m, half);
-                float big = 0.0f;
-                for (int w = 0; w < kParts; ++w) big = larger(column_most[(half * kParts + w) * COLS + n], big);
-                const float s = output_scale(big);
-                found[tid] = s;
-                if (chan < cols) write_scale(static_cast<int64_t>(it.row) + n, chan / kBlock, s);
-            }
-            consumers_sync();
-#pragma unroll
-            for (int k = 0; k < kPairs; ++k)
-#pragma unroll
-                for (int half = 0; half < kHalves; ++half) {
-                    const int chan = half == 0 ? first : second;
-                    if (chan >= cols) continue;
-                    uint8_t* to = static_cast<uint8_t*>(a.y) + (static_cast<int64_t>(it.row) + column(k, 0)) * a.y_ld + chan;
-#pragma unroll
-                    for (int n = 0; n < kChunk; ++n, to += a.y_ld)
-                        if (column(k, n) < it.rows)
-                            *to = static_cast<uint8_t>(codes(make_float2(results[k][half][n], 0.0f), found[half * COLS + column(k, n)]));
+                // e4m3: the largest of 128 channels (of numbers that are not negative the bits compare as they do)
+                float* const big = most + (group * 2 + turn) * 2 * kParts;
+                turn ^= 1;
+                const uint32_t of_one = __reduce_max_sync(kFullMask, __float_as_uint(fabsf(one)));
+                const uint32_t of_two = SWIGLU ? 0u : __reduce_max_sync(kFullMask, __float_as_uint(fabsf(two)));
+                if (lane == 0) big[part] = __uint_as_float(of_one), big[kParts + part] = __uint_as_float(of_two);
+                asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
+                for (int half = 0; half < (SWIGLU ? 1 : 2); ++half) {
+                    const float* b = big + half * kParts;
+                    const float s = output_scale(larger(larger(b[0], b[1]), larger(b[2], b[3])));
+                    const int to = half == 0 ? first : second;   // (columns are a multiple of 128)
+                    if (to >= cols) continue;
+                    if (chan == 0) write_scale(row, to / kBlock, s);
+                    static_cast<uint8_t*>(a.y)[row * a.y_ld + to] = static_cast<uint8_t>(codes(make_float2(half == 0 ? one : two, 0.0f), s));
                 }
+            };
+            float* const meet = reinterpret_cast<float*>(ring) + chan;   // [2 halves][COLS][128], of a shared item
+#pragma unroll 1
+            for (int k = 0; k * kChunk < there; ++k) {
+#pragma unroll
+                for (int c = 0; c < COLS; c += kChunk) {   // (constant places in registers)
+                    if (c != k * kChunk) continue;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int n = 0; n < kChunk; n += 2) {
+                            const float2 v = apart(acc[half][(c + n) / 2]);
+                            float* to = join + ((group * 2 + half) * kChunk + n) * 128 + chan;
+                            to[0] = v.x, to[128] = v.y;
+                        }
+                }
+                consumers_sync();
+#pragma unroll 1
+                for (int n = group; n < kChunk && k * kChunk + n < it.rows; n += kGroups) {
+                    const float* from = join + n * 128 + chan;
+                    float one = from[0] + from[2 * kChunk * 128], two = from[kChunk * 128] + from[3 * kChunk * 128];
+                    if (*dead) one = two = __int_as_float(0x7fffffff);
+                    if (split == 1) {
+                        finish(k * kChunk + n, one, two);
+                    } else {
+                        meet[(k * kChunk + n) * 128] = one;
+                        meet[(COLS + k * kChunk + n) * 128] = two;
+                    }
+                }
+                consumers_sync();
+            }
+            if (!LANES && split > 1) {   // each CTA has every split-th column (the ring is used up: the cluster has one item)
+                __syncwarp();
+                cluster_sync();
+#pragma unroll 1
+                for (int column = sharer + split * group; column < it.rows; column += split * kGroups) {
+                    float one[kMostSplit], two[kMostSplit], sum[2] = {0.0f, 0.0f};   // (all on their way before the first is needed)
+#pragma unroll
+                    for (int q = 0; q < kMostSplit; ++q) {
+                        const uint32_t from = in_cta(smem_addr(meet + column * 128), min(q, split - 1));
+                        one[q] = q < split ? load_cluster(from) : 0.0f;
+                        two[q] = q < split ? load_cluster(from + COLS * 512) : 0.0f;
+                    }
+#pragma unroll
+                    for (int q = 0; q < kMostSplit; ++q) sum[0] += one[q], sum[1] += two[q];
+                    finish(column, sum[0], sum[1]);
+                }
+                __syncwarp();
+                cluster_sync();
+            }
         }
     } else {
         if constexpr (S::kMoved) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -412,10 +419,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (leader) {
                 int slot = 0;
                 uint32_t parity = 1;   // (the first round of the ring waits for nothing)
-                for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+                for (int64_t i = item0; i < items; i += item_step) {
                     const Tile it = tile_at(a.g, plan, table, i);
                     const int x_boxes = (max(it.rows, 1) + S::kBox - 1) / S::kBox;
-                    for (int b = 0; b < blocks; ++b) {
+                    for (int b = block0; b < block1; ++b) {
                         const uint32_t bar = full + 8 * slot, at_w = smem_addr(ring) + slot * S::kStageBytes, at_x = at_w + kWBytes;
                         barrier_wait_inline(empty + 8 * slot, parity, dead);
                         barrier_expect(bar, kWBytes + x_boxes * S::kBox * kBlock);
@@ -433,11 +440,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t base = (1u << 4) | (128u / 16 << 24);   // fp32 sums, 128 lanes
                 int slot = 0, buffer = 0;
                 uint32_t parity = 0, parities = 15;   // parities: a bit for each buffer of sums
-                for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+                for (int64_t i = item0; i < items; i += item_step) {
                     const Tile it = tile_at(a.g, plan, table, i);
                     const bool lanes = LANES && it.rows > COLS;
                     const uint32_t shape = base | (lanes ? e5m2 << 7 : e5m2 << 10) | static_cast<uint32_t>((lanes ? 256 : columns_of(it.rows)) / 8) << 17;
-                    for (int b = 0; b < blocks; ++b) {
+                    for (int b = block0; b < block1; ++b) {
                         if (lanes) {
                             buffer = (buffer + 1) & 2;   // an even one and the next
                             barrier_wait_inline(sums_empty + 8 * buffer + 8, (parities >> (buffer + 1)) & 1, dead);
@@ -480,19 +487,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int wk = lane / 4 % kScaleBlocks, wj = lane % 4;   // the first lanes load the weights' scales: block, which one
             const auto row_of = [&](int j) { return by_rows ? j * (32 / kScaleBlocks) + lane / kScaleBlocks : j * 32 % S::kRows + lane; };
             const auto block_of = [&](int j) { return by_rows ? lane % kScaleBlocks : j * 32 / S::kRows; };
-            for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+            for (int64_t i = item0; i < items; i += item_step) {
                 const Tile it = tile_at(a.g, plan, table, i);
                 const bool lanes = LANES && it.rows > COLS;
                 const int o = lanes ? weight_row(it.m, wj / 2) + wj % 2 * 64 : wj == 0 ? weight_row(it.m, 0) : weight_row(it.m, 1) + (wj - 1) * 128;
                 const float* w_scales = a.w_scales + (static_cast<int64_t>(it.expert) * scale_rows + min(o / kBlock, scale_rows - 1)) * blocks;
-                for (int b = 0; b < blocks; b += kScaleBlocks) {
+                for (int b = block0; b < block1; b += kScaleBlocks) {
                     if (turn == 0) {
                         float v[kEach];
 #pragma unroll
                         for (int j = 0; j < kEach; ++j) {
                             const int n = row_of(j), k = block_of(j);
                             v[j] = 0.0f;
-                            if (n < it.rows && b + k < blocks) {
+                            if (n < it.rows && b + k < block1) {
                                 const int64_t from = (static_cast<int64_t>(it.row) + n) * a.x_scale_row + (b + k) * a.x_scale_block;
                                 v[j] = a.x_ue8m0 ? ue8m0(static_cast<const uint8_t*>(a.x_scales)[from]) : static_cast<const float*>(a.x_scales)[from];
                             }
@@ -512,6 +519,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
+    if (warp >= kLoader && split > 1 && item0 < items) {   // (as the consumers do)
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
+    }
     tmem_fence_before();
     __syncthreads();
     if (warp == kLoader) {
@@ -523,9 +535,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int COLS, bool LANES, bool SWIGLU>
 cudaError_t launch_shape(const Fp8Args& a, cudaStream_t stream) {
     using S = Shape<COLS, LANES>;
-    static int known[64];
-    int sms = 0;
-    cudaError_t err = prepare_persistent(expert_fp8_kernel<COLS, LANES, SWIGLU>, S::kShared, known, &sms);
+    static ClusterRoom known[64];
+    static int ready[64];
+    ClusterRoom room{};
+    cudaError_t err = cluster_room(expert_fp8_kernel<COLS, LANES, SWIGLU>, kThreads, S::kShared, known, ready, &room);
     if (err != cudaSuccess) return err;
     const int64_t I = a.I, O = a.O, E = a.g.E;
     const int cols = SWIGLU ? a.O / 2 : a.O;
@@ -542,8 +555,12 @@ cudaError_t launch_shape(const Fp8Args& a, cudaStream_t stream) {
     if (err != cudaSuccess) return err;
     const int64_t used = a.g.rows < a.g.E ? a.g.rows : a.g.E;
     const int64_t most = (a.g.rows + used * (p.cap - 1)) / p.cap * p.m_tiles;
-    return launch_dependent(expert_fp8_kernel<COLS, LANES, SWIGLU>, dim3(static_cast<unsigned>(most < sms ? most : sms)), dim3(kThreads),
-                            S::kShared, stream, a, p, w_map, x_map);
+    // few items are shared by the CTAs of clusters, all at once on the device
+    int split = 1;
+    for (int i = 1; !LANES && split < kMostSplit && 2 * split <= a.I / kBlock && most <= room.clusters[i]; ++i) split *= 2;
+    const int64_t clusters = most < room.clusters[0] / split ? most : room.clusters[0] / split;
+    return launch_clusters(expert_fp8_kernel<COLS, LANES, SWIGLU>, static_cast<int>(clusters), split, kThreads, S::kShared, stream, a, p, split,
+                           w_map, x_map);
 }
 
 template <bool SWIGLU>

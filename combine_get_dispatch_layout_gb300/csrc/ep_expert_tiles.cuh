@@ -135,6 +135,9 @@ __device__ __forceinline__ Tile tile_at(const ExpertRows& g, const TilePlan& p, 
 // Columns of the product for n rows of a tile.
 __device__ __forceinline__ int columns_of(int n) { return max((n + 15) / 16 * 16, 16); }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void tmem_alloc_one(uint32_t to) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(to) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -152,10 +155,10 @@ __device__ __forceinline__ void multiply_one(uint32_t sums, uint64_t a, uint64_t
 // ---- pairs: two CTAs of a cluster multiply as one, operand A's 256 rows and operand B's columns half in each. The first
 // issues for both; each has the sums of its own 128 rows in its TMEM.
 
-__device__ __forceinline__ uint32_t pair_rank() {
+__device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r & 1;
+    return r;
 }
 // Address, for the cluster, of the same place in a CTA's shared memory.
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
@@ -164,8 +167,10 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
     return r;
 }
 __device__ __forceinline__ uint32_t in_first(uint32_t addr) { return in_cta(addr, 0); }
-__device__ __forceinline__ void store_other(uint32_t addr, uint32_t rank, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(in_cta(addr, rank)), "f"(v) : "memory");
+__device__ __forceinline__ float load_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 // On a barrier of either CTA. (It orders no memory but, behind the tcgen05 fence, the tensor memory that has been read:
 // as a release for the CTA it held the thread for 1000 clocks, for the cluster for 2000.)
@@ -284,54 +289,52 @@ cudaError_t box_map(CUtensorMap* map, const void* base, int dtype, int64_t x, in
                : cudaErrorInvalidValue;
 }
 
-// SMs of the current device, with the kernel's shared memory limit raised: looked up once per device (a race writes
-// the same value).
-template <typename Kernel>
-cudaError_t prepare_persistent(Kernel kernel, int smem, int* known, int* sms) {
-    constexpr int kDevices = 64;
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    if (dev < kDevices && (*sms = __atomic_load_n(&known[dev], __ATOMIC_ACQUIRE)) > 0) return cudaSuccess;
-    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (err == cudaSuccess) err = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-    if (err == cudaSuccess && dev < kDevices) __atomic_store_n(&known[dev], *sms, __ATOMIC_RELEASE);
-    return err;
-}
+// Clusters of 1, 2, 4 and 8 CTAs of a kernel that a device holds at once.
+struct ClusterRoom {
+    int clusters[4];
+};
 
-// Pairs of CTAs of a kernel that the current device holds at once, with the kernel's shared memory limit raised: looked up
-// once per device (a race writes the same value).
+// Of the current device, with the kernel's shared memory limit raised: looked up once per device (a race writes the same
+// values, `ready` after them).
 template <typename Kernel>
-cudaError_t pairs_at_once(Kernel kernel, int threads, int smem, int* known, int* pairs) {
+cudaError_t cluster_room(Kernel kernel, int threads, int smem, ClusterRoom* known, int* ready, ClusterRoom* room) {
     constexpr int kDevices = 64;
     int dev = 0, sms = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
-    if (dev < kDevices && (*pairs = __atomic_load_n(&known[dev], __ATOMIC_ACQUIRE)) > 0) return cudaSuccess;
+    if (dev < kDevices && __atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE)) {
+        *room = known[dev];
+        return cudaSuccess;
+    }
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (err != cudaSuccess) return err;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(sms / 2 * 2);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    err = cudaOccupancyMaxActiveClusters(pairs, kernel, &cfg);
-    if (err == cudaSuccess && *pairs < 1) err = cudaErrorInvalidConfiguration;
-    if (err == cudaSuccess && dev < kDevices) __atomic_store_n(&known[dev], *pairs, __ATOMIC_RELEASE);
+    room->clusters[0] = sms;
+    for (int i = 1; i < 4 && err == cudaSuccess; ++i) {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 1 << i;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(sms >> i << i);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        err = cudaOccupancyMaxActiveClusters(&room->clusters[i], kernel, &cfg);
+    }
+    if (err == cudaSuccess && room->clusters[1] < 1) err = cudaErrorInvalidConfiguration;
+    if (err == cudaSuccess && dev < kDevices) {
+        known[dev] = *room;
+        __atomic_store_n(&ready[dev], 1, __ATOMIC_RELEASE);
+    }
     return err;
 }
 
-// Launches `pairs` clusters of two CTAs as a programmatic dependent of the work before.
+// Launches clusters of `size` CTAs as a programmatic dependent of the work before.
 template <typename... Params, typename... Args>
-cudaError_t launch_pairs(void (*kernel)(Params...), int pairs, int threads, int smem, cudaStream_t stream, Args... args) {
+cudaError_t launch_clusters(void (*kernel)(Params...), int clusters, int size, int threads, int smem, cudaStream_t stream, const Args&... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * pairs);
+    cfg.gridDim = dim3(clusters * size);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -339,10 +342,10 @@ cudaError_t launch_pairs(void (*kernel)(Params...), int pairs, int threads, int 
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.x = size;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = size > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

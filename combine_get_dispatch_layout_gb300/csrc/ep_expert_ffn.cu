@@ -40,7 +40,7 @@ struct Gemm {
     TilePlan plan;
     int lanes;           // channels of the output
     int inner;           // contraction (of kGradW: the expert's rows instead)
-    int columns;         // kGradW: rows of the output
+    int columns;         // kGradW: length of the output's rows, which are the lanes
     int n_tiles;         // kGradW: tiles of them
     int atoms;           // kStep deep parts of a stage (kGradW: 1)
     int stages, stage_bytes, atom_bytes, box;   // box: rows of a box of operand B (kGradW: of both)
@@ -51,7 +51,7 @@ struct Gemm {
     int out_fp32, accumulate;       // kGradW
 };
 
-// An item: `cols` columns (rows of the output) from `col` on, lanes from m * kLanes on, `steps` stages; of kGradW the
+// An item: `cols` columns (rows of the output; of kGradW places in its rows) from `col` on, lanes from m * kLanes on, `steps` stages; of kGradW the
 // contraction is over rows [row, row + rows).
 struct Item {
     int expert, m, col, cols, row, rows, steps;
@@ -298,9 +298,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         const auto half_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); };
         int buffer = 0, chunk = 0;
         uint32_t parity = 0;
+        const auto release = [&] {   // the buffer of sums
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) barrier_arrive_pair(in_first(sums_empty + 8 * buffer));
+            buffer ^= 1;
+            if (buffer == 0) parity ^= 1;
+        };
+        // Weight gradients: a thread has a row of the output and kWide neighbouring places of it at a time. Rows of 16 bits go
+        // through shared memory, so that four lanes write 64 bytes of one; its 16-byte pieces are swapped by row against
+        // bank conflicts.
+        const auto weight_gradients = [&](const Gemm& a, const Item& it, uint32_t mine, int tile) {
+            constexpr int kWide = 32;
+            static_assert(128 * kWide * 2 <= kHalfBytes, "");
+            if (it.steps > 0) {
+                barrier_wait(sums_full + 8 * buffer, parity, dead);
+                tmem_fence_after();
+            }
+            const int64_t first = static_cast<int64_t>(it.expert) * a.lanes + tile;   // the CTA's first row
+            const int rows = a.lanes - tile, r = part * 32 + lane;
+            for (int c0 = half * kWide; c0 < it.cols; c0 += 2 * kWide) {
+                uint32_t raw[kWide];
+                if (it.steps > 0) {
+                    tmem_load32(mine + c0, raw);
+                    tmem_loaded(raw);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kWide; ++j) raw[j] = 0;
+                }
+                if (*dead) {
+#pragma unroll
+                    for (int j = 0; j < kWide; ++j) raw[j] = 0x7fffffff;
+                }
+                const int many = min(kWide, it.cols - c0);   // (a multiple of 8)
+                if (a.out_fp32) {
+                    float* to = static_cast<float*>(a.out) + (first + r) * a.columns + it.col + c0;
+#pragma unroll
+                    for (int j = 0; j < kWide; j += 4) {
+                        if (r >= rows || j >= many) continue;
+                        float4 v = make_float4(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1]), __uint_as_float(raw[j + 2]), __uint_as_float(raw[j + 3]));
+                        if (a.accumulate) {
+                            const float4 old = *reinterpret_cast<const float4*>(to + j);
+                            v.x += old.x, v.y += old.y, v.z += old.z, v.w += old.w;
+                        }
+                        *reinterpret_cast<float4*>(to + j) = v;
+                    }
+                    continue;
+                }
+#pragma unroll
+                for (int q = 0; q < kWide / 8; ++q) {
+                    Vec8<T> v;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v.v[j] = from_float<T>(__uint_as_float(raw[8 * q + j]));
+                    if (a.accumulate && r < rows && 8 * q < many) {
+                        Vec8<T> old;
+                        old.raw = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.out) + (first + r) * a.columns + it.col + c0 + 8 * q);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v.v[j] = from_float<T>(to_float(old.v[j]) + __uint_as_float(raw[8 * q + j]));
+                    }
+                    *reinterpret_cast<uint4*>(out + r * (2 * kWide) + (q ^ (r >> 1 & 3)) * 16) = v.raw;
+                }
+                half_sync();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int row = k * 32 + (tid & 127) / 4, q = tid % 4;
+                    if (row < rows && 8 * q < many)
+                        *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (first + row) * a.columns + it.col + c0 + 8 * q) =
+                            *reinterpret_cast<const uint4*>(out + row * (2 * kWide) + (q ^ (row >> 1 & 3)) * 16);
+                }
+                half_sync();   // (there is no second place)
+            }
+        };
         walk([&](auto kind, const Gemm& a, const CUtensorMap&, const CUtensorMap&, int64_t start, int64_t items) {
         constexpr int WHAT = decltype(kind)::value;
-        const bool staged = WHAT != kGradW || !(a.out_fp32 || a.accumulate);
         // kGradAct: this thread's pieces of gate's and up's rows of a chunk of columns
         uint4 ahead[4] = {};
         const auto fetch = [&](const Item& it, int c0, int chan0, int bytes) {
@@ -318,46 +388,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the CTA's first channel, this thread's; of gate and up a warp's lanes are 16 gate and 16 up rows
             const int tile = it.m * kLanes + rank * (kLanes / 2), chan0 = WHAT == kGateUp ? tile / 2 : tile;
             const int chan = WHAT == kGateUp ? chan0 + part * 16 + (lane & 15) : chan0 + part * 32 + lane;
-            const bool real = chan < a.lanes;
             const int bytes = min(WHAT == kGateUp ? 64 : 128, a.lanes - chan0) * 2;   // of a row of this CTA (a multiple of 16)
             if (WHAT == kGradAct && half * kChunk < it.cols) fetch(it, half * kChunk, chan0, bytes);
-            if (it.steps > 0) {
-                barrier_wait(sums_full + 8 * buffer, parity, dead);
-                tmem_fence_after();
+            if constexpr (WHAT == kGradW) {
+                weight_gradients(a, it, mine, tile);
+                if (it.steps > 0) release();
+                continue;
             }
+            barrier_wait(sums_full + 8 * buffer, parity, dead);
+            tmem_fence_after();
             for (int c0 = half * kChunk; c0 < it.cols; c0 += 2 * kChunk, ++chunk) {
                 uint32_t raw[kChunk];
-                if (it.steps > 0) {
-                    tmem_load16(mine + c0, raw);
-                    tmem_loaded(raw);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kChunk; ++j) raw[j] = 0;
-                }
+                tmem_load16(mine + c0, raw);
+                tmem_loaded(raw);
                 if (*dead) {
 #pragma unroll
                     for (int j = 0; j < kChunk; ++j) raw[j] = 0x7fffffff;
                 }
                 const int many = min(kChunk, it.cols - c0);
-                if (WHAT == kGradW && !staged) {
-                    if (real) {
-                        const int64_t at = (static_cast<int64_t>(it.expert) * a.columns + it.col + c0) * a.out_ld + chan;
-#pragma unroll
-                        for (int j = 0; j < kChunk; ++j)
-                            if (j < many) {
-                                float v = __uint_as_float(raw[j]);
-                                if (a.out_fp32) {
-                                    float* to = static_cast<float*>(a.out) + at + j * a.out_ld;
-                                    *to = a.accumulate ? *to + v : v;
-                                } else {
-                                    T* to = static_cast<T*>(a.out) + at + j * a.out_ld;
-                                    *to = from_float<T>(to_float(*to) + v);
-                                }
-                            }
-                    }
-                    continue;
-                }
-                const int64_t row0 = WHAT == kGradW ? static_cast<int64_t>(it.expert) * a.columns + it.col + c0 : static_cast<int64_t>(it.row) + c0;
+                const int64_t row0 = static_cast<int64_t>(it.row) + c0;
                 const int place = WHAT == kGradAct ? 0 : chunk & 1;   // (kGradAct has both places: gate and up, or their gradients)
                 unsigned char* const to = out + place * (kChunk * kRowBytes);
                 unsigned char* const act_to = act_out + place * (kChunk * kActBytes);
@@ -424,13 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if constexpr (WHAT == kGradAct) half_sync();   // (there is no second place)
                 }
             }
-            if (it.steps > 0) {
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) barrier_arrive_pair(in_first(sums_empty + 8 * buffer));
-                buffer ^= 1;
-                if (buffer == 0) parity ^= 1;
-            }
+            release();
         }
         });
     }
@@ -521,19 +564,19 @@ cudaError_t forward(const FfnArgs& f, cudaStream_t stream) {
     return err == cudaSuccess ? launch_gemms<T, kDown, kNone>(p, none, stream) : err;
 }
 
-// dW [E][columns][lanes] = (by [rows][columns])^T x [rows][lanes]
-cudaError_t weight_gradient(Operands* p, const FfnArgs& f, void* out, const void* x, int lanes, int64_t x_ld, const void* by, int columns,
+// dW [E][outputs][inputs] = (by [rows][outputs])^T x [rows][inputs]: the outputs are the lanes
+cudaError_t weight_gradient(Operands* p, const FfnArgs& f, void* out, const void* x, int inputs, int64_t x_ld, const void* by, int outputs,
                             int64_t by_ld) {
-    Gemm& a = p->gemm = gemm_of(f, out, lanes, lanes, kLanes, 0);
+    Gemm& a = p->gemm = gemm_of(f, out, inputs, outputs, kLanes, 0);
     if (!out) return cudaSuccess;
     const int mean = f.g.rows / f.g.E;
     a.box = mean < 32 ? 16 : mean < 256 ? 32 : 64;
     a.plan.cap = 256;
-    a.columns = columns;
-    a.n_tiles = ceil_div(columns, a.plan.cap);
+    a.columns = inputs;
+    a.n_tiles = ceil_div(inputs, a.plan.cap);
     a.out_fp32 = f.grad_w_fp32, a.accumulate = f.accumulate;
-    const cudaError_t err = rows_map(&p->a_map, f, x, lanes, x_ld, a.box);
-    return err == cudaSuccess ? rows_map(&p->b_map, f, by, columns, by_ld, a.box) : err;
+    const cudaError_t err = rows_map(&p->a_map, f, by, outputs, by_ld, a.box);
+    return err == cudaSuccess ? rows_map(&p->b_map, f, x, inputs, x_ld, a.box) : err;
 }
 
 // Two launches of two products each that do not depend on each other: their ends and starts cost once.

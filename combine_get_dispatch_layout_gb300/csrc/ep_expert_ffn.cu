@@ -164,47 +164,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             int slot = 0;
             uint32_t parity = 1;   // (the first round of the ring waits for nothing)
             walk([&](auto kind, const Gemm& a, const CUtensorMap& a_map, const CUtensorMap& b_map, int64_t start, int64_t items) {
-              constexpr int WHAT = decltype(kind)::value;
-              for (int64_t i = start; i < items; i += pairs) {
-                const Item it = item_at<WHAT>(a, table, i, items);
-                const int half = columns_of(it.cols) / 2;   // columns of each CTA
-                const int b_boxes = WHAT == kGradW ? (half + 63) / 64 : (half + a.box - 1) / a.box;
-                const int lane0 = it.m * kLanes + rank * (kLanes / 2), col0 = it.col + rank * half;
-                for (int s = 0; s < it.steps; ++s) {
-                    // both CTAs' boxes count on the first one's barrier
-                    const uint32_t mine = full + 8 * slot, at_a = smem_addr(ring) + slot * a.stage_bytes, at_b = at_a + kABytes;
-                    const uint32_t bar = in_first(mine);
-                    barrier_wait_inline(empty + 8 * slot, parity, dead);
-                    if constexpr (WHAT == kGradW) {
-                        // [64 channels] x [box rows] of both operands, boxes with real rows only
-                        // (a stage that has to be cleaned first counts on a barrier of each CTA's own)
-                        const bool own = unclean<WHAT>(it, s);
-                        const uint32_t to = own ? part_full + 8 * slot : bar;
-                        const int down = (min(kStep, it.rows - s * kStep) + a.box - 1) / a.box, all = (2 + b_boxes) * down;
-                        if (rank == 0 || own) barrier_expect(own ? to : mine, all * a.box * 128 * (own ? 1 : 2));
-                        for (int k = 0; k < down; ++k) {
-                            const int row = it.row + s * kStep + k * a.box, at = k * a.box * 128;
-                            for (int j = 0; j < 2; ++j) load_box_pair(at_a + j * 8192 + at, &a_map, lane0 + j * 64, row, 0, 0, to);
-                            for (int j = 0; j < b_boxes; ++j) load_box_pair(at_b + j * 8192 + at, &b_map, col0 + j * 64, row, 0, 0, to);
-                        }
-                    } else {
-                        if (rank == 0) barrier_expect(mine, 2 * a.atoms * (kABytes + b_boxes * a.box * 128));
-                        for (int part = 0; part < a.atoms; ++part) {   // (zeros behind the contraction's end)
-                            const int k = (s * a.atoms + part) * kStep;
-                            const uint32_t to_a = at_a + part * a.atom_bytes, to_b = to_a + kABytes;
-                            if constexpr (WHAT == kGateUp) {   // the 16 gate and the 16 up rows of each warp
-                                for (int j = 0; j < 4; ++j) load_box_pair(to_a + j * 4096, &a_map, k, lane0 / 2 + j * 16, 0, it.expert, bar);
-                            } else if constexpr (WHAT == kDown) {
-                                load_box_pair(to_a, &a_map, k, lane0, 0, it.expert, bar);
-                            } else {
-                                for (int j = 0; j < 2; ++j) load_box_pair(to_a + j * 8192, &a_map, lane0 + j * 64, k, 0, it.expert, bar);
+                constexpr int WHAT = decltype(kind)::value;
+                for (int64_t i = start; i < items; i += pairs) {
+                    const Item it = item_at<WHAT>(a, table, i, items);
+                    const int half = columns_of(it.cols) / 2;   // columns of each CTA
+                    const int b_boxes = WHAT == kGradW ? (half + 63) / 64 : (half + a.box - 1) / a.box;
+                    const int lane0 = it.m * kLanes + rank * (kLanes / 2), col0 = it.col + rank * half;
+                    for (int s = 0; s < it.steps; ++s) {
+                        // both CTAs' boxes count on the first one's barrier
+                        const uint32_t mine = full + 8 * slot, at_a = smem_addr(ring) + slot * a.stage_bytes, at_b = at_a + kABytes;
+                        const uint32_t bar = in_first(mine);
+                        barrier_wait_inline(empty + 8 * slot, parity, dead);
+                        if constexpr (WHAT == kGradW) {
+                            // [64 channels] x [box rows] of both operands, boxes with real rows only
+                            // (a stage that has to be cleaned first counts on a barrier of each CTA's own)
+                            const bool own = unclean<WHAT>(it, s);
+                            const uint32_t to = own ? part_full + 8 * slot : bar;
+                            const int down = (min(kStep, it.rows - s * kStep) + a.box - 1) / a.box, all = (2 + b_boxes) * down;
+                            if (rank == 0 || own) barrier_expect(own ? to : mine, all * a.box * 128 * (own ? 1 : 2));
+                            for (int k = 0; k < down; ++k) {
+                                const int row = it.row + s * kStep + k * a.box, at = k * a.box * 128;
+                                for (int j = 0; j < 2; ++j) load_box_pair(at_a + j * 8192 + at, &a_map, lane0 + j * 64, row, 0, 0, to);
+                                for (int j = 0; j < b_boxes; ++j) load_box_pair(at_b + j * 8192 + at, &b_map, col0 + j * 64, row, 0, 0, to);
                             }
-                            for (int j = 0; j < b_boxes; ++j) load_box_pair(to_b + j * a.box * 128, &b_map, k, col0 + j * a.box, 0, 0, bar);
+                        } else {
+                            if (rank == 0) barrier_expect(mine, 2 * a.atoms * (kABytes + b_boxes * a.box * 128));
+                            for (int part = 0; part < a.atoms; ++part) {   // (zeros behind the contraction's end)
+                                const int k = (s * a.atoms + part) * kStep;
+                                const uint32_t to_a = at_a + part * a.atom_bytes, to_b = to_a + kABytes;
+                                if constexpr (WHAT == kGateUp) {   // the 16 gate and the 16 up rows of each warp
+                                    for (int j = 0; j < 4; ++j) load_box_pair(to_a + j * 4096, &a_map, k, lane0 / 2 + j * 16, 0, it.expert, bar);
+                                } else if constexpr (WHAT == kDown) {
+                                    load_box_pair(to_a, &a_map, k, lane0, 0, it.expert, bar);
+                                } else {
+                                    for (int j = 0; j < 2; ++j) load_box_pair(to_a + j * 8192, &a_map, lane0 + j * 64, k, 0, it.expert, bar);
+                                }
+                                for (int j = 0; j < b_boxes; ++j) load_box_pair(to_b + j * a.box * 128, &b_map, k, col0 + j * a.box, 0, 0, bar);
+                            }
                         }
+                        if (++slot == a.stages) slot = 0, parity ^= 1;
                     }
-                    if (++slot == a.stages) slot = 0, parity ^= 1;
                 }
-              }
             });
         }
         __syncwarp();
@@ -213,49 +213,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             int slot = 0, buffer = 0;
             uint32_t parities = 0, sums_parity = 1, clean_parity = 0;   // parities, clean_parity: a bit for each slot
             walk([&](auto kind, const Gemm& a, const CUtensorMap&, const CUtensorMap&, int64_t start, int64_t items) {
-              constexpr int WHAT = decltype(kind)::value;
-              // fp32 sums; operands' type; A outward, B outward; 256 lanes
-              constexpr uint32_t kType = std::is_same_v<T, __nv_bfloat16> ? 1u : 0u;
-              constexpr bool kAOut = WHAT >= kGradAct, kBOut = WHAT == kGradW;
-              constexpr uint32_t kShape = (1u << 4) | (kType << 7) | (kType << 10) | (kAOut ? 1u << 15 : 0u) | (kBOut ? 1u << 16 : 0u) |
-                                              (static_cast<uint32_t>(kLanes / 16) << 24);
-              for (int64_t i = start; i < items; i += pairs) {
-                const Item it = item_at<WHAT>(a, table, i, items);
-                if (it.steps == 0) continue;
-                const uint32_t shape = kShape | static_cast<uint32_t>(columns_of(it.cols) / 8) << 17;
-                const uint32_t sums = tmem + buffer * 256;
-                barrier_wait_inline(sums_empty + 8 * buffer, sums_parity, dead);
-                for (int s = 0; s < it.steps; ++s) {
-                    const uint32_t at_a = smem_addr(ring) + slot * a.stage_bytes, at_b = at_a + kABytes;
-                    const uint64_t da = kAOut ? operand_outward(at_a, 8192) : operand(at_a, 1024);
-                    const uint64_t db = kBOut ? operand_outward(at_b, 8192) : operand(at_b, 1024);
-                    if (unclean<WHAT>(it, s)) {
-                        barrier_wait_cluster(clean + 8 * slot, (clean_parity >> slot) & 1, dead);
-                        clean_parity ^= 1u << slot;
-                    } else {
-                        barrier_wait_inline(full + 8 * slot, (parities >> slot) & 1, dead);
-                        parities ^= 1u << slot;
-                    }
-                    tmem_fence_after();
-                    const int depth = WHAT == kGradW ? min((it.rows - s * kStep + 15) / 16, kStep / 16) : kStep / 16;   // products of 16
-                    if (WHAT != kGradW || depth == kStep / 16) {
-                        for (int part = 0; part < (WHAT == kGradW ? 1 : a.atoms); ++part) {
-                            const uint64_t on = part * (a.atom_bytes / 16);
-#pragma unroll
-                            for (int k = 0; k < kStep / 16; ++k)
-                                multiply_pair(sums, da + on + k * (kAOut ? 128 : 2), db + on + k * (kBOut ? 128 : 2), shape,
-                                              s > 0 || part > 0 || k > 0);
+                constexpr int WHAT = decltype(kind)::value;
+                // fp32 sums; operands' type; A outward, B outward; 256 lanes
+                constexpr uint32_t kType = std::is_same_v<T, __nv_bfloat16> ? 1u : 0u;
+                constexpr bool kAOut = WHAT >= kGradAct, kBOut = WHAT == kGradW;
+                constexpr uint32_t kShape = (1u << 4) | (kType << 7) | (kType << 10) | (kAOut ? 1u << 15 : 0u) | (kBOut ? 1u << 16 : 0u) |
+                                                  (static_cast<uint32_t>(kLanes / 16) << 24);
+                for (int64_t i = start; i < items; i += pairs) {
+                    const Item it = item_at<WHAT>(a, table, i, items);
+                    if (it.steps == 0) continue;
+                    const uint32_t shape = kShape | static_cast<uint32_t>(columns_of(it.cols) / 8) << 17;
+                    const uint32_t sums = tmem + buffer * 256;
+                    barrier_wait_inline(sums_empty + 8 * buffer, sums_parity, dead);
+                    for (int s = 0; s < it.steps; ++s) {
+                        const uint32_t at_a = smem_addr(ring) + slot * a.stage_bytes, at_b = at_a + kABytes;
+                        const uint64_t da = kAOut ? operand_outward(at_a, 8192) : operand(at_a, 1024);
+                        const uint64_t db = kBOut ? operand_outward(at_b, 8192) : operand(at_b, 1024);
+                        if (unclean<WHAT>(it, s)) {
+                            barrier_wait_cluster(clean + 8 * slot, (clean_parity >> slot) & 1, dead);
+                            clean_parity ^= 1u << slot;
+                        } else {
+                            barrier_wait_inline(full + 8 * slot, (parities >> slot) & 1, dead);
+                            parities ^= 1u << slot;
                         }
-                    } else {
-                        for (int k = 0; k < depth; ++k) multiply_pair(sums, da + k * 128, db + k * 128, shape, s > 0 || k > 0);
+                        tmem_fence_after();
+                        const int depth = WHAT == kGradW ? min((it.rows - s * kStep + 15) / 16, kStep / 16) : kStep / 16;   // products of 16
+                        if (WHAT != kGradW || depth == kStep / 16) {
+                            for (int part = 0; part < (WHAT == kGradW ? 1 : a.atoms); ++part) {
+                                const uint64_t on = part * (a.atom_bytes / 16);
+#pragma unroll
+                                for (int k = 0; k < kStep / 16; ++k)
+                                    multiply_pair(sums, da + on + k * (kAOut ? 128 : 2), db + on + k * (kBOut ? 128 : 2), shape,
+                                                  s > 0 || part > 0 || k > 0);
+                            }
+                        } else {
+                            for (int k = 0; k < depth; ++k) multiply_pair(sums, da + k * 128, db + k * 128, shape, s > 0 || k > 0);
+                        }
+                        pair_done(empty + 8 * slot);
+                        if (s + 1 == it.steps) pair_done(sums_full + 8 * buffer);
+                        if (++slot == a.stages) slot = 0;
                     }
-                    pair_done(empty + 8 * slot);
-                    if (s + 1 == it.steps) pair_done(sums_full + 8 * buffer);
-                    if (++slot == a.stages) slot = 0;
+                    buffer ^= 1;
+                    if (buffer == 0) sums_parity ^= 1;
                 }
-                buffer ^= 1;
-                if (buffer == 0) sums_parity ^= 1;
-              }
             });
         }
         __syncwarp();
@@ -265,30 +265,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             int slot = 0;
             uint32_t parities = 0;   // a bit for each slot
             walk([&](auto kind, const Gemm& a, const CUtensorMap&, const CUtensorMap&, int64_t start, int64_t items) {
-              constexpr int WHAT = decltype(kind)::value;
-              for (int64_t i = start; i < items; i += pairs) {
-                const Item it = item_at<WHAT>(a, table, i, items);
-                if constexpr (WHAT != kGradW) {
-                    slot = (slot + it.steps) % a.stages;
-                } else {
-                    for (int s = 0; s < it.steps; ++s) {
-                        if (unclean<WHAT>(it, s)) {
-                            barrier_wait_inline(part_full + 8 * slot, (parities >> slot) & 1, dead);
-                            parities ^= 1u << slot;
-                            const int left = it.rows - s * kStep, end = (left + 15) / 16 * 16, lines = 2 + (columns_of(it.cols) / 2 + 63) / 64;
-                            for (int j = lane; j < (end - left) * lines * 8; j += 32) {
-                                const int line = j / 8, row = left + line / lines;
-                                *reinterpret_cast<uint4*>(ring + slot * a.stage_bytes + line % lines * 8192 + row * 128 + j % 8 * 16) =
-                                    make_uint4(0, 0, 0, 0);
+                constexpr int WHAT = decltype(kind)::value;
+                for (int64_t i = start; i < items; i += pairs) {
+                    const Item it = item_at<WHAT>(a, table, i, items);
+                    if constexpr (WHAT != kGradW) {
+                        slot = (slot + it.steps) % a.stages;
+                    } else {
+                        for (int s = 0; s < it.steps; ++s) {
+                            if (unclean<WHAT>(it, s)) {
+                                barrier_wait_inline(part_full + 8 * slot, (parities >> slot) & 1, dead);
+                                parities ^= 1u << slot;
+                                const int left = it.rows - s * kStep, end = (left + 15) / 16 * 16, lines = 2 + (columns_of(it.cols) / 2 + 63) / 64;
+                                for (int j = lane; j < (end - left) * lines * 8; j += 32) {
+                                    const int line = j / 8, row = left + line / lines;
+                                    *reinterpret_cast<uint4*>(ring + slot * a.stage_bytes + line % lines * 8192 + row * 128 + j % 8 * 16) =
+                                        make_uint4(0, 0, 0, 0);
+                                }
+                                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                                __syncwarp();
+                                if (lane == 0) barrier_arrive_cluster(in_first(clean + 8 * slot));
                             }
-                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                            __syncwarp();
-                            if (lane == 0) barrier_arrive_cluster(in_first(clean + 8 * slot));
+                            if (++slot == a.stages) slot = 0;
                         }
-                        if (++slot == a.stages) slot = 0;
                     }
                 }
-              }
             });
         }
     } else {
@@ -336,7 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < kWide; j += 4) {
                         if (r >= rows || j >= many) continue;
-                        float4 v = make_float4(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1]), __uint_as_float(raw[j + 2]), __uint_as_float(raw[j + 3]));
+                        float4 v = make_float4(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1]), __uint_as_float(raw[j + 2]),
+                                               __uint_as_float(raw[j + 3]));
                         if (a.accumulate) {
                             const float4 old = *reinterpret_cast<const float4*>(to + j);
                             v.x += old.x, v.y += old.y, v.z += old.z, v.w += old.w;
@@ -370,111 +371,112 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         walk([&](auto kind, const Gemm& a, const CUtensorMap&, const CUtensorMap&, int64_t start, int64_t items) {
-        constexpr int WHAT = decltype(kind)::value;
-        // kGradAct: this thread's pieces of gate's and up's rows of a chunk of columns
-        uint4 ahead[4] = {};
-        const auto fetch = [&](const Item& it, int c0, int chan0, int bytes) {
-            const int piece_at = tid % 16 * 16;
+            constexpr int WHAT = decltype(kind)::value;
+            if constexpr (WHAT == kGradW) half_sync();   // (the product before may still be read from where rows go)
+            // kGradAct: this thread's pieces of gate's and up's rows of a chunk of columns
+            uint4 ahead[4] = {};
+            const auto fetch = [&](const Item& it, int c0, int chan0, int bytes) {
+                const int piece_at = tid % 16 * 16;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int j = (tid & 127) / 16 + k % 2 * 8;
-                const T* row = static_cast<const T*>(a.in) + (static_cast<int64_t>(it.row) + c0 + j) * a.in_ld + chan0 + (k < 2 ? 0 : a.lanes);
-                if (c0 + j < it.cols && piece_at < bytes) ahead[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row) + piece_at);
-            }
-        };
-        for (int64_t i = start; i < items; i += pairs) {
-            const Item it = item_at<WHAT>(a, table, i, items);
-            const uint32_t mine = tmem + buffer * 256 + (static_cast<uint32_t>(part) << 21);   // lane 32 * part, upper half
-            // the CTA's first channel, this thread's; of gate and up a warp's lanes are 16 gate and 16 up rows
-            const int tile = it.m * kLanes + rank * (kLanes / 2), chan0 = WHAT == kGateUp ? tile / 2 : tile;
-            const int chan = WHAT == kGateUp ? chan0 + part * 16 + (lane & 15) : chan0 + part * 32 + lane;
-            const int bytes = min(WHAT == kGateUp ? 64 : 128, a.lanes - chan0) * 2;   // of a row of this CTA (a multiple of 16)
-            if (WHAT == kGradAct && half * kChunk < it.cols) fetch(it, half * kChunk, chan0, bytes);
-            if constexpr (WHAT == kGradW) {
-                weight_gradients(a, it, mine, tile);
-                if (it.steps > 0) release();
-                continue;
-            }
-            barrier_wait(sums_full + 8 * buffer, parity, dead);
-            tmem_fence_after();
-            for (int c0 = half * kChunk; c0 < it.cols; c0 += 2 * kChunk, ++chunk) {
-                uint32_t raw[kChunk];
-                tmem_load16(mine + c0, raw);
-                tmem_loaded(raw);
-                if (*dead) {
-#pragma unroll
-                    for (int j = 0; j < kChunk; ++j) raw[j] = 0x7fffffff;
+                for (int k = 0; k < 4; ++k) {
+                    const int j = (tid & 127) / 16 + k % 2 * 8;
+                    const T* row = static_cast<const T*>(a.in) + (static_cast<int64_t>(it.row) + c0 + j) * a.in_ld + chan0 + (k < 2 ? 0 : a.lanes);
+                    if (c0 + j < it.cols && piece_at < bytes)
+                        ahead[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row) + piece_at);
                 }
-                const int many = min(kChunk, it.cols - c0);
-                const int64_t row0 = static_cast<int64_t>(it.row) + c0;
-                const int place = WHAT == kGradAct ? 0 : chunk & 1;   // (kGradAct has both places: gate and up, or their gradients)
-                unsigned char* const to = out + place * (kChunk * kRowBytes);
-                unsigned char* const act_to = act_out + place * (kChunk * kActBytes);
-                // 16-byte pieces of the rows: this thread's are of rows `piece / 16` and that plus 8
-                const int piece_row = (tid & 127) / 16, piece_at = tid % 16 * 16;
-                if constexpr (WHAT == kGateUp) {
-                    if (a.out2) {
-                        T* at = reinterpret_cast<T*>(to + (lane < 16 ? 0 : 128)) + part * 16 + (lane & 15);
+            };
+            for (int64_t i = start; i < items; i += pairs) {
+                const Item it = item_at<WHAT>(a, table, i, items);
+                const uint32_t mine = tmem + buffer * 256 + (static_cast<uint32_t>(part) << 21);   // lane 32 * part, upper half
+                // the CTA's first channel (of gate and up a warp's lanes are 16 gate and 16 up rows)
+                const int tile = it.m * kLanes + rank * (kLanes / 2), chan0 = WHAT == kGateUp ? tile / 2 : tile;
+                const int bytes = min(WHAT == kGateUp ? 64 : 128, a.lanes - chan0) * 2;   // of a row of this CTA (a multiple of 16)
+                if (WHAT == kGradAct && half * kChunk < it.cols) fetch(it, half * kChunk, chan0, bytes);
+                if constexpr (WHAT == kGradW) {
+                    weight_gradients(a, it, mine, tile);
+                    if (it.steps > 0) release();
+                    continue;
+                }
+                barrier_wait(sums_full + 8 * buffer, parity, dead);
+                tmem_fence_after();
+                for (int c0 = half * kChunk; c0 < it.cols; c0 += 2 * kChunk, ++chunk) {
+                    uint32_t raw[kChunk];
+                    tmem_load16(mine + c0, raw);
+                    tmem_loaded(raw);
+                    if (*dead) {
 #pragma unroll
-                        for (int j = 0; j < kChunk; ++j) at[j * (kRowBytes / 2)] = from_float<T>(__uint_as_float(raw[j]));
+                        for (int j = 0; j < kChunk; ++j) raw[j] = 0x7fffffff;
                     }
-                    T* at = reinterpret_cast<T*>(act_to + (lane >> 4) * kActBytes) + part * 16 + (lane & 15);
+                    const int many = min(kChunk, it.cols - c0);
+                    const int64_t row0 = static_cast<int64_t>(it.row) + c0;
+                    const int place = WHAT == kGradAct ? 0 : chunk & 1;   // (kGradAct has both places: gate and up, or their gradients)
+                    unsigned char* const to = out + place * (kChunk * kRowBytes);
+                    unsigned char* const act_to = act_out + place * (kChunk * kActBytes);
+                    // 16-byte pieces of the rows: this thread's are of rows `piece / 16` and that plus 8
+                    const int piece_row = (tid & 127) / 16, piece_at = tid % 16 * 16;
+                    if constexpr (WHAT == kGateUp) {
+                        if (a.out2) {
+                            T* at = reinterpret_cast<T*>(to + (lane < 16 ? 0 : 128)) + part * 16 + (lane & 15);
 #pragma unroll
-                    for (int j = 0; j < kChunk; j += 2) {   // gate lanes take the even columns, up lanes the odd ones
-                        const float own = __uint_as_float(lane < 16 ? raw[j] : raw[j + 1]);
-                        const float got = __uint_as_float(__shfl_xor_sync(kFullMask, lane < 16 ? raw[j + 1] : raw[j], 16));
-                        at[j * (kActBytes / 2)] = from_float<T>(lane < 16 ? silu(own) * got : silu(got) * own);
-                    }
-                    half_sync();
-                    const int row = (tid & 127) / 8, byte = tid % 8 * 16;
-                    if (row < many && byte < bytes)
-                        *reinterpret_cast<uint4*>(reinterpret_cast<char*>(static_cast<T*>(a.out) + (row0 + row) * a.out_ld + chan0) + byte) =
-                            *reinterpret_cast<const uint4*>(act_to + row * kActBytes + byte);
-                    if (a.out2) {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int j = piece_row + 8 * k, at_byte = piece_at & 127;
-                            T* both = static_cast<T*>(a.out2) + (row0 + j) * a.out2_ld + chan0 + (piece_at < 128 ? 0 : a.lanes);
-                            if (j < many && at_byte < bytes)
-                                *reinterpret_cast<uint4*>(reinterpret_cast<char*>(both) + at_byte) =
-                                    *reinterpret_cast<const uint4*>(to + j * kRowBytes + piece_at);
+                            for (int j = 0; j < kChunk; ++j) at[j * (kRowBytes / 2)] = from_float<T>(__uint_as_float(raw[j]));
                         }
-                    }
-                } else {
-                    T* at = reinterpret_cast<T*>(to) + part * 32 + lane;
-                    if constexpr (WHAT == kGradAct) {
-                        // gate and up come as the gradients leave, a chunk ahead
+                        T* at = reinterpret_cast<T*>(act_to + (lane >> 4) * kActBytes) + part * 16 + (lane & 15);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *reinterpret_cast<uint4*>(to + (k / 2 * kChunk + piece_row + k % 2 * 8) * kRowBytes + piece_at) = ahead[k];
+                        for (int j = 0; j < kChunk; j += 2) {   // gate lanes take the even columns, up lanes the odd ones
+                            const float own = __uint_as_float(lane < 16 ? raw[j] : raw[j + 1]);
+                            const float got = __uint_as_float(__shfl_xor_sync(kFullMask, lane < 16 ? raw[j + 1] : raw[j], 16));
+                            at[j * (kActBytes / 2)] = from_float<T>(lane < 16 ? silu(own) * got : silu(got) * own);
+                        }
                         half_sync();
-                        if (c0 + 2 * kChunk < it.cols) fetch(it, c0 + 2 * kChunk, chan0, bytes);
+                        const int row = (tid & 127) / 8, byte = tid % 8 * 16;
+                        if (row < many && byte < bytes)
+                            *reinterpret_cast<uint4*>(reinterpret_cast<char*>(static_cast<T*>(a.out) + (row0 + row) * a.out_ld + chan0) + byte) =
+                                *reinterpret_cast<const uint4*>(act_to + row * kActBytes + byte);
+                        if (a.out2) {
 #pragma unroll
-                        for (int j = 0; j < kChunk; ++j) {
-                            const float d = __uint_as_float(raw[j]);
-                            T &g = at[j * (kRowBytes / 2)], &u = at[(kChunk + j) * (kRowBytes / 2)];
-                            const float gate = to_float(g), up = to_float(u), s = sigmoid(gate);
-                            g = from_float<T>(d * up * s * (1.0f + gate * (1.0f - s)));
-                            u = from_float<T>(d * gate * s);
+                            for (int k = 0; k < 2; ++k) {
+                                const int j = piece_row + 8 * k, at_byte = piece_at & 127;
+                                T* both = static_cast<T*>(a.out2) + (row0 + j) * a.out2_ld + chan0 + (piece_at < 128 ? 0 : a.lanes);
+                                if (j < many && at_byte < bytes)
+                                    *reinterpret_cast<uint4*>(reinterpret_cast<char*>(both) + at_byte) =
+                                        *reinterpret_cast<const uint4*>(to + j * kRowBytes + piece_at);
+                            }
                         }
                     } else {
+                        T* at = reinterpret_cast<T*>(to) + part * 32 + lane;
+                        if constexpr (WHAT == kGradAct) {
+                            // gate and up come as the gradients leave, a chunk ahead
 #pragma unroll
-                        for (int j = 0; j < kChunk; ++j) at[j * (kRowBytes / 2)] = from_float<T>(__uint_as_float(raw[j]));
-                    }
-                    half_sync();
+                            for (int k = 0; k < 4; ++k)
+                                *reinterpret_cast<uint4*>(to + (k / 2 * kChunk + piece_row + k % 2 * 8) * kRowBytes + piece_at) = ahead[k];
+                            half_sync();
+                            if (c0 + 2 * kChunk < it.cols) fetch(it, c0 + 2 * kChunk, chan0, bytes);
 #pragma unroll
-                    for (int k = 0; k < (WHAT == kGradAct ? 4 : 2); ++k) {
-                        const int j = piece_row + k % 2 * 8;
-                        T* row = static_cast<T*>(a.out) + (row0 + j) * a.out_ld + chan0 + (k < 2 ? 0 : a.lanes);
-                        if (j < many && piece_at < bytes)
-                            *reinterpret_cast<uint4*>(reinterpret_cast<char*>(row) + piece_at) =
-                                *reinterpret_cast<const uint4*>(to + (k / 2 * kChunk + j) * kRowBytes + piece_at);
+                            for (int j = 0; j < kChunk; ++j) {
+                                const float d = __uint_as_float(raw[j]);
+                                T &g = at[j * (kRowBytes / 2)], &u = at[(kChunk + j) * (kRowBytes / 2)];
+                                const float gate = to_float(g), up = to_float(u), s = sigmoid(gate);
+                                g = from_float<T>(d * up * s * (1.0f + gate * (1.0f - s)));
+                                u = from_float<T>(d * gate * s);
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < kChunk; ++j) at[j * (kRowBytes / 2)] = from_float<T>(__uint_as_float(raw[j]));
+                        }
+                        half_sync();
+#pragma unroll
+                        for (int k = 0; k < (WHAT == kGradAct ? 4 : 2); ++k) {
+                            const int j = piece_row + k % 2 * 8;
+                            T* row = static_cast<T*>(a.out) + (row0 + j) * a.out_ld + chan0 + (k < 2 ? 0 : a.lanes);
+                            if (j < many && piece_at < bytes)
+                                *reinterpret_cast<uint4*>(reinterpret_cast<char*>(row) + piece_at) =
+                                    *reinterpret_cast<const uint4*>(to + (k / 2 * kChunk + j) * kRowBytes + piece_at);
+                        }
+                        if constexpr (WHAT == kGradAct) half_sync();   // (there is no second place)
                     }
-                    if constexpr (WHAT == kGradAct) half_sync();   // (there is no second place)
                 }
+                release();
             }
-            release();
-        }
         });
     }
     tmem_fence_before();

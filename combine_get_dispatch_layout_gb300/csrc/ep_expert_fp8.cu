@@ -111,7 +111,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t items = tile_count(a.g, plan, table);
     // CTAs of a cluster that share items have one each at most, of which each takes some of the blocks.
     const int sharer = split > 1 ? cluster_rank() : 0;
-    const int block0 = static_cast<int>(static_cast<int64_t>(blocks) * sharer / split), block1 = static_cast<int>(static_cast<int64_t>(blocks) * (sharer + 1) / split);
+    const int block0 = static_cast<int>(static_cast<int64_t>(blocks) * sharer / split);
+    const int block1 = static_cast<int>(static_cast<int64_t>(blocks) * (sharer + 1) / split);
     const int64_t item0 = blockIdx.x / split, item_step = split > 1 ? items : gridDim.x;
 
     // First channel of an item's halves (of gate and up they are the same ones), and their first weight rows.
@@ -443,7 +444,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int64_t i = item0; i < items; i += item_step) {
                     const Tile it = tile_at(a.g, plan, table, i);
                     const bool lanes = LANES && it.rows > COLS;
-                    const uint32_t shape = base | (lanes ? e5m2 << 7 : e5m2 << 10) | static_cast<uint32_t>((lanes ? 256 : columns_of(it.rows)) / 8) << 17;
+                    const uint32_t columns = lanes ? 256 : columns_of(it.rows);
+                    const uint32_t shape = base | (lanes ? e5m2 << 7 : e5m2 << 10) | columns / 8 << 17;
                     for (int b = block0; b < block1; ++b) {
                         if (lanes) {
                             buffer = (buffer + 1) & 2;   // an even one and the next

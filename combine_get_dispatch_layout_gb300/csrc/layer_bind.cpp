@@ -372,7 +372,7 @@ long expert_w4(PyObject* const* a) {
 
 // (x, x_scales, weights, weight_scales, y, y_scales, expert_offsets, expert_counts, activation, scale_mode, stream)
 long expert_fp8(PyObject* const* a) {
-    const Tensor &x = on_gpu(tensor(a[0], "x"), "x"), &w = tensor(a[2], "weights"), &y = tensor(a[4], "y");
+    const Tensor &x = tensor(a[0], "x"), &w = tensor(a[2], "weights"), &y = tensor(a[4], "y");
     dimensions(x, 2, "x");
     dimensions(w, 3, "weights");
     const int64_t n = x.size(0), I = x.size(1), E = w.size(0), O = w.size(1), blocks = I / 128;
@@ -382,7 +382,7 @@ long expert_fp8(PyObject* const* a) {
     c.y_dtype = type_code(y, "y", false, true);
     c.activation = small(a[8], "activation");
     const int64_t cols = c.activation == EP_ACT_SWIGLU ? O / 2 : O;
-    const Rows xr = rows(x, x.scalar_type(), {n, I}, "x"), yr = gpu_rows(a[4], y.scalar_type(), {n, cols}, "y");
+    const Rows xr = gpu_rows(a[0], x.scalar_type(), {n, I}, "x"), yr = gpu_rows(a[4], y.scalar_type(), {n, cols}, "y");
     c.x_ld = n > 1 ? xr.ld : (xr.ld + 15) / 16 * 16;
     c.y_ld = yr.ld;
     const Scales xs = scales(a[1], n, blocks, false, "x_scales");

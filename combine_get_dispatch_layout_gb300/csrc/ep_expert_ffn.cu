@@ -515,9 +515,8 @@ cudaError_t launch_gemms(Operands& first, Operands& second, cudaStream_t stream)
     for (Gemm* a : {&first.gemm, &second.gemm}) {
         a->stage_bytes = bytes;
         a->stages = kRing / bytes < kMostStages ? kRing / bytes : kMostStages;
-        const int64_t used = a->g.rows < a->g.E ? a->g.rows : a->g.E;
         if (a->columns > 0) items += static_cast<int64_t>(a->g.E) * a->plan.m_tiles * a->n_tiles;
-        else if (a->plan.m_tiles > 0) items += (a->g.rows + used * (a->plan.cap - 1)) / a->plan.cap * a->plan.m_tiles;
+        else if (a->plan.m_tiles > 0) items += most_tiles(a->g, a->plan.cap) * a->plan.m_tiles;
     }
     if (items == 0) return cudaSuccess;
     return launch_clusters(expert_gemm_kernel<T, FIRST, SECOND>, static_cast<int>(items < pairs ? items : pairs), 2, kThreads, kShared, stream,
@@ -535,6 +534,8 @@ Gemm gemm_of(const FfnArgs& f, void* out, int64_t out_ld, int lanes, int of_tile
     while (((f.g.E - 1) >> a.plan.shift) + 1 > kTileTable) ++a.plan.shift;
     const int64_t used = f.g.rows < f.g.E ? f.g.rows : f.g.E, mean = (f.g.rows - 1) / used + 1;
     a.plan.cap = mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 112 ? 128 : 256;
+    // (smaller tiles where there would be work for half the pairs at most: a stage takes as long for few rows)
+    while (a.plan.cap > 32 && a.plan.m_tiles > 0 && 4 * most_tiles(f.g, a.plan.cap) * a.plan.m_tiles <= sm_count()) a.plan.cap /= 2;
     a.box = a.plan.cap <= 64 ? 16 : 64;
     a.out = out;
     a.out_ld = out_ld;

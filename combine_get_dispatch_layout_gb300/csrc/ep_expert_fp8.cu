@@ -210,6 +210,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr int kHalves = SWIGLU ? 1 : 2;
             if (a.y_dtype != EP_DTYPE_FP8_E4M3) {
                 const bool bf16 = a.y_dtype == EP_DTYPE_BF16, wide = a.y_ld % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
+                if (!wide) {   // rows on any byte: 32 rows x 32 channels at a time through shared memory, a row a warp's store
+                    uint32_t* const turn = reinterpret_cast<uint32_t*>(join) + warp * (32 * 16);
+#pragma unroll
+                    for (int half = 0; half < kHalves; ++half)
+#pragma unroll
+                        for (int n0 = 0; n0 < 32; n0 += 16) {
+                            const int chan = (half == 0 ? first : second) + 2 * n0;
+#pragma unroll
+                            for (int n = 0; n < 16; ++n) {
+                                const float2 v = apart(acc[half][n0 + n]);
+                                const __nv_bfloat162 vb = __floats2bfloat162_rn(v.x, v.y);
+                                const __half2 vh = __floats2half2_rn(v.x, v.y);
+                                turn[lane * 16 + ((n + lane / 2) & 15)] = bf16 ? *reinterpret_cast<const uint32_t*>(&vb) : *reinterpret_cast<const uint32_t*>(&vh);
+                            }
+                            __syncwarp();
+                            const int most_rows = min(it.rows - part * 32, 32);
+                            uint16_t* to = static_cast<uint16_t*>(a.y) + (static_cast<int64_t>(it.row) + part * 32) * a.y_ld + chan + lane;
+                            for (int k = 0; k < most_rows; ++k, to += a.y_ld)
+                                if (chan + lane < cols) *to = reinterpret_cast<const uint16_t*>(turn + k * 16)[(2 * ((lane / 2 + k / 2) & 15)) + (lane & 1)];
+                            __syncwarp();
+                        }
+                    return;
+                }
                 if (!real) return;
 #pragma unroll
                 for (int half = 0; half < kHalves; ++half) {
@@ -225,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const __half2 vh = __floats2half2_rn(v.x, v.y);
                             w[k] = bf16 ? *reinterpret_cast<const uint32_t*>(&vb) : *reinterpret_cast<const uint32_t*>(&vh);
                         }
-                        if (wide && chan + 2 * n + 8 <= cols) {
+                        if (chan + 2 * n + 8 <= cols) {
                             *reinterpret_cast<uint4*>(to + 2 * n) = make_uint4(w[0], w[1], w[2], w[3]);
                         } else {
 #pragma unroll
@@ -555,8 +578,7 @@ cudaError_t launch_shape(const Fp8Args& a, cudaStream_t stream) {
                  : box_map(&w_map, a.w, EP_DTYPE_FP8_E4M3, I, O, 1, E, I, I * O, I * O, kTileRows, 1);
     if (err == cudaSuccess) err = box_map(&x_map, a.x, EP_DTYPE_FP8_E4M3, I, a.g.rows, 1, 1, a.x_ld, a.x_ld, a.x_ld, S::kBox, 1);
     if (err != cudaSuccess) return err;
-    const int64_t used = a.g.rows < a.g.E ? a.g.rows : a.g.E;
-    const int64_t most = (a.g.rows + used * (p.cap - 1)) / p.cap * p.m_tiles;
+    const int64_t most = most_tiles(a.g, p.cap) * p.m_tiles;
     // few items are shared by the CTAs of clusters, all at once on the device
     int split = 1;
     for (int i = 1; !LANES && split < kMostSplit && 2 * split <= a.I / kBlock && most <= room.clusters[i]; ++i) split *= 2;
@@ -568,9 +590,12 @@ cudaError_t launch_shape(const Fp8Args& a, cudaStream_t stream) {
 template <bool SWIGLU>
 cudaError_t launch_activation(const Fp8Args& a, cudaStream_t stream) {
     const int used = a.g.rows < a.g.E ? a.g.rows : a.g.E, mean = (a.g.rows - 1) / used + 1;
-    if (mean <= 24) return launch_shape<32, false, SWIGLU>(a, stream);
+    // Few rows an expert, or a number of tiles that leaves half the SMs idle all the same: short tiles.
+    const int cols = SWIGLU ? a.O / 2 : a.O, m_tiles = ceil_div(cols, SWIGLU ? kTileRows / 2 : kTileRows);
+    const auto few = [&](int cap) { return 2 * most_tiles(a.g, cap) * m_tiles <= sm_count(); };
+    if (mean <= 24 || few(64)) return launch_shape<32, false, SWIGLU>(a, stream);
     // (64 neighbouring up rows have one scale)
-    if (mean <= 48 || (SWIGLU && a.O / 2 % 64 != 0)) return launch_shape<64, false, SWIGLU>(a, stream);
+    if (mean <= 48 || few(128) || (SWIGLU && a.O / 2 % 64 != 0)) return launch_shape<64, false, SWIGLU>(a, stream);
     return launch_shape<64, true, SWIGLU>(a, stream);
 }
 

@@ -35,16 +35,6 @@ __device__ __forceinline__ int rows_of(const ExpertRows& g, const Tables* t, int
     first = r.x;
     return r.y;
 }
-template <int THREADS>
-__device__ __forceinline__ void fill_rows(const ExpertRows& g, Tables* t) {
-    if (g.E > kRowTable) return;
-    for (int e = threadIdx.x; e < g.E; e += THREADS) {
-        int first;
-        const int n = rows_of(g, e, first);
-        t->rows[e] = make_int2(first, n);
-    }
-}
-
 // Tiles of an expert's product: m_tiles along the weights' rows, and along its own rows as many as `cap` rows a tile
 // make, of nearly equal width. All weight tiles are passed over for `chunk` tiles of rows at a time, so that the CTAs
 // at work together share the weights of few tiles and the inputs of few.
@@ -68,7 +58,7 @@ __device__ __forceinline__ int tile_width(int n, int tiles, int cap, int whole) 
 // Fills the tables, by all threads of the CTA (THREADS of them); they are there after the next barrier.
 template <int THREADS>
 __device__ __forceinline__ void fill_tables(const ExpertRows& g, const TilePlan& p, Tables* t, int* warp_sum) {
-    fill_rows<THREADS>(g, t);
+    static_assert(kRowTable <= THREADS, "");
     int* const table = t->tiles;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const auto tiles_of = [&](int e) {
@@ -79,7 +69,16 @@ __device__ __forceinline__ void fill_tables(const ExpertRows& g, const TilePlan&
     const int per = (entries + THREADS - 1) / THREADS, lo = min(entries, tid * per), hi = min(entries, lo + per);
     const int e0 = lo << p.shift, e1 = min(g.E, hi << p.shift);
     int own = 0;
-    for (int e = e0; e < e1; ++e) own += tiles_of(e);
+    if (g.E <= kRowTable) {   // an expert a thread
+        if (tid < g.E) {
+            int first;
+            const int n = rows_of(g, tid, first);
+            t->rows[tid] = make_int2(first, n);
+            own = (n + p.cap - 1) / p.cap;
+        }
+    } else {
+        for (int e = e0; e < e1; ++e) own += tiles_of(e);
+    }
     int scan = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -92,6 +91,10 @@ __device__ __forceinline__ void fill_tables(const ExpertRows& g, const TilePlan&
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w)
         if (w < warp) base += warp_sum[w];
+    if (g.E <= kRowTable) {
+        if (tid <= g.E) table[tid] = base;   // (the thread behind the last has all of them)
+        return;
+    }
     for (int e = e0; e < e1; ++e) {
         if ((e & ((1 << p.shift) - 1)) == 0) table[e >> p.shift] = base;
         base += tiles_of(e);
@@ -287,6 +290,23 @@ cudaError_t box_map(CUtensorMap* map, const void* base, int dtype, int64_t x, in
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
                : cudaErrorInvalidValue;
+}
+
+// SMs of the current device, 0 on an error: looked up once per device (a race writes the same value).
+int sm_count() {
+    static int known[64];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < 64 && (sms = __atomic_load_n(&known[dev], __ATOMIC_RELAXED)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) __atomic_store_n(&known[dev], sms, __ATOMIC_RELAXED);
+    return sms;
+}
+
+// Tiles of rows at most, of `cap` rows each.
+int64_t most_tiles(const ExpertRows& g, int cap) {
+    const int64_t used = g.rows < g.E ? g.rows : g.E;
+    return (g.rows + used * (cap - 1)) / cap;
 }
 
 // Clusters of 1, 2, 4 and 8 CTAs of a kernel that a device holds at once.

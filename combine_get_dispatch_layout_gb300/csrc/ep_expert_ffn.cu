@@ -113,9 +113,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = cluster_rank();
     if (warp == kCleaner && elected()) {
-        prefetch_map(&first_a_map);
-        prefetch_map(&first_b_map);
-        if constexpr (SECOND != kNone) {
+        if (first.out) {
+            prefetch_map(&first_a_map);
+            prefetch_map(&first_b_map);
+        }
+        if (SECOND != kNone && second.out) {
             prefetch_map(&second_a_map);
             prefetch_map(&second_b_map);
         }
@@ -311,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const auto weight_gradients = [&](const Gemm& a, const Item& it, uint32_t mine, int tile) {
             constexpr int kWide = 32;
             static_assert(128 * kWide * 2 <= kHalfBytes, "");
+            if (it.steps == 0 && a.accumulate) return;
             if (it.steps > 0) {
                 barrier_wait(sums_full + 8 * buffer, parity, dead);
                 tmem_fence_after();
@@ -504,7 +507,7 @@ cudaError_t launch_gemms(Operands& first, Operands& second, cudaStream_t stream)
     cudaError_t err = cluster_room(expert_gemm_kernel<T, FIRST, SECOND>, kThreads, kShared, known, ready, &room);
     if (err != cudaSuccess) return err;
     const int pairs = room.clusters[1];
-    first.gemm.atoms = first.gemm.plan.cap <= 64 ? 2 : 1;
+    first.gemm.atoms = first.gemm.plan.cap <= 128 ? 2 : 1;
     second.gemm.atoms = 1;
     int bytes = 0;   // one ring serves both
     for (Gemm* a : {&first.gemm, &second.gemm}) {
@@ -572,8 +575,7 @@ cudaError_t weight_gradient(Operands* p, const FfnArgs& f, void* out, const void
                             int64_t by_ld) {
     Gemm& a = p->gemm = gemm_of(f, out, inputs, outputs, kLanes, 0);
     if (!out) return cudaSuccess;
-    const int mean = f.g.rows / f.g.E;
-    a.box = mean < 32 ? 16 : mean < 256 ? 32 : 64;
+    a.box = 32;
     a.plan.cap = 256;
     a.columns = inputs;
     a.n_tiles = ceil_div(inputs, a.plan.cap);

@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr int kHalves = SWIGLU ? 1 : 2;
             if (a.y_dtype != EP_DTYPE_FP8_E4M3) {
                 const bool bf16 = a.y_dtype == EP_DTYPE_BF16, wide = a.y_ld % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
-                if (!wide) {   // rows on any byte: 32 rows x 32 channels at a time through shared memory, a row a warp's store
+                if (!wide) {   // rows that start anywhere: 32 rows x 32 channels at a time through shared memory, a row a warp's store
+                    static_assert(!LANES || S::kJoin >= kConsumers * 16, "");
                     uint32_t* const turn = reinterpret_cast<uint32_t*>(join) + warp * (32 * 16);
 #pragma unroll
                     for (int half = 0; half < kHalves; ++half)
@@ -231,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (chan + lane < cols) *to = reinterpret_cast<const uint16_t*>(turn + k * 16)[(2 * ((lane / 2 + k / 2) & 15)) + (lane & 1)];
                             __syncwarp();
                         }
+                    consumers_sync();   // (a tile with rows as columns uses `join` otherwise)
                     return;
                 }
                 if (!real) return;
@@ -592,10 +594,10 @@ cudaError_t launch_activation(const Fp8Args& a, cudaStream_t stream) {
     const int used = a.g.rows < a.g.E ? a.g.rows : a.g.E, mean = (a.g.rows - 1) / used + 1;
     // Few rows an expert, or a number of tiles that leaves half the SMs idle all the same: short tiles.
     const int cols = SWIGLU ? a.O / 2 : a.O, m_tiles = ceil_div(cols, SWIGLU ? kTileRows / 2 : kTileRows);
-    const auto few = [&](int cap) { return 2 * most_tiles(a.g, cap) * m_tiles <= sm_count(); };
-    if (mean <= 24 || few(64)) return launch_shape<32, false, SWIGLU>(a, stream);
+    const auto few = [&](int cap, int times) { return times * most_tiles(a.g, cap) * m_tiles <= sm_count(); };
+    if (mean <= 24 || few(64, 2)) return launch_shape<32, false, SWIGLU>(a, stream);
     // (64 neighbouring up rows have one scale)
-    if (mean <= 48 || few(128) || (SWIGLU && a.O / 2 % 64 != 0)) return launch_shape<64, false, SWIGLU>(a, stream);
+    if (mean <= 48 || few(128, 3) || (SWIGLU && a.O / 2 % 64 != 0)) return launch_shape<64, false, SWIGLU>(a, stream);
     return launch_shape<64, true, SWIGLU>(a, stream);
 }
 

@@ -58,7 +58,7 @@ __device__ __forceinline__ int tile_width(int n, int tiles, int cap, int whole) 
 // Fills the tables, by all threads of the CTA (THREADS of them); they are there after the next barrier.
 template <int THREADS>
 __device__ __forceinline__ void fill_tables(const ExpertRows& g, const TilePlan& p, Tables* t, int* warp_sum) {
-    static_assert(kRowTable <= THREADS, "");
+    static_assert(kRowTable < THREADS, "");
     int* const table = t->tiles;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const auto tiles_of = [&](int e) {

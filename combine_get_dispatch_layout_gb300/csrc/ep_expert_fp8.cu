@@ -169,23 +169,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             fetch(0);
             buffer = (buffer + 1) & 2;   // an even one and the next
-            for (int b = 0; b < blocks; ++b) {
+
+            uint32_t raw[2][16];
+            const auto begin = [&] {
                 barrier_wait_inline(sums_full + 8 * buffer, (parities >> buffer) & 1, dead);
                 tmem_fence_after();
+                tmem_load16(mine + buffer * 128 + h * 64, raw[0]);
+            };
+            begin();
+            for (int b = 0; b < blocks; ++b) {
+                
                 const uint32_t at = mine + buffer * 128 + h * 64;
-                uint32_t raw[2][16];
-                tmem_load16(at, raw[0]);
                 const uint64_t f0 = both(s0), f1 = both(s1);
                 if (b + 1 < blocks) fetch(b + 1);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {   // a chunk of sums is on its way while the one before is added
+                for (int c = 0; c < 8; ++c) {
                     tmem_loaded(raw[c & 1]);
                     if (c < 7) {
                         tmem_load16(at + (c + 1) / 4 * 128 + (c + 1) % 4 * 16, raw[(c + 1) & 1]);
                     } else {
                         tmem_fence_before();
                         __syncwarp();
-                        if (lane == 0) barrier_arrive(sums_empty + 8 * (buffer + h));   // (the issuer waits for both)
+                        if (lane == 0) barrier_arrive(sums_empty + 8 * (buffer + h));
+                        parities ^= 1u << buffer;
+                        buffer ^= 2;
+                        if (b + 1 < blocks) begin();
                     }
 #pragma unroll
                     for (int n = 0; n < 8; ++n) {
@@ -193,8 +201,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         to = fma2(pair(raw[c & 1][2 * n], raw[c & 1][2 * n + 1]), c < 4 ? f0 : f1, to);
                     }
                 }
-                parities ^= 1u << buffer;
-                buffer ^= 2;
             }
             if (*dead) {
 #pragma unroll
@@ -584,6 +590,7 @@ cudaError_t launch_shape(const Fp8Args& a, cudaStream_t stream) {
     // few items are shared by the CTAs of clusters, all at once on the device
     int split = 1;
     for (int i = 1; !LANES && split < kMostSplit && 2 * split <= a.I / kBlock && most <= room.clusters[i]; ++i) split *= 2;
+    p.flip = room.clusters[0];
     const int64_t clusters = most < room.clusters[0] / split ? most : room.clusters[0] / split;
     return launch_clusters(expert_fp8_kernel<COLS, LANES, SWIGLU>, static_cast<int>(clusters), split, kThreads, S::kShared, stream, a, p, split,
                            w_map, x_map);

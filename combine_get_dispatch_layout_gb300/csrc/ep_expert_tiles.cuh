@@ -42,6 +42,7 @@ struct TilePlan {
     int m_tiles, cap, chunk;
     int whole;   // tiles of `cap` rows and a rest, instead of equal ones
     int shift;   // an entry of the table stands for 2^shift experts
+    int flip;    // items after which the order of tiles turns about: CTAs would else have only full or only nearly empty ones
 };
 struct Tile {
     int expert, m;     // m: tile of weight rows
@@ -129,7 +130,9 @@ __device__ __forceinline__ Tile tile_at(const ExpertRows& g, const TilePlan& p, 
     const int wide = max(min(p.chunk, tiles - c * p.chunk), 1);
     t.m = r / wide;
     const int width = tile_width(max(n, 1), max(tiles, 1), p.cap, p.whole);
-    const int64_t at = static_cast<int64_t>(c * p.chunk + r % wide) * width;
+    int place = r % wide;
+    if (p.flip > 0 && (it / p.flip & 1)) place = wide - 1 - place;
+    const int64_t at = static_cast<int64_t>(c * p.chunk + place) * width;
     t.row = first + static_cast<int>(min(at, static_cast<int64_t>(n)));
     t.rows = static_cast<int>(max(min(static_cast<int64_t>(width), n - at), static_cast<int64_t>(0)));
     return t;

@@ -15,7 +15,8 @@ namespace {
 
 constexpr int kEpilogueWarps = 8;
 constexpr int kLoader = kEpilogueWarps, kIssuer = kLoader + 1, kCleaner = kLoader + 2;   // warps
-constexpr int kThreads = 32 * (kEpilogueWarps + 3);
+constexpr int kCleaners = 3;                    // each has its slots of the ring
+constexpr int kThreads = 32 * (kEpilogueWarps + 2 + kCleaners);
 constexpr int kLanes = 256;                     // of a pair: 128 in each CTA's TMEM
 constexpr int kStep = 64;                       // contraction of a stage: 128 bytes
 constexpr int kABytes = kLanes / 2 * kStep * 2;
@@ -267,8 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             });
         }
         __syncwarp();
-    } else if (warp == kCleaner) {
-        // Rows behind an expert's last belong to others: zeros instead, in both operands, some stages before their product.
+    } else if (warp >= kCleaner) {
+        // Rows behind an expert's last belong to others: zeros instead, in both operands, some stages before their product. (Two warps: the release that their arrivals are
+        // takes 2000 clocks.)
         if constexpr (FIRST == kGradW || SECOND == kGradW) {
             int slot = 0;
             uint32_t parities = 0;   // a bit for each slot
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         slot = (slot + it.steps) % a.stages;
                     } else {
                         for (int s = 0; s < it.steps; ++s) {
-                            if (unclean<WHAT>(it, s)) {
+                            if (unclean<WHAT>(it, s) && slot * kCleaners / a.stages == warp - kCleaner) {
                                 barrier_wait_inline(part_full + 8 * slot, (parities >> slot) & 1, dead);
                                 parities ^= 1u << slot;
                                 const int left = it.rows - s * kStep, end = (left + 15) / 16 * 16, lines = 2 + (columns_of(it.cols) / 2 + 63) / 64;
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             });
         }
-    } else {
+    } else {   // (the first kEpilogueWarps)
         const int half = warp >> 2, part = warp & 3;   // of the chunks of columns; of the lanes
         unsigned char* const out = ring + kRing + half * kHalfBytes;
         unsigned char* const act_out = out + kOutBytes;
@@ -313,19 +315,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             buffer ^= 1;
             if (buffer == 0) parity ^= 1;
         };
-        // Weight gradients: a thread has a row of the output and kWide neighbouring places of it at a time. Rows of 16 bits go
-        // through shared memory, so that four lanes write 64 bytes of one; its 16-byte pieces are swapped by row against
-        // bank conflicts.
+        // Weight gradients: a thread has a row of the output and 32 neighbouring places of it at a time. They leave through the
+        // warp's own part of the shared memory, 64 bytes of its 32 rows at a time, so that four lanes write 64 bytes of one; the
+        // 16-byte pieces are swapped by row against bank conflicts.
         const auto weight_gradients = [&](const Gemm& a, const Item& it, uint32_t mine, int tile) {
             constexpr int kWide = 32;
-            static_assert(128 * kWide * 2 <= kHalfBytes, "");
+            static_assert(32 * 64 <= kHalfBytes / 4 && kHalfBytes % 64 == 0, "");
             if (it.steps == 0 && a.accumulate) return;
             if (it.steps > 0) {
                 barrier_wait(sums_full + 8 * buffer, parity, dead);
                 tmem_fence_after();
             }
-            const int64_t first = static_cast<int64_t>(it.expert) * a.lanes + tile;   // the CTA's first row
-            const int rows = a.lanes - tile, r = part * 32 + lane;
+            unsigned char* const own = out + part * (kHalfBytes / 4);
+            const int64_t first = static_cast<int64_t>(it.expert) * a.lanes + tile + part * 32;   // the warp's first row
+            const int rows = a.lanes - tile - part * 32, size = a.out_fp32 ? 4 : 2;
+            const int64_t pitch = static_cast<int64_t>(a.columns) * size;
+            // this thread's pieces are of rows lane / 4 and every eighth after that
+            char* const to = static_cast<char*>(a.out) + (first + lane / 4) * pitch + lane % 4 * 16;
+            // the pieces of the place from `at` bytes on, of which `bytes` are real
+            const auto leave = [&](const uint4 (&piece)[4], int64_t at, int bytes, bool add) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(own + lane * 64 + (q ^ (lane >> 1 & 3)) * 16) = piece[q];
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int row = k * 8 + lane / 4;
+                    if (row >= rows || lane % 4 * 16 >= bytes) continue;
+                    uint4 v = *reinterpret_cast<const uint4*>(own + row * 64 + (lane % 4 ^ (row >> 1 & 3)) * 16);
+                    uint4* const place = reinterpret_cast<uint4*>(to + 8 * k * pitch + at);
+                    if (add) {
+                        const float4 old = *reinterpret_cast<const float4*>(place);
+                        v = make_uint4(__float_as_uint(old.x + __uint_as_float(v.x)), __float_as_uint(old.y + __uint_as_float(v.y)),
+                                       __float_as_uint(old.z + __uint_as_float(v.z)), __float_as_uint(old.w + __uint_as_float(v.w)));
+                    }
+                    *place = v;
+                }
+                __syncwarp();
+            };
             for (int c0 = half * kWide; c0 < it.cols; c0 += 2 * kWide) {
                 uint32_t raw[kWide];
                 if (it.steps > 0) {
@@ -340,43 +366,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < kWide; ++j) raw[j] = 0x7fffffff;
                 }
                 const int many = min(kWide, it.cols - c0);   // (a multiple of 8)
+                const int64_t at = static_cast<int64_t>(it.col + c0) * size;
+                uint4 piece[4];
                 if (a.out_fp32) {
-                    float* to = static_cast<float*>(a.out) + (first + r) * a.columns + it.col + c0;
 #pragma unroll
-                    for (int j = 0; j < kWide; j += 4) {
-                        if (r >= rows || j >= many) continue;
-                        float4 v = make_float4(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1]), __uint_as_float(raw[j + 2]),
-                                               __uint_as_float(raw[j + 3]));
-                        if (a.accumulate) {
-                            const float4 old = *reinterpret_cast<const float4*>(to + j);
-                            v.x += old.x, v.y += old.y, v.z += old.z, v.w += old.w;
-                        }
-                        *reinterpret_cast<float4*>(to + j) = v;
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            piece[q] = make_uint4(raw[16 * h + 4 * q], raw[16 * h + 4 * q + 1], raw[16 * h + 4 * q + 2], raw[16 * h + 4 * q + 3]);
+                        leave(piece, at + h * 64, many * 4 - h * 64, a.accumulate);
                     }
                     continue;
                 }
 #pragma unroll
-                for (int q = 0; q < kWide / 8; ++q) {
+                for (int q = 0; q < 4; ++q) {
                     Vec8<T> v;
+                    if (a.accumulate && lane < rows && 8 * q < many) {
+                        Vec8<T> old;
+                        old.raw = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.out) + (first + lane) * pitch + at + 16 * q);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) raw[8 * q + j] = __float_as_uint(to_float(old.v[j]) + __uint_as_float(raw[8 * q + j]));
+                    }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v.v[j] = from_float<T>(__uint_as_float(raw[8 * q + j]));
-                    if (a.accumulate && r < rows && 8 * q < many) {
-                        Vec8<T> old;
-                        old.raw = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.out) + (first + r) * a.columns + it.col + c0 + 8 * q);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) v.v[j] = from_float<T>(to_float(old.v[j]) + __uint_as_float(raw[8 * q + j]));
-                    }
-                    *reinterpret_cast<uint4*>(out + r * (2 * kWide) + (q ^ (r >> 1 & 3)) * 16) = v.raw;
+                    piece[q] = v.raw;
                 }
-                half_sync();
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int row = k * 32 + (tid & 127) / 4, q = tid % 4;
-                    if (row < rows && 8 * q < many)
-                        *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (first + row) * a.columns + it.col + c0 + 8 * q) =
-                            *reinterpret_cast<const uint4*>(out + row * (2 * kWide) + (q ^ (row >> 1 & 3)) * 16);
-                }
-                half_sync();   // (there is no second place)
+                leave(piece, at, many * 2, false);
             }
         };
         walk([&](auto kind, const Gemm& a, const CUtensorMap&, const CUtensorMap&, int64_t start, int64_t items) {

@@ -5,9 +5,27 @@
 //   gate_up = x W1^T,  act = silu(gate) * up,  y = act W2^T
 //   dact = dy W2,  dgate = dact up s (1 + gate (1 - s)),  dup = dact gate s,  s = 1 / (1 + exp(-gate))
 //   dx = [dgate dup] W1,  dW1 = [dgate dup]^T x,  dW2 = dy^T act
-// Each is one product D [128 lanes][columns] of a tile: the lanes are always the dimension that is contiguous in the
-// output (channels of a row), the columns its rows, so that one store pattern serves all, and few rows cost few
-// columns. Operands come as they lie in memory, contraction inward (K-major) or outward (MN-major), no transposes.
+// Each is one product D [lanes][columns] of a tile: the lanes are the output's channels (the dimension that is contiguous
+// in it; of the weights' gradients its rows), the columns its rows, so that few rows cost few columns. Operands come as
+// they lie in memory, contraction inward (K-major) or outward (MN-major): no transposed copies.
+//
+// Roundings. act and grad_gate_up are rounded to the tensors' type because they are operands of the next product, whose
+// tensor core takes 16-bit operands, and outputs of the call; all sums, gate, up and the sigmoid are fp32 until then.
+//
+// Kernel. A pair of CTAs on two SMs multiplies as one: 256 lanes, up to 256 columns, of which each CTA loads half, so that
+// an SM reads 32 KB for 4.2 M products (alone with a tile of 128 x 256 it would be 48 KB: training step 3.85 ms, with pairs 3.5).
+// Persistent: a loader thread fills a ring by TMA, an issuer thread multiplies, eight warps empty one of two buffers of
+// sums in TMEM while the other fills. Rows go out through shared memory in 16-byte pieces (2-byte stores of a channel a
+// thread: training step 3.43 ms, now 3.3).
+// Two launches forward; backward two of two products each that do not depend on one another, so that the second fills what
+// the first leaves idle (small block's gradients 46 to 37 us against four launches).
+//
+// What bounds it (one GB300). 16384 tokens of top 6 of 64 experts, 4096 x 2048: 3.3 ms, 1500 TFLOP/s, gradients 7.0 ms,
+// 1415 TFLOP/s (of one dense 8192-row block 1815): the power limit, at which a plain library product holds 1731, and the
+// partly filled last tiles. 16 tokens of top 6 of 64 experts, 4096 x 2048: 366 us, 7.0 TB/s of weights: memory. 2048 tokens of
+// top 4 of 60 uneven experts, 2056 x 1368: 213 us, 5.4 TB/s; its gradients 520: tiles of 137 rows on average use half the columns of a
+// stage, so what the SMs read from L2 (about 9.7 TB/s) counts, and of the weights' gradients (two or three stages an item)
+// the epilogue. One row of 64 x 64: 10 us for two launches, the latency of start, tables, first load, product and store.
 #include "ep_expert_tiles.cuh"
 
 namespace ep {
@@ -20,7 +38,7 @@ constexpr int kThreads = 32 * (kEpilogueWarps + 2 + kCleaners);
 constexpr int kLanes = 256;                     // of a pair: 128 in each CTA's TMEM
 constexpr int kStep = 64;                       // contraction of a stage: 128 bytes
 constexpr int kABytes = kLanes / 2 * kStep * 2;
-constexpr int kMostStages = 10;
+constexpr int kMostStages = 6;                  // of 32 KB; those of two parts are larger
 constexpr int kRing = 192 * 1024;
 // Outputs leave through shared memory: chunks of kChunk rows of 128 channels (gate and up of 64), of which two fit for each
 // half of the epilogue's warps, and for the activation rows of 64 channels, apart so that two rows lie in other banks.
@@ -53,8 +71,8 @@ struct Gemm {
     int follows;         // the kernel before is one of the same call
 };
 
-// An item: `cols` columns (rows of the output; of kGradW places in its rows) from `col` on, lanes from m * kLanes on, `steps` stages; of kGradW the
-// contraction is over rows [row, row + rows).
+// An item: `cols` columns (rows of the output; of kGradW places in its rows) from `col` on, lanes from m * kLanes on,
+// `steps` stages; of kGradW the contraction is over rows [row, row + rows).
 struct Item {
     int expert, m, col, cols, row, rows, steps;
 };
@@ -114,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int warp_sum[kThreads / 32];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = cluster_rank();
-    if (warp == kCleaner && elected()) {
+    if (warp == kCleaner && elected()) {   // (a product without an output has no maps)
         if (first.out) {
             prefetch_map(&first_a_map);
             prefetch_map(&first_b_map);
@@ -269,8 +287,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp >= kCleaner) {
-        // Rows behind an expert's last belong to others: zeros instead, in both operands, some stages before their product. (Two warps: the release that their arrivals are
-        // takes 2000 clocks.)
+        // Rows behind an expert's last belong to others, NaN perhaps: zeros instead, in both operands, some stages before their
+        // product. Each warp has its slots of the ring (a barrier's phase must not pass it by), next to one another, so that
+        // stages that come every second or third slot are spread: the release of its arrival takes a warp 2000 clocks (60 experts
+        // of 136 rows, 2056 x 1368, all gradients: one warp 572 us, slots in turn 600, these 520).
         if constexpr (FIRST == kGradW || SECOND == kGradW) {
             int slot = 0;
             uint32_t parities = 0;   // a bit for each slot
@@ -315,7 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             buffer ^= 1;
             if (buffer == 0) parity ^= 1;
         };
-        // Weight gradients: a thread has a row of the output and 32 neighbouring places of it at a time. They leave through the
+        // Weight gradients: written once, summed over the expert's rows in one item, in order, so that the same inputs give the
+        // same bits. (Two pairs on one item of many rows would have to join in memory; there are E m_tiles n_tiles items.)
+        // A thread has a row of the output and 32 neighbouring places of it at a time. They leave through the
         // warp's own part of the shared memory, 64 bytes of its 32 rows at a time, so that four lanes write 64 bytes of one; the
         // 16-byte pieces are swapped by row against bank conflicts.
         const auto weight_gradients = [&](const Gemm& a, const Item& it, uint32_t mine, int tile) {
@@ -528,6 +550,8 @@ cudaError_t launch_gemms(Operands& first, Operands& second, bool* launched, cuda
     cudaError_t err = cluster_room(expert_gemm_kernel<T, FIRST, SECOND>, kThreads, kShared, known, ready, &room);
     if (err != cudaSuccess) return err;
     const int pairs = room.clusters[1];
+    // Two 64-deep parts a stage where both fit four times into the ring: the issuer spends 0.2 us a stage whatever its size (32
+    // experts of 2048 x 1024: mean 16 rows 81.0 to 77.9 us, mean 80 90.7 to 87.4; one expert of 4096 x 2048, 512 rows: 44.8 to 38.6).
     first.gemm.atoms = first.gemm.plan.cap <= 128 ? 2 : 1;
     second.gemm.atoms = 1;
     int bytes = 0;   // one ring serves both
@@ -538,7 +562,7 @@ cudaError_t launch_gemms(Operands& first, Operands& second, bool* launched, cuda
     int64_t items = 0;
     for (Gemm* a : {&first.gemm, &second.gemm}) {
         a->stage_bytes = bytes;
-        a->stages = kRing / bytes < kMostStages ? kRing / bytes : kMostStages;
+        a->stages = kRing / bytes < kMostStages ? kRing / bytes : kMostStages;   // (4 to 6)
         if (a->columns > 0) items += static_cast<int64_t>(a->g.E) * a->plan.m_tiles * a->n_tiles;
         else if (a->plan.m_tiles > 0) items += most_tiles(a->g, a->plan.cap) * a->plan.m_tiles;
     }
@@ -556,13 +580,19 @@ Gemm gemm_of(const FfnArgs& f, void* out, int64_t out_ld, int lanes, int of_tile
     a.lanes = lanes;
     a.inner = inner;
     a.plan.m_tiles = out ? ceil_div(lanes, of_tile) : 0;
+    // (the pairs at work together share 16 tiles of rows and some of the weights: dense 8192-row block 902 us; 4: 915, 64: 937, 1: 994)
     a.plan.chunk = 16;
     while (((f.g.E - 1) >> a.plan.shift) + 1 > kTileTable) ++a.plan.shift;
     const int64_t used = f.g.rows < f.g.E ? f.g.rows : f.g.E, mean = (f.g.rows - 1) / used + 1;
+    // Rows of a tile at most: the smallest that holds most experts' rows in one tile. Smaller ones leave room for more stages and
+    // cost fewer columns of zeros, larger ones read the weights less often. 32 experts of 2048 x 1024, us forward at mean rows
+    //   24: 77.8 (32), 79.1 (64)     48: 90 (32), 83.1 (64), 86.9 (128)     112: 105 (64), 92.3 (128), 97.0 (256)
+    //   128: 96.8 (128), 99.1 (256), but gradients 217.7 and 210.3          200: 122.8 (128), 110.7 (256)
     a.plan.cap = mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 112 ? 128 : 256;
-    // (smaller tiles where there would be work for half the pairs at most: a stage takes as long for few rows)
+    // Smaller ones where at most half the pairs would have work: a stage of few rows takes little less than one of many, so more
+    // pairs with shorter tiles end sooner (one expert of 4096 x 2048: 64 rows 39.0 to 29.9 us, 256 rows 51.6 to 35.2).
     while (a.plan.cap > 32 && a.plan.m_tiles > 0 && 4 * most_tiles(f.g, a.plan.cap) * a.plan.m_tiles <= sm_count()) a.plan.cap /= 2;
-    a.box = a.plan.cap <= 64 ? 16 : 64;
+    a.box = a.plan.cap <= 64 ? 16 : 64;   // (each CTA loads half of a tile's rows, rounded up to boxes: small ones for small tiles)
     a.out = out;
     a.out_ld = out_ld;
     return a;
@@ -599,7 +629,7 @@ cudaError_t weight_gradient(Operands* p, const FfnArgs& f, void* out, const void
                             int64_t by_ld) {
     Gemm& a = p->gemm = gemm_of(f, out, inputs, outputs, kLanes, 0);
     if (!out) return cudaSuccess;
-    a.box = 32;
+    a.box = 32;   // (rows of a stage come by 32: 32 experts of 200 rows 226 us, by 16 234, by 64 226.5; of 8 rows 187.5, 187.2, 188.1)
     a.plan.cap = 256;
     a.columns = inputs;
     a.n_tiles = ceil_div(inputs, a.plan.cap);

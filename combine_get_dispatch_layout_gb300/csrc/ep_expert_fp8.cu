@@ -3,8 +3,25 @@
 //
 // Mathematics. y[n, o] = sum over blocks b of sx[n, b] sw[o / 128, b] * sum over i in b of cx[n, i] cw[o, i]. The inner
 // sums, 128 products of two codes, run through the tensor cores with fp32 sums; each is then scaled and added in fp32
-// registers. With the activation: silu(gate) * up. An fp8 output is quantised as the dispatch quantises: amax of 128
-// channels / 448, codes by IEEE division.
+// registers, because the scales change from block to block and so cannot stay behind in the tensor cores' sums. The two
+// scales are multiplied first. With the activation: silu(gate) * up of the fp32 sums. An fp8 output is quantised as the
+// dispatch quantises: amax of 128 channels / 448, codes by IEEE division; that is the format that the next call reads.
+//
+// Kernel. An item is 256 weight rows (gate and up of the same 128 channels with the activation) times a tile of rows of one
+// expert, on one CTA: a loader thread (TMA ring, 128 inputs a stage), an issuer thread (four buffers of sums in TMEM), two
+// warps that bring scales, and eight warps that take each block's sums from TMEM and add them. Two layouts:
+//   rows as columns (up to 64 rows): a thread has a channel of each half and all rows; two groups of four warps take every other
+//     block and join at the end. Few rows cost few columns. The rows' scales are read from shared memory, four clocks for
+//     four of them a warp, which is what bounds tiles of many rows.
+//   rows as lanes (65 to 128 rows): a thread has a row and 64 channels of each half; its scales are two numbers a block.
+// The sums of the next chunk, and at a block's end of the next block, are on their way while a chunk is added (16 columns;
+// without the block's end: 8192 x 4096 x 8192 386 us, with it 352).
+//
+// What bounds it (one GB300). Decode, 256 tokens of top 8 of 256 experts, 7168 x 2048, both products: 1650 us, 6.9 TB/s of
+// weights: memory. One token of the same: 42 us, 5.6 TB/s after 6 us of start. 4 rows of one 4096 x 4096 matrix: 9.3 us, start and
+// latency. Prompt of 8192 tokens, 7168 x 4096: 2.87 ms, 1340 TFLOP/s (8192 dense rows: 1560, of 16384 inputs 1810): 48 KB a block and
+// SM from L2 at 62 GB/s an SM are 770 ns, the products 270, the additions about 600. As CTA pairs (32 KB a block) it took as long
+// for prompts and 1.85 ms instead of 1.62 for the decode step: the two CTAs wait for one another's consumers.
 #include "ep_expert_tiles.cuh"
 
 namespace ep {
@@ -18,10 +35,10 @@ constexpr int kConsumers = 32 * kParts * kGroups;
 constexpr int kLoader = kConsumers / 32, kIssuer = kLoader + 1, kScaler = kLoader + 2;   // warps; two scalers
 constexpr int kThreads = kConsumers + 128;
 constexpr int kWBytes = kTileRows * kBlock;
-constexpr int kBuffers = 4;                     // of sums in TMEM, 128 columns apart
+constexpr int kBuffers = 4;                     // of sums in TMEM, 128 columns apart (rows as lanes: two of 256)
 constexpr int kScaleSlots = 4;                  // of the ring of scales
 constexpr int kMostStages = 6;
-constexpr int kMostSplit = 8;                   // CTAs of a cluster that share an item
+constexpr int kMostSplit = 8;                   // CTAs of a cluster that share an item (the largest portable cluster)
 
 // COLS: rows of x that are columns of a product, at most. LANES: tiles of more rows have them as lanes.
 template <int COLS, bool LANES>
@@ -578,7 +595,7 @@ cudaError_t launch_shape(const Fp8Args& a, cudaStream_t stream) {
     TilePlan p{};
     p.cap = S::kRows;
     p.whole = LANES;
-    p.chunk = 16;
+    p.chunk = 16;   // (of no weight: 1, 16 and 64 within 1 % on prompts)
     p.m_tiles = ceil_div(cols, SWIGLU ? kTileRows / 2 : kTileRows);
     while (((a.g.E - 1) >> p.shift) + 1 > kTileTable) ++p.shift;
     CUtensorMap w_map, x_map;
@@ -587,7 +604,8 @@ cudaError_t launch_shape(const Fp8Args& a, cudaStream_t stream) {
     if (err == cudaSuccess) err = box_map(&x_map, a.x, EP_DTYPE_FP8_E4M3, I, a.g.rows, 1, 1, a.x_ld, a.x_ld, a.x_ld, S::kBox, 1);
     if (err != cudaSuccess) return err;
     const int64_t most = most_tiles(a.g, p.cap) * p.m_tiles;
-    // few items are shared by the CTAs of clusters, all at once on the device
+    // Few items are shared by the CTAs of clusters, each with some of the blocks, whose sums meet in shared memory: where all
+    // items are on the device at once with that many CTAs each (4096 x 4096, one row: 16.5 to 8.5 us; 64 rows 19.6 to 12.1).
     int split = 1;
     for (int i = 1; !LANES && split < kMostSplit && 2 * split <= a.I / kBlock && most <= room.clusters[i]; ++i) split *= 2;
     p.flip = room.clusters[0];
@@ -599,11 +617,15 @@ cudaError_t launch_shape(const Fp8Args& a, cudaStream_t stream) {
 template <bool SWIGLU>
 cudaError_t launch_activation(const Fp8Args& a, cudaStream_t stream) {
     const int used = a.g.rows < a.g.E ? a.g.rows : a.g.E, mean = (a.g.rows - 1) / used + 1;
-    // Few rows an expert, or a number of tiles that leaves half the SMs idle all the same: short tiles.
+    // Tiles of 32, 64 or (rows as lanes) 128 rows, the smallest that hold most experts' rows in one tile. 32 experts of 4096 x 2048 with
+    // the activation, us at mean rows
+    //   24: 52.0 (32), 54.6 (64), 56.1 (128)   32: 61.0, 58.3, 60.5   48: 72.8, 64.5, 67.5   64: 88.5, 83.0, 69.2   112: 121, 111, 63
+    // Shorter ones where at most half of the SMs, or a third, would have work (4096 x 4096: 64 rows 31.2 us as 128, 12.1 as 32; 256 rows
+    // 29.2 as 128, 24.4 as 64, 20.7 as 32; 512 rows 29.7, 30.8, 36.7).
     const int cols = SWIGLU ? a.O / 2 : a.O, m_tiles = ceil_div(cols, SWIGLU ? kTileRows / 2 : kTileRows);
     const auto few = [&](int cap, int times) { return times * most_tiles(a.g, cap) * m_tiles <= sm_count(); };
     if (mean <= 24 || few(64, 2)) return launch_shape<32, false, SWIGLU>(a, stream);
-    // (64 neighbouring up rows have one scale)
+    // (rows as lanes need one scale for 64 neighbouring up rows)
     if (mean <= 48 || few(128, 3) || (SWIGLU && a.O / 2 % 64 != 0)) return launch_shape<64, false, SWIGLU>(a, stream);
     return launch_shape<64, true, SWIGLU>(a, stream);
 }

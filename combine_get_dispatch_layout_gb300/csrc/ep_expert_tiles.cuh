@@ -35,6 +35,7 @@ __device__ __forceinline__ int rows_of(const ExpertRows& g, const Tables* t, int
     first = r.x;
     return r.y;
 }
+
 // Tiles of an expert's product: m_tiles along the weights' rows, and along its own rows as many as `cap` rows a tile
 // make, of nearly equal width. All weight tiles are passed over for `chunk` tiles of rows at a time, so that the CTAs
 // at work together share the weights of few tiles and the inputs of few.
@@ -42,7 +43,9 @@ struct TilePlan {
     int m_tiles, cap, chunk;
     int whole;   // tiles of `cap` rows and a rest, instead of equal ones
     int shift;   // an entry of the table stands for 2^shift experts
-    int flip;    // items after which the order of tiles turns about: CTAs would else have only full or only nearly empty ones
+    // Items after which the order of an expert's tiles turns about, or 0: with a full and a short tile each and an even number of
+    // CTAs some would have only full ones (fp8, 128 experts of 138 rows, 7168 x 4096: 1265 to 980 us).
+    int flip;
 };
 struct Tile {
     int expert, m;     // m: tile of weight rows

@@ -301,10 +301,12 @@ typedef struct {
  *                 codes are those of ep_dispatch_ex for the fp32 results: amax of
  *                 128 columns / 448, codes of result / scale. What it writes is
  *                 what the next call reads as x. Ignored with a 16-bit y.
- * The 128 products of a block are summed in fp32, the block's sum times its two
- * scales is added in fp32, and y is rounded once, after the activation. A row
- * with a NaN gives NaN. Rows that belong to no expert are not written. Offsets
- * are taken as at most `rows`; rows, I and O are at most 2^31 - 512.
+ * The 128 products of a block are summed in fp32, the block's sum times the
+ * product of its two scales (in fp32: below 2^-126 it loses bits, past the
+ * largest number it is infinite) is added in fp32, and y is rounded once, after
+ * the activation. A row with a NaN gives NaN. Rows that belong to no expert are
+ * not written. Offsets are taken as at most `rows`; rows, I and O are at most
+ * 2^31 - 512.
  */
 EP_API ep_status_t ep_expert_fp8(const void* x, const void* x_scales, int64_t rows, int I, const uint8_t* weights,
                                  const float* weight_scales, const int32_t* expert_offsets,

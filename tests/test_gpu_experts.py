@@ -6,10 +6,14 @@ off by at most n * 2^-23 of the sum of magnitudes (every addition rounded or tru
 carried through its slope (that of silu is at most 1.1).
 """
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 pytestmark = pytest.mark.gpu
 U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
 TINY = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25, torch.float32: 2.0 ** -149}   # half the smallest step
@@ -733,3 +737,76 @@ def test_gradients_against_differences(ep):
         # and the third-order term of a step of 2^-6
         noise = 2 * 2.0 ** -11 * 6 * (n * H) ** 0.5 * H ** 0.5
         assert abs(got - want) <= 0.02 * abs(want) + noise, (k, got, want, noise)
+
+
+def test_train_experts_example(ep):
+    """The example's layer on two micro-batches against 64-bit autograd of the same layer, routing taken from the example."""
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    import train_experts
+    T, H, F, E, K = 70, 128, 72, 8, 3
+    layer = train_experts.ExpertLayer(T, hidden=H, inner=F, experts=E, topk=K)
+    g = gen(16)
+    gate, w1, w2 = (t.double().requires_grad_() for t in (layer.gate, layer.up16, layer.down16))
+    for k in range(2):
+        x, d_out = randn(g, T, H, dtype=torch.bfloat16), randn(g, T, H, dtype=torch.bfloat16)
+        out = layer.forward(x).clone()
+        dx = layer.backward(d_out, add=k > 0)
+        X = x.double().requires_grad_()
+        top = torch.softmax((X @ gate.t()).gather(1, layer.idx), 1)
+        hidden = torch.einsum("tkfh,th->tkf", w1[layer.idx], X)
+        a = torch.nn.functional.silu(hidden[..., :F]) * hidden[..., F:]
+        result = (torch.einsum("tkhf,tkf->tkh", w2[layer.idx], a) * top[..., None]).sum(1)
+        (result * d_out.double()).sum().backward()
+        # as above, and dx is the sum of two rounded parts
+        for got, want in ((out, result.detach()), (dx, X.grad)):
+            assert (got.double() - want).norm() <= 6 * 2.0 ** -8 * want.norm()
+    for got, want in ((layer.grad_gate, gate.grad), (layer.grad_up, w1.grad), (layer.grad_down, w2.grad)):
+        assert (got.double() - want).norm() <= 5 * 2.0 ** -8 * want.norm()
+    before = layer.w_up.clone()
+    layer.step(0.5)
+    assert torch.equal(layer.w_up, before - 0.5 * layer.grad_up) and torch.equal(layer.up16, layer.w_up.bfloat16())
+    layer.handle.destroy()
+
+
+def test_train_experts_example_runs_as_a_program():
+    r = subprocess.run([sys.executable, os.path.join(ROOT, "examples", "train_experts.py"), "--tokens", "96", "--steps", "3",
+                        "--hidden", "256", "--inner", "128"], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    assert "gradients finite: True" in r.stdout
+
+
+@pytest.mark.parametrize("late", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_fp8_odd_output_rows_of_full_and_short_tiles(ep, late, dtype):
+    """Outputs whose rows start anywhere, experts of full tiles beside short ones, so that a CTA has both in turn."""
+    counts = [128 + 3 * k % 50 if k % 3 else 200 - 7 * (k % 9) for k in range(40)]
+    I, O, n = 256, 515, sum(counts)
+    g = gen(17)
+    x, xs = fp8_rows(g, n, I)
+    w, ws = fp8_weights(g, len(counts), O, I)
+    wide = torch.full((n, O + 6), math.nan, dtype=dtype, device="cuda")
+    y = wide[:, 3:3 + O] if late else wide[:, :O]
+    ep.ep_expert_fp8(x, xs, w, ws, y, expert_offsets=offsets_of(counts))
+    want, tol = fp8_reference(counts, x, xs, w, ws, False)
+    within(y, want, tol + U[dtype] * want.abs() + TINY[dtype])
+    assert wide[:, 3 + O if late else O:].isnan().all() and (not late or wide[:, :3].isnan().all())
+
+
+def test_experts_without_rows_keep_accumulated_gradients(ep):
+    """With accumulate an expert without rows keeps what is there, to the bit."""
+    counts, H, F = [0, 33, 0, 5], 136, 40
+    n, g = sum(counts), gen(18)
+    x, up, down = block_inputs(g, counts, H, F, torch.bfloat16)
+    act, y, gate_up = (torch.empty(n, k, dtype=torch.bfloat16, device="cuda") for k in (F, H, 2 * F))
+    off = offsets_of(counts)
+    ep.ep_expert_ffn(x, up, down, act, y, gate_up=gate_up, expert_offsets=off)
+    for dtype in (torch.bfloat16, torch.float32):
+        d_up, d_down = randn(g, 4, 2 * F, H, dtype=dtype), randn(g, 4, H, F, dtype=dtype)
+        d_up[0, 0, :3] = torch.tensor([-0.0, math.inf, math.nan])
+        old = d_up.clone(), d_down.clone()
+        ep.ep_expert_ffn_backward(y, x, gate_up, act, up, down, torch.empty_like(gate_up), torch.empty_like(x), d_up, d_down,
+                                  expert_offsets=off, accumulate=True)
+        bits = torch.int32 if dtype == torch.float32 else torch.int16
+        for got, was in zip((d_up, d_down), old):
+            assert torch.equal(got[[0, 2]].view(bits), was[[0, 2]].view(bits))
+            assert not torch.equal(got[1], was[1]) and not torch.equal(got[3], was[3])

@@ -134,7 +134,7 @@ __device__ __forceinline__ Tile tile_at(const ExpertRows& g, const TilePlan& p, 
     t.m = r / wide;
     const int width = tile_width(max(n, 1), max(tiles, 1), p.cap, p.whole);
     int place = r % wide;
-    if (p.flip > 0 && (it / p.flip & 1)) place = wide - 1 - place;
+    if (p.flip > 0 && ((it - place) / p.flip & 1)) place = wide - 1 - place;   // (all of these tiles or none, so that each has its turn)
     const int64_t at = static_cast<int64_t>(c * p.chunk + place) * width;
     t.row = first + static_cast<int>(min(at, static_cast<int64_t>(n)));
     t.rows = static_cast<int>(max(min(static_cast<int64_t>(width), n - at), static_cast<int64_t>(0)));

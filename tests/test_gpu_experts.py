@@ -810,3 +810,10 @@ def test_experts_without_rows_keep_accumulated_gradients(ep):
         for got, was in zip((d_up, d_down), old):
             assert torch.equal(got[[0, 2]].view(bits), was[[0, 2]].view(bits))
             assert not torch.equal(got[1], was[1]) and not torch.equal(got[3], was[3])
+
+
+@pytest.mark.parametrize("counts,I,O", [([5447], 128, 1030), ([138] * 60, 128, 700), ([300, 0, 777, 65, 1025, 90, 131] * 6, 256, 1290)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_fp8_every_tile_has_its_turn(ep, counts, I, O, swiglu):
+    """More tiles than CTAs, several of an expert, at every place against the number of CTAs: all rows are written."""
+    run_fp8(ep, counts, I, O, swiglu)

@@ -22,10 +22,11 @@
 //
 // What bounds it (one GB300). 16384 tokens of top 6 of 64 experts, 4096 x 2048: 3.3 ms, 1500 TFLOP/s, gradients 7.0 ms,
 // 1415 TFLOP/s (of one dense 8192-row block 1815): the power limit, at which a plain library product holds 1731, and the
-// partly filled last tiles. 16 tokens of top 6 of 64 experts, 4096 x 2048: 366 us, 7.0 TB/s of weights: memory. 2048 tokens of
-// top 4 of 60 uneven experts, 2056 x 1368: 213 us, 5.4 TB/s; its gradients 520: tiles of 137 rows on average use half the columns of a
-// stage, so what the SMs read from L2 (about 9.7 TB/s) counts, and of the weights' gradients (two or three stages an item)
-// the epilogue. One row of 64 x 64: 10 us for two launches, the latency of start, tables, first load, product and store.
+// partly filled last tiles. 16 tokens of top 6 of 64 experts, 4096 x 2048: 366 us, 7.0 TB/s of weights: memory. 2048 tokens
+// of top 4 of 60 uneven experts, 2056 x 1368: 213 us, 5.4 TB/s; its gradients 520: tiles of 137 rows on average use half
+// the columns of a stage, so the bytes that come into the SMs count (9.9 TB/s of at most 12.6), and of the weights'
+// gradients, with two or three stages an item, the epilogue. One row of 64 x 64: 10 us for two launches, the latency of
+// start, tables, first load, product and store.
 #include "ep_expert_tiles.cuh"
 
 namespace ep {

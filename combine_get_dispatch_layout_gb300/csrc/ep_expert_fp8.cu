@@ -19,9 +19,11 @@
 //
 // What bounds it (one GB300). Decode, 256 tokens of top 8 of 256 experts, 7168 x 2048, both products: 1650 us, 6.9 TB/s of
 // weights: memory. One token of the same: 42 us, 5.6 TB/s after 6 us of start. 4 rows of one 4096 x 4096 matrix: 9.3 us, start and
-// latency. Prompt of 8192 tokens, 7168 x 4096: 2.87 ms, 1340 TFLOP/s (8192 dense rows: 1560, of 16384 inputs 1810): 48 KB a block and
-// SM from L2 at 62 GB/s an SM are 770 ns, the products 270, the additions about 600. As CTA pairs (32 KB a block) it took as long
-// for prompts and 1.85 ms instead of 1.62 for the decode step: the two CTAs wait for one another's consumers.
+// latency. Prompt of 8192 tokens, 7168 x 4096: 2.87 ms, 1340 TFLOP/s (8192 dense rows: 1560, of 16384 inputs 1810): a block of a
+// full tile takes an SM 770 ns; 577 without the additions, which is 48 KB at the 83 GB/s that come into an SM; the products are
+// 210 of them. Twice the warps for the additions: the same 770. As CTA pairs (32 KB a block) it took as long for prompts and
+// 1.85 ms instead of 1.62 for the decode step, because the two CTAs wait for one another's consumers; with the weights sent to two CTAs
+// by multicast full tiles took 770 ns too (as much comes into each SM), and experts of 138 rows 1227 us instead of 980.
 #include "ep_expert_tiles.cuh"
 
 namespace ep {

@@ -218,7 +218,8 @@ def ep_expert_ffn_backward(grad_y, x, gate_up, act, w_gate_up, w_down, grad_gate
     and those of grad_x [rows, H], grad_w_gate_up [E, 2F, H] and grad_w_down
     [E, H, F] that are given. The weights' are of the tensors' type or fp32, and
     with accumulate they are added to what is there. x is needed for
-    grad_w_gate_up only, act for grad_w_down and w_gate_up for grad_x."""
+    grad_w_gate_up only, act for grad_w_down and w_gate_up for grad_x.
+    grad_gate_up may be gate_up itself, grad_x may be grad_y."""
     _check((_bound or _bind()).expert_ffn_backward(grad_y, x, gate_up, act, w_gate_up, w_down, grad_gate_up, grad_x,
                                                    grad_w_gate_up, grad_w_down, expert_offsets, expert_counts, accumulate,
                                                    stream), "ep_expert_ffn_backward")

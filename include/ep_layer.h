@@ -358,8 +358,8 @@ EP_API ep_status_t ep_expert_ffn(const void* x, int64_t rows, int H, const void*
  *
  *  gate_up, act   as ep_expert_ffn wrote them.
  *  grad_gate_up   device, [rows, 2F]: written, and read for the others (which are
- *                 products of the rounded grad_gate_up).
- *  grad_x         device, [rows, H], or NULL.
+ *                 products of the rounded grad_gate_up). May be gate_up itself.
+ *  grad_x         device, [rows, H], or NULL. May be grad_y itself.
  *  grad_w_gate_up, grad_w_down
  *                 device, the weights' shapes, dense, 16-byte aligned, or NULL.
  *                 Every element is written (added to, with config.accumulate);
@@ -367,6 +367,7 @@ EP_API ep_status_t ep_expert_ffn(const void* x, int64_t rows, int H, const void*
  * Sums are fp32 and taken in a fixed order: the same inputs give the same bits.
  * Rows that belong to no expert are not written and enter nothing. Without
  * grad_x and grad_w_gate_up, grad_gate_up is still written.
+ * Otherwise outputs overlap nothing that is read.
  */
 EP_API ep_status_t ep_expert_ffn_backward(const void* grad_y, const void* x, const void* gate_up, const void* act,
                                           int64_t rows, int H, const void* w_gate_up, const void* w_down,

@@ -817,3 +817,55 @@ def test_experts_without_rows_keep_accumulated_gradients(ep):
 def test_fp8_every_tile_has_its_turn(ep, counts, I, O, swiglu):
     """More tiles than CTAs, several of an expert, at every place against the number of CTAs: all rows are written."""
     run_fp8(ep, counts, I, O, swiglu)
+
+
+@pytest.mark.parametrize("counts", [[1, 40], [300, 0, 129], [20] * 30])
+@pytest.mark.parametrize("H,F", [(64, 72), (264, 520)])
+def test_gradients_in_place(ep, counts, H, F):
+    """grad_gate_up may take the place of gate_up, and grad_x that of grad_y: the same bits as apart."""
+    g, n, off = gen(19), sum(counts), offsets_of(counts)
+    x, up, down = block_inputs(g, counts, H, F, torch.bfloat16)
+    act, y, gate_up = (torch.empty(n, k, dtype=torch.bfloat16, device="cuda") for k in (F, H, 2 * F))
+    ep.ep_expert_ffn(x, up, down, act, y, gate_up=gate_up, expert_offsets=off)
+    dy = randn(g, n, H, dtype=torch.bfloat16)
+    dgu, dx, dup, ddown = (torch.full_like(t, math.nan) for t in (gate_up, x, up, down))
+    ep.ep_expert_ffn_backward(dy, x, gate_up, act, up, down, dgu, dx, dup, ddown, expert_offsets=off)
+    dup2, ddown2 = torch.full_like(up, math.nan), torch.full_like(down, math.nan)
+    ep.ep_expert_ffn_backward(dy, x, gate_up, act, up, down, gate_up, dy, dup2, ddown2, expert_offsets=off)
+    for got, want in ((gate_up, dgu), (dy, dx), (dup2, dup), (ddown2, ddown)):
+        assert torch.equal(got, want)
+
+
+def test_in_a_captured_step_twice(ep):
+    """A captured forward and backward between which an eager call runs on other buffers, replayed several times."""
+    counts, H, F = [70, 3, 0, 190], 136, 88
+    g, n, off = gen(20), sum(counts), offsets_of(counts)
+
+    def buffers():
+        x, up, down = block_inputs(g, counts, H, F, torch.bfloat16)
+        outs = [torch.empty(n, k, dtype=torch.bfloat16, device="cuda") for k in (F, H, 2 * F, 2 * F, H)]
+        return x, up, down, outs, torch.zeros(4, 2 * F, H, device="cuda"), torch.zeros(4, H, F, device="cuda")
+
+    def step(x, up, down, outs, dup, ddown):
+        act, y, gate_up, dgu, dx = outs
+        ep.ep_expert_ffn(x, up, down, act, y, gate_up=gate_up, expert_offsets=off)
+        ep.ep_expert_ffn_backward(y, x, gate_up, act, up, down, dgu, dx, dup, ddown, expert_offsets=off, accumulate=True)
+
+    one, two = buffers(), buffers()
+    step(*one)
+    step(*two)
+    want = [t.clone() for t in one[3]] + [one[4].clone(), one[5].clone()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(*one)
+    for t in one[3]:
+        t.fill_(math.nan)
+    one[4].zero_()
+    one[5].zero_()
+    for _ in range(2):
+        graph.replay()
+        step(*two)
+    for got, w in zip(one[3], want):
+        assert torch.equal(got, w)
+    # the same fp32 gradient added twice is its double, exactly
+    assert torch.equal(one[4], 2 * want[5]) and torch.equal(one[5], 2 * want[6])

@@ -233,11 +233,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             constexpr int kHalves = SWIGLU ? 1 : 2;
+            // 64 bytes of each of the warp's rows (at the rows' end `bytes`), through the warp's part of `join` (16-byte pieces
+            // swapped by row against bank conflicts): four lanes write a row's
+            static_assert(!LANES || S::kJoin >= kConsumers * 16, "");
+            uint32_t* const turn = reinterpret_cast<uint32_t*>(join) + warp * (32 * 16);
+            const int most_rows = min(it.rows - part * 32, 32);
+            const int64_t row0 = static_cast<int64_t>(it.row) + part * 32;
+            const auto leave = [&](const uint32_t (&w)[16], char* to, int64_t pitch, int bytes) {
+                uint4* const lines = reinterpret_cast<uint4*>(turn);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) lines[lane * 4 + (q ^ (lane >> 1 & 3))] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+                __syncwarp();
+                const int at = lane % 4 * 16;
+                to += lane / 4 * pitch + at;
+#pragma unroll
+                for (int k = 0; k < 32; k += 8, to += 8 * pitch) {
+                    if (k + lane / 4 >= most_rows || at >= bytes) continue;
+                    const uint4 v = lines[(k + lane / 4) * 4 + (lane % 4 ^ lane / 8)];
+                    if (at + 16 <= bytes) {
+                        *reinterpret_cast<uint4*>(to) = v;
+                    } else {
+                        const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (at + 2 * j < bytes) reinterpret_cast<uint16_t*>(to)[j] = static_cast<uint16_t>(word[j / 2] >> (j % 2 * 16));
+                    }
+                }
+                __syncwarp();
+            };
             if (a.y_dtype != EP_DTYPE_FP8_E4M3) {
                 const bool bf16 = a.y_dtype == EP_DTYPE_BF16, wide = a.y_ld % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
                 if (!wide) {   // rows that start anywhere: 32 rows x 32 channels at a time through shared memory, a row a warp's store
-                    static_assert(!LANES || S::kJoin >= kConsumers * 16, "");
-                    uint32_t* const turn = reinterpret_cast<uint32_t*>(join) + warp * (32 * 16);
 #pragma unroll
                     for (int half = 0; half < kHalves; ++half)
 #pragma unroll
@@ -251,8 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 turn[lane * 16 + ((n + lane / 2) & 15)] = bf16 ? *reinterpret_cast<const uint32_t*>(&vb) : *reinterpret_cast<const uint32_t*>(&vh);
                             }
                             __syncwarp();
-                            const int most_rows = min(it.rows - part * 32, 32);
-                            uint16_t* to = static_cast<uint16_t*>(a.y) + (static_cast<int64_t>(it.row) + part * 32) * a.y_ld + chan + lane;
+                            uint16_t* to = static_cast<uint16_t*>(a.y) + row0 * a.y_ld + chan + lane;
                             for (int k = 0; k < most_rows; ++k, to += a.y_ld)
                                 if (chan + lane < cols) *to = reinterpret_cast<const uint16_t*>(turn + k * 16)[(2 * ((lane / 2 + k / 2) & 15)) + (lane & 1)];
                             __syncwarp();
@@ -260,30 +285,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     consumers_sync();   // (a tile with rows as columns uses `join` otherwise)
                     return;
                 }
-                if (!real) return;
 #pragma unroll
                 for (int half = 0; half < kHalves; ++half) {
-                    const int chan = half == 0 ? first : second;
-                    uint16_t* to = static_cast<uint16_t*>(a.y) + row * a.y_ld + chan;
 #pragma unroll
-                    for (int n = 0; n < 32; n += 4) {
-                        uint32_t w[4];
+                    for (int n0 = 0; n0 < 32; n0 += 16) {
+                        const int chan = (half == 0 ? first : second) + 2 * n0;
+                        uint32_t w[16];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 v = apart(acc[half][n + k]);
+                        for (int n = 0; n < 16; ++n) {
+                            const float2 v = apart(acc[half][n0 + n]);
                             const __nv_bfloat162 vb = __floats2bfloat162_rn(v.x, v.y);
                             const __half2 vh = __floats2half2_rn(v.x, v.y);
-                            w[k] = bf16 ? *reinterpret_cast<const uint32_t*>(&vb) : *reinterpret_cast<const uint32_t*>(&vh);
+                            w[n] = bf16 ? *reinterpret_cast<const uint32_t*>(&vb) : *reinterpret_cast<const uint32_t*>(&vh);
                         }
-                        if (chan + 2 * n + 8 <= cols) {
-                            *reinterpret_cast<uint4*>(to + 2 * n) = make_uint4(w[0], w[1], w[2], w[3]);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                if (chan + 2 * n + k < cols) to[2 * n + k] = static_cast<uint16_t>(w[k / 2] >> (k % 2 * 16));
-                        }
+                        leave(w, reinterpret_cast<char*>(static_cast<uint16_t*>(a.y) + row0 * a.y_ld + chan), a.y_ld * 2, (cols - chan) * 2);
                     }
                 }
+                consumers_sync();
                 return;
             }
             // e4m3: the largest of 128 channels, of which another warp's thread has the other 64
@@ -304,26 +322,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int half = 0; half < kHalves; ++half) {
                 const int chan = half == 0 ? first : second;
                 const float s = output_scale(larger(most[(half * 2 + (h ^ 1)) * 128 + part * 32 + lane], big[half]));
-                if (!real || chan >= cols) continue;   // (columns are a multiple of 128)
-                if (h == 0) write_scale(row, chan / kBlock, s);
-                uint8_t* to = static_cast<uint8_t*>(a.y) + row * a.y_ld + chan;
+                if (chan >= cols) continue;   // (columns are a multiple of 128)
+                if (h == 0 && real) write_scale(row, chan / kBlock, s);
+                uint32_t w[16];
 #pragma unroll
-                for (int n = 0; n < 32; n += 8) {
-                    uint32_t w[4];
+                for (int n = 0; n < 16; ++n) w[n] = codes(apart(acc[half][2 * n]), s) | codes(apart(acc[half][2 * n + 1]), s) << 16;
+                if (wide) {
+                    leave(w, static_cast<char*>(a.y) + row0 * a.y_ld + chan, a.y_ld, 64);
+                } else if (real) {
+                    uint8_t* to = static_cast<uint8_t*>(a.y) + row * a.y_ld + chan;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 v = apart(acc[half][n + 2 * k]), u = apart(acc[half][n + 2 * k + 1]);
-                        w[k] = codes(v, s) | codes(u, s) << 16;
-                    }
-                    if (wide) {
-                        *reinterpret_cast<uint4*>(to + 2 * n) = make_uint4(w[0], w[1], w[2], w[3]);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) to[2 * n + k] = static_cast<uint8_t>(w[k / 4] >> (k % 4 * 8));
-                    }
+                    for (int k = 0; k < 64; ++k) to[k] = static_cast<uint8_t>(w[k / 4] >> (k % 4 * 8));
                 }
             }
-            consumers_sync();   // (`most` is written again)
+            consumers_sync();   // (`most` and `join` are written again)
         };
         for (int64_t i = item0; i < items; i += item_step) {
             const Tile it = tile_at(a.g, plan, table, i);

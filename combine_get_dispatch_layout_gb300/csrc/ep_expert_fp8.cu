@@ -509,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t columns = lanes ? 256 : columns_of(it.rows);
                     const uint32_t shape = base | (lanes ? e5m2 << 7 : e5m2 << 10) | columns / 8 << 17;
                     for (int b = block0; b < block1; ++b) {
+                        barrier_wait_inline(full + 8 * slot, parity, dead);
                         if (lanes) {
                             buffer = (buffer + 1) & 2;   // an even one and the next
                             barrier_wait_inline(sums_empty + 8 * buffer + 8, (parities >> (buffer + 1)) & 1, dead);
@@ -516,7 +517,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         barrier_wait_inline(sums_empty + 8 * buffer, (parities >> buffer) & 1, dead);
                         parities ^= 1u << buffer;
-                        barrier_wait_inline(full + 8 * slot, parity, dead);
                         tmem_fence_after();
                         const uint32_t at_w = smem_addr(ring) + slot * S::kStageBytes;
                         const uint64_t dw = operand(at_w, 1024), dx = operand(at_w + kWBytes, 1024);

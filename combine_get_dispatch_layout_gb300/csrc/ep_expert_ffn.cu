@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int j = 0; j < kChunk; j += 2) {   // gate lanes take the even columns, up lanes the odd ones
                             const float own = __uint_as_float(lane < 16 ? raw[j] : raw[j + 1]);
                             const float got = __uint_as_float(__shfl_xor_sync(kFullMask, lane < 16 ? raw[j + 1] : raw[j], 16));
-                            at[j * (kActBytes / 2)] = from_float<T>(lane < 16 ? silu(own) * got : silu(got) * own);
+                            const float gate = lane < 16 ? own : got, up = lane < 16 ? got : own;
+                            at[j * (kActBytes / 2)] = from_float<T>(silu(gate) * up);
                         }
                         half_sync();
                         const int row = (tid & 127) / 8, byte = tid % 8 * 16;
@@ -593,6 +594,7 @@ Gemm gemm_of(const FfnArgs& f, void* out, int64_t out_ld, int lanes, int of_tile
     // Smaller ones where at most half the pairs would have work: a stage of few rows takes little less than one of many, so more
     // pairs with shorter tiles end sooner (one expert of 4096 x 2048: 64 rows 39.0 to 29.9 us, 256 rows 51.6 to 35.2).
     while (a.plan.cap > 32 && a.plan.m_tiles > 0 && 4 * most_tiles(f.g, a.plan.cap) * a.plan.m_tiles <= sm_count()) a.plan.cap /= 2;
+    while (1 << a.plan.cap_shift < a.plan.cap) ++a.plan.cap_shift;
     a.box = a.plan.cap <= 64 ? 16 : 64;   // (each CTA loads half of a tile's rows, rounded up to boxes: small ones for small tiles)
     a.out = out;
     a.out_ld = out_ld;

@@ -608,6 +608,7 @@ cudaError_t launch_shape(const Fp8Args& a, cudaStream_t stream) {
     const int cols = SWIGLU ? a.O / 2 : a.O;
     TilePlan p{};
     p.cap = S::kRows;
+    while (1 << p.cap_shift < p.cap) ++p.cap_shift;
     p.whole = LANES;
     p.chunk = 16;   // (of no weight: 1, 16 and 64 within 1 % on prompts)
     p.m_tiles = ceil_div(cols, SWIGLU ? kTileRows / 2 : kTileRows);

@@ -40,7 +40,7 @@ __device__ __forceinline__ int rows_of(const ExpertRows& g, const Tables* t, int
 // make, of nearly equal width. All weight tiles are passed over for `chunk` tiles of rows at a time, so that the CTAs
 // at work together share the weights of few tiles and the inputs of few.
 struct TilePlan {
-    int m_tiles, cap, chunk;
+    int m_tiles, cap, cap_shift, chunk;   // cap = 2^cap_shift
     int whole;   // tiles of `cap` rows and a rest, instead of equal ones
     int shift;   // an entry of the table stands for 2^shift experts
     // Items after which the order of an expert's tiles turns about, or 0: with a full and a short tile each and an even number of
@@ -54,10 +54,7 @@ struct Tile {
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a - 1) / b + 1; }   // a >= 1
 
-// Width of the tiles of n rows, a multiple of 16. Equal widths where none is left without rows by the rounding.
-__device__ __forceinline__ int tile_width(int n, int tiles, int cap, int whole) {
-    return 16 * tiles < cap && !whole ? (ceil_div(n, tiles) + 15) / 16 * 16 : cap;
-}
+__device__ __forceinline__ int tiles_of(const TilePlan& p, int n) { return static_cast<int>((static_cast<uint32_t>(n) + p.cap - 1) >> p.cap_shift); }
 
 // Fills the tables, by all threads of the CTA (THREADS of them); they are there after the next barrier.
 template <int THREADS>
@@ -65,9 +62,9 @@ __device__ __forceinline__ void fill_tables(const ExpertRows& g, const TilePlan&
     static_assert(kRowTable < THREADS, "");
     int* const table = t->tiles;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const auto tiles_of = [&](int e) {
+    const auto tiles_at = [&](int e) {
         int first;
-        return (rows_of(g, e, first) + p.cap - 1) / p.cap;
+        return tiles_of(p, rows_of(g, e, first));
     };
     const int entries = ((g.E - 1) >> p.shift) + 1;
     const int per = (entries + THREADS - 1) / THREADS, lo = min(entries, tid * per), hi = min(entries, lo + per);
@@ -78,10 +75,10 @@ __device__ __forceinline__ void fill_tables(const ExpertRows& g, const TilePlan&
             int first;
             const int n = rows_of(g, tid, first);
             t->rows[tid] = make_int2(first, n);
-            own = (n + p.cap - 1) / p.cap;
+            own = tiles_of(p, n);
         }
     } else {
-        for (int e = e0; e < e1; ++e) own += tiles_of(e);
+        for (int e = e0; e < e1; ++e) own += tiles_at(e);
     }
     int scan = own;
 #pragma unroll
@@ -101,7 +98,7 @@ __device__ __forceinline__ void fill_tables(const ExpertRows& g, const TilePlan&
     }
     for (int e = e0; e < e1; ++e) {
         if ((e & ((1 << p.shift) - 1)) == 0) table[e >> p.shift] = base;
-        base += tiles_of(e);
+        base += tiles_at(e);
     }
     if (hi == entries && lo < hi) table[entries] = base;
 }
@@ -110,32 +107,42 @@ __device__ __forceinline__ int64_t tile_count(const ExpertRows& g, const TilePla
     return static_cast<int64_t>(t->tiles[((g.E - 1) >> p.shift) + 1]) * p.m_tiles;
 }
 
-// (Offsets that contradict one another can make tiles without rows, never one outside [0, rows).)
-__device__ __forceinline__ Tile tile_at(const ExpertRows& g, const TilePlan& p, const Tables* tables, int64_t it) {
+// (Offsets that contradict one another can make tiles without rows, never one outside [0, rows). Items are fewer than 2^31:
+// each has 32 rows x 128 channels of a buffer or is an expert's last along its rows; every role looks each item up, so the
+// common cases go without divisions: 1500 to 1000 clocks.)
+__device__ __forceinline__ Tile tile_at(const ExpertRows& g, const TilePlan& p, const Tables* tables, int64_t item) {
     const int* const table = tables->tiles;
+    const uint32_t it = static_cast<uint32_t>(item), m_tiles = p.m_tiles;
+    const int unit = static_cast<int>(it / m_tiles);   // tiles of rows before it, if all weight tiles of one came together
     int lo = 0, hi = (g.E - 1) >> p.shift;   // the last entry whose first tile is not behind `it`
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if (static_cast<int64_t>(table[mid]) * p.m_tiles <= it) lo = mid;
+        if (table[mid] <= unit) lo = mid;
         else hi = mid - 1;
     }
-    int64_t in = it - static_cast<int64_t>(table[lo]) * p.m_tiles;
-    int first, e = lo << p.shift, n = rows_of(g, tables, e, first), tiles = (n + p.cap - 1) / p.cap;
-    while (in >= static_cast<int64_t>(tiles) * p.m_tiles && e + 1 < g.E) {   // (an entry of several experts)
-        in -= static_cast<int64_t>(tiles) * p.m_tiles;
+    uint32_t in = it - table[lo] * m_tiles;
+    int first, e = lo << p.shift, n = rows_of(g, tables, e, first), tiles = tiles_of(p, n);
+    while (in >= tiles * m_tiles && e + 1 < g.E) {   // (an entry of several experts)
+        in -= tiles * m_tiles;
         n = rows_of(g, tables, ++e, first);
-        tiles = (n + p.cap - 1) / p.cap;
+        tiles = tiles_of(p, n);
     }
     Tile t;
     t.expert = e;
-    const int64_t per_chunk = static_cast<int64_t>(p.chunk) * p.m_tiles;
-    const int c = in < per_chunk ? 0 : static_cast<int>(in / per_chunk), r = static_cast<int>(in - c * per_chunk);
-    const int wide = max(min(p.chunk, tiles - c * p.chunk), 1);
-    t.m = r / wide;
-    const int width = tile_width(max(n, 1), max(tiles, 1), p.cap, p.whole);
-    int place = r % wide;
-    if (p.flip > 0 && ((it - place) / p.flip & 1)) place = wide - 1 - place;   // (all of these tiles or none, so that each has its turn)
-    const int64_t at = static_cast<int64_t>(c * p.chunk + place) * width;
+    int place = 0, width = p.cap;
+    if (tiles <= 1) {
+        t.m = static_cast<int>(min(in, m_tiles - 1));
+    } else {
+        const uint32_t per_chunk = p.chunk * m_tiles;
+        const int c = in < per_chunk ? 0 : static_cast<int>(in / per_chunk);
+        const uint32_t r = in - c * per_chunk, wide = max(min(p.chunk, tiles - c * p.chunk), 1);
+        t.m = static_cast<int>(r / wide);
+        place = static_cast<int>(r - t.m * wide);
+        if (p.flip > 0 && ((it - place) / p.flip & 1)) place = static_cast<int>(wide) - 1 - place;   // (all of these tiles or none, so that each has its turn)
+        place += c * p.chunk;
+        if (!p.whole && 16 * tiles < p.cap) width = (ceil_div(n, tiles) + 15) / 16 * 16;   // nearly equal, none left without rows by the rounding
+    }
+    const int64_t at = static_cast<int64_t>(place) * width;
     t.row = first + static_cast<int>(min(at, static_cast<int64_t>(n)));
     t.rows = static_cast<int>(max(min(static_cast<int64_t>(width), n - at), static_cast<int64_t>(0)));
     return t;
@@ -263,14 +270,15 @@ __device__ __forceinline__ float exp_of(float v) {
     const float t = v * 1.44269504f;
     const float rest = fmaf(v, 1.44269504f, -t) + v * 1.92596299e-8f;
     float e;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));   // (what it would flush to 0 is nothing beside the 1 that it is added to)
     return e < INFINITY ? fmaf(e, rest * 0.69314718f, e) : e;
 }
-// 1 / (1 + exp(-v)); the approximate reciprocal is within 1 unit in the last place, and 0 of infinity
+// 1 / (1 + exp(-v)); the approximate reciprocal is within 1 unit in the last place, and 0 of infinity. A quarter of the sum has a
+// normal one, so that the instructions that flush subnormals do (those that do not take several times as many).
 __device__ __forceinline__ float sigmoid(float v) {
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp_of(-v)));
-    return r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(exp_of(-v), 0.25f, 0.25f)));
+    return 0.25f * r;
 }
 __device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 

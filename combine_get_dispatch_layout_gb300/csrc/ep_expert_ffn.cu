@@ -344,11 +344,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const auto weight_gradients = [&](const Gemm& a, const Item& it, uint32_t mine, int tile) {
             constexpr int kWide = 32;
             static_assert(32 * 64 <= kHalfBytes / 4 && kHalfBytes % 64 == 0, "");
-            if (it.steps == 0 && a.accumulate) return;
-            if (it.steps > 0) {
-                barrier_wait(sums_full + 8 * buffer, parity, dead);
-                tmem_fence_after();
+            if (it.steps == 0) {   // no rows: zeros, a row a warp's store
+                const int bytes = it.cols * (a.out_fp32 ? 4 : 2), some = min(a.lanes - tile - part * 32, 32);
+                if (a.accumulate) return;
+                for (int row = half; row < some; row += 2) {
+                    const int64_t at = (static_cast<int64_t>(it.expert) * a.lanes + tile + part * 32 + row) * a.columns + it.col;
+                    char* const to = static_cast<char*>(a.out) + at * (a.out_fp32 ? 4 : 2);
+                    for (int b = lane * 16; b < bytes; b += 512) *reinterpret_cast<uint4*>(to + b) = make_uint4(0, 0, 0, 0);
+                }
+                return;
             }
+            barrier_wait(sums_full + 8 * buffer, parity, dead);
+            tmem_fence_after();
             unsigned char* const own = out + part * (kHalfBytes / 4);
             const int64_t first = static_cast<int64_t>(it.expert) * a.lanes + tile + part * 32;   // the warp's first row
             const int rows = a.lanes - tile - part * 32, size = a.out_fp32 ? 4 : 2;
@@ -377,13 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             for (int c0 = half * kWide; c0 < it.cols; c0 += 2 * kWide) {
                 uint32_t raw[kWide];
-                if (it.steps > 0) {
-                    tmem_load32(mine + c0, raw);
-                    tmem_loaded(raw);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kWide; ++j) raw[j] = 0;
-                }
+                tmem_load32(mine + c0, raw);
+                tmem_loaded(raw);
                 if (*dead) {
 #pragma unroll
                     for (int j = 0; j < kWide; ++j) raw[j] = 0x7fffffff;

@@ -16,16 +16,16 @@
 // an SM reads 32 KB for 4.2 M products (alone with a tile of 128 x 256 it would be 48 KB: training step 3.85 ms, with pairs 3.5).
 // Persistent: a loader thread fills a ring by TMA, an issuer thread multiplies, eight warps empty one of two buffers of
 // sums in TMEM while the other fills. Rows go out through shared memory in 16-byte pieces (2-byte stores of a channel a
-// thread: training step 3.43 ms, now 3.3).
+// thread: training step 3.43 ms, through shared memory 3.26).
 // Two launches forward; backward two of two products each that do not depend on one another, so that the second fills what
 // the first leaves idle (small block's gradients 46 to 37 us against four launches).
 //
-// What bounds it (one GB300). 16384 tokens of top 6 of 64 experts, 4096 x 2048: 3.3 ms, 1500 TFLOP/s, gradients 7.0 ms,
-// 1415 TFLOP/s (of one dense 8192-row block 1815): the power limit, at which a plain library product holds 1731, and the
+// What bounds it (one GB300). 16384 tokens of top 6 of 64 experts, 4096 x 2048: 3.25 ms, 1520 TFLOP/s, gradients 7.0 ms,
+// 1415 TFLOP/s (of one dense 8192-row block 1820 to 1900): the power limit, at which a plain library product holds 1731, and the
 // partly filled last tiles. 16 tokens of top 6 of 64 experts, 4096 x 2048: 366 us, 7.0 TB/s of weights: memory. 2048 tokens
-// of top 4 of 60 uneven experts, 2056 x 1368: 213 us, 5.4 TB/s; its gradients 520: tiles of 137 rows on average use half
+// of top 4 of 60 uneven experts, 2056 x 1368: 203 us, 5.6 TB/s; its gradients 520: tiles of 137 rows on average use half
 // the columns of a stage, so the bytes that come into the SMs count (9.9 TB/s of at most 12.6), and of the weights'
-// gradients, with two or three stages an item, the epilogue. One row of 64 x 64: 10 us for two launches, the latency of
+// gradients, with two or three stages an item, the epilogue. One row of 64 x 64: 8.5 us for two launches, the latency of
 // start, tables, first load, product and store.
 #include "ep_expert_tiles.cuh"
 

@@ -17,13 +17,14 @@
 // The sums of the next chunk, and at a block's end of the next block, are on their way while a chunk is added (16 columns;
 // without the block's end: 8192 x 4096 x 8192 386 us, with it 352).
 //
-// What bounds it (one GB300). Decode, 256 tokens of top 8 of 256 experts, 7168 x 2048, both products: 1650 us, 6.9 TB/s of
-// weights: memory. One token of the same: 42 us, 5.6 TB/s after 6 us of start. 4 rows of one 4096 x 4096 matrix: 9.3 us, start and
-// latency. Prompt of 8192 tokens, 7168 x 4096: 2.87 ms, 1340 TFLOP/s (8192 dense rows: 1560, of 16384 inputs 1810): a block of a
-// full tile takes an SM 770 ns; 577 without the additions, which is 48 KB at the 83 GB/s that come into an SM; the products are
-// 210 of them. Twice the warps for the additions: the same 770. As CTA pairs (32 KB a block) it took as long for prompts and
-// 1.85 ms instead of 1.62 for the decode step, because the two CTAs wait for one another's consumers; with the weights sent to two CTAs
-// by multicast full tiles took 770 ns too (as much comes into each SM), and experts of 138 rows 1227 us instead of 980.
+// What bounds it (one GB300). Decode, 256 tokens of top 8 of 256 experts, 7168 x 2048, both products: 1640 us, 6.9 TB/s of
+// weights: memory. One token of the same, gate and up: 41 us, 5.7 TB/s after 6 us of start. 4 rows of one 4096 x 4096 matrix:
+// 8.2 us, start and latency. Prompt of 8192 tokens, 7168 x 4096: 2.6 to 2.8 ms, 1370 to 1470 TFLOP/s (256 rows of each of 128 experts:
+// 1800): a block of a full tile takes an SM 710 ns; without the additions 577, which is 48 KB at the 83 GB/s that come into
+// an SM; the products are 210 of them. Twice the warps for the additions: no less. As CTA pairs (32 KB a block) it took as long
+// for prompts and 1.85 ms instead of 1.62 for the decode step, because the two CTAs wait for one another's consumers; with the
+// weights sent to two CTAs by multicast full tiles took as long too (as much comes into each SM), and experts of 138 rows 1227
+// us instead of 980. Rows as lanes leave through shared memory, four lanes a row's 64 bytes: prompt 2.87 to 2.70 ms.
 #include "ep_expert_tiles.cuh"
 
 namespace ep {

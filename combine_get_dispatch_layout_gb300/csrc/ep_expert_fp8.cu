@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (a.y_scale_mode == EP_SCALE_UE8M0) static_cast<uint8_t*>(a.y_scales)[to] = static_cast<uint8_t>(__float_as_uint(s) >> 23);
         else static_cast<float*>(a.y_scales)[to] = s;
     };
+    const auto code8 = [](float v, float s) -> uint8_t { return s == 0.0f ? 0 : __nv_cvt_float_to_fp8(__fdiv_rn(v, s), __NV_SATFINITE, __NV_E4M3); };
     const auto codes = [](float2 v, float s) -> uint32_t {
         return s == 0.0f ? 0u : __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v.x, s), __fdiv_rn(v.y, s)), __NV_SATFINITE, __NV_E4M3);
     };
@@ -423,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int to = half == 0 ? first : second;   // (columns are a multiple of 128)
                     if (to >= cols) continue;
                     if (chan == 0) write_scale(row, to / kBlock, s);
-                    static_cast<uint8_t*>(a.y)[row * a.y_ld + to] = static_cast<uint8_t>(codes(make_float2(half == 0 ? one : two, 0.0f), s));
+                    static_cast<uint8_t*>(a.y)[row * a.y_ld + to] = code8(half == 0 ? one : two, s);
                 }
             };
             float* const meet = reinterpret_cast<float*>(ring) + chan;   // [2 halves][COLS][128], of a shared item

@@ -26,6 +26,7 @@
 // weights sent to two CTAs by multicast full tiles took as long too (as much comes into each SM), and experts of 138 rows 1227
 // us instead of 980. Rows as lanes leave through shared memory, four lanes a row's 64 bytes: prompt 2.87 to 2.70 ms.
 #include "ep_expert_tiles.cuh"
+#include "ep_sums_turn.cuh"
 
 namespace ep {
 namespace {
@@ -38,7 +39,6 @@ constexpr int kConsumers = 32 * kParts * kGroups;
 constexpr int kLoader = kConsumers / 32, kIssuer = kLoader + 1, kScaler = kLoader + 2;   // warps; two scalers
 constexpr int kThreads = kConsumers + 128;
 constexpr int kWBytes = kTileRows * kBlock;
-constexpr int kBuffers = 4;                     // of sums in TMEM, 128 columns apart (rows as lanes: two of 256)
 constexpr int kScaleSlots = 4;                  // of the ring of scales
 constexpr int kMostStages = 6;
 constexpr int kMostSplit = 8;                   // CTAs of a cluster that share an item (the largest portable cluster)
@@ -503,8 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (leader) {
                 const uint32_t e5m2 = a.x_dtype == EP_DTYPE_FP8_E5M2 ? 1u : 0u;
                 const uint32_t base = (1u << 4) | (128u / 16 << 24);   // fp32 sums, 128 lanes
-                int slot = 0, buffer = 0;
-                uint32_t parity = 0, parities = 15;   // parities: a bit for each buffer of sums
+                SumsTurn turn;
+                int slot = 0;
+                uint32_t parity = 0;
                 for (int64_t i = item0; i < items; i += item_step) {
                     const Tile it = tile_at(a.g, plan, table, i);
                     const bool lanes = LANES && it.rows > COLS;
@@ -512,13 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t shape = base | (lanes ? e5m2 << 7 : e5m2 << 10) | columns / 8 << 17;
                     for (int b = block0; b < block1; ++b) {
                         barrier_wait_inline(full + 8 * slot, parity, dead);
-                        if (lanes) {
-                            buffer = (buffer + 1) & 2;   // an even one and the next
-                            barrier_wait_inline(sums_empty + 8 * buffer + 8, (parities >> (buffer + 1)) & 1, dead);
-                            parities ^= 2u << buffer;
-                        }
-                        barrier_wait_inline(sums_empty + 8 * buffer, (parities >> buffer) & 1, dead);
-                        parities ^= 1u << buffer;
+                        const int buffer = turn.next(lanes, [&](int which, uint32_t phase) { barrier_wait_inline(sums_empty + 8 * which, phase, dead); });
                         tmem_fence_after();
                         const uint32_t at_w = smem_addr(ring) + slot * S::kStageBytes;
                         const uint64_t dw = operand(at_w, 1024), dx = operand(at_w + kWBytes, 1024);
@@ -536,7 +531,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         multiply_done(sums_full + 8 * buffer);
                         multiply_done(empty + 8 * slot);
                         if (++slot == S::kStages) slot = 0, parity ^= 1;
-                        buffer = (buffer + (lanes ? 2 : 1)) % kBuffers;
                     }
                 }
             }

@@ -265,8 +265,10 @@ __device__ __forceinline__ void pair_done(uint32_t bar) {
                  : "memory");
 }
 
-// exp(v): 2^t for t = v log2(e) in two parts, so that large |v| lose nothing (about 2 units in the last place).
+// exp(v): 2^t for t = v log2(e) in two parts, so that large |v| lose nothing (about 2 units in the last place). Below -104 it is 0
+// beside the 1 that it is added to; t would become infinite, its two parts NaN. (NaN stays.)
 __device__ __forceinline__ float exp_of(float v) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(-104.0f));
     const float t = v * 1.44269504f;
     const float rest = fmaf(v, 1.44269504f, -t) + v * 1.92596299e-8f;
     float e;

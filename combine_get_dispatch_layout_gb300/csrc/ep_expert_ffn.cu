@@ -506,8 +506,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const float d = __uint_as_float(raw[j]);
                                 T &g = at[j * (kRowBytes / 2)], &u = at[(kChunk + j) * (kRowBytes / 2)];
                                 const float gate = to_float(g), up = to_float(u), s = sigmoid(gate);
-                                g = from_float<T>(d * up * s * (1.0f + gate * (1.0f - s)));
-                                u = from_float<T>(d * gate * s);
+                                // (the sigmoid first: what it is multiplied with may pass fp32's range before it, and where it is 0 give NaN)
+                                g = from_float<T>(s * (1.0f + gate * (1.0f - s)) * up * d);
+                                u = from_float<T>(gate * s * d);
                             }
                         } else {
 #pragma unroll

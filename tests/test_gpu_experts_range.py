@@ -127,3 +127,12 @@ def triples(gates, dtype):
 def test_gradients_at_large_gates(ep, dtype, E):
     gate, up, d = triples(GATES, dtype)
     check_gradients(act_gradients(ep, gate, up, d, dtype, E), gate, up, d, dtype)
+
+
+@pytest.mark.parametrize("E", [1, 40])
+def test_gradients_of_large_products_stay_numbers(ep, E):
+    """The gradient at act times up or gate may pass fp32's range where the sigmoid is small: their product is 0 or a number."""
+    g, u, d = torch.meshgrid(torch.tensor([-3.38e38, -1e38, -1e4, -60.0, -5.0, 4.0, 1e4]), torch.tensor([1e30, -3e38, 2.0]),
+                             torch.tensor([3.0, -1e9, 1e30, 3e38]), indexing="ij")
+    gate, up, d = (t.reshape(-1).bfloat16().cuda() for t in (g, u, d))
+    check_gradients(act_gradients(ep, gate, up, d, torch.bfloat16, E), gate, up, d, torch.bfloat16)

@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float own = __uint_as_float(lane < 16 ? raw[j] : raw[j + 1]);
                             const float got = __uint_as_float(__shfl_xor_sync(kFullMask, lane < 16 ? raw[j + 1] : raw[j], 16));
                             const float gate = lane < 16 ? own : got, up = lane < 16 ? got : own;
-                            at[j * (kActBytes / 2)] = from_float<T>(silu(gate) * up);
+                            at[j * (kActBytes / 2)] = from_float<T>(gated(gate, up));
                         }
                         half_sync();
                         const int row = (tid & 127) / 8, byte = tid % 8 * 16;
@@ -505,10 +505,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int j = 0; j < kChunk; ++j) {
                                 const float d = __uint_as_float(raw[j]);
                                 T &g = at[j * (kRowBytes / 2)], &u = at[(kChunk + j) * (kRowBytes / 2)];
-                                const float gate = to_float(g), up = to_float(u), s = sigmoid(gate);
-                                // (the sigmoid first: what it is multiplied with may pass fp32's range before it, and where it is 0 give NaN)
-                                g = from_float<T>(s * (1.0f + gate * (1.0f - s)) * up * d);
-                                u = from_float<T>(gate * s * d);
+                                const float gate = to_float(g), up = to_float(u);
+                                // (the sigmoid first: what it is multiplied with may pass fp32's range before it, and where it is 0 give
+                                // NaN; its small factor in two parts, which loses bits only where the slope times up is below 2^-188)
+                                const Sigmoid s = sigmoid_of(gate);
+                                const float f = s.far ? 0x1p-62f : 1.0f, not_s = s.far ? 1.0f : 1.0f - s.r;
+                                g = from_float<T>(s.r * (1.0f + gate * not_s) * (up * f) * (d * f));
+                                u = from_float<T>(gate * s.r * (d * f * f));
                             }
                         } else {
 #pragma unroll

@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int n = 0; n < 32; ++n) {
                     const float2 g = apart(acc[0][n]), u = apart(acc[1][n]);
-                    acc[0][n] = pair(__float_as_uint(silu(g.x) * u.x), __float_as_uint(silu(g.y) * u.y));
+                    acc[0][n] = pair(__float_as_uint(gated(g.x, u.x)), __float_as_uint(gated(g.y, u.y)));
                 }
             }
             constexpr int kHalves = SWIGLU ? 1 : 2;
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int chan = part * 32 + lane;
             int turn = 0;
             const auto finish = [&](int column, float one, float two) {   // the two halves' sums of this thread's channels
-                if (SWIGLU) one = silu(one) * two;
+                if (SWIGLU) one = gated(one, two);
                 const int64_t row = static_cast<int64_t>(it.row) + column;
                 if (a.y_dtype != EP_DTYPE_FP8_E4M3) {
                     uint16_t* to = static_cast<uint16_t*>(a.y) + row * a.y_ld;

@@ -104,7 +104,7 @@ def act_gradients(ep, gate, up, d, dtype, E):
     return grads[:, :len(gate)], grads[:, F:F + len(gate)]
 
 
-def check_gradients(got, gate, up, d, dtype):
+def check_gradients(got, gate, up, d, dtype, small=0.0):
     gate, up, d = gate.double(), up.double(), d.double()
     s = 1 / (1 + torch.exp(-gate))
     most = torch.finfo(dtype).max * (1 + U[dtype] / 2)
@@ -114,7 +114,7 @@ def check_gradients(got, gate, up, d, dtype):
     for g, want, size in ((got[0], d * up * slope, terms), (got[1], d * (gate * s), (d * gate * s).abs())):
         want = torch.where(want.abs() >= most, torch.sign(want) * INF, want).expand_as(g)
         size = size.nan_to_num(0, 0).clamp(max=most)
-        within(g, want, (16 * F32 * size).expand_as(g) + U[dtype] * want.abs().nan_to_num(0, 0) + TINY[dtype])
+        within(g, want, (16 * F32 * size).expand_as(g) + U[dtype] * want.abs().nan_to_num(0, 0) + TINY[dtype] + small)
 
 
 def triples(gates, dtype):
@@ -136,3 +136,31 @@ def test_gradients_of_large_products_stay_numbers(ep, E):
                              torch.tensor([3.0, -1e9, 1e30, 3e38]), indexing="ij")
     gate, up, d = (t.reshape(-1).bfloat16().cuda() for t in (g, u, d))
     check_gradients(act_gradients(ep, gate, up, d, torch.bfloat16, E), gate, up, d, torch.bfloat16)
+
+
+TAIL = [-88.5, -88.75, -89.0, -90.0, -92.5, -95.0, -99.0, -102.0, -103.5, -104.0, -105.0, -110.0, -150.0]
+
+
+@pytest.mark.parametrize("E", [1, 30])
+def test_block_at_far_negative_gates(ep, E):
+    """Down to -110, where exp(-gate) is past fp32's range and the sigmoid below its normal numbers: large ups still show them."""
+    gate, up = pairs(TAIL, [1.0, 1e10, -1e20, 1e30, 3e38], torch.bfloat16)
+    act = block_act(ep, gate, up, torch.bfloat16, E)
+    check_act(act, gate.expand_as(act), up.expand_as(act), torch.bfloat16)
+
+
+@pytest.mark.parametrize("E,most", [(1, 30), (48, 40), (48, 65)])
+def test_fp8_at_far_negative_gates(ep, E, most):
+    gate, up = pairs(TAIL, [1.0, 1e10, -1e20, 1e30, 3e38], torch.float32)
+    for g, u in ((gate[:most], up[:most]), (gate[-most:], up[-most:])):
+        act = fp8_act(ep, g, u, torch.bfloat16, E)
+        check_act(act, g[None, :, None].expand_as(act), u[None, :, None].expand_as(act), torch.bfloat16)
+
+
+@pytest.mark.parametrize("E", [1, 40])
+def test_gradients_at_far_negative_gates(ep, E):
+    g, u, d = torch.meshgrid(torch.tensor(TAIL), torch.tensor([1.0, -1e20, 1e30]), torch.tensor([1.0, 1e-10, -1e20, 1e38]), indexing="ij")
+    gate, up, d = (t.reshape(-1).bfloat16().cuda() for t in (g, u, d))
+    # The sigmoid's factor 2^-124 is taken in two parts: slope * 2^124 * (up * 2^-62) may be a subnormal number, off by 2^-150, before
+    # it is multiplied with d * 2^-62.
+    check_gradients(act_gradients(ep, gate, up, d, torch.bfloat16, E), gate, up, d, torch.bfloat16, 2.0 ** -212 * d.double().abs())

@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const __half2 vh = __floats2half2_rn(v.x, v.y);
                             w[n] = bf16 ? *reinterpret_cast<const uint32_t*>(&vb) : *reinterpret_cast<const uint32_t*>(&vh);
                         }
-                        leave(w, reinterpret_cast<char*>(static_cast<uint16_t*>(a.y) + row0 * a.y_ld + chan), a.y_ld * 2, (cols - chan) * 2);
+                        leave(w, reinterpret_cast<char*>(static_cast<uint16_t*>(a.y) + row0 * a.y_ld + chan), a.y_ld * 2, min(cols - chan, 32) * 2);
                     }
                 }
                 consumers_sync();

@@ -164,3 +164,27 @@ def test_gradients_at_far_negative_gates(ep, E):
     # The sigmoid's factor 2^-124 is taken in two parts: slope * 2^124 * (up * 2^-62) may be a subnormal number, off by 2^-150, before
     # it is multiplied with d * 2^-62.
     check_gradients(act_gradients(ep, gate, up, d, torch.bfloat16, E), gate, up, d, torch.bfloat16, 2.0 ** -212 * d.double().abs())
+
+
+def test_fp8_more_than_2_to_the_30_channels(ep):
+    """Rows of x as lanes, and an output whose rows are longer than 2^31 bytes."""
+    torch.cuda.empty_cache()
+    n, O = 65, (1 << 30) + 512
+    if torch.cuda.mem_get_info()[0] < 129 * O + n * 2 * O + (1 << 32):
+        pytest.skip("needs 260 GiB")
+    w = torch.zeros(1, O, 128, dtype=torch.uint8, device="cuda")
+    some = torch.tensor([0, 5, 127, 128, 300, 511, 512, 1 << 29, O - 513, O - 1])
+    codes = torch.randint(0, 0x70, (len(some), 128), generator=torch.Generator().manual_seed(1), dtype=torch.uint8)
+    w[0, some.cuda()] = codes.cuda()
+    x = torch.ones(n, 128, device="cuda").to(E4M3)
+    scales = torch.arange(1, n + 1, device="cuda").float()[:, None]
+    y = torch.full((n, O), NAN, dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_fp8(x, scales, w.view(E4M3), torch.ones(1, O // 128, 1, device="cuda"), y)
+    sums = codes.view(E4M3).double().sum(1)
+    want = torch.arange(1, n + 1).double()[:, None] * sums
+    # sums of 128 numbers of one sign, by a step of fp32 each at most, and two products
+    within(y[:, some.cuda()], want, (130 * F32 + U[y.dtype]) * want)
+    for part in (y[:, :4096], y[:, -4096:]):
+        assert not part.isnan().any()
+    del w, y
+    torch.cuda.empty_cache()

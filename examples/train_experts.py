@@ -84,7 +84,7 @@ class ExpertLayer:
                                   expert_offsets=self.offsets, accumulate=add)
         ep.ep_dispatch_backward(self.handle, self.returned, self.grad_x)
         ep.ep_router_topk_backward(self.logits, self.idx, self.grad_weights, self.grad_logits, renormalize=True)
-        self.grad_gate.mul_(float(add)).addmm_(self.grad_logits.t(), self.x.float())
+        self.grad_gate.addmm_(self.grad_logits.t(), self.x.float(), beta=float(add))   # (with 0 what was there does not count, NaN either)
         self.grad_x += (self.grad_logits @ self.gate).bfloat16()
         return self.grad_x
 

@@ -327,3 +327,71 @@ def test_one_expert_without_offsets(ep, rows):
 
     for a, b in zip(step(), step(expert_offsets=offsets_of([rows]))):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ streams and graphs
+
+def mixed_calls(ep):
+    """Calls of all forms on buffers of their own: (call(stream), its outputs)."""
+    calls = []
+    for counts, I, O in (([3], 2048, 512), (FP8_COUNTS["lanes"], 256, 768), (FP8_COUNTS[64], 384, 640)):
+        g, n = gen(I), sum(counts)
+        x, xs = fp8_rows(g, n, I)
+        w, ws = fp8_weights(g, len(counts), O, I)
+        y, off = torch.empty(n, O, dtype=torch.bfloat16, device="cuda"), offsets_of(counts)
+        calls.append((lambda s, a=(x, xs, w, ws, y), o=off: ep.ep_expert_fp8(*a, expert_offsets=o, stream=s), [y]))
+    for cap in (64, 256):
+        counts, H, F = BLOCK_COUNTS[cap], 520, 264
+        g, n, off = gen(cap), sum(counts), offsets_of(counts)
+        x, up, down = plain.block_inputs(g, counts, H, F, torch.bfloat16)
+        outs = [torch.empty(n, k, dtype=torch.bfloat16, device="cuda") for k in (F, H, 2 * F, 2 * F, H)] + [torch.empty_like(up), torch.empty_like(down)]
+
+        def step(s, a=(x, up, down), outs=outs, off=off):
+            ep.ep_expert_ffn(*a, outs[0], outs[1], gate_up=outs[2], expert_offsets=off, stream=s)
+            ep.ep_expert_ffn_backward(a[0], a[0], outs[2], outs[0], a[1], a[2], *outs[3:], expert_offsets=off, stream=s)
+
+        calls.append((step, outs))
+    return calls
+
+
+def test_all_forms_at_once_on_streams_of_their_own(ep):
+    calls = mixed_calls(ep)
+    for call, _ in calls:
+        call(None)
+    want = [[t.clone() for t in outs] for _, outs in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for s, (call, _) in zip(streams, calls):
+            call(s)
+    torch.cuda.synchronize()
+    for (_, outs), w in zip(calls, want):
+        assert all(torch.equal(a, b) for a, b in zip(outs, w))
+
+
+def test_all_forms_in_two_graphs_at_once(ep):
+    """Two graphs of all forms, each captured on a stream of its own and replayed beside the other."""
+    sets = [mixed_calls(ep) for _ in range(2)]
+    for call, _ in sets[0]:
+        call(None)
+    want = [t.clone() for _, outs in sets[0] for t in outs]
+    torch.cuda.synchronize()
+    streams, graphs = [torch.cuda.Stream() for _ in sets], []
+    for s, calls in zip(streams, sets):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            for call, _ in calls:
+                call(None)
+        graphs.append(graph)
+    for calls in sets:
+        for _, outs in calls:
+            for t in outs:
+                t.fill_(math.nan)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, graph in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for calls in sets:
+        assert all(torch.equal(a, b) for a, b in zip([t for _, outs in calls for t in outs], want))

@@ -20,10 +20,10 @@
 // Two launches forward; backward two of two products each that do not depend on one another, so that the second fills what
 // the first leaves idle (small block's gradients 46 to 37 us against four launches).
 //
-// What bounds it (one GB300). 16384 tokens of top 6 of 64 experts, 4096 x 2048: 3.25 ms, 1520 TFLOP/s, gradients 7.0 ms,
-// 1415 TFLOP/s (of one dense 8192-row block 1820 to 1900): the power limit, at which a plain library product holds 1731, and the
-// partly filled last tiles. 16 tokens of top 6 of 64 experts, 4096 x 2048: 366 us, 7.0 TB/s of weights: memory. 2048 tokens
-// of top 4 of 60 uneven experts, 2056 x 1368: 203 us, 5.6 TB/s; its gradients 520: tiles of 137 rows on average use half
+// What bounds it (one GB300). 16384 tokens of top 6 of 64 experts, 4096 x 2048: 3.2 to 3.4 ms by the card, 1470 to 1540 TFLOP/s, gradients 6.9 to
+// 7.1 ms, 1390 to 1440 TFLOP/s (of one dense 8192-row block 1820 to 1900): the power limit, at which a plain library product holds 1731, and the
+// partly filled last tiles. 16 tokens of top 6 of 64 experts, 4096 x 2048: 350 to 375 us, 6.8 to 7.3 TB/s of weights: memory. 2048 tokens
+// of top 4 of 60 uneven experts, 2056 x 1368: 203 to 226 us, 5.1 to 5.6 TB/s; its gradients 518 to 549: tiles of 137 rows on average use half
 // the columns of a stage, so the bytes that come into the SMs count (9.9 TB/s of at most 12.6), and of the weights'
 // gradients, with two or three stages an item, the epilogue. One row of 64 x 64: 8.5 us for two launches, the latency of
 // start, tables, first load, product and store.

@@ -17,9 +17,9 @@
 // The sums of the next chunk, and at a block's end of the next block, are on their way while a chunk is added (16 columns;
 // without the block's end: 8192 x 4096 x 8192 386 us, with it 352).
 //
-// What bounds it (one GB300). Decode, 256 tokens of top 8 of 256 experts, 7168 x 2048, both products: 1640 us, 6.9 TB/s of
+// What bounds it (one GB300). Decode, 256 tokens of top 8 of 256 experts, 7168 x 2048, both products: 1590 to 1640 us, 6.9 to 7.1 TB/s of
 // weights: memory. One token of the same, gate and up: 41 us, 5.7 TB/s after 6 us of start. 4 rows of one 4096 x 4096 matrix:
-// 8.2 us, start and latency. Prompt of 8192 tokens, 7168 x 4096: 2.6 to 2.8 ms, 1370 to 1470 TFLOP/s (256 rows of each of 128 experts:
+// 8.2 us, start and latency. Prompt of 8192 tokens, 7168 x 4096: 2.6 to 2.8 ms, 1360 to 1470 TFLOP/s (256 rows of each of 128 experts:
 // 1800): a block of a full tile takes an SM 710 ns; without the additions 577, which is 48 KB at the 83 GB/s that come into
 // an SM; the products are 210 of them. Twice the warps for the additions: no less. As CTA pairs (32 KB a block) it took as long
 // for prompts and 1.85 ms instead of 1.62 for the decode step, because the two CTAs wait for one another's consumers; with the
@@ -199,7 +199,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             begin();
             for (int b = 0; b < blocks; ++b) {
-                
                 const uint32_t at = mine + buffer * 128 + h * 64;
                 const uint64_t f0 = both(s0), f1 = both(s1);
                 if (b + 1 < blocks) fetch(b + 1);
